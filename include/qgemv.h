@@ -67,7 +67,8 @@ typedef enum {
   QGEMV_ERR_TIMEOUT = 6,            /* a kernel gave up on a bounded wait (see check_error) */
   QGEMV_ERR_OOM = 7,                /* qgemv_create could not allocate its workspace */
   QGEMV_ERR_NO_DEVICE = 8,          /* no usable CUDA device / not an sm_103 device */
-  QGEMV_ERR_TOO_LARGE = 9           /* shape needs more than qgemv_run_noalloc's fixed scratch */
+  QGEMV_ERR_TOO_LARGE = 9,          /* shape needs more than qgemv_run_noalloc's fixed scratch */
+  QGEMV_ERR_BAD_INDEX = 10          /* a kernel met an index out of range (see check_error) */
 } qgemv_status_t;
 
 typedef struct qgemv_handle_s* qgemv_handle_t;
@@ -114,7 +115,9 @@ qgemv_status_t qgemv_unpack(qgemv_handle_t h, qgemv_format_t fmt, const void* pa
 
 /* Synchronise `stream`, then read and clear the handle's device error word.  Returns
  * QGEMV_ERR_TIMEOUT if any kernel since the last check gave up on a bounded wait (its y
- * is then undefined), QGEMV_ERR_CUDA if the stream reported an error, else QGEMV_OK. */
+ * is then undefined), QGEMV_ERR_BAD_INDEX if one met an index out of range in device memory
+ * (a page, slot, position, length or adapter; what it did instead is said at its entry
+ * point), QGEMV_ERR_CUDA if the stream reported an error, else QGEMV_OK. */
 qgemv_status_t qgemv_check_error(qgemv_handle_t h, cudaStream_t stream);
 
 /* Static description of a status code (never NULL). */
@@ -293,6 +296,199 @@ qgemv_status_t qgemv_run_batch(qgemv_handle_t h, qgemv_format_t fmt, const void*
 qgemv_status_t qgemv_run_gemm(qgemv_handle_t h, qgemv_format_t fmt, const void* x, int64_t M,
                               const void* packed_W, int64_t N, int64_t K, float* y,
                               cudaStream_t stream);
+
+/* ---------------------------------------------------------------- serving a batch of requests
+ * What stands between the projections of a decode step that serves many requests: the pages of
+ * a key-value cache are planned on the GPU (qgemv_page_plan), the QKV projection's rows are
+ * rotated and written into them (qgemv_kv_store), each new token attends to its request's
+ * pages (qgemv_attn_decode), and low-rank adapters are added to a projection's output
+ * (qgemv_run_lora).  Every call is described by a struct (host memory, read during the call
+ * only); nothing is allocated and nothing synchronises, so a step can be captured in a CUDA
+ * graph.  Lengths, page tables, slots, positions and adapter numbers are read on the device;
+ * one that is out of range is never used to address memory: what happens instead is said at
+ * each entry point, and qgemv_check_error then reports QGEMV_ERR_BAD_INDEX.  Element types are
+ * those of qgemv_out_t.  Strides are counted in elements. */
+
+/* A paged key-value cache.  k and v: device, page p at p * page_stride, inside it
+ * [kv_heads][page_size][head_dim] elements, contiguous and 16-byte aligned (page_stride * element size a
+ * multiple of 16 too; page_stride >= kv_heads * page_size * head_dim).  QGEMV_KV_E4M3: an e4m3
+ * code c of token t and head h stands for c * scale[t, h]; k_scale and v_scale: device fp32,
+ * [page][kv_heads][page_size], page p at p * scale_stride (ignored for the other types).
+ * head_dim 64, 128 or 256; page_size 8 or a multiple of 16. */
+typedef enum { QGEMV_KV_F16 = 1, QGEMV_KV_BF16 = 2, QGEMV_KV_E4M3 = 3 } qgemv_kv_t;
+typedef struct {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int64_t page_stride;
+  int64_t scale_stride;
+  int32_t pages;
+  int32_t page_size;
+  int32_t kv_heads;
+  int32_t head_dim;
+  qgemv_kv_t type;
+} qgemv_kv_cache_t;
+
+/* Block tables and slot maps of one step.  Request r has cached[r] tokens in its pages and
+ * brings fresh[r] new ones (both counted as 0 when negative); the new tokens of all requests
+ * are numbered 0, 1, ... in request order.  Position i of request r lives in page
+ * table[r][i / page_size]; a token that opens a page takes the next one from the top of the
+ * stack free_pages[0 .. *free_count), in token order, and writes it into the table (other
+ * entries of the table are left alone).  A token gets no slot when it lies past `capacity` or
+ * past its row of the table, or when the stack is empty; neither do the later tokens of
+ * that request.  A negative page in the table where a token's own page should be is reported,
+ * and the token gets slot -1.
+ *   lens[r]       cached[r] + the new tokens of r that have a slot: the length to attend over
+ *   offsets[r]    number of the first new token of request r; offsets[requests] = their total
+ *                 (both at most 2^31 - 1, where larger ones stay)
+ *   slots[t]      page * page_size + position % page_size, or -1    (t < capacity)
+ *   positions[t]  position in the request, or -1
+ *   owners[t]     request, or -1 past the total
+ *   counts[0..3]  new tokens (at most 2^31 - 1), those with a slot, pages taken, pages that
+ *                 were missing
+ * free_pages and *free_count are only read: the caller lowers its count by counts[2].
+ * positions, owners and offsets may be NULL.  All pointers device; slots, positions and
+ * owners 16-byte aligned.  requests >= 0, page_size >= 1, table_width >= 1 and <= table_stride,
+ * 0 <= capacity < 2^31. */
+typedef struct {
+  const int32_t* cached;
+  const int32_t* fresh;
+  int32_t* table;
+  int64_t table_stride;
+  const int32_t* free_pages;
+  const int32_t* free_count;
+  int32_t* lens;
+  int32_t* offsets;
+  int64_t* slots;
+  int32_t* positions;
+  int32_t* owners;
+  int32_t* counts;
+  int64_t capacity;
+  int32_t requests;
+  int32_t table_width;
+  int32_t page_size;
+} qgemv_page_plan_t;
+
+qgemv_status_t qgemv_page_plan(qgemv_handle_t h, const qgemv_page_plan_t* plan, cudaStream_t stream);
+
+/* Rotates the q and k rows of `tokens` tokens and stores k and v in the cache.  Row t of q, k
+ * and v starts at t * its stride and holds its heads one after another (the three can be
+ * slices of one projection's output); element type `in`.
+ *   rope          fp32 [rope_positions][rot_dim]: of each position rot_dim / 2 cosines, then
+ *                 rot_dim / 2 sines; NULL: nothing is rotated.  Pair i (a, b) becomes
+ *                 (a cos_i - b sin_i, b cos_i + a sin_i), with a, b the elements i and
+ *                 i + rot_dim / 2 of a head, or 2 i and 2 i + 1 when interleaved = 1; elements
+ *                 from rot_dim on are kept.  rot_dim: a multiple of 16, at most head_dim.
+ *   positions[t]  -1: an unused row, whose q_out is zeros.  Another position outside the
+ *                 rope table counts as -1 and is reported.
+ *   slots[t]      as qgemv_page_plan gives them; -1: k and v of the row are not stored.
+ *                 Another slot outside the cache counts as -1 and is reported.  No slot may
+ *                 occur twice.
+ *   q, q_out      may both be NULL; q_out [tokens][q_heads][head_dim] of type q_type (F16 or
+ *                 BF16), row t at t * q_out_stride.
+ * The rotation is computed in fp32 and rounded once to the cache's or q_out's type.  An E4M3
+ * cache gets scale = max|x| / 448 of the token's head (1 where that is 0 or not a positive
+ * finite number) and the codes e4m3(x / scale), rounded to nearest even.
+ * Pointers 16-byte aligned, row strides a multiple of 16 bytes.  slots, positions (and rope)
+ * are needed also where no row is rotated. */
+typedef struct {
+  qgemv_kv_cache_t cache;
+  const void* q;
+  const void* k;
+  const void* v;
+  int64_t q_stride;
+  int64_t k_stride;
+  int64_t v_stride;
+  void* q_out;
+  int64_t q_out_stride;
+  const int64_t* slots;
+  const int32_t* positions;
+  const float* rope;
+  int64_t tokens;
+  int32_t rope_positions;
+  int32_t rot_dim;
+  int32_t interleaved;
+  int32_t q_heads;
+  qgemv_out_t in;
+  qgemv_out_t q_type;
+} qgemv_kv_store_t;
+
+qgemv_status_t qgemv_kv_store(qgemv_handle_t h, const qgemv_kv_store_t* store, cudaStream_t stream);
+
+/* Attention of one new token per request over its pages:
+ *   out[r, g] = sum_t softmax_t(scale * q[r, g] . k[t]) v[t],   lo <= t < lens[r],
+ *   lse[r, g] = log sum_t exp(scale * q[r, g] . k[t])           (natural logarithm)
+ * with lo = max(0, lens[r] - window) (0 when window = 0), and k, v of kv head
+ * g / (q_heads / kv_heads).  lens[r] counts the new token, whose k and v are stored.  A row
+ * that sees no token, or whose every score is -inf, gives out = 0 and lse = -inf.
+ *   q, out        [requests][q_heads][head_dim], row r at r * stride, `type` F16 or BF16 (that of
+ *                 the cache, unless it is E4M3).
+ *   table         [requests] rows of table_width pages at r * table_stride.  A page outside
+ *                 the cache is skipped with its tokens and reported; a length past the table's
+ *                 row counts as its end and is reported.
+ *   lse           fp32 [requests][q_heads], or NULL.
+ * Scores, the softmax and the sums are held in fp32 (16-bit products are exact); the weights
+ * enter the second product as two 16-bit parts.  What lies in the cache outside the tokens
+ * that a row sees, NaN included, does not reach it.  Deterministic: the same inputs give the
+ * same bits.  Uses the handle's workspace like qgemv_run.  q_heads a multiple of kv_heads;
+ * out must not overlap q. */
+typedef struct {
+  qgemv_kv_cache_t cache;
+  const void* q;
+  int64_t q_stride;
+  void* out;
+  int64_t out_stride;
+  float* lse;
+  const int32_t* table;
+  int64_t table_stride;
+  const int32_t* lens;
+  float scale;
+  int32_t window;
+  int32_t requests;
+  int32_t table_width;
+  int32_t q_heads;
+  qgemv_out_t type;
+} qgemv_attn_decode_t;
+
+qgemv_status_t qgemv_attn_decode(qgemv_handle_t h, const qgemv_attn_decode_t* attn, cudaStream_t stream);
+
+/* Low-rank adapters of many requests beside a shared projection: for row m with adapter
+ * a = ids[m] of rank r = ranks[a],
+ *   y[m, n] = base[m, n] + scales[a] * sum_{j < r} B[a, n, j] * (sum_k A[a, j, k] * x[m, k])
+ * and y[m, n] = base[m, n] when ids[m] is -1 (or another number outside 0 .. adapters - 1,
+ * which is reported).  base = NULL counts as zeros; base = y (same stride) adds in place.
+ *   x             [rows][K], row m at m * x_stride; A [adapters][rank][K]; B [adapters][N][rank];
+ *                 all of `type` F16 or BF16.
+ *   ranks         [adapters], 0 .. rank (others are clamped); NULL: `rank` for all.  What lies
+ *                 in A and B past an adapter's rank does not reach the result.
+ *   scales        [adapters] fp32; NULL: 1.
+ *   base, y       [rows][N] of type `out`, row m at m * y_stride (both).
+ * Products are exact, sums in fp32; the inner sums enter the second product in full fp32
+ * precision (two or three 16-bit parts); y is rounded once.  Deterministic.  rank a multiple
+ * of 8, 8 .. 128; K a multiple of 8; x, A, B, base and y 16-byte aligned, x_stride a multiple
+ * of 8. */
+typedef struct {
+  const void* x;
+  int64_t x_stride;
+  const void* A;
+  const void* B;
+  const int32_t* ids;
+  const int32_t* ranks;
+  const float* scales;
+  const void* base;
+  void* y;
+  int64_t y_stride;
+  int64_t rows;
+  int64_t N;
+  int64_t K;
+  int32_t adapters;
+  int32_t rank;
+  qgemv_out_t type;
+  qgemv_out_t out;
+} qgemv_lora_t;
+
+qgemv_status_t qgemv_run_lora(qgemv_handle_t h, const qgemv_lora_t* lora, cudaStream_t stream);
 
 /* Capacity of qgemv_run_noalloc's scratch, in fp32 column sums: N * ceil(K / 2048) of them. */
 #define QGEMV_NOALLOC_MAX_COLUMN_SUMS 262144

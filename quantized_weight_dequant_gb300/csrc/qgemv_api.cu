@@ -10,6 +10,7 @@
 #include "../../include/qgemv.h"
 #include "qgemm_tc.cuh"
 #include "qgemv_batch.cuh"
+#include "qgemv_handle.cuh"
 #include "qgemv_simple.cuh"
 #include "qgemv_stream.cuh"
 
@@ -23,34 +24,6 @@ using namespace qg;
 
 constexpr int kMaxWarps = 16;                    // per CTA (launch bound 512 threads)
 constexpr size_t kRedBudget = 16 * 1024;         // cross-warp reduction buffer per CTA
-constexpr size_t kWsFloats = size_t{4} << 20;    // split-K column sums: N * K-columns <= 4 Mi
-constexpr int kMaxRanges = 1024;                 // split-K row ranges (one counter each)
-
-struct Handle {
-  int device = 0;
-  int sms = 0;
-  int l2_bytes = 0;
-  size_t smem_optin = 0;
-  int* err = nullptr;
-  float* ws = nullptr;  // split-K column sums
-  int* cnt = nullptr;   // split-K per-range arrival counts, zero between launches
-  int ctas_per_sm = 2;
-  int ksplit = 0;       // 0: split K-columns over CTAs when the workspace holds them; 1: never
-  int grid_per_sm = 0;  // CTAs launched per SM (0: as many as fit, ctas_per_sm)
-  size_t dyn_smem_max[6][3][3] = {};  // [format][R 1/2/4][D 2/3/4]
-  size_t group_smem_max[2][3] = {};   // mixed-format grouped kernel [R 2/4][D 2/3/4]
-  size_t group1_smem_max[6][2][2][3] = {};  // one-format grouped kernels [format][pairs][R 2/4][D 2/3/4]
-  size_t batch_smem_max[6][2] = {};          // small-batch kernels [format][D 2/3]
-  void* encode_tiled = nullptr;              // the driver's cuTensorMapEncodeTiled (null: no TMA path)
-  int tc_cluster_max[3] = {1, 1, 1};         // largest cluster (K splits) the GEMM kernels can run [BT 64/128/256]
-  int force_path = 0;
-  int ring_depth = 0;
-  int rows_per_stage = 0;
-  uint64_t spin_ns = 1000000000ull;
-  int pdl = 0;
-  int test_stall = 0;
-};
-
 bool fmt_ok(int f) { return f >= 0 && f <= 5; }
 
 int k_multiple(int f) {
@@ -492,6 +465,7 @@ const char* qgemv_status_string(qgemv_status_t s) {
     case QGEMV_ERR_OOM: return "out of device memory";
     case QGEMV_ERR_NO_DEVICE: return "no usable sm_103 device";
     case QGEMV_ERR_TOO_LARGE: return "shape exceeds the fixed scratch of qgemv_run_noalloc";
+    case QGEMV_ERR_BAD_INDEX: return "a kernel met an index out of range";
   }
   return "unknown status";
 }
@@ -977,7 +951,7 @@ qgemv_status_t qgemv_check_error(qgemv_handle_t hh, cudaStream_t stream) {
   int e = 0;
   if (cudaMemcpy(&e, h->err, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return QGEMV_ERR_CUDA;
   if (e != 0 && cudaMemset(h->err, 0, sizeof(int)) != cudaSuccess) return QGEMV_ERR_CUDA;
-  return (e & kDevErrTimeout) ? QGEMV_ERR_TIMEOUT : QGEMV_OK;
+  return (e & kDevErrTimeout) ? QGEMV_ERR_TIMEOUT : (e & kDevErrIndex) ? QGEMV_ERR_BAD_INDEX : QGEMV_OK;
 }
 
 }  // extern "C"

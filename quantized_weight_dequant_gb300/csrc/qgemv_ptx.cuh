@@ -5,6 +5,10 @@
 
 namespace qg {
 
+// Bits of the handle's device error word (qgemv_check_error).
+constexpr int kDevErrTimeout = 1;
+constexpr int kDevErrIndex = 2;
+
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }

@@ -46,8 +46,6 @@
 
 namespace qg {
 
-constexpr int kDevErrTimeout = 1;
-
 struct StreamArgs {
   const uint8_t* W;     // stream 1: rows of packed blocks / NVFP4 nibbles
   const uint8_t* W2;    // stream 2: NVFP4 scales (null otherwise)
