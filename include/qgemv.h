@@ -313,7 +313,8 @@ qgemv_status_t qgemv_run_gemm(qgemv_handle_t h, qgemv_format_t fmt, const void* 
  * [kv_heads][page_size][head_dim] elements, contiguous and 16-byte aligned (page_stride * element size a
  * multiple of 16 too; page_stride >= kv_heads * page_size * head_dim).  QGEMV_KV_E4M3: an e4m3
  * code c of token t and head h stands for c * scale[t, h]; k_scale and v_scale: device fp32,
- * [page][kv_heads][page_size], page p at p * scale_stride (ignored for the other types).
+ * [page][kv_heads][page_size], page p at p * scale_stride, 16-byte aligned with scale_stride a
+ * multiple of 4 (ignored for the other types).
  * head_dim 64, 128 or 256; page_size 8 or a multiple of 16. */
 typedef enum { QGEMV_KV_F16 = 1, QGEMV_KV_BF16 = 2, QGEMV_KV_E4M3 = 3 } qgemv_kv_t;
 typedef struct {

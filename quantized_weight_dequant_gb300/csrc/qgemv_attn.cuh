@@ -1,8 +1,41 @@
 // Attention of one new token per request over a paged key-value cache.
+//
+//   s_t = scale q . k_t,   p_t = 2^(s_t log2e - m),   out = sum_t p_t v_t / sum_t p_t
+//
+// in one pass over the cache with a running maximum m: when it moves, the sum and the output
+// are scaled by 2^(m_old - m_new).  Per key-value head the query heads that share it (its group)
+// are the rows of one small matrix product, so the cache is read once for all of them.
+//
+// The kernel is bound by the bytes of the cache, so everything else is arranged around a steady
+// stream of copies:
+//  * Work.  The cache of a request and key-value head is cut into tiles of TT tokens (4 KB or
+//    8 KB of keys).  All tiles of the batch, in the order (request, head, token), are cut into
+//    equal contiguous shares, one per CTA and inside it one per warp, whatever the requests'
+//    lengths: every CTA sums the lengths itself and finds its share, so nothing is planned on
+//    the host and ragged batches keep all SMs busy to the end.
+//  * Copies.  Every warp has its own ring of stages, filled by TMA (a tile's pages are rows of a
+//    five-dimensional tensor: 128-byte row parts, in-page token, part, head, page) and waited
+//    for on an mbarrier.  Page numbers are read one tile ahead of the copies that use them.  No
+//    warp waits for another until the end.
+//  * Products.  mma.sync m16n8k16: q (rows: query heads) times keys (columns: tokens), then the
+//    weights times values.  Memory sets the pace: an SM gets 22 bytes per clock, one 16-token
+//    tile of 128-wide bf16 heads every 370 clocks, whose 32 matrix instructions and about 150
+//    others take the four schedulers some 50 clocks; tcgen05 would add a round trip through
+//    tensor memory for products of 8 rows.
+//  * Precision.  A weight enters the second product as the sum of two 16-bit values.  With at
+//    most 8 heads in a group the low parts are rows 8..15 of the same instruction, which would
+//    be empty otherwise; with 9..16 they are a second instruction.
+//  * 8-bit caches: codes are converted to fp16 in registers (exactly); key scales multiply the
+//    scores, value scales the weights.  The weights are kept within fp16's range by a running
+//    factor c (out = c O): it follows the largest w_t = p_t vscale_t like m follows the scores.
+//  * Join.  A (request, head) that lies inside one warp's share is written by that warp.
+//    Others leave (m, l, O) pieces: in shared memory, which the CTA joins in token order, and
+//    where CTAs share one in the workspace, which the CTA that arrives last joins in CTA order.
+//    The results do not depend on which one that is.
 #pragma once
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
-#include <cuda_fp8.h>
 
 #include <cstdint>
 
@@ -11,64 +44,756 @@
 
 namespace qg {
 
-__device__ __forceinline__ float kv_to_float(const void* p, int64_t i, int type) {
-  if (type == QGEMV_KV_F16) return __half2float(static_cast<const __half*>(p)[i]);
-  if (type == QGEMV_KV_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-  const __nv_fp8_e4m3 v = static_cast<const __nv_fp8_e4m3*>(p)[i];
-  return static_cast<float>(v);
+constexpr int kAttnWarps = 4;
+constexpr int kAttnThreads = 32 * kAttnWarps;
+constexpr int kAttnInfo = 4;  // tile descriptors kept per warp (one more than stages)
+
+struct AttnArgs {
+  const void* q;
+  void* out;
+  float* lse;
+  const int32_t* table;
+  const int32_t* lens;
+  const float* k_scale;
+  const float* v_scale;
+  int64_t q_stride, out_stride, table_stride, scale_stride;
+  float scale_log2;  // scale * log2(e)
+  int window, requests, table_width, q_heads, kv_heads, group, splits;  // splits: groups of up to MR heads per kv head
+  int page_size, pages;
+  int chunk_log2;    // tokens copied at once: the largest power of two that divides the page, at most TT
+  int type;          // element type of q and out
+  int min_tiles;     // a warp's smallest share
+  float* ws;
+  int* cnt;
+  int* err;
+  uint64_t spin_ns;
+  int stall;
+};
+
+// Shapes that follow from the head size and the cache type (KT: qgemv_kv_t).
+template <int D, int KT, int MR>
+struct AttnShape {
+  static constexpr int kEl = KT == QGEMV_KV_E4M3 ? 1 : 2;
+  static constexpr int kRow = D * kEl;                        // bytes of a token's head
+  static constexpr int kRB = kRow < 128 ? kRow : 128;         // bytes of a row part in shared memory
+  static constexpr int kParts = kRow / kRB;
+  static constexpr int kTT = kRow >= 256 ? 16 : 4096 / kRow;  // tokens per tile
+  static constexpr int kTile = kTT * kRow;                    // bytes of keys (and of values)
+  static constexpr int kScaleBytes = KT == QGEMV_KV_E4M3 ? 2 * kTT * 4 : 0;
+  static constexpr int kPiece = MR * (D + 2);                 // floats of a piece: m, l, O
+  static constexpr int kCtasPerSm = kRow == 512 || (D == 256 && MR == 16) ? 1 : 2;
+  static constexpr int kBudget = kCtasPerSm == 1 ? 232448 : 115712;
+  static constexpr int kFixed = 1024 + kAttnWarps * kPiece * 4 + kAttnWarps * (kAttnInfo * 32 + 32) + 2048;  // static ones too
+  static constexpr int kFit = (kBudget - kFixed) / (kAttnWarps * (2 * kTile + kScaleBytes));
+  static constexpr int kStages = kFit < 3 ? kFit : 3;
+  static constexpr int kSmem = kFixed - 2048 + kAttnWarps * kStages * (2 * kTile + kScaleBytes);
+  static_assert(kStages >= 2 && kPiece * 4 <= kStages * 2 * kTile, "shared memory");
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-// The definition, one warp per request and query head: lanes over the head's elements, tokens
-// one after another with a running maximum m and sum l; the sum and the output are scaled by
-// exp(m_old - m_new) when the maximum moves.
-template <int D>
-__global__ void __launch_bounds__(128) attn_decode_kernel(const qgemv_attn_decode_t p, int* err) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int64_t unit = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  if (unit >= static_cast<int64_t>(p.requests) * p.q_heads) return;
-  const int r = static_cast<int>(unit / p.q_heads), g = static_cast<int>(unit % p.q_heads);
-  const int P = p.cache.page_size, head = g / (p.q_heads / p.cache.kv_heads);
-  const int64_t end = static_cast<int64_t>(p.table_width) * P;
-  int64_t len = p.lens[r];
+__device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&v)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t (&v)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+               : "r"(a)
+               : "memory");
+}
+
+template <bool BF>
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  if constexpr (BF)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Two fp32 values as a 16-bit pair (a in the low half), and what the pair leaves of them.
+template <bool BF>
+__device__ __forceinline__ uint32_t pair16(float a, float b) {
+  uint32_t u;
+  if constexpr (BF)
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u) : "f"(b), "f"(a));
+  else
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(u) : "f"(b), "f"(a));
+  return u;
+}
+template <bool BF>
+__device__ __forceinline__ float2 unpair16(uint32_t u) {
+  if constexpr (BF) return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+  return __half22float2(*reinterpret_cast<const __half2*>(&u));
+}
+template <bool BF>
+__device__ __forceinline__ void split16(float a, float b, uint32_t& hi, uint32_t& lo) {
+  hi = pair16<BF>(a, b);
+  const float2 f = unpair16<BF>(hi);
+  lo = pair16<BF>(a - f.x, b - f.y);
+}
+
+// Two e4m3 codes as fp16 (exact).
+__device__ __forceinline__ uint32_t e4m3x2(uint32_t two) {
+  uint32_t u;
+  asm("{.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(u) : "r"(two));
+  return u;
+}
+
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, int x, int row, int part, int head, int page, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(row), "r"(part), "r"(head), "r"(page), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src), "r"(bytes),
+               "r"(bar)
+               : "memory");
+}
+
+// What a warp has to know of a tile when it computes it (shared memory, one per tile in flight).
+struct AttnTile {
+  int r, hx;      // request; kv head * splits + split
+  int tok;        // first token
+  int lo, hi;     // tokens that the request sees
+  int ends;       // bit 0: first tile of its (request, head); bit 1: last
+  uint32_t bad;   // chunks whose page is outside the cache
+  int pad;
+};
+
+// A piece of a (request, head) that more than one warp has a share of; its tiles are lo .. hi.
+struct AttnPiece {
+  int64_t lo, hi;
+  int r, hx;
+};
+
+// Length of request r in tokens, clamped to its row of the table.
+__device__ __forceinline__ int attn_clamp(const AttnArgs& p, int len) {
+  const int64_t end = min(static_cast<int64_t>(p.table_width) * p.page_size, int64_t{0x7fffff00});
   if (len < 0 || len > end) {
-    if (lane == 0) atomicOr(err, kDevErrIndex);
-    len = len < 0 ? 0 : end;
+    atomicOr(p.err, kDevErrIndex);
+    return len < 0 ? 0 : static_cast<int>(end);
   }
-  float q[E], o[E] = {};
-  for (int e = 0; e < E; ++e) q[e] = kv_to_float(p.q, r * p.q_stride + static_cast<int64_t>(g) * D + lane + 32 * e, p.type);
+  return len;
+}
+__device__ __forceinline__ int attn_first(const AttnArgs& p, int len) { return p.window && len > p.window ? len - p.window : 0; }
+
+// Two neighbouring outputs.
+__device__ __forceinline__ void attn_store2(const AttnArgs& p, int64_t at, float a, float b) {
+  uint32_t* o = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + at);
+  *o = p.type == QGEMV_OUT_F16 ? pair16<false>(a, b) : pair16<true>(a, b);
+}
+
+__device__ __forceinline__ float attn_lse(float m, float l) {
+  return l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : __int_as_float(0xff800000);
+}
+
+// Joins pieces i = 0 .. n-1 (at piece(i): m[MR], l[MR], O[MR][D]) of request r and head group hx, in
+// this order, by all threads of the CTA.  The result is written out, or (to != null) left as one
+// piece.  wt: shared memory for n * MR weights, fl: for MR sums.
+template <int D, int MR, class Piece>
+__device__ __forceinline__ void attn_join(const AttnArgs& p, int r, int hx, int n, Piece piece, float* wt, float* fl, float* to) {
+  const int kv = hx / p.splits, g0 = (hx - kv * p.splits) * MR, heads = min(MR, p.group - g0);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const float neg = __int_as_float(0xff800000);
-  float m = neg, l = 0.f;
-  for (int64_t t = p.window ? max(len - p.window, int64_t{0}) : 0; t < len; ++t) {
-    const int page = p.table[r * p.table_stride + t / P];
-    if (page < 0 || page >= p.cache.pages) {
-      if (lane == 0) atomicOr(err, kDevErrIndex);
+  for (int g = warp; g < MR; g += kAttnWarps) {
+    float m = neg, l = 0.f;
+    for (int i = lane; i < n; i += 32) m = fmaxf(m, piece(i)[g]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float base = m == neg ? 0.f : m;
+    for (int i = lane; i < n; i += 32) {
+      const float w = ex2(piece(i)[g] - base);
+      wt[i * MR + g] = w;
+      l += w * piece(i)[MR + g];
+    }
+    l = warp_sum(l);
+    if (lane == 0) {
+      fl[g] = l;
+      if (to) to[g] = m, to[MR + g] = l;
+      if (!to && p.lse && g < heads) p.lse[static_cast<int64_t>(r) * p.q_heads + kv * p.group + g0 + g] = attn_lse(m, l);
+    }
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < heads * (D / 4); e += kAttnThreads) {
+    const int g = e / (D / 4), d = (e - g * (D / 4)) * 4;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) {
+      const float w = wt[i * MR + g];
+      const float4 o = *reinterpret_cast<const float4*>(piece(i) + 2 * MR + g * D + d);
+      s.x += w * o.x, s.y += w * o.y, s.z += w * o.z, s.w += w * o.w;
+    }
+    if (to) {
+      *reinterpret_cast<float4*>(to + 2 * MR + g * D + d) = s;
+    } else {
+      const float l = fl[g], f = l != 0.f ? 1.f / l : 0.f;
+      const int64_t at = r * p.out_stride + static_cast<int64_t>(kv * p.group + g0 + g) * D + d;
+      attn_store2(p, at, s.x * f, s.y * f);
+      attn_store2(p, at + 2, s.z * f, s.w * f);
+    }
+  }
+  __syncthreads();
+}
+
+template <int D, int KT, int MR>
+__global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm)
+    attn_decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const __grid_constant__ AttnArgs p) {
+  using Sh = AttnShape<D, KT, MR>;
+  constexpr bool kBF = KT == QGEMV_KV_BF16, kF8 = KT == QGEMV_KV_E4M3;
+  constexpr int TT = Sh::kTT, S = Sh::kStages, NT = TT / 8;  // NT: 8-token column tiles of the scores
+  constexpr int OT = D / 8;                                  // 8-wide column tiles of the output
+  extern __shared__ uint8_t dyn[];
+  __shared__ int64_t scan[kAttnWarps];
+  __shared__ int64_t start_at[kAttnWarps];  // first tile of each warp within its request
+  __shared__ int start_r[kAttnWarps];
+  __shared__ AttnPiece piece_of[2 * kAttnWarps];  // of each warp the one that began before its share, and the last
+  __shared__ AttnPiece shared_of[2];
+  __shared__ float wt_small[2 * kAttnWarps * MR], fl[MR];
+  __shared__ int last_flag;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int quad = lane & 3, row = lane >> 2;
+  const float neg = __int_as_float(0xff800000);
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t{1023});
+  float* heads_mem = reinterpret_cast<float*>(ring + kAttnWarps * S * 2 * Sh::kTile);
+  uint8_t* scales_mem = reinterpret_cast<uint8_t*>(heads_mem + kAttnWarps * Sh::kPiece);
+  AttnTile* info = reinterpret_cast<AttnTile*>(scales_mem + kAttnWarps * S * Sh::kScaleBytes) + warp * kAttnInfo;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(scales_mem + kAttnWarps * S * Sh::kScaleBytes + kAttnWarps * kAttnInfo * 32) + warp * 4;
+  const uint32_t ring_w = smem_u32(ring) + warp * S * 2 * Sh::kTile;
+  const uint32_t scale_w = smem_u32(scales_mem) + warp * S * Sh::kScaleBytes;
+  if (lane < S) mbar_init(smem_u32(bars + lane), 1);
+  if (lane == 0) {
+    piece_of[2 * warp].r = piece_of[2 * warp + 1].r = -1;
+    fence_mbar_init();
+  }
+
+  // ---- the share of this CTA and of its warps
+  const int hxs = p.kv_heads * p.splits;
+  auto tiles_of = [&](int len) { return (len + TT - 1) / TT - attn_first(p, len) / TT; };
+  const int per = (p.requests + kAttnThreads - 1) / kAttnThreads, r_lo = min(static_cast<int>(threadIdx.x) * per, p.requests),
+            r_hi = min(r_lo + per, p.requests);
+  int64_t mine = 0;
+  bool none = false;  // a request without tokens whose rows this CTA writes
+  for (int r = r_lo; r < r_hi; ++r) {
+    const int n = tiles_of(attn_clamp(p, p.lens[r]));
+    mine += n;
+    none |= n == 0 && r % gridDim.x == blockIdx.x;
+  }
+  mine *= hxs;
+  int64_t upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += u;
+  }
+  if (lane == 31) scan[warp] = upto;
+  const bool any_none = __syncthreads_or(none);
+  int64_t total = 0, before = upto - mine;
+#pragma unroll
+  for (int w = 0; w < kAttnWarps; ++w) {
+    if (w < warp) before += scan[w];
+    total += scan[w];
+  }
+  const int64_t least = static_cast<int64_t>(p.min_tiles) * kAttnWarps;
+  const int ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), (total + least - 1) / least));  // with a share
+  const int cta = blockIdx.x;
+  const bool busy = cta < ctas;
+  const int64_t c_lo = busy ? total * cta / ctas : 0, c_hi = busy ? total * (cta + 1) / ctas : 0;
+  if (busy) {
+#pragma unroll
+    for (int w = 0; w < kAttnWarps; ++w) {
+      const int64_t at = c_lo + (c_hi - c_lo) * w / kAttnWarps;
+      if (at >= before && at < before + mine) {
+        int64_t pre = before;
+        int r = r_lo;
+        for (; r < r_hi - 1; ++r) {
+          const int64_t n = static_cast<int64_t>(tiles_of(attn_clamp(p, p.lens[r]))) * hxs;
+          if (at < pre + n) break;
+          pre += n;
+        }
+        start_r[w] = r;
+        start_at[w] = at - pre;
+      }
+    }
+  }
+  if (any_none) {
+    for (int r = cta; r < p.requests; r += gridDim.x) {
+      if (tiles_of(attn_clamp(p, p.lens[r]))) continue;
+      for (int e = threadIdx.x; e < p.q_heads * (D / 2); e += kAttnThreads) attn_store2(p, r * p.out_stride + 2 * e, 0.f, 0.f);
+      if (p.lse)
+        for (int g = threadIdx.x; g < p.q_heads; g += kAttnThreads) p.lse[static_cast<int64_t>(r) * p.q_heads + g] = neg;
+    }
+  }
+  if (!busy) return;
+  __syncthreads();
+  const int64_t w_lo = c_lo + (c_hi - c_lo) * warp / kAttnWarps, w_hi = c_lo + (c_hi - c_lo) * (warp + 1) / kAttnWarps;
+  const int n_tiles = static_cast<int>(w_hi - w_lo);
+
+  // ---- the walk over the tiles: position of the next tile to describe
+  int it_r = 0, it_hx = 0, it_t = 0, it_first = 0, it_end = 0, it_lo = 0, it_len = 0, it_next = 0;
+  auto enter = [&](int r, int len) {
+    it_r = r;
+    it_len = len;
+    it_lo = attn_first(p, len);
+    it_first = it_lo / TT;
+    it_end = (len + TT - 1) / TT;
+    it_next = r + 1 < p.requests ? p.lens[r + 1] : 0;  // used when this request is through
+  };
+  if (n_tiles > 0) {
+    const int r = start_r[warp];
+    enter(r, attn_clamp(p, p.lens[r]));
+    const int n = it_end - it_first;
+    it_hx = static_cast<int>(start_at[warp] / n);
+    it_t = it_first + static_cast<int>(start_at[warp] - static_cast<int64_t>(it_hx) * n);
+  }
+  const int ch = 1 << p.chunk_log2, chunks = TT >> p.chunk_log2;
+  // Describes the next tile in info[i % kAttnInfo]; lane j gets the page of its chunk j (-1: not
+  // to be copied) and steps on.
+  auto describe = [&](int i) -> int {
+    const int tok = it_t * TT;
+    int page = -1;
+    const int at = tok + (lane << p.chunk_log2);
+    if (lane < chunks && at < it_len && at + ch > it_lo) page = p.table[it_r * p.table_stride + at / p.page_size];
+    if (lane == 0) {
+      AttnTile& d = info[i % kAttnInfo];
+      d.r = it_r;
+      d.hx = it_hx;
+      d.tok = tok;
+      d.lo = it_lo;
+      d.hi = it_len;
+      d.ends = (it_t == it_first ? 1 : 0) | (it_t == it_end - 1 ? 2 : 0);
+    }
+    if (++it_t == it_end) {
+      if (++it_hx == hxs) {
+        it_hx = 0;
+        int r = it_r + 1;
+        while (r < p.requests) {
+          const int len = attn_clamp(p, it_next);
+          enter(r, len);
+          if (it_end > it_first) break;
+          ++r;
+        }
+      }
+      it_t = it_first;
+    }
+    return page;
+  };
+  // Copies tile i, whose pages `describe` gave, into its stage.
+  auto issue = [&](int i, int page) {
+    const int s = i % S;
+    AttnTile& d = info[i % kAttnInfo];
+    const bool want = page != -1 || (lane < chunks && d.tok + (lane << p.chunk_log2) < d.hi && d.tok + (lane << p.chunk_log2) + ch > d.lo);
+    const bool in = page >= 0 && page < p.pages;
+    const uint32_t bad = __ballot_sync(0xffffffffu, want && !in);
+    const uint32_t good = __ballot_sync(0xffffffffu, want && in);
+    const uint32_t bar = smem_u32(bars + s);
+    if (lane == 0) {
+      d.bad = bad;
+      if (bad) atomicOr(p.err, kDevErrIndex);
+      const uint32_t bytes = static_cast<uint32_t>(__popc(good)) * (2 * Sh::kRow + (kF8 ? 8 : 0)) << p.chunk_log2;
+      mbar_arrive_expect_tx(bar, bytes);
+    }
+    __syncwarp();
+    if (want && in) {
+      const int kv = d.hx / p.splits, at = d.tok + (lane << p.chunk_log2), in_page = at % p.page_size;
+      const uint32_t dst = ring_w + s * 2 * Sh::kTile + (lane << p.chunk_log2) * Sh::kRow;
+      tma_load_5d(dst, &map_k, 0, in_page, 0, kv, page, bar);
+      tma_load_5d(dst + Sh::kTile, &map_v, 0, in_page, 0, kv, page, bar);
+      if constexpr (kF8) {
+        const int64_t src = page * p.scale_stride + static_cast<int64_t>(kv) * p.page_size + in_page;
+        const uint32_t sd = scale_w + s * Sh::kScaleBytes + (lane << p.chunk_log2) * 4;
+        bulk_load(sd, p.k_scale + src, 4u << p.chunk_log2, bar);
+        bulk_load(sd + TT * 4, p.v_scale + src, 4u << p.chunk_log2, bar);
+      }
+    }
+  };
+  int next_page = -1;
+  {
+    int pages[S + 1];
+#pragma unroll
+    for (int i = 0; i <= S; ++i) pages[i] = i < n_tiles ? describe(i) : -1;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < S; ++i)
+      if (i < n_tiles && !(p.stall && cta == 0 && warp == 0 && i == 0)) issue(i, pages[i]);
+    next_page = pages[S];
+  }
+
+  // Byte offset of token t of a tile, row part `part`, in shared memory (before the swizzle).
+  auto line_of = [&](int t, int part) {
+    return (t >> p.chunk_log2) * (Sh::kRow << p.chunk_log2) + part * (Sh::kRB << p.chunk_log2) + (t & (ch - 1)) * Sh::kRB;
+  };
+  // 16-byte unit c of the row at `line` after the copy's swizzle (address bits 4.. xor bits 7..).
+  auto unit_of = [&](uint32_t line, int c) { return line + static_cast<uint32_t>((c ^ ((line >> 7) & (Sh::kRB / 16 - 1))) << 4); };
+
+  constexpr int KS = D / 16;  // k steps of the scores
+  uint32_t qa[KS][MR == 8 ? 2 : 4];
+  float q_back[2] = {1.f, 1.f};  // what the fp16 queries of rows `row`, `row` + 8 were divided by
+  float o[OT][4];
+  float m[2] = {neg, neg}, l[2] = {0.f, 0.f}, c[2] = {1.f, 1.f};
+  bool alive = true;
+
+  // Query rows `row` (and `row` + 8) of the tile's group in the order of the matrix product's A operand.
+  auto load_q = [&](const AttnTile& d) {
+    const int kv = d.hx / p.splits, g0 = (d.hx - kv * p.splits) * MR;
+#pragma unroll
+    for (int j = 0; j < MR / 8; ++j) {
+      const int g = g0 + row + 8 * j;
+      const uint16_t* src = static_cast<const uint16_t*>(p.q) + d.r * p.q_stride + static_cast<int64_t>(kv * p.group + g) * D;
+      const bool there = g < p.group;
+      uint32_t u[KS][2];
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        if constexpr (kF8) {  // four consecutive elements: the order of four codes in a register
+          const uint2 v = there ? *reinterpret_cast<const uint2*>(src + 16 * k + 4 * quad) : make_uint2(0, 0);
+          u[k][0] = v.x, u[k][1] = v.y;
+        } else {
+          u[k][0] = there ? *reinterpret_cast<const uint32_t*>(src + 16 * k + 2 * quad) : 0u;
+          u[k][1] = there ? *reinterpret_cast<const uint32_t*>(src + 16 * k + 2 * quad + 8) : 0u;
+        }
+      }
+      if (kF8 && p.type == QGEMV_OUT_BF16) {
+        // bf16 queries as fp16 times a power of two per head: the largest in [2^14, 2^15), so every
+        // one within 2^28 of it is exact
+        float top = 0.f;
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float2 f = unpair16<true>(u[k][e]);
+            top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+          }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const int ex = (__float_as_int(top) >> 23) & 0xff;
+        // 2^(141 - ex) takes 1.x 2^(ex - 127) to 1.x 2^14; both factors stay normal for 15 <= ex <= 254
+        const bool fine = ex >= 15 && ex < 255;
+        const float by = fine ? __int_as_float((127 + 141 - ex) << 23) : 1.f;
+        q_back[j] = fine ? __int_as_float((127 - 141 + ex) << 23) : 1.f;
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float2 f = unpair16<true>(u[k][e]);
+            u[k][e] = pair16<false>(f.x * by, f.y * by);
+          }
+      }
+#pragma unroll
+      for (int k = 0; k < KS; ++k) qa[k][j] = u[k][0], qa[k][MR / 8 + j] = u[k][1];
+    }
+  };
+
+  // The sums of the finished (part of a) request and head: out, or a piece.
+  auto finish = [&](const AttnTile& d, int i, bool whole, int slot) {
+    const int kv = d.hx / p.splits, g0 = (d.hx - kv * p.splits) * MR;
+#pragma unroll
+    for (int j = 0; j < MR / 8; ++j) {
+      l[j] += __shfl_xor_sync(0xffffffffu, l[j], 1);
+      l[j] += __shfl_xor_sync(0xffffffffu, l[j], 2);
+    }
+    float* piece = slot == 0 ? heads_mem + warp * Sh::kPiece : reinterpret_cast<float*>(ring + warp * S * 2 * Sh::kTile);
+    if (!whole && lane == 0) {
+      const int64_t lo = w_lo + i - (d.tok / TT - d.lo / TT);
+      piece_of[2 * warp + slot] = AttnPiece{lo, lo + (d.hi + TT - 1) / TT - d.lo / TT, d.r, d.hx};
+    }
+#pragma unroll
+    for (int j = 0; j < MR / 8; ++j) {
+      const int g = row + 8 * j;
+      const bool there = g0 + g < p.group;
+      const float f = (whole ? (l[j] != 0.f ? 1.f / l[j] : 0.f) : 1.f) * (kF8 ? c[j] : 1.f);
+      if (quad == 0) {
+        if (!whole)
+          piece[g] = m[j], piece[MR + g] = l[j];
+        else if (there && p.lse)
+          p.lse[static_cast<int64_t>(d.r) * p.q_heads + kv * p.group + g0 + g] = attn_lse(m[j], l[j]);
+      }
+      const int64_t at = d.r * p.out_stride + static_cast<int64_t>(kv * p.group + g0 + g) * D;
+      auto put = [&](int e, float a, float b) {
+        if (!whole)
+          *reinterpret_cast<float2*>(piece + 2 * MR + g * D + e) = make_float2(a, b);
+        else if (there)
+          attn_store2(p, at + e, a, b);
+      };
+#pragma unroll
+      for (int t = 0; t < OT; ++t) {
+        if constexpr (kF8) {  // column tiles 2 i and 2 i + 1 hold the even and the odd elements
+          if (t & 1) continue;
+          float a[2], b[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            a[e] = (MR == 8 ? o[t][e] + o[t][2 + e] : o[t][2 * j + e]) * f;
+            b[e] = (MR == 8 ? o[t + 1][e] + o[t + 1][2 + e] : o[t + 1][2 * j + e]) * f;
+          }
+          put(8 * t + 4 * quad, a[0], b[0]);
+          put(8 * t + 4 * quad + 2, a[1], b[1]);
+        } else {
+          const float a = MR == 8 ? o[t][0] + o[t][2] : o[t][2 * j], b = MR == 8 ? o[t][1] + o[t][3] : o[t][2 * j + 1];
+          put(8 * t + 2 * quad, a * f, b * f);
+        }
+      }
+    }
+  };
+
+  bool begun = false;  // the current (request, head) began in this warp's share
+  for (int i = 0; i < n_tiles; ++i) {
+    const int s = i % S;
+    const AttnTile d = info[i % kAttnInfo];
+    if (i == 0 || (d.ends & 1)) {
+      begun = d.ends & 1;
+      load_q(d);
+#pragma unroll
+      for (int t = 0; t < OT; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
+      m[0] = m[1] = neg;
+      l[0] = l[1] = 0.f;
+      c[0] = c[1] = 0.f;
+    }
+    if (alive && !mbar_wait_bounded(smem_u32(bars + s), (i / S) & 1, p.spin_ns)) {
+      alive = false;
+      if (lane == 0) atomicOr(p.err, kDevErrTimeout);
+    }
+    alive = __all_sync(0xffffffffu, alive);
+    const uint32_t kb = ring_w + s * 2 * Sh::kTile, vb = kb + Sh::kTile;
+    const bool edge = d.tok < d.lo || d.tok + TT > d.hi || d.bad;
+
+    // scores: rows are heads, columns tokens
+    float sc[NT][4];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) sc[t][0] = sc[t][1] = sc[t][2] = sc[t][3] = 0.f;
+#pragma unroll
+    for (int b = 0; b < TT / 16; ++b) {
+      const int tl = 16 * b + (lane >> 4) * 8 + (lane & 7), half = (lane >> 3) & 1;  // this lane's row of the 8x8 matrices
+      if constexpr (!kF8) {
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          uint32_t w[4];
+          ldsm4(unit_of(kb + line_of(tl, k / 4), (k % 4) * 2 + half), w);
+          if constexpr (MR == 8) {
+            mma16816<kBF>(sc[2 * b], qa[k][0], 0u, qa[k][1], 0u, w[0], w[1]);
+            mma16816<kBF>(sc[2 * b + 1], qa[k][0], 0u, qa[k][1], 0u, w[2], w[3]);
+          } else {
+            mma16816<kBF>(sc[2 * b], qa[k][0], qa[k][1], qa[k][2], qa[k][3], w[0], w[1]);
+            mma16816<kBF>(sc[2 * b + 1], qa[k][0], qa[k][1], qa[k][2], qa[k][3], w[2], w[3]);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < KS; k += 2) {  // 16 codes per unit: two k steps per load
+          uint32_t w[4];
+          ldsm4(unit_of(kb + line_of(tl, k * 16 / Sh::kRB), (k * 16 % Sh::kRB) / 16 + half), w);
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              const uint32_t u = w[2 * n + e], b0 = e4m3x2(u & 0xffffu), b1 = e4m3x2(u >> 16);
+              if constexpr (MR == 8)
+                mma16816<false>(sc[2 * b + n], qa[k + e][0], 0u, qa[k + e][1], 0u, b0, b1);
+              else
+                mma16816<false>(sc[2 * b + n], qa[k + e][0], qa[k + e][1], qa[k + e][2], qa[k + e][3], b0, b1);
+            }
+        }
+      }
+    }
+    // softmax over the tile: this lane has tokens 8 t + 2 quad + {0, 1}
+    float2 vsc[NT];
+    float top[2] = {neg, neg};
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      float2 ks = make_float2(p.scale_log2, p.scale_log2);
+      if constexpr (kF8) {
+        const uint32_t sa = scale_w + s * Sh::kScaleBytes + (8 * t + 2 * quad) * 4;
+        asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(ks.x), "=f"(ks.y) : "r"(sa));
+        asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(vsc[t].x), "=f"(vsc[t].y) : "r"(sa + TT * 4));
+        ks.x *= p.scale_log2, ks.y *= p.scale_log2;
+      }
+#pragma unroll
+      for (int j = 0; j < MR / 8; ++j) {
+        sc[t][2 * j] *= kF8 ? ks.x * q_back[j] : ks.x;
+        sc[t][2 * j + 1] *= kF8 ? ks.y * q_back[j] : ks.y;
+      }
+      if (edge) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int tk = 8 * t + 2 * quad + e;
+          if (d.tok + tk < d.lo || d.tok + tk >= d.hi || (d.bad >> (tk >> p.chunk_log2) & 1)) {
+            sc[t][e] = sc[t][2 + e] = neg;
+            (e ? vsc[t].y : vsc[t].x) = 0.f;
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < MR / 8; ++j) top[j] = fmaxf(top[j], fmaxf(sc[t][2 * j], sc[t][2 * j + 1]));
+    }
+    bool moved = false;
+    float keep[2] = {1.f, 1.f};
+#pragma unroll
+    for (int j = 0; j < MR / 8; ++j) {
+      top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], 1));
+      top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], 2));
+      const float mn = fmaxf(m[j], top[j]), base = mn == neg ? 0.f : mn;
+      keep[j] = ex2(m[j] - base);
+      moved |= mn > m[j];
+      m[j] = mn;
+      l[j] *= keep[j];
+      float largest = 0.f;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        float a = ex2(sc[t][2 * j] - base), b = ex2(sc[t][2 * j + 1] - base);
+        l[j] += a + b;
+        if constexpr (kF8) {
+          a *= vsc[t].x, b *= vsc[t].y;
+          largest = fmaxf(largest, fmaxf(fabsf(a), fabsf(b)));
+        }
+        sc[t][2 * j] = a;
+        sc[t][2 * j + 1] = b;
+      }
+      if constexpr (kF8) {
+        // out = c O: c takes the change of m; O is scaled only when the weights outgrow it
+        largest = fmaxf(largest, __shfl_xor_sync(0xffffffffu, largest, 1));
+        largest = fmaxf(largest, __shfl_xor_sync(0xffffffffu, largest, 2));
+        c[j] *= keep[j];
+        keep[j] = 1.f;
+        if (largest > c[j]) {
+          const float cn = __int_as_float((__float_as_int(largest) & 0x7f800000) + 0x00800000);  // the power of two above
+          keep[j] = c[j] / cn;
+          c[j] = cn;
+        }
+        const float inv = c[j] > 0.f ? 1.f / c[j] : 0.f;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) sc[t][2 * j] *= inv, sc[t][2 * j + 1] *= inv;
+      }
+    }
+    if constexpr (kF8) moved = keep[0] != 1.f || (MR == 16 && keep[1] != 1.f);
+    if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+      for (int t = 0; t < OT; ++t) {
+        o[t][0] *= keep[0], o[t][1] *= keep[0];
+        o[t][2] *= keep[MR / 8 - 1], o[t][3] *= keep[MR / 8 - 1];
+      }
+    }
+    if (edge) {  // what the values of unseen tokens hold must not meet their zero weights
+      for (int e = lane; e < Sh::kTile / 16; e += 32) {
+        const int tk = e / (Sh::kRow / 16), u = e - tk * (Sh::kRow / 16);
+        if (d.tok + tk < d.lo || d.tok + tk >= d.hi || (d.bad >> (tk >> p.chunk_log2) & 1)) {
+          const uint32_t a = vb + line_of(tk, u / (Sh::kRB / 16)) + (u % (Sh::kRB / 16)) * 16;
+          asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0u) : "memory");
+        }
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before a later copy into this stage
+      __syncwarp();
+    }
+    // weights times values
+#pragma unroll
+    for (int b = 0; b < TT / 16; ++b) {
+      uint32_t hi[2][2], lo[2][2];  // [row half][token half]
+#pragma unroll
+      for (int j = 0; j < MR / 8; ++j)
+#pragma unroll
+        for (int n = 0; n < 2; ++n) split16<kBF>(sc[2 * b + n][2 * j], sc[2 * b + n][2 * j + 1], hi[j][n], lo[j][n]);
+      const int tl = 16 * b + (lane & 15);  // matrices: tokens 0..7, 8..15 of two 16-byte units
+      auto add = [&](float (&acc)[4], uint32_t b0, uint32_t b1) {
+        if constexpr (MR == 8) {
+          mma16816<kBF>(acc, hi[0][0], lo[0][0], hi[0][1], lo[0][1], b0, b1);
+        } else {
+          mma16816<kBF>(acc, hi[0][0], hi[1][0], hi[0][1], hi[1][1], b0, b1);
+          mma16816<kBF>(acc, lo[0][0], lo[1][0], lo[0][1], lo[1][1], b0, b1);
+        }
+      };
+#pragma unroll
+      for (int u = 0; u < Sh::kRow / 16; u += 2) {
+        uint32_t w[4];
+        ldsm4t(unit_of(vb + line_of(tl, u / (Sh::kRB / 16)), u % (Sh::kRB / 16) + (lane >> 4)), w);
+        if constexpr (!kF8) {
+          add(o[u], w[0], w[1]);
+          add(o[u + 1], w[2], w[3]);
+        } else {
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            // bytes: token a (even, odd element), token a + 1 (even, odd element)
+            const uint32_t x = __byte_perm(w[2 * n], 0, 0x3120), y = __byte_perm(w[2 * n + 1], 0, 0x3120);
+            add(o[2 * (u + n)], e4m3x2(x & 0xffffu), e4m3x2(y & 0xffffu));
+            add(o[2 * (u + n) + 1], e4m3x2(x >> 16), e4m3x2(y >> 16));
+          }
+        }
+      }
+    }
+    const bool last = i == n_tiles - 1;
+    if ((d.ends & 2) && begun) {
+      finish(d, i, true, 0);
+    } else if ((d.ends & 2) && !last) {
+      finish(d, i, false, 0);  // began before this share: the first piece
+    } else if (last) {
+      __syncwarp();  // the piece goes where the copies were
+      finish(d, i, false, 1);  // goes on behind this share, or is all of it
+    }
+    __syncwarp();  // every lane is done with the stage and with info[i]
+    if (i + S < n_tiles && alive) {
+      issue(i + S, next_page);
+      next_page = i + S + 1 < n_tiles ? describe(i + S + 1) : -1;
+      __syncwarp();
+    }
+  }
+  if (!alive) {  // copies still in flight after a wait that gave up
+    for (int s = 0; s < S; ++s) {
+      mbar_wait_bounded(smem_u32(bars + s), 0, p.spin_ns);
+      mbar_wait_bounded(smem_u32(bars + s), 1, p.spin_ns);
+    }
+  }
+  __syncthreads();
+
+  // ---- join: the warps' pieces in order; those of one (request, head) follow one another
+  int shared_n = 0;  // those that reach beyond this CTA: at most its first and its last
+  for (int k = 0; k < 2 * kAttnWarps;) {
+    if (piece_of[k].r < 0) {
+      ++k;
       continue;
     }
-    const int64_t line = static_cast<int64_t>(head) * P + t % P, at = page * p.cache.page_stride + line * D;
-    const int64_t sat = page * p.cache.scale_stride + line;
-    const bool coded = p.cache.type == QGEMV_KV_E4M3;
-    float s = 0.f;
-    for (int e = 0; e < E; ++e) s += q[e] * kv_to_float(p.cache.k, at + lane + 32 * e, p.cache.type);
-    s = warp_sum(s) * p.scale;
-    if (coded) s *= p.cache.k_scale[sat];
-    const float mn = fmaxf(m, s), base = mn == neg ? 0.f : mn;
-    const float keep = expf(m - base), w = expf(s - base);
-    m = mn;
-    l = l * keep + w;
-    const float wv = coded ? w * p.cache.v_scale[sat] : w;
-    for (int e = 0; e < E; ++e)
-      o[e] = o[e] * keep + (w != 0.f ? wv * kv_to_float(p.cache.v, at + lane + 32 * e, p.cache.type) : 0.f);
+    const AttnPiece a = piece_of[k];
+    uint32_t list = 0;  // slots of the pieces, four bits each
+    int n = 0;
+    for (; k < 2 * kAttnWarps; ++k) {
+      if (piece_of[k].r < 0) continue;
+      if (piece_of[k].r != a.r || piece_of[k].hx != a.hx) break;
+      list |= static_cast<uint32_t>(k) << (4 * n++);
+    }
+    auto piece = [&](int i) -> const float* {
+      const int q = list >> (4 * i) & 15;
+      return q & 1 ? reinterpret_cast<const float*>(ring + (q >> 1) * S * 2 * Sh::kTile) : heads_mem + (q >> 1) * Sh::kPiece;
+    };
+    const bool inside = a.lo >= c_lo && a.hi <= c_hi;
+    float* to = inside ? nullptr : p.ws + static_cast<int64_t>(2 * cta + (a.lo >= c_lo ? 1 : 0)) * Sh::kPiece;
+    attn_join<D, MR>(p, a.r, a.hx, n, piece, wt_small, fl, to);
+    if (!inside) {
+      if (threadIdx.x == 0) shared_of[shared_n] = a;
+      ++shared_n;
+    }
   }
-  for (int e = 0; e < E; ++e) {
-    const float v = l != 0.f ? o[e] / l : 0.f;
-    const int64_t at = r * p.out_stride + static_cast<int64_t>(g) * D + lane + 32 * e;
-    if (p.type == QGEMV_OUT_F16)
-      static_cast<__half*>(p.out)[at] = __float2half_rn(v);
-    else
-      static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(v);
+  for (int k = 0; k < shared_n; ++k) {
+    __threadfence();
+    __syncthreads();
+    const AttnPiece a = shared_of[k];
+    // shares are [floor(total c / ctas), floor(total (c + 1) / ctas)): the CTAs of the first and the last tile
+    const int first = static_cast<int>(((a.lo + 1) * ctas - 1) / total), n = static_cast<int>((a.hi * ctas - 1) / total) - first + 1;
+    if (threadIdx.x == 0) {
+      last_flag = atomicAdd(p.cnt + first, 1) == n - 1;
+      if (last_flag) p.cnt[first] = 0;  // for the next launch
+      __threadfence();
+    }
+    __syncthreads();
+    if (!last_flag) continue;
+    auto piece = [&](int i) -> const float* { return p.ws + static_cast<int64_t>(2 * (first + i) + (i == 0 ? 1 : 0)) * Sh::kPiece; };
+    attn_join<D, MR>(p, a.r, a.hx, n, piece, reinterpret_cast<float*>(ring), fl, nullptr);
   }
-  if (p.lse && lane == 0) p.lse[static_cast<int64_t>(r) * p.q_heads + g] = l != 0.f ? m + logf(l) : neg;
 }
 
 }  // namespace qg

@@ -21,6 +21,7 @@ inline qgemv_status_t check_cache(const qgemv_kv_cache_t& c) {
     return QGEMV_ERR_BAD_SHAPE;
   if (c.type == QGEMV_KV_E4M3 && (c.scale_stride < lines || c.scale_stride > (int64_t{1} << 32))) return QGEMV_ERR_BAD_SHAPE;
   if (!aligned16(c.k) || !aligned16(c.v) || c.page_stride * kv_elem_bytes(c) % 16) return QGEMV_ERR_MISALIGNED;
+  if (c.type == QGEMV_KV_E4M3 && (!aligned16(c.k_scale) || !aligned16(c.v_scale) || c.scale_stride % 4)) return QGEMV_ERR_MISALIGNED;
   return QGEMV_OK;
 }
 

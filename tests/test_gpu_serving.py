@@ -638,3 +638,19 @@ def test_descriptions_refuse_wrong_tensors():
         qgemv.attn_decode_desc(c, q, table[:1], lens, q, 1.0)
     with pytest.raises(ValueError):
         qgemv.lora_desc(k[0, 0], k[0], k[0], lens, k[0, 0])
+
+
+def test_attention_that_gives_up_waiting_reports_it_and_recovers(h):
+    lens = [700, 30]
+    want, lse, *_ = attend_case(h, lens, 8, 2, 128, "f16", "f16", 16, seed=9)
+    qgemv.set_option(h, qgemv.OPT_SPIN_LIMIT_NS, 2_000_000)
+    qgemv.set_option(h, qgemv.OPT_TEST_STALL, 1)
+    try:
+        attend_case(h, lens, 8, 2, 128, "f16", "f16", 16, seed=9)
+        assert qgemv.check_error(h) == qgemv.ERR_TIMEOUT
+    finally:
+        qgemv.set_option(h, qgemv.OPT_TEST_STALL, 0)
+        qgemv.set_option(h, qgemv.OPT_SPIN_LIMIT_NS, 1_000_000_000)
+    got, lse2, *_ = attend_case(h, lens, 8, 2, 128, "f16", "f16", 16, seed=9)
+    assert qgemv.check_error(h) == qgemv.OK
+    assert torch.equal(want, got) and torch.equal(lse, lse2)
