@@ -60,9 +60,12 @@ struct AttnArgs {
   float scale_log2;  // scale * log2(e)
   int window, requests, table_width, q_heads, kv_heads, group, splits;  // splits: groups of up to MR heads per kv head
   int page_size, pages;
+  uint32_t page_mul;  // t / page_size = (t * page_mul) >> 32 >> page_shift for 0 <= t < 2^31
+  int page_shift;
   int chunk_log2;    // tokens copied at once: the largest power of two that divides the page, at most TT
   int type;          // element type of q and out
-  int min_tiles;     // a warp's smallest share
+  int min_units;     // a CTA's smallest share
+  int seg_cost;      // units that a (request, head) costs beyond its tiles
   float* ws;
   int* cnt;
   int* err;
@@ -83,7 +86,7 @@ struct AttnShape {
   static constexpr int kPiece = MR * (D + 2);                 // floats of a piece: m, l, O
   static constexpr int kCtasPerSm = kRow == 512 || (D == 256 && MR == 16) ? 1 : 2;
   static constexpr int kBudget = kCtasPerSm == 1 ? 232448 : 115712;
-  static constexpr int kFixed = 1024 + kAttnWarps * kPiece * 4 + kAttnWarps * (kAttnInfo * 32 + 32) + 2048;  // static ones too
+  static constexpr int kFixed = 1024 + kAttnWarps * kPiece * 4 + kAttnWarps * (kAttnInfo * 40 + 32) + 2048;  // static ones too
   static constexpr int kFit = (kBudget - kFixed) / (kAttnWarps * (2 * kTile + kScaleBytes));
   static constexpr int kStages = kFit < 3 ? kFit : 3;
   static constexpr int kSmem = kFixed - 2048 + kAttnWarps * kStages * (2 * kTile + kScaleBytes);
@@ -169,14 +172,20 @@ struct AttnTile {
   int lo, hi;     // tokens that the request sees
   int ends;       // bit 0: first tile of its (request, head); bit 1: last
   uint32_t bad;   // chunks whose page is outside the cache
-  int pad;
+  int64_t at;     // first unit of the (request, head)
 };
 
-// A piece of a (request, head) that more than one warp has a share of; its tiles are lo .. hi.
+static_assert(sizeof(AttnTile) == 40, "shared memory layout");
+
+// A piece of a (request, head) that more than one warp has a share of; its tiles are the units lo .. hi.
 struct AttnPiece {
   int64_t lo, hi;
   int r, hx;
 };
+
+__device__ __forceinline__ int attn_page(const AttnArgs& p, int t) {
+  return static_cast<int>(__umulhi(static_cast<uint32_t>(t), p.page_mul) >> p.page_shift);
+}
 
 // Length of request r in tokens, clamped to its row of the table.
 __device__ __forceinline__ int attn_clamp(const AttnArgs& p, int len) {
@@ -189,6 +198,18 @@ __device__ __forceinline__ int attn_clamp(const AttnArgs& p, int len) {
 }
 __device__ __forceinline__ int attn_first(const AttnArgs& p, int len) { return p.window && len > p.window ? len - p.window : 0; }
 
+// The kv head and the first query head in its group of head group hx.
+template <int MR>
+__device__ __forceinline__ void attn_group(const AttnArgs& p, int hx, int& kv, int& g0) {
+  kv = p.splits == 1 ? hx : hx / p.splits;
+  g0 = (hx - kv * p.splits) * MR;
+}
+
+// a / b for b < 2^31: 32-bit arithmetic where a allows it.
+__device__ __forceinline__ int64_t attn_div(int64_t a, int b) {
+  return a >> 32 ? a / b : static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b));
+}
+
 // Two neighbouring outputs.
 __device__ __forceinline__ void attn_store2(const AttnArgs& p, int64_t at, float a, float b) {
   uint32_t* o = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + at);
@@ -200,51 +221,56 @@ __device__ __forceinline__ float attn_lse(float m, float l) {
 }
 
 // Joins pieces i = 0 .. n-1 (at piece(i): m[MR], l[MR], O[MR][D]) of request r and head group hx, in
-// this order, by all threads of the CTA.  The result is written out, or (to != null) left as one
-// piece.  wt: shared memory for n * MR weights, fl: for MR sums.
-template <int D, int MR, class Piece>
-__device__ __forceinline__ void attn_join(const AttnArgs& p, int r, int hx, int n, Piece piece, float* wt, float* fl, float* to) {
-  const int kv = hx / p.splits, g0 = (hx - kv * p.splits) * MR, heads = min(MR, p.group - g0);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// this order, by all threads of the CTA: a thread takes four elements of a head through U pieces at
+// a time, whose loads are all in flight together.  The result is written out, or (to != null) left as
+// one piece.
+template <int D, int MR, int U, bool SMEM, class Piece>
+__device__ __forceinline__ void attn_join(const AttnArgs& p, int r, int hx, int n, Piece piece, float* to) {
+  int kv, g0;
+  attn_group<MR>(p, hx, kv, g0);
+  const int heads = min(MR, p.group - g0);
   const float neg = __int_as_float(0xff800000);
-  for (int g = warp; g < MR; g += kAttnWarps) {
-    float m = neg, l = 0.f;
-    for (int i = lane; i < n; i += 32) m = fmaxf(m, piece(i)[g]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float base = m == neg ? 0.f : m;
-    for (int i = lane; i < n; i += 32) {
-      const float w = ex2(piece(i)[g] - base);
-      wt[i * MR + g] = w;
-      l += w * piece(i)[MR + g];
-    }
-    l = warp_sum(l);
-    if (lane == 0) {
-      fl[g] = l;
-      if (to) to[g] = m, to[MR + g] = l;
-      if (!to && p.lse && g < heads) p.lse[static_cast<int64_t>(r) * p.q_heads + kv * p.group + g0 + g] = attn_lse(m, l);
-    }
-  }
-  __syncthreads();
   for (int e = threadIdx.x; e < heads * (D / 4); e += kAttnThreads) {
     const int g = e / (D / 4), d = (e - g * (D / 4)) * 4;
+    float m = neg, l = 0.f;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int i = 0; i < n; ++i) {
-      const float w = wt[i * MR + g];
-      const float4 o = *reinterpret_cast<const float4*>(piece(i) + 2 * MR + g * D + d);
-      s.x += w * o.x, s.y += w * o.y, s.z += w * o.z, s.w += w * o.w;
+    for (int i0 = 0; i0 < n; i0 += U) {
+      float mi[U], li[U];
+      float4 o[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float* q = piece(min(i0 + u, n - 1));
+        const float4* oq = reinterpret_cast<const float4*>(q + 2 * MR + g * D + d);
+        mi[u] = SMEM ? q[g] : __ldcg(q + g);
+        li[u] = SMEM ? q[MR + g] : __ldcg(q + MR + g);
+        o[u] = SMEM ? *oq : __ldcg(oq);
+      }
+      float mn = m;
+#pragma unroll
+      for (int u = 0; u < U; ++u) mn = fmaxf(mn, mi[u]);
+      const float base = mn == neg ? 0.f : mn, f = ex2(m - base);
+      m = mn;
+      l *= f;
+      s.x *= f, s.y *= f, s.z *= f, s.w *= f;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (i0 + u >= n) break;
+        const float w = ex2(mi[u] - base);
+        l += w * li[u];
+        s.x += w * o[u].x, s.y += w * o[u].y, s.z += w * o[u].z, s.w += w * o[u].w;
+      }
     }
     if (to) {
+      if (d == 0) to[g] = m, to[MR + g] = l;
       *reinterpret_cast<float4*>(to + 2 * MR + g * D + d) = s;
     } else {
-      const float l = fl[g], f = l != 0.f ? 1.f / l : 0.f;
+      const float f = l != 0.f ? 1.f / l : 0.f;
       const int64_t at = r * p.out_stride + static_cast<int64_t>(kv * p.group + g0 + g) * D + d;
       attn_store2(p, at, s.x * f, s.y * f);
       attn_store2(p, at + 2, s.z * f, s.w * f);
+      if (d == 0 && p.lse) p.lse[static_cast<int64_t>(r) * p.q_heads + kv * p.group + g0 + g] = attn_lse(m, l);
     }
   }
-  __syncthreads();
 }
 
 template <int D, int KT, int MR>
@@ -260,8 +286,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
   __shared__ int start_r[kAttnWarps];
   __shared__ AttnPiece piece_of[2 * kAttnWarps];  // of each warp the one that began before its share, and the last
   __shared__ AttnPiece shared_of[2];
-  __shared__ float wt_small[2 * kAttnWarps * MR], fl[MR];
-  __shared__ int last_flag;
+  __shared__ int shared_from[2], shared_count[2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int quad = lane & 3, row = lane >> 2;
   const float neg = __int_as_float(0xff800000);
@@ -269,7 +294,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
   float* heads_mem = reinterpret_cast<float*>(ring + kAttnWarps * S * 2 * Sh::kTile);
   uint8_t* scales_mem = reinterpret_cast<uint8_t*>(heads_mem + kAttnWarps * Sh::kPiece);
   AttnTile* info = reinterpret_cast<AttnTile*>(scales_mem + kAttnWarps * S * Sh::kScaleBytes) + warp * kAttnInfo;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(scales_mem + kAttnWarps * S * Sh::kScaleBytes + kAttnWarps * kAttnInfo * 32) + warp * 4;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(scales_mem + kAttnWarps * S * Sh::kScaleBytes + kAttnWarps * kAttnInfo * 40) + warp * 4;
   const uint32_t ring_w = smem_u32(ring) + warp * S * 2 * Sh::kTile;
   const uint32_t scale_w = smem_u32(scales_mem) + warp * S * Sh::kScaleBytes;
   if (lane < S) mbar_init(smem_u32(bars + lane), 1);
@@ -280,15 +305,21 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
 
   // ---- the share of this CTA and of its warps
   const int hxs = p.kv_heads * p.splits;
+  // Shares are counted in units: a tile is one, and a (request, head) begins with p.seg_cost more, for
+  // what it takes to begin and end one.
   auto tiles_of = [&](int len) { return (len + TT - 1) / TT - attn_first(p, len) / TT; };
+  auto units_of = [&](int len) {
+    const int n = tiles_of(len);
+    return n ? n + p.seg_cost : 0;
+  };
   const int per = (p.requests + kAttnThreads - 1) / kAttnThreads, r_lo = min(static_cast<int>(threadIdx.x) * per, p.requests),
             r_hi = min(r_lo + per, p.requests);
   int64_t mine = 0;
   bool none = false;  // a request without tokens whose rows this CTA writes
   for (int r = r_lo; r < r_hi; ++r) {
-    const int n = tiles_of(attn_clamp(p, p.lens[r]));
+    const int n = units_of(attn_clamp(p, p.lens[r]));
     mine += n;
-    none |= n == 0 && r % gridDim.x == blockIdx.x;
+    none |= n == 0;
   }
   mine *= hxs;
   int64_t upto = mine;
@@ -305,20 +336,27 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
     if (w < warp) before += scan[w];
     total += scan[w];
   }
-  const int64_t least = static_cast<int64_t>(p.min_tiles) * kAttnWarps;
-  const int ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), (total + least - 1) / least));  // with a share
   const int cta = blockIdx.x;
+  const int ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), attn_div(total + p.min_units - 1, p.min_units)));  // with a share
   const bool busy = cta < ctas;
-  const int64_t c_lo = busy ? total * cta / ctas : 0, c_hi = busy ? total * (cta + 1) / ctas : 0;
+  const int64_t each = busy ? attn_div(total, ctas) : 0;  // the first `more` CTAs have one unit more
+  const int more = static_cast<int>(total - each * ctas);
+  const int64_t c_lo = each * cta + min(cta, more), c_hi = c_lo + each + (cta < more ? 1 : 0);
+  auto cta_of = [&](int64_t unit) {
+    const int64_t big = (each + 1) * more;
+    return static_cast<int>(unit < big ? attn_div(unit, static_cast<int>(each + 1)) : more + attn_div(unit - big, static_cast<int>(each)));
+  };
+  auto warp_lo = [&](int w) { return c_lo + ((c_hi - c_lo) * w >> 2); };
+  static_assert(kAttnWarps == 4, "warp shares are quarters");
   if (busy) {
 #pragma unroll
     for (int w = 0; w < kAttnWarps; ++w) {
-      const int64_t at = c_lo + (c_hi - c_lo) * w / kAttnWarps;
+      const int64_t at = warp_lo(w);
       if (at >= before && at < before + mine) {
         int64_t pre = before;
         int r = r_lo;
         for (; r < r_hi - 1; ++r) {
-          const int64_t n = static_cast<int64_t>(tiles_of(attn_clamp(p, p.lens[r]))) * hxs;
+          const int64_t n = static_cast<int64_t>(units_of(attn_clamp(p, p.lens[r]))) * hxs;
           if (at < pre + n) break;
           pre += n;
         }
@@ -337,11 +375,11 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
   }
   if (!busy) return;
   __syncthreads();
-  const int64_t w_lo = c_lo + (c_hi - c_lo) * warp / kAttnWarps, w_hi = c_lo + (c_hi - c_lo) * (warp + 1) / kAttnWarps;
-  const int n_tiles = static_cast<int>(w_hi - w_lo);
 
   // ---- the walk over the tiles: position of the next tile to describe
   int it_r = 0, it_hx = 0, it_t = 0, it_first = 0, it_end = 0, it_lo = 0, it_len = 0, it_next = 0;
+  int64_t left = warp_lo(warp + 1) - warp_lo(warp);  // units of the share still to be walked
+  int64_t it_at = 0;                                 // first unit of the current (request, head)
   auto enter = [&](int r, int len) {
     it_r = r;
     it_len = len;
@@ -350,13 +388,17 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
     it_end = (len + TT - 1) / TT;
     it_next = r + 1 < p.requests ? p.lens[r + 1] : 0;  // used when this request is through
   };
-  if (n_tiles > 0) {
+  if (left > 0) {
     const int r = start_r[warp];
     enter(r, attn_clamp(p, p.lens[r]));
-    const int n = it_end - it_first;
-    it_hx = static_cast<int>(start_at[warp] / n);
-    it_t = it_first + static_cast<int>(start_at[warp] - static_cast<int64_t>(it_hx) * n);
+    const int n = it_end - it_first + p.seg_cost;
+    it_hx = static_cast<int>(attn_div(start_at[warp], n));
+    const int in = static_cast<int>(start_at[warp] - static_cast<int64_t>(it_hx) * n);
+    it_at = warp_lo(warp) - in;
+    it_t = it_first + max(in - p.seg_cost, 0);
+    left -= max(p.seg_cost - in, 0);
   }
+  int n_tiles = left > 0 ? 0x7fffffff : 0;  // known when the last one has been described
   const int ch = 1 << p.chunk_log2, chunks = TT >> p.chunk_log2;
   // Describes the next tile in info[i % kAttnInfo]; lane j gets the page of its chunk j (-1: not
   // to be copied) and steps on.
@@ -364,7 +406,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
     const int tok = it_t * TT;
     int page = -1;
     const int at = tok + (lane << p.chunk_log2);
-    if (lane < chunks && at < it_len && at + ch > it_lo) page = p.table[it_r * p.table_stride + at / p.page_size];
+    if (lane < chunks && at < it_len && at + ch > it_lo) page = p.table[it_r * p.table_stride + attn_page(p, at)];
     if (lane == 0) {
       AttnTile& d = info[i % kAttnInfo];
       d.r = it_r;
@@ -373,20 +415,22 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
       d.lo = it_lo;
       d.hi = it_len;
       d.ends = (it_t == it_first ? 1 : 0) | (it_t == it_end - 1 ? 2 : 0);
+      d.at = it_at;
     }
+    --left;
     if (++it_t == it_end) {
-      if (++it_hx == hxs) {
+      it_at += it_end - it_first + p.seg_cost;
+      left -= p.seg_cost;
+      if (++it_hx == hxs && left > 0) {
         it_hx = 0;
-        int r = it_r + 1;
-        while (r < p.requests) {
-          const int len = attn_clamp(p, it_next);
-          enter(r, len);
+        for (int r = it_r + 1; r < p.requests; ++r) {
+          enter(r, attn_clamp(p, it_next));
           if (it_end > it_first) break;
-          ++r;
         }
       }
       it_t = it_first;
     }
+    if (left <= 0) n_tiles = i + 1;
     return page;
   };
   // Copies tile i, whose pages `describe` gave, into its stage.
@@ -406,7 +450,9 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
     }
     __syncwarp();
     if (want && in) {
-      const int kv = d.hx / p.splits, at = d.tok + (lane << p.chunk_log2), in_page = at % p.page_size;
+      int kv, g0;
+      attn_group<MR>(p, d.hx, kv, g0);
+      const int at = d.tok + (lane << p.chunk_log2), in_page = at - attn_page(p, at) * p.page_size;
       const uint32_t dst = ring_w + s * 2 * Sh::kTile + (lane << p.chunk_log2) * Sh::kRow;
       tma_load_5d(dst, &map_k, 0, in_page, 0, kv, page, bar);
       tma_load_5d(dst + Sh::kTile, &map_v, 0, in_page, 0, kv, page, bar);
@@ -444,25 +490,34 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
   float m[2] = {neg, neg}, l[2] = {0.f, 0.f}, c[2] = {1.f, 1.f};
   bool alive = true;
 
-  // Query rows `row` (and `row` + 8) of the tile's group in the order of the matrix product's A operand.
-  auto load_q = [&](const AttnTile& d) {
-    const int kv = d.hx / p.splits, g0 = (d.hx - kv * p.splits) * MR;
+  // Query rows `row` (and `row` + 8) of the tile's group in the order of the matrix product's A operand:
+  // requested while the tile before is computed, so that their latency is not seen.
+  uint32_t qn[MR / 8][KS][2];
+  auto fetch_q = [&](int i) {
+    const int r = info[i % kAttnInfo].r, hx = info[i % kAttnInfo].hx;
+    int kv, g0;
+    attn_group<MR>(p, hx, kv, g0);
 #pragma unroll
     for (int j = 0; j < MR / 8; ++j) {
       const int g = g0 + row + 8 * j;
-      const uint16_t* src = static_cast<const uint16_t*>(p.q) + d.r * p.q_stride + static_cast<int64_t>(kv * p.group + g) * D;
+      const uint16_t* src = static_cast<const uint16_t*>(p.q) + r * p.q_stride + static_cast<int64_t>(kv * p.group + g) * D;
       const bool there = g < p.group;
-      uint32_t u[KS][2];
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
         if constexpr (kF8) {  // four consecutive elements: the order of four codes in a register
           const uint2 v = there ? *reinterpret_cast<const uint2*>(src + 16 * k + 4 * quad) : make_uint2(0, 0);
-          u[k][0] = v.x, u[k][1] = v.y;
+          qn[j][k][0] = v.x, qn[j][k][1] = v.y;
         } else {
-          u[k][0] = there ? *reinterpret_cast<const uint32_t*>(src + 16 * k + 2 * quad) : 0u;
-          u[k][1] = there ? *reinterpret_cast<const uint32_t*>(src + 16 * k + 2 * quad + 8) : 0u;
+          qn[j][k][0] = there ? *reinterpret_cast<const uint32_t*>(src + 16 * k + 2 * quad) : 0u;
+          qn[j][k][1] = there ? *reinterpret_cast<const uint32_t*>(src + 16 * k + 2 * quad + 8) : 0u;
         }
       }
+    }
+  };
+  auto take_q = [&]() {
+#pragma unroll
+    for (int j = 0; j < MR / 8; ++j) {
+      uint32_t(&u)[KS][2] = qn[j];
       if (kF8 && p.type == QGEMV_OUT_BF16) {
         // bf16 queries as fp16 times a power of two per head: the largest in [2^14, 2^15), so every
         // one within 2^28 of it is exact
@@ -495,8 +550,9 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
   };
 
   // The sums of the finished (part of a) request and head: out, or a piece.
-  auto finish = [&](const AttnTile& d, int i, bool whole, int slot) {
-    const int kv = d.hx / p.splits, g0 = (d.hx - kv * p.splits) * MR;
+  auto finish = [&](const AttnTile& d, bool whole, int slot) {
+    int kv, g0;
+    attn_group<MR>(p, d.hx, kv, g0);
 #pragma unroll
     for (int j = 0; j < MR / 8; ++j) {
       l[j] += __shfl_xor_sync(0xffffffffu, l[j], 1);
@@ -504,7 +560,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
     }
     float* piece = slot == 0 ? heads_mem + warp * Sh::kPiece : reinterpret_cast<float*>(ring + warp * S * 2 * Sh::kTile);
     if (!whole && lane == 0) {
-      const int64_t lo = w_lo + i - (d.tok / TT - d.lo / TT);
+      const int64_t lo = d.at + p.seg_cost;
       piece_of[2 * warp + slot] = AttnPiece{lo, lo + (d.hi + TT - 1) / TT - d.lo / TT, d.r, d.hx};
     }
 #pragma unroll
@@ -546,12 +602,15 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
   };
 
   bool begun = false;  // the current (request, head) began in this warp's share
+  constexpr bool kAhead = D < 256;  // there the registers are needed for the sums
+  if (kAhead && n_tiles > 0) fetch_q(0);
   for (int i = 0; i < n_tiles; ++i) {
     const int s = i % S;
     const AttnTile d = info[i % kAttnInfo];
     if (i == 0 || (d.ends & 1)) {
       begun = d.ends & 1;
-      load_q(d);
+      if constexpr (!kAhead) fetch_q(i);
+      take_q();
 #pragma unroll
       for (int t = 0; t < OT; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
       m[0] = m[1] = neg;
@@ -564,6 +623,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
     }
     alive = __all_sync(0xffffffffu, alive);
     const uint32_t kb = ring_w + s * 2 * Sh::kTile, vb = kb + Sh::kTile;
+    if (kAhead && i + 1 < n_tiles && (info[(i + 1) % kAttnInfo].ends & 1)) fetch_q(i + 1);
     const bool edge = d.tok < d.lo || d.tok + TT > d.hi || d.bad;
 
     // scores: rows are heads, columns tokens
@@ -729,12 +789,12 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
     }
     const bool last = i == n_tiles - 1;
     if ((d.ends & 2) && begun) {
-      finish(d, i, true, 0);
+      finish(d, true, 0);
     } else if ((d.ends & 2) && !last) {
-      finish(d, i, false, 0);  // began before this share: the first piece
+      finish(d, false, 0);  // began before this share: the first piece
     } else if (last) {
       __syncwarp();  // the piece goes where the copies were
-      finish(d, i, false, 1);  // goes on behind this share, or is all of it
+      finish(d, false, 1);  // goes on behind this share, or is all of it
     }
     __syncwarp();  // every lane is done with the stage and with info[i]
     if (i + S < n_tiles && alive) {
@@ -754,11 +814,11 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
   // ---- join: the warps' pieces in order; those of one (request, head) follow one another
   int shared_n = 0;  // those that reach beyond this CTA: at most its first and its last
   for (int k = 0; k < 2 * kAttnWarps;) {
-    if (piece_of[k].r < 0) {
+    const AttnPiece a = piece_of[k];
+    if (a.r < 0) {
       ++k;
       continue;
     }
-    const AttnPiece a = piece_of[k];
     uint32_t list = 0;  // slots of the pieces, four bits each
     int n = 0;
     for (; k < 2 * kAttnWarps; ++k) {
@@ -772,27 +832,30 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
     };
     const bool inside = a.lo >= c_lo && a.hi <= c_hi;
     float* to = inside ? nullptr : p.ws + static_cast<int64_t>(2 * cta + (a.lo >= c_lo ? 1 : 0)) * Sh::kPiece;
-    attn_join<D, MR>(p, a.r, a.hx, n, piece, wt_small, fl, to);
+    attn_join<D, MR, 4, true>(p, a.r, a.hx, n, piece, to);
     if (!inside) {
       if (threadIdx.x == 0) shared_of[shared_n] = a;
       ++shared_n;
     }
   }
-  for (int k = 0; k < shared_n; ++k) {
+  if (shared_n == 0) return;
+  __syncthreads();
+  if (static_cast<int>(threadIdx.x) < shared_n) {
+    const AttnPiece a = shared_of[threadIdx.x];
+    const int first = cta_of(a.lo), n = cta_of(a.hi - 1) - first + 1;
+    __threadfence();  // the CTA's pieces, which the barrier ordered before, to all CTAs
+    const bool last = atomicAdd(p.cnt + first, 1) == n - 1;
     __threadfence();
-    __syncthreads();
-    const AttnPiece a = shared_of[k];
-    // shares are [floor(total c / ctas), floor(total (c + 1) / ctas)): the CTAs of the first and the last tile
-    const int first = static_cast<int>(((a.lo + 1) * ctas - 1) / total), n = static_cast<int>((a.hi * ctas - 1) / total) - first + 1;
-    if (threadIdx.x == 0) {
-      last_flag = atomicAdd(p.cnt + first, 1) == n - 1;
-      if (last_flag) p.cnt[first] = 0;  // for the next launch
-      __threadfence();
-    }
-    __syncthreads();
-    if (!last_flag) continue;
+    if (last) p.cnt[first] = 0;  // for the next launch
+    shared_from[threadIdx.x] = first;
+    shared_count[threadIdx.x] = last ? n : 0;
+  }
+  __syncthreads();
+  for (int k = 0; k < shared_n; ++k) {
+    const int first = shared_from[k], n = shared_count[k];
+    if (n == 0) continue;
     auto piece = [&](int i) -> const float* { return p.ws + static_cast<int64_t>(2 * (first + i) + (i == 0 ? 1 : 0)) * Sh::kPiece; };
-    attn_join<D, MR>(p, a.r, a.hx, n, piece, reinterpret_cast<float*>(ring), fl, nullptr);
+    attn_join<D, MR, 16, false>(p, shared_of[k].r, shared_of[k].hx, n, piece, nullptr);
   }
 }
 
