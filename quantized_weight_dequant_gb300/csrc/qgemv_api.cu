@@ -951,6 +951,8 @@ qgemv_status_t qgemv_check_error(qgemv_handle_t hh, cudaStream_t stream) {
   int e = 0;
   if (cudaMemcpy(&e, h->err, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return QGEMV_ERR_CUDA;
   if (e != 0 && cudaMemset(h->err, 0, sizeof(int)) != cudaSuccess) return QGEMV_ERR_CUDA;
+  // a CTA that gave up may not have counted itself in: the next launch needs zeros
+  if ((e & kDevErrTimeout) && cudaMemset(h->cnt, 0, kMaxRanges * sizeof(int)) != cudaSuccess) return QGEMV_ERR_CUDA;
   return (e & kDevErrTimeout) ? QGEMV_ERR_TIMEOUT : (e & kDevErrIndex) ? QGEMV_ERR_BAD_INDEX : QGEMV_OK;
 }
 

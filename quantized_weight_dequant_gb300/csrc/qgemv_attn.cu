@@ -119,7 +119,7 @@ extern "C" qgemv_status_t qgemv_attn_decode(qgemv_handle_t hh, const qgemv_attn_
   a.pages = p.cache.pages;
   a.type = p.type;
   a.min_units = 8;
-  a.seg_cost = 1;
+  a.seg_cost = 2;
   // the reciprocal for t / page_size: with 2^(l-1) < page_size <= 2^l the product's excess over 2^(31+l)
   // is at most page_size <= 2^l per unit of t < 2^31
   int l = 3;

@@ -45,8 +45,7 @@
 namespace qg {
 
 constexpr int kAttnWarps = 4;
-constexpr int kAttnThreads = 32 * kAttnWarps;
-constexpr int kAttnInfo = 4;  // tile descriptors kept per warp (one more than stages)
+constexpr int kAttnThreads = 32 * (kAttnWarps + 1);  // and one that copies
 
 struct AttnArgs {
   const void* q;
@@ -84,12 +83,13 @@ struct AttnShape {
   static constexpr int kTile = kTT * kRow;                    // bytes of keys (and of values)
   static constexpr int kScaleBytes = KT == QGEMV_KV_E4M3 ? 2 * kTT * 4 : 0;
   static constexpr int kPiece = MR * (D + 2);                 // floats of a piece: m, l, O
-  static constexpr int kCtasPerSm = kRow == 512 || (D == 256 && MR == 16) ? 1 : 2;
+  static constexpr int kCtasPerSm = D == 256 ? 1 : 2;
   static constexpr int kBudget = kCtasPerSm == 1 ? 232448 : 115712;
-  static constexpr int kFixed = 1024 + kAttnWarps * kPiece * 4 + kAttnWarps * (kAttnInfo * 40 + 32) + 2048;  // static ones too
-  static constexpr int kFit = (kBudget - kFixed) / (kAttnWarps * (2 * kTile + kScaleBytes));
+  static constexpr int kStatic = 1600;  // at least the kernel's static shared memory
+  static constexpr int kFixed = 1024 + kAttnWarps * kPiece * 4;
+  static constexpr int kFit = (kBudget - kFixed - kStatic) / (kAttnWarps * (2 * kTile + kScaleBytes));
   static constexpr int kStages = kFit < 3 ? kFit : 3;
-  static constexpr int kSmem = kFixed - 2048 + kAttnWarps * kStages * (2 * kTile + kScaleBytes);
+  static constexpr int kSmem = kFixed + kAttnWarps * kStages * (2 * kTile + kScaleBytes);
   static_assert(kStages >= 2 && kPiece * 4 <= kStages * 2 * kTile, "shared memory");
 };
 
@@ -175,12 +175,23 @@ struct AttnTile {
   int64_t at;     // first unit of the (request, head)
 };
 
-static_assert(sizeof(AttnTile) == 40, "shared memory layout");
+// Where a warp's share begins: first unit of its (request, head), units left after its cost, tiles to skip.
+struct AttnStart {
+  int64_t at, left;
+  int r, hx, skip;
+};
 
 // A piece of a (request, head) that more than one warp has a share of; its tiles are the units lo .. hi.
 struct AttnPiece {
   int64_t lo, hi;
   int r, hx;
+};
+
+// The n pieces of one (request, head) that are to be joined: the CTA's own (slots: 2 warp + which, four bits
+// each; to: the workspace piece that they become, or -1), or those of n CTAs from CTA `to` on.
+struct AttnSet {
+  int r, hx, n, to;
+  uint32_t slots;
 };
 
 __device__ __forceinline__ int attn_page(const AttnArgs& p, int t) {
@@ -220,57 +231,58 @@ __device__ __forceinline__ float attn_lse(float m, float l) {
   return l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : __int_as_float(0xff800000);
 }
 
-// Joins pieces i = 0 .. n-1 (at piece(i): m[MR], l[MR], O[MR][D]) of request r and head group hx, in
-// this order, by all threads of the CTA: a thread takes four elements of a head through U pieces at
-// a time, whose loads are all in flight together.  The result is written out, or (to != null) left as
-// one piece.
-template <int D, int MR, int U, bool SMEM, class Piece>
-__device__ __forceinline__ void attn_join(const AttnArgs& p, int r, int hx, int n, Piece piece, float* to) {
-  int kv, g0;
-  attn_group<MR>(p, hx, kv, g0);
-  const int heads = min(MR, p.group - g0);
+// A load that sees what other CTAs published, from shared or global memory.
+__device__ __forceinline__ float4 ld_piece4(const float* q) {
+  float4 v;
+  asm volatile("ld.relaxed.gpu.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(q) : "memory");
+  return v;
+}
+__device__ __forceinline__ float ld_piece(const float* q) {
+  float v;
+  asm volatile("ld.relaxed.gpu.f32 %0, [%1];" : "=f"(v) : "l"(q) : "memory");
+  return v;
+}
+
+// Joins four elements (from d) of head g of n pieces (at piece(i): m[MR], l[MR], O[MR][D]) in their order,
+// U at a time, whose loads are all in flight together.
+template <int MR, int D, class Piece>
+__device__ __forceinline__ float4 attn_join(int n, int g, int d, Piece piece, float& m, float& l) {
+  constexpr int U = 8;
   const float neg = __int_as_float(0xff800000);
-  for (int e = threadIdx.x; e < heads * (D / 4); e += kAttnThreads) {
-    const int g = e / (D / 4), d = (e - g * (D / 4)) * 4;
-    float m = neg, l = 0.f;
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = 0; i0 < n; i0 += U) {
-      float mi[U], li[U];
-      float4 o[U];
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  m = neg, l = 0.f;
+#pragma unroll 1
+  for (int i0 = 0; i0 < n; i0 += U) {
+    float mi[U], li[U];
+    float4 o[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const float* q = piece(min(i0 + u, n - 1));
-        const float4* oq = reinterpret_cast<const float4*>(q + 2 * MR + g * D + d);
-        mi[u] = SMEM ? q[g] : __ldcg(q + g);
-        li[u] = SMEM ? q[MR + g] : __ldcg(q + MR + g);
-        o[u] = SMEM ? *oq : __ldcg(oq);
+    for (int u = 0; u < U; ++u) {
+      if (i0 + u < n) {
+        const float* q = piece(i0 + u);
+        mi[u] = ld_piece(q + g);
+        li[u] = ld_piece(q + MR + g);
+        o[u] = ld_piece4(q + 2 * MR + g * D + d);
+      } else {
+        mi[u] = neg;
       }
-      float mn = m;
+    }
+    float mn = m;
 #pragma unroll
-      for (int u = 0; u < U; ++u) mn = fmaxf(mn, mi[u]);
-      const float base = mn == neg ? 0.f : mn, f = ex2(m - base);
-      m = mn;
-      l *= f;
-      s.x *= f, s.y *= f, s.z *= f, s.w *= f;
+    for (int u = 0; u < U; ++u) mn = fmaxf(mn, mi[u]);
+    const float base = mn == neg ? 0.f : mn, f = ex2(m - base);
+    m = mn;
+    l *= f;
+    s.x *= f, s.y *= f, s.z *= f, s.w *= f;
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (i0 + u >= n) break;
+    for (int u = 0; u < U; ++u) {
+      if (i0 + u < n) {
         const float w = ex2(mi[u] - base);
         l += w * li[u];
         s.x += w * o[u].x, s.y += w * o[u].y, s.z += w * o[u].z, s.w += w * o[u].w;
       }
     }
-    if (to) {
-      if (d == 0) to[g] = m, to[MR + g] = l;
-      *reinterpret_cast<float4*>(to + 2 * MR + g * D + d) = s;
-    } else {
-      const float f = l != 0.f ? 1.f / l : 0.f;
-      const int64_t at = r * p.out_stride + static_cast<int64_t>(kv * p.group + g0 + g) * D + d;
-      attn_store2(p, at, s.x * f, s.y * f);
-      attn_store2(p, at + 2, s.z * f, s.w * f);
-      if (d == 0 && p.lse) p.lse[static_cast<int64_t>(r) * p.q_heads + kv * p.group + g0 + g] = attn_lse(m, l);
-    }
   }
+  return s;
 }
 
 template <int D, int KT, int MR>
@@ -281,26 +293,27 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
   constexpr int TT = Sh::kTT, S = Sh::kStages, NT = TT / 8;  // NT: 8-token column tiles of the scores
   constexpr int OT = D / 8;                                  // 8-wide column tiles of the output
   extern __shared__ uint8_t dyn[];
-  __shared__ int64_t scan[kAttnWarps];
-  __shared__ int64_t start_at[kAttnWarps];  // first tile of each warp within its request
-  __shared__ int start_r[kAttnWarps];
+  __shared__ int64_t scan[kAttnWarps + 1];
+  __shared__ AttnStart start_of[kAttnWarps];
+  __shared__ AttnTile info_of[kAttnWarps][4];
+  __shared__ uint64_t bars_of[kAttnWarps][8];     // of each stage: its copies are there; it is free again
   __shared__ AttnPiece piece_of[2 * kAttnWarps];  // of each warp the one that began before its share, and the last
   __shared__ AttnPiece shared_of[2];
-  __shared__ int shared_from[2], shared_count[2];
+  __shared__ AttnSet set_of[2 * kAttnWarps];
+  __shared__ int set_count[2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int quad = lane & 3, row = lane >> 2;
   const float neg = __int_as_float(0xff800000);
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t{1023});
   float* heads_mem = reinterpret_cast<float*>(ring + kAttnWarps * S * 2 * Sh::kTile);
   uint8_t* scales_mem = reinterpret_cast<uint8_t*>(heads_mem + kAttnWarps * Sh::kPiece);
-  AttnTile* info = reinterpret_cast<AttnTile*>(scales_mem + kAttnWarps * S * Sh::kScaleBytes) + warp * kAttnInfo;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(scales_mem + kAttnWarps * S * Sh::kScaleBytes + kAttnWarps * kAttnInfo * 40) + warp * 4;
-  const uint32_t ring_w = smem_u32(ring) + warp * S * 2 * Sh::kTile;
-  const uint32_t scale_w = smem_u32(scales_mem) + warp * S * Sh::kScaleBytes;
-  if (lane < S) mbar_init(smem_u32(bars + lane), 1);
-  if (lane == 0) {
-    piece_of[2 * warp].r = piece_of[2 * warp + 1].r = -1;
-    fence_mbar_init();
+  if (warp < kAttnWarps) {
+    if (lane < 2 * S) mbar_init(smem_u32(&bars_of[warp][lane]), 1);
+    if (lane == 0) {
+      piece_of[2 * warp].r = piece_of[2 * warp + 1].r = -1;
+      fence_mbar_init();
+    }
+  } else if (lane < 2) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(lane ? &map_v : &map_k)) : "memory");
   }
 
   // ---- the share of this CTA and of its warps
@@ -315,9 +328,11 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
   const int per = (p.requests + kAttnThreads - 1) / kAttnThreads, r_lo = min(static_cast<int>(threadIdx.x) * per, p.requests),
             r_hi = min(r_lo + per, p.requests);
   int64_t mine = 0;
-  bool none = false;  // a request without tokens whose rows this CTA writes
+  int first_units = 0;  // of this thread's first request
+  bool none = false;    // a request without tokens
   for (int r = r_lo; r < r_hi; ++r) {
     const int n = units_of(attn_clamp(p, p.lens[r]));
+    if (r == r_lo) first_units = n;
     mine += n;
     none |= n == 0;
   }
@@ -332,7 +347,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
   const bool any_none = __syncthreads_or(none);
   int64_t total = 0, before = upto - mine;
 #pragma unroll
-  for (int w = 0; w < kAttnWarps; ++w) {
+  for (int w = 0; w <= kAttnWarps; ++w) {
     if (w < warp) before += scan[w];
     total += scan[w];
   }
@@ -349,20 +364,18 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
   auto warp_lo = [&](int w) { return c_lo + ((c_hi - c_lo) * w >> 2); };
   static_assert(kAttnWarps == 4, "warp shares are quarters");
   if (busy) {
-#pragma unroll
+#pragma unroll 1
     for (int w = 0; w < kAttnWarps; ++w) {
       const int64_t at = warp_lo(w);
-      if (at >= before && at < before + mine) {
-        int64_t pre = before;
-        int r = r_lo;
-        for (; r < r_hi - 1; ++r) {
-          const int64_t n = static_cast<int64_t>(units_of(attn_clamp(p, p.lens[r]))) * hxs;
-          if (at < pre + n) break;
-          pre += n;
-        }
-        start_r[w] = r;
-        start_at[w] = at - pre;
+      if (at < before || at >= before + mine) continue;
+      int64_t pre = before;
+      int r = r_lo, n = first_units;
+      while (r < r_hi - 1 && at >= pre + static_cast<int64_t>(n) * hxs) {
+        pre += static_cast<int64_t>(n) * hxs;
+        n = units_of(attn_clamp(p, p.lens[++r]));
       }
+      const int hx = static_cast<int>(attn_div(at - pre, n)), in = static_cast<int>(at - pre - static_cast<int64_t>(hx) * n);
+      start_of[w] = AttnStart{at - in, warp_lo(w + 1) - at - max(p.seg_cost - in, 0), r, hx, max(in - p.seg_cost, 0)};
     }
   }
   if (any_none) {
@@ -376,125 +389,128 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
   if (!busy) return;
   __syncthreads();
 
-  // ---- the walk over the tiles: position of the next tile to describe
-  int it_r = 0, it_hx = 0, it_t = 0, it_first = 0, it_end = 0, it_lo = 0, it_len = 0, it_next = 0;
-  int64_t left = warp_lo(warp + 1) - warp_lo(warp);  // units of the share still to be walked
-  int64_t it_at = 0;                                 // first unit of the current (request, head)
-  auto enter = [&](int r, int len) {
-    it_r = r;
-    it_len = len;
-    it_lo = attn_first(p, len);
-    it_first = it_lo / TT;
-    it_end = (len + TT - 1) / TT;
-    it_next = r + 1 < p.requests ? p.lens[r + 1] : 0;  // used when this request is through
-  };
-  if (left > 0) {
-    const int r = start_r[warp];
-    enter(r, attn_clamp(p, p.lens[r]));
-    const int n = it_end - it_first + p.seg_cost;
-    it_hx = static_cast<int>(attn_div(start_at[warp], n));
-    const int in = static_cast<int>(start_at[warp] - static_cast<int64_t>(it_hx) * n);
-    it_at = warp_lo(warp) - in;
-    it_t = it_first + max(in - p.seg_cost, 0);
-    left -= max(p.seg_cost - in, 0);
-  }
-  int n_tiles = left > 0 ? 0x7fffffff : 0;  // known when the last one has been described
-  const int ch = 1 << p.chunk_log2, chunks = TT >> p.chunk_log2;
-  // Describes the next tile in info[i % kAttnInfo]; lane j gets the page of its chunk j (-1: not
-  // to be copied) and steps on.
-  auto describe = [&](int i) -> int {
-    const int tok = it_t * TT;
-    int page = -1;
-    const int at = tok + (lane << p.chunk_log2);
-    if (lane < chunks && at < it_len && at + ch > it_lo) page = p.table[it_r * p.table_stride + attn_page(p, at)];
-    if (lane == 0) {
-      AttnTile& d = info[i % kAttnInfo];
+  if (warp == kAttnWarps) {
+    // ---- the copying warp: lanes 8 w .. 8 w + 7 walk the tiles of warp w, all four walks in step
+    const int w = lane >> 3, j = lane & 7;
+    const AttnStart st = start_of[w];
+    int64_t left = st.left, it_at = st.at;
+    int it_r = st.r, it_hx = st.hx, it_t = 0, it_first = 0, it_end = 0, it_lo = 0, it_len = 0, it_next = 0;
+    auto enter = [&](int r, int len) {
+      it_r = r;
+      it_len = len;
+      it_lo = attn_first(p, len);
+      it_first = it_lo / TT;
+      it_end = (len + TT - 1) / TT;
+      it_next = r + 1 < p.requests ? p.lens[r + 1] : 0;  // used when this request is through
+    };
+    enter(st.r, attn_clamp(p, p.lens[st.r]));
+    it_t = it_first + st.skip;
+    const int ch = 1 << p.chunk_log2, chunks = TT >> p.chunk_log2;
+    static_assert(TT <= 64, "a tile has at most eight chunks");
+    const uint32_t full = smem_u32(&bars_of[w][0]), empty = smem_u32(&bars_of[w][S]);
+    const uint32_t ring_w = smem_u32(ring) + w * S * 2 * Sh::kTile, scale_w = smem_u32(scales_mem) + w * S * Sh::kScaleBytes;
+    AttnTile d;      // the next tile
+    int page = -1;   // the page of its chunk j
+    bool want = false;
+    bool more_tiles = left > 0, alive = true;
+    auto describe = [&]() {
+      const int at = it_t * TT + (j << p.chunk_log2);
+      want = j < chunks && at < it_len && at + ch > it_lo;
+      page = want ? p.table[it_r * p.table_stride + attn_page(p, at)] : -1;
       d.r = it_r;
       d.hx = it_hx;
-      d.tok = tok;
+      d.tok = it_t * TT;
       d.lo = it_lo;
       d.hi = it_len;
       d.ends = (it_t == it_first ? 1 : 0) | (it_t == it_end - 1 ? 2 : 0);
       d.at = it_at;
-    }
-    --left;
-    if (++it_t == it_end) {
-      it_at += it_end - it_first + p.seg_cost;
-      left -= p.seg_cost;
-      if (++it_hx == hxs && left > 0) {
-        it_hx = 0;
-        for (int r = it_r + 1; r < p.requests; ++r) {
-          enter(r, attn_clamp(p, it_next));
-          if (it_end > it_first) break;
+      --left;
+      if (++it_t == it_end) {
+        it_at += it_end - it_first + p.seg_cost;
+        left -= p.seg_cost;
+        if (++it_hx == hxs && left > 0) {
+          it_hx = 0;
+          for (int r = it_r + 1; r < p.requests; ++r) {
+            enter(r, attn_clamp(p, it_next));
+            if (it_end > it_first) break;
+          }
+        }
+        it_t = it_first;
+      }
+      if (left <= 0) d.ends |= 4;
+    };
+    if (more_tiles) describe();
+    if (p.stall && cta == 0) more_tiles = false;  // nothing is copied: every wait of this CTA runs out
+#pragma unroll 1
+    for (int i = 0, s = 0, lap = 0; __any_sync(0xffffffffu, more_tiles); ++i) {
+      if (more_tiles && lap > 0 && !mbar_wait_bounded(empty + 8 * s, (lap - 1) & 1, p.spin_ns)) alive = false;
+      alive = __all_sync(0xffffffffu, alive);
+      more_tiles = more_tiles && alive;
+      const bool in = page >= 0 && page < p.pages;
+      const uint32_t bad = __ballot_sync(0xffffffffu, more_tiles && want && !in) >> (8 * w) & 0xff;
+      const uint32_t good = __ballot_sync(0xffffffffu, more_tiles && want && in) >> (8 * w) & 0xff;
+      if (j == 0 && more_tiles) {
+        d.bad = bad;
+        if (bad) atomicOr(p.err, kDevErrIndex);
+        info_of[w][s] = d;
+        mbar_arrive_expect_tx(full + 8 * s, static_cast<uint32_t>(__popc(good)) * (2 * Sh::kRow + (kF8 ? 8 : 0)) << p.chunk_log2);
+      }
+      __syncwarp();
+      if (more_tiles && want && in) {
+        int kv, g0;
+        attn_group<MR>(p, d.hx, kv, g0);
+        const int at = d.tok + (j << p.chunk_log2), in_page = at - attn_page(p, at) * p.page_size;
+        const uint32_t dst = ring_w + s * 2 * Sh::kTile + (j << p.chunk_log2) * Sh::kRow;
+        tma_load_5d(dst, &map_k, 0, in_page, 0, kv, page, full + 8 * s);
+        tma_load_5d(dst + Sh::kTile, &map_v, 0, in_page, 0, kv, page, full + 8 * s);
+        if constexpr (kF8) {
+          const int64_t src = page * p.scale_stride + static_cast<int64_t>(kv) * p.page_size + in_page;
+          const uint32_t sd = scale_w + s * Sh::kScaleBytes + (j << p.chunk_log2) * 4;
+          bulk_load(sd, p.k_scale + src, 4u << p.chunk_log2, full + 8 * s);
+          bulk_load(sd + TT * 4, p.v_scale + src, 4u << p.chunk_log2, full + 8 * s);
         }
       }
-      it_t = it_first;
+      more_tiles = more_tiles && left > 0;
+      if (more_tiles) describe();
+      if (++s == S) s = 0, ++lap;
     }
-    if (left <= 0) n_tiles = i + 1;
-    return page;
-  };
-  // Copies tile i, whose pages `describe` gave, into its stage.
-  auto issue = [&](int i, int page) {
-    const int s = i % S;
-    AttnTile& d = info[i % kAttnInfo];
-    const bool want = page != -1 || (lane < chunks && d.tok + (lane << p.chunk_log2) < d.hi && d.tok + (lane << p.chunk_log2) + ch > d.lo);
-    const bool in = page >= 0 && page < p.pages;
-    const uint32_t bad = __ballot_sync(0xffffffffu, want && !in);
-    const uint32_t good = __ballot_sync(0xffffffffu, want && in);
-    const uint32_t bar = smem_u32(bars + s);
-    if (lane == 0) {
-      d.bad = bad;
-      if (bad) atomicOr(p.err, kDevErrIndex);
-      const uint32_t bytes = static_cast<uint32_t>(__popc(good)) * (2 * Sh::kRow + (kF8 ? 8 : 0)) << p.chunk_log2;
-      mbar_arrive_expect_tx(bar, bytes);
-    }
-    __syncwarp();
-    if (want && in) {
-      int kv, g0;
-      attn_group<MR>(p, d.hx, kv, g0);
-      const int at = d.tok + (lane << p.chunk_log2), in_page = at - attn_page(p, at) * p.page_size;
-      const uint32_t dst = ring_w + s * 2 * Sh::kTile + (lane << p.chunk_log2) * Sh::kRow;
-      tma_load_5d(dst, &map_k, 0, in_page, 0, kv, page, bar);
-      tma_load_5d(dst + Sh::kTile, &map_v, 0, in_page, 0, kv, page, bar);
-      if constexpr (kF8) {
-        const int64_t src = page * p.scale_stride + static_cast<int64_t>(kv) * p.page_size + in_page;
-        const uint32_t sd = scale_w + s * Sh::kScaleBytes + (lane << p.chunk_log2) * 4;
-        bulk_load(sd, p.k_scale + src, 4u << p.chunk_log2, bar);
-        bulk_load(sd + TT * 4, p.v_scale + src, 4u << p.chunk_log2, bar);
-      }
-    }
-  };
-  int next_page = -1;
-  {
-    int pages[S + 1];
-#pragma unroll
-    for (int i = 0; i <= S; ++i) pages[i] = i < n_tiles ? describe(i) : -1;
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < S; ++i)
-      if (i < n_tiles && !(p.stall && cta == 0 && warp == 0 && i == 0)) issue(i, pages[i]);
-    next_page = pages[S];
-  }
+    if (!alive && lane == 0) atomicOr(p.err, kDevErrTimeout);
+  } else {
+    // ---- the computing warps
+    const int quad = lane & 3, row = lane >> 2;
+    const uint32_t ring_w = smem_u32(ring) + warp * S * 2 * Sh::kTile, scale_w = smem_u32(scales_mem) + warp * S * Sh::kScaleBytes;
+    const uint32_t full = smem_u32(&bars_of[warp][0]), empty = smem_u32(&bars_of[warp][S]);
+    const int ch = 1 << p.chunk_log2;
 
   // Byte offset of token t of a tile, row part `part`, in shared memory (before the swizzle).
   auto line_of = [&](int t, int part) {
     return (t >> p.chunk_log2) * (Sh::kRow << p.chunk_log2) + part * (Sh::kRB << p.chunk_log2) + (t & (ch - 1)) * Sh::kRB;
   };
-  // 16-byte unit c of the row at `line` after the copy's swizzle (address bits 4.. xor bits 7..).
-  auto unit_of = [&](uint32_t line, int c) { return line + static_cast<uint32_t>((c ^ ((line >> 7) & (Sh::kRB / 16 - 1))) << 4); };
+  // The copy's swizzle exchanges the 16-byte units of a row: address bits 4.. xor bits 7... Rows start at
+  // multiples of their length, so unit u of this lane's row is at (stage + row) ^ turn ^ 16 u, where the row
+  // and the turn do not depend on the tile.
+  uint32_t k_row[TT / 16], v_row[TT / 16], k_turn[TT / 16], v_turn[TT / 16];
+#pragma unroll
+  for (int b = 0; b < TT / 16; ++b) {
+    // rows of the 8x8 matrices that a lane addresses: keys (tokens 0..7, units u, u + 1; tokens 8..15, the same),
+    // values (tokens 0..7, 8..15 of unit u; the same of unit u + 1)
+    k_row[b] = line_of(16 * b + (lane >> 4) * 8 + (lane & 7), 0);
+    v_row[b] = line_of(16 * b + (lane & 15), 0);
+    k_turn[b] = ((k_row[b] >> 7 & (Sh::kRB / 16 - 1)) ^ (lane >> 3 & 1)) << 4;
+    v_turn[b] = ((v_row[b] >> 7 & (Sh::kRB / 16 - 1)) ^ (lane >> 4)) << 4;
+  }
+  const uint32_t part_step = Sh::kRB << p.chunk_log2;
 
   constexpr int KS = D / 16;  // k steps of the scores
   uint32_t qa[KS][MR == 8 ? 2 : 4];
   float q_back[2] = {1.f, 1.f};  // what the fp16 queries of rows `row`, `row` + 8 were divided by
   float o[OT][4];
   float m[2] = {neg, neg}, l[2] = {0.f, 0.f}, c[2] = {1.f, 1.f};
-  bool alive = true;
 
-  // Query rows `row` (and `row` + 8) of the tile's group in the order of the matrix product's A operand:
-  // requested while the tile before is computed, so that their latency is not seen.
+  // Query rows `row` (and `row` + 8) of a group in the order of the matrix product's A operand, requested
+  // before the tile that needs them.
   uint32_t qn[MR / 8][KS][2];
-  auto fetch_q = [&](int i) {
-    const int r = info[i % kAttnInfo].r, hx = info[i % kAttnInfo].hx;
+  auto fetch_q = [&](int r, int hx) {
     int kv, g0;
     attn_group<MR>(p, hx, kv, g0);
 #pragma unroll
@@ -601,66 +617,66 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
     }
   };
 
-  bool begun = false;  // the current (request, head) began in this warp's share
-  constexpr bool kAhead = D < 256;  // there the registers are needed for the sums
-  if (kAhead && n_tiles > 0) fetch_q(0);
-  for (int i = 0; i < n_tiles; ++i) {
-    const int s = i % S;
-    const AttnTile d = info[i % kAttnInfo];
-    if (i == 0 || (d.ends & 1)) {
-      begun = d.ends & 1;
-      if constexpr (!kAhead) fetch_q(i);
-      take_q();
+    const AttnStart st = start_of[warp];
+    bool alive = true, begun = false;  // begun: the current (request, head) began in this warp's share
+    bool asked = false;                // its queries have been requested
+    if (st.left > 0) {
+      fetch_q(st.r, st.hx);
+      asked = true;
+    }
+#pragma unroll 1
+    for (int i = 0, s = 0, lap = 0; st.left > 0; ++i) {
+      alive = mbar_wait_bounded(full + 8 * s, lap & 1, p.spin_ns);
+      alive = __all_sync(0xffffffffu, alive);
+      if (!alive) {
+        if (lane == 0) atomicOr(p.err, kDevErrTimeout);
+        break;
+      }
+      const AttnTile d = info_of[warp][s];
+      if (i == 0 || (d.ends & 1)) {
+        begun = d.ends & 1;
+        if (!asked) fetch_q(d.r, d.hx);
+        asked = false;
+        take_q();
 #pragma unroll
-      for (int t = 0; t < OT; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
-      m[0] = m[1] = neg;
-      l[0] = l[1] = 0.f;
-      c[0] = c[1] = 0.f;
-    }
-    if (alive && !mbar_wait_bounded(smem_u32(bars + s), (i / S) & 1, p.spin_ns)) {
-      alive = false;
-      if (lane == 0) atomicOr(p.err, kDevErrTimeout);
-    }
-    alive = __all_sync(0xffffffffu, alive);
+        for (int t = 0; t < OT; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
+        m[0] = m[1] = neg;
+        l[0] = l[1] = 0.f;
+        c[0] = c[1] = 0.f;
+      }
+      const bool last = d.ends & 4;
+      const int s_next = s + 1 == S ? 0 : s + 1;
+      if (D < 256 && (d.ends & 2) && !last && mbar_try_wait(full + 8 * s_next, (s_next ? lap : lap + 1) & 1)) {
+        fetch_q(info_of[warp][s_next].r, info_of[warp][s_next].hx);
+        asked = true;
+      }
+      asked = __all_sync(0xffffffffu, asked);
     const uint32_t kb = ring_w + s * 2 * Sh::kTile, vb = kb + Sh::kTile;
-    if (kAhead && i + 1 < n_tiles && (info[(i + 1) % kAttnInfo].ends & 1)) fetch_q(i + 1);
     const bool edge = d.tok < d.lo || d.tok + TT > d.hi || d.bad;
 
     // scores: rows are heads, columns tokens
     float sc[NT][4];
 #pragma unroll
     for (int t = 0; t < NT; ++t) sc[t][0] = sc[t][1] = sc[t][2] = sc[t][3] = 0.f;
+    uint32_t ka[TT / 16];
 #pragma unroll
-    for (int b = 0; b < TT / 16; ++b) {
-      const int tl = 16 * b + (lane >> 4) * 8 + (lane & 7), half = (lane >> 3) & 1;  // this lane's row of the 8x8 matrices
-      if constexpr (!kF8) {
+    for (int b = 0; b < TT / 16; ++b) ka[b] = (kb + k_row[b]) ^ k_turn[b];
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          uint32_t w[4];
-          ldsm4(unit_of(kb + line_of(tl, k / 4), (k % 4) * 2 + half), w);
-          if constexpr (MR == 8) {
-            mma16816<kBF>(sc[2 * b], qa[k][0], 0u, qa[k][1], 0u, w[0], w[1]);
-            mma16816<kBF>(sc[2 * b + 1], qa[k][0], 0u, qa[k][1], 0u, w[2], w[3]);
-          } else {
-            mma16816<kBF>(sc[2 * b], qa[k][0], qa[k][1], qa[k][2], qa[k][3], w[0], w[1]);
-            mma16816<kBF>(sc[2 * b + 1], qa[k][0], qa[k][1], qa[k][2], qa[k][3], w[2], w[3]);
+    for (int k = 0; k < KS; k += kF8 ? 2 : 1) {  // a 16-byte unit holds half a k step, or one of codes
+#pragma unroll
+      for (int b = 0; b < TT / 16; ++b) {
+        uint32_t w[4];
+        ldsm4((ka[b] + k * 16 * Sh::kEl / Sh::kRB * part_step) ^ (k * 16 * Sh::kEl % Sh::kRB), w);
+#pragma unroll
+        for (int e = 0; e < (kF8 ? 2 : 1); ++e) {
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const uint32_t u = w[2 * n + e], b0 = kF8 ? e4m3x2(u & 0xffffu) : w[2 * n], b1 = kF8 ? e4m3x2(u >> 16) : w[2 * n + 1];
+            if constexpr (MR == 8)
+              mma16816<kBF>(sc[2 * b + n], qa[k + e][0], 0u, qa[k + e][1], 0u, b0, b1);
+            else
+              mma16816<kBF>(sc[2 * b + n], qa[k + e][0], qa[k + e][1], qa[k + e][2], qa[k + e][3], b0, b1);
           }
-        }
-      } else {
-#pragma unroll
-        for (int k = 0; k < KS; k += 2) {  // 16 codes per unit: two k steps per load
-          uint32_t w[4];
-          ldsm4(unit_of(kb + line_of(tl, k * 16 / Sh::kRB), (k * 16 % Sh::kRB) / 16 + half), w);
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-              const uint32_t u = w[2 * n + e], b0 = e4m3x2(u & 0xffffu), b1 = e4m3x2(u >> 16);
-              if constexpr (MR == 8)
-                mma16816<false>(sc[2 * b + n], qa[k + e][0], 0u, qa[k + e][1], 0u, b0, b1);
-              else
-                mma16816<false>(sc[2 * b + n], qa[k + e][0], qa[k + e][1], qa[k + e][2], qa[k + e][3], b0, b1);
-            }
         }
       }
     }
@@ -760,7 +776,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
       for (int j = 0; j < MR / 8; ++j)
 #pragma unroll
         for (int n = 0; n < 2; ++n) split16<kBF>(sc[2 * b + n][2 * j], sc[2 * b + n][2 * j + 1], hi[j][n], lo[j][n]);
-      const int tl = 16 * b + (lane & 15);  // matrices: tokens 0..7, 8..15 of two 16-byte units
+      const uint32_t va = (vb + v_row[b]) ^ v_turn[b];
       auto add = [&](float (&acc)[4], uint32_t b0, uint32_t b1) {
         if constexpr (MR == 8) {
           mma16816<kBF>(acc, hi[0][0], lo[0][0], hi[0][1], lo[0][1], b0, b1);
@@ -772,7 +788,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
 #pragma unroll
       for (int u = 0; u < Sh::kRow / 16; u += 2) {
         uint32_t w[4];
-        ldsm4t(unit_of(vb + line_of(tl, u / (Sh::kRB / 16)), u % (Sh::kRB / 16) + (lane >> 4)), w);
+        ldsm4t((va + u * 16 / Sh::kRB * part_step) ^ (u * 16 % Sh::kRB), w);
         if constexpr (!kF8) {
           add(o[u], w[0], w[1]);
           add(o[u + 1], w[2], w[3]);
@@ -787,75 +803,97 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
         }
       }
     }
-    const bool last = i == n_tiles - 1;
-    if ((d.ends & 2) && begun) {
-      finish(d, true, 0);
-    } else if ((d.ends & 2) && !last) {
-      finish(d, false, 0);  // began before this share: the first piece
-    } else if (last) {
-      __syncwarp();  // the piece goes where the copies were
-      finish(d, false, 1);  // goes on behind this share, or is all of it
-    }
-    __syncwarp();  // every lane is done with the stage and with info[i]
-    if (i + S < n_tiles && alive) {
-      issue(i + S, next_page);
-      next_page = i + S + 1 < n_tiles ? describe(i + S + 1) : -1;
-      __syncwarp();
-    }
+    __syncwarp();  // every lane is done with the stage
+    if (lane == 0 && !last) mbar_arrive(empty + 8 * s);
+    const bool whole = (d.ends & 2) && begun;
+    // one that began before this share, or goes on behind it, leaves a piece: where the copies were when it
+    // is the last that the warp has to do, else in a place of its own
+    if ((d.ends & 2) || last) finish(d, whole, !last ? 0 : 1);
+    if (last) break;
+    s = s_next;
+    if (s == 0) ++lap;
   }
   if (!alive) {  // copies still in flight after a wait that gave up
     for (int s = 0; s < S; ++s) {
-      mbar_wait_bounded(smem_u32(bars + s), 0, p.spin_ns);
-      mbar_wait_bounded(smem_u32(bars + s), 1, p.spin_ns);
+      mbar_wait_bounded(full + 8 * s, 0, p.spin_ns);
+      mbar_wait_bounded(full + 8 * s, 1, p.spin_ns);
     }
+  }
   }
   __syncthreads();
 
-  // ---- join: the warps' pieces in order; those of one (request, head) follow one another
-  int shared_n = 0;  // those that reach beyond this CTA: at most its first and its last
-  for (int k = 0; k < 2 * kAttnWarps;) {
-    const AttnPiece a = piece_of[k];
-    if (a.r < 0) {
-      ++k;
-      continue;
+  // ---- join: the warps' pieces in order; those of one (request, head) follow one another and are one
+  // set.  First the sets of this CTA, then those that it is the last to bring a piece of.
+  int sets = 0, shared_n = 0;
+  if (warp == 0) {
+    const AttnPiece a = piece_of[lane & 7];
+    const bool there = lane < 2 * kAttnWarps && a.r >= 0;
+    const uint32_t mask = __ballot_sync(0xffffffffu, there), below = mask & ((1u << lane) - 1);
+    const int prev = below ? 31 - __clz(below) : lane;
+    const int pr = __shfl_sync(0xffffffffu, a.r, prev), ph = __shfl_sync(0xffffffffu, a.hx, prev);
+    const bool starts = there && (!below || pr != a.r || ph != a.hx);
+    const uint32_t begin = __ballot_sync(0xffffffffu, starts);
+    const bool shared = a.lo < c_lo || a.hi > c_hi;
+    const uint32_t out = __ballot_sync(0xffffffffu, starts && shared);
+    if (starts) {
+      const uint32_t next = begin & ~((2u << lane) - 1);  // its pieces end before the next set's first
+      AttnSet& t = set_of[__popc(begin & ((1u << lane) - 1))];
+      t.r = a.r;
+      t.hx = a.hx;
+      uint32_t own = mask & ~((1u << lane) - 1) & (next ? (next & -next) - 1 : 0xffu), list = 0;
+      t.n = __popc(own);
+      for (int k = 0; own; own &= own - 1, k += 4) list |= static_cast<uint32_t>(__ffs(own) - 1) << k;
+      t.slots = list;
+      t.to = shared ? 2 * cta + (a.lo >= c_lo ? 1 : 0) : -1;
+      if (shared) shared_of[__popc(out & ((1u << lane) - 1))] = a;
     }
-    uint32_t list = 0;  // slots of the pieces, four bits each
-    int n = 0;
-    for (; k < 2 * kAttnWarps; ++k) {
-      if (piece_of[k].r < 0) continue;
-      if (piece_of[k].r != a.r || piece_of[k].hx != a.hx) break;
-      list |= static_cast<uint32_t>(k) << (4 * n++);
-    }
-    auto piece = [&](int i) -> const float* {
-      const int q = list >> (4 * i) & 15;
-      return q & 1 ? reinterpret_cast<const float*>(ring + (q >> 1) * S * 2 * Sh::kTile) : heads_mem + (q >> 1) * Sh::kPiece;
-    };
-    const bool inside = a.lo >= c_lo && a.hi <= c_hi;
-    float* to = inside ? nullptr : p.ws + static_cast<int64_t>(2 * cta + (a.lo >= c_lo ? 1 : 0)) * Sh::kPiece;
-    attn_join<D, MR, 4, true>(p, a.r, a.hx, n, piece, to);
-    if (!inside) {
-      if (threadIdx.x == 0) shared_of[shared_n] = a;
-      ++shared_n;
-    }
-  }
-  if (shared_n == 0) return;
-  __syncthreads();
-  if (static_cast<int>(threadIdx.x) < shared_n) {
-    const AttnPiece a = shared_of[threadIdx.x];
-    const int first = cta_of(a.lo), n = cta_of(a.hi - 1) - first + 1;
-    __threadfence();  // the CTA's pieces, which the barrier ordered before, to all CTAs
-    const bool last = atomicAdd(p.cnt + first, 1) == n - 1;
-    __threadfence();
-    if (last) p.cnt[first] = 0;  // for the next launch
-    shared_from[threadIdx.x] = first;
-    shared_count[threadIdx.x] = last ? n : 0;
+    if (lane == 0) set_count[0] = __popc(begin), set_count[1] = __popc(out);
   }
   __syncthreads();
-  for (int k = 0; k < shared_n; ++k) {
-    const int first = shared_from[k], n = shared_count[k];
-    if (n == 0) continue;
-    auto piece = [&](int i) -> const float* { return p.ws + static_cast<int64_t>(2 * (first + i) + (i == 0 ? 1 : 0)) * Sh::kPiece; };
-    attn_join<D, MR, 16, false>(p, shared_of[k].r, shared_of[k].hx, n, piece, nullptr);
+  sets = set_count[0], shared_n = set_count[1];
+#pragma unroll 1
+  for (int round = 0; round < 2; ++round) {
+    // four elements of a head per thread: D / 4 threads a head, MR heads a set
+    constexpr int kPer = MR * (D / 4);
+#pragma unroll 1
+    for (int e = threadIdx.x; e < sets * kPer; e += kAttnThreads) {
+      const AttnSet t = set_of[e / kPer];
+      const int g = e % kPer / (D / 4), d = e % (D / 4) * 4;
+      int kv, g0;
+      attn_group<MR>(p, t.hx, kv, g0);
+      if (g0 + g >= p.group || t.r < 0) continue;
+      float m, l;
+      auto piece = [&](int i) -> const float* {
+        if (round) return p.ws + static_cast<int64_t>(2 * (t.to + i) + (i == 0 ? 1 : 0)) * Sh::kPiece;
+        const int q = t.slots >> (4 * i) & 15;
+        return q & 1 ? reinterpret_cast<const float*>(ring + (q >> 1) * S * 2 * Sh::kTile) : heads_mem + (q >> 1) * Sh::kPiece;
+      };
+      const float4 o = attn_join<MR, D>(t.n, g, d, piece, m, l);
+      if (!round && t.to >= 0) {
+        float* to = p.ws + static_cast<int64_t>(t.to) * Sh::kPiece;
+        if (d == 0) to[g] = m, to[MR + g] = l;
+        *reinterpret_cast<float4*>(to + 2 * MR + g * D + d) = o;
+      } else {
+        const float f = l != 0.f ? 1.f / l : 0.f;
+        const int64_t at = t.r * p.out_stride + static_cast<int64_t>(kv * p.group + g0 + g) * D + d;
+        attn_store2(p, at, o.x * f, o.y * f);
+        attn_store2(p, at + 2, o.z * f, o.w * f);
+        if (d == 0 && p.lse) p.lse[static_cast<int64_t>(t.r) * p.q_heads + kv * p.group + g0 + g] = attn_lse(m, l);
+      }
+    }
+    if (round || shared_n == 0) return;
+    __syncthreads();
+    sets = shared_n;
+    if (static_cast<int>(threadIdx.x) < shared_n) {
+      const AttnPiece a = shared_of[threadIdx.x];
+      const int first = cta_of(a.lo), n = cta_of(a.hi - 1) - first + 1;
+      __threadfence();  // the CTA's pieces, which the barrier ordered before, to all CTAs
+      const bool last = atomicAdd(p.cnt + first, 1) == n - 1;
+      __threadfence();
+      if (last) p.cnt[first] = 0;  // for the next launch
+      set_of[threadIdx.x] = AttnSet{last ? a.r : -1, a.hx, n, first, 0};
+    }
+    __syncthreads();
   }
 }
 
