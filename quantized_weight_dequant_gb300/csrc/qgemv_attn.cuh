@@ -45,7 +45,7 @@
 namespace qg {
 
 constexpr int kAttnWarps = 4;
-constexpr int kAttnThreads = 32 * (kAttnWarps + 1);  // and one that copies
+constexpr int kAttnThreads = 32 * kAttnWarps;
 
 struct AttnArgs {
   const void* q;
@@ -80,6 +80,7 @@ struct AttnShape {
   static constexpr int kRB = kRow < 128 ? kRow : 128;         // bytes of a row part in shared memory
   static constexpr int kParts = kRow / kRB;
   static constexpr int kTT = kRow >= 256 ? 16 : 4096 / kRow;  // tokens per tile
+  static constexpr int kTTLog2 = kTT == 16 ? 4 : kTT == 32 ? 5 : 6;
   static constexpr int kTile = kTT * kRow;                    // bytes of keys (and of values)
   static constexpr int kScaleBytes = KT == QGEMV_KV_E4M3 ? 2 * kTT * 4 : 0;
   static constexpr int kPiece = MR * (D + 2);                 // floats of a piece: m, l, O
@@ -153,16 +154,25 @@ __device__ __forceinline__ uint32_t e4m3x2(uint32_t two) {
   return u;
 }
 
+// True in one lane of the (whole) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t yes;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(yes));
+  return yes != 0;
+}
+
 __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, int x, int row, int part, int head, int page, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(row), "r"(part), "r"(head), "r"(page), "r"(bar)
       : "memory");
 }
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src), "r"(bytes),
-               "r"(bar)
-               : "memory");
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// One arrival on `bar` when this thread's cp.async so far are there.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 // What a warp has to know of a tile when it computes it (shared memory, one per tile in flight).
@@ -293,10 +303,10 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
   constexpr int TT = Sh::kTT, S = Sh::kStages, NT = TT / 8;  // NT: 8-token column tiles of the scores
   constexpr int OT = D / 8;                                  // 8-wide column tiles of the output
   extern __shared__ uint8_t dyn[];
-  __shared__ int64_t scan[kAttnWarps + 1];
+  __shared__ int64_t scan[kAttnWarps];
   __shared__ AttnStart start_of[kAttnWarps];
   __shared__ AttnTile info_of[kAttnWarps][4];
-  __shared__ uint64_t bars_of[kAttnWarps][8];     // of each stage: its copies are there; it is free again
+  __shared__ uint64_t bars_of[kAttnWarps][4];     // of each stage: its copies are there
   __shared__ AttnPiece piece_of[2 * kAttnWarps];  // of each warp the one that began before its share, and the last
   __shared__ AttnPiece shared_of[2];
   __shared__ AttnSet set_of[2 * kAttnWarps];
@@ -306,15 +316,13 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t{1023});
   float* heads_mem = reinterpret_cast<float*>(ring + kAttnWarps * S * 2 * Sh::kTile);
   uint8_t* scales_mem = reinterpret_cast<uint8_t*>(heads_mem + kAttnWarps * Sh::kPiece);
-  if (warp < kAttnWarps) {
-    if (lane < 2 * S) mbar_init(smem_u32(&bars_of[warp][lane]), 1);
-    if (lane == 0) {
-      piece_of[2 * warp].r = piece_of[2 * warp + 1].r = -1;
-      fence_mbar_init();
-    }
-  } else if (lane < 2) {
-    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(lane ? &map_v : &map_k)) : "memory");
+  if (lane < S) mbar_init(smem_u32(&bars_of[warp][lane]), kF8 ? 33 : 1);  // the elected lane, and each for its scales
+  if (lane == 0) {
+    piece_of[2 * warp].r = piece_of[2 * warp + 1].r = -1;
+    fence_mbar_init();
   }
+  if (threadIdx.x < 2)
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(threadIdx.x ? &map_v : &map_k)) : "memory");
 
   // ---- the share of this CTA and of its warps
   const int hxs = p.kv_heads * p.splits;
@@ -347,7 +355,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
   const bool any_none = __syncthreads_or(none);
   int64_t total = 0, before = upto - mine;
 #pragma unroll
-  for (int w = 0; w <= kAttnWarps; ++w) {
+  for (int w = 0; w < kAttnWarps; ++w) {
     if (w < warp) before += scan[w];
     total += scan[w];
   }
@@ -389,43 +397,55 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
   if (!busy) return;
   __syncthreads();
 
-  if (warp == kAttnWarps) {
-    // ---- the copying warp: lanes 8 w .. 8 w + 7 walk the tiles of warp w, all four walks in step
-    const int w = lane >> 3, j = lane & 7;
-    const AttnStart st = start_of[w];
-    int64_t left = st.left, it_at = st.at;
-    int it_r = st.r, it_hx = st.hx, it_t = 0, it_first = 0, it_end = 0, it_lo = 0, it_len = 0, it_next = 0;
-    auto enter = [&](int r, int len) {
-      it_r = r;
-      it_len = len;
-      it_lo = attn_first(p, len);
-      it_first = it_lo / TT;
-      it_end = (len + TT - 1) / TT;
-      it_next = r + 1 < p.requests ? p.lens[r + 1] : 0;  // used when this request is through
-    };
+  const int quad = lane & 3, row = lane >> 2;
+  const uint32_t ring_w = smem_u32(ring) + warp * S * 2 * Sh::kTile, scale_w = smem_u32(scales_mem) + warp * S * Sh::kScaleBytes;
+  const uint32_t full = smem_u32(&bars_of[warp][0]);
+  const int ch = 1 << p.chunk_log2, chunks = TT >> p.chunk_log2;
+
+  // ---- the walk over the tiles of this warp's share, in batches of tiles of one (request, head) whose chunks
+  // have a lane each: the lane asks for its chunk's page while the batch before is copied
+  const AttnStart st = start_of[warp];
+  int64_t left = st.left, it_at = st.at;
+  int it_r = st.r, it_hx = st.hx, it_t = 0, it_first = 0, it_end = 0, it_lo = 0, it_len = 0, it_next = 0, it_n = 0, it_page = -1;
+  bool it_want = false;
+  auto enter = [&](int r, int len) {
+    it_r = r;
+    it_len = len;
+    it_lo = attn_first(p, len);
+    it_first = it_lo / TT;
+    it_end = (len + TT - 1) / TT;
+    it_next = r + 1 < p.requests ? p.lens[r + 1] : 0;  // used when this request is through
+  };
+  auto ask = [&]() {  // the batch that begins at tile it_t
+    const int at = it_t * TT + (lane << p.chunk_log2);
+    it_n = static_cast<int>(min(left, static_cast<int64_t>(min(it_end - it_t, 32 >> (Sh::kTTLog2 - p.chunk_log2)))));
+    it_want = left > 0 && lane < it_n * chunks && at < it_len && at + ch > it_lo;
+    it_page = it_want ? p.table[it_r * p.table_stride + attn_page(p, at)] : -1;
+  };
+  if (left > 0) {
     enter(st.r, attn_clamp(p, p.lens[st.r]));
     it_t = it_first + st.skip;
-    const int ch = 1 << p.chunk_log2, chunks = TT >> p.chunk_log2;
-    static_assert(TT <= 64, "a tile has at most eight chunks");
-    const uint32_t full = smem_u32(&bars_of[w][0]), empty = smem_u32(&bars_of[w][S]);
-    const uint32_t ring_w = smem_u32(ring) + w * S * 2 * Sh::kTile, scale_w = smem_u32(scales_mem) + w * S * Sh::kScaleBytes;
-    AttnTile d;      // the next tile
-    int page = -1;   // the page of its chunk j
-    bool want = false;
-    bool more_tiles = left > 0, alive = true;
-    auto describe = [&]() {
-      const int at = it_t * TT + (j << p.chunk_log2);
-      want = j < chunks && at < it_len && at + ch > it_lo;
-      page = want ? p.table[it_r * p.table_stride + attn_page(p, at)] : -1;
-      d.r = it_r;
-      d.hx = it_hx;
-      d.tok = it_t * TT;
-      d.lo = it_lo;
-      d.hi = it_len;
-      d.ends = (it_t == it_first ? 1 : 0) | (it_t == it_end - 1 ? 2 : 0);
-      d.at = it_at;
-      --left;
-      if (++it_t == it_end) {
+    ask();
+  }
+  int b_r = 0, b_hx = 0, b_t = 0, b_n = 0, b_first = 0, b_end = 0, b_lo = 0, b_len = 0, b_page = -1, b_k = 0, b_kv = 0;  // the batch in hand
+  int64_t b_at = 0;
+  uint32_t b_good = 0, b_bad = 0;
+  bool to_copy = left > 0;
+  // Copies the next tile into stage s.
+  auto issue = [&](int s) {
+    if (b_k == b_n) {
+      b_k = 0;
+      b_r = it_r, b_hx = it_hx, b_t = it_t, b_n = it_n, b_first = it_first, b_end = it_end, b_lo = it_lo, b_len = it_len, b_at = it_at;
+      b_page = it_page;
+      const bool in = it_page >= 0 && it_page < p.pages;
+      b_good = __ballot_sync(0xffffffffu, it_want && in);
+      b_bad = __ballot_sync(0xffffffffu, it_want && !in);
+      if (b_bad && lane == 0) atomicOr(p.err, kDevErrIndex);
+      int g0;
+      attn_group<MR>(p, b_hx, b_kv, g0);
+      it_t += it_n;
+      left -= it_n;
+      if (it_t == it_end) {
         it_at += it_end - it_first + p.seg_cost;
         left -= p.seg_cost;
         if (++it_hx == hxs && left > 0) {
@@ -437,50 +457,44 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
         }
         it_t = it_first;
       }
-      if (left <= 0) d.ends |= 4;
-    };
-    if (more_tiles) describe();
-    if (p.stall && cta == 0) more_tiles = false;  // nothing is copied: every wait of this CTA runs out
-#pragma unroll 1
-    for (int i = 0, s = 0, lap = 0; __any_sync(0xffffffffu, more_tiles); ++i) {
-      if (more_tiles && lap > 0 && !mbar_wait_bounded(empty + 8 * s, (lap - 1) & 1, p.spin_ns)) alive = false;
-      alive = __all_sync(0xffffffffu, alive);
-      more_tiles = more_tiles && alive;
-      const bool in = page >= 0 && page < p.pages;
-      const uint32_t bad = __ballot_sync(0xffffffffu, more_tiles && want && !in) >> (8 * w) & 0xff;
-      const uint32_t good = __ballot_sync(0xffffffffu, more_tiles && want && in) >> (8 * w) & 0xff;
-      if (j == 0 && more_tiles) {
-        d.bad = bad;
-        if (bad) atomicOr(p.err, kDevErrIndex);
-        info_of[w][s] = d;
-        mbar_arrive_expect_tx(full + 8 * s, static_cast<uint32_t>(__popc(good)) * (2 * Sh::kRow + (kF8 ? 8 : 0)) << p.chunk_log2);
+      ask();
+    }
+    const int t = b_t + b_k, tok = t * TT, shift = b_k * chunks;
+    const uint32_t mask = (2u << (chunks - 1)) - 1, good = b_good >> shift & mask;
+    ++b_k;
+    to_copy = b_k < b_n || left > 0;
+    const uint32_t bar = full + 8 * s, dst = ring_w + s * 2 * Sh::kTile;
+    if (elect_one()) {
+      AttnTile& d = info_of[warp][s];
+      d.r = b_r;
+      d.hx = b_hx;
+      d.tok = tok;
+      d.lo = b_lo;
+      d.hi = b_len;
+      d.ends = (t == b_first ? 1 : 0) | (t == b_end - 1 ? 2 : 0) | (to_copy ? 0 : 4);
+      d.bad = b_bad >> shift & mask;
+      d.at = b_at;
+      mbar_arrive_expect_tx(bar, static_cast<uint32_t>(__popc(good)) * 2 * Sh::kRow << p.chunk_log2);
+    }
+    for (int j = 0; j < chunks; ++j) {
+      const int page = __shfl_sync(0xffffffffu, b_page, shift + j), at = tok + (j << p.chunk_log2), in_page = at - attn_page(p, at) * p.page_size;
+      if (!(good >> j & 1)) continue;
+      if (elect_one()) {
+        tma_load_5d(dst + (j << p.chunk_log2) * Sh::kRow, &map_k, 0, in_page, 0, b_kv, page, bar);
+        tma_load_5d(dst + Sh::kTile + (j << p.chunk_log2) * Sh::kRow, &map_v, 0, in_page, 0, b_kv, page, bar);
       }
       __syncwarp();
-      if (more_tiles && want && in) {
-        int kv, g0;
-        attn_group<MR>(p, d.hx, kv, g0);
-        const int at = d.tok + (j << p.chunk_log2), in_page = at - attn_page(p, at) * p.page_size;
-        const uint32_t dst = ring_w + s * 2 * Sh::kTile + (j << p.chunk_log2) * Sh::kRow;
-        tma_load_5d(dst, &map_k, 0, in_page, 0, kv, page, full + 8 * s);
-        tma_load_5d(dst + Sh::kTile, &map_v, 0, in_page, 0, kv, page, full + 8 * s);
-        if constexpr (kF8) {
-          const int64_t src = page * p.scale_stride + static_cast<int64_t>(kv) * p.page_size + in_page;
-          const uint32_t sd = scale_w + s * Sh::kScaleBytes + (j << p.chunk_log2) * 4;
-          bulk_load(sd, p.k_scale + src, 4u << p.chunk_log2, full + 8 * s);
-          bulk_load(sd + TT * 4, p.v_scale + src, 4u << p.chunk_log2, full + 8 * s);
+      if constexpr (kF8) {  // two scales per token, 16 bytes a lane
+        const int per = ch >> 2, u = lane & (per - 1);
+        if (lane < 2 * per) {
+          const int64_t from = page * p.scale_stride + static_cast<int64_t>(b_kv) * p.page_size + in_page + 4 * u;
+          cp_async16(scale_w + s * Sh::kScaleBytes + (lane < per ? 0 : TT * 4) + (j << p.chunk_log2) * 4 + 16 * u, (lane < per ? p.k_scale : p.v_scale) + from);
         }
       }
-      more_tiles = more_tiles && left > 0;
-      if (more_tiles) describe();
-      if (++s == S) s = 0, ++lap;
     }
-    if (!alive && lane == 0) atomicOr(p.err, kDevErrTimeout);
-  } else {
-    // ---- the computing warps
-    const int quad = lane & 3, row = lane >> 2;
-    const uint32_t ring_w = smem_u32(ring) + warp * S * 2 * Sh::kTile, scale_w = smem_u32(scales_mem) + warp * S * Sh::kScaleBytes;
-    const uint32_t full = smem_u32(&bars_of[warp][0]), empty = smem_u32(&bars_of[warp][S]);
-    const int ch = 1 << p.chunk_log2;
+    if constexpr (kF8) cp_async_arrive(bar);
+    __syncwarp();
+  };
 
   // Byte offset of token t of a tile, row part `part`, in shared memory (before the swizzle).
   auto line_of = [&](int t, int part) {
@@ -617,40 +631,46 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
     }
   };
 
-    const AttnStart st = start_of[warp];
-    bool alive = true, begun = false;  // begun: the current (request, head) began in this warp's share
-    bool asked = false;                // its queries have been requested
-    if (st.left > 0) {
-      fetch_q(st.r, st.hx);
+  bool alive = true, begun = false;  // begun: the current (request, head) began in this warp's share
+  bool asked = false;                // its queries have been requested
+  const bool any = st.left > 0;
+  if (any) {
+    fetch_q(st.r, st.hx);
+    asked = true;
+  }
+  if (p.stall && cta == 0) to_copy = false;  // nothing is copied: the waits of this CTA run out
+#pragma unroll 1
+  for (int i = 1 - S, s = 1, lap = 0; any; ++i) {
+    // stage s - 1 is free: before the first tile all are, then tile i - 1 was its last
+    if (to_copy) issue(s == 0 ? S - 1 : s - 1);
+    if (i < 0) {
+      s = s + 1 == S ? 0 : s + 1;
+      continue;
+    }
+    alive = mbar_wait_bounded(full + 8 * s, lap & 1, p.spin_ns);
+    alive = __all_sync(0xffffffffu, alive);
+    if (!alive) {
+      if (lane == 0) atomicOr(p.err, kDevErrTimeout);
+      break;
+    }
+    const AttnTile d = info_of[warp][s];
+    if (i == 0 || (d.ends & 1)) {
+      begun = d.ends & 1;
+      if (!asked) fetch_q(d.r, d.hx);
+      asked = false;
+      take_q();
+#pragma unroll
+      for (int t = 0; t < OT; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
+      m[0] = m[1] = neg;
+      l[0] = l[1] = 0.f;
+      c[0] = c[1] = 0.f;
+    }
+    const bool last = d.ends & 4;
+    const int s_next = s + 1 == S ? 0 : s + 1;
+    if (D < 256 && (d.ends & 2) && !last) {  // the next tile, already on its way, begins another
+      fetch_q(info_of[warp][s_next].r, info_of[warp][s_next].hx);
       asked = true;
     }
-#pragma unroll 1
-    for (int i = 0, s = 0, lap = 0; st.left > 0; ++i) {
-      alive = mbar_wait_bounded(full + 8 * s, lap & 1, p.spin_ns);
-      alive = __all_sync(0xffffffffu, alive);
-      if (!alive) {
-        if (lane == 0) atomicOr(p.err, kDevErrTimeout);
-        break;
-      }
-      const AttnTile d = info_of[warp][s];
-      if (i == 0 || (d.ends & 1)) {
-        begun = d.ends & 1;
-        if (!asked) fetch_q(d.r, d.hx);
-        asked = false;
-        take_q();
-#pragma unroll
-        for (int t = 0; t < OT; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
-        m[0] = m[1] = neg;
-        l[0] = l[1] = 0.f;
-        c[0] = c[1] = 0.f;
-      }
-      const bool last = d.ends & 4;
-      const int s_next = s + 1 == S ? 0 : s + 1;
-      if (D < 256 && (d.ends & 2) && !last && mbar_try_wait(full + 8 * s_next, (s_next ? lap : lap + 1) & 1)) {
-        fetch_q(info_of[warp][s_next].r, info_of[warp][s_next].hx);
-        asked = true;
-      }
-      asked = __all_sync(0xffffffffu, asked);
     const uint32_t kb = ring_w + s * 2 * Sh::kTile, vb = kb + Sh::kTile;
     const bool edge = d.tok < d.lo || d.tok + TT > d.hi || d.bad;
 
@@ -804,7 +824,6 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
       }
     }
     __syncwarp();  // every lane is done with the stage
-    if (lane == 0 && !last) mbar_arrive(empty + 8 * s);
     const bool whole = (d.ends & 2) && begun;
     // one that began before this share, or goes on behind it, leaves a piece: where the copies were when it
     // is the last that the warp has to do, else in a place of its own
@@ -818,7 +837,6 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
       mbar_wait_bounded(full + 8 * s, 0, p.spin_ns);
       mbar_wait_bounded(full + 8 * s, 1, p.spin_ns);
     }
-  }
   }
   __syncthreads();
 
