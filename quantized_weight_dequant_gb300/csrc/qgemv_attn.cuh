@@ -176,13 +176,14 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
 }
 
 // What a warp has to know of a tile when it computes it (shared memory, one per tile in flight).
-struct AttnTile {
-  int r, hx;      // request; kv head * splits + split
-  int tok;        // first token
-  int lo, hi;     // tokens that the request sees
-  int ends;       // bit 0: first tile of its (request, head); bit 1: last
-  uint32_t bad;   // chunks whose page is outside the cache
-  int64_t at;     // first unit of the (request, head)
+struct __align__(16) AttnTile {
+  int r, hx;     // request; kv head * splits + split
+  int lo, hi;    // tokens that the request sees
+  int tok;       // first token
+  int ends;      // bit 0: first tile of its (request, head); bit 1: last; bit 2: last of the share
+  int bad;       // chunks whose page is outside the cache
+  int pad;
+  int64_t at;    // first unit of the (request, head)
 };
 
 // Where a warp's share begins: first unit of its (request, head), units left after its cost, tiles to skip.
@@ -360,7 +361,8 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
     total += scan[w];
   }
   const int cta = blockIdx.x;
-  const int ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), attn_div(total + p.min_units - 1, p.min_units)));  // with a share
+  const int ctas = total >= static_cast<int64_t>(p.min_units) * gridDim.x ? gridDim.x  // with a share
+                                                                          : static_cast<int>(attn_div(total + p.min_units - 1, p.min_units));
   const bool busy = cta < ctas;
   const int64_t each = busy ? attn_div(total, ctas) : 0;  // the first `more` CTAs have one unit more
   const int more = static_cast<int>(total - each * ctas);
@@ -427,7 +429,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
     it_t = it_first + st.skip;
     ask();
   }
-  int b_r = 0, b_hx = 0, b_t = 0, b_n = 0, b_first = 0, b_end = 0, b_lo = 0, b_len = 0, b_page = -1, b_k = 0, b_kv = 0;  // the batch in hand
+  int b_r = 0, b_hx = 0, b_t = 0, b_n = 0, b_first = 0, b_end = 0, b_lo = 0, b_len = 0, b_page = -1, b_in = 0, b_k = 0, b_kv = 0;  // the batch in hand
   int64_t b_at = 0;
   uint32_t b_good = 0, b_bad = 0;
   bool to_copy = left > 0;
@@ -437,6 +439,8 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
       b_k = 0;
       b_r = it_r, b_hx = it_hx, b_t = it_t, b_n = it_n, b_first = it_first, b_end = it_end, b_lo = it_lo, b_len = it_len, b_at = it_at;
       b_page = it_page;
+      b_in = b_t * TT + (lane << p.chunk_log2);
+      b_in -= attn_page(p, b_in) * p.page_size;
       const bool in = it_page >= 0 && it_page < p.pages;
       b_good = __ballot_sync(0xffffffffu, it_want && in);
       b_bad = __ballot_sync(0xffffffffu, it_want && !in);
@@ -464,34 +468,33 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
     ++b_k;
     to_copy = b_k < b_n || left > 0;
     const uint32_t bar = full + 8 * s, dst = ring_w + s * 2 * Sh::kTile;
-    if (elect_one()) {
-      AttnTile& d = info_of[warp][s];
-      d.r = b_r;
-      d.hx = b_hx;
-      d.tok = tok;
-      d.lo = b_lo;
-      d.hi = b_len;
-      d.ends = (t == b_first ? 1 : 0) | (t == b_end - 1 ? 2 : 0) | (to_copy ? 0 : 4);
-      d.bad = b_bad >> shift & mask;
-      d.at = b_at;
-      mbar_arrive_expect_tx(bar, static_cast<uint32_t>(__popc(good)) * 2 * Sh::kRow << p.chunk_log2);
-    }
-    for (int j = 0; j < chunks; ++j) {
-      const int page = __shfl_sync(0xffffffffu, b_page, shift + j), at = tok + (j << p.chunk_log2), in_page = at - attn_page(p, at) * p.page_size;
-      if (!(good >> j & 1)) continue;
+    auto copy = [&](int j) {  // chunk j of the tile
+      const int page = __shfl_sync(0xffffffffu, b_page, shift + j), in_page = __shfl_sync(0xffffffffu, b_in, shift + j);
+      if (!(good >> j & 1)) return;
+      const uint32_t to = dst + (j << p.chunk_log2) * Sh::kRow;
       if (elect_one()) {
-        tma_load_5d(dst + (j << p.chunk_log2) * Sh::kRow, &map_k, 0, in_page, 0, b_kv, page, bar);
-        tma_load_5d(dst + Sh::kTile + (j << p.chunk_log2) * Sh::kRow, &map_v, 0, in_page, 0, b_kv, page, bar);
+        tma_load_5d(to, &map_k, 0, in_page, 0, b_kv, page, bar);
+        tma_load_5d(to + Sh::kTile, &map_v, 0, in_page, 0, b_kv, page, bar);
       }
-      __syncwarp();
       if constexpr (kF8) {  // two scales per token, 16 bytes a lane
-        const int per = ch >> 2, u = lane & (per - 1);
-        if (lane < 2 * per) {
-          const int64_t from = page * p.scale_stride + static_cast<int64_t>(b_kv) * p.page_size + in_page + 4 * u;
-          cp_async16(scale_w + s * Sh::kScaleBytes + (lane < per ? 0 : TT * 4) + (j << p.chunk_log2) * 4 + 16 * u, (lane < per ? p.k_scale : p.v_scale) + from);
+        const int each16 = ch >> 2, u = lane & (each16 - 1);
+        if (lane < 2 * each16) {
+          const int64_t from = page * p.scale_stride + b_kv * p.page_size + in_page + 4 * u;
+          cp_async16(scale_w + s * Sh::kScaleBytes + (lane < each16 ? 0 : TT * 4) + (j << p.chunk_log2) * 4 + 16 * u,
+                     (lane < each16 ? p.k_scale : p.v_scale) + from);
         }
       }
+    };
+    if (elect_one()) {
+      int4* d = reinterpret_cast<int4*>(&info_of[warp][s]);
+      d[0] = make_int4(b_r, b_hx, b_lo, b_len);
+      d[1] = make_int4(tok, (t == b_first ? 1 : 0) | (t == b_end - 1 ? 2 : 0) | (to_copy ? 0 : 4), b_bad >> shift & mask, 0);
+      *reinterpret_cast<int64_t*>(d + 2) = b_at;
+      mbar_arrive_expect_tx(bar, static_cast<uint32_t>(__popc(good)) * 2 * Sh::kRow << p.chunk_log2);
     }
+    copy(0);
+#pragma unroll 1
+    for (int j = 1; j < chunks; ++j) copy(j);
     if constexpr (kF8) cp_async_arrive(bar);
     __syncwarp();
   };
