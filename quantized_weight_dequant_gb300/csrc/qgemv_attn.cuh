@@ -40,6 +40,7 @@
 #include <cstdint>
 
 #include "../../include/qgemv.h"
+#include "qgemv_mma.cuh"
 #include "qgemv_ptx.cuh"
 
 namespace qg {
@@ -111,40 +112,6 @@ __device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t (&v)[4]) {
                : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
                : "r"(a)
                : "memory");
-}
-
-template <bool BF>
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  if constexpr (BF)
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-  else
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// Two fp32 values as a 16-bit pair (a in the low half), and what the pair leaves of them.
-template <bool BF>
-__device__ __forceinline__ uint32_t pair16(float a, float b) {
-  uint32_t u;
-  if constexpr (BF)
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u) : "f"(b), "f"(a));
-  else
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(u) : "f"(b), "f"(a));
-  return u;
-}
-template <bool BF>
-__device__ __forceinline__ float2 unpair16(uint32_t u) {
-  if constexpr (BF) return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
-  return __half22float2(*reinterpret_cast<const __half2*>(&u));
-}
-template <bool BF>
-__device__ __forceinline__ void split16(float a, float b, uint32_t& hi, uint32_t& lo) {
-  hi = pair16<BF>(a, b);
-  const float2 f = unpair16<BF>(hi);
-  lo = pair16<BF>(a - f.x, b - f.y);
 }
 
 // Two e4m3 codes as fp16 (exact).
