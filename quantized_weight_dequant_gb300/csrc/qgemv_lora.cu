@@ -12,13 +12,48 @@ using namespace qg;
 
 namespace {
 
-template <bool BF>
+template <int TG, bool BF>
 const void* kernel_for(int out) {
   switch (out) {
-    case QGEMV_OUT_F32: return reinterpret_cast<const void*>(lora_kernel<BF, QGEMV_OUT_F32>);
-    case QGEMV_OUT_F16: return reinterpret_cast<const void*>(lora_kernel<BF, QGEMV_OUT_F16>);
-    default: return reinterpret_cast<const void*>(lora_kernel<BF, QGEMV_OUT_BF16>);
+    case QGEMV_OUT_F32: return reinterpret_cast<const void*>(lora_kernel<BF, QGEMV_OUT_F32, TG>);
+    case QGEMV_OUT_F16: return reinterpret_cast<const void*>(lora_kernel<BF, QGEMV_OUT_F16, TG>);
+    default: return reinterpret_cast<const void*>(lora_kernel<BF, QGEMV_OUT_BF16, TG>);
   }
+}
+
+template <int TG>
+qgemv_status_t launch(const Handle& h, const qgemv_lora_t& p, cudaStream_t stream) {
+  // Clusters per 32 rows: one for each adapter that they can have, but no more in all than run at once
+  // (then a cluster takes its share of the adapters one after another).
+  const int64_t chunks = (p.rows + kLoraRows - 1) / kLoraRows;
+  const int64_t most = std::min<int64_t>(kLoraRows, p.rows), resident = int64_t{h.sms} * LoraShape<TG>::kCtasPerSm / kLoraCluster;
+  int slots = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(most, (resident + chunks - 1) / chunks)));
+  const int64_t grid = chunks * slots * kLoraCluster;
+  if (grid > 0x7fffffff) return QGEMV_ERR_BAD_SHAPE;
+  const void* fn = p.type == QGEMV_OUT_BF16 ? kernel_for<TG, true>(p.out) : kernel_for<TG, false>(p.out);
+  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(LoraSmem<TG>)) != cudaSuccess) {
+    cudaGetLastError();
+    return QGEMV_ERR_CUDA;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+  cfg.blockDim = dim3(LoraShape<TG>::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = sizeof(LoraSmem<TG>);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kLoraCluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int* err = h.err;
+  void* args[] = {const_cast<qgemv_lora_t*>(&p), &slots, &err};
+  if (cudaLaunchKernelExC(&cfg, fn, args) != cudaSuccess) {
+    cudaGetLastError();
+    return QGEMV_ERR_CUDA;
+  }
+  return QGEMV_OK;
 }
 
 }  // namespace
@@ -37,35 +72,5 @@ extern "C" qgemv_status_t qgemv_run_lora(qgemv_handle_t hh, const qgemv_lora_t* 
   if (!aligned16(p.x) || !aligned16(p.A) || !aligned16(p.B) || !aligned16(p.base) || !aligned16(p.y) || p.x_stride % 8)
     return QGEMV_ERR_MISALIGNED;
   if (p.rows == 0) return QGEMV_OK;
-  // Clusters per 32 rows: one for each adapter that they can have, but no more than four per eight SMs where
-  // many rows fill the GPU (then a cluster takes its share of the adapters one after another).
-  const int64_t chunks = (p.rows + kLoraRows - 1) / kLoraRows;
-  const int64_t most = std::min<int64_t>(kLoraRows, p.rows);
-  int slots = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(most, (4 * h->sms / kLoraCluster + chunks - 1) / chunks)));
-  const int64_t grid = chunks * slots * kLoraCluster;
-  if (grid > 0x7fffffff) return QGEMV_ERR_BAD_SHAPE;
-  const void* fn = p.type == QGEMV_OUT_BF16 ? kernel_for<true>(p.out) : kernel_for<false>(p.out);
-  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(LoraSmem)) != cudaSuccess) {
-    cudaGetLastError();
-    return QGEMV_ERR_CUDA;
-  }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
-  cfg.blockDim = dim3(kLoraThreads, 1, 1);
-  cfg.dynamicSmemBytes = sizeof(LoraSmem);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = kLoraCluster;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  int* err = h->err;
-  void* args[] = {const_cast<qgemv_lora_t*>(&p), &slots, &err};
-  if (cudaLaunchKernelExC(&cfg, fn, args) != cudaSuccess) {
-    cudaGetLastError();
-    return QGEMV_ERR_CUDA;
-  }
-  return QGEMV_OK;
+  return p.rows <= kLoraFewRows ? launch<1>(*h, p, stream) : launch<4>(*h, p, stream);
 }
