@@ -15,12 +15,11 @@ namespace {
 qgemv_status_t launched() { return cudaGetLastError() == cudaSuccess ? QGEMV_OK : QGEMV_ERR_CUDA; }
 
 template <int T>
-void launch_store(const qgemv_kv_store_t& p, int64_t grid, int* err, cudaStream_t s) {
-  const unsigned g = static_cast<unsigned>(grid);
+void launch_store(const qgemv_kv_store_t& p, dim3 g, int threads, int* err, cudaStream_t s) {
   switch (p.cache.head_dim) {
-    case 64: kv_store_kernel<T, 64><<<g, 256, 0, s>>>(p, err); break;
-    case 128: kv_store_kernel<T, 128><<<g, 256, 0, s>>>(p, err); break;
-    default: kv_store_kernel<T, 256><<<g, 256, 0, s>>>(p, err); break;
+    case 64: kv_store_kernel<T, 64><<<g, threads, 0, s>>>(p, err); break;
+    case 128: kv_store_kernel<T, 128><<<g, threads, 0, s>>>(p, err); break;
+    default: kv_store_kernel<T, 256><<<g, threads, 0, s>>>(p, err); break;
   }
 }
 
@@ -38,7 +37,8 @@ qgemv_status_t qgemv_page_plan(qgemv_handle_t hh, const qgemv_page_plan_t* plan,
   if (!p.counts || !p.free_count || (p.capacity > 0 && !p.slots)) return QGEMV_ERR_INVALID_ARG;
   if (p.requests > 0 && (!p.cached || !p.fresh || !p.table || !p.free_pages || !p.lens)) return QGEMV_ERR_INVALID_ARG;
   if (!aligned16(p.slots) || !aligned16(p.positions) || !aligned16(p.owners)) return QGEMV_ERR_MISALIGNED;
-  const int threads = kPlanThreads;
+  // one scan step for up to 512 requests; a few need a few warps, whose scan is shorter
+  const int threads = std::min(kPlanThreads, (std::max(p.requests, 128) + 31) / 32 * 32);
   int64_t per = kPlanThreads * kPlanVec;
   const int64_t grid = std::max<int64_t>(1, std::min<int64_t>((p.capacity + per - 1) / per, h->sms));
   per = (p.capacity + grid - 1) / grid;
@@ -67,14 +67,16 @@ qgemv_status_t qgemv_kv_store(qgemv_handle_t hh, const qgemv_kv_store_t* store, 
       p.v_stride % unit || (p.q && (p.q_stride % unit || p.q_out_stride % 8)))
     return QGEMV_ERR_MISALIGNED;
   if (p.tokens == 0) return QGEMV_OK;
-  const int64_t heads = Hq + 2 * Hk, per_cta = 256 / (D / 8);  // heads per CTA
-  if (p.tokens > (int64_t{1} << 40) / heads) return QGEMV_ERR_BAD_SHAPE;
-  const int64_t grid = (p.tokens * heads + per_cta - 1) / per_cta;
-  if (grid > 0x7fffffff) return QGEMV_ERR_BAD_SHAPE;
+  if (p.tokens > 0x7fffffff || Hq + 2 * Hk > 0xfffff) return QGEMV_ERR_BAD_SHAPE;
+  // a thread for each eight elements of the token's heads, in whole warps
+  const int threads = static_cast<int>(std::min<int64_t>(kStoreThreads, ((Hq + 2 * Hk) * (D / 8) + 31) / 32 * 32));
+  // few tokens: their heads are spread over as many CTAs as keep one head a thread group, and the SMs busy
+  const int64_t groups = ((Hq + 2 * Hk) * (D / 8) + threads - 1) / threads;
+  const dim3 grid(static_cast<unsigned>(p.tokens), static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(groups, 2 * h->sms / p.tokens))));
   switch (p.in) {
-    case QGEMV_OUT_F32: launch_store<QGEMV_OUT_F32>(p, grid, h->err, stream); break;
-    case QGEMV_OUT_F16: launch_store<QGEMV_OUT_F16>(p, grid, h->err, stream); break;
-    default: launch_store<QGEMV_OUT_BF16>(p, grid, h->err, stream); break;
+    case QGEMV_OUT_F32: launch_store<QGEMV_OUT_F32>(p, grid, threads, h->err, stream); break;
+    case QGEMV_OUT_F16: launch_store<QGEMV_OUT_F16>(p, grid, threads, h->err, stream); break;
+    default: launch_store<QGEMV_OUT_BF16>(p, grid, threads, h->err, stream); break;
   }
   return launched();
 }

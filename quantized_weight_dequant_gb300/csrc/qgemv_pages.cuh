@@ -27,7 +27,7 @@ struct PlanItem {
   int32_t have;   // pages before
 };
 
-constexpr int kPlanThreads = 512;   // also the requests per scan step
+constexpr int kPlanThreads = 512;   // at most; also the requests per scan step
 constexpr int kPlanVec = 4;         // consecutive tokens per thread
 
 __device__ __forceinline__ int64_t shfl_up64(int64_t v, int d) { return __shfl_up_sync(0xffffffffu, v, d); }
@@ -63,9 +63,8 @@ __device__ __forceinline__ int32_t sat32(int64_t v) { return v > 0x7fffffff ? 0x
 __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const qgemv_page_plan_t p, int64_t per_cta, int* err) {
   __shared__ PlanItem item[kPlanThreads];
   __shared__ int64_t ws[2][32];
-  __shared__ unsigned long long tot[3];
   const int tid = threadIdx.x;
-  if (tid < 3) tot[tid] = 0;
+  int64_t n_kept = 0, n_got = 0, n_missing = 0;  // of this thread's requests
   const int64_t t0 = blockIdx.x * per_cta, t1 = min(t0 + per_cta, p.capacity);
   const int64_t P = p.page_size, room_all = min(static_cast<int64_t>(p.table_width) * P, int64_t{0x7fffffff});
   const int64_t F = max(*p.free_count, 0);
@@ -90,9 +89,9 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const qgemv_pag
     if (blockIdx.x == 0 && r < p.requests) {
       p.lens[r] = static_cast<int32_t>(c + kept);
       if (p.offsets) p.offsets[r] = sat32(off);
-      if (kept) atomicAdd(&tot[0], static_cast<unsigned long long>(kept));
-      if (got) atomicAdd(&tot[1], static_cast<unsigned long long>(got));
-      if (need1 > got) atomicAdd(&tot[2], static_cast<unsigned long long>(need1 - got));
+      n_kept += kept;
+      n_got += got;
+      n_missing += need1 - got;
     }
     __syncthreads();
     const int64_t a = max(t0, tok), b = min(t1, tok + dt);  // this step's tokens in this CTA's range
@@ -105,6 +104,8 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const qgemv_pag
         if (item[i + half].off <= lo) i += half;
         span -= half;
       }
+      // neighbouring tokens, and most of those of a thread, are of one page: the table is read when it changes
+      int32_t page = -1, page_at = -1, page_of = -1;
       int64_t slot[kPlanVec];
       int32_t pos[kPlanVec], own[kPlanVec];
       const int skip = static_cast<int>(lo - v * kPlanVec);
@@ -121,13 +122,11 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const qgemv_pag
         if (k >= q.kept) continue;
         pos[j] = static_cast<int32_t>(q.c + k);
         const int32_t at = pos[j] / p.page_size, in = pos[j] - at * p.page_size;
-        int32_t* cell = p.table + (r0 + i) * p.table_stride + at;
-        int32_t page;
-        if (at >= q.have) {
-          page = p.free_pages[F - 1 - (q.base + (at - q.have))];
-          if (in == 0) *cell = page;
-        } else {
-          page = *cell;
+        if (at != page_at || i != page_of) {
+          int32_t* cell = p.table + (r0 + i) * p.table_stride + at;
+          page_at = at, page_of = i;
+          page = at >= q.have ? p.free_pages[F - 1 - (q.base + (at - q.have))] : *cell;
+          if (at >= q.have && in == 0) *cell = page;
         }
         if (page >= 0)
           slot[j] = static_cast<int64_t>(page) * p.page_size + in;
@@ -159,24 +158,43 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const qgemv_pag
     if (p.positions) p.positions[t] = -1;
     if (p.owners) p.owners[t] = -1;
   }
-  if (blockIdx.x == 0 && tid == 0) {
-    if (p.offsets) p.offsets[p.requests] = sat32(tok);
-    p.counts[0] = sat32(tok);
-    for (int i = 0; i < 3; ++i) p.counts[1 + i] = sat32(static_cast<int64_t>(tot[i]));
+  if (blockIdx.x == 0) {  // the totals
+    int64_t e0, e1, kept, got, missing, unused;
+    block_scan2(n_kept, n_got, e0, e1, kept, got, ws);
+    __syncthreads();
+    block_scan2(n_missing, 0, e0, e1, missing, unused, ws);
+    if (tid == 0) {
+      if (p.offsets) p.offsets[p.requests] = sat32(tok);
+      p.counts[0] = sat32(tok);
+      p.counts[1] = sat32(kept);
+      p.counts[2] = sat32(got);
+      p.counts[3] = sat32(missing);
+    }
   }
 }
 
 // ------------------------------------------------------------------------------ cache store
-// Eight consecutive elements of a head per thread, all in fp32.
+// Eight consecutive elements of a head, as they are in memory and in fp32.
 template <int T>
-__device__ __forceinline__ void load8(const void* base, int64_t i, float (&v)[8]) {
+struct Raw8 {
+  uint4 v[T == QGEMV_OUT_F32 ? 2 : 1];
+};
+template <int T>
+__device__ __forceinline__ Raw8<T> load_raw(const uint8_t* at) {
+  Raw8<T> r;
+  const uint4* p = reinterpret_cast<const uint4*>(at);
+  r.v[0] = p[0];
+  if constexpr (T == QGEMV_OUT_F32) r.v[1] = p[1];
+  return r;
+}
+template <int T>
+__device__ __forceinline__ void to_float(const Raw8<T>& r, float (&v)[8]) {
   if constexpr (T == QGEMV_OUT_F32) {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + i);
-    const float4 a = p[0], b = p[1];
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    const uint32_t w[8] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w, r.v[1].x, r.v[1].y, r.v[1].z, r.v[1].w};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(w[j]);
   } else {
-    const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + i);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       if constexpr (T == QGEMV_OUT_F16) {
@@ -205,98 +223,134 @@ __device__ __forceinline__ uint4 pack8(int type, const float (&v)[8]) {
   return make_uint4(pack2(type, v[0], v[1]), pack2(type, v[2], v[3]), pack2(type, v[4], v[5]), pack2(type, v[6], v[7]));
 }
 
-// Thread i of the launch takes eight elements of one head of one token; the D / 8 threads of a
-// head are neighbours in a warp.  The heads of a token are its q heads, then k, then v.
+// A CTA (or gridDim.y, where tokens are few) per token: the D / 8 threads of a head are neighbours in a warp and take the token's heads (q, then
+// k, then v) in turn, so that slot, position and angles are read once.  Bound by the bytes of q, k and v: the
+// reads of kU heads are in flight together, and the first of them before slot and position are known.
+constexpr int kStoreThreads = 256;
+
 template <int T, int D>
-__global__ void __launch_bounds__(256) kv_store_kernel(const qgemv_kv_store_t p, int* err) {
+__global__ void __launch_bounds__(kStoreThreads, T == QGEMV_OUT_F32 ? 3 : 4) kv_store_kernel(const __grid_constant__ qgemv_kv_store_t p, int* err) {
   constexpr int L = D / 8;  // threads per head
+  constexpr int kU = T == QGEMV_OUT_F32 ? 2 : 3;
   const int hq = p.q_out ? p.q_heads : 0, hk = p.cache.kv_heads;
-  const int heads = hq + 2 * hk;
-  const int64_t unit = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / L;
-  const int64_t t = unit / heads;
-  if (t >= p.tokens) return;  // whole heads leave together
-  const int head = static_cast<int>(unit - t * heads), d = (threadIdx.x % L) * 8;
-  const bool is_q = head < hq, is_k = !is_q && head < hq + hk;
-  const int h = is_q ? head : is_k ? head - hq : head - hq - hk;
-  int64_t slot = -1, page = 0;
+  const int heads = hq + 2 * hk, step = static_cast<int>(blockDim.x * gridDim.y) / L;
+  const int64_t t = blockIdx.x;
+  const int d = (threadIdx.x % L) * 8;
+  const int half = p.rot_dim / 2;
+  const bool first = d < half;
+  const bool turns = p.rope && d < p.rot_dim;
+  // element of the head's other half that this thread's first one is paired with
+  const int mate = first ? d + half : d - half;
+  constexpr int kEl = T == QGEMV_OUT_F32 ? 4 : 2;
+  // this thread's elements of the token's first q, k and v head; the heads are numbered through
+  const uint8_t* q_at = static_cast<const uint8_t*>(p.q) + (t * p.q_stride + d) * kEl;
+  const uint8_t* k_at = static_cast<const uint8_t*>(p.k) + (t * p.k_stride + d) * kEl - hq * (D * kEl);
+  const uint8_t* v_at = static_cast<const uint8_t*>(p.v) + (t * p.v_stride + d) * kEl - (hq + hk) * (D * kEl);
+  const bool pairs = turns && !p.interleaved;
+  const int to_mate = (mate - d) * kEl;
+  Raw8<T> v[kU], o[kU];
+  auto read = [&](int h0) {
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int head = h0 + u * step;
+      if (head >= heads) break;
+      const uint8_t* at = (head < hq ? q_at : head < hq + hk ? k_at : v_at) + head * (D * kEl);
+      v[u] = load_raw<T>(at);
+      if (pairs && head < hq + hk) o[u] = load_raw<T>(at + to_mate);
+    }
+  };
+  const int h_first = static_cast<int>(blockIdx.y * blockDim.x + threadIdx.x) / L;
+  read(h_first);
+  const int64_t slot = p.slots[t];
+  int32_t pos = p.positions[t];
+  int64_t page = -1, cell = 0;  // cell: elements from a head's page row to this thread's
   int in = 0;
-  if (!is_q) {
-    slot = p.slots[t];
-    page = slot / p.cache.page_size;
+  if (slot >= 0) {
+    page = slot >> 32 ? slot / p.cache.page_size : static_cast<uint32_t>(slot) / static_cast<uint32_t>(p.cache.page_size);
     in = static_cast<int>(slot - page * p.cache.page_size);
-    if (slot < 0 || page >= p.cache.pages) {
-      if (slot != -1 && d == 0) atomicOr(err, kDevErrIndex);
-      return;
-    }
+    cell = page * p.cache.page_stride + static_cast<int64_t>(in) * D + d;
   }
-  int32_t pos = is_q || is_k ? p.positions[t] : 0;
-  if (pos != -1 && p.rope && (pos < 0 || pos >= p.rope_positions)) {
-    if (d == 0) atomicOr(err, kDevErrIndex);
-    pos = -1;
-  }
-  const void* src = is_q ? p.q : is_k ? p.k : p.v;
-  const int64_t row = t * (is_q ? p.q_stride : is_k ? p.k_stride : p.v_stride) + static_cast<int64_t>(h) * D;
-  float v[8];
-  load8<T>(src, row + d, v);
-  if ((is_q || is_k) && p.rope && d < p.rot_dim && pos >= 0) {
+  const bool stored = slot >= 0 && page < p.cache.pages;
+  bool lost = pos != -1 && p.rope && (pos < 0 || pos >= p.rope_positions);
+  if (threadIdx.x == 0 && blockIdx.y == 0 && (lost || (!stored && slot != -1))) atomicOr(err, kDevErrIndex);
+  if (lost) pos = -1;
+  float c[8], s[8];
+  if (turns && pos >= 0) {
     const float* tab = p.rope + static_cast<int64_t>(pos) * p.rot_dim;
-    const int half = p.rot_dim / 2;
     if (p.interleaved) {
-      const float4 c = *reinterpret_cast<const float4*>(tab + d / 2), s = *reinterpret_cast<const float4*>(tab + half + d / 2);
-      const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float a = v[2 * j], b = v[2 * j + 1];
-        v[2 * j] = a * cc[j] - b * ss[j];
-        v[2 * j + 1] = b * cc[j] + a * ss[j];
-      }
+      const float4 a = *reinterpret_cast<const float4*>(tab + d / 2), b = *reinterpret_cast<const float4*>(tab + half + d / 2);
+      c[0] = a.x, c[1] = a.y, c[2] = a.z, c[3] = a.w, s[0] = b.x, s[1] = b.y, s[2] = b.z, s[3] = b.w;
     } else {
-      const bool first = d < half;
-      const int i = first ? d : d - half;
-      float o[8], c[8], s[8];
-      load8<T>(src, row + (first ? d + half : d - half), o);
-      load8<QGEMV_OUT_F32>(tab, i, c);
-      load8<QGEMV_OUT_F32>(tab, half + i, s);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = first ? v[j] * c[j] - o[j] * s[j] : v[j] * c[j] + o[j] * s[j];
+      to_float<QGEMV_OUT_F32>(load_raw<QGEMV_OUT_F32>(reinterpret_cast<const uint8_t*>(tab + (first ? d : mate))), c);
+      to_float<QGEMV_OUT_F32>(load_raw<QGEMV_OUT_F32>(reinterpret_cast<const uint8_t*>(tab + half + (first ? d : mate))), s);
     }
   }
-  if (is_q) {
-    if (pos < 0) {
+  const int el = p.cache.type == QGEMV_KV_E4M3 ? 1 : 2;
+  uint8_t* q_to = static_cast<uint8_t*>(p.q_out) + (t * p.q_out_stride + d) * 2;
+  for (int h0 = h_first; h0 < heads; h0 += kU * step) {
+    if (h0 != h_first) read(h0);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = 0.f;
+    for (int u = 0; u < kU; ++u) {
+      const int head = h0 + u * step;
+      if (head >= heads) break;
+      float x[8];
+      to_float<T>(v[u], x);
+      if (turns && pos >= 0 && head < hq + hk) {
+        if (p.interleaved) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float a = x[2 * j], b = x[2 * j + 1];
+            x[2 * j] = a * c[j] - b * s[j];
+            x[2 * j + 1] = b * c[j] + a * s[j];
+          }
+        } else {
+          float y[8];
+          to_float<T>(o[u], y);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[j] = first ? x[j] * c[j] - y[j] * s[j] : x[j] * c[j] + y[j] * s[j];
+        }
+      }
+      if (head < hq) {
+        if (pos < 0) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[j] = 0.f;
+        }
+        *reinterpret_cast<uint4*>(q_to + head * (2 * D)) = pack8(p.q_type, x);
+        continue;
+      }
+      if (!stored) continue;
+      const bool is_k = head < hq + hk;
+      const int h = head - (is_k ? hq : hq + hk), lines = p.cache.page_size;
+      uint8_t* to = static_cast<uint8_t*>(is_k ? p.cache.k : p.cache.v) + (cell + static_cast<int64_t>(h * lines) * D) * el;
+      if (el == 2) {
+        *reinterpret_cast<uint4*>(to) = pack8(p.cache.type, x);
+        continue;
+      }
+      float top = 0.f;
+      bool nan = false;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[j])), nan |= x[j] != x[j];
+      if (nan) top = __int_as_float(0x7f800000);
+      const uint32_t mates = L == 32 ? 0xffffffffu : ((1u << (L & 31)) - 1) << ((threadIdx.x & 31) / L * L);
+#pragma unroll
+      for (int k = L / 2; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(mates, top, k));
+      float scale = __fdiv_rn(top, 448.f);
+      if (!(scale > 0.f && scale < __int_as_float(0x7f800000))) scale = 1.f;
+      scale = fmaxf(scale, 1.17549435e-38f);  // its reciprocal stays finite
+      const float by = __frcp_rn(scale);
+      uint32_t w[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float* y = x + 4 * j;
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[0] * by, y[1] * by), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[2] * by, y[3] * by), __NV_SATFINITE, __NV_E4M3);
+        w[j] = lo | hi << 16;
+      }
+      *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
+      if (d == 0)
+        (is_k ? p.cache.k_scale : p.cache.v_scale)[page * p.cache.scale_stride + h * lines + in] = scale;
     }
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.q_out) + t * p.q_out_stride + static_cast<int64_t>(h) * D + d) =
-        pack8(p.q_type, v);
-    return;
   }
-  const int64_t line = static_cast<int64_t>(h) * p.cache.page_size + in;
-  const int64_t at = page * p.cache.page_stride + line * D + d;
-  void* dst = is_k ? p.cache.k : p.cache.v;
-  if (p.cache.type != QGEMV_KV_E4M3) {
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(dst) + at) = pack8(p.cache.type, v);
-    return;
-  }
-  float top = 0.f;
-  bool nan = false;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(v[j])), nan |= v[j] != v[j];
-  if (nan) top = __int_as_float(0x7f800000);
-  const uint32_t mates = L == 32 ? 0xffffffffu : ((1u << (L & 31)) - 1) << ((threadIdx.x & 31) / L * L);
-#pragma unroll
-  for (int o = L / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(mates, top, o));
-  float scale = __fdiv_rn(top, 448.f);
-  if (!(scale > 0.f && scale < __int_as_float(0x7f800000))) scale = 1.f;
-  uint32_t w[2];
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const float* x = v + 4 * j;
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(x[0], scale), __fdiv_rn(x[1], scale)), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(x[2], scale), __fdiv_rn(x[3], scale)), __NV_SATFINITE, __NV_E4M3);
-    w[j] = lo | hi << 16;
-  }
-  *reinterpret_cast<uint2*>(static_cast<uint8_t*>(dst) + at) = make_uint2(w[0], w[1]);
-  if (d == 0) (is_k ? p.cache.k_scale : p.cache.v_scale)[page * p.cache.scale_stride + line] = scale;
 }
 
 }  // namespace qg

@@ -17,7 +17,7 @@ inline qgemv_status_t check_cache(const qgemv_kv_cache_t& c) {
       (c.page_size != 8 && (c.page_size < 16 || c.page_size % 16)))
     return QGEMV_ERR_BAD_SHAPE;
   const int64_t lines = static_cast<int64_t>(c.kv_heads) * c.page_size;
-  if (lines > (int64_t{1} << 40) / c.head_dim || c.page_stride < lines * c.head_dim || c.page_stride > (int64_t{1} << 38))
+  if (lines > 0x7fffffff || c.page_stride < lines * c.head_dim || c.page_stride > (int64_t{1} << 38))
     return QGEMV_ERR_BAD_SHAPE;
   if (c.type == QGEMV_KV_E4M3 && (c.scale_stride < lines || c.scale_stride > (int64_t{1} << 32))) return QGEMV_ERR_BAD_SHAPE;
   if (!aligned16(c.k) || !aligned16(c.v) || c.page_stride * kv_elem_bytes(c) % 16) return QGEMV_ERR_MISALIGNED;
