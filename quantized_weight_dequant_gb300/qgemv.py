@@ -141,10 +141,26 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
+def _first_current_stream() -> int:
+    """The current stream's handle.  torch.cuda.current_stream() builds an object for it, 3 us a call, as long as a
+    small launch takes in all; after the first call (which initialises CUDA) the plain handle is asked for."""
+    global _current_stream
+    import torch
+    handle = torch.cuda.current_stream().cuda_stream
+    raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+    if raw is not None and device is not None and raw(device()) == handle:
+        _current_stream = lambda: raw(device())  # noqa: E731
+    else:
+        _current_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+    return handle
+
+
+_current_stream = _first_current_stream
+
+
 def _stream(stream) -> int | None:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
