@@ -12,53 +12,68 @@ using namespace qg;
 
 namespace {
 
-template <int TG, bool BF>
-const void* kernel_for(int out) {
-  switch (out) {
-    case QGEMV_OUT_F32: return reinterpret_cast<const void*>(lora_kernel<BF, QGEMV_OUT_F32, TG>);
-    case QGEMV_OUT_F16: return reinterpret_cast<const void*>(lora_kernel<BF, QGEMV_OUT_F16, TG>);
-    default: return reinterpret_cast<const void*>(lora_kernel<BF, QGEMV_OUT_BF16, TG>);
-  }
-}
-
-template <int TG>
-qgemv_status_t launch(const Handle& h, const qgemv_lora_t& p, cudaStream_t stream) {
-  // Clusters per kRows rows: one for each adapter that they can have, but no more in all than run at once
-  // (then a cluster takes its share of the adapters one after another).
-  constexpr int kRows = LoraShape<TG>::kRows;
-  const int64_t chunks = (p.rows + kRows - 1) / kRows;
-  const int64_t most = std::min<int64_t>(kRows, p.rows), resident = int64_t{h.sms} * LoraShape<TG>::kCtasPerSm / kLoraCluster;
-  int slots = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(most, (resident + chunks - 1) / chunks)));
-  // Clusters that share an adapter's N, where there are fewer than two rounds of them: at least three tiles for
-  // a warp.
-  const int64_t tiles = (p.N + 31) / 32;
-  int shares = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(2 * resident / (chunks * slots), tiles / (3 * kLoraWarps * kLoraCluster))));
-  const int64_t grid = chunks * slots * shares * kLoraCluster;
-  if (grid > 0x7fffffff) return QGEMV_ERR_BAD_SHAPE;
-  const void* fn = p.type == QGEMV_OUT_BF16 ? kernel_for<TG, true>(p.out) : kernel_for<TG, false>(p.out);
-  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(LoraSmem<TG>)) != cudaSuccess) {
-    cudaGetLastError();
-    return QGEMV_ERR_CUDA;
-  }
+bool start(const void* fn, int64_t grid, size_t smem, int cluster, bool dependent, void** args, cudaStream_t stream) {
+  if (smem > 48 * 1024 && cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess) return false;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
   cfg.blockDim = dim3(kLoraThreads, 1, 1);
-  cfg.dynamicSmemBytes = sizeof(LoraSmem<TG>);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = kLoraCluster;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
+  if (cluster > 1) {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+  } else {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = dependent ? 1 : 0;
+  }
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  return cudaLaunchKernelExC(&cfg, fn, args) == cudaSuccess;
+}
+
+// Rows whose sums fit the workspace are one pair of launches.
+template <bool BF, int OUT>
+bool launch(const Handle& h, qgemv_lora_t p, const LoraWork& work, cudaStream_t stream) {
+  const bool few = p.rows <= kLoraFewRows;
+  const int64_t per = few ? LoraShape<1>::kRows : LoraShape<2>::kRows, chunks = (p.rows + per - 1) / per;
+  // Sums: clusters per chunk of rows, one for each adapter that they can have, but no more in all than run at
+  // once (then a cluster takes its share of the adapters one after another).
+  const int64_t resident = int64_t{h.sms} * 4 / kLoraCluster;
+  int slots = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min(per, p.rows), (resident + chunks - 1) / chunks)));
+  LoraWork w = work;
   int* err = h.err;
-  void* args[] = {const_cast<qgemv_lora_t*>(&p), &slots, &shares, &err};
-  if (cudaLaunchKernelExC(&cfg, fn, args) != cudaSuccess) {
-    cudaGetLastError();
-    return QGEMV_ERR_CUDA;
+  void* sums[] = {&p, &w, &slots, &err};
+  const void* fn = few ? reinterpret_cast<const void*>(lora_sums_kernel<BF, 1>) : reinterpret_cast<const void*>(lora_sums_kernel<BF, 2>);
+  if (!start(fn, chunks * slots * kLoraCluster, 0, kLoraCluster, false, sums, stream)) return false;
+  const int64_t tiles = (p.N + 31) / 32;
+  if (few) {
+    // CTAs that share an adapter's N: about three rounds of them, and at least two tiles for a warp
+    slots = static_cast<int>(std::min<int64_t>(32, p.rows));
+    int shares = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(12 * h.sms / (chunks * slots), tiles / (2 * kLoraWarps))));
+    void* args[] = {&p, &w, &slots, &shares};
+    return start(reinterpret_cast<const void*>(lora_few_kernel<BF, OUT>), chunks * slots * shares, sizeof(LoraFewSmem), 1, true, args, stream);
   }
-  return QGEMV_OK;
+  // as many parts of the rows as fill the GPU once, at least two tiles of rows each
+  const int64_t cols = (p.N + 32 * kLoraWarps - 1) / (32 * kLoraWarps);
+  const int nb = w.blocks == 1 ? 1 : w.blocks == 2 ? 2 : 4;
+  const int64_t at_once = int64_t{h.sms} * (nb == 1 ? 4 : nb == 2 ? 3 : 2);
+  int splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(at_once / cols, (p.rows + 31) / 32)));
+  void* args[] = {&p, &w, &splits};
+  fn = nb == 1 ? reinterpret_cast<const void*>(lora_many_kernel<BF, OUT, 1>)
+       : nb == 2 ? reinterpret_cast<const void*>(lora_many_kernel<BF, OUT, 2>) : reinterpret_cast<const void*>(lora_many_kernel<BF, OUT, 4>);
+  return start(fn, cols * splits, 0, 1, true, args, stream);
+}
+
+template <bool BF>
+bool launch_out(const Handle& h, const qgemv_lora_t& p, const LoraWork& work, cudaStream_t stream) {
+  switch (p.out) {
+    case QGEMV_OUT_F32: return launch<BF, QGEMV_OUT_F32>(h, p, work, stream);
+    case QGEMV_OUT_F16: return launch<BF, QGEMV_OUT_F16>(h, p, work, stream);
+    default: return launch<BF, QGEMV_OUT_BF16>(h, p, work, stream);
+  }
 }
 
 }  // namespace
@@ -76,6 +91,26 @@ extern "C" qgemv_status_t qgemv_run_lora(qgemv_handle_t hh, const qgemv_lora_t* 
   if (p.rows > 0 && (!p.x || !p.ids || !p.y)) return QGEMV_ERR_INVALID_ARG;
   if (!aligned16(p.x) || !aligned16(p.A) || !aligned16(p.B) || !aligned16(p.base) || !aligned16(p.y) || p.x_stride % 8)
     return QGEMV_ERR_MISALIGNED;
-  if (p.rows == 0) return QGEMV_OK;
-  return p.rows <= kLoraFewRows ? launch<1>(*h, p, stream) : launch<2>(*h, p, stream);
+  const bool bf = p.type == QGEMV_OUT_BF16;
+  LoraWork work{};
+  work.blocks = (p.rank + 31) / 32;
+  const int64_t row_bytes = int64_t{64} * work.blocks * lora_parts(bf);
+  // rows at a time: whole tiles of 16, their sums and factors in the workspace
+  const int64_t most = static_cast<int64_t>(kWsFloats) * 4 / (row_bytes + 4) / 32 * 32;
+  work.parts = reinterpret_cast<uint4*>(h->ws);
+  for (int64_t m = 0; m < p.rows; m += most) {
+    qgemv_lora_t q = p;
+    q.rows = std::min(most, p.rows - m);
+    q.x = static_cast<const uint8_t*>(p.x) + m * p.x_stride * 2;
+    q.ids = p.ids + m;
+    const int64_t at = m * p.y_stride * (p.out == QGEMV_OUT_F32 ? 4 : 2);
+    q.base = p.base ? static_cast<const uint8_t*>(p.base) + at : nullptr;
+    q.y = static_cast<uint8_t*>(p.y) + at;
+    work.factor = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(h->ws) + (q.rows + 15) / 16 * 16 * row_bytes);
+    if (!(bf ? launch_out<true>(*h, q, work, stream) : launch_out<false>(*h, q, work, stream))) {
+      cudaGetLastError();
+      return QGEMV_ERR_CUDA;
+    }
+  }
+  return QGEMV_OK;
 }

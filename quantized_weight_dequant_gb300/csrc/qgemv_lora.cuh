@@ -1,26 +1,24 @@
 // Low-rank adapters of many requests beside a shared projection:
 //   t = A_a x_m  (rank r_a),   y_m = base_m + s_a B_a t
 //
-// With a few rows per adapter the kernel is bound by the bytes of A and B, with many rows by those of
-// base and y; a row's own work is 2 r (K + N) operations.  One launch does both products:
-//  * A cluster of eight CTAs takes the rows of one adapter among 16 or 32 neighbouring rows of the batch.
-//    Each CTA forms the inner sums over its eighth of K; the eight partial sums meet through
-//    distributed shared memory (each CTA adds all of them in rank order), and each CTA writes its
-//    eighth of N.  So the inner sums never leave the chip, and a single row still uses eight SMs.
-//  * Every lane fetches what it will multiply itself, B's rows and the base, through a ring of cp.async
-//    in shared memory, and its first stages before the first product begins: no barrier, no registers.
-//  * Both products run on mma.sync m16n8k16, the first with A's rows as its 16 and the tokens as its 8, the
+// With a few rows per adapter the work is bound by the bytes of A and B, with many rows by those of base
+// and y; a row's own work is 2 r (K + N) operations.  Two launches, the second a dependent one: it starts
+// while the first runs, fetches its first rows of B and the base, and waits for t only then.
+//  * Sums (lora_sums_kernel).  A cluster of eight CTAs takes the rows of one adapter among 16 or 32
+//    neighbouring rows of the batch, each CTA an eighth of K; the partial sums meet through distributed
+//    shared memory, where each CTA adds those of its own tokens in rank order.  The sums (fp32) are left in
+//    the workspace as what the second product multiplies: two fp16 parts scaled by a power of two per row
+//    (the row's largest in [2^14, 2^15)), or three bf16 parts: at least 21 bits.
+//  * Outputs of few rows (lora_few_kernel): the rows of one adapter stay, its B streams by, through a
+//    ring of cp.async in which every lane fetches what it will multiply itself (no barrier, no
+//    registers).  Several CTAs share N.
+//  * Outputs of many rows (lora_many_kernel): 32 rows of B stay in a warp's registers, the tokens stream
+//    by, 16 at a time.
+//  * All products run on mma.sync m16n8k16, the first with A's rows as its 16 and the tokens as its 8, the
 //    second with the tokens as its 16 and B's rows as its 8.  A lane's operands are 16 consecutive bytes of
 //    its row: the order of k within a 32-wide block is the same permutation on both sides, so no shared
 //    memory or ldmatrix is needed for A, B or x.  B's rows are dealt to the two 8-wide halves of a 16-row
 //    tile so that a lane ends up with four consecutive outputs of a token.
-//  * The inner sums (fp32) enter the second product as two fp16 parts scaled by a power of two per row
-//    (the row's largest in [2^14, 2^15)), or three bf16 parts: at least 21 bits.  Up to eight tokens have
-//    their first two parts in the upper and the lower eight rows of one instruction.
-//  * Two shapes, both of CTAs of 4 warps: up to 8 tokens at a time of an adapter's rows among 32 (a few
-//    rows per adapter), and up to 16 among 16 (many rows: more clusters than run at once, so that they
-//    even out over the SMs).  Where the rows are few, several clusters share an adapter's N; each forms
-//    the inner sums for itself.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -34,12 +32,20 @@
 namespace qg {
 
 constexpr int kLoraMaxRank = 128;
-constexpr int kLoraFewRows = 256;  // up to here eight tokens at a time
+constexpr int kLoraFewRows = 256;  // up to here eight tokens of an adapter at a time, and B streams by
 constexpr int kLoraCluster = 8;
 constexpr int kLoraLd = kLoraMaxRank + 4;  // floats per token of the sums in shared memory
-
 constexpr int kLoraWarps = 4;
 constexpr int kLoraThreads = 32 * kLoraWarps;
+
+// The rows of a launch in the workspace: per row, the parts of its sums (blocks of 32 ranks, kParts, four
+// lanes of 16 bytes), then per row its factor (the adapter's scale over the parts' power of two).
+struct LoraWork {
+  uint4* parts;
+  float* factor;
+  int blocks;  // 32-wide blocks of the largest rank
+};
+__host__ __device__ constexpr int lora_parts(bool bf) { return bf ? 3 : 2; }
 
 // TG: groups of eight tokens taken at a time.
 template <int TG>
@@ -47,26 +53,40 @@ struct LoraShape {
   static constexpr int kTokens = 8 * TG;
   static constexpr int kRows = TG == 1 ? 32 : 16;   // neighbouring rows of the batch per cluster
   static constexpr int kRT = 4;                     // 16-row tiles of A taken at a time
-  static constexpr int kCtasPerSm = TG == 1 ? 4 : 3;
-  static constexpr int kDepth = TG == 1 ? 3 : 2;    // stages of a lane's ring
-  static constexpr int kPieces = 4 + 2 * TG;        // 16-byte pieces of a stage: four of B, two of the base per token
 };
 
 template <int TG>
 struct LoraSmem {
-  using Sh = LoraShape<TG>;
-  uint4 ring[kLoraWarps][Sh::kDepth][Sh::kPieces][32];
-  float own[Sh::kTokens][kLoraLd];                  // this CTA's sums over its part of K
-  union {
-    float part[kLoraWarps][Sh::kTokens][16 * Sh::kRT + 4];  // first product: per warp
-    struct {
-      float sum[Sh::kTokens][kLoraLd];                      // over all of K
-      uint4 frag[TG][kLoraMaxRank / 32][3][32];             // 16-bit parts of the sums, as a lane's operand
-    };
-  };
-  float factor[Sh::kTokens];                        // of a token: the adapter's scale over the parts' power of two
-  int row[Sh::kRows];                               // rows of the adapter in hand
+  float own[8 * TG][kLoraLd];                                             // this CTA's sums over its part of K
+  float part[kLoraWarps][8 * TG][16 * LoraShape<TG>::kRT + 4];            // those of a warp
+  int row[LoraShape<TG>::kRows];                                          // rows of the adapter in hand
 };
+
+// The distinct adapters among `n_rows` (up to 32) rows from m0 on, found by one warp: rows_of[i] is the mask of
+// the rows of the i-th, in order of first appearance (those without one among them).  Returns their number.
+__device__ __forceinline__ int lora_distinct(const qgemv_lora_t& p, int64_t m0, int n_rows, uint32_t* rows_of, int* err) {
+  const int lane = threadIdx.x & 31;
+  int id = -2;  // past the rows
+  if (lane < n_rows && m0 + lane < p.rows) {
+    id = p.ids[m0 + lane];
+    if (id < -1 || id >= p.adapters) {
+      if (err) atomicOr(err, kDevErrIndex);
+      id = -1;
+    }
+  }
+  const uint32_t same = __match_any_sync(0xffffffffu, id);
+  const bool first = id != -2 && __ffs(same) - 1 == lane;
+  const uint32_t firsts = __ballot_sync(0xffffffffu, first);
+  if (first) rows_of[__popc(firsts & ((1u << lane) - 1))] = same;
+  return __popc(firsts);
+}
+__device__ __forceinline__ int lora_adapter(const qgemv_lora_t& p, int64_t m) {
+  const int id = p.ids[m];
+  return id >= 0 && id < p.adapters ? id : -1;
+}
+__device__ __forceinline__ int lora_rank(const qgemv_lora_t& p, int a) {
+  return a < 0 ? 0 : p.ranks ? min(max(p.ranks[a], 0), p.rank) : p.rank;
+}
 
 __device__ __forceinline__ float4 cluster_ld4(uint32_t a, uint32_t rank) {
   uint32_t r;
@@ -77,6 +97,7 @@ __device__ __forceinline__ float4 cluster_ld4(uint32_t a, uint32_t rank) {
 }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 // `bytes` (8 or 16) of cp.async, of which `in` are read and the rest are zeros.
 template <int BYTES>
 __device__ __forceinline__ void cp_async_fill(uint32_t dst, const void* src, int in) {
@@ -130,6 +151,24 @@ __device__ __forceinline__ void lora_store4(void* p, int64_t i, int n, bool vec,
       else
         static_cast<uint16_t*>(p)[i + e] = static_cast<uint16_t>(pair16<kBF>(w[e], 0.f));
     }
+}
+
+template <int OUT>
+__device__ __forceinline__ float4 lora_four(const uint4& d) {  // four outputs in the first 16 or 8 bytes
+  if constexpr (OUT == QGEMV_OUT_F32) return make_float4(__uint_as_float(d.x), __uint_as_float(d.y), __uint_as_float(d.z), __uint_as_float(d.w));
+  const float2 a = unpair16<OUT == QGEMV_OUT_BF16>(d.x), b = unpair16<OUT == QGEMV_OUT_BF16>(d.y);
+  return make_float4(a.x, a.y, b.x, b.y);
+}
+
+// Zeros in place of what lies past rank r in four rows' ranks j .. j + 7 (those are read where j < r).
+__device__ __forceinline__ void lora_mask(uint4 (&w)[4], int j, int r) {
+  if (j >= r || j + 8 <= r) return;
+#pragma unroll
+  for (int h = 0; h < 4; ++h) {
+    uint32_t* q = reinterpret_cast<uint32_t*>(&w[h]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) q[e] &= j + 2 * e >= r ? 0u : j + 2 * e + 1 >= r ? 0xffffu : 0xffffffffu;
+  }
 }
 
 // First product over the 32-wide blocks b0 .. b1 of K for ranks j0 .. j0 + 16 RT - 1 and 8 TG tokens, the
@@ -191,67 +230,114 @@ __device__ __forceinline__ void lora_shrink(const qgemv_lora_t& p, LoraSmem<TG>&
   __syncthreads();
 }
 
-// The sums of 8 TG tokens as operands of the second product: lane (g, c) of block b takes ranks
-// 32 b + 8 c .. + 7 of token 8 t + g.
 template <bool BF, int TG>
-__device__ __forceinline__ void lora_parts(LoraSmem<TG>& sm, int t, int blocks, float scale) {
-  const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  const float* s = &sm.sum[8 * t + g][8 * c];
-  float by = 1.f, back = 1.f;
-  if constexpr (!BF) {
-    float top = 0.f;
-    for (int b = 0; b < blocks; ++b)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(s[32 * b + e]));
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    const int ex = __float_as_int(top) >> 23 & 0xff;
-    if (ex >= 15 && ex < 255) {  // 2^(141 - ex) takes 1.x 2^(ex - 127) to 1.x 2^14
-      by = __int_as_float((127 + 141 - ex) << 23);
-      back = __int_as_float((127 - 141 + ex) << 23);
-    }
+__global__ void __launch_bounds__(kLoraThreads, 4) lora_sums_kernel(const __grid_constant__ qgemv_lora_t p, const LoraWork work, int slots, int* err) {
+  using Sh = LoraShape<TG>;
+  constexpr int kParts = lora_parts(BF);
+  __shared__ __align__(16) LoraSmem<TG> sm;
+  __shared__ uint32_t rows_of[32];
+  __shared__ int count;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rank = static_cast<int>(blockIdx.x) % kLoraCluster, cluster = static_cast<int>(blockIdx.x) / kLoraCluster;
+  const int slot = cluster % slots;
+  const int64_t m0 = static_cast<int64_t>(cluster / slots) * Sh::kRows;
+  pdl_launch_dependents();  // the second launch may start; it waits for this one's end before it reads the sums
+  if (warp == 0) {
+    const int n = lora_distinct(p, m0, Sh::kRows, rows_of, slot == 0 && rank == 0 ? err : nullptr);
+    if (lane == 0) count = n;
   }
-  for (int b = 0; b < blocks; ++b) {
-    uint32_t hi[4], mid[4], lo[4];
+  __syncthreads();
+  const int64_t blocks = (p.K + 31) / 32;
+  const int64_t b0 = blocks * rank / kLoraCluster, b1 = blocks * (rank + 1) / kLoraCluster;
+  for (int i = slot; i < count; i += slots) {
+    const uint32_t mask = rows_of[i];
+    const int n_tok = __popc(mask), a = lora_adapter(p, m0 + __ffs(mask) - 1), r = lora_rank(p, a);
+    if (r == 0) continue;
+    const float scale = p.scales ? p.scales[a] : 1.f;
+    if (warp == 0 && (mask >> lane & 1)) sm.row[__popc(mask & ((1u << lane) - 1))] = static_cast<int>(m0) + lane;
+    __syncthreads();
+    const uint16_t* A = static_cast<const uint16_t*>(p.A) + static_cast<int64_t>(a) * p.rank * p.K;
+    for (int k0 = 0; k0 < n_tok; k0 += Sh::kTokens) {  // up to kTokens of its rows at a time
+      const int n = min(n_tok - k0, Sh::kTokens);
+      for (int j = 0; j < r; j += 16 * Sh::kRT) lora_shrink<BF, TG>(p, sm, sm.row + k0, A, r, j, n, b0, b1);
+      cluster_arrive();
+      cluster_wait();
+      // a warp per token of this CTA, four ranks a lane
+      for (int tok = rank + kLoraCluster * warp; tok < n; tok += kLoraCluster * kLoraWarps) {
+        const int j = 4 * lane;
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+        if (j < r) {
+          const uint32_t at = smem_u32(&sm.own[tok][j]);
+          float4 q[kLoraCluster];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      float u = s[32 * b + 2 * e] * by, v = s[32 * b + 2 * e + 1] * by;
-      hi[e] = pair16<BF>(u, v);
-      float2 f = unpair16<BF>(hi[e]);
-      u -= f.x, v -= f.y;
-      mid[e] = pair16<BF>(u, v);
-      f = unpair16<BF>(mid[e]);
-      lo[e] = pair16<BF>(u - f.x, v - f.y);
+          for (int c = 0; c < kLoraCluster; ++c) q[c] = cluster_ld4(at, c);
+#pragma unroll
+          for (int c = 0; c < kLoraCluster; ++c) v[0] += q[c].x, v[1] += q[c].y, v[2] += q[c].z, v[3] += q[c].w;
+        }
+        float by = 1.f, back = 1.f;
+        if constexpr (!BF) {
+          float top = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          const int ex = __float_as_int(top) >> 23 & 0xff;
+          if (ex >= 15 && ex < 255) {  // 2^(141 - ex) takes 1.x 2^(ex - 127) to 1.x 2^14
+            by = __int_as_float((127 + 141 - ex) << 23);
+            back = __int_as_float((127 - 141 + ex) << 23);
+          }
+        }
+        const int64_t m = sm.row[k0 + tok];
+        if (lane < 8 * work.blocks) {
+          uint2* to = reinterpret_cast<uint2*>(work.parts + (m * work.blocks + lane / 8) * (4 * kParts) + lane % 8 / 2) + lane % 2;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] *= by;
+#pragma unroll
+          for (int q = 0; q < kParts; ++q) {
+            const uint32_t u0 = pair16<BF>(v[0], v[1]), u1 = pair16<BF>(v[2], v[3]);
+            to[8 * q] = make_uint2(u0, u1);
+            const float2 f0 = unpair16<BF>(u0), f1 = unpair16<BF>(u1);
+            v[0] -= f0.x, v[1] -= f0.y, v[2] -= f1.x, v[3] -= f1.y;
+          }
+        }
+        if (lane == 0) work.factor[m] = scale * back;
+      }
+      cluster_arrive();
+      cluster_wait();  // no CTA reads this one's sums: they are used again, or the CTA ends
     }
-    sm.frag[t][b][0][lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    sm.frag[t][b][1][lane] = make_uint4(mid[0], mid[1], mid[2], mid[3]);
-    if (BF) sm.frag[t][b][2][lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    __syncthreads();
   }
-  if (c == 0) sm.factor[8 * t + g] = scale * back;
 }
 
-// Second product: outputs of the 32-row tiles t0 .. t1 of N, dealt to the warps in turn, for up to 8 TG
-// tokens.  A stage of a lane's ring is one 32-wide block of ranks of a tile: 16 bytes of four rows of B and,
+// ------------------------------------------------------------------------- outputs of few rows
+// A stage of a lane's ring is one 32-wide block of ranks of a 32-row tile of N: 16 bytes of four rows of B and,
 // with a tile's first block, the base of its outputs.  Lane (g, c), half k of a tile (16 rows): rows
-// 4 (g / 2) + g % 2 and two further; outputs 4 c .. 4 c + 3 of tokens g and g + 8.
-template <bool BF, int TG, int OUT>
-struct LoraExpand {
-  using Sh = LoraShape<TG>;
-  static constexpr int D = Sh::kDepth;
+// 4 (g / 2) + g % 2 and two further; outputs 4 c .. 4 c + 3 of token g.  The tokens are the instruction's first
+// eight rows, and their second parts the other eight (the third of bf16 another instruction).
+constexpr int kLoraDepth = 3;   // stages of a lane's ring
+constexpr int kLoraPieces = 6;  // 16-byte pieces of a stage
+
+struct LoraFewSmem {
+  uint4 ring[kLoraWarps][kLoraDepth][kLoraPieces][32];
+  uint4 parts[kLoraMaxRank / 32][3][32];  // of the tokens in hand, as a lane's operand
+  float factor[8];
+  int row[32];
+};
+
+template <bool BF, int OUT>
+struct LoraStream {
   static constexpr int kBytes = OUT == QGEMV_OUT_F32 ? 16 : 8;  // of four outputs
+  static constexpr int kStep = 32 * kLoraWarps;                 // outputs from a warp's tile to its next
   const qgemv_lora_t& p;
-  LoraSmem<TG>& sm;
+  LoraFewSmem& sm;
   const int N, r, blocks, t1;
   int ask_tile, ask_b, ask_s, ask_n;  // ask_n: first row of the lane in the tile to be asked for
   const uint16_t* ask_row;            // its 16 bytes
-  const uint8_t* base[TG];            // this lane's outputs of its tokens, in the tile to be asked for and
-  uint8_t* y[TG];                     // in the tile in hand; null: no such token
+  const uint8_t* base;                // this lane's outputs of its token, in the tile to be asked for and
+  uint8_t* y;                         // in the tile in hand; null: no such token
   int64_t to_second, to_tile;         // elements from a row to the lane's second; from the last block of a tile to the next tile
   uint32_t mine;                      // this lane's first piece of its warp's ring
   bool vec;
-  static constexpr int kStep = 32 * kLoraWarps;  // outputs from a warp's tile to its next
 
-  __device__ __forceinline__ LoraExpand(const qgemv_lora_t& p_, LoraSmem<TG>& sm_, const int* rows, const uint16_t* B, int r_, int n_tok, int t0, int t1_)
+  __device__ __forceinline__ LoraStream(const qgemv_lora_t& p_, LoraFewSmem& sm_, const int* rows, const uint16_t* B, int r_, int n_tok, int t0, int t1_)
       : p(p_), sm(sm_), N(static_cast<int>(p_.N)), r(r_), blocks((r_ + 31) / 32), t1(t1_), ask_b(0), ask_s(0) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
     ask_tile = t0 + warp;
@@ -261,30 +347,22 @@ struct LoraExpand {
     to_tile = static_cast<int64_t>(kStep) * p.rank - 32 * (blocks - 1);
     mine = smem_u32(&sm.ring[warp][0][0][lane]);
     vec = p.y_stride % 4 == 0;
-#pragma unroll
-    for (int h = 0; h < TG; ++h) {
-      const bool there = 8 * h + g < n_tok;
-      const int64_t at = there ? (rows[8 * h + g] * p.y_stride + 4 * c + 32 * ask_tile) * (kBytes / 4) : 0;
-      base[h] = there && p.base ? static_cast<const uint8_t*>(p.base) + at : nullptr;
-      y[h] = there ? static_cast<uint8_t*>(p.y) + at : nullptr;
-    }
+    const int64_t at = g < n_tok ? (rows[g] * p.y_stride + 4 * c + 32 * ask_tile) * (kBytes / 4) : 0;
+    base = g < n_tok && p.base ? static_cast<const uint8_t*>(p.base) + at : nullptr;
+    y = g < n_tok ? static_cast<uint8_t*>(p.y) + at : nullptr;
   }
   __device__ __forceinline__ void ask() {  // the next stage
     if (ask_tile < t1) {
-      const uint32_t to = mine + ask_s * (Sh::kPieces * 512);
+      const uint32_t to = mine + ask_s * (kLoraPieces * 512);
       const int c8 = 8 * (threadIdx.x & 3);
       const bool in = 32 * ask_b + c8 < r;
 #pragma unroll
       for (int h = 0; h < 4; ++h)  // rows 0, 2, 16, 18 from the lane's first
         cp_async_fill<16>(to + h * 512, ask_row + (h & 1) * to_second + (h >> 1) * 8 * to_second, in && ask_n + 2 * (h & 1) + 16 * (h >> 1) < N ? 16 : 0);
-      if (ask_b == 0 && vec) {
+      if (ask_b == 0 && vec && base) {
 #pragma unroll
         for (int k = 0; k < 2; ++k)
-          if (32 * ask_tile + 16 * k + c8 / 2 + 4 <= N) {
-#pragma unroll
-            for (int h = 0; h < TG; ++h)
-              if (base[h]) cp_async_fill<kBytes>(to + (4 + 2 * h + k) * 512, base[h] + 4 * k * kBytes, kBytes);
-          }
+          if (32 * ask_tile + 16 * k + c8 / 2 + 4 <= N) cp_async_fill<kBytes>(to + (4 + k) * 512, base + 4 * k * kBytes, kBytes);
       }
       if (++ask_b < blocks) {
         ask_row += 32;
@@ -293,146 +371,87 @@ struct LoraExpand {
         ask_tile += kLoraWarps;
         ask_n += kStep;
         ask_row += to_tile;
-#pragma unroll
-        for (int h = 0; h < TG; ++h)
-          if (base[h]) base[h] += kStep * (kBytes / 4);
+        if (base) base += kStep * (kBytes / 4);
       }
     }
     cp_async_commit();
-    if (++ask_s == D) ask_s = 0;
+    if (++ask_s == kLoraDepth) ask_s = 0;
   }
   __device__ __forceinline__ void begin() {
 #pragma unroll 1
-    for (int i = 0; i < D; ++i) ask();
+    for (int i = 0; i < kLoraDepth; ++i) ask();
   }
   __device__ __forceinline__ void run(int t0) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
-    float factor[TG];
-#pragma unroll
-    for (int h = 0; h < TG; ++h) factor[h] = sm.factor[8 * h + g];
+    const float f = sm.factor[g];
     int s = 0;
 #pragma unroll 1
     for (int tile = t0 + warp; tile < t1; tile += kLoraWarps) {
       float acc[2][2][4] = {};
-      uint4 old[TG][2];
+      uint4 old[2];
 #pragma unroll 1
       for (int b = 0; b < blocks; ++b) {
-        cp_async_wait<D - 1>();
-        const uint32_t from = mine + s * (Sh::kPieces * 512);
+        cp_async_wait<kLoraDepth - 1>();
+        const uint32_t from = mine + s * (kLoraPieces * 512);
         uint4 w[4];
 #pragma unroll
         for (int h = 0; h < 4; ++h) w[h] = lds_v4(from + h * 512);
-        if (b == 0) {
-#pragma unroll
-          for (int h = 0; h < 2 * TG; ++h) old[h >> 1][h & 1] = lds_v4(from + (4 + h) * 512);
-        }
+        if (b == 0) old[0] = lds_v4(from + 4 * 512), old[1] = lds_v4(from + 5 * 512);
         ask();
-        if (++s == D) s = 0;
-        const int j = 32 * b + 8 * c;
-        if (j < r && j + 8 > r) {  // what lies past the adapter's rank does not count
-#pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            uint32_t* q = reinterpret_cast<uint32_t*>(&w[h]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) q[e] &= j + 2 * e >= r ? 0u : j + 2 * e + 1 >= r ? 0xffffu : 0xffffffffu;
-          }
-        }
+        if (++s == kLoraDepth) s = 0;
+        lora_mask(w, 32 * b + 8 * c, r);
         auto add = [&](const uint4& s0, const uint4& s1) {  // operand rows 0..7 and 8..15
 #pragma unroll
           for (int h = 0; h < 4; ++h) mma16816<BF>(acc[h >> 1][h & 1], s0.x, s1.x, s0.y, s1.y, w[h].x, w[h].y);
 #pragma unroll
           for (int h = 0; h < 4; ++h) mma16816<BF>(acc[h >> 1][h & 1], s0.z, s1.z, s0.w, s1.w, w[h].z, w[h].w);
         };
-        if constexpr (TG == 1) {
-          add(sm.frag[0][b][0][lane], sm.frag[0][b][1][lane]);
-          if constexpr (BF) add(sm.frag[0][b][2][lane], make_uint4(0, 0, 0, 0));
-        } else {
-#pragma unroll
-          for (int q = 0; q < (BF ? 3 : 2); ++q) add(sm.frag[0][b][q][lane], sm.frag[1][b][q][lane]);
-        }
+        add(sm.parts[b][0][lane], sm.parts[b][1][lane]);
+        if constexpr (BF) add(sm.parts[b][2][lane], make_uint4(0, 0, 0, 0));
       }
+      if (!y) continue;
 #pragma unroll
-      for (int h = 0; h < TG; ++h) {
-        if (!y[h]) continue;
-        const float f = factor[h];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int n_left = N - 32 * tile - 16 * k - 4 * c;
-          uint8_t* to = y[h] + 4 * k * kBytes;
-          float4 v;
-          if constexpr (TG == 1)
-            v = make_float4(acc[k][0][0] + acc[k][0][2], acc[k][0][1] + acc[k][0][3], acc[k][1][0] + acc[k][1][2], acc[k][1][1] + acc[k][1][3]);
-          else
-            v = make_float4(acc[k][0][2 * h], acc[k][0][2 * h + 1], acc[k][1][2 * h], acc[k][1][2 * h + 1]);
-          v = make_float4(f * v.x, f * v.y, f * v.z, f * v.w);
-          if (vec && n_left >= 4) {
-            if (p.base) {
-              const uint4 d = old[h][k];
-              if constexpr (OUT == QGEMV_OUT_F32) {
-                v.x += __uint_as_float(d.x), v.y += __uint_as_float(d.y), v.z += __uint_as_float(d.z), v.w += __uint_as_float(d.w);
-              } else {
-                const float2 a = unpair16<OUT == QGEMV_OUT_BF16>(d.x), e = unpair16<OUT == QGEMV_OUT_BF16>(d.y);
-                v.x += a.x, v.y += a.y, v.z += e.x, v.w += e.y;
-              }
-            }
-            lora_store4<OUT>(to, 0, 4, true, v);
-          } else if (n_left > 0) {
-            if (p.base) {
-              const int64_t back = static_cast<const uint8_t*>(p.base) - static_cast<const uint8_t*>(p.y);
-              const float4 d = lora_load4<OUT>(to + back, 0, n_left, false);
-              v.x += d.x, v.y += d.y, v.z += d.z, v.w += d.w;
-            }
-            lora_store4<OUT>(to, 0, n_left, false, v);
-          }
+      for (int k = 0; k < 2; ++k) {
+        const int n_left = N - 32 * tile - 16 * k - 4 * c;
+        uint8_t* to = y + 4 * k * kBytes;
+        float4 v = make_float4(f * (acc[k][0][0] + acc[k][0][2]), f * (acc[k][0][1] + acc[k][0][3]), f * (acc[k][1][0] + acc[k][1][2]),
+                               f * (acc[k][1][1] + acc[k][1][3]));
+        if (n_left <= 0) continue;
+        const bool whole = vec && n_left >= 4;
+        if (p.base) {
+          const int64_t back = static_cast<const uint8_t*>(p.base) - static_cast<const uint8_t*>(p.y);
+          const float4 d = whole ? lora_four<OUT>(old[k]) : lora_load4<OUT>(to + back, 0, n_left, false);
+          v.x += d.x, v.y += d.y, v.z += d.z, v.w += d.w;
         }
-        y[h] += kStep * (kBytes / 4);
+        lora_store4<OUT>(to, 0, n_left, whole, v);
       }
+      y += kStep * (kBytes / 4);
     }
     cp_async_wait<0>();  // the ring is used again
   }
 };
 
-template <bool BF, int OUT, int TG>
-__global__ void __launch_bounds__(kLoraThreads, LoraShape<TG>::kCtasPerSm) lora_kernel(const qgemv_lora_t p, int slots, int shares, int* err) {
-  using Sh = LoraShape<TG>;
-  constexpr int kLoraRows = Sh::kRows;
+template <bool BF, int OUT>
+__global__ void __launch_bounds__(kLoraThreads, 4) lora_few_kernel(const __grid_constant__ qgemv_lora_t p, const LoraWork work, int slots, int shares) {
+  constexpr int kParts = lora_parts(BF);
   extern __shared__ __align__(16) uint8_t dyn[];
-  LoraSmem<TG>& sm = *reinterpret_cast<LoraSmem<TG>*>(dyn);
-  __shared__ uint32_t rows_of[kLoraRows];  // of each distinct adapter among the rows: their mask
+  LoraFewSmem& sm = *reinterpret_cast<LoraFewSmem*>(dyn);
+  __shared__ uint32_t rows_of[32];
   __shared__ int count;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int rank = static_cast<int>(blockIdx.x) % kLoraCluster;
-  const int cluster = static_cast<int>(blockIdx.x) / kLoraCluster, share = cluster % shares;
-  const int slot = cluster / shares % slots;
-  const int64_t chunk = cluster / shares / slots;
-  const int64_t m0 = chunk * kLoraRows;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
+  const int share = static_cast<int>(blockIdx.x) % shares, slot = static_cast<int>(blockIdx.x) / shares % slots;
+  const int64_t m0 = static_cast<int64_t>(static_cast<int>(blockIdx.x) / shares / slots) * 32;
   if (warp == 0) {
-    const int64_t m = m0 + lane;
-    int id = -2;  // past the rows
-    if (lane < kLoraRows && m < p.rows) {
-      id = p.ids[m];
-      if (id < -1 || id >= p.adapters) {
-        if (slot == 0 && share == 0 && rank == 0) atomicOr(err, kDevErrIndex);
-        id = -1;
-      }
-    }
-    const uint32_t same = __match_any_sync(0xffffffffu, id);
-    const bool first = id != -2 && __ffs(same) - 1 == lane;
-    const uint32_t firsts = __ballot_sync(0xffffffffu, first);
-    if (first) rows_of[__popc(firsts & ((1u << lane) - 1))] = same;
-    if (lane == 0) count = __popc(firsts);
+    const int n = lora_distinct(p, m0, 32, rows_of, nullptr);
+    if (lane == 0) count = n;
   }
   __syncthreads();
-  const int64_t blocks = (p.K + 31) / 32, tiles = (p.N + 31) / 32, parts = shares * kLoraCluster, part = share * kLoraCluster + rank;
-  const int64_t b0 = blocks * rank / kLoraCluster, b1 = blocks * (rank + 1) / kLoraCluster;
-  const int t0 = static_cast<int>(tiles * part / parts), t1 = static_cast<int>(tiles * (part + 1) / parts);
+  const int64_t tiles = (p.N + 31) / 32;
+  const int t0 = static_cast<int>(tiles * share / shares), t1 = static_cast<int>(tiles * (share + 1) / shares);
+  bool waited = false;
   for (int i = slot; i < count; i += slots) {
     const uint32_t mask = rows_of[i];
-    const int n_tok = __popc(mask);
-    const int id = p.ids[m0 + __ffs(mask) - 1];
-    const int a = id >= 0 && id < p.adapters ? id : -1;
-    const int r = a < 0 ? 0 : p.ranks ? min(max(p.ranks[a], 0), p.rank) : p.rank;
-    const float scale = a >= 0 && p.scales ? p.scales[a] : 1.f;
+    const int n_tok = __popc(mask), a = lora_adapter(p, m0 + __ffs(mask) - 1), r = lora_rank(p, a);
     if (warp == 0 && (mask >> lane & 1)) sm.row[__popc(mask & ((1u << lane) - 1))] = static_cast<int>(m0) + lane;
     __syncthreads();
     if (r == 0) {  // no adapter: the base itself
@@ -448,35 +467,129 @@ __global__ void __launch_bounds__(kLoraThreads, LoraShape<TG>::kCtasPerSm) lora_
       __syncthreads();
       continue;
     }
-    const uint16_t* A = static_cast<const uint16_t*>(p.A) + static_cast<int64_t>(a) * p.rank * p.K;
     const uint16_t* B = static_cast<const uint16_t*>(p.B) + static_cast<int64_t>(a) * p.N * p.rank;
-    for (int k0 = 0; k0 < n_tok; k0 += Sh::kTokens) {  // up to kTokens of its rows at a time
-      const int* rows = sm.row + k0;
-      const int n = min(n_tok - k0, Sh::kTokens);
-      LoraExpand<BF, TG, OUT> expand(p, sm, rows, B, r, n, t0, t1);
-      expand.begin();
-      for (int j = 0; j < r; j += 16 * Sh::kRT) lora_shrink<BF, TG>(p, sm, rows, A, r, j, n, b0, b1);
-      cluster_arrive();
-      cluster_wait();
-      const int r4 = (r + 31) / 32 * 8;  // float4 per token; past the rank the sums are zeros
-      for (int e = threadIdx.x; e < (n + 7) / 8 * 8 * r4; e += kLoraThreads) {
-        const int tok = e / r4, j = e % r4 * 4;
-        const uint32_t at = smem_u32(&sm.own[tok][j]);
-        float4 v[kLoraCluster];
-#pragma unroll
-        for (int q = 0; q < kLoraCluster; ++q) v[q] = cluster_ld4(at, q);
-        float4 s = v[0];
-#pragma unroll
-        for (int q = 1; q < kLoraCluster; ++q) s.x += v[q].x, s.y += v[q].y, s.z += v[q].z, s.w += v[q].w;
-        *reinterpret_cast<float4*>(&sm.sum[tok][j]) = s;
+    for (int k0 = 0; k0 < n_tok; k0 += 8) {
+      const int n = min(n_tok - k0, 8);
+      LoraStream<BF, OUT> stream(p, sm, sm.row + k0, B, r, n, t0, t1);
+      stream.begin();
+      if (!waited) pdl_wait();  // for the sums
+      waited = true;
+      const int blocks = (r + 31) / 32;
+      for (int q = warp; q < blocks * kParts; q += kLoraWarps) {
+        const int b = q / kParts, part = q - b * kParts;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (g < n) v = __ldcg(work.parts + (static_cast<int64_t>(sm.row[k0 + g]) * work.blocks + b) * (4 * kParts) + part * 4 + c);
+        sm.parts[b][part][lane] = v;
       }
-      cluster_arrive();  // this CTA reads the others' sums no more
+      if (threadIdx.x < 8) sm.factor[threadIdx.x] = static_cast<int>(threadIdx.x) < n ? __ldcg(work.factor + sm.row[k0 + threadIdx.x]) : 0.f;
       __syncthreads();
-      if (warp < (n + 7) / 8) lora_parts<BF, TG>(sm, warp, (r + 31) / 32, scale);
+      stream.run(t0);
       __syncthreads();
-      expand.run(t0);
-      cluster_wait();  // no CTA reads this one's sums: they are used again, or the CTA ends
-      __syncthreads();
+    }
+  }
+  if (!waited) pdl_wait();  // the launch ends after the one before it
+}
+
+// ------------------------------------------------------------------------- outputs of many rows
+// A warp keeps 32 rows of B (NB blocks of 32 ranks) and walks over tiles of 16 rows of the batch; sums and
+// base of the next tile are requested before the tile in hand is multiplied.  In a tile whose rows have
+// several adapters, one is taken after another, with the sums of the others' rows as zeros.
+template <bool BF, int OUT, int NB>
+__global__ void __launch_bounds__(kLoraThreads, NB == 1 ? 4 : NB == 2 ? 3 : 2)
+    lora_many_kernel(const __grid_constant__ qgemv_lora_t p, const LoraWork work, int splits) {
+  constexpr int kParts = lora_parts(BF);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
+  const int split = static_cast<int>(blockIdx.x) % splits;
+  const int n0 = (static_cast<int>(blockIdx.x) / splits * kLoraWarps + warp) * 32;
+  const int64_t tiles = (p.rows + 15) / 16;
+  const int t0 = static_cast<int>(tiles * split / splits), t1 = static_cast<int>(tiles * (split + 1) / splits);
+  const int N = static_cast<int>(p.N), rows = static_cast<int>(p.rows);
+  const bool vec = p.y_stride % 4 == 0;
+  const int left[2] = {N - n0 - 4 * c, N - n0 - 16 - 4 * c};  // outputs from the lane's first in each half
+  pdl_wait();
+  if (n0 >= N) return;
+  struct Rows {  // rows g and g + 8 of a tile
+    int id[2];
+    float factor[2];
+    float4 base[2][2];
+    uint4 part[NB][kParts][2];
+  };
+  auto read = [&](int tile, Rows& t) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int m = 16 * tile + 8 * h + g;
+      const bool there = m < rows;
+      t.id[h] = there ? lora_adapter(p, m) : -1;
+      if (t.id[h] >= 0 && lora_rank(p, t.id[h]) == 0) t.id[h] = -1;
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        t.base[h][k] = there && p.base && left[k] > 0 ? lora_load4<OUT>(p.base, m * p.y_stride + n0 + 16 * k + 4 * c, left[k], vec) : make_float4(0.f, 0.f, 0.f, 0.f);
+      const bool sums = t.id[h] >= 0;
+      t.factor[h] = sums ? work.factor[m] : 0.f;
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int q = 0; q < kParts; ++q)
+          t.part[b][q][h] = sums && b < work.blocks ? work.parts[(static_cast<int64_t>(m) * work.blocks + b) * (4 * kParts) + q * 4 + c] : make_uint4(0, 0, 0, 0);
+    }
+  };
+  uint4 w[NB][4];
+  int cur = -1;
+  auto hold = [&](int a) {  // the rows of B of adapter a
+    if (a == cur) return;
+    cur = a;
+    const int r = lora_rank(p, a);
+    const uint16_t* at = static_cast<const uint16_t*>(p.B) + (static_cast<int64_t>(a) * p.N + n0 + 4 * (g >> 1) + (g & 1)) * p.rank + 8 * c;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        const int row = 2 * (h & 1) + 16 * (h >> 1);
+        w[b][h] = 32 * b + 8 * c < r && n0 + 4 * (g >> 1) + (g & 1) + row < N ? *reinterpret_cast<const uint4*>(at + row * p.rank + 32 * b) : make_uint4(0, 0, 0, 0);
+      }
+      lora_mask(w[b], 32 * b + 8 * c, r);
+    }
+  };
+  Rows next;
+  if (t0 < t1) read(t0, next);
+#pragma unroll 1
+  for (int tile = t0; tile < t1; ++tile) {
+    Rows t = next;
+    if (tile + 1 < t1) read(tile + 1, next);
+    float acc[2][2][4] = {};
+    for (;;) {
+      // the adapter of the first row that still has one
+      const uint32_t has0 = __ballot_sync(0xffffffffu, t.id[0] >= 0), has1 = __ballot_sync(0xffffffffu, t.id[1] >= 0);
+      if (!(has0 | has1)) break;
+      const int a = has0 ? __shfl_sync(0xffffffffu, t.id[0], __ffs(has0) - 1) : __shfl_sync(0xffffffffu, t.id[1], __ffs(has1) - 1);
+      hold(a);
+      const bool in0 = t.id[0] == a, in1 = t.id[1] == a;
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int q = 0; q < kParts; ++q) {
+          const uint4 zero = make_uint4(0, 0, 0, 0), s0 = in0 ? t.part[b][q][0] : zero, s1 = in1 ? t.part[b][q][1] : zero;
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            mma16816<BF>(acc[h >> 1][h & 1], s0.x, s1.x, s0.y, s1.y, w[b][h].x, w[b][h].y);
+            mma16816<BF>(acc[h >> 1][h & 1], s0.z, s1.z, s0.w, s1.w, w[b][h].z, w[b][h].w);
+          }
+        }
+      if (in0) t.id[0] = -1;
+      if (in1) t.id[1] = -1;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int m = 16 * tile + 8 * h + g;
+      if (m >= rows) continue;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        if (left[k] <= 0) continue;
+        const float f = t.factor[h];
+        const float4 d = t.base[h][k];
+        lora_store4<OUT>(p.y, m * p.y_stride + n0 + 16 * k + 4 * c, left[k], vec,
+                         make_float4(d.x + f * acc[k][0][2 * h], d.y + f * acc[k][0][2 * h + 1], d.z + f * acc[k][1][2 * h], d.w + f * acc[k][1][2 * h + 1]));
+      }
     }
   }
 }
