@@ -50,9 +50,9 @@ bool launch(const Handle& h, qgemv_lora_t p, const LoraWork& work, cudaStream_t 
   if (!start(fn, chunks * slots * kLoraCluster, 0, kLoraCluster, false, sums, stream)) return false;
   const int64_t tiles = (p.N + 31) / 32;
   if (few) {
-    // CTAs that share an adapter's N: about three rounds of them, and at least two tiles for a warp
+    // CTAs that share an adapter's N: about two rounds of them, and at least two tiles for a warp
     slots = static_cast<int>(std::min<int64_t>(32, p.rows));
-    int shares = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(12 * h.sms / (chunks * slots), tiles / (2 * kLoraWarps))));
+    int shares = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8 * h.sms / (chunks * slots), tiles / (2 * kLoraWarps))));
     void* args[] = {&p, &w, &slots, &shares};
     return start(reinterpret_cast<const void*>(lora_few_kernel<BF, OUT>), chunks * slots * shares, sizeof(LoraFewSmem), 1, true, args, stream);
   }
@@ -95,8 +95,8 @@ extern "C" qgemv_status_t qgemv_run_lora(qgemv_handle_t hh, const qgemv_lora_t* 
   LoraWork work{};
   work.blocks = (p.rank + 31) / 32;
   const int64_t row_bytes = int64_t{64} * work.blocks * lora_parts(bf);
-  // rows at a time: whole tiles of 16, their sums and factors in the workspace
-  const int64_t most = static_cast<int64_t>(kWsFloats) * 4 / (row_bytes + 4) / 32 * 32;
+  // rows at a time: whole tiles of 16, their sums, factors and adapters in the workspace
+  const int64_t most = static_cast<int64_t>(kWsFloats) * 4 / (row_bytes + 8) / 32 * 32;
   work.parts = reinterpret_cast<uint4*>(h->ws);
   for (int64_t m = 0; m < p.rows; m += most) {
     qgemv_lora_t q = p;
@@ -107,6 +107,7 @@ extern "C" qgemv_status_t qgemv_run_lora(qgemv_handle_t hh, const qgemv_lora_t* 
     q.base = p.base ? static_cast<const uint8_t*>(p.base) + at : nullptr;
     q.y = static_cast<uint8_t*>(p.y) + at;
     work.factor = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(h->ws) + (q.rows + 15) / 16 * 16 * row_bytes);
+    work.adapter = reinterpret_cast<int*>(work.factor + q.rows);
     if (!(bf ? launch_out<true>(*h, q, work, stream) : launch_out<false>(*h, q, work, stream))) {
       cudaGetLastError();
       return QGEMV_ERR_CUDA;

@@ -39,10 +39,12 @@ constexpr int kLoraWarps = 4;
 constexpr int kLoraThreads = 32 * kLoraWarps;
 
 // The rows of a launch in the workspace: per row, the parts of its sums (blocks of 32 ranks, kParts, four
-// lanes of 16 bytes), then per row its factor (the adapter's scale over the parts' power of two).
+// lanes of 16 bytes), then per row its factor (the adapter's scale over the parts' power of two) and its
+// adapter (-1: none, or one of rank 0).
 struct LoraWork {
   uint4* parts;
   float* factor;
+  int* adapter;
   int blocks;  // 32-wide blocks of the largest rank
 };
 __host__ __device__ constexpr int lora_parts(bool bf) { return bf ? 3 : 2; }
@@ -176,7 +178,7 @@ __device__ __forceinline__ void lora_mask(uint4 (&w)[4], int j, int r) {
 template <bool BF, int TG>
 __device__ __forceinline__ void lora_shrink(const qgemv_lora_t& p, LoraSmem<TG>& sm, const int* rows, const uint16_t* A, int r, int j0, int n_tok, int64_t b0, int64_t b1) {
   constexpr int RT = LoraShape<TG>::kRT;
-  constexpr int U = TG == 1 ? 2 : 1;  // blocks in flight
+  constexpr int U = 2;  // blocks in flight
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
   float acc[RT][TG][4];
 #pragma unroll
@@ -252,6 +254,7 @@ __global__ void __launch_bounds__(kLoraThreads, 4) lora_sums_kernel(const __grid
   for (int i = slot; i < count; i += slots) {
     const uint32_t mask = rows_of[i];
     const int n_tok = __popc(mask), a = lora_adapter(p, m0 + __ffs(mask) - 1), r = lora_rank(p, a);
+    if (rank == 0 && warp == 0 && (mask >> lane & 1)) work.adapter[m0 + lane] = r ? a : -1;
     if (r == 0) continue;
     const float scale = p.scales ? p.scales[a] : 1.f;
     if (warp == 0 && (mask >> lane & 1)) sm.row[__popc(mask & ((1u << lane) - 1))] = static_cast<int>(m0) + lane;
@@ -499,6 +502,7 @@ __global__ void __launch_bounds__(kLoraThreads, NB == 1 ? 4 : NB == 2 ? 3 : 2)
     lora_many_kernel(const __grid_constant__ qgemv_lora_t p, const LoraWork work, int splits) {
   constexpr int kParts = lora_parts(BF);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
+  constexpr int kBytes = OUT == QGEMV_OUT_F32 ? 16 : 8;  // of four outputs
   const int split = static_cast<int>(blockIdx.x) % splits;
   const int n0 = (static_cast<int>(blockIdx.x) / splits * kLoraWarps + warp) * 32;
   const int64_t tiles = (p.rows + 15) / 16;
@@ -506,6 +510,7 @@ __global__ void __launch_bounds__(kLoraThreads, NB == 1 ? 4 : NB == 2 ? 3 : 2)
   const int N = static_cast<int>(p.N), rows = static_cast<int>(p.rows);
   const bool vec = p.y_stride % 4 == 0;
   const int left[2] = {N - n0 - 4 * c, N - n0 - 16 - 4 * c};  // outputs from the lane's first in each half
+  const bool whole = vec && n0 + 32 <= N;                     // all lanes' outputs are there, four at once
   pdl_wait();
   if (n0 >= N) return;
   struct Rows {  // rows g and g + 8 of a tile
@@ -514,29 +519,45 @@ __global__ void __launch_bounds__(kLoraThreads, NB == 1 ? 4 : NB == 2 ? 3 : 2)
     float4 base[2][2];
     uint4 part[NB][kParts][2];
   };
-  auto read = [&](int tile, Rows& t) {
+  // of row g of the next tile to be read: base, parts; of the tile in hand: y
+  const int m_first = 16 * t0 + g;
+  const int64_t row8 = 8 * p.y_stride * (kBytes / 4), lane_at = (m_first * p.y_stride + n0 + 4 * c) * (kBytes / 4);
+  const uint8_t* base_at = static_cast<const uint8_t*>(p.base) + lane_at;
+  uint8_t* y_at = static_cast<uint8_t*>(p.y) + lane_at;
+  const int part_row = 4 * kParts * work.blocks;
+  const uint4* part_at = work.parts + static_cast<int64_t>(m_first) * part_row + c;
+  int m_next = m_first;
+  auto read = [&](Rows& t) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int m = 16 * tile + 8 * h + g;
+      const int m = m_next + 8 * h;
       const bool there = m < rows;
-      t.id[h] = there ? lora_adapter(p, m) : -1;
-      if (t.id[h] >= 0 && lora_rank(p, t.id[h]) == 0) t.id[h] = -1;
+      t.id[h] = there ? work.adapter[m] : -1;
+      t.factor[h] = t.id[h] >= 0 ? work.factor[m] : 0.f;
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
-        t.base[h][k] = there && p.base && left[k] > 0 ? lora_load4<OUT>(p.base, m * p.y_stride + n0 + 16 * k + 4 * c, left[k], vec) : make_float4(0.f, 0.f, 0.f, 0.f);
-      const bool sums = t.id[h] >= 0;
-      t.factor[h] = sums ? work.factor[m] : 0.f;
+      for (int k = 0; k < 2; ++k) {
+        t.base[h][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (p.base && there) {
+          const uint8_t* at = base_at + h * row8 + k * 4 * kBytes;
+          if (whole)
+            t.base[h][k] = lora_load4<OUT>(at, 0, 4, true);
+          else if (left[k] > 0)
+            t.base[h][k] = lora_load4<OUT>(at, 0, left[k], vec);
+        }
+      }
 #pragma unroll
       for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int q = 0; q < kParts; ++q)
-          t.part[b][q][h] = sums && b < work.blocks ? work.parts[(static_cast<int64_t>(m) * work.blocks + b) * (4 * kParts) + q * 4 + c] : make_uint4(0, 0, 0, 0);
+          t.part[b][q][h] = there && (NB < 4 || b < work.blocks) ? part_at[h * 8 * part_row + (b * kParts + q) * 4] : make_uint4(0, 0, 0, 0);
     }
+    m_next += 16;
+    base_at += 2 * row8;
+    part_at += 16 * part_row;
   };
   uint4 w[NB][4];
   int cur = -1;
   auto hold = [&](int a) {  // the rows of B of adapter a
-    if (a == cur) return;
     cur = a;
     const int r = lora_rank(p, a);
     const uint16_t* at = static_cast<const uint16_t*>(p.B) + (static_cast<int64_t>(a) * p.N + n0 + 4 * (g >> 1) + (g & 1)) * p.rank + 8 * c;
@@ -551,46 +572,53 @@ __global__ void __launch_bounds__(kLoraThreads, NB == 1 ? 4 : NB == 2 ? 3 : 2)
     }
   };
   Rows next;
-  if (t0 < t1) read(t0, next);
+  if (t0 < t1) read(next);
 #pragma unroll 1
-  for (int tile = t0; tile < t1; ++tile) {
+  for (int tile = t0, m = m_first; tile < t1; ++tile, m += 16) {
     Rows t = next;
-    if (tile + 1 < t1) read(tile + 1, next);
+    if (tile + 1 < t1) read(next);
     float acc[2][2][4] = {};
-    for (;;) {
-      // the adapter of the first row that still has one
-      const uint32_t has0 = __ballot_sync(0xffffffffu, t.id[0] >= 0), has1 = __ballot_sync(0xffffffffu, t.id[1] >= 0);
-      if (!(has0 | has1)) break;
-      const int a = has0 ? __shfl_sync(0xffffffffu, t.id[0], __ffs(has0) - 1) : __shfl_sync(0xffffffffu, t.id[1], __ffs(has1) - 1);
-      hold(a);
-      const bool in0 = t.id[0] == a, in1 = t.id[1] == a;
+    auto add = [&](bool in0, bool in1) {
 #pragma unroll
       for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int q = 0; q < kParts; ++q) {
           const uint4 zero = make_uint4(0, 0, 0, 0), s0 = in0 ? t.part[b][q][0] : zero, s1 = in1 ? t.part[b][q][1] : zero;
 #pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            mma16816<BF>(acc[h >> 1][h & 1], s0.x, s1.x, s0.y, s1.y, w[b][h].x, w[b][h].y);
-            mma16816<BF>(acc[h >> 1][h & 1], s0.z, s1.z, s0.w, s1.w, w[b][h].z, w[b][h].w);
-          }
+          for (int h = 0; h < 4; ++h) mma16816<BF>(acc[h >> 1][h & 1], s0.x, s1.x, s0.y, s1.y, w[b][h].x, w[b][h].y);
+#pragma unroll
+          for (int h = 0; h < 4; ++h) mma16816<BF>(acc[h >> 1][h & 1], s0.z, s1.z, s0.w, s1.w, w[b][h].z, w[b][h].w);
         }
+    };
+#pragma unroll 1
+    for (;;) {  // mostly once: rows of one adapter follow one another
+      const uint32_t has0 = __ballot_sync(0xffffffffu, t.id[0] >= 0), has1 = __ballot_sync(0xffffffffu, t.id[1] >= 0);
+      if (!(has0 | has1)) break;
+      // the adapter of the first row that still has one
+      const int a = __shfl_sync(0xffffffffu, has0 ? t.id[0] : t.id[1], __ffs(has0 ? has0 : has1) - 1);
+      if (a != cur) hold(a);
+      const bool in0 = t.id[0] == a, in1 = t.id[1] == a;
+      add(in0, in1);
       if (in0) t.id[0] = -1;
       if (in1) t.id[1] = -1;
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int m = 16 * tile + 8 * h + g;
-      if (m >= rows) continue;
+      if (m + 8 * h >= rows) continue;
+      const float f = t.factor[h];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        if (left[k] <= 0) continue;
-        const float f = t.factor[h];
         const float4 d = t.base[h][k];
-        lora_store4<OUT>(p.y, m * p.y_stride + n0 + 16 * k + 4 * c, left[k], vec,
-                         make_float4(d.x + f * acc[k][0][2 * h], d.y + f * acc[k][0][2 * h + 1], d.z + f * acc[k][1][2 * h], d.w + f * acc[k][1][2 * h + 1]));
+        const float4 v = make_float4(acc[k][0][2 * h], acc[k][0][2 * h + 1], acc[k][1][2 * h], acc[k][1][2 * h + 1]);
+        const float4 out = make_float4(d.x + f * v.x, d.y + f * v.y, d.z + f * v.z, d.w + f * v.w);
+        uint8_t* to = y_at + h * row8 + k * 4 * kBytes;
+        if (whole)
+          lora_store4<OUT>(to, 0, 4, true, out);
+        else if (left[k] > 0)
+          lora_store4<OUT>(to, 0, left[k], vec, out);
       }
     }
+    y_at += 2 * row8;
   }
 }
 
