@@ -38,15 +38,15 @@ bool start(const void* fn, int64_t grid, size_t smem, int cluster, bool dependen
 template <bool BF, int OUT>
 bool launch(const Handle& h, qgemv_lora_t p, const LoraWork& work, cudaStream_t stream) {
   const bool few = p.rows <= kLoraFewRows;
-  const int64_t per = few ? LoraShape<1>::kRows : LoraShape<2>::kRows, chunks = (p.rows + per - 1) / per;
+  const int64_t chunks = (p.rows + kLoraChunk - 1) / kLoraChunk;
   // Sums: clusters per chunk of rows, one for each adapter that they can have, but no more in all than run at
   // once (then a cluster takes its share of the adapters one after another).
   const int64_t resident = int64_t{h.sms} * 4 / kLoraCluster;
-  int slots = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min(per, p.rows), (resident + chunks - 1) / chunks)));
+  int slots = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(kLoraChunk, p.rows), (resident + chunks - 1) / chunks)));
   LoraWork w = work;
   int* err = h.err;
   void* sums[] = {&p, &w, &slots, &err};
-  const void* fn = few ? reinterpret_cast<const void*>(lora_sums_kernel<BF, 1>) : reinterpret_cast<const void*>(lora_sums_kernel<BF, 2>);
+  const void* fn = few ? reinterpret_cast<const void*>(lora_sums_kernel<BF, 1>) : reinterpret_cast<const void*>(lora_sums_kernel<BF, 4>);
   if (!start(fn, chunks * slots * kLoraCluster, 0, kLoraCluster, false, sums, stream)) return false;
   const int64_t tiles = (p.N + 31) / 32;
   if (few) {

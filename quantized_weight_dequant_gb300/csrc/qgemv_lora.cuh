@@ -4,7 +4,7 @@
 // With a few rows per adapter the work is bound by the bytes of A and B, with many rows by those of base
 // and y; a row's own work is 2 r (K + N) operations.  Two launches, the second a dependent one: it starts
 // while the first runs, fetches its first rows of B and the base, and waits for t only then.
-//  * Sums (lora_sums_kernel).  A cluster of eight CTAs takes the rows of one adapter among 16 or 32
+//  * Sums (lora_sums_kernel).  A cluster of eight CTAs takes the rows of one adapter among 32
 //    neighbouring rows of the batch, each CTA an eighth of K; the partial sums meet through distributed
 //    shared memory, where each CTA adds those of its own tokens in rank order.  The sums (fp32) are left in
 //    the workspace as what the second product multiplies: two fp16 parts scaled by a power of two per row
@@ -34,6 +34,7 @@ namespace qg {
 constexpr int kLoraMaxRank = 128;
 constexpr int kLoraFewRows = 256;  // up to here eight tokens of an adapter at a time, and B streams by
 constexpr int kLoraCluster = 8;
+constexpr int kLoraChunk = 32;     // neighbouring rows of the batch whose adapters one warp finds
 constexpr int kLoraLd = kLoraMaxRank + 4;  // floats per token of the sums in shared memory
 constexpr int kLoraWarps = 4;
 constexpr int kLoraThreads = 32 * kLoraWarps;
@@ -53,23 +54,22 @@ __host__ __device__ constexpr int lora_parts(bool bf) { return bf ? 3 : 2; }
 template <int TG>
 struct LoraShape {
   static constexpr int kTokens = 8 * TG;
-  static constexpr int kRows = TG == 1 ? 32 : 16;   // neighbouring rows of the batch per cluster
-  static constexpr int kRT = 4;                     // 16-row tiles of A taken at a time
+  static constexpr int kRT = TG == 1 ? 4 : 2;       // 16-row tiles of A taken at a time
 };
 
 template <int TG>
 struct LoraSmem {
   float own[8 * TG][kLoraLd];                                             // this CTA's sums over its part of K
   float part[kLoraWarps][8 * TG][16 * LoraShape<TG>::kRT + 4];            // those of a warp
-  int row[LoraShape<TG>::kRows];                                          // rows of the adapter in hand
+  int row[kLoraChunk];                                                    // rows of the adapter in hand
 };
 
-// The distinct adapters among `n_rows` (up to 32) rows from m0 on, found by one warp: rows_of[i] is the mask of
+// The distinct adapters among the kLoraChunk rows from m0 on, found by one warp: rows_of[i] is the mask of
 // the rows of the i-th, in order of first appearance (those without one among them).  Returns their number.
-__device__ __forceinline__ int lora_distinct(const qgemv_lora_t& p, int64_t m0, int n_rows, uint32_t* rows_of, int* err) {
+__device__ __forceinline__ int lora_distinct(const qgemv_lora_t& p, int64_t m0, uint32_t* rows_of, int* err) {
   const int lane = threadIdx.x & 31;
   int id = -2;  // past the rows
-  if (lane < n_rows && m0 + lane < p.rows) {
+  if (m0 + lane < p.rows) {
     id = p.ids[m0 + lane];
     if (id < -1 || id >= p.adapters) {
       if (err) atomicOr(err, kDevErrIndex);
@@ -242,10 +242,10 @@ __global__ void __launch_bounds__(kLoraThreads, 4) lora_sums_kernel(const __grid
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rank = static_cast<int>(blockIdx.x) % kLoraCluster, cluster = static_cast<int>(blockIdx.x) / kLoraCluster;
   const int slot = cluster % slots;
-  const int64_t m0 = static_cast<int64_t>(cluster / slots) * Sh::kRows;
+  const int64_t m0 = static_cast<int64_t>(cluster / slots) * kLoraChunk;
   pdl_launch_dependents();  // the second launch may start; it waits for this one's end before it reads the sums
   if (warp == 0) {
-    const int n = lora_distinct(p, m0, Sh::kRows, rows_of, slot == 0 && rank == 0 ? err : nullptr);
+    const int n = lora_distinct(p, m0, rows_of, slot == 0 && rank == 0 ? err : nullptr);
     if (lane == 0) count = n;
   }
   __syncthreads();
@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(kLoraThreads, 4) lora_few_kernel(const __grid_
   const int share = static_cast<int>(blockIdx.x) % shares, slot = static_cast<int>(blockIdx.x) / shares % slots;
   const int64_t m0 = static_cast<int64_t>(static_cast<int>(blockIdx.x) / shares / slots) * 32;
   if (warp == 0) {
-    const int n = lora_distinct(p, m0, 32, rows_of, nullptr);
+    const int n = lora_distinct(p, m0, rows_of, nullptr);
     if (lane == 0) count = n;
   }
   __syncthreads();
@@ -494,9 +494,11 @@ __global__ void __launch_bounds__(kLoraThreads, 4) lora_few_kernel(const __grid_
 }
 
 // ------------------------------------------------------------------------- outputs of many rows
-// A warp keeps 32 rows of B (NB blocks of 32 ranks) and walks over tiles of 16 rows of the batch; sums and
-// base of the next tile are requested before the tile in hand is multiplied.  In a tile whose rows have
-// several adapters, one is taken after another, with the sums of the others' rows as zeros.
+// A warp keeps 32 rows of B (NB blocks of 32 ranks) and walks over tiles of 16 rows of the batch.  The base,
+// which comes from memory, is asked for kLoraAhead tiles ahead through a ring of cp.async (each lane its own
+// 64 bytes of a tile); the sums come from L2 when they are needed.  In a tile whose rows have several
+// adapters, one is taken after another, with the sums of the others' rows as zeros.
+constexpr int kLoraAhead = 4;
 template <bool BF, int OUT, int NB>
 __global__ void __launch_bounds__(kLoraThreads, NB == 1 ? 4 : NB == 2 ? 3 : 2)
     lora_many_kernel(const __grid_constant__ qgemv_lora_t p, const LoraWork work, int splits) {
@@ -511,49 +513,30 @@ __global__ void __launch_bounds__(kLoraThreads, NB == 1 ? 4 : NB == 2 ? 3 : 2)
   const bool vec = p.y_stride % 4 == 0;
   const int left[2] = {N - n0 - 4 * c, N - n0 - 16 - 4 * c};  // outputs from the lane's first in each half
   const bool whole = vec && n0 + 32 <= N;                     // all lanes' outputs are there, four at once
-  pdl_wait();
-  if (n0 >= N) return;
-  struct Rows {  // rows g and g + 8 of a tile
-    int id[2];
-    float factor[2];
-    float4 base[2][2];
-    uint4 part[NB][kParts][2];
-  };
-  // of row g of the next tile to be read: base, parts; of the tile in hand: y
+  __shared__ uint4 ring[kLoraWarps][kLoraAhead][4][32];
+  // of row g of the next tile to be asked for: base; of the tile in hand: y, parts
   const int m_first = 16 * t0 + g;
   const int64_t row8 = 8 * p.y_stride * (kBytes / 4), lane_at = (m_first * p.y_stride + n0 + 4 * c) * (kBytes / 4);
-  const uint8_t* base_at = static_cast<const uint8_t*>(p.base) + lane_at;
+  const uint8_t* base_at = p.base ? static_cast<const uint8_t*>(p.base) + lane_at : nullptr;
   uint8_t* y_at = static_cast<uint8_t*>(p.y) + lane_at;
   const int part_row = 4 * kParts * work.blocks;
   const uint4* part_at = work.parts + static_cast<int64_t>(m_first) * part_row + c;
-  int m_next = m_first;
-  auto read = [&](Rows& t) {
+  int m_ask = m_first, ask_s = 0;
+  const int m_end = min(rows, 16 * t1);
+  const uint32_t mine = smem_u32(&ring[warp][0][0][lane]);
+  auto ask = [&]() {
+    if (whole && base_at) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int m = m_next + 8 * h;
-      const bool there = m < rows;
-      t.id[h] = there ? work.adapter[m] : -1;
-      t.factor[h] = t.id[h] >= 0 ? work.factor[m] : 0.f;
+      for (int h = 0; h < 2; ++h)
+        if (m_ask + 8 * h < m_end) {
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        t.base[h][k] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (p.base && there) {
-          const uint8_t* at = base_at + h * row8 + k * 4 * kBytes;
-          if (whole)
-            t.base[h][k] = lora_load4<OUT>(at, 0, 4, true);
-          else if (left[k] > 0)
-            t.base[h][k] = lora_load4<OUT>(at, 0, left[k], vec);
+          for (int k = 0; k < 2; ++k) cp_async_fill<kBytes>(mine + (ask_s * 4 + 2 * h + k) * 512, base_at + h * row8 + k * 4 * kBytes, kBytes);
         }
-      }
-#pragma unroll
-      for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int q = 0; q < kParts; ++q)
-          t.part[b][q][h] = there && (NB < 4 || b < work.blocks) ? part_at[h * 8 * part_row + (b * kParts + q) * 4] : make_uint4(0, 0, 0, 0);
+      base_at += 2 * row8;
+      m_ask += 16;
     }
-    m_next += 16;
-    base_at += 2 * row8;
-    part_at += 16 * part_row;
+    cp_async_commit();
+    if (++ask_s == kLoraAhead) ask_s = 0;
   };
   uint4 w[NB][4];
   int cur = -1;
@@ -571,19 +554,36 @@ __global__ void __launch_bounds__(kLoraThreads, NB == 1 ? 4 : NB == 2 ? 3 : 2)
       lora_mask(w[b], 32 * b + 8 * c, r);
     }
   };
-  Rows next;
-  if (t0 < t1) read(next);
+  const uint8_t* old_at = base_at;  // of the tile in hand
+#pragma unroll 1
+  for (int i = 0; i < kLoraAhead; ++i) ask();
+  pdl_wait();  // for the sums; the base is not theirs
+  int s = 0;
 #pragma unroll 1
   for (int tile = t0, m = m_first; tile < t1; ++tile, m += 16) {
-    Rows t = next;
-    if (tile + 1 < t1) read(next);
+    int id[2];
+    float factor[2];
+    uint4 part[NB][kParts][2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const bool there = m + 8 * h < rows;
+      id[h] = there ? work.adapter[m + 8 * h] : -1;
+      factor[h] = there ? work.factor[m + 8 * h] : 0.f;
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int q = 0; q < kParts; ++q)
+          part[b][q][h] = there && (NB < 4 || b < work.blocks) ? part_at[h * 8 * part_row + (b * kParts + q) * 4] : make_uint4(0, 0, 0, 0);
+    }
+    part_at += 16 * part_row;
+    const int id_of[2] = {id[0], id[1]};
     float acc[2][2][4] = {};
     auto add = [&](bool in0, bool in1) {
 #pragma unroll
       for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int q = 0; q < kParts; ++q) {
-          const uint4 zero = make_uint4(0, 0, 0, 0), s0 = in0 ? t.part[b][q][0] : zero, s1 = in1 ? t.part[b][q][1] : zero;
+          const uint4 zero = make_uint4(0, 0, 0, 0), s0 = in0 ? part[b][q][0] : zero, s1 = in1 ? part[b][q][1] : zero;
 #pragma unroll
           for (int h = 0; h < 4; ++h) mma16816<BF>(acc[h >> 1][h & 1], s0.x, s1.x, s0.y, s1.y, w[b][h].x, w[b][h].y);
 #pragma unroll
@@ -592,32 +592,36 @@ __global__ void __launch_bounds__(kLoraThreads, NB == 1 ? 4 : NB == 2 ? 3 : 2)
     };
 #pragma unroll 1
     for (;;) {  // mostly once: rows of one adapter follow one another
-      const uint32_t has0 = __ballot_sync(0xffffffffu, t.id[0] >= 0), has1 = __ballot_sync(0xffffffffu, t.id[1] >= 0);
+      const uint32_t has0 = __ballot_sync(0xffffffffu, id[0] >= 0), has1 = __ballot_sync(0xffffffffu, id[1] >= 0);
       if (!(has0 | has1)) break;
       // the adapter of the first row that still has one
-      const int a = __shfl_sync(0xffffffffu, has0 ? t.id[0] : t.id[1], __ffs(has0 ? has0 : has1) - 1);
+      const int a = __shfl_sync(0xffffffffu, has0 ? id[0] : id[1], __ffs(has0 ? has0 : has1) - 1);
       if (a != cur) hold(a);
-      const bool in0 = t.id[0] == a, in1 = t.id[1] == a;
+      const bool in0 = id[0] == a, in1 = id[1] == a;
       add(in0, in1);
-      if (in0) t.id[0] = -1;
-      if (in1) t.id[1] = -1;
+      if (in0) id[0] = -1;
+      if (in1) id[1] = -1;
     }
+    cp_async_wait<kLoraAhead - 1>();
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       if (m + 8 * h >= rows) continue;
-      const float f = t.factor[h];
+      const float f = id_of[h] >= 0 ? factor[h] : 0.f;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const float4 d = t.base[h][k];
-        const float4 v = make_float4(acc[k][0][2 * h], acc[k][0][2 * h + 1], acc[k][1][2 * h], acc[k][1][2 * h + 1]);
-        const float4 out = make_float4(d.x + f * v.x, d.y + f * v.y, d.z + f * v.z, d.w + f * v.w);
-        uint8_t* to = y_at + h * row8 + k * 4 * kBytes;
-        if (whole)
-          lora_store4<OUT>(to, 0, 4, true, out);
-        else if (left[k] > 0)
-          lora_store4<OUT>(to, 0, left[k], vec, out);
+        if (left[k] <= 0) continue;
+        float4 v = make_float4(f * acc[k][0][2 * h], f * acc[k][0][2 * h + 1], f * acc[k][1][2 * h], f * acc[k][1][2 * h + 1]);
+        const int64_t off = h * row8 + k * 4 * kBytes;
+        if (old_at) {
+          const float4 d = whole ? lora_four<OUT>(lds_v4(mine + (s * 4 + 2 * h + k) * 512)) : lora_load4<OUT>(old_at + off, 0, left[k], vec);
+          v.x += d.x, v.y += d.y, v.z += d.z, v.w += d.w;
+        }
+        lora_store4<OUT>(y_at + off, 0, left[k], vec, v);
       }
     }
+    if (old_at) old_at += 2 * row8;
+    ask();
+    if (++s == kLoraAhead) s = 0;
     y_at += 2 * row8;
   }
 }
