@@ -48,8 +48,9 @@ qgemv_status_t launch(const Handle& h, const qgemv_attn_decode_t& p, AttnArgs a,
   const int64_t tiles = (static_cast<int64_t>(p.table_width) * p.cache.page_size + Sh::kTT - 1) / Sh::kTT;
   const int64_t most = std::min<int64_t>(int64_t{1} << 40, tiles) * p.requests;
   const int64_t shares = std::min<int64_t>(int64_t{1} << 30, most) * (1 + a.seg_cost) * a.kv_heads * a.splits / a.min_units + 1;
-  const int64_t grid = std::min<int64_t>(static_cast<int64_t>(h.sms) * Sh::kCtasPerSm, shares);
-  if (grid > kMaxRanges || grid * 2 * Sh::kPiece > static_cast<int64_t>(kWsFloats)) return QGEMV_ERR_BAD_SHAPE;
+  int64_t grid = std::min<int64_t>(static_cast<int64_t>(h.sms) * Sh::kCtasPerSm, shares);
+  static_assert(3 * kAttnCounters <= kMaxRanges && int64_t{4} * kAttnCounters / (3 - Sh::kCtasPerSm) * Sh::kPiece <= int64_t{kWsFloats}, "workspace");
+  grid = std::min<int64_t>(grid, kAttnCounters / (3 - Sh::kCtasPerSm));  // two pieces per CTA and group
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
   cfg.blockDim = dim3(kAttnThreads, 1, 1);

@@ -47,6 +47,7 @@ namespace qg {
 
 constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = 32 * kAttnWarps;
+constexpr int kAttnCounters = 340;  // at most so many CTAs, with three counters each
 
 struct AttnArgs {
   const void* q;
@@ -87,7 +88,7 @@ struct AttnShape {
   static constexpr int kPiece = MR * (D + 2);                 // floats of a piece: m, l, O
   static constexpr int kCtasPerSm = D == 256 ? 1 : 2;
   static constexpr int kBudget = kCtasPerSm == 1 ? 232448 : 115712;
-  static constexpr int kStatic = 1600;  // at least the kernel's static shared memory
+  static constexpr int kStatic = 1664;  // at least the kernel's static shared memory
   static constexpr int kFixed = 1024 + kAttnWarps * kPiece * 4;
   static constexpr int kFit = (kBudget - kFixed - kStatic) / (kAttnWarps * (2 * kTile + kScaleBytes));
   static constexpr int kStages = kFit < 3 ? kFit : 3;
@@ -165,12 +166,17 @@ struct AttnPiece {
   int r, hx;
 };
 
-// The n pieces of one (request, head) that are to be joined: the CTA's own (slots: 2 warp + which, four bits
-// each; to: the workspace piece that they become, or -1), or those of n CTAs from CTA `to` on.
+// The n pieces of one (request, head) that are to be joined (r = -1: none), into workspace piece `to` or (-1) the
+// output.  The CTA's own: slots, 2 warp + which, four bits each.  In the workspace: piece `from`, then every
+// `step` from `next` on.
 struct AttnSet {
   int r, hx, n, to;
   uint32_t slots;
+  int from, next, step;
 };
+
+// More pieces than this are joined in groups first, each by the CTA that completes it.
+constexpr int kAttnJoinMax = 24, kAttnJoinGroup = 16;
 
 __device__ __forceinline__ int attn_page(const AttnArgs& p, int t) {
   return static_cast<int>(__umulhi(static_cast<uint32_t>(t), p.page_mul) >> p.page_shift);
@@ -825,22 +831,19 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
     const uint32_t out = __ballot_sync(0xffffffffu, starts && shared);
     if (starts) {
       const uint32_t next = begin & ~((2u << lane) - 1);  // its pieces end before the next set's first
-      AttnSet& t = set_of[__popc(begin & ((1u << lane) - 1))];
-      t.r = a.r;
-      t.hx = a.hx;
       uint32_t own = mask & ~((1u << lane) - 1) & (next ? (next & -next) - 1 : 0xffu), list = 0;
-      t.n = __popc(own);
+      const int n = __popc(own);
       for (int k = 0; own; own &= own - 1, k += 4) list |= static_cast<uint32_t>(__ffs(own) - 1) << k;
-      t.slots = list;
-      t.to = shared ? 2 * cta + (a.lo >= c_lo ? 1 : 0) : -1;
+      set_of[__popc(begin & ((1u << lane) - 1))] = AttnSet{a.r, a.hx, n, shared ? 2 * cta + (a.lo >= c_lo ? 1 : 0) : -1, list, 0, 0, 0};
       if (shared) shared_of[__popc(out & ((1u << lane) - 1))] = a;
     }
     if (lane == 0) set_count[0] = __popc(begin), set_count[1] = __popc(out);
   }
   __syncthreads();
   sets = set_count[0], shared_n = set_count[1];
+  // rounds: the CTA's own sets; those that it completed among the CTAs (of one group, where there are many); the groups
 #pragma unroll 1
-  for (int round = 0; round < 2; ++round) {
+  for (int round = 0;; ++round) {
     // four elements of a head per thread: D / 4 threads a head, MR heads a set
     constexpr int kPer = MR * (D / 4);
 #pragma unroll 1
@@ -852,12 +855,12 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
       if (g0 + g >= p.group || t.r < 0) continue;
       float m, l;
       auto piece = [&](int i) -> const float* {
-        if (round) return p.ws + static_cast<int64_t>(2 * (t.to + i) + (i == 0 ? 1 : 0)) * Sh::kPiece;
+        if (round) return p.ws + static_cast<int64_t>(i ? t.next + t.step * (i - 1) : t.from) * Sh::kPiece;
         const int q = t.slots >> (4 * i) & 15;
         return q & 1 ? reinterpret_cast<const float*>(ring + (q >> 1) * S * 2 * Sh::kTile) : heads_mem + (q >> 1) * Sh::kPiece;
       };
       const float4 o = attn_join<MR, D>(t.n, g, d, piece, m, l);
-      if (!round && t.to >= 0) {
+      if (t.to >= 0) {
         float* to = p.ws + static_cast<int64_t>(t.to) * Sh::kPiece;
         if (d == 0) to[g] = m, to[MR + g] = l;
         *reinterpret_cast<float4*>(to + 2 * MR + g * D + d) = o;
@@ -869,19 +872,41 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
         if (d == 0 && p.lse) p.lse[static_cast<int64_t>(t.r) * p.q_heads + kv * p.group + g0 + g] = attn_lse(m, l);
       }
     }
-    if (round || shared_n == 0) return;
+    if (round == 2 || shared_n == 0) return;
     __syncthreads();
     sets = shared_n;
+    bool again = false;
     if (static_cast<int>(threadIdx.x) < shared_n) {
       const AttnPiece a = shared_of[threadIdx.x];
       const int first = cta_of(a.lo), n = cta_of(a.hi - 1) - first + 1;
-      __threadfence();  // the CTA's pieces, which the barrier ordered before, to all CTAs
-      const bool last = atomicAdd(p.cnt + first, 1) == n - 1;
-      __threadfence();
-      if (last) p.cnt[first] = 0;  // for the next launch
-      set_of[threadIdx.x] = AttnSet{last ? a.r : -1, a.hx, n, first, 0};
+      const bool many = n > kAttnJoinMax;
+      AttnSet t = set_of[threadIdx.x];
+      if (round == 0 || (t.r >= 0 && t.to >= 0)) {  // in the second round: a group that it joined
+        // Counters: of a (request, head) at the CTA where it begins; of its groups at the CTA where they begin, the
+        // first group's apart from the others', since another's first group may begin there too.
+        const int groups = (n + kAttnJoinGroup - 1) / kAttnJoinGroup, grp = (cta - first) / kAttnJoinGroup, at = first + grp * kAttnJoinGroup;
+        const bool group = round == 0 && many;
+        int* counter = p.cnt + (group ? (grp ? 2 : 1) * kAttnCounters + at : first);
+        const int all = group ? min(kAttnJoinGroup, n - grp * kAttnJoinGroup) : many ? groups : n;
+        __threadfence();  // the CTA's pieces, which the barrier ordered before, to all CTAs
+        const bool last = atomicAdd(counter, 1) == all - 1;
+        __threadfence();
+        if (last) *counter = 0;  // for the next launch
+        const int slots = 2 * gridDim.x;  // pieces of groups come behind those of CTAs
+        t = AttnSet{last ? a.r : -1, a.hx, all, -1, 0, 0, 0, 0};
+        if (group)
+          t.to = slots + 2 * at + (grp ? 1 : 0), t.from = 2 * at + (grp ? 0 : 1), t.next = 2 * (at + 1), t.step = 2;
+        else if (many)
+          t.from = slots + 2 * first, t.next = slots + 2 * (first + kAttnJoinGroup) + 1, t.step = 2 * kAttnJoinGroup;
+        else
+          t.from = 2 * first + 1, t.next = 2 * (first + 1), t.step = 2;
+        again = last;
+      } else {
+        t.r = -1;
+      }
+      set_of[threadIdx.x] = t;
     }
-    __syncthreads();
+    if (!__syncthreads_or(again)) return;
   }
 }
 

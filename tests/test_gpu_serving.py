@@ -388,6 +388,19 @@ def test_attention_of_one_long_request_split_over_the_gpu(h):
     check_attend(got, lse, q, ref, scale)
 
 
+@pytest.mark.parametrize("lens,hq,hk,dim,typ", [([60000], 1, 1, 64, "f16"), ([90001], 8, 1, 128, "e4m3"), ([70000], 16, 1, 256, "bf16"),
+                                                ([30, 50001, 2, 40000], 4, 1, 128, "bf16"), ([9000, 9000, 9000], 16, 1, 64, "e4m3")])
+def test_attention_pieces_of_many_ctas_join_in_groups(h, lens, hq, hk, dim, typ):
+    qt = "f16" if typ == "e4m3" else typ
+    got, lse, q, ref, scale, d = attend_case(h, lens, hq, hk, dim, typ, qt, 16, seed=11)
+    check_attend(got, lse, q, ref, scale)
+    first = got.clone()
+    for _ in range(3):
+        qgemv.attn_decode(h, d)
+    torch.cuda.synchronize()
+    assert torch.equal(first, got) and qgemv.check_error(h) == qgemv.OK
+
+
 @pytest.mark.parametrize("typ,qt", [("f16", "f16"), ("bf16", "bf16"), ("e4m3", "bf16")])
 def test_attention_with_one_key_that_outweighs_the_rest(h, typ, qt):
     got, lse, q, ref, scale, _ = attend_case(h, [2000, 50], 8, 2, 128, typ, qt, 16, spike=4.0, scale=0.5)
