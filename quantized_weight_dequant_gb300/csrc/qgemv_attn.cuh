@@ -215,23 +215,12 @@ __device__ __forceinline__ float attn_lse(float m, float l) {
   return l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : __int_as_float(0xff800000);
 }
 
-// A load that sees what other CTAs published, from shared or global memory.
-__device__ __forceinline__ float4 ld_piece4(const float* q) {
-  float4 v;
-  asm volatile("ld.relaxed.gpu.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(q) : "memory");
-  return v;
-}
-__device__ __forceinline__ float ld_piece(const float* q) {
-  float v;
-  asm volatile("ld.relaxed.gpu.f32 %0, [%1];" : "=f"(v) : "l"(q) : "memory");
-  return v;
-}
-
-// Joins four elements (from d) of head g of n pieces (at piece(i): m[MR], l[MR], O[MR][D]) in their order,
-// U at a time, whose loads are all in flight together.
-template <int MR, int D, class Piece>
+// Joins four elements (from d) of head g of n pieces (at piece(i): m[MR], l[MR], O[MR][D]; SMEM: in shared
+// memory, else in the workspace, read past L1) in their order, U at a time, whose loads are all in flight
+// together.
+template <int MR, int D, bool SMEM, class Piece>
 __device__ __forceinline__ float4 attn_join(int n, int g, int d, Piece piece, float& m, float& l) {
-  constexpr int U = 8;
+  constexpr int U = SMEM ? 4 : 8;
   const float neg = __int_as_float(0xff800000);
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
   m = neg, l = 0.f;
@@ -243,9 +232,10 @@ __device__ __forceinline__ float4 attn_join(int n, int g, int d, Piece piece, fl
     for (int u = 0; u < U; ++u) {
       if (i0 + u < n) {
         const float* q = piece(i0 + u);
-        mi[u] = ld_piece(q + g);
-        li[u] = ld_piece(q + MR + g);
-        o[u] = ld_piece4(q + 2 * MR + g * D + d);
+        const float4* v = reinterpret_cast<const float4*>(q + 2 * MR + g * D + d);
+        mi[u] = SMEM ? q[g] : __ldcg(q + g);
+        li[u] = SMEM ? q[MR + g] : __ldcg(q + MR + g);
+        o[u] = SMEM ? *v : __ldcg(v);
       } else {
         mi[u] = neg;
       }
@@ -361,15 +351,18 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
       start_of[w] = AttnStart{at - in, warp_lo(w + 1) - at - max(p.seg_cost - in, 0), r, hx, max(in - p.seg_cost, 0)};
     }
   }
-  if (any_none) {
+  auto write_none = [&]() {  // the rows of requests that see no token
     for (int r = cta; r < p.requests; r += gridDim.x) {
       if (tiles_of(attn_clamp(p, p.lens[r]))) continue;
       for (int e = threadIdx.x; e < p.q_heads * (D / 2); e += kAttnThreads) attn_store2(p, r * p.out_stride + 2 * e, 0.f, 0.f);
       if (p.lse)
         for (int g = threadIdx.x; g < p.q_heads; g += kAttnThreads) p.lse[static_cast<int64_t>(r) * p.q_heads + g] = neg;
     }
+  };
+  if (!busy) {
+    if (any_none) write_none();
+    return;
   }
-  if (!busy) return;
   __syncthreads();
 
   const int quad = lane & 3, row = lane >> 2;
@@ -814,6 +807,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
       mbar_wait_bounded(full + 8 * s, 1, p.spin_ns);
     }
   }
+  if (any_none) write_none();  // while the last warps finish
   __syncthreads();
 
   // ---- join: the warps' pieces in order; those of one (request, head) follow one another and are one
@@ -854,12 +848,12 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
       attn_group<MR>(p, t.hx, kv, g0);
       if (g0 + g >= p.group || t.r < 0) continue;
       float m, l;
-      auto piece = [&](int i) -> const float* {
-        if (round) return p.ws + static_cast<int64_t>(i ? t.next + t.step * (i - 1) : t.from) * Sh::kPiece;
+      auto mine = [&](int i) -> const float* {
         const int q = t.slots >> (4 * i) & 15;
-        return q & 1 ? reinterpret_cast<const float*>(ring + (q >> 1) * S * 2 * Sh::kTile) : heads_mem + (q >> 1) * Sh::kPiece;
+        return reinterpret_cast<const float*>(q & 1 ? ring + (q >> 1) * S * 2 * Sh::kTile : reinterpret_cast<const uint8_t*>(heads_mem + (q >> 1) * Sh::kPiece));
       };
-      const float4 o = attn_join<MR, D>(t.n, g, d, piece, m, l);
+      auto theirs = [&](int i) -> const float* { return p.ws + static_cast<int64_t>(i ? t.next + t.step * (i - 1) : t.from) * Sh::kPiece; };
+      const float4 o = round ? attn_join<MR, D, false>(t.n, g, d, theirs, m, l) : attn_join<MR, D, true>(t.n, g, d, mine, m, l);
       if (t.to >= 0) {
         float* to = p.ws + static_cast<int64_t>(t.to) * Sh::kPiece;
         if (d == 0) to[g] = m, to[MR + g] = l;
