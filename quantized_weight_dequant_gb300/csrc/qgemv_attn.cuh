@@ -167,7 +167,7 @@ struct AttnPiece {
 };
 
 // The n pieces of one (request, head) that are to be joined (r = -1: none), into workspace piece `to` or (-1) the
-// output.  The CTA's own: slots, 2 warp + which, four bits each.  In the workspace: piece `from`, then every
+// output.  The CTA's own: a mask of slots 2 warp + which.  In the workspace: piece `from`, then every
 // `step` from `next` on.
 struct AttnSet {
   int r, hx, n, to;
@@ -213,6 +213,12 @@ __device__ __forceinline__ void attn_store2(const AttnArgs& p, int64_t at, float
 
 __device__ __forceinline__ float attn_lse(float m, float l) {
   return l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : __int_as_float(0xff800000);
+}
+
+__device__ __forceinline__ int atom_add_acq_rel(int* p, int v) {
+  int old;
+  asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
+  return old;
 }
 
 // Joins four elements (from d) of head g of n pieces (at piece(i): m[MR], l[MR], O[MR][D]; SMEM: in shared
@@ -825,10 +831,8 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
     const uint32_t out = __ballot_sync(0xffffffffu, starts && shared);
     if (starts) {
       const uint32_t next = begin & ~((2u << lane) - 1);  // its pieces end before the next set's first
-      uint32_t own = mask & ~((1u << lane) - 1) & (next ? (next & -next) - 1 : 0xffu), list = 0;
-      const int n = __popc(own);
-      for (int k = 0; own; own &= own - 1, k += 4) list |= static_cast<uint32_t>(__ffs(own) - 1) << k;
-      set_of[__popc(begin & ((1u << lane) - 1))] = AttnSet{a.r, a.hx, n, shared ? 2 * cta + (a.lo >= c_lo ? 1 : 0) : -1, list, 0, 0, 0};
+      const uint32_t own = mask & ~((1u << lane) - 1) & (next ? (next & -next) - 1 : 0xffu);
+      set_of[__popc(begin & ((1u << lane) - 1))] = AttnSet{a.r, a.hx, __popc(own), shared ? 2 * cta + (a.lo >= c_lo ? 1 : 0) : -1, own, 0, 0, 0};
       if (shared) shared_of[__popc(out & ((1u << lane) - 1))] = a;
     }
     if (lane == 0) set_count[0] = __popc(begin), set_count[1] = __popc(out);
@@ -848,8 +852,10 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
       attn_group<MR>(p, t.hx, kv, g0);
       if (g0 + g >= p.group || t.r < 0) continue;
       float m, l;
-      auto mine = [&](int i) -> const float* {
-        const int q = t.slots >> (4 * i) & 15;
+      uint32_t slots = t.slots;
+      auto mine = [&](int) -> const float* {  // they are asked for in order
+        const int q = __ffs(slots) - 1;
+        slots &= slots - 1;
         return reinterpret_cast<const float*>(q & 1 ? ring + (q >> 1) * S * 2 * Sh::kTile : reinterpret_cast<const uint8_t*>(heads_mem + (q >> 1) * Sh::kPiece));
       };
       auto theirs = [&](int i) -> const float* { return p.ws + static_cast<int64_t>(i ? t.next + t.step * (i - 1) : t.from) * Sh::kPiece; };
@@ -882,9 +888,8 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
         const bool group = round == 0 && many;
         int* counter = p.cnt + (group ? (grp ? 2 : 1) * kAttnCounters + at : first);
         const int all = group ? min(kAttnJoinGroup, n - grp * kAttnJoinGroup) : many ? groups : n;
-        __threadfence();  // the CTA's pieces, which the barrier ordered before, to all CTAs
-        const bool last = atomicAdd(counter, 1) == all - 1;
-        __threadfence();
+        // releases the CTA's pieces, which the barrier ordered before, and acquires the others'
+        const bool last = atom_add_acq_rel(counter, 1) == all - 1;
         if (last) *counter = 0;  // for the next launch
         const int slots = 2 * gridDim.x;  // pieces of groups come behind those of CTAs
         t = AttnSet{last ? a.r : -1, a.hx, all, -1, 0, 0, 0, 0};
