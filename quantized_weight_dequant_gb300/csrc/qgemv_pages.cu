@@ -14,13 +14,18 @@ namespace {
 
 qgemv_status_t launched() { return cudaGetLastError() == cudaSuccess ? QGEMV_OK : QGEMV_ERR_CUDA; }
 
-template <int T>
+template <int T, bool INTER>
 void launch_store(const qgemv_kv_store_t& p, dim3 g, int threads, int* err, cudaStream_t s) {
   switch (p.cache.head_dim) {
-    case 64: kv_store_kernel<T, 64><<<g, threads, 0, s>>>(p, err); break;
-    case 128: kv_store_kernel<T, 128><<<g, threads, 0, s>>>(p, err); break;
-    default: kv_store_kernel<T, 256><<<g, threads, 0, s>>>(p, err); break;
+    case 64: kv_store_kernel<T, 64, INTER><<<g, threads, 0, s>>>(p, err); break;
+    case 128: kv_store_kernel<T, 128, INTER><<<g, threads, 0, s>>>(p, err); break;
+    default: kv_store_kernel<T, 256, INTER><<<g, threads, 0, s>>>(p, err); break;
   }
+}
+
+template <int T>
+void launch_store(const qgemv_kv_store_t& p, dim3 g, int threads, int* err, cudaStream_t s) {
+  p.interleaved ? launch_store<T, true>(p, g, threads, err, s) : launch_store<T, false>(p, g, threads, err, s);
 }
 
 }  // namespace

@@ -228,8 +228,8 @@ __device__ __forceinline__ uint4 pack8(int type, const float (&v)[8]) {
 // reads of kU heads are in flight together, and the first of them before slot and position are known.
 constexpr int kStoreThreads = 256;
 
-template <int T, int D>
-__global__ void __launch_bounds__(kStoreThreads, T == QGEMV_OUT_F32 ? 3 : 4) kv_store_kernel(const __grid_constant__ qgemv_kv_store_t p, int* err) {
+template <int T, int D, bool INTER>  // INTER: pairs of neighbours
+__global__ void __launch_bounds__(kStoreThreads, T == QGEMV_OUT_F32 ? 3 : INTER ? 5 : 4) kv_store_kernel(const __grid_constant__ qgemv_kv_store_t p, int* err) {
   constexpr int L = D / 8;  // threads per head
   constexpr int kU = T == QGEMV_OUT_F32 ? 2 : 3;
   const int hq = p.q_out ? p.q_heads : 0, hk = p.cache.kv_heads;
@@ -246,7 +246,6 @@ __global__ void __launch_bounds__(kStoreThreads, T == QGEMV_OUT_F32 ? 3 : 4) kv_
   const uint8_t* q_at = static_cast<const uint8_t*>(p.q) + (t * p.q_stride + d) * kEl;
   const uint8_t* k_at = static_cast<const uint8_t*>(p.k) + (t * p.k_stride + d) * kEl - hq * (D * kEl);
   const uint8_t* v_at = static_cast<const uint8_t*>(p.v) + (t * p.v_stride + d) * kEl - (hq + hk) * (D * kEl);
-  const bool pairs = turns && !p.interleaved;
   const int to_mate = (mate - d) * kEl;
   Raw8<T> v[kU], o[kU];
   auto read = [&](int h0) {
@@ -256,7 +255,7 @@ __global__ void __launch_bounds__(kStoreThreads, T == QGEMV_OUT_F32 ? 3 : 4) kv_
       if (head >= heads) break;
       const uint8_t* at = (head < hq ? q_at : head < hq + hk ? k_at : v_at) + head * (D * kEl);
       v[u] = load_raw<T>(at);
-      if (pairs && head < hq + hk) o[u] = load_raw<T>(at + to_mate);
+      if (!INTER && turns && head < hq + hk) o[u] = load_raw<T>(at + to_mate);
     }
   };
   const int h_first = static_cast<int>(blockIdx.y * blockDim.x + threadIdx.x) / L;
@@ -274,10 +273,10 @@ __global__ void __launch_bounds__(kStoreThreads, T == QGEMV_OUT_F32 ? 3 : 4) kv_
   bool lost = pos != -1 && p.rope && (pos < 0 || pos >= p.rope_positions);
   if (threadIdx.x == 0 && blockIdx.y == 0 && (lost || (!stored && slot != -1))) atomicOr(err, kDevErrIndex);
   if (lost) pos = -1;
-  float c[8], s[8];
+  float c[INTER ? 4 : 8], s[INTER ? 4 : 8];
   if (turns && pos >= 0) {
     const float* tab = p.rope + static_cast<int64_t>(pos) * p.rot_dim;
-    if (p.interleaved) {
+    if constexpr (INTER) {
       const float4 a = *reinterpret_cast<const float4*>(tab + d / 2), b = *reinterpret_cast<const float4*>(tab + half + d / 2);
       c[0] = a.x, c[1] = a.y, c[2] = a.z, c[3] = a.w, s[0] = b.x, s[1] = b.y, s[2] = b.z, s[3] = b.w;
     } else {
@@ -296,7 +295,7 @@ __global__ void __launch_bounds__(kStoreThreads, T == QGEMV_OUT_F32 ? 3 : 4) kv_
       float x[8];
       to_float<T>(v[u], x);
       if (turns && pos >= 0 && head < hq + hk) {
-        if (p.interleaved) {
+        if constexpr (INTER) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const float a = x[2 * j], b = x[2 * j + 1];
