@@ -226,10 +226,10 @@ __device__ __forceinline__ uint4 pack8(int type, const float (&v)[8]) {
 // A CTA (or gridDim.y, where tokens are few) per token: the D / 8 threads of a head are neighbours in a warp and take the token's heads (q, then
 // k, then v) in turn, so that slot, position and angles are read once.  Bound by the bytes of q, k and v: the
 // reads of kU heads are in flight together, and the first of them before slot and position are known.
-constexpr int kStoreThreads = 256;
+constexpr int kStoreThreads = 128;
 
 template <int T, int D, bool INTER>  // INTER: pairs of neighbours
-__global__ void __launch_bounds__(kStoreThreads, T == QGEMV_OUT_F32 ? 3 : INTER ? 5 : 4) kv_store_kernel(const __grid_constant__ qgemv_kv_store_t p, int* err) {
+__global__ void __launch_bounds__(kStoreThreads, T == QGEMV_OUT_F32 ? 6 : 8) kv_store_kernel(const __grid_constant__ qgemv_kv_store_t p, int* err) {
   constexpr int L = D / 8;  // threads per head
   constexpr int kU = T == QGEMV_OUT_F32 ? 2 : 3;
   const int hq = p.q_out ? p.q_heads : 0, hk = p.cache.kv_heads;
