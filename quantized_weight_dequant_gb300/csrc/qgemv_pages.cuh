@@ -65,24 +65,31 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const qgemv_pag
   __shared__ int64_t ws[2][32];
   const int tid = threadIdx.x;
   int64_t n_kept = 0, n_got = 0, n_missing = 0;  // of this thread's requests
+  __shared__ unsigned long long sums[3];
+  if (tid < 3) sums[tid] = 0;
   const int64_t t0 = blockIdx.x * per_cta, t1 = min(t0 + per_cta, p.capacity);
   const int64_t P = p.page_size, room_all = min(static_cast<int64_t>(p.table_width) * P, int64_t{0x7fffffff});
   const int64_t F = max(*p.free_count, 0);
   int64_t tok = 0, pages = 0;  // carried over the scan steps
+  // pages of n tokens: n, like every position, is below 2^31
+  auto pages_of = [&](int64_t n) { return static_cast<int64_t>((static_cast<uint32_t>(n) + static_cast<uint32_t>(p.page_size) - 1) / static_cast<uint32_t>(p.page_size)); };
+  int next_c = tid < p.requests ? p.cached[tid] : 0, next_f = tid < p.requests ? p.fresh[tid] : 0;
   for (int r0 = 0; r0 < p.requests; r0 += blockDim.x) {
     const int r = r0 + tid;
-    int64_t c = 0, f = 0;
-    if (r < p.requests) c = max(p.cached[r], 0), f = max(p.fresh[r], 0);
+    const int64_t c = max(next_c, 0), f = max(next_f, 0);
+    const int r_next = r + static_cast<int>(blockDim.x);  // read while this step is worked on
+    next_c = r_next < p.requests ? p.cached[r_next] : 0;
+    next_f = r_next < p.requests ? p.fresh[r_next] : 0;
     const int64_t room = min(f, max(room_all - c, int64_t{0}));
-    const int64_t have = (c + P - 1) / P;
-    const int64_t need = room > 0 ? (c + room + P - 1) / P - have : 0;
+    const int64_t have = pages_of(c);
+    const int64_t need = room > 0 ? pages_of(c + room) - have : 0;
     int64_t off, base, dt, dp;
     block_scan2(f, need, off, base, dt, dp, ws);
     off += tok;
     base += pages;
     // what the capacity and the stack leave of it
     const int64_t f1 = min(room, max(p.capacity - off, int64_t{0}));
-    const int64_t need1 = f1 > 0 ? (c + f1 + P - 1) / P - have : 0;
+    const int64_t need1 = f1 == room ? need : f1 > 0 ? pages_of(c + f1) - have : 0;
     const int64_t got = min(need1, max(F - base, int64_t{0}));
     const int64_t kept = got < need1 ? (have + got) * P - c : f1;
     item[tid] = PlanItem{off, base, static_cast<int32_t>(c), static_cast<int32_t>(kept), static_cast<int32_t>(have)};
@@ -159,17 +166,20 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const qgemv_pag
     if (p.owners) p.owners[t] = -1;
   }
   if (blockIdx.x == 0) {  // the totals
-    int64_t e0, e1, kept, got, missing, unused;
-    block_scan2(n_kept, n_got, e0, e1, kept, got, ws);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+      n_kept += __shfl_xor_sync(0xffffffffu, n_kept, d);
+      n_got += __shfl_xor_sync(0xffffffffu, n_got, d);
+      n_missing += __shfl_xor_sync(0xffffffffu, n_missing, d);
+    }
+    __syncthreads();  // the sums' zeros
+    if (tid % 32 == 0) atomicAdd(&sums[0], static_cast<unsigned long long>(n_kept)), atomicAdd(&sums[1], static_cast<unsigned long long>(n_got)), atomicAdd(&sums[2], static_cast<unsigned long long>(n_missing));
     __syncthreads();
-    block_scan2(n_missing, 0, e0, e1, missing, unused, ws);
     if (tid == 0) {
       if (p.offsets) p.offsets[p.requests] = sat32(tok);
       p.counts[0] = sat32(tok);
-      p.counts[1] = sat32(kept);
-      p.counts[2] = sat32(got);
-      p.counts[3] = sat32(missing);
     }
+    if (tid < 3) p.counts[1 + tid] = sat32(static_cast<int64_t>(sums[tid]));
   }
 }
 
