@@ -26,8 +26,8 @@
 //    most 8 heads in a group the low parts are rows 8..15 of the same instruction, which would
 //    be empty otherwise; with 9..16 they are a second instruction.
 //  * 8-bit caches: codes are converted to fp16 in registers (exactly); key scales multiply the
-//    scores, value scales the weights.  The weights are kept within fp16's range by a running
-//    factor c (out = c O): it follows the largest w_t = p_t vscale_t like m follows the scores.
+//    scores, value scales the weights.  There m follows the largest s_t log2e + log2 vscale_t, so that the
+//    weights p_t vscale_t end at 1 and fp16 holds them whatever the scales; l is counted from the same m.
 //  * Join.  A (request, head) that lies inside one warp's share is written by that warp.
 //    Others leave (m, l, O) pieces: in shared memory, which the CTA joins in token order, and
 //    where CTAs share one in the workspace, which the CTA that arrives last joins in CTA order.
@@ -115,11 +115,14 @@ __device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t (&v)[4]) {
                : "memory");
 }
 
-// Two e4m3 codes as fp16 (exact).
-__device__ __forceinline__ uint32_t e4m3x2(uint32_t two) {
-  uint32_t u;
-  asm("{.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(u) : "r"(two));
-  return u;
+// Four e4m3 codes as two fp16 pairs (exact).
+__device__ __forceinline__ void e4m3x4(uint32_t four, uint32_t& lo, uint32_t& hi) {
+  asm("{.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}" : "=r"(lo), "=r"(hi) : "r"(four));
+}
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 // True in one lane of the (whole) warp.
@@ -492,9 +495,9 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
 
   constexpr int KS = D / 16;  // k steps of the scores
   uint32_t qa[KS][MR == 8 ? 2 : 4];
-  float q_back[2] = {1.f, 1.f};  // what the fp16 queries of rows `row`, `row` + 8 were divided by
+  float q_scale[2];  // scale_log2 times what the fp16 queries of rows `row`, `row` + 8 were divided by
   float o[OT][4];
-  float m[2] = {neg, neg}, l[2] = {0.f, 0.f}, c[2] = {1.f, 1.f};
+  float m[2] = {neg, neg}, l[2] = {0.f, 0.f};
 
   // Query rows `row` (and `row` + 8) of a group in the order of the matrix product's A operand, requested
   // before the tile that needs them.
@@ -523,6 +526,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
 #pragma unroll
     for (int j = 0; j < MR / 8; ++j) {
       uint32_t(&u)[KS][2] = qn[j];
+      q_scale[j] = p.scale_log2;
       if (kF8 && p.type == QGEMV_OUT_BF16) {
         // bf16 queries as fp16 times a power of two per head: the largest in [2^14, 2^15), so every
         // one within 2^28 of it is exact
@@ -540,7 +544,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
         // 2^(141 - ex) takes 1.x 2^(ex - 127) to 1.x 2^14; both factors stay normal for 15 <= ex <= 254
         const bool fine = ex >= 15 && ex < 255;
         const float by = fine ? __int_as_float((127 + 141 - ex) << 23) : 1.f;
-        q_back[j] = fine ? __int_as_float((127 - 141 + ex) << 23) : 1.f;
+        if (fine) q_scale[j] *= __int_as_float((127 - 141 + ex) << 23);
 #pragma unroll
         for (int k = 0; k < KS; ++k)
 #pragma unroll
@@ -572,7 +576,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
     for (int j = 0; j < MR / 8; ++j) {
       const int g = row + 8 * j;
       const bool there = g0 + g < p.group;
-      const float f = (whole ? (l[j] != 0.f ? 1.f / l[j] : 0.f) : 1.f) * (kF8 ? c[j] : 1.f);
+      const float f = whole ? (l[j] != 0.f ? 1.f / l[j] : 0.f) : 1.f;
       if (quad == 0) {
         if (!whole)
           piece[g] = m[j], piece[MR + g] = l[j];
@@ -638,7 +642,6 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
       for (int t = 0; t < OT; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
       m[0] = m[1] = neg;
       l[0] = l[1] = 0.f;
-      c[0] = c[1] = 0.f;
     }
     const bool last = d.ends & 4;
     const int s_next = s + 1 == S ? 0 : s + 1;
@@ -666,7 +669,8 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
         for (int e = 0; e < (kF8 ? 2 : 1); ++e) {
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
-            const uint32_t u = w[2 * n + e], b0 = kF8 ? e4m3x2(u & 0xffffu) : w[2 * n], b1 = kF8 ? e4m3x2(u >> 16) : w[2 * n + 1];
+            uint32_t b0 = w[2 * n], b1 = w[2 * n + 1];
+            if constexpr (kF8) e4m3x4(w[2 * n + e], b0, b1);
             if constexpr (MR == 8)
               mma16816<kBF>(sc[2 * b + n], qa[k + e][0], 0u, qa[k + e][1], 0u, b0, b1);
             else
@@ -685,12 +689,11 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
         const uint32_t sa = scale_w + s * Sh::kScaleBytes + (8 * t + 2 * quad) * 4;
         asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(ks.x), "=f"(ks.y) : "r"(sa));
         asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(vsc[t].x), "=f"(vsc[t].y) : "r"(sa + TT * 4));
-        ks.x *= p.scale_log2, ks.y *= p.scale_log2;
       }
 #pragma unroll
       for (int j = 0; j < MR / 8; ++j) {
-        sc[t][2 * j] *= kF8 ? ks.x * q_back[j] : ks.x;
-        sc[t][2 * j + 1] *= kF8 ? ks.y * q_back[j] : ks.y;
+        sc[t][2 * j] *= kF8 ? ks.x * q_scale[j] : ks.x;
+        sc[t][2 * j + 1] *= kF8 ? ks.y * q_scale[j] : ks.y;
       }
       if (edge) {
 #pragma unroll
@@ -702,8 +705,10 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
           }
         }
       }
+      // where a scale is below 2^-100 its weights are smaller than they might be, and l still far from its end
+      const float2 up = kF8 ? make_float2(fmaxf(lg2(fabsf(vsc[t].x)), -100.f), fmaxf(lg2(fabsf(vsc[t].y)), -100.f)) : make_float2(0.f, 0.f);
 #pragma unroll
-      for (int j = 0; j < MR / 8; ++j) top[j] = fmaxf(top[j], fmaxf(sc[t][2 * j], sc[t][2 * j + 1]));
+      for (int j = 0; j < MR / 8; ++j) top[j] = fmaxf(top[j], kF8 ? fmaxf(sc[t][2 * j] + up.x, sc[t][2 * j + 1] + up.y) : fmaxf(sc[t][2 * j], sc[t][2 * j + 1]));
     }
     bool moved = false;
     float keep[2] = {1.f, 1.f};
@@ -716,35 +721,14 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
       moved |= mn > m[j];
       m[j] = mn;
       l[j] *= keep[j];
-      float largest = 0.f;
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        float a = ex2(sc[t][2 * j] - base), b = ex2(sc[t][2 * j + 1] - base);
+        const float a = ex2(sc[t][2 * j] - base), b = ex2(sc[t][2 * j + 1] - base);
         l[j] += a + b;
-        if constexpr (kF8) {
-          a *= vsc[t].x, b *= vsc[t].y;
-          largest = fmaxf(largest, fmaxf(fabsf(a), fabsf(b)));
-        }
-        sc[t][2 * j] = a;
-        sc[t][2 * j + 1] = b;
-      }
-      if constexpr (kF8) {
-        // out = c O: c takes the change of m; O is scaled only when the weights outgrow it
-        largest = fmaxf(largest, __shfl_xor_sync(0xffffffffu, largest, 1));
-        largest = fmaxf(largest, __shfl_xor_sync(0xffffffffu, largest, 2));
-        c[j] *= keep[j];
-        keep[j] = 1.f;
-        if (largest > c[j]) {
-          const float cn = __int_as_float((__float_as_int(largest) & 0x7f800000) + 0x00800000);  // the power of two above
-          keep[j] = c[j] / cn;
-          c[j] = cn;
-        }
-        const float inv = c[j] > 0.f ? 1.f / c[j] : 0.f;
-#pragma unroll
-        for (int t = 0; t < NT; ++t) sc[t][2 * j] *= inv, sc[t][2 * j + 1] *= inv;
+        sc[t][2 * j] = kF8 ? a * vsc[t].x : a;
+        sc[t][2 * j + 1] = kF8 ? b * vsc[t].y : b;
       }
     }
-    if constexpr (kF8) moved = keep[0] != 1.f || (MR == 16 && keep[1] != 1.f);
     if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
       for (int t = 0; t < OT; ++t) {
@@ -791,9 +775,11 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
             // bytes: token a (even, odd element), token a + 1 (even, odd element)
-            const uint32_t x = __byte_perm(w[2 * n], 0, 0x3120), y = __byte_perm(w[2 * n + 1], 0, 0x3120);
-            add(o[2 * (u + n)], e4m3x2(x & 0xffffu), e4m3x2(y & 0xffffu));
-            add(o[2 * (u + n) + 1], e4m3x2(x >> 16), e4m3x2(y >> 16));
+            uint32_t x0, x1, y0, y1;
+            e4m3x4(__byte_perm(w[2 * n], 0, 0x3120), x0, x1);
+            e4m3x4(__byte_perm(w[2 * n + 1], 0, 0x3120), y0, y1);
+            add(o[2 * (u + n)], x0, y0);
+            add(o[2 * (u + n) + 1], x1, y1);
           }
         }
       }
