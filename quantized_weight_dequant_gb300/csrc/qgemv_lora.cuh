@@ -61,13 +61,26 @@ template <int TG>
 struct LoraSmem {
   float own[8 * TG][kLoraLd];                                             // this CTA's sums over its part of K
   float part[kLoraWarps][8 * TG][16 * LoraShape<TG>::kRT + 4];            // those of a warp
-  int row[kLoraChunk];                                                    // rows of the adapter in hand
 };
 
-// The distinct adapters among the kLoraChunk rows from m0 on, found by one warp: rows_of[i] is the mask of
-// the rows of the i-th, in order of first appearance (those without one among them).  Returns their number.
-__device__ __forceinline__ int lora_distinct(const qgemv_lora_t& p, int64_t m0, uint32_t* rows_of, int* err) {
+// The rows of one adapter among kLoraChunk neighbouring ones: n of them, from `first` on in the chunk's list.
+struct LoraGroup {
+  int n, first, adapter, rank;  // rank 0: no adapter, or one of rank 0
+};
+struct LoraChunk {
+  LoraGroup group[kLoraChunk];  // in order of first appearance
+  int row[kLoraChunk];          // rows, group by group
+  int count;
+};
+
+__device__ __forceinline__ int lora_rank(const qgemv_lora_t& p, int a) {
+  return a < 0 ? 0 : p.ranks ? min(max(p.ranks[a], 0), p.rank) : p.rank;
+}
+
+// Groups the rows from m0 on by their adapters (one warp; every lane asks for its own row's adapter and rank).
+__device__ __forceinline__ void lora_groups(const qgemv_lora_t& p, int64_t m0, LoraChunk& out, int* err) {
   const int lane = threadIdx.x & 31;
+  const uint32_t before = (1u << lane) - 1;
   int id = -2;  // past the rows
   if (m0 + lane < p.rows) {
     id = p.ids[m0 + lane];
@@ -76,18 +89,22 @@ __device__ __forceinline__ int lora_distinct(const qgemv_lora_t& p, int64_t m0, 
       id = -1;
     }
   }
+  const int r = lora_rank(p, id);
   const uint32_t same = __match_any_sync(0xffffffffu, id);
-  const bool first = id != -2 && __ffs(same) - 1 == lane;
-  const uint32_t firsts = __ballot_sync(0xffffffffu, first);
-  if (first) rows_of[__popc(firsts & ((1u << lane) - 1))] = same;
-  return __popc(firsts);
-}
-__device__ __forceinline__ int lora_adapter(const qgemv_lora_t& p, int64_t m) {
-  const int id = p.ids[m];
-  return id >= 0 && id < p.adapters ? id : -1;
-}
-__device__ __forceinline__ int lora_rank(const qgemv_lora_t& p, int a) {
-  return a < 0 ? 0 : p.ranks ? min(max(p.ranks[a], 0), p.rank) : p.rank;
+  const int leader = __ffs(same) - 1;
+  const bool leads = id != -2 && leader == lane;
+  const int n = leads ? __popc(same) : 0;
+  int upto = n;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += u;
+  }
+  const int first = __shfl_sync(0xffffffffu, upto - n, leader);
+  if (id != -2) out.row[first + __popc(same & before)] = static_cast<int>(m0) + lane;
+  const uint32_t leaders = __ballot_sync(0xffffffffu, leads);
+  if (leads) out.group[__popc(leaders & before)] = LoraGroup{n, first, id, r};
+  if (lane == 0) out.count = __popc(leaders);
 }
 
 __device__ __forceinline__ float4 cluster_ld4(uint32_t a, uint32_t rank) {
@@ -237,32 +254,26 @@ __global__ void __launch_bounds__(kLoraThreads, 4) lora_sums_kernel(const __grid
   using Sh = LoraShape<TG>;
   constexpr int kParts = lora_parts(BF);
   __shared__ __align__(16) LoraSmem<TG> sm;
-  __shared__ uint32_t rows_of[32];
-  __shared__ int count;
+  __shared__ LoraChunk chunk;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rank = static_cast<int>(blockIdx.x) % kLoraCluster, cluster = static_cast<int>(blockIdx.x) / kLoraCluster;
   const int slot = cluster % slots;
-  const int64_t m0 = static_cast<int64_t>(cluster / slots) * kLoraChunk;
   pdl_launch_dependents();  // the second launch may start; it waits for this one's end before it reads the sums
-  if (warp == 0) {
-    const int n = lora_distinct(p, m0, rows_of, slot == 0 && rank == 0 ? err : nullptr);
-    if (lane == 0) count = n;
-  }
+  if (warp == 0) lora_groups(p, static_cast<int64_t>(cluster / slots) * kLoraChunk, chunk, slot == 0 && rank == 0 ? err : nullptr);
   __syncthreads();
   const int64_t blocks = (p.K + 31) / 32;
   const int64_t b0 = blocks * rank / kLoraCluster, b1 = blocks * (rank + 1) / kLoraCluster;
-  for (int i = slot; i < count; i += slots) {
-    const uint32_t mask = rows_of[i];
-    const int n_tok = __popc(mask), a = lora_adapter(p, m0 + __ffs(mask) - 1), r = lora_rank(p, a);
-    if (rank == 0 && warp == 0 && (mask >> lane & 1)) work.adapter[m0 + lane] = r ? a : -1;
+  for (int i = slot; i < chunk.count; i += slots) {
+    const LoraGroup group = chunk.group[i];
+    const int n_tok = group.n, a = group.adapter, r = group.rank;
+    const int* all = chunk.row + group.first;
+    if (rank == 0 && static_cast<int>(threadIdx.x) < n_tok) work.adapter[all[threadIdx.x]] = r ? a : -1;
     if (r == 0) continue;
     const float scale = p.scales ? p.scales[a] : 1.f;
-    if (warp == 0 && (mask >> lane & 1)) sm.row[__popc(mask & ((1u << lane) - 1))] = static_cast<int>(m0) + lane;
-    __syncthreads();
     const uint16_t* A = static_cast<const uint16_t*>(p.A) + static_cast<int64_t>(a) * p.rank * p.K;
     for (int k0 = 0; k0 < n_tok; k0 += Sh::kTokens) {  // up to kTokens of its rows at a time
       const int n = min(n_tok - k0, Sh::kTokens);
-      for (int j = 0; j < r; j += 16 * Sh::kRT) lora_shrink<BF, TG>(p, sm, sm.row + k0, A, r, j, n, b0, b1);
+      for (int j = 0; j < r; j += 16 * Sh::kRT) lora_shrink<BF, TG>(p, sm, all + k0, A, r, j, n, b0, b1);
       cluster_arrive();
       cluster_wait();
       // a warp per token of this CTA, four ranks a lane
@@ -288,7 +299,7 @@ __global__ void __launch_bounds__(kLoraThreads, 4) lora_sums_kernel(const __grid
             back = __int_as_float((127 - 141 + ex) << 23);
           }
         }
-        const int64_t m = sm.row[k0 + tok];
+        const int64_t m = all[k0 + tok];
         if (lane < 8 * work.blocks) {
           uint2* to = reinterpret_cast<uint2*>(work.parts + (m * work.blocks + lane / 8) * (4 * kParts) + lane % 8 / 2) + lane % 2;
 #pragma unroll
@@ -306,7 +317,6 @@ __global__ void __launch_bounds__(kLoraThreads, 4) lora_sums_kernel(const __grid
       cluster_arrive();
       cluster_wait();  // no CTA reads this one's sums: they are used again, or the CTA ends
     }
-    __syncthreads();
   }
 }
 
@@ -322,7 +332,6 @@ struct LoraFewSmem {
   uint4 ring[kLoraWarps][kLoraDepth][kLoraPieces][32];
   uint4 parts[kLoraMaxRank / 32][3][32];  // of the tokens in hand, as a lane's operand
   float factor[8];
-  int row[32];
 };
 
 template <bool BF, int OUT>
@@ -439,41 +448,34 @@ __global__ void __launch_bounds__(kLoraThreads, 4) lora_few_kernel(const __grid_
   constexpr int kParts = lora_parts(BF);
   extern __shared__ __align__(16) uint8_t dyn[];
   LoraFewSmem& sm = *reinterpret_cast<LoraFewSmem*>(dyn);
-  __shared__ uint32_t rows_of[32];
-  __shared__ int count;
+  __shared__ LoraChunk chunk;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
   const int share = static_cast<int>(blockIdx.x) % shares, slot = static_cast<int>(blockIdx.x) / shares % slots;
-  const int64_t m0 = static_cast<int64_t>(static_cast<int>(blockIdx.x) / shares / slots) * 32;
-  if (warp == 0) {
-    const int n = lora_distinct(p, m0, rows_of, nullptr);
-    if (lane == 0) count = n;
-  }
+  if (warp == 0) lora_groups(p, static_cast<int64_t>(static_cast<int>(blockIdx.x) / shares / slots) * kLoraChunk, chunk, nullptr);
   __syncthreads();
   const int64_t tiles = (p.N + 31) / 32;
   const int t0 = static_cast<int>(tiles * share / shares), t1 = static_cast<int>(tiles * (share + 1) / shares);
   bool waited = false;
-  for (int i = slot; i < count; i += slots) {
-    const uint32_t mask = rows_of[i];
-    const int n_tok = __popc(mask), a = lora_adapter(p, m0 + __ffs(mask) - 1), r = lora_rank(p, a);
-    if (warp == 0 && (mask >> lane & 1)) sm.row[__popc(mask & ((1u << lane) - 1))] = static_cast<int>(m0) + lane;
-    __syncthreads();
+  for (int i = slot; i < chunk.count; i += slots) {
+    const LoraGroup group = chunk.group[i];
+    const int n_tok = group.n, a = group.adapter, r = group.rank;
+    const int* all = chunk.row + group.first;
     if (r == 0) {  // no adapter: the base itself
       if (p.base != p.y) {
         const bool vec = p.y_stride % 4 == 0;
         for (int t = 0; t < n_tok; ++t)
           for (int64_t n = int64_t{32} * t0 + 4 * threadIdx.x; n < min(int64_t{32} * t1, p.N); n += 4 * kLoraThreads) {
-            const int64_t at = sm.row[t] * p.y_stride + n;
+            const int64_t at = all[t] * p.y_stride + n;
             const int left = static_cast<int>(min(p.N - n, int64_t{4}));
             lora_store4<OUT>(p.y, at, left, vec, p.base ? lora_load4<OUT>(p.base, at, left, vec) : make_float4(0.f, 0.f, 0.f, 0.f));
           }
       }
-      __syncthreads();
       continue;
     }
     const uint16_t* B = static_cast<const uint16_t*>(p.B) + static_cast<int64_t>(a) * p.N * p.rank;
     for (int k0 = 0; k0 < n_tok; k0 += 8) {
       const int n = min(n_tok - k0, 8);
-      LoraStream<BF, OUT> stream(p, sm, sm.row + k0, B, r, n, t0, t1);
+      LoraStream<BF, OUT> stream(p, sm, all + k0, B, r, n, t0, t1);
       stream.begin();
       if (!waited) pdl_wait();  // for the sums
       waited = true;
@@ -481,10 +483,10 @@ __global__ void __launch_bounds__(kLoraThreads, 4) lora_few_kernel(const __grid_
       for (int q = warp; q < blocks * kParts; q += kLoraWarps) {
         const int b = q / kParts, part = q - b * kParts;
         uint4 v = make_uint4(0, 0, 0, 0);
-        if (g < n) v = __ldcg(work.parts + (static_cast<int64_t>(sm.row[k0 + g]) * work.blocks + b) * (4 * kParts) + part * 4 + c);
+        if (g < n) v = __ldcg(work.parts + (static_cast<int64_t>(all[k0 + g]) * work.blocks + b) * (4 * kParts) + part * 4 + c);
         sm.parts[b][part][lane] = v;
       }
-      if (threadIdx.x < 8) sm.factor[threadIdx.x] = static_cast<int>(threadIdx.x) < n ? __ldcg(work.factor + sm.row[k0 + threadIdx.x]) : 0.f;
+      if (threadIdx.x < 8) sm.factor[threadIdx.x] = static_cast<int>(threadIdx.x) < n ? __ldcg(work.factor + all[k0 + threadIdx.x]) : 0.f;
       __syncthreads();
       stream.run(t0);
       __syncthreads();
