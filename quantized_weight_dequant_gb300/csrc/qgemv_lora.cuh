@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(kLoraThreads, 4) lora_sums_kernel(const __grid
 // with a tile's first block, the base of its outputs.  Lane (g, c), half k of a tile (16 rows): rows
 // 4 (g / 2) + g % 2 and two further; outputs 4 c .. 4 c + 3 of token g.  The tokens are the instruction's first
 // eight rows, and their second parts the other eight (the third of bf16 another instruction).
-constexpr int kLoraDepth = 3;   // stages of a lane's ring
+constexpr int kLoraDepth = 2;   // stages of a lane's ring
 constexpr int kLoraPieces = 6;  // 16-byte pieces of a stage
 
 struct LoraFewSmem {
