@@ -414,6 +414,38 @@ def test_attention_with_large_bf16_queries_over_an_8_bit_cache(h):
     check_attend(got, lse, q, ref, scale)
 
 
+@pytest.mark.parametrize("order", [1, -1])
+def test_attention_over_value_scales_of_very_different_size(h, order):
+    """Tokens whose values are 2^60 apart, the small ones with the larger scores or the other way round: the
+    weights keep their precision against the largest contribution."""
+    g = gen(21)
+    n, page, dim = 200, 16, 64
+    kc, vc, ks, vs = make_cache(g, "e4m3", 13, 1, page, dim)
+    k, v = ((randn(g, n, dim) * 100).clamp(-440, 440).to(F8) for _ in range(2))
+    sk = torch.full((n,), 0.01, device="cuda")
+    size = torch.linspace(-50, 10, n, device="cuda")
+    sv = torch.exp2(size * order if order > 0 else size.flip(0)).contiguous()
+    t = torch.arange(n, device="cuda")
+    kc[t // page, 0, t % page], vc[t // page, 0, t % page] = k.view(torch.uint8), v.view(torch.uint8)
+    ks[t // page, 0, t % page], vs[t // page, 0, t % page] = sk, sv
+    q = (randn(g, 1, 4, dim) * 3).half()
+    out, lse = torch.empty_like(q), torch.empty(1, 4, device="cuda")
+    table = torch.arange(13, dtype=torch.int32, device="cuda")[None].contiguous()
+    qgemv.attn_decode(h, qgemv.attn_decode_desc(qgemv.kv_cache(kc, vc, ks, vs), q, table, ints([n]), out, 0.5, lse=lse))
+    kk, vv = k.double() * sk.double()[:, None], v.double() * sv.double()[:, None]
+    o, want, pv, qk = attend_reference(q[0].double(), kk, vv, 0.5)
+    score = steps(dim) * qk + 2.0 ** -21 * qk
+    within(lse[0], want, score + steps(n) + 2.0 ** -20 + 2.0 ** -22 * want.abs(), "lse")
+    # a weight below 2^-14 of the largest is rounded to 2^-25 of it, by each of the n tokens and for the largest code
+    p = torch.softmax(q[0].double() @ kk.t() * 0.5, -1)
+    lost = n * 2.0 ** -25 * 448 * (p * sv.double()).amax(-1)
+    tol = HALF_ULP[out.dtype] * o.abs() + TINY[out.dtype] + (2 * score[:, None] + 2 * steps(n) + 2.0 ** -16) * pv + lost[:, None]
+    # outputs past fp16's range are infinities
+    far, inside = o.abs() - tol >= 65520, o.abs() + tol < 65504
+    assert torch.equal(out[0][far].double(), torch.sign(o[far]) * math.inf)
+    within(out[0][inside], o[inside], tol[inside], "out")
+
+
 def test_attention_rows_with_infinite_scores(h):
     def edit(table, lens, q, kc, vc):
         kc[table[0, 0].item(), :, :2] = -math.inf  # tokens 0 and 1 of request 0: every score -inf
