@@ -307,7 +307,10 @@ qgemv_status_t qgemv_run_gemm(qgemv_handle_t h, qgemv_format_t fmt, const void* 
  * graph.  Lengths, page tables, slots, positions and adapter numbers are read on the device;
  * one that is out of range is never used to address memory: what happens instead is said at
  * each entry point, and qgemv_check_error then reports QGEMV_ERR_BAD_INDEX.  Element types are
- * those of qgemv_out_t.  Strides are counted in elements. */
+ * those of qgemv_out_t.  Strides are counted in elements.  The kernels are programmatic
+ * dependent launches whatever QGEMV_OPT_PDL says: they may be set up while the kernel before
+ * them on the stream ends, and read and write memory only after it.  Calls use the handle's
+ * workspace like qgemv_run: one at a time per handle. */
 
 /* A paged key-value cache.  k and v: device, page p at p * page_stride, inside it
  * [kv_heads][page_size][head_dim] elements, contiguous and 16-byte aligned (page_stride * element size a

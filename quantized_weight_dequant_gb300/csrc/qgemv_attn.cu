@@ -39,10 +39,6 @@ qgemv_status_t launch(const Handle& h, const qgemv_attn_decode_t& p, AttnArgs a,
   CUtensorMap mk, mv;
   if (!encode<Sh>(h, p.cache, p.cache.k, a.chunk_log2, &mk) || !encode<Sh>(h, p.cache, p.cache.v, a.chunk_log2, &mv)) return QGEMV_ERR_CUDA;
   const void* fn = reinterpret_cast<const void*>(attn_decode_kernel<D, KT, MR>);
-  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem) != cudaSuccess) {
-    cudaGetLastError();
-    return QGEMV_ERR_CUDA;
-  }
   a.splits = (a.group + MR - 1) / MR;
   // as many CTAs as run at once, and no more than the most tiles that the table can hold
   const int64_t tiles = (static_cast<int64_t>(p.table_width) * p.cache.page_size + Sh::kTT - 1) / Sh::kTT;
@@ -51,17 +47,8 @@ qgemv_status_t launch(const Handle& h, const qgemv_attn_decode_t& p, AttnArgs a,
   int64_t grid = std::min<int64_t>(static_cast<int64_t>(h.sms) * Sh::kCtasPerSm, shares);
   static_assert(3 * kAttnCounters <= kMaxRanges && int64_t{4} * kAttnCounters / (3 - Sh::kCtasPerSm) * Sh::kPiece <= int64_t{kWsFloats}, "workspace");
   grid = std::min<int64_t>(grid, kAttnCounters / (3 - Sh::kCtasPerSm));  // two pieces per CTA and group
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
-  cfg.blockDim = dim3(kAttnThreads, 1, 1);
-  cfg.dynamicSmemBytes = Sh::kSmem;
-  cfg.stream = stream;
   void* args[] = {&mk, &mv, &a};
-  if (cudaLaunchKernelExC(&cfg, fn, args) != cudaSuccess) {
-    cudaGetLastError();
-    return QGEMV_ERR_CUDA;
-  }
-  return QGEMV_OK;
+  return launch_dependent(fn, dim3(static_cast<unsigned>(grid)), kAttnThreads, Sh::kSmem, 1, args, stream) ? QGEMV_OK : QGEMV_ERR_CUDA;
 }
 
 template <int D, int KT>

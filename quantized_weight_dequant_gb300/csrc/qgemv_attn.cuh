@@ -300,6 +300,8 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
   if (threadIdx.x < 2)
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(threadIdx.x ? &map_v : &map_k)) : "memory");
 
+  pdl_wait();
+
   // ---- the share of this CTA and of its warps
   const int hxs = p.kv_heads * p.splits;
   // Shares are counted in units: a tile is one, and a (request, head) begins with p.seg_cost more, for
@@ -826,6 +828,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
       mbar_wait_bounded(full + 8 * s, 1, p.spin_ns);
     }
   }
+  pdl_launch_dependents();
   if (any_none) write_none();  // while the last warps finish
   __syncthreads();
 

@@ -12,28 +12,6 @@ using namespace qg;
 
 namespace {
 
-bool start(const void* fn, int64_t grid, size_t smem, int cluster, bool dependent, void** args, cudaStream_t stream) {
-  if (smem > 48 * 1024 && cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess) return false;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
-  cfg.blockDim = dim3(kLoraThreads, 1, 1);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  if (cluster > 1) {
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-  } else {
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = dependent ? 1 : 0;
-  }
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelExC(&cfg, fn, args) == cudaSuccess;
-}
-
 // Rows whose sums fit the workspace are one pair of launches.
 template <bool BF, int OUT>
 bool launch(const Handle& h, qgemv_lora_t p, const LoraWork& work, cudaStream_t stream) {
@@ -47,14 +25,15 @@ bool launch(const Handle& h, qgemv_lora_t p, const LoraWork& work, cudaStream_t 
   int* err = h.err;
   void* sums[] = {&p, &w, &slots, &err};
   const void* fn = few ? reinterpret_cast<const void*>(lora_sums_kernel<BF, 1>) : reinterpret_cast<const void*>(lora_sums_kernel<BF, 4>);
-  if (!start(fn, chunks * slots * kLoraCluster, 0, kLoraCluster, false, sums, stream)) return false;
+  if (!launch_dependent(fn, dim3(static_cast<unsigned>(chunks * slots * kLoraCluster)), kLoraThreads, 0, kLoraCluster, sums, stream)) return false;
   const int64_t tiles = (p.N + 31) / 32;
   if (few) {
     // CTAs that share an adapter's N: about two rounds of them, and at least two tiles for a warp
     slots = static_cast<int>(std::min<int64_t>(32, p.rows));
     int shares = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8 * h.sms / (chunks * slots), tiles / (2 * kLoraWarps))));
     void* args[] = {&p, &w, &slots, &shares};
-    return start(reinterpret_cast<const void*>(lora_few_kernel<BF, OUT>), chunks * slots * shares, sizeof(LoraFewSmem), 1, true, args, stream);
+    return launch_dependent(reinterpret_cast<const void*>(lora_few_kernel<BF, OUT>), dim3(static_cast<unsigned>(chunks * slots * shares)), kLoraThreads,
+                            sizeof(LoraFewSmem), 1, args, stream);
   }
   // as many parts of the rows as fill the GPU once, at least two tiles of rows each
   const int64_t cols = (p.N + 32 * kLoraWarps - 1) / (32 * kLoraWarps);
@@ -64,7 +43,7 @@ bool launch(const Handle& h, qgemv_lora_t p, const LoraWork& work, cudaStream_t 
   void* args[] = {&p, &w, &splits};
   fn = nb == 1 ? reinterpret_cast<const void*>(lora_many_kernel<BF, OUT, 1>)
        : nb == 2 ? reinterpret_cast<const void*>(lora_many_kernel<BF, OUT, 2>) : reinterpret_cast<const void*>(lora_many_kernel<BF, OUT, 4>);
-  return start(fn, cols * splits, 0, 1, true, args, stream);
+  return launch_dependent(fn, dim3(static_cast<unsigned>(cols * splits)), kLoraThreads, 0, 1, args, stream);
 }
 
 template <bool BF>
@@ -108,10 +87,7 @@ extern "C" qgemv_status_t qgemv_run_lora(qgemv_handle_t hh, const qgemv_lora_t* 
     q.y = static_cast<uint8_t*>(p.y) + at;
     work.factor = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(h->ws) + (q.rows + 15) / 16 * 16 * row_bytes);
     work.adapter = reinterpret_cast<int*>(work.factor + q.rows);
-    if (!(bf ? launch_out<true>(*h, q, work, stream) : launch_out<false>(*h, q, work, stream))) {
-      cudaGetLastError();
-      return QGEMV_ERR_CUDA;
-    }
+    if (!(bf ? launch_out<true>(*h, q, work, stream) : launch_out<false>(*h, q, work, stream))) return QGEMV_ERR_CUDA;
   }
   return QGEMV_OK;
 }

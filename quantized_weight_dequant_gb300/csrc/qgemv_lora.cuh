@@ -258,7 +258,10 @@ __global__ void __launch_bounds__(kLoraThreads, 4) lora_sums_kernel(const __grid
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rank = static_cast<int>(blockIdx.x) % kLoraCluster, cluster = static_cast<int>(blockIdx.x) / kLoraCluster;
   const int slot = cluster % slots;
-  pdl_launch_dependents();  // the second launch may start; it waits for this one's end before it reads the sums
+  // The second launch may start once the launch before this one has ended (the base may be its); it waits for
+  // this one's end before it reads the sums.
+  pdl_wait();
+  pdl_launch_dependents();
   if (warp == 0) lora_groups(p, static_cast<int64_t>(cluster / slots) * kLoraChunk, chunk, slot == 0 && rank == 0 ? err : nullptr);
   __syncthreads();
   const int64_t blocks = (p.K + 31) / 32;
@@ -492,6 +495,7 @@ __global__ void __launch_bounds__(kLoraThreads, 4) lora_few_kernel(const __grid_
       __syncthreads();
     }
   }
+  pdl_launch_dependents();
   if (!waited) pdl_wait();  // the launch ends after the one before it
 }
 

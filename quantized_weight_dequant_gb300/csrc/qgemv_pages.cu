@@ -12,20 +12,18 @@ using namespace qg;
 
 namespace {
 
-qgemv_status_t launched() { return cudaGetLastError() == cudaSuccess ? QGEMV_OK : QGEMV_ERR_CUDA; }
-
 template <int T, bool INTER>
-void launch_store(const qgemv_kv_store_t& p, dim3 g, int threads, int* err, cudaStream_t s) {
-  switch (p.cache.head_dim) {
-    case 64: kv_store_kernel<T, 64, INTER><<<g, threads, 0, s>>>(p, err); break;
-    case 128: kv_store_kernel<T, 128, INTER><<<g, threads, 0, s>>>(p, err); break;
-    default: kv_store_kernel<T, 256, INTER><<<g, threads, 0, s>>>(p, err); break;
+const void* store_kernel_for(int dim) {
+  switch (dim) {
+    case 64: return reinterpret_cast<const void*>(kv_store_kernel<T, 64, INTER>);
+    case 128: return reinterpret_cast<const void*>(kv_store_kernel<T, 128, INTER>);
+    default: return reinterpret_cast<const void*>(kv_store_kernel<T, 256, INTER>);
   }
 }
 
 template <int T>
-void launch_store(const qgemv_kv_store_t& p, dim3 g, int threads, int* err, cudaStream_t s) {
-  p.interleaved ? launch_store<T, true>(p, g, threads, err, s) : launch_store<T, false>(p, g, threads, err, s);
+const void* store_kernel_for(int dim, bool interleaved) {
+  return interleaved ? store_kernel_for<T, true>(dim) : store_kernel_for<T, false>(dim);
 }
 
 }  // namespace
@@ -48,8 +46,10 @@ qgemv_status_t qgemv_page_plan(qgemv_handle_t hh, const qgemv_page_plan_t* plan,
   const int64_t grid = std::max<int64_t>(1, std::min<int64_t>((p.capacity + per - 1) / per, h->sms));
   per = (p.capacity + grid - 1) / grid;
   per = (per + kPlanVec - 1) / kPlanVec * kPlanVec;  // ranges start at whole vectors
-  page_plan_kernel<<<static_cast<unsigned>(grid), threads, 0, stream>>>(p, per, h->err);
-  return launched();
+  int* err = h->err;
+  void* args[] = {const_cast<qgemv_page_plan_t*>(&p), &per, &err};
+  const bool ok = launch_dependent(reinterpret_cast<const void*>(page_plan_kernel), dim3(static_cast<unsigned>(grid)), threads, 0, 1, args, stream);
+  return ok ? QGEMV_OK : QGEMV_ERR_CUDA;
 }
 
 qgemv_status_t qgemv_kv_store(qgemv_handle_t hh, const qgemv_kv_store_t* store, cudaStream_t stream) {
@@ -78,12 +78,14 @@ qgemv_status_t qgemv_kv_store(qgemv_handle_t hh, const qgemv_kv_store_t* store, 
   // few tokens: their heads are spread over as many CTAs as keep one head a thread group, and the SMs busy
   const int64_t groups = ((Hq + 2 * Hk) * (D / 8) + threads - 1) / threads;
   const dim3 grid(static_cast<unsigned>(p.tokens), static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(groups, 2 * h->sms / p.tokens))));
-  switch (p.in) {
-    case QGEMV_OUT_F32: launch_store<QGEMV_OUT_F32>(p, grid, threads, h->err, stream); break;
-    case QGEMV_OUT_F16: launch_store<QGEMV_OUT_F16>(p, grid, threads, h->err, stream); break;
-    default: launch_store<QGEMV_OUT_BF16>(p, grid, threads, h->err, stream); break;
-  }
-  return launched();
+  const bool inter = p.interleaved == 1;
+  const int dim = p.cache.head_dim;
+  const void* fn = p.in == QGEMV_OUT_F32   ? store_kernel_for<QGEMV_OUT_F32>(dim, inter)
+                   : p.in == QGEMV_OUT_F16 ? store_kernel_for<QGEMV_OUT_F16>(dim, inter)
+                                           : store_kernel_for<QGEMV_OUT_BF16>(dim, inter);
+  int* err = h->err;
+  void* args[] = {const_cast<qgemv_kv_store_t*>(&p), &err};
+  return launch_dependent(fn, grid, threads, 0, 1, args, stream) ? QGEMV_OK : QGEMV_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -63,6 +63,7 @@ __device__ __forceinline__ int32_t sat32(int64_t v) { return v > 0x7fffffff ? 0x
 __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const qgemv_page_plan_t p, int64_t per_cta, int* err) {
   __shared__ PlanItem item[kPlanThreads];
   __shared__ int64_t ws[2][32];
+  pdl_wait();
   const int tid = threadIdx.x;
   int64_t n_kept = 0, n_got = 0, n_missing = 0;  // of this thread's requests
   __shared__ unsigned long long sums[3];
@@ -160,6 +161,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const qgemv_pag
     pages += dp;
     __syncthreads();  // item and ws are rewritten
   }
+  pdl_launch_dependents();
   for (int64_t t = max(t0, tok) + tid; t < t1; t += blockDim.x) {  // past the last token
     p.slots[t] = -1;
     if (p.positions) p.positions[t] = -1;
@@ -268,6 +270,8 @@ __global__ void __launch_bounds__(kStoreThreads, T == QGEMV_OUT_F32 ? 6 : 8) kv_
       if (!INTER && turns && head < hq + hk) o[u] = load_raw<T>(at + to_mate);
     }
   };
+  pdl_launch_dependents();
+  pdl_wait();
   const int h_first = static_cast<int>(blockIdx.y * blockDim.x + threadIdx.x) / L;
   read(h_first);
   const int64_t slot = p.slots[t];

@@ -1,6 +1,8 @@
-// Argument checks shared by the entry points that read or write a paged key-value cache.
+// Launches of the serving operators, and the argument checks of those that read or write a paged cache.
 #pragma once
 #include <cstdint>
+
+#include <cuda_runtime.h>
 
 #include "../../include/qgemv.h"
 
@@ -9,6 +11,33 @@ namespace qg {
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 inline int64_t kv_elem_bytes(const qgemv_kv_cache_t& c) { return c.type == QGEMV_KV_E4M3 ? 1 : 2; }
+
+// A programmatic dependent launch: the kernel may start while the one before it on the stream ends, so every
+// kernel launched here waits (pdl_wait) before it touches memory, and lets the next one start in turn.  Among
+// small launches this takes the launch latency out of the stream (1.5 us each).
+inline bool launch_dependent(const void* fn, dim3 grid, int threads, size_t smem, int cluster, void** args, cudaStream_t stream) {
+  if (smem > 48 * 1024 && cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  if (cudaLaunchKernelExC(&cfg, fn, args) == cudaSuccess) return true;
+  cudaGetLastError();
+  return false;
+}
 
 inline qgemv_status_t check_cache(const qgemv_kv_cache_t& c) {
   if (!c.k || !c.v || c.type < QGEMV_KV_F16 || c.type > QGEMV_KV_E4M3) return QGEMV_ERR_INVALID_ARG;
