@@ -19,6 +19,10 @@
 //    its row: the order of k within a 32-wide block is the same permutation on both sides, so no shared
 //    memory or ldmatrix is needed for A, B or x.  B's rows are dealt to the two 8-wide halves of a 16-row
 //    tile so that a lane ends up with four consecutive outputs of a token.
+// Measured: one row of rank 16, K 4096, N 6144: 6.8 us, the latency of two launches; 64 rows of 48 adapters of
+// ranks up to 64, K 4096, N 12288: 27.8 us (10 of them the sums; the outputs' CTAs take 6 us to begin, and rows
+// of short ranks cost whole 64-byte pieces of memory); 2048 rows of 4, rank 32, N 14336: 60.6 us (sums 13,
+// outputs 47 at 5 TB/s).
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

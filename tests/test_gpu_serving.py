@@ -374,7 +374,7 @@ def test_attention_matches_64_bits_and_sees_nothing_outside(h, lens, hq, hk, dim
 
 @pytest.mark.parametrize("n,hi,hq,hk,dim,typ,page", [(200, 90, 8, 2, 128, "f16", 16), (300, 700, 4, 2, 64, "bf16", 32),
                                                      (7, 20000, 16, 4, 128, "e4m3", 16), (33, 2500, 32, 8, 128, "bf16", 64),
-                                                     (600, 40, 2, 1, 256, "f16", 16)])
+                                                     (600, 40, 2, 1, 256, "f16", 16), (2100, 30, 1, 1, 64, "bf16", 8)])
 def test_attention_of_many_ragged_requests(h, n, hi, hq, hk, dim, typ, page):
     r = torch.Generator().manual_seed(n)
     lens = torch.randint(0, hi + 1, (n,), generator=r).tolist()
@@ -473,6 +473,36 @@ def test_attention_clamps_lengths_out_of_range_and_reports_them(h):
     check_attend(got, lse, q, [ref[0], (ref[1][0][:0], ref[1][1][:0])], scale)
 
 
+@pytest.mark.parametrize("typ", ["bf16", "e4m3"])
+def test_store_and_attention_past_32_bits_of_cache(h, typ):
+    """Pages more than 2^32 elements into the cache."""
+    page, hk, dim = 64, 8, 128
+    pages = 2 ** 32 // (page * hk * dim) + 40
+    dt = torch.uint8 if typ == "e4m3" else torch.bfloat16
+    kc, vc = (torch.empty(pages, hk, page, dim, dtype=dt, device="cuda") for _ in range(2))
+    ks, vs = (torch.empty(pages, hk, page, device="cuda") for _ in range(2)) if typ == "e4m3" else (None, None)
+    cache = qgemv.kv_cache(kc, vc, ks, vs)
+    g = gen(31)
+    n = 150
+    mine = torch.tensor([pages - 1, 3, pages - 20], device="cuda")
+    t = torch.arange(n, device="cuda")
+    slots = mine[t // page] * page + t % page
+    k, v = (randn(g, n, hk * dim).bfloat16() for _ in range(2))
+    qgemv.kv_store(h, qgemv.kv_store_desc(cache, k, v, slots, t.int()))
+    q = (randn(g, 1, hk * 2, dim) * 2).bfloat16()
+    out, lse = torch.empty_like(q), torch.empty(1, hk * 2, device="cuda")
+    table = mine.int()[None].contiguous()
+    qgemv.attn_decode(h, qgemv.attn_decode_desc(cache, q, table, ints([n]), out, dim ** -0.5, lse=lse))
+    assert qgemv.check_error(h) == qgemv.OK
+    at = (mine[t // page], slice(None), t % page)
+    if typ == "e4m3":
+        stored = [c[at].view(F8).double() * s[at].double()[..., None] for c, s in ((kc, ks), (vc, vs))]
+    else:
+        stored = [c[at].double() for c in (kc, vc)]
+        assert torch.equal(kc[at].reshape(n, -1), k) and torch.equal(vc[at].reshape(n, -1), v)
+    check_attend(out, lse, q, [stored], dim ** -0.5)
+
+
 def test_attention_repeats_bit_for_bit_on_another_stream_and_in_a_graph(h):
     side = torch.cuda.Stream()
     lens = [4000, 17, 900, 0, 2500, 1]
@@ -550,6 +580,11 @@ LORAS = [  # rows, used, loaded, rank, K, N, type, out
 def test_adapters_match_64_bits(h, rows, used, loaded, rank, K, N, typ, out):
     lora_case(h, rows, used, loaded, rank, K, N, typ, out, pad=8 if N % 2 else 0)
     assert qgemv.check_error(h) == qgemv.OK
+
+
+def test_adapters_of_more_rows_than_the_workspace_holds_at_once(h):
+    lora_case(h, 130001, 3, 3, 8, 16, 9, "f16", "f32")
+    lora_case(h, 30011, 2, 2, 128, 24, 40, "bf16", "bf16", pad=8)
 
 
 @pytest.mark.parametrize("rank,typ", [(8, "f16"), (64, "bf16"), (128, "f16")])
