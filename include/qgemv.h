@@ -390,7 +390,7 @@ qgemv_status_t qgemv_page_plan(qgemv_handle_t h, const qgemv_page_plan_t* plan, 
  *                 Another slot outside the cache counts as -1 and is reported.  No slot may
  *                 occur twice.
  *   q, q_out      may both be NULL; q_out [tokens][q_heads][head_dim] of type q_type (F16 or
- *                 BF16), row t at t * q_out_stride.
+ *                 BF16), row t at t * q_out_stride; it must not overlap q, k or v.
  * The rotation is computed in fp32 and rounded once to the cache's or q_out's type.  An E4M3
  * cache gets scale = max|x| / 448 of the token's head (1 where that is 0 or not finite, and at
  * least 2^-126) and the codes e4m3(x * (1 / scale)), rounded to nearest even.

@@ -42,7 +42,7 @@ qgemv_status_t launch(const Handle& h, const qgemv_attn_decode_t& p, AttnArgs a,
   a.splits = (a.group + MR - 1) / MR;
   // as many CTAs as run at once, and no more than the most tiles that the table can hold
   const int64_t tiles = (static_cast<int64_t>(p.table_width) * p.cache.page_size + Sh::kTT - 1) / Sh::kTT;
-  const int64_t most = std::min<int64_t>(int64_t{1} << 40, tiles) * p.requests;
+  const int64_t most = std::min<int64_t>(int64_t{1} << 30, tiles) * p.requests;
   const int64_t shares = std::min<int64_t>(int64_t{1} << 30, most) * (1 + a.seg_cost) * a.kv_heads * a.splits / a.min_units + 1;
   int64_t grid = std::min<int64_t>(static_cast<int64_t>(h.sms) * Sh::kCtasPerSm, shares);
   static_assert(3 * kAttnCounters <= kMaxRanges && int64_t{4} * kAttnCounters / (3 - Sh::kCtasPerSm) * Sh::kPiece <= int64_t{kWsFloats}, "workspace");
@@ -111,7 +111,7 @@ extern "C" qgemv_status_t qgemv_attn_decode(qgemv_handle_t hh, const qgemv_attn_
   // the reciprocal for t / page_size: with 2^(l-1) < page_size <= 2^l the product's excess over 2^(31+l)
   // is at most page_size <= 2^l per unit of t < 2^31
   int l = 3;
-  while ((1 << l) < a.page_size) ++l;
+  while ((int64_t{1} << l) < a.page_size) ++l;
   a.page_mul = static_cast<uint32_t>((uint64_t{1} << (31 + l)) / a.page_size + 1);
   a.page_shift = l - 1;
   a.ws = h->ws;

@@ -586,47 +586,47 @@ __global__ void __launch_bounds__(kLoraThreads, NB == 1 ? 4 : NB == 2 ? 3 : 2)
           part[b][q][h] = there && (NB < 4 || b < work.blocks) ? part_at[h * 8 * part_row + (b * kParts + q) * 4] : make_uint4(0, 0, 0, 0);
     }
     part_at += 16 * part_row;
-    const int id_of[2] = {id[0], id[1]};
-    float acc[2][2][4] = {};
-    auto add = [&](bool in0, bool in1) {
-#pragma unroll
-      for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int q = 0; q < kParts; ++q) {
-          const uint4 zero = make_uint4(0, 0, 0, 0), s0 = in0 ? part[b][q][0] : zero, s1 = in1 ? part[b][q][1] : zero;
-#pragma unroll
-          for (int h = 0; h < 4; ++h) mma16816<BF>(acc[h >> 1][h & 1], s0.x, s1.x, s0.y, s1.y, w[b][h].x, w[b][h].y);
-#pragma unroll
-          for (int h = 0; h < 4; ++h) mma16816<BF>(acc[h >> 1][h & 1], s0.z, s1.z, s0.w, s1.w, w[b][h].z, w[b][h].w);
-        }
-    };
-#pragma unroll 1
-    for (;;) {  // mostly once: rows of one adapter follow one another
-      const uint32_t has0 = __ballot_sync(0xffffffffu, id[0] >= 0), has1 = __ballot_sync(0xffffffffu, id[1] >= 0);
-      if (!(has0 | has1)) break;
-      // the adapter of the first row that still has one
-      const int a = __shfl_sync(0xffffffffu, has0 ? id[0] : id[1], __ffs(has0 ? has0 : has1) - 1);
-      if (a != cur) hold(a);
-      const bool in0 = id[0] == a, in1 = id[1] == a;
-      add(in0, in1);
-      if (in0) id[0] = -1;
-      if (in1) id[1] = -1;
-    }
     cp_async_wait<kLoraAhead - 1>();
+    // One adapter after another, and the rows without one: mostly a single pass, as rows of one adapter follow
+    // one another.  A pass has its own sums, of which it writes its rows': an adapter with infinities or NaN
+    // makes NaN of the others' rows.
+    bool todo[2] = {m < rows, m + 8 < rows};
+#pragma unroll 1
+    for (;;) {
+      const uint32_t has0 = __ballot_sync(0xffffffffu, todo[0]), has1 = __ballot_sync(0xffffffffu, todo[1]);
+      if (!(has0 | has1)) break;
+      const int a = __shfl_sync(0xffffffffu, has0 ? id[0] : id[1], __ffs(has0 ? has0 : has1) - 1);
+      const bool in[2] = {todo[0] && id[0] == a, todo[1] && id[1] == a};
+      float acc[2][2][4] = {};
+      if (a >= 0) {
+        if (a != cur) hold(a);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (m + 8 * h >= rows) continue;
-      const float f = id_of[h] >= 0 ? factor[h] : 0.f;
+        for (int b = 0; b < NB; ++b)
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        if (left[k] <= 0) continue;
-        float4 v = make_float4(f * acc[k][0][2 * h], f * acc[k][0][2 * h + 1], f * acc[k][1][2 * h], f * acc[k][1][2 * h + 1]);
-        const int64_t off = h * row8 + k * 4 * kBytes;
-        if (old_at) {
-          const float4 d = whole ? lora_four<OUT>(lds_v4(mine + (s * 4 + 2 * h + k) * 512)) : lora_load4<OUT>(old_at + off, 0, left[k], vec);
-          v.x += d.x, v.y += d.y, v.z += d.z, v.w += d.w;
+          for (int q = 0; q < kParts; ++q) {
+            const uint4 zero = make_uint4(0, 0, 0, 0), s0 = in[0] ? part[b][q][0] : zero, s1 = in[1] ? part[b][q][1] : zero;
+#pragma unroll
+            for (int h = 0; h < 4; ++h) mma16816<BF>(acc[h >> 1][h & 1], s0.x, s1.x, s0.y, s1.y, w[b][h].x, w[b][h].y);
+#pragma unroll
+            for (int h = 0; h < 4; ++h) mma16816<BF>(acc[h >> 1][h & 1], s0.z, s1.z, s0.w, s1.w, w[b][h].z, w[b][h].w);
+          }
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (!in[h]) continue;
+        todo[h] = false;
+        const float f = a >= 0 ? factor[h] : 0.f;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          if (left[k] <= 0) continue;
+          float4 v = make_float4(f * acc[k][0][2 * h], f * acc[k][0][2 * h + 1], f * acc[k][1][2 * h], f * acc[k][1][2 * h + 1]);
+          const int64_t off = h * row8 + k * 4 * kBytes;
+          if (old_at) {
+            const float4 d = whole ? lora_four<OUT>(lds_v4(mine + (s * 4 + 2 * h + k) * 512)) : lora_load4<OUT>(old_at + off, 0, left[k], vec);
+            v.x += d.x, v.y += d.y, v.z += d.z, v.w += d.w;
+          }
+          lora_store4<OUT>(y_at + off, 0, left[k], vec, v);
         }
-        lora_store4<OUT>(y_at + off, 0, left[k], vec, v);
       }
     }
     if (old_at) old_at += 2 * row8;

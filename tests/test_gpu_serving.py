@@ -627,6 +627,35 @@ def test_adapters_keep_small_and_large_inner_sums(h, size):
         within(y[m], ref, B[a].double().abs() @ (near + steps(16) * low.abs()) + 2.0 ** -22 * ref.abs(), f"row {m}")
 
 
+@pytest.mark.parametrize("rows", [20, 300])
+@pytest.mark.parametrize("typ", ["f16", "bf16"])
+def test_infinities_and_nan_stay_with_their_adapter_and_row(h, rows, typ):
+    """Neighbouring rows of other adapters, and of none, come out bit for bit as beside sound ones."""
+    g = gen(12)
+    x, A, B = randn(g, rows, 256).to(TYPES[typ]), randn(g, 5, 32, 256).to(TYPES[typ]), randn(g, 5, 70, 32).to(TYPES[typ])
+    base, ids = randn(g, rows, 70), ints([(m * 7 + m // 6) % 6 - 1 for m in range(rows)])
+
+    def run():
+        y = torch.empty(rows, 70, device="cuda")
+        qgemv.run_lora(h, qgemv.lora_desc(x, A, B, ids, y, base=base))
+        torch.cuda.synchronize()
+        return y
+
+    sound = run()
+    assert sound.isfinite().all()
+    B[1, 3, :] = float("inf")
+    B[2] = NAN
+    A[3, 5, 9] = float("inf")
+    x[9] = NAN
+    sick = (ids >= 1) & (ids <= 3)
+    sick[9] = True
+    y = run()
+    assert torch.equal(y[~sick], sound[~sick])
+    others = y[ids == 1][:, [n for n in range(70) if n != 3]]
+    assert others.isfinite().all() and not y[ids == 1][:, 3].isfinite().any()
+    assert not y[(ids == 2) | (ids == 3)].isfinite().any()
+
+
 def test_adapters_repeat_bit_for_bit_in_a_graph(h):
     y, _, _, d = lora_case(h, 70, 20, 20, 32, 1024, 700, "bf16", "f32", seed=3)
     first = y.clone()
