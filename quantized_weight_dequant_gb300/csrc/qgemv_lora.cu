@@ -41,9 +41,13 @@ bool launch(const Handle& h, qgemv_lora_t p, const LoraWork& work, cudaStream_t 
   const int64_t at_once = int64_t{h.sms} * (nb == 1 ? 4 : nb == 2 ? 3 : 2);
   int splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(at_once / cols, (p.rows + 31) / 32)));
   void* args[] = {&p, &w, &splits};
-  fn = nb == 1 ? reinterpret_cast<const void*>(lora_many_kernel<BF, OUT, 1>)
-       : nb == 2 ? reinterpret_cast<const void*>(lora_many_kernel<BF, OUT, 2>) : reinterpret_cast<const void*>(lora_many_kernel<BF, OUT, 4>);
-  return launch_dependent(fn, dim3(static_cast<unsigned>(cols * splits)), kLoraThreads, 0, 1, args, stream);
+  const dim3 grid(static_cast<unsigned>(cols * splits));
+  auto run = [&](const void* kernel, size_t stage) { return launch_dependent(kernel, grid, kLoraThreads, (kLoraAhead + 1) * stage, 1, args, stream); };
+  switch (nb) {
+    case 1: return run(reinterpret_cast<const void*>(lora_many_kernel<BF, OUT, 1>), sizeof(LoraManyStage<BF, 1>));
+    case 2: return run(reinterpret_cast<const void*>(lora_many_kernel<BF, OUT, 2>), sizeof(LoraManyStage<BF, 2>));
+    default: return run(reinterpret_cast<const void*>(lora_many_kernel<BF, OUT, 4>), sizeof(LoraManyStage<BF, 4>));
+  }
 }
 
 template <bool BF>
@@ -85,8 +89,7 @@ extern "C" qgemv_status_t qgemv_run_lora(qgemv_handle_t hh, const qgemv_lora_t* 
     const int64_t at = m * p.y_stride * (p.out == QGEMV_OUT_F32 ? 4 : 2);
     q.base = p.base ? static_cast<const uint8_t*>(p.base) + at : nullptr;
     q.y = static_cast<uint8_t*>(p.y) + at;
-    work.factor = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(h->ws) + (q.rows + 15) / 16 * 16 * row_bytes);
-    work.adapter = reinterpret_cast<int*>(work.factor + q.rows);
+    work.row = reinterpret_cast<LoraRow*>(reinterpret_cast<uint8_t*>(h->ws) + (q.rows + 15) / 16 * 16 * row_bytes);
     if (!(bf ? launch_out<true>(*h, q, work, stream) : launch_out<false>(*h, q, work, stream))) return QGEMV_ERR_CUDA;
   }
   return QGEMV_OK;

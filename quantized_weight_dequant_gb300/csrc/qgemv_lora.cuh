@@ -21,8 +21,8 @@
 //    tile so that a lane ends up with four consecutive outputs of a token.
 // Measured: one row of rank 16, K 4096, N 6144: 6.8 us, the latency of two launches; 64 rows of 48 adapters of
 // ranks up to 64, K 4096, N 12288: 27.8 us (10 of them the sums; the outputs' CTAs take 6 us to begin, and rows
-// of short ranks cost whole 64-byte pieces of memory); 2048 rows of 4, rank 32, N 14336: 60.6 us (sums 13,
-// outputs 47 at 5 TB/s).
+// of short ranks cost whole 64-byte pieces of memory); 2048 rows of 4, rank 32, N 14336: 50.4 us (sums 13,
+// outputs 37 at 6.3 TB/s).
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -43,13 +43,17 @@ constexpr int kLoraLd = kLoraMaxRank + 4;  // floats per token of the sums in sh
 constexpr int kLoraWarps = 4;
 constexpr int kLoraThreads = 32 * kLoraWarps;
 
+// What a launch keeps of a row beside its sums: its adapter (-1: none, or one of rank 0), and the adapter's
+// scale over the parts' power of two.
+struct __align__(8) LoraRow {
+  int adapter;
+  float factor;
+};
 // The rows of a launch in the workspace: per row, the parts of its sums (blocks of 32 ranks, kParts, four
-// lanes of 16 bytes), then per row its factor (the adapter's scale over the parts' power of two) and its
-// adapter (-1: none, or one of rank 0).
+// lanes of 16 bytes).
 struct LoraWork {
   uint4* parts;
-  float* factor;
-  int* adapter;
+  LoraRow* row;
   int blocks;  // 32-wide blocks of the largest rank
 };
 __host__ __device__ constexpr int lora_parts(bool bf) { return bf ? 3 : 2; }
@@ -274,7 +278,7 @@ __global__ void __launch_bounds__(kLoraThreads, 4) lora_sums_kernel(const __grid
     const LoraGroup group = chunk.group[i];
     const int n_tok = group.n, a = group.adapter, r = group.rank;
     const int* all = chunk.row + group.first;
-    if (rank == 0 && static_cast<int>(threadIdx.x) < n_tok) work.adapter[all[threadIdx.x]] = r ? a : -1;
+    if (rank == 0 && static_cast<int>(threadIdx.x) < n_tok) work.row[all[threadIdx.x]].adapter = r ? a : -1;
     if (r == 0) continue;
     const float scale = p.scales ? p.scales[a] : 1.f;
     const uint16_t* A = static_cast<const uint16_t*>(p.A) + static_cast<int64_t>(a) * p.rank * p.K;
@@ -319,7 +323,7 @@ __global__ void __launch_bounds__(kLoraThreads, 4) lora_sums_kernel(const __grid
             v[0] -= f0.x, v[1] -= f0.y, v[2] -= f1.x, v[3] -= f1.y;
           }
         }
-        if (lane == 0) work.factor[m] = scale * back;
+        if (lane == 0) work.row[m].factor = scale * back;
       }
       cluster_arrive();
       cluster_wait();  // no CTA reads this one's sums: they are used again, or the CTA ends
@@ -493,7 +497,7 @@ __global__ void __launch_bounds__(kLoraThreads, 4) lora_few_kernel(const __grid_
         if (g < n) v = __ldcg(work.parts + (static_cast<int64_t>(all[k0 + g]) * work.blocks + b) * (4 * kParts) + part * 4 + c);
         sm.parts[b][part][lane] = v;
       }
-      if (threadIdx.x < 8) sm.factor[threadIdx.x] = static_cast<int>(threadIdx.x) < n ? __ldcg(work.factor + all[k0 + threadIdx.x]) : 0.f;
+      if (threadIdx.x < 8) sm.factor[threadIdx.x] = static_cast<int>(threadIdx.x) < n ? __ldcg(&work.row[all[k0 + threadIdx.x]].factor) : 0.f;
       __syncthreads();
       stream.run(t0);
       __syncthreads();
@@ -504,14 +508,22 @@ __global__ void __launch_bounds__(kLoraThreads, 4) lora_few_kernel(const __grid_
 }
 
 // ------------------------------------------------------------------------- outputs of many rows
-// A warp keeps 32 rows of B (NB blocks of 32 ranks) and walks over tiles of 16 rows of the batch.  The base,
-// which comes from memory, is asked for kLoraAhead tiles ahead through a ring of cp.async (each lane its own
-// 64 bytes of a tile); the sums come from L2 when they are needed.  In a tile whose rows have several
-// adapters, one is taken after another, with the sums of the others' rows as zeros.
-constexpr int kLoraAhead = 4;
+// A warp keeps 32 rows of B (NB blocks of 32 ranks) and walks over tiles of 16 rows of the batch.  What a tile
+// needs is asked for kLoraAhead tiles ahead, through a ring of cp.async: a lane's own 64 bytes of the base, and for
+// all warps of the CTA together the rows' adapters, factors and sums.  2048 rows, N 14336, rank 32: 50.4 us with the
+// inner sums (60.6 with the sums read from L2 by each warp when it needs them), rank 64: 60, rank 128: 113; with
+// three tiles ahead 51.2, 84 and 113.
+constexpr int kLoraAhead = 2;
+template <bool BF, int NB>
+struct LoraManyStage {
+  uint4 sums[NB * lora_parts(BF)][2][32];  // block and part, row half
+  uint4 base[kLoraWarps][4][32];           // row half and half of the outputs
+  LoraRow row[16];
+};
 template <bool BF, int OUT, int NB>
 __global__ void __launch_bounds__(kLoraThreads, NB == 1 ? 4 : NB == 2 ? 3 : 2)
     lora_many_kernel(const __grid_constant__ qgemv_lora_t p, const LoraWork work, int splits) {
+  using Stage = LoraManyStage<BF, NB>;
   constexpr int kParts = lora_parts(BF);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
   constexpr int kBytes = OUT == QGEMV_OUT_F32 ? 16 : 8;  // of four outputs
@@ -519,34 +531,42 @@ __global__ void __launch_bounds__(kLoraThreads, NB == 1 ? 4 : NB == 2 ? 3 : 2)
   const int n0 = (static_cast<int>(blockIdx.x) / splits * kLoraWarps + warp) * 32;
   const int64_t tiles = (p.rows + 15) / 16;
   const int t0 = static_cast<int>(tiles * split / splits), t1 = static_cast<int>(tiles * (split + 1) / splits);
-  const int N = static_cast<int>(p.N), rows = static_cast<int>(p.rows);
+  const int N = static_cast<int>(p.N);
   const bool vec = p.y_stride % 4 == 0;
   const int left[2] = {N - n0 - 4 * c, N - n0 - 16 - 4 * c};  // outputs from the lane's first in each half
   const bool whole = vec && n0 + 32 <= N;                     // all lanes' outputs are there, four at once
-  __shared__ uint4 ring[kLoraWarps][kLoraAhead][4][32];
-  // of row g of the next tile to be asked for: base; of the tile in hand: y, parts
-  const int m_first = 16 * t0 + g;
+  extern __shared__ __align__(16) uint8_t dyn[];
+  Stage* ring = reinterpret_cast<Stage*>(dyn);
+  const int m_first = 16 * t0 + g, m_end = static_cast<int>(min(p.rows, int64_t{16} * t1));
   const int64_t row8 = 8 * p.y_stride * (kBytes / 4), lane_at = (m_first * p.y_stride + n0 + 4 * c) * (kBytes / 4);
-  const uint8_t* base_at = p.base ? static_cast<const uint8_t*>(p.base) + lane_at : nullptr;
-  uint8_t* y_at = static_cast<uint8_t*>(p.y) + lane_at;
   const int part_row = 4 * kParts * work.blocks;
+  // of row g of the next tile to be asked for
+  const uint8_t* base_at = p.base ? static_cast<const uint8_t*>(p.base) + lane_at : nullptr;
   const uint4* part_at = work.parts + static_cast<int64_t>(m_first) * part_row + c;
-  int m_ask = m_first, ask_s = 0;
-  const int m_end = min(rows, 16 * t1);
-  const uint32_t mine = smem_u32(&ring[warp][0][0][lane]);
-  auto ask = [&]() {
-    if (whole && base_at) {
+  int m_base = m_first, m_sums = m_first;
+  // of the tile in hand
+  const uint8_t* old_at = base_at;
+  uint8_t* y_at = static_cast<uint8_t*>(p.y) + lane_at;
+  auto ask_base = [&](Stage& st) {
+    if (!whole || !base_at) return;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (m_base + 8 * h < m_end) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) cp_async_fill<kBytes>(smem_u32(&st.base[warp][2 * h + k][lane]), base_at + h * row8 + k * 4 * kBytes, kBytes);
+      }
+    base_at += 2 * row8;
+    m_base += 16;
+  };
+  auto ask_sums = [&](Stage& st) {  // a fourth of the CTA's
+    for (int q = warp; q < kParts * work.blocks; q += kLoraWarps)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        if (m_ask + 8 * h < m_end) {
-#pragma unroll
-          for (int k = 0; k < 2; ++k) cp_async_fill<kBytes>(mine + (ask_s * 4 + 2 * h + k) * 512, base_at + h * row8 + k * 4 * kBytes, kBytes);
-        }
-      base_at += 2 * row8;
-      m_ask += 16;
-    }
+        if (m_sums + 8 * h < m_end) cp_async_fill<16>(smem_u32(&st.sums[q][h][lane]), part_at + h * 8 * part_row + q * 4, 16);
+    if (warp == kLoraWarps - 1 && c < 2 && m_sums + 8 * c < m_end) cp_async_fill<8>(smem_u32(&st.row[g + 8 * c]), work.row + m_sums + 8 * c, 8);
+    part_at += 16 * part_row;
+    m_sums += 16;
     cp_async_commit();
-    if (++ask_s == kLoraAhead) ask_s = 0;
   };
   uint4 w[NB][4];
   int cur = -1;
@@ -564,65 +584,62 @@ __global__ void __launch_bounds__(kLoraThreads, NB == 1 ? 4 : NB == 2 ? 3 : 2)
       lora_mask(w[b], 32 * b + 8 * c, r);
     }
   };
-  const uint8_t* old_at = base_at;  // of the tile in hand
 #pragma unroll 1
-  for (int i = 0; i < kLoraAhead; ++i) ask();
+  for (int i = 0; i < kLoraAhead; ++i) ask_base(ring[i]);
   pdl_wait();  // for the sums; the base is not theirs
+#pragma unroll 1
+  for (int i = 0; i < kLoraAhead; ++i) ask_sums(ring[i]);
   int s = 0;
 #pragma unroll 1
   for (int tile = t0, m = m_first; tile < t1; ++tile, m += 16) {
-    int id[2];
-    float factor[2];
-    uint4 part[NB][kParts][2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const bool there = m + 8 * h < rows;
-      id[h] = there ? work.adapter[m + 8 * h] : -1;
-      factor[h] = there ? work.factor[m + 8 * h] : 0.f;
-#pragma unroll
-      for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int q = 0; q < kParts; ++q)
-          part[b][q][h] = there && (NB < 4 || b < work.blocks) ? part_at[h * 8 * part_row + (b * kParts + q) * 4] : make_uint4(0, 0, 0, 0);
-    }
-    part_at += 16 * part_row;
+    const Stage& st = ring[s];
     cp_async_wait<kLoraAhead - 1>();
+    __syncthreads();  // every warp's copies are there, and every warp is through with the tile before
+    Stage& next = ring[s == 0 ? kLoraAhead : s - 1];
+    ask_base(next);
+    ask_sums(next);
+    LoraRow row[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) row[h] = m + 8 * h < m_end ? st.row[g + 8 * h] : LoraRow{-1, 0.f};
     // One adapter after another, and the rows without one: mostly a single pass, as rows of one adapter follow
     // one another.  A pass has its own sums, of which it writes its rows': an adapter with infinities or NaN
     // makes NaN of the others' rows.
-    bool todo[2] = {m < rows, m + 8 < rows};
+    bool todo[2] = {m < m_end, m + 8 < m_end};
 #pragma unroll 1
     for (;;) {
       const uint32_t has0 = __ballot_sync(0xffffffffu, todo[0]), has1 = __ballot_sync(0xffffffffu, todo[1]);
       if (!(has0 | has1)) break;
-      const int a = __shfl_sync(0xffffffffu, has0 ? id[0] : id[1], __ffs(has0 ? has0 : has1) - 1);
-      const bool in[2] = {todo[0] && id[0] == a, todo[1] && id[1] == a};
+      const int a = __shfl_sync(0xffffffffu, has0 ? row[0].adapter : row[1].adapter, __ffs(has0 ? has0 : has1) - 1);
+      const bool in[2] = {todo[0] && row[0].adapter == a, todo[1] && row[1].adapter == a};
       float acc[2][2][4] = {};
       if (a >= 0) {
         if (a != cur) hold(a);
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
+        for (int b = 0; b < NB; ++b) {
+          if (NB == 4 && b == 3 && work.blocks == 3) break;
 #pragma unroll
           for (int q = 0; q < kParts; ++q) {
-            const uint4 zero = make_uint4(0, 0, 0, 0), s0 = in[0] ? part[b][q][0] : zero, s1 = in[1] ? part[b][q][1] : zero;
+            const uint4 zero = make_uint4(0, 0, 0, 0);
+            const uint4 s0 = in[0] ? st.sums[b * kParts + q][0][lane] : zero, s1 = in[1] ? st.sums[b * kParts + q][1][lane] : zero;
 #pragma unroll
             for (int h = 0; h < 4; ++h) mma16816<BF>(acc[h >> 1][h & 1], s0.x, s1.x, s0.y, s1.y, w[b][h].x, w[b][h].y);
 #pragma unroll
             for (int h = 0; h < 4; ++h) mma16816<BF>(acc[h >> 1][h & 1], s0.z, s1.z, s0.w, s1.w, w[b][h].z, w[b][h].w);
           }
+        }
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         if (!in[h]) continue;
         todo[h] = false;
-        const float f = a >= 0 ? factor[h] : 0.f;
+        const float f = a >= 0 ? row[h].factor : 0.f;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           if (left[k] <= 0) continue;
           float4 v = make_float4(f * acc[k][0][2 * h], f * acc[k][0][2 * h + 1], f * acc[k][1][2 * h], f * acc[k][1][2 * h + 1]);
           const int64_t off = h * row8 + k * 4 * kBytes;
           if (old_at) {
-            const float4 d = whole ? lora_four<OUT>(lds_v4(mine + (s * 4 + 2 * h + k) * 512)) : lora_load4<OUT>(old_at + off, 0, left[k], vec);
+            const float4 d = whole ? lora_four<OUT>(st.base[warp][2 * h + k][lane]) : lora_load4<OUT>(old_at + off, 0, left[k], vec);
             v.x += d.x, v.y += d.y, v.z += d.z, v.w += d.w;
           }
           lora_store4<OUT>(y_at + off, 0, left[k], vec, v);
@@ -630,9 +647,8 @@ __global__ void __launch_bounds__(kLoraThreads, NB == 1 ? 4 : NB == 2 ? 3 : 2)
       }
     }
     if (old_at) old_at += 2 * row8;
-    ask();
-    if (++s == kLoraAhead) s = 0;
     y_at += 2 * row8;
+    if (++s > kLoraAhead) s = 0;
   }
 }
 
