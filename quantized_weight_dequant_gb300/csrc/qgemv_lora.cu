@@ -20,7 +20,7 @@ bool launch(const Handle& h, qgemv_lora_t p, const LoraWork& work, cudaStream_t 
   // Sums: clusters per chunk of rows, one for each adapter that they can have, but no more in all than run at
   // once (then a cluster takes its share of the adapters one after another).
   const int64_t resident = int64_t{h.sms} * 4 / kLoraCluster;
-  int slots = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(kLoraChunk, p.rows), (resident + chunks - 1) / chunks)));
+  int slots = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(kLoraChunk, p.rows), resident / chunks)));
   LoraWork w = work;
   int* err = h.err;
   void* sums[] = {&p, &w, &slots, &err};
@@ -28,12 +28,10 @@ bool launch(const Handle& h, qgemv_lora_t p, const LoraWork& work, cudaStream_t 
   if (!launch_dependent(fn, dim3(static_cast<unsigned>(chunks * slots * kLoraCluster)), kLoraThreads, 0, kLoraCluster, sums, stream)) return false;
   const int64_t tiles = (p.N + 31) / 32;
   if (few) {
-    // CTAs that share an adapter's N: about two rounds of them, and at least two tiles for a warp
-    slots = static_cast<int>(std::min<int64_t>(32, p.rows));
-    int shares = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8 * h.sms / (chunks * slots), tiles / (2 * kLoraWarps))));
-    void* args[] = {&p, &w, &slots, &shares};
-    return launch_dependent(reinterpret_cast<const void*>(lora_few_kernel<BF, OUT>), dim3(static_cast<unsigned>(chunks * slots * shares)), kLoraThreads,
-                            sizeof(LoraFewSmem), 1, args, stream);
+    // as many CTAs as run at once, each with at least two tiles for a warp
+    const unsigned grid = static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(int64_t{h.sms} * 4, p.rows * tiles / (2 * kLoraWarps))));
+    void* args[] = {&p, &w};
+    return launch_dependent(reinterpret_cast<const void*>(lora_few_kernel<BF, OUT>), dim3(grid), kLoraThreads, sizeof(LoraFewSmem), 1, args, stream);
   }
   // as many parts of the rows as fill the GPU once, at least two tiles of rows each
   const int64_t cols = (p.N + 32 * kLoraWarps - 1) / (32 * kLoraWarps);

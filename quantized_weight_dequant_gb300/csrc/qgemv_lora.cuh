@@ -11,7 +11,7 @@
 //    (the row's largest in [2^14, 2^15)), or three bf16 parts: at least 21 bits.
 //  * Outputs of few rows (lora_few_kernel): the rows of one adapter stay, its B streams by, through a
 //    ring of cp.async in which every lane fetches what it will multiply itself (no barrier, no
-//    registers).  Several CTAs share N.
+//    registers).  All CTAs run at once and have equal shares of the tiles of all rows.
 //  * Outputs of many rows (lora_many_kernel): 32 rows of B stay in a warp's registers, the tokens stream
 //    by, 16 at a time.
 //  * All products run on mma.sync m16n8k16, the first with A's rows as its 16 and the tokens as its 8, the
@@ -20,8 +20,8 @@
 //    memory or ldmatrix is needed for A, B or x.  B's rows are dealt to the two 8-wide halves of a 16-row
 //    tile so that a lane ends up with four consecutive outputs of a token.
 // Measured: one row of rank 16, K 4096, N 6144: 6.8 us, the latency of two launches; 64 rows of 48 adapters of
-// ranks up to 64, K 4096, N 12288: 27.8 us (10 of them the sums; the outputs' CTAs take 6 us to begin, and rows
-// of short ranks cost whole 64-byte pieces of memory); 2048 rows of 4, rank 32, N 14336: 50.4 us (sums 13,
+// ranks up to 64, K 4096, N 12288: 24.5 us (7 of them the sums; the outputs' CTAs take 4 us to begin, and rows
+// of short ranks cost whole 64-byte pieces of memory); 2048 rows of 4, rank 32, N 14336: 49.2 us (sums 12,
 // outputs 37 at 6.3 TB/s).
 #pragma once
 #include <cuda_bf16.h>
@@ -85,33 +85,45 @@ __device__ __forceinline__ int lora_rank(const qgemv_lora_t& p, int a) {
   return a < 0 ? 0 : p.ranks ? min(max(p.ranks[a], 0), p.rank) : p.rank;
 }
 
-// Groups the rows from m0 on by their adapters (one warp; every lane asks for its own row's adapter and rank).
-__device__ __forceinline__ void lora_groups(const qgemv_lora_t& p, int64_t m0, LoraChunk& out, int* err) {
+// One warp looks at the kLoraChunk rows from m0 on, a lane at one: its adapter (-2: past the rows) and rank, how
+// many of them have that adapter, its place among those, and where those begin in a list of the rows by adapter.
+struct LoraLane {
+  int id, rank, n, place, first;
+};
+__device__ __forceinline__ LoraLane lora_lane(const qgemv_lora_t& p, int64_t m0, int* err) {
   const int lane = threadIdx.x & 31;
-  const uint32_t before = (1u << lane) - 1;
-  int id = -2;  // past the rows
+  LoraLane out;
+  out.id = -2;
   if (m0 + lane < p.rows) {
-    id = p.ids[m0 + lane];
-    if (id < -1 || id >= p.adapters) {
+    out.id = p.ids[m0 + lane];
+    if (out.id < -1 || out.id >= p.adapters) {
       if (err) atomicOr(err, kDevErrIndex);
-      id = -1;
+      out.id = -1;
     }
   }
-  const int r = lora_rank(p, id);
-  const uint32_t same = __match_any_sync(0xffffffffu, id);
-  const int leader = __ffs(same) - 1;
-  const bool leads = id != -2 && leader == lane;
-  const int n = leads ? __popc(same) : 0;
-  int upto = n;
+  out.rank = lora_rank(p, out.id);
+  const uint32_t same = __match_any_sync(0xffffffffu, out.id);
+  out.n = __popc(same);
+  out.place = __popc(same & ((1u << lane) - 1));
+  int upto = out.id != -2 && out.place == 0 ? out.n : 0;
+  const int own = upto;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int u = __shfl_up_sync(0xffffffffu, upto, o);
     if (lane >= o) upto += u;
   }
-  const int first = __shfl_sync(0xffffffffu, upto - n, leader);
-  if (id != -2) out.row[first + __popc(same & before)] = static_cast<int>(m0) + lane;
+  out.first = __shfl_sync(0xffffffffu, upto - own, __ffs(same) - 1);
+  return out;
+}
+
+// Groups the rows from m0 on by their adapters.
+__device__ __forceinline__ void lora_groups(const qgemv_lora_t& p, int64_t m0, LoraChunk& out, int* err) {
+  const int lane = threadIdx.x & 31;
+  const LoraLane me = lora_lane(p, m0, err);
+  const bool there = me.id != -2, leads = there && me.place == 0;
+  if (there) out.row[me.first + me.place] = static_cast<int>(m0) + lane;
   const uint32_t leaders = __ballot_sync(0xffffffffu, leads);
-  if (leads) out.group[__popc(leaders & before)] = LoraGroup{n, first, id, r};
+  if (leads) out.group[__popc(leaders & ((1u << lane) - 1))] = LoraGroup{me.n, me.first, me.id, me.rank};
   if (lane == 0) out.count = __popc(leaders);
 }
 
@@ -265,12 +277,12 @@ __global__ void __launch_bounds__(kLoraThreads, 4) lora_sums_kernel(const __grid
   __shared__ LoraChunk chunk;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rank = static_cast<int>(blockIdx.x) % kLoraCluster, cluster = static_cast<int>(blockIdx.x) / kLoraCluster;
-  const int slot = cluster % slots;
+  const int chunks = static_cast<int>((p.rows + kLoraChunk - 1) / kLoraChunk), slot = cluster / chunks;  // those without an adapter come last
   // The second launch may start once the launch before this one has ended (the base may be its); it waits for
   // this one's end before it reads the sums.
   pdl_wait();
   pdl_launch_dependents();
-  if (warp == 0) lora_groups(p, static_cast<int64_t>(cluster / slots) * kLoraChunk, chunk, slot == 0 && rank == 0 ? err : nullptr);
+  if (warp == 0) lora_groups(p, static_cast<int64_t>(cluster % chunks) * kLoraChunk, chunk, slot == 0 && rank == 0 ? err : nullptr);
   __syncthreads();
   const int64_t blocks = (p.K + 31) / 32;
   const int64_t b0 = blocks * rank / kLoraCluster, b1 = blocks * (rank + 1) / kLoraCluster;
@@ -377,11 +389,16 @@ struct LoraStream {
   __device__ __forceinline__ void ask() {  // the next stage
     if (ask_tile < t1) {
       const uint32_t to = mine + ask_s * (kLoraPieces * 512);
-      const int c8 = 8 * (threadIdx.x & 3);
-      const bool in = 32 * ask_b + c8 < r;
+      const int c8 = 8 * (threadIdx.x & 3), in = 32 * ask_b + c8 < r ? 16 : 0;
+      if (32 * ask_tile + 32 <= N) {
 #pragma unroll
-      for (int h = 0; h < 4; ++h)  // rows 0, 2, 16, 18 from the lane's first
-        cp_async_fill<16>(to + h * 512, ask_row + (h & 1) * to_second + (h >> 1) * 8 * to_second, in && ask_n + 2 * (h & 1) + 16 * (h >> 1) < N ? 16 : 0);
+        for (int h = 0; h < 4; ++h)  // rows 0, 2, 16, 18 from the lane's first
+          cp_async_fill<16>(to + h * 512, ask_row + (h & 1) * to_second + (h >> 1) * 8 * to_second, in);
+      } else {
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+          cp_async_fill<16>(to + h * 512, ask_row + (h & 1) * to_second + (h >> 1) * 8 * to_second, ask_n + 2 * (h & 1) + 16 * (h >> 1) < N ? in : 0);
+      }
       if (ask_b == 0 && vec && base) {
 #pragma unroll
         for (int k = 0; k < 2; ++k)
@@ -454,50 +471,115 @@ struct LoraStream {
   }
 };
 
+// Up to eight rows of one adapter among kLoraChunk neighbouring ones, from `first` on in their list, whose outputs
+// cost `cost` units a tile (`at`: units of the chunk's items before).
+struct LoraItem {
+  int64_t at;
+  int n, first, adapter, rank, cost;
+};
+struct LoraItems {
+  int64_t total;
+  LoraItem item[kLoraChunk];
+  int row[kLoraChunk];
+  int count;
+};
+__device__ __forceinline__ int64_t lora_div(int64_t a, int b) {  // 32-bit arithmetic where a allows it
+  return a >> 32 ? a / b : static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b));
+}
+__device__ __forceinline__ void lora_items(const qgemv_lora_t& p, int64_t m0, int tiles, LoraItems& out) {
+  const int lane = threadIdx.x & 31;
+  const LoraLane me = lora_lane(p, m0, nullptr);
+  const bool there = me.id != -2;
+  if (there) out.row[me.first + me.place] = static_cast<int>(m0) + lane;
+  const int n = min(me.n - me.place, 8);
+  // by the bytes: a block of 32 ranks of a tile of B is 2 KB, a row's base and outputs 256 bytes, which alone
+  // (no adapter) take longer, four copies of a thread at a time
+  int cost = me.rank ? 8 * ((me.rank + 31) / 32) + n : p.base != p.y ? 3 * n : 0;
+  if (!there || me.place % 8) cost = 0;
+  const int64_t units = static_cast<int64_t>(cost) * tiles;
+  int64_t upto = units;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += u;
+  }
+  const uint32_t items = __ballot_sync(0xffffffffu, cost > 0);
+  if (cost) out.item[__popc(items & ((1u << lane) - 1))] = LoraItem{upto - units, n, me.first + me.place, me.id, me.rank, cost};
+  if (lane == 31) out.total = upto, out.count = __popc(items);
+}
+
+// All tiles of all items are cut into equal shares, one per CTA, all of which run at once: every CTA looks at all
+// rows and finds its share.  Against CTAs that divide each adapter's tiles, in two rounds: 64 rows of 48 adapters of
+// ranks up to 64, N 12288: 27.0 -> 24.5 us; 128 rows of 16, rank 128: 48 -> 34; 256 rows of one, rank 64, N 6144:
+// 74 -> 22; 16 rows of 16, rank 16, N 6144: 8.1 -> 8.6.
 template <bool BF, int OUT>
-__global__ void __launch_bounds__(kLoraThreads, 4) lora_few_kernel(const __grid_constant__ qgemv_lora_t p, const LoraWork work, int slots, int shares) {
+__global__ void __launch_bounds__(kLoraThreads, 4) lora_few_kernel(const __grid_constant__ qgemv_lora_t p, const LoraWork work) {
   constexpr int kParts = lora_parts(BF);
   extern __shared__ __align__(16) uint8_t dyn[];
   LoraFewSmem& sm = *reinterpret_cast<LoraFewSmem*>(dyn);
-  __shared__ LoraChunk chunk;
+  __shared__ LoraItems list[kLoraFewRows / kLoraChunk];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
-  const int share = static_cast<int>(blockIdx.x) % shares, slot = static_cast<int>(blockIdx.x) / shares % slots;
-  if (warp == 0) lora_groups(p, static_cast<int64_t>(static_cast<int>(blockIdx.x) / shares / slots) * kLoraChunk, chunk, nullptr);
+  const int tiles = static_cast<int>((p.N + 31) / 32), chunks = static_cast<int>((p.rows + kLoraChunk - 1) / kLoraChunk);
+  for (int q = warp; q < chunks; q += kLoraWarps) lora_items(p, static_cast<int64_t>(q) * kLoraChunk, tiles, list[q]);
   __syncthreads();
-  const int64_t tiles = (p.N + 31) / 32;
-  const int t0 = static_cast<int>(tiles * share / shares), t1 = static_cast<int>(tiles * (share + 1) / shares);
+  int64_t total = 0;
+  for (int q = 0; q < chunks; ++q) total += list[q].total;
+  const int cta = static_cast<int>(blockIdx.x);
+  const int64_t each = lora_div(total, static_cast<int>(gridDim.x)), more = total - each * gridDim.x;
+  int64_t lo = each * cta + min(static_cast<int64_t>(cta), more), hi = lo + each + (cta < more ? 1 : 0);  // from the chunk's first unit
   bool waited = false;
-  for (int i = slot; i < chunk.count; i += slots) {
-    const LoraGroup group = chunk.group[i];
-    const int n_tok = group.n, a = group.adapter, r = group.rank;
-    const int* all = chunk.row + group.first;
-    if (r == 0) {  // no adapter: the base itself
-      if (p.base != p.y) {
+  for (int q = 0; q < chunks && hi > 0; lo -= list[q].total, hi -= list[q].total, ++q) {
+    const LoraItems& chunk = list[q];
+    if (lo >= chunk.total) continue;
+    const LoraItem& own = chunk.item[lane];
+    int i = __popc(__ballot_sync(0xffffffffu, lane < chunk.count && own.at + static_cast<int64_t>(own.cost) * tiles <= lo));
+    for (; i < chunk.count && chunk.item[i].at < hi; ++i) {
+      const LoraItem item = chunk.item[i];
+      auto tile_at = [&](int64_t unit) {  // the first that begins at or after it
+        const int64_t in = unit - item.at;
+        return in <= 0 ? 0 : static_cast<int>(min(lora_div(in + item.cost - 1, item.cost), static_cast<int64_t>(tiles)));
+      };
+      const int t0 = tile_at(lo), t1 = tile_at(hi);
+      if (t0 >= t1) continue;
+      const int n = item.n, r = item.rank;
+      const int* rows = chunk.row + item.first;
+      if (r == 0) {  // no adapter: the base itself
         const bool vec = p.y_stride % 4 == 0;
-        for (int t = 0; t < n_tok; ++t)
-          for (int64_t n = int64_t{32} * t0 + 4 * threadIdx.x; n < min(int64_t{32} * t1, p.N); n += 4 * kLoraThreads) {
-            const int64_t at = all[t] * p.y_stride + n;
-            const int left = static_cast<int>(min(p.N - n, int64_t{4}));
-            lora_store4<OUT>(p.y, at, left, vec, p.base ? lora_load4<OUT>(p.base, at, left, vec) : make_float4(0.f, 0.f, 0.f, 0.f));
+        const int64_t end = min(int64_t{32} * t1, p.N);
+        for (int t = 0; t < n; ++t)
+          for (int64_t e0 = int64_t{32} * t0 + 4 * threadIdx.x; e0 < end; e0 += 4 * 4 * kLoraThreads) {
+            float4 v[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const int64_t e = e0 + 4 * kLoraThreads * u;
+              v[u] = p.base && e < end ? lora_load4<OUT>(p.base, rows[t] * p.y_stride + e, static_cast<int>(min(p.N - e, int64_t{4})), vec) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const int64_t e = e0 + 4 * kLoraThreads * u;
+              if (e < end) lora_store4<OUT>(p.y, rows[t] * p.y_stride + e, static_cast<int>(min(p.N - e, int64_t{4})), vec, v[u]);
+            }
           }
+        continue;
       }
-      continue;
-    }
-    const uint16_t* B = static_cast<const uint16_t*>(p.B) + static_cast<int64_t>(a) * p.N * p.rank;
-    for (int k0 = 0; k0 < n_tok; k0 += 8) {
-      const int n = min(n_tok - k0, 8);
-      LoraStream<BF, OUT> stream(p, sm, all + k0, B, r, n, t0, t1);
+      LoraStream<BF, OUT> stream(p, sm, rows, static_cast<const uint16_t*>(p.B) + static_cast<int64_t>(item.adapter) * p.N * p.rank, r, n, t0, t1);
       stream.begin();
       if (!waited) pdl_wait();  // for the sums
       waited = true;
       const int blocks = (r + 31) / 32;
-      for (int q = warp; q < blocks * kParts; q += kLoraWarps) {
-        const int b = q / kParts, part = q - b * kParts;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (g < n) v = __ldcg(work.parts + (static_cast<int64_t>(all[k0 + g]) * work.blocks + b) * (4 * kParts) + part * 4 + c);
-        sm.parts[b][part][lane] = v;
+      uint4 v[kParts];  // at most 4 kParts operands of four warps
+      const uint4* parts = work.parts + static_cast<int64_t>(rows[g < n ? g : 0]) * work.blocks * (4 * kParts) + c;
+#pragma unroll
+      for (int u = 0; u < kParts; ++u) {
+        const int e = warp + kLoraWarps * u;
+        v[u] = g < n && e < blocks * kParts ? __ldcg(parts + 4 * e) : make_uint4(0, 0, 0, 0);
       }
-      if (threadIdx.x < 8) sm.factor[threadIdx.x] = static_cast<int>(threadIdx.x) < n ? __ldcg(&work.row[all[k0 + threadIdx.x]].factor) : 0.f;
+      if (threadIdx.x < 8) sm.factor[threadIdx.x] = static_cast<int>(threadIdx.x) < n ? __ldcg(&work.row[rows[threadIdx.x]].factor) : 0.f;
+#pragma unroll
+      for (int u = 0; u < kParts; ++u) {
+        const int e = warp + kLoraWarps * u;
+        if (e < blocks * kParts) sm.parts[e / kParts][e % kParts][lane] = v[u];
+      }
       __syncthreads();
       stream.run(t0);
       __syncthreads();

@@ -16,7 +16,8 @@ inline int64_t kv_elem_bytes(const qgemv_kv_cache_t& c) { return c.type == QGEMV
 // kernel launched here waits (pdl_wait) before it touches memory, and lets the next one start in turn.  Among
 // small launches this takes the launch latency out of the stream (1.5 us each).
 inline bool launch_dependent(const void* fn, dim3 grid, int threads, size_t smem, int cluster, void** args, cudaStream_t stream) {
-  if (smem > 48 * 1024 && cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess) {
+  // up to 48 KB, with what the kernel has statically (none more than 24 KB beside dynamic memory), need no request
+  if (smem > 24 * 1024 && cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess) {
     cudaGetLastError();
     return false;
   }
