@@ -237,17 +237,25 @@ __device__ __forceinline__ uint4 pack8(int type, const float (&v)[8]) {
   return make_uint4(pack2(type, v[0], v[1]), pack2(type, v[2], v[3]), pack2(type, v[4], v[5]), pack2(type, v[6], v[7]));
 }
 
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+  return m;
+}
+
 // A CTA (or gridDim.y, where tokens are few) per token: the D / 8 threads of a head are neighbours in a warp and take the token's heads (q, then
 // k, then v) in turn, so that slot, position and angles are read once.  Bound by the bytes of q, k and v: the
 // reads of kU heads are in flight together, and the first of them before slot and position are known.
-// Eight CTAs of four warps on an SM: 8191 tokens of 48 bf16 heads of 128 into e4m3 36.6 us (5.2 TB/s;
-// 40.4 us as five CTAs of eight warps), into bf16 41.3 us; 64 tokens of fp32 rows 2.0 us in a graph.
+// Eight CTAs of four warps on an SM: 8191 tokens of 48 bf16 heads of 128 into e4m3 36.4 us (5.2 TB/s;
+// 40.4 us as five CTAs of eight warps, 38.3 as CTAs that walk over the tokens; six heads in flight spill), into
+// bf16 40.4 us (41.5 with the pairs' other halves read instead of exchanged among the lanes); 4096 tokens of fp32
+// rows into fp16 27.9 us; 64 tokens of them 2.5 us in a graph.
 constexpr int kStoreThreads = 128;
 
 template <int T, int D, bool INTER>  // INTER: pairs of neighbours
 __global__ void __launch_bounds__(kStoreThreads, T == QGEMV_OUT_F32 ? 6 : 8) kv_store_kernel(const __grid_constant__ qgemv_kv_store_t p, int* err) {
   constexpr int L = D / 8;  // threads per head
-  constexpr int kU = T == QGEMV_OUT_F32 ? 2 : 3;
+  constexpr int kU = 3;
   const int hq = p.q_out ? p.q_heads : 0, hk = p.cache.kv_heads;
   const int heads = hq + 2 * hk, step = static_cast<int>(blockDim.x * gridDim.y) / L;
   const int64_t t = blockIdx.x;
@@ -255,23 +263,22 @@ __global__ void __launch_bounds__(kStoreThreads, T == QGEMV_OUT_F32 ? 6 : 8) kv_
   const int half = p.rot_dim / 2;
   const bool first = d < half;
   const bool turns = p.rope && d < p.rot_dim;
-  // element of the head's other half that this thread's first one is paired with
-  const int mate = first ? d + half : d - half;
+  // the lanes of this head, and that of them whose elements this thread's are paired with
+  const int lane = threadIdx.x & 31;
+  const uint32_t mates = L == 32 ? 0xffffffffu : ((1u << (L & 31)) - 1) << (lane / L * L);
+  const int mate = !turns ? lane : first ? lane + half / 8 : lane - half / 8;
   constexpr int kEl = T == QGEMV_OUT_F32 ? 4 : 2;
   // this thread's elements of the token's first q, k and v head; the heads are numbered through
   const uint8_t* q_at = static_cast<const uint8_t*>(p.q) + (t * p.q_stride + d) * kEl;
   const uint8_t* k_at = static_cast<const uint8_t*>(p.k) + (t * p.k_stride + d) * kEl - hq * (D * kEl);
   const uint8_t* v_at = static_cast<const uint8_t*>(p.v) + (t * p.v_stride + d) * kEl - (hq + hk) * (D * kEl);
-  const int to_mate = (mate - d) * kEl;
-  Raw8<T> v[kU], o[kU];
+  Raw8<T> v[kU];
   auto read = [&](int h0) {
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       const int head = h0 + u * step;
       if (head >= heads) break;
-      const uint8_t* at = (head < hq ? q_at : head < hq + hk ? k_at : v_at) + head * (D * kEl);
-      v[u] = load_raw<T>(at);
-      if (!INTER && turns && head < hq + hk) o[u] = load_raw<T>(at + to_mate);
+      v[u] = load_raw<T>((head < hq ? q_at : head < hq + hk ? k_at : v_at) + head * (D * kEl));
     }
   };
   pdl_launch_dependents();
@@ -298,8 +305,8 @@ __global__ void __launch_bounds__(kStoreThreads, T == QGEMV_OUT_F32 ? 6 : 8) kv_
       const float4 a = *reinterpret_cast<const float4*>(tab + d / 2), b = *reinterpret_cast<const float4*>(tab + half + d / 2);
       c[0] = a.x, c[1] = a.y, c[2] = a.z, c[3] = a.w, s[0] = b.x, s[1] = b.y, s[2] = b.z, s[3] = b.w;
     } else {
-      to_float<QGEMV_OUT_F32>(load_raw<QGEMV_OUT_F32>(reinterpret_cast<const uint8_t*>(tab + (first ? d : mate))), c);
-      to_float<QGEMV_OUT_F32>(load_raw<QGEMV_OUT_F32>(reinterpret_cast<const uint8_t*>(tab + half + (first ? d : mate))), s);
+      to_float<QGEMV_OUT_F32>(load_raw<QGEMV_OUT_F32>(reinterpret_cast<const uint8_t*>(tab + (first ? d : d - half))), c);
+      to_float<QGEMV_OUT_F32>(load_raw<QGEMV_OUT_F32>(reinterpret_cast<const uint8_t*>(tab + half + (first ? d : d - half))), s);
     }
   }
   const int el = p.cache.type == QGEMV_KV_E4M3 ? 1 : 2;
@@ -312,19 +319,31 @@ __global__ void __launch_bounds__(kStoreThreads, T == QGEMV_OUT_F32 ? 6 : 8) kv_
       if (head >= heads) break;
       float x[8];
       to_float<T>(v[u], x);
-      if (turns && pos >= 0 && head < hq + hk) {
+      if (p.rope && pos >= 0 && head < hq + hk) {
         if constexpr (INTER) {
+          if (turns) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float a = x[2 * j], b = x[2 * j + 1];
-            x[2 * j] = a * c[j] - b * s[j];
-            x[2 * j + 1] = b * c[j] + a * s[j];
+            for (int j = 0; j < 4; ++j) {
+              const float a = x[2 * j], b = x[2 * j + 1];
+              x[2 * j] = a * c[j] - b * s[j];
+              x[2 * j + 1] = b * c[j] + a * s[j];
+            }
           }
         } else {
-          float y[8];
-          to_float<T>(o[u], y);
+          Raw8<T> o;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) x[j] = first ? x[j] * c[j] - y[j] * s[j] : x[j] * c[j] + y[j] * s[j];
+          for (int j = 0; j < static_cast<int>(sizeof(o.v) / 16); ++j) {
+            o.v[j].x = __shfl_sync(mates, v[u].v[j].x, mate);
+            o.v[j].y = __shfl_sync(mates, v[u].v[j].y, mate);
+            o.v[j].z = __shfl_sync(mates, v[u].v[j].z, mate);
+            o.v[j].w = __shfl_sync(mates, v[u].v[j].w, mate);
+          }
+          if (turns) {
+            float y[8];
+            to_float<T>(o, y);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = first ? x[j] * c[j] - y[j] * s[j] : x[j] * c[j] + y[j] * s[j];
+          }
         }
       }
       if (head < hq) {
@@ -343,14 +362,11 @@ __global__ void __launch_bounds__(kStoreThreads, T == QGEMV_OUT_F32 ? 6 : 8) kv_
         *reinterpret_cast<uint4*>(to) = pack8(p.cache.type, x);
         continue;
       }
-      float top = 0.f;
-      bool nan = false;
+      float top = 0.f;  // NaN where one of them is
 #pragma unroll
-      for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[j])), nan |= x[j] != x[j];
-      if (nan) top = __int_as_float(0x7f800000);
-      const uint32_t mates = L == 32 ? 0xffffffffu : ((1u << (L & 31)) - 1) << ((threadIdx.x & 31) / L * L);
+      for (int j = 0; j < 8; ++j) top = max_nan(top, fabsf(x[j]));
 #pragma unroll
-      for (int k = L / 2; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(mates, top, k));
+      for (int k = L / 2; k > 0; k >>= 1) top = max_nan(top, __shfl_xor_sync(mates, top, k));
       float scale = __fdiv_rn(top, 448.f);
       if (!(scale > 0.f && scale < __int_as_float(0x7f800000))) scale = 1.f;
       scale = fmaxf(scale, 1.17549435e-38f);  // its reciprocal stays finite
