@@ -434,7 +434,8 @@ qgemv_status_t qgemv_kv_store(qgemv_handle_t h, const qgemv_kv_store_t* store, c
  *   lse           fp32 [requests][q_heads], or NULL.
  * Scores, the softmax and the sums are held in fp32 (16-bit products are exact); the weights
  * enter the second product as two 16-bit parts.  What lies in the cache outside the tokens
- * that a row sees, NaN included, does not reach it.  Deterministic: the same inputs give the
+ * that a row sees, NaN included, does not reach it; an infinite value that it sees gives NaN in
+ * its element (the two parts of a weight may differ in sign).  Deterministic: the same inputs give the
  * same bits.  Uses the handle's workspace like qgemv_run.  q_heads a multiple of kv_heads;
  * out must not overlap q. */
 typedef struct {
@@ -469,7 +470,8 @@ qgemv_status_t qgemv_attn_decode(qgemv_handle_t h, const qgemv_attn_decode_t* at
  *   scales        [adapters] fp32; NULL: 1.
  *   base, y       [rows][N] of type `out`, row m at m * y_stride (both).
  * Products are exact, sums in fp32; the inner sums enter the second product in full fp32
- * precision (two or three 16-bit parts); y is rounded once.  Deterministic.  rank a multiple
+ * precision (two or three 16-bit parts); y is rounded once.  Infinities and NaN in an adapter or
+ * a row of x make the results that use them infinite or NaN, and no others.  Deterministic.  rank a multiple
  * of 8, 8 .. 128; K a multiple of 8; x, A, B, base and y 16-byte aligned, x_stride a multiple
  * of 8. */
 typedef struct {

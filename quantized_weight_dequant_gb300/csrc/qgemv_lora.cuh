@@ -19,7 +19,7 @@
 //    its row: the order of k within a 32-wide block is the same permutation on both sides, so no shared
 //    memory or ldmatrix is needed for A, B or x.  B's rows are dealt to the two 8-wide halves of a 16-row
 //    tile so that a lane ends up with four consecutive outputs of a token.
-// Measured: one row of rank 16, K 4096, N 6144: 6.8 us, the latency of two launches; 64 rows of 48 adapters of
+// Measured: one row of rank 16, K 4096, N 6144: 6.5 us, the latency of two launches; 64 rows of 48 adapters of
 // ranks up to 64, K 4096, N 12288: 24.5 us (7 of them the sums; the outputs' CTAs take 4 us to begin, and rows
 // of short ranks cost whole 64-byte pieces of memory); 2048 rows of 4, rank 32, N 14336: 49.2 us (sums 12,
 // outputs 37 at 6.3 TB/s).
