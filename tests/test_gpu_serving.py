@@ -383,6 +383,15 @@ def test_attention_of_many_ragged_requests(h, n, hi, hq, hk, dim, typ, page):
     check_attend(got, lse, q, ref, scale)
 
 
+@pytest.mark.parametrize("n,length,hq,hk,dim,typ", [
+    (64, 480, 32, 8, 128, "bf16"), (64, 481, 16, 8, 128, "f16"), (40, 1500, 16, 8, 256, "e4m3"), (20, 450, 8, 2, 128, "e4m3")])
+def test_attention_of_requests_of_one_length(h, n, length, hq, hk, dim, typ):
+    """Heads as long as the longest that stay whole, one token longer, and where some of the GPU is idle."""
+    got, lse, q, ref, scale, _ = attend_case(h, [length] * n, hq, hk, dim, typ, "f16" if typ == "e4m3" else typ, 16, seed=length)
+    check_attend(got, lse, q, ref, scale)
+    assert qgemv.check_error(h) == qgemv.OK
+
+
 def test_attention_of_one_long_request_split_over_the_gpu(h):
     got, lse, q, ref, scale, _ = attend_case(h, [100003], 8, 1, 128, "f16", "f16", 16)
     check_attend(got, lse, q, ref, scale)
