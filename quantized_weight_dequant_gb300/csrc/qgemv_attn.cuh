@@ -298,11 +298,11 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t{1023});
   float* heads_mem = reinterpret_cast<float*>(ring + kAttnWarps * S * 2 * Sh::kTile);
   uint8_t* scales_mem = reinterpret_cast<uint8_t*>(heads_mem + kAttnWarps * Sh::kPiece);
-  if (lane < S) mbar_init(smem_u32(&bars_of[warp][lane]), kF8 ? 33 : 1);  // the elected lane, and each for its scales
-  if (lane == 0) {
-    piece_of[2 * warp].r = piece_of[2 * warp + 1].r = -1;
-    fence_mbar_init();
+  if (lane < S) {
+    mbar_init(smem_u32(&bars_of[warp][lane]), kF8 ? 33 : 1);  // the elected lane, and each for its scales
+    fence_mbar_init();  // by every lane that made one: a fence orders its own thread's before the copies' signals
   }
+  if (lane == 0) piece_of[2 * warp].r = piece_of[2 * warp + 1].r = -1;
   if (threadIdx.x < 2)
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(threadIdx.x ? &map_v : &map_k)) : "memory");
 
