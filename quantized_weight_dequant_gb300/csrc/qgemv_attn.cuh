@@ -26,12 +26,15 @@
 //    Measured: 32 requests of 24 to 44 thousand tokens, 64 query and 8 key-value heads, bf16:
 //    621 us, 6.97 TB/s; 16 requests of 9 to 70 thousand in e4m3: 165 us, 6.2 TB/s; 64 requests of
 //    1 to 6000 in bf16: 40 us, 4.7 TB/s; one request of 1000 in fp16: 12 us, all latency.
-//  * Precision.  A weight enters the second product as the sum of two 16-bit values.  With at
-//    most 8 heads in a group the low parts are rows 8..15 of the same instruction, which would
+//  * Precision.  A weight enters the second product as the sum of two 16-bit values: 16 bits of it in
+//    bf16, 2^-17 against the output's 2^-9, and 22 in fp16.  fp16's steps end at 2^-24, so there weights, at
+//    most 1, are taken times 2^14 and the output divided by it: below 2^-38 of the largest they are rounded
+//    away, where they are counted in l (times 1, that was 2^-24: 4000 tokens 17.5 nats below one of value 0 gave 0).
+//    With at most 8 heads in a group the low parts are rows 8..15 of the same instruction, which would
 //    be empty otherwise; with 9..16 they are a second instruction.
 //  * 8-bit caches: codes are converted to fp16 in registers (exactly); key scales multiply the
 //    scores, value scales the weights.  There m follows the largest s_t log2e + log2 vscale_t, so that the
-//    weights p_t vscale_t end at 1 and fp16 holds them whatever the scales; l is counted from the same m.
+//    weights p_t vscale_t end at 1 (before the 2^14) and fp16 holds them whatever the scales; l is counted from the same m.
 //  * Join.  A (request, head) that lies inside one warp's share is written by that warp.
 //    Others leave (m, l, O) pieces: in shared memory, which the CTA joins in token order, and
 //    where CTAs share one in the workspace, which the CTA that arrives last joins in CTA order.
@@ -281,6 +284,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
     attn_decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const __grid_constant__ AttnArgs p) {
   using Sh = AttnShape<D, KT, MR>;
   constexpr bool kBF = KT == QGEMV_KV_BF16, kF8 = KT == QGEMV_KV_E4M3;
+  constexpr float kLift = kBF ? 1.f : 16384.f;  // what the weights are multiplied by for the second product
   constexpr int TT = Sh::kTT, S = Sh::kStages, NT = TT / 8;  // NT: 8-token column tiles of the scores
   constexpr int OT = D / 8;                                  // 8-wide column tiles of the output
   extern __shared__ uint8_t dyn[];
@@ -612,7 +616,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
     for (int j = 0; j < MR / 8; ++j) {
       const int g = row + 8 * j;
       const bool there = g0 + g < p.group;
-      const float f = whole ? (l[j] != 0.f ? 1.f / l[j] : 0.f) : 1.f;
+      const float f = whole ? (l[j] != 0.f ? 1.f / kLift / l[j] : 0.f) : 1.f;
       if (quad == 0) {
         if (!whole)
           piece[g] = m[j], piece[MR + g] = l[j];
@@ -761,8 +765,8 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
       for (int t = 0; t < NT; ++t) {
         const float a = ex2(sc[t][2 * j] - base), b = ex2(sc[t][2 * j + 1] - base);
         l[j] += a + b;
-        sc[t][2 * j] = kF8 ? a * vsc[t].x : a;
-        sc[t][2 * j + 1] = kF8 ? b * vsc[t].y : b;
+        sc[t][2 * j] = (kF8 ? a * vsc[t].x : a) * kLift;
+        sc[t][2 * j + 1] = (kF8 ? b * vsc[t].y : b) * kLift;
       }
     }
     if (__any_sync(0xffffffffu, moved)) {
@@ -888,7 +892,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, KT, MR>::kCtasPerSm
         if (d == 0) to[g] = m, to[MR + g] = l;
         *reinterpret_cast<float4*>(to + 2 * MR + g * D + d) = o;
       } else {
-        const float f = l != 0.f ? 1.f / l : 0.f;
+        const float f = l != 0.f ? 1.f / kLift / l : 0.f;
         const int64_t at = t.r * p.out_stride + static_cast<int64_t>(kv * p.group + g0 + g) * D + d;
         attn_store2(p, at, o.x * f, o.y * f);
         attn_store2(p, at + 2, o.z * f, o.w * f);

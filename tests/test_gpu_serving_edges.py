@@ -7,7 +7,8 @@ import pytest
 import torch
 
 from quantized_weight_dequant_gb300 import qgemv
-from test_gpu_serving import attend_case, check_attend, h  # noqa: F401
+from test_gpu_serving import (F8, HALF_ULP, TINY, attend_case, attend_reference, check_attend, gen, h, ints, make_cache,  # noqa: F401
+                              randn, steps, within)
 
 pytestmark = pytest.mark.gpu
 
@@ -27,3 +28,81 @@ def test_the_first_copies_of_every_stage_are_waited_for(h, typ, dim):  # noqa: F
             qgemv.attn_decode(h, d)
             assert torch.equal(got, first)
     assert qgemv.check_error(h) == qgemv.OK
+
+
+# ------------------------------------------------------------------------------ attention: weights far below the largest
+def sink_case(g, typ, gaps, page, dim, pages):
+    """A cache of `pages` pages, whose token 0 scores gaps[i] above all others against query i and has the value 0."""
+    kc, vc, ks, vs = make_cache(g, typ, pages, 1, page, dim)
+    v = 1 + 0.25 * randn(g, pages, 1, page, dim)
+    k = torch.zeros_like(v)
+    v[0, 0, 0], k[0, 0, 0, 0] = 0, 1
+    if typ == "e4m3":
+        for c, x in ((kc, k), (vc, v)):
+            c.copy_(x.to(F8).view(torch.uint8))
+        ks.fill_(1)
+        vs.fill_(1)
+        k, v = k.to(F8).double(), v.to(F8).double()
+    else:
+        kc.copy_(k)
+        vc.copy_(v)
+        k, v = kc.double(), vc.double()
+    q = torch.zeros(1, len(gaps), dim, device="cuda", dtype=torch.bfloat16 if typ == "bf16" else torch.float16)
+    q[0, :, 0] = torch.tensor(gaps, device="cuda").to(q.dtype)
+    return kc, vc, ks, vs, k[:, 0], v[:, 0], q
+
+
+@pytest.mark.parametrize("typ", ["f16", "bf16", "e4m3"])
+@pytest.mark.parametrize("heads", [8, 12])
+def test_many_small_weights_beside_one_large_add_up(h, typ, heads):  # noqa: F811
+    """One token of value 0 outweighs each of thousands of others by 10 to 22 nats: what is left of the output is
+    theirs alone, each with a weight down to 2^-32 of the largest, which fp16 parts round to 2^-39 of it.  So many
+    requests that most (request, head)s are one warp's, in which the large one comes first."""""
+    page, dim, n, requests = 64, 64, 4003, 1500
+    gaps = [10 + 12 * i / (heads - 1) for i in range(heads)]
+    kc, vc, ks, vs, k, v, q = sink_case(gen(41), typ, gaps, page, dim, 9)
+    row = torch.cat([torch.zeros(1, device="cuda"), 1 + torch.arange(-(-n // page) - 1, device="cuda") % 8]).int()
+    table = row[None].repeat(requests, 1)
+    out, lse = torch.empty(requests, heads, dim, device="cuda", dtype=q.dtype), torch.empty(requests, heads, device="cuda")
+    qgemv.attn_decode(h, qgemv.attn_decode_desc(qgemv.kv_cache(kc, vc, ks, vs), q.repeat(requests, 1, 1), table, ints([n] * requests),
+                                                out, 1.0, lse=lse))
+    assert qgemv.check_error(h) == qgemv.OK
+    kk, vv = (x[row.long()].reshape(-1, dim)[:n] for x in (k, v))
+    o, want, pv, qk = attend_reference(q[0].double(), kk, vv, 1.0)
+    score = steps(dim) * qk + 2.0 ** -21 * qk
+    tokens = steps(n) + 2.0 ** -20
+    within(lse, want, score + tokens + 2.0 ** -22 * want.abs(), "lse")
+    lost = n * 2.0 ** -39 * vv.abs().amax()
+    within(out, o, HALF_ULP[out.dtype] * o.abs() + TINY[out.dtype] + (2 * score[:, None] + 2 * tokens + 2.0 ** -16) * pv + lost, "out")
+
+
+@pytest.mark.parametrize("order", [1, -1])
+def test_small_value_scales_beside_large_ones_keep_their_part(h, order):  # noqa: F811
+    """Value scales 2^60 apart, where the tokens of the largest have zeros: a weight times its scale is rounded to
+    2^-25 beside a largest of 2^14, by each of the n tokens and for the largest code."""
+    g = gen(22)
+    n, page, dim = 200, 16, 64
+    kc, vc, ks, vs = make_cache(g, "e4m3", 13, 1, page, dim)
+    k, v = ((randn(g, n, dim) * 100).clamp(-440, 440).to(F8) for _ in range(2))
+    size = torch.linspace(-50, 10, n, device="cuda") * order
+    sk, sv = torch.full((n,), 0.01, device="cuda"), torch.exp2(size)
+    v = torch.where((size > -9)[:, None] & (torch.arange(dim, device="cuda") % 2 == 1), torch.zeros((), device="cuda"), v.float()).to(F8)
+    t = torch.arange(n, device="cuda")
+    kc[t // page, 0, t % page], vc[t // page, 0, t % page] = k.view(torch.uint8), v.view(torch.uint8)
+    ks[t // page, 0, t % page], vs[t // page, 0, t % page] = sk, sv
+    q = (randn(g, 1, 4, dim) * 0.5).half()
+    out = torch.empty_like(q)
+    table = torch.arange(13, dtype=torch.int32, device="cuda")[None].contiguous()
+    # so many requests of it that most heads are one warp's
+    many, outs = q.repeat(1500, 1, 1), out.repeat(1500, 1, 1)
+    qgemv.attn_decode(h, qgemv.attn_decode_desc(qgemv.kv_cache(kc, vc, ks, vs), many, table.repeat(1500, 1), ints([n] * 1500), outs, 0.5))
+    kk, vv = k.double() * sk.double()[:, None], v.double() * sv.double()[:, None]
+    o, _, pv, qk = attend_reference(q[0].double(), kk, vv, 0.5)
+    score = steps(dim) * qk + 2.0 ** -21 * qk
+    p = torch.softmax(q[0].double() @ kk.t() * 0.5, -1)
+    lost = n * 2.0 ** -39 * 448 * (p * sv.double()).amax(-1)
+    tol = HALF_ULP[out.dtype] * o.abs() + TINY[out.dtype] + (2 * score[:, None] + 2 * steps(n) + 2.0 ** -16) * pv + lost[:, None]
+    # outputs past fp16's range are infinities
+    far, inside = o.abs() - tol >= 65520, o.abs() + tol < 65504
+    assert torch.equal(outs[:, far].double(), (torch.sign(o[far]) * math.inf).expand(1500, -1))
+    within(outs[:, inside], o[inside], tol[inside], "out")
