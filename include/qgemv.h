@@ -470,8 +470,8 @@ qgemv_status_t qgemv_attn_decode(qgemv_handle_t h, const qgemv_attn_decode_t* at
  *                 in A and B past an adapter's rank does not reach the result.
  *   scales        [adapters] fp32; NULL: 1.
  *   base, y       [rows][N] of type `out`, row m at m * y_stride (both).
- * Products are exact, sums in fp32; the inner sums enter the second product in full fp32
- * precision (two or three 16-bit parts); y is rounded once.  Infinities and NaN in an adapter or
+ * Products are exact, sums in fp32; the inner sums enter the second product as two or three 16-bit
+ * parts, with at least 21 bits of each whatever the size of the row's others; y is rounded once.  Infinities and NaN in an adapter or
  * a row of x make the results that use them infinite or NaN, and no others.  Deterministic.  rank a multiple
  * of 8, 8 .. 128; K a multiple of 8; x, A, B, base and y 16-byte aligned, x_stride a multiple
  * of 8. */

@@ -77,7 +77,7 @@ extern "C" qgemv_status_t qgemv_run_lora(qgemv_handle_t hh, const qgemv_lora_t* 
   work.blocks = (p.rank + 31) / 32;
   const int64_t row_bytes = int64_t{64} * work.blocks * lora_parts(bf);
   // rows at a time: whole tiles of 16, their sums, factors and adapters in the workspace
-  const int64_t most = static_cast<int64_t>(kWsFloats) * 4 / (row_bytes + 8) / 32 * 32;
+  const int64_t most = static_cast<int64_t>(kWsFloats) * 4 / (row_bytes + static_cast<int64_t>(sizeof(LoraRow))) / 32 * 32;
   work.parts = reinterpret_cast<uint4*>(h->ws);
   for (int64_t m = 0; m < p.rows; m += most) {
     qgemv_lora_t q = p;

@@ -8,7 +8,9 @@
 //    neighbouring rows of the batch, each CTA an eighth of K; the partial sums meet through distributed
 //    shared memory, where each CTA adds those of its own tokens in rank order.  The sums (fp32) are left in
 //    the workspace as what the second product multiplies: two fp16 parts scaled by a power of two per row
-//    (the row's largest in [2^14, 2^15)), or three bf16 parts: at least 21 bits.
+//    (the row's largest in [2^14, 2^15)), or three bf16 parts: at least 21 bits of each sum.  fp16's steps end
+//    at 2^-24, so a row with a sum below 2^-4 (2^-18 of its largest; some in a million of random ones) stays in
+//    fp32, and its outputs take three bf16 parts of the sums times two of B, which hold fp16's 11 bits.
 //  * Outputs of few rows (lora_few_kernel): the rows of one adapter stay, its B streams by, through a
 //    ring of cp.async in which every lane fetches what it will multiply itself (no barrier, no
 //    registers).  All CTAs run at once and have equal shares of the tiles of all rows.
@@ -43,11 +45,12 @@ constexpr int kLoraLd = kLoraMaxRank + 4;  // floats per token of the sums in sh
 constexpr int kLoraWarps = 4;
 constexpr int kLoraThreads = 32 * kLoraWarps;
 
-// What a launch keeps of a row beside its sums: its adapter (-1: none, or one of rank 0), and the adapter's
-// scale over the parts' power of two.
-struct __align__(8) LoraRow {
+// What a launch keeps of a row beside its sums: its adapter (-1: none, or one of rank 0), the adapter's scale over
+// the parts' power of two, and whether the two parts are not fp16 but the halves of fp32 sums (wide).
+struct __align__(16) LoraRow {
   int adapter;
   float factor;
+  int wide, pad;
 };
 // The rows of a launch in the workspace: per row, the parts of its sums (blocks of 32 ranks, kParts, four
 // lanes of 16 bytes).
@@ -210,6 +213,34 @@ __device__ __forceinline__ void lora_mask(uint4 (&w)[4], int j, int r) {
   }
 }
 
+// The second product of wide rows: eight sums of a row in a lane (their high and low halves) as three bf16 parts, and
+// two rows of B (fp16 pairs) as two, whose products are added to acc.  Few rows come here, so it costs what it costs.
+struct LoraWide {
+  uint32_t part[3][4];
+  __device__ __forceinline__ LoraWide(const uint4& high, const uint4& low) {
+    const uint32_t h[4] = {high.x, high.y, high.z, high.w}, l[4] = {low.x, low.y, low.z, low.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float a = __uint_as_float(h[i] << 16 | (l[i] & 0xffffu)), b = __uint_as_float((h[i] & 0xffff0000u) | l[i] >> 16);
+#pragma unroll
+      for (int q = 0; q < 3; ++q) {
+        part[q][i] = pair16<true>(a, b);
+        const float2 f = unpair16<true>(part[q][i]);
+        a -= f.x, b -= f.y;
+      }
+    }
+  }
+};
+// acc += (operand rows 0..7: a, 8..15: b; words 2 i and 2 i + 1) times the B rows' words u, v.
+__device__ __forceinline__ void lora_add_wide(float (&acc)[4], const uint32_t (&a)[4], const uint32_t (&b)[4], int i, uint32_t u, uint32_t v) {
+  const float2 fu = unpair16<false>(u), fv = unpair16<false>(v);
+  uint32_t u0, u1, v0, v1;
+  split16<true>(fu.x, fu.y, u0, u1);
+  split16<true>(fv.x, fv.y, v0, v1);
+  mma16816<true>(acc, a[2 * i], b[2 * i], a[2 * i + 1], b[2 * i + 1], u0, v0);
+  mma16816<true>(acc, a[2 * i], b[2 * i], a[2 * i + 1], b[2 * i + 1], u1, v1);
+}
+
 // First product over the 32-wide blocks b0 .. b1 of K for ranks j0 .. j0 + 16 RT - 1 and 8 TG tokens, the
 // blocks dealt to the warps in turn; the warps' sums go to sm.part.  Lane (g, c) = (lane / 4, lane % 4).
 template <bool BF, int TG>
@@ -312,6 +343,7 @@ __global__ void __launch_bounds__(kLoraThreads, 4) lora_sums_kernel(const __grid
           for (int c = 0; c < kLoraCluster; ++c) v[0] += q[c].x, v[1] += q[c].y, v[2] += q[c].z, v[3] += q[c].w;
         }
         float by = 1.f, back = 1.f;
+        bool wide = false;
         if constexpr (!BF) {
           float top = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
 #pragma unroll
@@ -321,21 +353,33 @@ __global__ void __launch_bounds__(kLoraThreads, 4) lora_sums_kernel(const __grid
             by = __int_as_float((127 + 141 - ex) << 23);
             back = __int_as_float((127 - 141 + ex) << 23);
           }
+          bool small = false;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) small |= v[e] != 0.f && fabsf(v[e]) * by < 0.0625f;
+          wide = __any_sync(0xffffffffu, small);
         }
         const int64_t m = all[k0 + tok];
         if (lane < 8 * work.blocks) {
           uint2* to = reinterpret_cast<uint2*>(work.parts + (m * work.blocks + lane / 8) * (4 * kParts) + lane % 8 / 2) + lane % 2;
+          if (wide) {
+            uint32_t u[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] *= by;
+            for (int e = 0; e < 4; ++e) u[e] = __float_as_uint(v[e]);
+            to[0] = make_uint2(__byte_perm(u[0], u[1], 0x7632), __byte_perm(u[2], u[3], 0x7632));
+            to[8] = make_uint2(__byte_perm(u[0], u[1], 0x5410), __byte_perm(u[2], u[3], 0x5410));
+          } else {
 #pragma unroll
-          for (int q = 0; q < kParts; ++q) {
-            const uint32_t u0 = pair16<BF>(v[0], v[1]), u1 = pair16<BF>(v[2], v[3]);
-            to[8 * q] = make_uint2(u0, u1);
-            const float2 f0 = unpair16<BF>(u0), f1 = unpair16<BF>(u1);
-            v[0] -= f0.x, v[1] -= f0.y, v[2] -= f1.x, v[3] -= f1.y;
+            for (int e = 0; e < 4; ++e) v[e] *= by;
+#pragma unroll
+            for (int q = 0; q < kParts; ++q) {
+              const uint32_t u0 = pair16<BF>(v[0], v[1]), u1 = pair16<BF>(v[2], v[3]);
+              to[8 * q] = make_uint2(u0, u1);
+              const float2 f0 = unpair16<BF>(u0), f1 = unpair16<BF>(u1);
+              v[0] -= f0.x, v[1] -= f0.y, v[2] -= f1.x, v[3] -= f1.y;
+            }
           }
         }
-        if (lane == 0) work.row[m].factor = scale * back;
+        if (lane == 0) work.row[m].factor = wide ? scale : scale * back, work.row[m].wide = wide;
       }
       cluster_arrive();
       cluster_wait();  // no CTA reads this one's sums: they are used again, or the CTA ends
@@ -355,6 +399,7 @@ struct LoraFewSmem {
   uint4 ring[kLoraWarps][kLoraDepth][kLoraPieces][32];
   uint4 parts[kLoraMaxRank / 32][3][32];  // of the tokens in hand, as a lane's operand
   float factor[8];
+  int wide[8];
 };
 
 template <bool BF, int OUT>
@@ -424,6 +469,7 @@ struct LoraStream {
   __device__ __forceinline__ void run(int t0) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
     const float f = sm.factor[g];
+    const bool wide = !BF && sm.wide[g], any_wide = !BF && __any_sync(0xffffffffu, wide);
     int s = 0;
 #pragma unroll 1
     for (int tile = t0 + warp; tile < t1; tile += kLoraWarps) {
@@ -446,8 +492,25 @@ struct LoraStream {
 #pragma unroll
           for (int h = 0; h < 4; ++h) mma16816<BF>(acc[h >> 1][h & 1], s0.z, s1.z, s0.w, s1.w, w[h].z, w[h].w);
         };
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        if (any_wide) {
+          const uint4 s0 = sm.parts[b][0][lane], s1 = sm.parts[b][1][lane];
+          add(wide ? zero : s0, wide ? zero : s1);
+          const LoraWide of(wide ? s0 : zero, wide ? s1 : zero);
+          constexpr uint32_t none[4] = {0, 0, 0, 0};
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            const uint32_t u[4] = {w[h].x, w[h].y, w[h].z, w[h].w};
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              lora_add_wide(acc[h >> 1][h & 1], of.part[0], of.part[1], i, u[2 * i], u[2 * i + 1]);
+              lora_add_wide(acc[h >> 1][h & 1], of.part[2], none, i, u[2 * i], u[2 * i + 1]);
+            }
+          }
+          continue;
+        }
         add(sm.parts[b][0][lane], sm.parts[b][1][lane]);
-        if constexpr (BF) add(sm.parts[b][2][lane], make_uint4(0, 0, 0, 0));
+        if constexpr (BF) add(sm.parts[b][2][lane], zero);
       }
       if (!y) continue;
 #pragma unroll
@@ -574,7 +637,11 @@ __global__ void __launch_bounds__(kLoraThreads, 4) lora_few_kernel(const __grid_
         const int e = warp + kLoraWarps * u;
         v[u] = g < n && e < blocks * kParts ? __ldcg(parts + 4 * e) : make_uint4(0, 0, 0, 0);
       }
-      if (threadIdx.x < 8) sm.factor[threadIdx.x] = static_cast<int>(threadIdx.x) < n ? __ldcg(&work.row[rows[threadIdx.x]].factor) : 0.f;
+      if (threadIdx.x < 8) {
+        const int4 row = static_cast<int>(threadIdx.x) < n ? __ldcg(reinterpret_cast<const int4*>(&work.row[rows[threadIdx.x]])) : make_int4(0, 0, 0, 0);
+        sm.factor[threadIdx.x] = __int_as_float(row.y);
+        sm.wide[threadIdx.x] = row.z;
+      }
 #pragma unroll
       for (int u = 0; u < kParts; ++u) {
         const int e = warp + kLoraWarps * u;
@@ -645,7 +712,7 @@ __global__ void __launch_bounds__(kLoraThreads, NB == 1 ? 4 : NB == 2 ? 3 : 2)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
         if (m_sums + 8 * h < m_end) cp_async_fill<16>(smem_u32(&st.sums[q][h][lane]), part_at + h * 8 * part_row + q * 4, 16);
-    if (warp == kLoraWarps - 1 && c < 2 && m_sums + 8 * c < m_end) cp_async_fill<8>(smem_u32(&st.row[g + 8 * c]), work.row + m_sums + 8 * c, 8);
+    if (warp == kLoraWarps - 1 && c < 2 && m_sums + 8 * c < m_end) cp_async_fill<16>(smem_u32(&st.row[g + 8 * c]), work.row + m_sums + 8 * c, 16);
     part_at += 16 * part_row;
     m_sums += 16;
     cp_async_commit();
@@ -682,7 +749,7 @@ __global__ void __launch_bounds__(kLoraThreads, NB == 1 ? 4 : NB == 2 ? 3 : 2)
     ask_sums(next);
     LoraRow row[2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) row[h] = m + 8 * h < m_end ? st.row[g + 8 * h] : LoraRow{-1, 0.f};
+    for (int h = 0; h < 2; ++h) row[h] = m + 8 * h < m_end ? st.row[g + 8 * h] : LoraRow{-1, 0.f, 0, 0};
     // One adapter after another, and the rows without one: mostly a single pass, as rows of one adapter follow
     // one another.  A pass has its own sums, of which it writes its rows': an adapter with infinities or NaN
     // makes NaN of the others' rows.
@@ -696,17 +763,32 @@ __global__ void __launch_bounds__(kLoraThreads, NB == 1 ? 4 : NB == 2 ? 3 : 2)
       float acc[2][2][4] = {};
       if (a >= 0) {
         if (a != cur) hold(a);
+        const bool wide[2] = {!BF && in[0] && row[0].wide, !BF && in[1] && row[1].wide}, any_wide = !BF && __any_sync(0xffffffffu, wide[0] || wide[1]);
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
           if (NB == 4 && b == 3 && work.blocks == 3) break;
 #pragma unroll
           for (int q = 0; q < kParts; ++q) {
             const uint4 zero = make_uint4(0, 0, 0, 0);
-            const uint4 s0 = in[0] ? st.sums[b * kParts + q][0][lane] : zero, s1 = in[1] ? st.sums[b * kParts + q][1][lane] : zero;
+            const uint4 s0 = in[0] && !wide[0] ? st.sums[b * kParts + q][0][lane] : zero, s1 = in[1] && !wide[1] ? st.sums[b * kParts + q][1][lane] : zero;
 #pragma unroll
             for (int h = 0; h < 4; ++h) mma16816<BF>(acc[h >> 1][h & 1], s0.x, s1.x, s0.y, s1.y, w[b][h].x, w[b][h].y);
 #pragma unroll
             for (int h = 0; h < 4; ++h) mma16816<BF>(acc[h >> 1][h & 1], s0.z, s1.z, s0.w, s1.w, w[b][h].z, w[b][h].w);
+          }
+          if (any_wide) {
+            const uint4 zero = make_uint4(0, 0, 0, 0);
+            auto of = [&](int half) {
+              return LoraWide(wide[half] ? st.sums[b * kParts][half][lane] : zero, wide[half] ? st.sums[b * kParts + 1][half][lane] : zero);
+            };
+            const LoraWide r0 = of(0), r1 = of(1);
+#pragma unroll
+            for (int q = 0; q < 3; ++q)
+#pragma unroll
+              for (int h = 0; h < 4; ++h) {
+                lora_add_wide(acc[h >> 1][h & 1], r0.part[q], r1.part[q], 0, w[b][h].x, w[b][h].y);
+                lora_add_wide(acc[h >> 1][h & 1], r0.part[q], r1.part[q], 1, w[b][h].z, w[b][h].w);
+              }
           }
         }
       }

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from quantized_weight_dequant_gb300 import qgemv
-from test_gpu_serving import (F8, HALF_ULP, TINY, attend_case, attend_reference, check_attend, gen, h, ints, make_cache,  # noqa: F401
+from test_gpu_serving import (F8, HALF_ULP, TINY, TYPES, attend_case, attend_reference, check_attend, gen, h, ints, make_cache,  # noqa: F401
                               randn, steps, within)
 
 pytestmark = pytest.mark.gpu
@@ -106,3 +106,55 @@ def test_small_value_scales_beside_large_ones_keep_their_part(h, order):  # noqa
     far, inside = o.abs() - tol >= 65520, o.abs() + tol < 65504
     assert torch.equal(outs[:, far].double(), (torch.sign(o[far]) * math.inf).expand(1500, -1))
     within(outs[:, inside], o[inside], tol[inside], "out")
+
+
+# ------------------------------------------------------------------------------ adapters: inner sums far apart
+def spread_case(g, rows, typ, rank, K=64, N=90):
+    """Rows of x with one element each, so that an inner sum is one exact product.  Columns of A from K / 2 on make
+    sums over 2^38 apart, with the inverse in B as far as it goes; every third output has the small ones only."""
+    dt = TYPES[typ]
+    size = torch.exp2(torch.linspace(14, -24, rank, device="cuda"))
+    A = randn(g, 2, rank, K)
+    A[:, :, K // 2:] *= size[:, None]
+    B = randn(g, 2, N, rank) * 0.4 * (1 / size).clamp(2.0 ** -14, 2.0 ** 15)
+    B[:, ::3] *= size < 2.0 ** -10
+    x = torch.zeros(rows, K, device="cuda")
+    x[torch.arange(rows), torch.randint(0, K, (rows,), generator=g, device="cuda")] = randn(g, rows) + 3
+    return x.to(dt), A.to(dt), B.to(dt)
+
+
+def spread_reference(x, A, B, ids):
+    """The outputs in 64 bits and their tolerance: 21 bits of every inner sum, an fp32 sum over them."""
+    low = torch.einsum("mk,mjk->mj", x.double(), A.double()[ids.long()])
+    Bm = B.double()[ids.long()]
+    ref = torch.einsum("mj,mnj->mn", low, Bm)
+    return ref, (2.0 ** -21 + steps(A.shape[1])) * torch.einsum("mj,mnj->mn", low.abs(), Bm.abs()) + 2.0 ** -22 * ref.abs()
+
+
+@pytest.mark.parametrize("typ", ["f16", "bf16"])
+@pytest.mark.parametrize("rows,rank", [(20, 16), (200, 72), (300, 16), (300, 64), (500, 72), (300, 128)])
+def test_inner_sums_far_below_the_rows_largest_keep_their_bits(h, rows, rank, typ):  # noqa: F811
+    g = gen(rows + rank)
+    x, A, B = spread_case(g, rows, typ, rank)
+    ids = (torch.arange(rows, device="cuda") // 3 % 2).int()
+    y = torch.empty(rows, 90, device="cuda")
+    qgemv.run_lora(h, qgemv.lora_desc(x, A, B, ids, y))
+    assert qgemv.check_error(h) == qgemv.OK
+    ref, tol = spread_reference(x, A, B, ids)
+    within(y, ref, tol, "y")
+
+
+@pytest.mark.parametrize("rows", [24, 320])
+def test_a_row_of_far_apart_sums_leaves_its_neighbours_as_they_are(h, rows):  # noqa: F811
+    """The rows of one adapter whose sums are near one another come out bit for bit as without the others."""
+    g = gen(5)
+    x, A, B = spread_case(g, rows, "f16", 32)
+    ids, base = torch.zeros(rows, dtype=torch.int32, device="cuda"), randn(g, rows, 90)
+    near = (x[:, :32] != 0).any(1)
+    alone, together = torch.empty(rows, 90, device="cuda"), torch.empty(rows, 90, device="cuda")
+    qgemv.run_lora(h, qgemv.lora_desc(x, A, B, ids, together, base=base))
+    qgemv.run_lora(h, qgemv.lora_desc(torch.where(near[:, None], x, torch.zeros_like(x)), A, B, ids, alone, base=base))
+    assert torch.equal(alone[near], together[near]) and qgemv.check_error(h) == qgemv.OK
+    assert torch.equal(alone[~near], base[~near])
+    ref, tol = spread_reference(x, A, B, ids)
+    within(together, ref + base.double(), tol + 2.0 ** -22 * base.double().abs(), "y")
