@@ -300,6 +300,12 @@ __device__ __forceinline__ void lora_shrink(const qgemv_lora_t& p, LoraSmem<TG>&
   __syncthreads();
 }
 
+// A finite value past bf16's largest would round to infinity: its first part ends there, the next hold the rest.
+__device__ __forceinline__ float lora_bf16_end(float v) {
+  const float end = __int_as_float(0x7f7f0000);
+  return fabsf(v) < __int_as_float(0x7f800000) ? fminf(fmaxf(v, -end), end) : v;
+}
+
 template <bool BF, int TG>
 __global__ void __launch_bounds__(kLoraThreads, 4) lora_sums_kernel(const __grid_constant__ qgemv_lora_t p, const LoraWork work, int slots, int* err) {
   using Sh = LoraShape<TG>;
@@ -372,7 +378,10 @@ __global__ void __launch_bounds__(kLoraThreads, 4) lora_sums_kernel(const __grid
             for (int e = 0; e < 4; ++e) v[e] *= by;
 #pragma unroll
             for (int q = 0; q < kParts; ++q) {
-              const uint32_t u0 = pair16<BF>(v[0], v[1]), u1 = pair16<BF>(v[2], v[3]);
+              float w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) w[e] = BF && q == 0 ? lora_bf16_end(v[e]) : v[e];
+              const uint32_t u0 = pair16<BF>(w[0], w[1]), u1 = pair16<BF>(w[2], w[3]);
               to[8 * q] = make_uint2(u0, u1);
               const float2 f0 = unpair16<BF>(u0), f1 = unpair16<BF>(u1);
               v[0] -= f0.x, v[1] -= f0.y, v[2] -= f1.x, v[3] -= f1.y;

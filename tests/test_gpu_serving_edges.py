@@ -158,3 +158,24 @@ def test_a_row_of_far_apart_sums_leaves_its_neighbours_as_they_are(h, rows):  # 
     assert torch.equal(alone[~near], base[~near])
     ref, tol = spread_reference(x, A, B, ids)
     within(together, ref + base.double(), tol + 2.0 ** -22 * base.double().abs(), "y")
+
+
+@pytest.mark.parametrize("rows", [5, 300])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_bf16_inner_sums_up_to_the_end_of_fp32_stay_finite(h, rows, sign):  # noqa: F811
+    """Sums of (2 - 2^-9) 2^127, which fp32 holds and bf16 rounds to infinity, brought back by the adapter's scale;
+    beside them, infinite ones stay with their rows."""
+    x, A = torch.zeros(rows, 16, device="cuda"), torch.zeros(1, 8, 16, device="cuda")
+    x[:, 0], x[:, 9] = sign * (2 - 2.0 ** -7) * 2.0 ** 63, sign * 1.5 * 2.0 ** 63
+    A[:, :, 0], A[:, :, 9] = 2.0 ** 64, 2.0 ** 56
+    x[3] *= 4
+    B = torch.zeros(1, 40, 8, device="cuda")
+    B[0, torch.arange(40), torch.arange(40) % 8] = torch.exp2(-torch.arange(40, device="cuda") / 8.0)
+    x, A, B = x.bfloat16(), A.bfloat16(), B.bfloat16()
+    y = torch.empty(rows, 40, device="cuda")
+    scale = torch.full((1,), 2.0 ** -100, device="cuda")
+    ids = torch.zeros(rows, dtype=torch.int32, device="cuda")
+    qgemv.run_lora(h, qgemv.lora_desc(x, A, B, ids, y, scales=scale))
+    ref = (2.0 ** -100 * sign * (2 - 2.0 ** -9) * 2.0 ** 127 * B[0].double().sum(-1)).expand(rows - 1, -1)
+    within(torch.cat([y[:3], y[4:]]), ref, (2.0 ** -21 + steps(8)) * ref.abs(), "y")  # one product each
+    assert not y[3].isfinite().any() and qgemv.check_error(h) == qgemv.OK
