@@ -353,7 +353,7 @@ typedef struct {
  *                 were missing
  * free_pages and *free_count are only read: the caller lowers its count by counts[2].
  * positions, owners and offsets may be NULL.  All pointers device; slots, positions and
- * owners 16-byte aligned.  requests >= 0, page_size >= 1, table_width >= 1 and <= table_stride,
+ * owners 16-byte aligned.  requests 0 .. 2^30, page_size >= 1, table_width >= 1 and <= table_stride,
  * 0 <= capacity < 2^31. */
 typedef struct {
   const int32_t* cached;
@@ -438,7 +438,7 @@ qgemv_status_t qgemv_kv_store(qgemv_handle_t h, const qgemv_kv_store_t* store, c
  * that a row sees, NaN included, does not reach it; an infinite value that it sees gives NaN in
  * its element (the two parts of a weight may differ in sign).  Deterministic: the same inputs give the
  * same bits.  Uses the handle's workspace like qgemv_run.  q_heads a multiple of kv_heads;
- * out must not overlap q. */
+ * requests 0 .. 2^30; out must not overlap q. */
 typedef struct {
   qgemv_kv_cache_t cache;
   const void* q;

@@ -73,7 +73,7 @@ extern "C" qgemv_status_t qgemv_attn_decode(qgemv_handle_t hh, const qgemv_attn_
   const qgemv_attn_decode_t& p = *attn;
   qgemv_status_t st = check_cache(p.cache);
   if (st != QGEMV_OK) return st;
-  if (p.requests < 0 || p.q_heads < 1 || p.q_heads % p.cache.kv_heads || p.table_width < 1 || p.table_stride < p.table_width)
+  if (p.requests < 0 || p.requests > kMaxRequests || p.q_heads < 1 || p.q_heads % p.cache.kv_heads || p.table_width < 1 || p.table_stride < p.table_width)
     return QGEMV_ERR_BAD_SHAPE;
   if (p.type != QGEMV_OUT_F16 && p.type != QGEMV_OUT_BF16) return QGEMV_ERR_INVALID_ARG;
   if (p.cache.type != QGEMV_KV_E4M3 && static_cast<int>(p.cache.type) != static_cast<int>(p.type)) return QGEMV_ERR_INVALID_ARG;

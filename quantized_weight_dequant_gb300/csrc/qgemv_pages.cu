@@ -34,7 +34,7 @@ qgemv_status_t qgemv_page_plan(qgemv_handle_t hh, const qgemv_page_plan_t* plan,
   const Handle* h = handle_of(hh);
   if (!h || !plan) return QGEMV_ERR_INVALID_ARG;
   const qgemv_page_plan_t& p = *plan;
-  if (p.requests < 0 || p.page_size < 1 || p.table_width < 1 || p.table_stride < p.table_width || p.capacity < 0 ||
+  if (p.requests < 0 || p.requests > kMaxRequests || p.page_size < 1 || p.table_width < 1 || p.table_stride < p.table_width || p.capacity < 0 ||
       p.capacity > 0x7fffffff)
     return QGEMV_ERR_BAD_SHAPE;
   if (!p.counts || !p.free_count || (p.capacity > 0 && !p.slots)) return QGEMV_ERR_INVALID_ARG;

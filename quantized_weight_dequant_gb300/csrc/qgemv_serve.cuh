@@ -10,6 +10,9 @@ namespace qg {
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
+// The kernels number requests in 32 bits and step past the last one by up to a block, so the end stays clear of 2^31.
+constexpr int kMaxRequests = 1 << 30;
+
 inline int64_t kv_elem_bytes(const qgemv_kv_cache_t& c) { return c.type == QGEMV_KV_E4M3 ? 1 : 2; }
 
 // A programmatic dependent launch: the kernel may start while the one before it on the stream ends, so every

@@ -179,3 +179,20 @@ def test_bf16_inner_sums_up_to_the_end_of_fp32_stay_finite(h, rows, sign):  # no
     ref = (2.0 ** -100 * sign * (2 - 2.0 ** -9) * 2.0 ** 127 * B[0].double().sum(-1)).expand(rows - 1, -1)
     within(torch.cat([y[:3], y[4:]]), ref, (2.0 ** -21 + steps(8)) * ref.abs(), "y")  # one product each
     assert not y[3].isfinite().any() and qgemv.check_error(h) == qgemv.OK
+
+
+# ------------------------------------------------------------------------------ sizes
+@pytest.mark.parametrize("requests", [2 ** 30 + 1, 2 ** 31 - 128, 2 ** 31 - 1])
+def test_more_requests_than_the_kernels_can_number_are_refused(h, requests):  # noqa: F811
+    def none(*n):
+        return torch.zeros(n, dtype=torch.int32, device="cuda")
+
+    slots = torch.zeros(4, dtype=torch.int64, device="cuda")
+    plan = qgemv.page_plan_desc(none(2), none(2), none(2, 3), none(5), none(1), 16, none(2), slots, none(4))
+    plan.requests = requests
+    assert qgemv.page_plan(h, plan, check=False) == qgemv.ERR_BAD_SHAPE
+    k, q = torch.zeros(3, 2, 16, 64, dtype=torch.float16, device="cuda"), torch.zeros(2, 4, 64, dtype=torch.float16, device="cuda")
+    attend = qgemv.attn_decode_desc(qgemv.kv_cache(k, k.clone()), q, none(2, 3), none(2), torch.empty_like(q), 0.1)
+    attend.requests = requests
+    assert qgemv.attn_decode(h, attend, check=False) == qgemv.ERR_BAD_SHAPE
+    assert qgemv.check_error(h) == qgemv.OK
