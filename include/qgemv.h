@@ -393,7 +393,8 @@ qgemv_status_t qgemv_page_plan(qgemv_handle_t h, const qgemv_page_plan_t* plan, 
  *                 BF16), row t at t * q_out_stride; it must not overlap q, k or v.
  * The rotation is computed in fp32 and rounded once to the cache's or q_out's type.  An E4M3
  * cache gets scale = max|x| / 448 of the token's head (1 where that is 0 or not finite, and at
- * least 2^-126) and the codes e4m3(x * (1 / scale)), rounded to nearest even.
+ * least 2^-126) and the codes e4m3(x / scale), rounded to nearest even; infinities become +-448,
+ * NaN stays NaN.
  * Pointers 16-byte aligned, row strides a multiple of 16 bytes.  slots, positions (and rope)
  * are needed also where no row is rotated. */
 typedef struct {

@@ -370,13 +370,22 @@ __global__ void __launch_bounds__(kStoreThreads, T == QGEMV_OUT_F32 ? 6 : 8) kv_
       float scale = __fdiv_rn(top, 448.f);
       if (!(scale > 0.f && scale < __int_as_float(0x7f800000))) scale = 1.f;
       scale = fmaxf(scale, 1.17549435e-38f);  // its reciprocal stays finite
+      // x / scale rounded once: the product with the reciprocal, then its remainder's share (Markstein, IBM J. Res.
+      // Dev. 34, 1990).  The product alone sends some quotients halfway between two codes to the other one; a division
+      // each costs 3 us of 36.7.
       const float by = __frcp_rn(scale);
+      const bool finite = top < __int_as_float(0x7f800000);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float y = x[j] * by;
+        x[j] = finite ? fmaf(fmaf(-y, scale, x[j]), by, y) : y;
+      }
       uint32_t w[2];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const float* y = x + 4 * j;
-        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[0] * by, y[1] * by), __NV_SATFINITE, __NV_E4M3);
-        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[2] * by, y[3] * by), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[0], y[1]), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[2], y[3]), __NV_SATFINITE, __NV_E4M3);
         w[j] = lo | hi << 16;
       }
       *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);

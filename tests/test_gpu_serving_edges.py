@@ -196,3 +196,28 @@ def test_more_requests_than_the_kernels_can_number_are_refused(h, requests):  # 
     attend.requests = requests
     assert qgemv.attn_decode(h, attend, check=False) == qgemv.ERR_BAD_SHAPE
     assert qgemv.check_error(h) == qgemv.OK
+
+
+# ------------------------------------------------------------------------------ store: codes
+@pytest.mark.parametrize("src", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_e4m3_codes_are_the_rounded_quotients_by_the_scale(h, src, dim):  # noqa: F811
+    """Scale and codes of unrotated heads bit for bit: max|x| / 448 and x / scale, each rounded to fp32 once, and
+    the quotient to e4m3.  Small whole numbers, so that many quotients are near the middle of two codes."""
+    g = gen(dim)
+    t, hk, page = 3000, 4, 16
+    kc, vc, ks, vs = make_cache(g, "e4m3", t // page + 3, hk, page, dim)
+    k = torch.randint(-300, 301, (t, hk, dim), generator=g, device="cuda").to(TYPES[src])
+    v = (randn(g, t, hk, dim) * torch.exp2(torch.randint(-20, 10, (t, hk, 1), generator=g, device="cuda"))).to(TYPES[src])
+    if src == "f32":  # scales down to the least, and values that are not normal
+        v[:40] *= torch.exp2(torch.arange(40, device="cuda") * -3.0)[:, None, None]
+    slots = torch.randperm(kc.shape[0] * page, generator=g, device="cuda")[:t].contiguous()
+    qgemv.kv_store(h, qgemv.kv_store_desc(qgemv.kv_cache(kc, vc, ks, vs), k.flatten(1), v.flatten(1), slots, ints([0] * t)))
+    assert qgemv.check_error(h) == qgemv.OK
+    for x, codes, scales in ((k, kc, ks), (v, vc, vs)):
+        top = x.float().abs().amax(-1)
+        # in 64 bits first: torch divides by a plain number as by its reciprocal
+        scale = torch.where(top > 0, (top.double() / 448).float(), 1.0).clamp(min=2.0 ** -126)
+        at = (slots // page, slice(None), slots % page)
+        assert torch.equal(scales[at], scale)
+        assert torch.equal(codes[at].view(F8).float(), (x.double() / scale[..., None].double()).float().to(F8).float())
