@@ -341,8 +341,9 @@ typedef struct {
  * stack free_pages[0 .. *free_count), in token order, and writes it into the table (other
  * entries of the table are left alone).  A token gets no slot when it lies past `capacity` or
  * past its row of the table, or when the stack is empty; neither do the later tokens of
- * that request.  A negative page in the table where a token's own page should be is reported,
- * and the token gets slot -1.
+ * that request.  A negative page in the table or the stack where a token's own page should be
+ * is reported, and the token gets slot -1; it keeps its position, which later tokens of the
+ * request follow, so lens and counts[1] count it.
  *   lens[r]       cached[r] + the new tokens of r that have a slot: the length to attend over
  *   offsets[r]    number of the first new token of request r; offsets[requests] = their total
  *                 (both at most 2^31 - 1, where larger ones stay)

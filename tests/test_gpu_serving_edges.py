@@ -7,8 +7,8 @@ import pytest
 import torch
 
 from quantized_weight_dequant_gb300 import qgemv
-from test_gpu_serving import (F8, HALF_ULP, TINY, TYPES, attend_case, attend_reference, check_attend, gen, h, ints, make_cache,  # noqa: F401
-                              randn, steps, within)
+from test_gpu_serving import (F8, HALF_ULP, TINY, TYPES, attend_case, attend_reference, check_attend, gen, h, ints,  # noqa: F401
+                              make_cache, plan_on_gpu, randn, steps, within)
 
 pytestmark = pytest.mark.gpu
 
@@ -221,3 +221,16 @@ def test_e4m3_codes_are_the_rounded_quotients_by_the_scale(h, src, dim):  # noqa
         at = (slots // page, slice(None), slots % page)
         assert torch.equal(scales[at], scale)
         assert torch.equal(codes[at].view(F8).float(), (x.double() / scale[..., None].double()).float().to(F8).float())
+
+
+# ------------------------------------------------------------------------------ page plan: broken tables
+def test_page_plan_counts_tokens_whose_page_is_negative(h):  # noqa: F811
+    """Positions go on past a page that the caller's table or stack has wrong: its tokens are not stored, those of
+    the next page are."""
+    got = plan_on_gpu(h, [20, 3], [14, 20], [[7, -1, -1], [5, -1, -1]], [9, -6, 2], 16, 34)
+    assert qgemv.check_error(h) == qgemv.ERR_BAD_INDEX
+    # request 0: tokens 20 .. 31 in page -1, 32 and 33 in page 2; request 1: 3 .. 15 in page 5, 16 .. 22 in page -6
+    assert got["slots"] == [-1] * 12 + [32, 33] + [80 + i for i in range(3, 16)] + [-1] * 7
+    assert got["positions"] == list(range(20, 34)) + list(range(3, 23))
+    assert got["lens"] == [34, 23] and got["counts"] == [34, 34, 2, 0]
+    assert got["table"] == [[7, -1, 2], [5, -6, -1]]
