@@ -437,8 +437,8 @@ qgemv_status_t qgemv_kv_store(qgemv_handle_t h, const qgemv_kv_store_t* store, c
  * Scores, the softmax and the sums are held in fp32 (16-bit products are exact); the weights
  * enter the second product as two 16-bit parts: 16 bits of each with BF16, 22 with F16 and E4M3, where
  * steps end at 2^-38 of the largest weight.  What lies in the cache outside the tokens
- * that a row sees, NaN included, does not reach it; an infinite value that it sees gives NaN in
- * its element (the two parts of a weight may differ in sign).  Deterministic: the same inputs give the
+ * that a row sees, NaN included, does not reach it; an infinite value that it sees makes
+ * its element infinite or NaN (the two parts of a weight may differ in sign).  Deterministic: the same inputs give the
  * same bits.  Uses the handle's workspace like qgemv_run.  q_heads a multiple of kv_heads;
  * requests 0 .. 2^30; out must not overlap q. */
 typedef struct {

@@ -6,9 +6,10 @@ import math
 import pytest
 import torch
 
+import test_gpu_serving
 from quantized_weight_dequant_gb300 import qgemv
 from test_gpu_serving import (F8, HALF_ULP, TINY, TYPES, attend_case, attend_reference, check_attend, gen, h, ints,  # noqa: F401
-                              make_cache, plan_on_gpu, randn, steps, within)
+                              lora_case, make_cache, plan_on_gpu, randn, steps, within)
 
 pytestmark = pytest.mark.gpu
 
@@ -234,3 +235,66 @@ def test_page_plan_counts_tokens_whose_page_is_negative(h):  # noqa: F811
     assert got["positions"] == list(range(20, 34)) + list(range(3, 23))
     assert got["lens"] == [34, 23] and got["counts"] == [34, 34, 2, 0]
     assert got["table"] == [[7, -1, 2], [5, -6, -1]]
+
+
+# ------------------------------------------------------------------------------ forms beside the usual ones
+@pytest.mark.parametrize("rows,used,rank,typ,out,form", [
+    (300, 5, 16, "f16", "f32", "inplace"), (300, 290, 16, "bf16", "f32", "inplace"), (700, 3, 64, "bf16", "bf16", "inplace"),
+    (450, 4, 128, "f16", "f16", "inplace"), (300, 5, 16, "f16", "f32", "none"), (600, 40, 40, "bf16", "bf16", "none"),
+    (513, 6, 32, "f16", "f16", "base"), (400, 2, 72, "bf16", "f16", "base")])
+def test_adapters_of_many_rows_in_place_without_a_base_and_in_16_bits(h, rows, used, rank, typ, out, form):  # noqa: F811
+    lora_case(h, rows, used, used + 1, rank, 264, 190, typ, out, inplace=form == "inplace", base=form != "none", pad=2)
+    assert qgemv.check_error(h) == qgemv.OK
+
+
+def test_many_rows_without_an_adapter_keep_the_base_in_place(h):  # noqa: F811
+    y, ids, base, _ = lora_case(h, 400, 0, 3, 16, 128, 100, "f16", "f32", ids=[-1] * 150 + [2, -1, 0] * 20 + [-1] * 190, inplace=True)
+    assert torch.equal(y[ids < 0].double(), base[ids < 0]) and qgemv.check_error(h) == qgemv.OK
+
+
+@pytest.mark.parametrize("gap", [4, 60])
+def test_an_e4m3_cache_whose_scales_have_gaps_between_pages(h, gap):  # noqa: F811
+    """Stored and attended to; the gaps hold NaN and stay as they are."""
+    g = gen(gap)
+    page, hk, dim, n = 16, 2, 64, 83
+    kc, vc, _, _ = make_cache(g, "e4m3", 9, hk, page, dim, 32)
+    wide = [torch.full((9, hk * page + gap), math.nan, device="cuda") for _ in range(2)]
+    ks, vs = (x[:, :hk * page].unflatten(1, (hk, page)) for x in wide)
+    cache = qgemv.kv_cache(kc, vc, ks, vs)
+    mine = torch.randperm(9, generator=g, device="cuda")[:6]
+    t = torch.arange(n, device="cuda")
+    k, v = randn(g, n, hk * dim).bfloat16(), randn(g, n, hk * dim).bfloat16()
+    qgemv.kv_store(h, qgemv.kv_store_desc(cache, k, v, mine[t // page] * page + t % page, t.int()))
+    q = (randn(g, 1, 4, dim) * 2).bfloat16()
+    out, lse = torch.empty_like(q), torch.empty(1, 4, device="cuda")
+    qgemv.attn_decode(h, qgemv.attn_decode_desc(cache, q, mine.int()[None].contiguous(), ints([n]), out, 0.125, lse=lse))
+    assert qgemv.check_error(h) == qgemv.OK
+    at = (mine[t // page], slice(None), t % page)
+    stored = [c[at].view(F8).double() * s[at].double()[..., None] for c, s in ((kc, ks), (vc, vs))]
+    for got, x in zip(stored, (k, v)):
+        x = x.double().unflatten(1, (hk, dim))
+        within(got, x, (2.0 ** -4 * x.abs() + x.abs().amax(-1, keepdim=True) / 448 * 2.0 ** -10) * 1.001, "stored")
+    check_attend(out, lse, q, [stored], 0.125)
+    assert all(x[:, hk * page:].isnan().all() for x in wide)
+
+
+@pytest.mark.parametrize("src,typ,qt", [("bf16", "bf16", "bf16"), ("f32", "e4m3", "f16"), ("f16", "f16", "f16")])
+def test_store_of_many_tokens_of_heads_of_256(h, src, typ, qt):  # noqa: F811
+    check = test_gpu_serving.test_store_rotates_rounds_once_and_writes_only_its_slots
+    check(h, 1201, 3, 2, 256, 256, True, src, typ, qt, 32, 0)
+    check(h, 1201, 3, 2, 256, 192, False, src, typ, qt, 32, 32)
+
+
+@pytest.mark.parametrize("typ", ["f16", "bf16"])
+@pytest.mark.parametrize("heads", [4, 12])
+def test_an_infinite_value_that_is_seen_stays_with_its_element(h, typ, heads):  # noqa: F811
+    """It gives an infinity or NaN there (inf times the low part of a weight, which may be 0 or negative), and leaves the
+    head's other elements, and requests that do not see it, as they are."""
+    def edit(table, lens, q, kc, vc):
+        vc[table[0, 1].item(), 0, 3, 5] = math.inf
+
+    sound, *_ = attend_case(h, [60, 45], heads, 1, 64, typ, typ, 16, seed=8)
+    got, lse, q, ref, scale, _ = attend_case(h, [60, 45], heads, 1, 64, typ, typ, 16, seed=8, edit=edit)
+    assert not got[0, :, 5].isfinite().any()
+    rest = torch.arange(64, device="cuda") != 5
+    assert torch.equal(got[0][:, rest], sound[0][:, rest]) and torch.equal(got[1], sound[1])
