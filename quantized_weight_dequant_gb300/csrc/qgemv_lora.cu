@@ -76,8 +76,9 @@ extern "C" qgemv_status_t qgemv_run_lora(qgemv_handle_t hh, const qgemv_lora_t* 
   LoraWork work{};
   work.blocks = (p.rank + 31) / 32;
   const int64_t row_bytes = int64_t{64} * work.blocks * lora_parts(bf);
+  const int64_t rest_bytes = bf ? 0 : int64_t{128} * work.blocks;
   // rows at a time: whole tiles of 16, their sums, factors and adapters in the workspace
-  const int64_t most = static_cast<int64_t>(kWsFloats) * 4 / (row_bytes + static_cast<int64_t>(sizeof(LoraRow))) / 32 * 32;
+  const int64_t most = static_cast<int64_t>(kWsFloats) * 4 / (row_bytes + static_cast<int64_t>(sizeof(LoraRow)) + rest_bytes) / 32 * 32;
   work.parts = reinterpret_cast<uint4*>(h->ws);
   for (int64_t m = 0; m < p.rows; m += most) {
     qgemv_lora_t q = p;
@@ -87,7 +88,9 @@ extern "C" qgemv_status_t qgemv_run_lora(qgemv_handle_t hh, const qgemv_lora_t* 
     const int64_t at = m * p.y_stride * (p.out == QGEMV_OUT_F32 ? 4 : 2);
     q.base = p.base ? static_cast<const uint8_t*>(p.base) + at : nullptr;
     q.y = static_cast<uint8_t*>(p.y) + at;
-    work.row = reinterpret_cast<LoraRow*>(reinterpret_cast<uint8_t*>(h->ws) + (q.rows + 15) / 16 * 16 * row_bytes);
+    const int64_t held = (q.rows + 15) / 16 * 16;
+    work.row = reinterpret_cast<LoraRow*>(reinterpret_cast<uint8_t*>(h->ws) + held * row_bytes);
+    work.rest = reinterpret_cast<float*>(work.row + held);
     if (!(bf ? launch_out<true>(*h, q, work, stream) : launch_out<false>(*h, q, work, stream))) return QGEMV_ERR_CUDA;
   }
   return QGEMV_OK;

@@ -9,8 +9,9 @@
 //    shared memory, where each CTA adds those of its own tokens in rank order.  The sums (fp32) are left in
 //    the workspace as what the second product multiplies: two fp16 parts scaled by a power of two per row
 //    (the row's largest in [2^14, 2^15)), or three bf16 parts: at least 21 bits of each sum.  fp16's steps end
-//    at 2^-24, so a row with a sum below 2^-4 (2^-18 of its largest; some in a million of random ones) stays in
-//    fp32, and its outputs take three bf16 parts of the sums times two of B, which hold fp16's 11 bits.
+//    at 2^-24, so where one of a row's 32 neighbouring sums is below 2^-4 (2^-18 of the row's largest; of random
+//    ones, one in some ten thousand) what the two parts leave of the 32 stays in fp32, and the outputs add three
+//    bf16 parts of it times two of B, which hold fp16's 11 bits.
 //  * Outputs of few rows (lora_few_kernel): the rows of one adapter stay, its B streams by, through a
 //    ring of cp.async in which every lane fetches what it will multiply itself (no barrier, no
 //    registers).  All CTAs run at once and have equal shares of the tiles of all rows.
@@ -46,17 +47,18 @@ constexpr int kLoraWarps = 4;
 constexpr int kLoraThreads = 32 * kLoraWarps;
 
 // What a launch keeps of a row beside its sums: its adapter (-1: none, or one of rank 0), the adapter's scale over
-// the parts' power of two, and whether the two parts are not fp16 but the halves of fp32 sums (wide).
+// the sums' power of two, and a bit for each block of 32 whose parts leave a rest (fp16).
 struct __align__(16) LoraRow {
   int adapter;
   float factor;
-  int wide, pad;
+  uint32_t rests, pad;
 };
 // The rows of a launch in the workspace: per row, the parts of its sums (blocks of 32 ranks, kParts, four
 // lanes of 16 bytes).
 struct LoraWork {
   uint4* parts;
   LoraRow* row;
+  float* rest;  // [rows][blocks][32], only where a row has the block's bit
   int blocks;  // 32-wide blocks of the largest rank
 };
 __host__ __device__ constexpr int lora_parts(bool bf) { return bf ? 3 : 2; }
@@ -202,43 +204,80 @@ __device__ __forceinline__ float4 lora_four(const uint4& d) {  // four outputs i
   return make_float4(a.x, a.y, b.x, b.y);
 }
 
-// Zeros in place of what lies past rank r in four rows' ranks j .. j + 7 (those are read where j < r).
-__device__ __forceinline__ void lora_mask(uint4 (&w)[4], int j, int r) {
+// Zeros in place of what lies past rank r in rows' ranks j .. j + 7 (those are read where j < r).
+template <int ROWS>
+__device__ __forceinline__ void lora_mask(uint4 (&w)[ROWS], int j, int r) {
   if (j >= r || j + 8 <= r) return;
 #pragma unroll
-  for (int h = 0; h < 4; ++h) {
+  for (int h = 0; h < ROWS; ++h) {
     uint32_t* q = reinterpret_cast<uint32_t*>(&w[h]);
 #pragma unroll
     for (int e = 0; e < 4; ++e) q[e] &= j + 2 * e >= r ? 0u : j + 2 * e + 1 >= r ? 0xffffu : 0xffffffffu;
   }
 }
 
-// The second product of wide rows: eight sums of a row in a lane (their high and low halves) as three bf16 parts, and
-// two rows of B (fp16 pairs) as two, whose products are added to acc.  Few rows come here, so it costs what it costs.
-struct LoraWide {
-  uint32_t part[3][4];
-  __device__ __forceinline__ LoraWide(const uint4& high, const uint4& low) {
-    const uint32_t h[4] = {high.x, high.y, high.z, high.w}, l[4] = {low.x, low.y, low.z, low.w};
+// What the parts left of the sums of rows m0 (operand rows 0..7) and m1 (8..15), in the blocks of r0 and r1, times
+// the 32 rows of B from n0 on, added to acc: three bf16 parts times two of B.  Rarely called, so it is a function of
+// its own that reads B again: in line it took registers and instruction cache from the loops around it (2048 rows,
+// N 14336, of rank 32 / 64 / 128: 50.5 / 61.7 / 125 us in line, 49.5 / 61.8 / 118 as a function, 49.4 / 59 / 112 with the
+// rest left out).
+__device__ __noinline__ void lora_rests(const qgemv_lora_t& p, const LoraWork& work, int a, int n0, int64_t m0, int64_t m1, uint32_t r0, uint32_t r1,
+                                        float4* acc) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3, r = lora_rank(p, a);
+  const uint32_t any = __reduce_or_sync(0xffffffffu, r0 | r1);
+#pragma unroll 1
+  for (int b = 0; b < work.blocks; ++b) {
+    if (!(any >> b & 1)) continue;
+    uint32_t part[3][2][4];  // [part][row half]
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float a = __uint_as_float(h[i] << 16 | (l[i] & 0xffffu)), b = __uint_as_float((h[i] & 0xffff0000u) | l[i] >> 16);
+    for (int k = 0; k < 2; ++k) {
+      const float4* at = reinterpret_cast<const float4*>(work.rest + ((k ? m1 : m0) * work.blocks + b) * 32 + 8 * c);
+      const bool there = (k ? r1 : r0) >> b & 1;
+      const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f), x = there ? __ldcg(at) : zero, y = there ? __ldcg(at + 1) : zero;
+      float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
-      for (int q = 0; q < 3; ++q) {
-        part[q][i] = pair16<true>(a, b);
-        const float2 f = unpair16<true>(part[q][i]);
-        a -= f.x, b -= f.y;
+      for (int q = 0; q < 3; ++q)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          part[q][k][i] = pair16<true>(v[2 * i], v[2 * i + 1]);
+          const float2 f = unpair16<true>(part[q][k][i]);
+          v[2 * i] -= f.x, v[2 * i + 1] -= f.y;
+        }
+    }
+#pragma unroll 1
+    for (int h = 0; h < 4; ++h) {
+      const int n = n0 + 4 * (g >> 1) + (g & 1) + 2 * (h & 1) + 16 * (h >> 1), j = 32 * b + 8 * c;
+      uint4 w[1] = {j < r && n < p.N ? *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.B) + (static_cast<int64_t>(a) * p.N + n) * p.rank + j)
+                                     : make_uint4(0, 0, 0, 0)};
+      lora_mask(w, j, r);
+      const uint32_t u[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = unpair16<false>(u[i]);
+        split16<true>(f.x, f.y, hi[i], lo[i]);
       }
+      float d[4] = {acc[h].x, acc[h].y, acc[h].z, acc[h].w};
+#pragma unroll
+      for (int q = 0; q < 3; ++q)
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+          mma16816<true>(d, part[q][0][i], part[q][1][i], part[q][0][i + 1], part[q][1][i + 1], hi[i], hi[i + 1]);
+          mma16816<true>(d, part[q][0][i], part[q][1][i], part[q][0][i + 1], part[q][1][i + 1], lo[i], lo[i + 1]);
+        }
+      acc[h] = make_float4(d[0], d[1], d[2], d[3]);
     }
   }
-};
-// acc += (operand rows 0..7: a, 8..15: b; words 2 i and 2 i + 1) times the B rows' words u, v.
-__device__ __forceinline__ void lora_add_wide(float (&acc)[4], const uint32_t (&a)[4], const uint32_t (&b)[4], int i, uint32_t u, uint32_t v) {
-  const float2 fu = unpair16<false>(u), fv = unpair16<false>(v);
-  uint32_t u0, u1, v0, v1;
-  split16<true>(fu.x, fu.y, u0, u1);
-  split16<true>(fv.x, fv.y, v0, v1);
-  mma16816<true>(acc, a[2 * i], b[2 * i], a[2 * i + 1], b[2 * i + 1], u0, v0);
-  mma16816<true>(acc, a[2 * i], b[2 * i], a[2 * i + 1], b[2 * i + 1], u1, v1);
+}
+__device__ __forceinline__ void lora_add_rests(const qgemv_lora_t& p, const LoraWork& work, int a, int n0, int64_t m0, int64_t m1, uint32_t r0, uint32_t r1,
+                                               float (&acc)[2][2][4]) {
+  float4 d[4];
+#pragma unroll
+  for (int h = 0; h < 4; ++h) d[h] = make_float4(acc[h >> 1][h & 1][0], acc[h >> 1][h & 1][1], acc[h >> 1][h & 1][2], acc[h >> 1][h & 1][3]);
+  lora_rests(p, work, a, n0, m0, m1, r0, r1, d);
+#pragma unroll
+  for (int h = 0; h < 4; ++h)
+    acc[h >> 1][h & 1][0] = d[h].x, acc[h >> 1][h & 1][1] = d[h].y, acc[h >> 1][h & 1][2] = d[h].z, acc[h >> 1][h & 1][3] = d[h].w;
 }
 
 // First product over the 32-wide blocks b0 .. b1 of K for ranks j0 .. j0 + 16 RT - 1 and 8 TG tokens, the
@@ -349,7 +388,7 @@ __global__ void __launch_bounds__(kLoraThreads, 4) lora_sums_kernel(const __grid
           for (int c = 0; c < kLoraCluster; ++c) v[0] += q[c].x, v[1] += q[c].y, v[2] += q[c].z, v[3] += q[c].w;
         }
         float by = 1.f, back = 1.f;
-        bool wide = false;
+        uint32_t tiny = 0;  // lanes with a sum too small for its parts
         if constexpr (!BF) {
           float top = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
 #pragma unroll
@@ -362,33 +401,30 @@ __global__ void __launch_bounds__(kLoraThreads, 4) lora_sums_kernel(const __grid
           bool small = false;
 #pragma unroll
           for (int e = 0; e < 4; ++e) small |= v[e] != 0.f && fabsf(v[e]) * by < 0.0625f;
-          wide = __any_sync(0xffffffffu, small);
+          tiny = __ballot_sync(0xffffffffu, small);
         }
         const int64_t m = all[k0 + tok];
         if (lane < 8 * work.blocks) {
           uint2* to = reinterpret_cast<uint2*>(work.parts + (m * work.blocks + lane / 8) * (4 * kParts) + lane % 8 / 2) + lane % 2;
-          if (wide) {
-            uint32_t u[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) u[e] = __float_as_uint(v[e]);
-            to[0] = make_uint2(__byte_perm(u[0], u[1], 0x7632), __byte_perm(u[2], u[3], 0x7632));
-            to[8] = make_uint2(__byte_perm(u[0], u[1], 0x5410), __byte_perm(u[2], u[3], 0x5410));
-          } else {
+          for (int e = 0; e < 4; ++e) v[e] *= by;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] *= by;
+          for (int q = 0; q < kParts; ++q) {
+            float w[4];
 #pragma unroll
-            for (int q = 0; q < kParts; ++q) {
-              float w[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) w[e] = BF && q == 0 ? lora_bf16_end(v[e]) : v[e];
-              const uint32_t u0 = pair16<BF>(w[0], w[1]), u1 = pair16<BF>(w[2], w[3]);
-              to[8 * q] = make_uint2(u0, u1);
-              const float2 f0 = unpair16<BF>(u0), f1 = unpair16<BF>(u1);
-              v[0] -= f0.x, v[1] -= f0.y, v[2] -= f1.x, v[3] -= f1.y;
-            }
+            for (int e = 0; e < 4; ++e) w[e] = BF && q == 0 ? lora_bf16_end(v[e]) : v[e];
+            const uint32_t u0 = pair16<BF>(w[0], w[1]), u1 = pair16<BF>(w[2], w[3]);
+            to[8 * q] = make_uint2(u0, u1);
+            const float2 f0 = unpair16<BF>(u0), f1 = unpair16<BF>(u1);
+            v[0] -= f0.x, v[1] -= f0.y, v[2] -= f1.x, v[3] -= f1.y;
           }
+          if (tiny >> (lane & 24) & 0xff)
+            *reinterpret_cast<float4*>(work.rest + (m * work.blocks + lane / 8) * 32 + lane % 8 * 4) = make_float4(v[0], v[1], v[2], v[3]);
         }
-        if (lane == 0) work.row[m].factor = wide ? scale : scale * back, work.row[m].wide = wide;
+        if (lane == 0) {
+          work.row[m].factor = scale * back;
+          work.row[m].rests = (tiny & 0xffu ? 1 : 0) | (tiny & 0xff00u ? 2 : 0) | (tiny & 0xff0000u ? 4 : 0) | (tiny >> 24 ? 8 : 0);
+        }
       }
       cluster_arrive();
       cluster_wait();  // no CTA reads this one's sums: they are used again, or the CTA ends
@@ -408,7 +444,7 @@ struct LoraFewSmem {
   uint4 ring[kLoraWarps][kLoraDepth][kLoraPieces][32];
   uint4 parts[kLoraMaxRank / 32][3][32];  // of the tokens in hand, as a lane's operand
   float factor[8];
-  int wide[8];
+  uint32_t rests[8];
 };
 
 template <bool BF, int OUT>
@@ -475,10 +511,10 @@ struct LoraStream {
 #pragma unroll 1
     for (int i = 0; i < kLoraDepth; ++i) ask();
   }
-  __device__ __forceinline__ void run(int t0) {
+  __device__ __forceinline__ void run(const LoraWork& work, const int* rows, int adapter, int t0) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
     const float f = sm.factor[g];
-    const bool wide = !BF && sm.wide[g], any_wide = !BF && __any_sync(0xffffffffu, wide);
+    const uint32_t rests = BF ? 0 : sm.rests[g], any_rests = BF ? 0 : __reduce_or_sync(0xffffffffu, rests);
     int s = 0;
 #pragma unroll 1
     for (int tile = t0 + warp; tile < t1; tile += kLoraWarps) {
@@ -501,26 +537,10 @@ struct LoraStream {
 #pragma unroll
           for (int h = 0; h < 4; ++h) mma16816<BF>(acc[h >> 1][h & 1], s0.z, s1.z, s0.w, s1.w, w[h].z, w[h].w);
         };
-        const uint4 zero = make_uint4(0, 0, 0, 0);
-        if (any_wide) {
-          const uint4 s0 = sm.parts[b][0][lane], s1 = sm.parts[b][1][lane];
-          add(wide ? zero : s0, wide ? zero : s1);
-          const LoraWide of(wide ? s0 : zero, wide ? s1 : zero);
-          constexpr uint32_t none[4] = {0, 0, 0, 0};
-#pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            const uint32_t u[4] = {w[h].x, w[h].y, w[h].z, w[h].w};
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              lora_add_wide(acc[h >> 1][h & 1], of.part[0], of.part[1], i, u[2 * i], u[2 * i + 1]);
-              lora_add_wide(acc[h >> 1][h & 1], of.part[2], none, i, u[2 * i], u[2 * i + 1]);
-            }
-          }
-          continue;
-        }
         add(sm.parts[b][0][lane], sm.parts[b][1][lane]);
-        if constexpr (BF) add(sm.parts[b][2][lane], zero);
+        if constexpr (BF) add(sm.parts[b][2][lane], make_uint4(0, 0, 0, 0));
       }
+      if (any_rests) lora_add_rests(p, work, adapter, 32 * tile, rests ? rows[g] : 0, 0, rests, 0, acc);
       if (!y) continue;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
@@ -585,7 +605,7 @@ __device__ __forceinline__ void lora_items(const qgemv_lora_t& p, int64_t m0, in
 // ranks up to 64, N 12288: 27.0 -> 24.5 us; 128 rows of 16, rank 128: 48 -> 34; 256 rows of one, rank 64, N 6144:
 // 74 -> 22; 16 rows of 16, rank 16, N 6144: 8.1 -> 8.6.
 template <bool BF, int OUT>
-__global__ void __launch_bounds__(kLoraThreads, 4) lora_few_kernel(const __grid_constant__ qgemv_lora_t p, const LoraWork work) {
+__global__ void __launch_bounds__(kLoraThreads, 4) lora_few_kernel(const __grid_constant__ qgemv_lora_t p, const __grid_constant__ LoraWork work) {
   constexpr int kParts = lora_parts(BF);
   extern __shared__ __align__(16) uint8_t dyn[];
   LoraFewSmem& sm = *reinterpret_cast<LoraFewSmem*>(dyn);
@@ -649,7 +669,7 @@ __global__ void __launch_bounds__(kLoraThreads, 4) lora_few_kernel(const __grid_
       if (threadIdx.x < 8) {
         const int4 row = static_cast<int>(threadIdx.x) < n ? __ldcg(reinterpret_cast<const int4*>(&work.row[rows[threadIdx.x]])) : make_int4(0, 0, 0, 0);
         sm.factor[threadIdx.x] = __int_as_float(row.y);
-        sm.wide[threadIdx.x] = row.z;
+        sm.rests[threadIdx.x] = static_cast<uint32_t>(row.z);
       }
 #pragma unroll
       for (int u = 0; u < kParts; ++u) {
@@ -657,7 +677,7 @@ __global__ void __launch_bounds__(kLoraThreads, 4) lora_few_kernel(const __grid_
         if (e < blocks * kParts) sm.parts[e / kParts][e % kParts][lane] = v[u];
       }
       __syncthreads();
-      stream.run(t0);
+      stream.run(work, rows, item.adapter, t0);
       __syncthreads();
     }
   }
@@ -680,7 +700,7 @@ struct LoraManyStage {
 };
 template <bool BF, int OUT, int NB>
 __global__ void __launch_bounds__(kLoraThreads, NB == 1 ? 4 : NB == 2 ? 3 : 2)
-    lora_many_kernel(const __grid_constant__ qgemv_lora_t p, const LoraWork work, int splits) {
+    lora_many_kernel(const __grid_constant__ qgemv_lora_t p, const __grid_constant__ LoraWork work, int splits) {
   using Stage = LoraManyStage<BF, NB>;
   constexpr int kParts = lora_parts(BF);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
@@ -758,7 +778,7 @@ __global__ void __launch_bounds__(kLoraThreads, NB == 1 ? 4 : NB == 2 ? 3 : 2)
     ask_sums(next);
     LoraRow row[2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) row[h] = m + 8 * h < m_end ? st.row[g + 8 * h] : LoraRow{-1, 0.f, 0, 0};
+    for (int h = 0; h < 2; ++h) row[h] = m + 8 * h < m_end ? st.row[g + 8 * h] : LoraRow{-1, 0.f, 0u, 0u};
     // One adapter after another, and the rows without one: mostly a single pass, as rows of one adapter follow
     // one another.  A pass has its own sums, of which it writes its rows': an adapter with infinities or NaN
     // makes NaN of the others' rows.
@@ -772,33 +792,22 @@ __global__ void __launch_bounds__(kLoraThreads, NB == 1 ? 4 : NB == 2 ? 3 : 2)
       float acc[2][2][4] = {};
       if (a >= 0) {
         if (a != cur) hold(a);
-        const bool wide[2] = {!BF && in[0] && row[0].wide, !BF && in[1] && row[1].wide}, any_wide = !BF && __any_sync(0xffffffffu, wide[0] || wide[1]);
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
           if (NB == 4 && b == 3 && work.blocks == 3) break;
 #pragma unroll
           for (int q = 0; q < kParts; ++q) {
             const uint4 zero = make_uint4(0, 0, 0, 0);
-            const uint4 s0 = in[0] && !wide[0] ? st.sums[b * kParts + q][0][lane] : zero, s1 = in[1] && !wide[1] ? st.sums[b * kParts + q][1][lane] : zero;
+            const uint4 s0 = in[0] ? st.sums[b * kParts + q][0][lane] : zero, s1 = in[1] ? st.sums[b * kParts + q][1][lane] : zero;
 #pragma unroll
             for (int h = 0; h < 4; ++h) mma16816<BF>(acc[h >> 1][h & 1], s0.x, s1.x, s0.y, s1.y, w[b][h].x, w[b][h].y);
 #pragma unroll
             for (int h = 0; h < 4; ++h) mma16816<BF>(acc[h >> 1][h & 1], s0.z, s1.z, s0.w, s1.w, w[b][h].z, w[b][h].w);
           }
-          if (any_wide) {
-            const uint4 zero = make_uint4(0, 0, 0, 0);
-            auto of = [&](int half) {
-              return LoraWide(wide[half] ? st.sums[b * kParts][half][lane] : zero, wide[half] ? st.sums[b * kParts + 1][half][lane] : zero);
-            };
-            const LoraWide r0 = of(0), r1 = of(1);
-#pragma unroll
-            for (int q = 0; q < 3; ++q)
-#pragma unroll
-              for (int h = 0; h < 4; ++h) {
-                lora_add_wide(acc[h >> 1][h & 1], r0.part[q], r1.part[q], 0, w[b][h].x, w[b][h].y);
-                lora_add_wide(acc[h >> 1][h & 1], r0.part[q], r1.part[q], 1, w[b][h].z, w[b][h].w);
-              }
-          }
+        }
+        if constexpr (!BF) {
+          const uint32_t rests[2] = {in[0] ? row[0].rests : 0u, in[1] ? row[1].rests : 0u}, any_rests = __reduce_or_sync(0xffffffffu, rests[0] | rests[1]);
+          if (any_rests) lora_add_rests(p, work, a, n0, m, m + 8, rests[0], rests[1], acc);
         }
       }
 #pragma unroll

@@ -145,6 +145,22 @@ def test_inner_sums_far_below_the_rows_largest_keep_their_bits(h, rows, rank, ty
     within(y, ref, tol, "y")
 
 
+@pytest.mark.parametrize("rows", [40, 400])
+def test_inner_sums_far_apart_of_ragged_ranks_ignore_what_lies_past_them(h, rows):  # noqa: F811
+    x, A, B = spread_case(gen(rows), rows, "f16", 72)
+    ids, ranks = (torch.arange(rows, device="cuda") % 3 - 1).int(), ints([37, 67])
+    for a, r in enumerate(ranks.tolist()):
+        A[a, r:], B[a, :, r:] = 0, 0
+    ref, tol = spread_reference(x, A, B, ids.clamp(min=0))
+    for a, r in enumerate(ranks.tolist()):
+        A[a, r:], B[a, :, r:] = math.nan, math.nan
+    y = torch.empty(rows, 90, device="cuda")
+    qgemv.run_lora(h, qgemv.lora_desc(x, A, B, ids, y, ranks=ranks))
+    assert qgemv.check_error(h) == qgemv.OK
+    there = (ids >= 0)[:, None]
+    within(y, ref * there, tol * there, "y")
+
+
 @pytest.mark.parametrize("rows", [24, 320])
 def test_a_row_of_far_apart_sums_leaves_its_neighbours_as_they_are(h, rows):  # noqa: F811
     """The rows of one adapter whose sums are near one another come out bit for bit as without the others."""
