@@ -22,9 +22,9 @@
 //    its row: the order of k within a 32-wide block is the same permutation on both sides, so no shared
 //    memory or ldmatrix is needed for A, B or x.  B's rows are dealt to the two 8-wide halves of a 16-row
 //    tile so that a lane ends up with four consecutive outputs of a token.
-// Measured: one row of rank 16, K 4096, N 6144: 6.5 us, the latency of two launches; 64 rows of 48 adapters of
-// ranks up to 64, K 4096, N 12288: 24.5 us (7 of them the sums; the outputs' CTAs take 4 us to begin, and rows
-// of short ranks cost whole 64-byte pieces of memory); 2048 rows of 4, rank 32, N 14336: 49.2 us (sums 12,
+// Measured: one row of rank 16, K 4096, N 6144: 6.7 us, the latency of two launches; 64 rows of 48 adapters of
+// ranks up to 64, K 4096, N 12288: 24.9 us (7 of them the sums; the outputs' CTAs take 4 us to begin, and rows
+// of short ranks cost whole 64-byte pieces of memory); 2048 rows of 4, rank 32, N 14336: 49.8 us (sums 12,
 // outputs 37 at 6.3 TB/s).
 #pragma once
 #include <cuda_bf16.h>
@@ -39,7 +39,11 @@
 namespace qg {
 
 constexpr int kLoraMaxRank = 128;
-constexpr int kLoraFewRows = 256;  // up to here eight tokens of an adapter at a time, and B streams by
+// Up to here eight tokens of an adapter at a time, and B streams by; past it B is held and the rows stream by.  256 and
+// 257 rows, rank 32, N 12288, of 1 / 16 / 64 / as many adapters as rows, shuffled: 24 / 43 / 49 / 62 and 13 / 47 / 71 /
+// 92 us; 16 in runs: 19 and 17.  Many rows are mostly prompts, whose rows of one adapter follow one another; where
+// they do not, B is fetched again at every change.
+constexpr int kLoraFewRows = 256;
 constexpr int kLoraCluster = 8;
 constexpr int kLoraChunk = 32;     // neighbouring rows of the batch whose adapters one warp finds
 constexpr int kLoraLd = kLoraMaxRank + 4;  // floats per token of the sums in shared memory
@@ -204,12 +208,11 @@ __device__ __forceinline__ float4 lora_four(const uint4& d) {  // four outputs i
   return make_float4(a.x, a.y, b.x, b.y);
 }
 
-// Zeros in place of what lies past rank r in rows' ranks j .. j + 7 (those are read where j < r).
-template <int ROWS>
-__device__ __forceinline__ void lora_mask(uint4 (&w)[ROWS], int j, int r) {
+// Zeros in place of what lies past rank r in four rows' ranks j .. j + 7 (those are read where j < r).
+__device__ __forceinline__ void lora_mask(uint4 (&w)[4], int j, int r) {
   if (j >= r || j + 8 <= r) return;
 #pragma unroll
-  for (int h = 0; h < ROWS; ++h) {
+  for (int h = 0; h < 4; ++h) {
     uint32_t* q = reinterpret_cast<uint32_t*>(&w[h]);
 #pragma unroll
     for (int e = 0; e < 4; ++e) q[e] &= j + 2 * e >= r ? 0u : j + 2 * e + 1 >= r ? 0xffffu : 0xffffffffu;
@@ -217,55 +220,59 @@ __device__ __forceinline__ void lora_mask(uint4 (&w)[ROWS], int j, int r) {
 }
 
 // What the parts left of the sums of rows m0 (operand rows 0..7) and m1 (8..15), in the blocks of r0 and r1, times
-// the 32 rows of B from n0 on, added to acc: three bf16 parts times two of B.  Rarely called, so it is a function of
-// its own that reads B again: in line it took registers and instruction cache from the loops around it (2048 rows,
-// N 14336, of rank 32 / 64 / 128: 50.5 / 61.7 / 125 us in line, 49.5 / 61.8 / 118 as a function, 49.4 / 59 / 112 with the
-// rest left out).
+// the 32 rows of B from n0 on, added to acc: three bf16 parts times two of B (the third times the first only, the
+// other is at 2^-24).  Rarely called, so it is a function of its own that reads B again: in line it took registers and
+// instruction cache from the loops around it.  2048 rows, N 14336, without such a row / with one / with two: rank 32
+// 49.6 / 51.1 / -, rank 64 59.5 / 61.5 / 63.5, rank 128 - / 117.5 / 119.5 us (4 us a row with one load after another).
 __device__ __noinline__ void lora_rests(const qgemv_lora_t& p, const LoraWork& work, int a, int n0, int64_t m0, int64_t m1, uint32_t r0, uint32_t r1,
                                         float4* acc) {
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3, r = lora_rank(p, a);
-  const uint32_t any = __reduce_or_sync(0xffffffffu, r0 | r1);
 #pragma unroll 1
-  for (int b = 0; b < work.blocks; ++b) {
-    if (!(any >> b & 1)) continue;
-    uint32_t part[3][2][4];  // [part][row half]
+  for (int e = 0; e < 2 * work.blocks; ++e) {  // a block and a half of the rows at a time
+    const int b = e >> 1, k = e & 1, j = 32 * b + 8 * c;
+    const bool there = (k ? r1 : r0) >> b & 1;
+    if (!__any_sync(0xffffffffu, there)) continue;
+    // all that is read is asked for before the first is used
+    const float4* at = reinterpret_cast<const float4*>(work.rest + ((k ? m1 : m0) * work.blocks + b) * 32 + 8 * c);
+    const float4 none = make_float4(0.f, 0.f, 0.f, 0.f), x = there ? __ldcg(at) : none, y = there ? __ldcg(at + 1) : none;
+    uint4 w[4];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const float4* at = reinterpret_cast<const float4*>(work.rest + ((k ? m1 : m0) * work.blocks + b) * 32 + 8 * c);
-      const bool there = (k ? r1 : r0) >> b & 1;
-      const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f), x = there ? __ldcg(at) : zero, y = there ? __ldcg(at + 1) : zero;
-      float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-#pragma unroll
-      for (int q = 0; q < 3; ++q)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          part[q][k][i] = pair16<true>(v[2 * i], v[2 * i + 1]);
-          const float2 f = unpair16<true>(part[q][k][i]);
-          v[2 * i] -= f.x, v[2 * i + 1] -= f.y;
-        }
-    }
-#pragma unroll 1
     for (int h = 0; h < 4; ++h) {
-      const int n = n0 + 4 * (g >> 1) + (g & 1) + 2 * (h & 1) + 16 * (h >> 1), j = 32 * b + 8 * c;
-      uint4 w[1] = {j < r && n < p.N ? *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.B) + (static_cast<int64_t>(a) * p.N + n) * p.rank + j)
-                                     : make_uint4(0, 0, 0, 0)};
-      lora_mask(w, j, r);
-      const uint32_t u[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
-      uint32_t hi[4], lo[4];
+      const int n = n0 + 4 * (g >> 1) + (g & 1) + 2 * (h & 1) + 16 * (h >> 1);
+      w[h] = j < r && n < p.N ? *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.B) + (static_cast<int64_t>(a) * p.N + n) * p.rank + j)
+                              : make_uint4(0, 0, 0, 0);
+    }
+    lora_mask(w, j, r);
+    float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+    uint32_t part[3][4];
+#pragma unroll
+    for (int q = 0; q < 3; ++q)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float2 f = unpair16<false>(u[i]);
-        split16<true>(f.x, f.y, hi[i], lo[i]);
+        part[q][i] = pair16<true>(v[2 * i], v[2 * i + 1]);
+        const float2 f = unpair16<true>(part[q][i]);
+        v[2 * i] -= f.x, v[2 * i + 1] -= f.y;
       }
-      float d[4] = {acc[h].x, acc[h].y, acc[h].z, acc[h].w};
 #pragma unroll
-      for (int q = 0; q < 3; ++q)
+    for (int h = 0; h < 4; ++h) {
+      const uint32_t u[4] = {w[h].x, w[h].y, w[h].z, w[h].w};
+      float d[4] = {k ? acc[h].z : acc[h].x, k ? acc[h].w : acc[h].y, 0.f, 0.f};  // eight rows of the product, and their second parts'
 #pragma unroll
-        for (int i = 0; i < 4; i += 2) {
-          mma16816<true>(d, part[q][0][i], part[q][1][i], part[q][0][i + 1], part[q][1][i + 1], hi[i], hi[i + 1]);
-          mma16816<true>(d, part[q][0][i], part[q][1][i], part[q][0][i + 1], part[q][1][i + 1], lo[i], lo[i + 1]);
+      for (int i = 0; i < 4; i += 2) {
+        uint32_t hi[2], lo[2];
+#pragma unroll
+        for (int o = 0; o < 2; ++o) {
+          const float2 f = unpair16<false>(u[i + o]);
+          split16<true>(f.x, f.y, hi[o], lo[o]);
         }
-      acc[h] = make_float4(d[0], d[1], d[2], d[3]);
+        mma16816<true>(d, part[0][i], part[1][i], part[0][i + 1], part[1][i + 1], hi[0], hi[1]);
+        mma16816<true>(d, part[0][i], part[1][i], part[0][i + 1], part[1][i + 1], lo[0], lo[1]);
+        mma16816<true>(d, part[2][i], 0u, part[2][i + 1], 0u, hi[0], hi[1]);
+      }
+      if (k)
+        acc[h].z = d[0] + d[2], acc[h].w = d[1] + d[3];
+      else
+        acc[h].x = d[0] + d[2], acc[h].y = d[1] + d[3];
     }
   }
 }
@@ -688,9 +695,9 @@ __global__ void __launch_bounds__(kLoraThreads, 4) lora_few_kernel(const __grid_
 // ------------------------------------------------------------------------- outputs of many rows
 // A warp keeps 32 rows of B (NB blocks of 32 ranks) and walks over tiles of 16 rows of the batch.  What a tile
 // needs is asked for kLoraAhead tiles ahead, through a ring of cp.async: a lane's own 64 bytes of the base, and for
-// all warps of the CTA together the rows' adapters, factors and sums.  2048 rows, N 14336, rank 32: 50.4 us with the
-// inner sums (60.6 with the sums read from L2 by each warp when it needs them), rank 64: 60, rank 128: 113; with
-// three tiles ahead 51.2, 84 and 113.
+// all warps of the CTA together the rows' adapters, factors and sums.  2048 rows, N 14336, rank 32: 49.8 us with the
+// inner sums (60.6 with the sums read from L2 by each warp when it needs them), rank 64: 60, rank 128: 117; with
+// three tiles ahead, as it was first, 51.2 for 50.4, 84 for 60 and 113 for 113.
 constexpr int kLoraAhead = 2;
 template <bool BF, int NB>
 struct LoraManyStage {
