@@ -15,7 +15,7 @@
 //    the host and ragged batches keep all SMs busy to the end.
 //  * Copies.  Every warp has its own ring of stages, filled by TMA (a tile's pages are rows of a
 //    five-dimensional tensor: 128-byte row parts, in-page token, part, head, page) and waited
-//    for on an mbarrier.  Page numbers are read one tile ahead of the copies that use them.  No
+//    for on an mbarrier.  Page numbers are read by lanes, a batch of tiles ahead of the copies that use them.  No
 //    warp waits for another until the end.
 //  * Products.  mma.sync m16n8k16: q (rows: query heads) times keys (columns: tokens), then the
 //    weights times values.  Memory sets the pace: an SM gets 22 bytes per clock, an 8 KB tile
@@ -24,8 +24,9 @@
 //    eight warps of an SM are through one every 160; of e4m3 codes, whose 8 KB are 32 tokens, in
 //    about 2500.  tcgen05 would add a round trip through tensor memory for products of 8 rows.
 //    Measured: 32 requests of 24 to 44 thousand tokens, 64 query and 8 key-value heads, bf16:
-//    621 us, 6.97 TB/s; 16 requests of 9 to 70 thousand in e4m3: 165 us, 6.2 TB/s; 64 requests of
-//    1 to 6000 in bf16: 40 us, 4.7 TB/s; one request of 1000 in fp16: 12 us, all latency.
+//    623 us, 6.95 TB/s; 16 requests of 9 to 70 thousand in e4m3: 165 us, 6.2 TB/s; 64 requests of
+//    1 to 6000 in bf16: 39.8 us, 4.7 TB/s; one request of 1000 in fp16: 11.9 us (11.3 in a graph), all latency.
+//    Heads of 256 spill registers (54 to 342 bytes a thread): 128 accumulators stand beside the queries.
 //  * Precision.  A weight enters the second product as the sum of two 16-bit values: 16 bits of it in
 //    bf16, 2^-17 against the output's 2^-9, and 22 in fp16.  fp16's steps end at 2^-24, so there weights, at
 //    most 1, are taken times 2^14 and the output divided by it: below 2^-38 of the largest they are rounded
@@ -93,7 +94,7 @@ struct AttnShape {
   static constexpr int kTile = kTT * kRow;                    // bytes of keys (and of values)
   static constexpr int kScaleBytes = KT == QGEMV_KV_E4M3 ? 2 * kTT * 4 : 0;
   static constexpr int kPiece = MR * (D + 2);                 // floats of a piece: m, l, O
-  // two where rings of two stages fit (64 requests of 2000 tokens, 8 heads of 256 in e4m3: 161 us with one, 107 with two)
+  // two where rings of two stages fit (64 requests of 2000 tokens, 8 heads of 256 in e4m3: 161 us with one, 107 to 112 with two)
   static constexpr int kCtasPerSm = D == 256 && (kEl == 2 || MR == 16) ? 1 : 2;
   static constexpr int kBudget = kCtasPerSm == 1 ? 232448 : 115712;
   static constexpr int kStatic = 1664;  // at least the kernel's static shared memory

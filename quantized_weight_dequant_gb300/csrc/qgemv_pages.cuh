@@ -19,7 +19,7 @@ namespace qg {
 //   have = ceil(c / P), need = ceil((c + room) / P) - have,  base = sum of need before r
 // Requests after the one that crosses `capacity` get nothing and no one after them reads their
 // base, so `need` may ignore the capacity and both sums come from one scan.  What bounds it is a
-// chain of latencies (lengths, scan, table and free list, writes): 4.9 us for 64 requests, 8.7 us
+// chain of latencies (lengths, scan, table and free list, writes): 4.7 us for 64 requests, 8.9 us
 // for 1024 requests that bring 128 thousand tokens, with what it writes at 0.3 TB/s.
 struct PlanItem {
   int64_t off;    // number of the request's first token
@@ -247,7 +247,7 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // k, then v) in turn, so that slot, position and angles are read once.  Bound by the bytes of q, k and v: the
 // reads of kU heads are in flight together, and the first of them before slot and position are known.
 // Eight CTAs of four warps on an SM: 8191 tokens of 48 bf16 heads of 128 into e4m3 36.4 us (5.2 TB/s;
-// 40.4 us as five CTAs of eight warps, 38.3 as CTAs that walk over the tokens; six heads in flight spill), into
+// 43.5 in pairs of halves, which spill 20 bytes a thread; as it was first: 40.4 us as five CTAs of eight warps, 38.3 as CTAs that walk over the tokens; six heads in flight spill), into
 // bf16 40.4 us (41.5 with the pairs' other halves read instead of exchanged among the lanes); 4096 tokens of fp32
 // rows into fp16 27.9 us; 64 tokens of them 2.5 us in a graph.
 constexpr int kStoreThreads = 128;
