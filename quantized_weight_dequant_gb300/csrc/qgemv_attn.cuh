@@ -25,7 +25,7 @@
 //    about 2500.  tcgen05 would add a round trip through tensor memory for products of 8 rows.
 //    Measured: 32 requests of 24 to 44 thousand tokens, 64 query and 8 key-value heads, bf16:
 //    623 us, 6.95 TB/s; 16 requests of 9 to 70 thousand in e4m3: 165 us, 6.2 TB/s; 64 requests of
-//    1 to 6000 in bf16: 39.8 us, 4.7 TB/s; one request of 1000 in fp16: 11.9 us (11.3 in a graph), all latency.
+//    1 to 6000 in bf16: 39.8 us, 4.7 TB/s; one request of 1000 in fp16: 12 us (11.3 in a graph), all latency.
 //    Heads of 256 spill registers (54 to 342 bytes a thread): 128 accumulators stand beside the queries.
 //  * Precision.  A weight enters the second product as the sum of two 16-bit values: 16 bits of it in
 //    bf16, 2^-17 against the output's 2^-9, and 22 in fp16.  fp16's steps end at 2^-24, so there weights, at
