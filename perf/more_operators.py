@@ -185,7 +185,7 @@ def _prepare_fp8(case, g, s):
     s["y"] = torch.empty(m, n, dtype=_TORCH[case["y"]], device="cuda")
     if own:
         from quantized_weight_dequant_gb300 import qgemv
-        s["desc"] = qgemv.fp8_desc(s["x"], s["xs"], s["W"], s["ws"], s["y"])
+        s["desc"] = qgemv.scaled_desc(s["x"], s["xs"], s["W"], s["ws"], s["y"])
 
 
 def _prepare_sample(case, g, s):
@@ -227,7 +227,7 @@ def run(s):
         qgemv.quant_rows(_handle(), s["desc"])
         return s["out"]
     if op == "fp8":
-        qgemv.run_fp8(_handle(), s["desc"])
+        qgemv.run_scaled(_handle(), s["desc"])
         return {"y": s["y"]}
     qgemv.sample(_handle(), s["desc"])
     return s["out"]
