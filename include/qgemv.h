@@ -499,6 +499,141 @@ typedef struct {
 
 qgemv_status_t qgemv_run_lora(qgemv_handle_t h, const qgemv_lora_t* lora, cudaStream_t stream);
 
+/* ---------------------------------------------------------------- projections in 8 bits
+ * What a decoder layer needs whose projections take activations and weights in e4m3: the norm
+ * that adds the residual and quantises (qgemv_run_norm), the quantisation of other rows, the
+ * MLP's gated product among them (qgemv_quant_rows), and the projection (qgemv_run_scaled).  An
+ * e4m3 code c in columns 128 b .. 128 b + 127 of row m stands for c * scale[m, b].  Descriptions,
+ * types, strides, launches, asynchrony and errors are those of the serving operators above. */
+
+/* Root-mean-square norm of `rows` rows of N values, with the residual's addition before it:
+ *   s = x + res,  res_out = s,  t = s / sqrt(mean(s^2) + eps) * (offset + weight)
+ * and t is written to y, or as codes with scales, or as both.
+ *   x             [rows][N] of type `in`, row m at m * x_stride.
+ *   res, res_out  [rows][N] of type `res_type`, rows at res_stride and res_out_stride.  res = NULL
+ *                 counts as zeros; res_out = NULL: not written.
+ *   weight        [N] of type weight_type; NULL: t = s / sqrt(mean(s^2) + eps).
+ *   y             [rows][N] of type `out`, row m at m * y_stride, or NULL.
+ *   codes         [rows][N] e4m3, row m at m * codes_stride, with scale[m * scale_stride + b], or NULL
+ *                 (then scale is not written).
+ * Everything is computed in fp32 and rounded once where it is written; s enters the norm as it is
+ * before its rounding to res_type.  scale = max|t| / 448 of its columns (1 where that is 0 or not
+ * finite, and at least 2^-126), codes e4m3(t / scale) rounded to nearest even; infinities become
+ * +-448, NaN stays NaN.  res_out may be res or x, and y may be x or res, with the same type and
+ * stride; outputs must not overlap inputs or one another otherwise.  N a multiple of 8 (of 16 with
+ * codes), 8 .. 65536; pointers (but scale's) and row strides 16-byte aligned. */
+typedef struct {
+  const void* x;
+  const void* res;
+  void* res_out;
+  const void* weight;
+  void* y;
+  void* codes;
+  float* scale;
+  int64_t x_stride;
+  int64_t res_stride;
+  int64_t res_out_stride;
+  int64_t y_stride;
+  int64_t codes_stride;
+  int64_t scale_stride;
+  int64_t rows;
+  int32_t N;
+  float eps;
+  float offset;
+  qgemv_out_t in;
+  qgemv_out_t res_type;
+  qgemv_out_t weight_type;
+  qgemv_out_t out;
+} qgemv_norm_t;
+
+qgemv_status_t qgemv_run_norm(qgemv_handle_t h, const qgemv_norm_t* norm, cudaStream_t stream);
+
+/* e4m3 codes and scales (as above) of `rows` rows of N values h: h = x, or with up the gated product
+ * h = silu(x) * up, silu(g) = g / (1 + e^-g), computed in fp32.
+ *   x, up         [rows][N] of type `in`, row m at m * x_stride and m * up_stride (gate and up can be
+ *                 halves of one projection's rows); up = NULL: no gate.
+ * N a multiple of 16; x, up and codes 16-byte aligned with row strides of a multiple of 16 bytes. */
+typedef struct {
+  const void* x;
+  const void* up;
+  void* codes;
+  float* scale;
+  int64_t x_stride;
+  int64_t up_stride;
+  int64_t codes_stride;
+  int64_t scale_stride;
+  int64_t rows;
+  int64_t N;
+  qgemv_out_t in;
+} qgemv_quant_t;
+
+qgemv_status_t qgemv_quant_rows(qgemv_handle_t h, const qgemv_quant_t* quant, cudaStream_t stream);
+
+/* A projection in 8 bits:
+ *   y[m, n] = sum_b x_scale[m, b] * w_scale[n / 128, b] * sum_{k in block b} x[m, k] * W[n, k]
+ * over blocks b of 128 columns (the last one can be shorter).
+ *   x             [M][K] e4m3, row m at m * x_stride; x_scale [M] rows of ceil(K / 128) at
+ *                 m * x_scale_stride.
+ *   W             [N][K] e4m3, contiguous; w_scale [ceil(N / 128)][ceil(K / 128)], contiguous.
+ *   y             [M][N] of type `out`, row m at m * y_stride.
+ * Products are exact, sums in fp32, each block's sum scaled in fp32; y is rounded once.  NaN codes and
+ * NaN or infinite scales reach the outputs of their rows and no others.  Deterministic.  M 0 ..
+ * 2^31 - 1, N 1 .. 2^31 - 1, K a multiple of 16 up to 2^31 - 16; x, W and y 16-byte aligned, x_stride a
+ * multiple of 16, the scales 4-byte aligned.  Uses the handle's workspace like qgemv_run; with QGEMV_OPT_PDL the first
+ * weights are requested before the kernel before it on the stream ends, which must then not write W. */
+typedef struct {
+  const void* x;
+  const float* x_scale;
+  const void* W;
+  const float* w_scale;
+  void* y;
+  int64_t x_stride;
+  int64_t x_scale_stride;
+  int64_t y_stride;
+  int64_t M;
+  int64_t N;
+  int64_t K;
+  qgemv_out_t out;
+} qgemv_scaled_t;
+
+qgemv_status_t qgemv_run_scaled(qgemv_handle_t h, const qgemv_scaled_t* scaled, cudaStream_t stream);
+
+/* The next token of each of `rows` requests from its logits and one random number:
+ *   w_i = exp((l_i - max l) / temperature); the tokens in the order of their logits, equal ones by
+ *   index; of these the first top_k; of these the shortest beginning whose weights reach top_p of
+ *   the sum of those; of these the tokens with w_i >= min_p; the token drawn is the first, by index,
+ *   at which the running sum of the weights that are left exceeds u * their sum.
+ *   logits        [rows][V] of type `type`, row m at m * stride.  NaN counts as -inf, which is never
+ *                 drawn; where the largest is +inf, only such tokens are.
+ *   u             [rows] fp32 in [0, 1) (others are clamped, NaN to 0).
+ *   temperature   [rows] fp32, NULL: 1 for all.  Not above 0, or NaN: the token with the largest logit
+ *                 (the first of them); below 2^-64 counts as 2^-64.
+ *   top_k         [rows] int32, NULL: none.  Below 1, or at least V: no limit.
+ *   top_p, min_p  [rows] fp32, NULL: none.  top_p not below 1 or NaN: no limit; below 0 counts as 0, which
+ *                 leaves the first token.  min_p not above 0 or NaN: no limit; above 1 counts as 1.
+ *   tokens        [rows] int32; -1 for a row without a token above -inf.
+ *   logprobs      [rows] fp32 or NULL: log of the probability with which the token was drawn, among those
+ *                 left (0 for the largest logit, -inf for token -1).
+ * Weights are held to 2^-32 of themselves, as whole numbers of 2^-43 (rounded down: smaller ones count as 0), their sums
+ * exactly, so a result does not depend on the order of a sum; borders are compared in 64 bits.
+ * V 1 .. 2^20; logits 16-byte aligned (rows need not be). */
+typedef struct {
+  const void* logits;
+  int64_t stride;
+  const float* u;
+  const float* temperature;
+  const int32_t* top_k;
+  const float* top_p;
+  const float* min_p;
+  int32_t* tokens;
+  float* logprobs;
+  int64_t rows;
+  int32_t V;
+  qgemv_out_t type;
+} qgemv_sample_t;
+
+qgemv_status_t qgemv_sample(qgemv_handle_t h, const qgemv_sample_t* sample, cudaStream_t stream);
+
 /* Capacity of qgemv_run_noalloc's scratch, in fp32 column sums: N * ceil(K / 2048) of them. */
 #define QGEMV_NOALLOC_MAX_COLUMN_SUMS 262144
 

@@ -1,0 +1,185 @@
+// Row operators of a layer with projections in 8 bits: the root-mean-square norm with the residual's
+// addition, and the quantisation of rows (or of the MLP's gated product) to e4m3 with a scale per 128.
+#pragma once
+#include <cstdint>
+
+#include "../../include/qgemv.h"
+#include "qgemv_elems.cuh"
+#include "qgemv_ptx.cuh"
+
+namespace qg {
+
+// Eight elements of a row at a time: a group of 128, which shares a scale, is 16 neighbouring lanes.
+constexpr int kGroupLanes = 16;
+
+// Eight elements whose type is known when the kernel runs: WIDE fp32, else fp16 or bf16 by `type`.
+template <bool WIDE>
+struct Elems8 {
+  uint4 v[WIDE ? 2 : 1];
+};
+template <bool WIDE>
+__device__ __forceinline__ Elems8<WIDE> load_elems(const void* row, int64_t at) {
+  Elems8<WIDE> r;
+  const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(row) + at * (WIDE ? 4 : 2));
+  r.v[0] = p[0];
+  if constexpr (WIDE) r.v[1] = p[1];
+  return r;
+}
+template <bool WIDE>
+__device__ __forceinline__ void elems_float(const Elems8<WIDE>& r, int type, float (&f)[8]) {
+  if constexpr (WIDE) {
+    to_float<QGEMV_OUT_F32>(Raw8<QGEMV_OUT_F32>{{r.v[0], r.v[1]}}, f);
+  } else if (type == QGEMV_OUT_F16) {
+    to_float<QGEMV_OUT_F16>(Raw8<QGEMV_OUT_F16>{{r.v[0]}}, f);
+  } else {
+    to_float<QGEMV_OUT_BF16>(Raw8<QGEMV_OUT_BF16>{{r.v[0]}}, f);
+  }
+}
+__device__ __forceinline__ void store_elems(void* row, int64_t at, int type, const float (&f)[8]) {
+  if (type == QGEMV_OUT_F32) {
+    float4* p = reinterpret_cast<float4*>(static_cast<float*>(row) + at);
+    p[0] = make_float4(f[0], f[1], f[2], f[3]);
+    p[1] = make_float4(f[4], f[5], f[6], f[7]);
+  } else {
+    *reinterpret_cast<uint4*>(static_cast<uint8_t*>(row) + at * 2) = pack8(type, f);
+  }
+}
+
+// Codes of this lane's eight elements, and their group's scale from its first lane.  All 32 lanes come here together;
+// lanes past the row's end bring zeros.
+__device__ __forceinline__ void store_codes(float (&f)[8], bool in, int first, uint8_t* codes, float* scale) {
+  float top = 0.f;  // NaN where one of them is
+#pragma unroll
+  for (int j = 0; j < 8; ++j) top = max_nan(top, fabsf(f[j]));
+#pragma unroll
+  for (int k = kGroupLanes / 2; k > 0; k >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, k));
+  const float s = e4m3_scale(top);
+  const uint2 c = e4m3_codes(f, top, s);
+  if (!in) return;
+  *reinterpret_cast<uint2*>(codes + first) = c;
+  if (first % (8 * kGroupLanes) == 0) scale[first / (8 * kGroupLanes)] = s;
+}
+
+// A row is held in registers, V times eight elements a thread, by one warp (kRowsPerCta rows in a CTA) or by a
+// whole CTA, so that every byte is read once and the norm of a row may overwrite it.
+constexpr int kNormWarps = 4;  // rows of a CTA where a warp has a row
+
+template <bool WIDE, int RES, int V, bool WARP>  // RES: 0 none, 1 of 16 bits, 2 fp32
+__global__ void __launch_bounds__(WARP ? 32 * kNormWarps : 1024) norm_kernel(const __grid_constant__ qgemv_norm_t p) {
+  __shared__ float part[32];
+  const int threads = WARP ? 32 : blockDim.x, tid = WARP ? threadIdx.x & 31 : threadIdx.x;
+  const int64_t m = WARP ? static_cast<int64_t>(blockIdx.x) * kNormWarps + threadIdx.x / 32 : blockIdx.x;
+  pdl_launch_dependents();
+  pdl_wait();
+  if (WARP && m >= p.rows) return;
+  constexpr int kEl = WIDE ? 4 : 2, kResEl = RES == 2 ? 4 : 2;
+  const uint8_t* x = static_cast<const uint8_t*>(p.x) + m * p.x_stride * kEl;
+  const uint8_t* res = static_cast<const uint8_t*>(p.res) + m * p.res_stride * kResEl;
+  Elems8<WIDE> a[V];
+  Elems8<RES == 2> b[RES ? V : 1];
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int at = (tid + j * threads) * 8;
+    if (at < p.N) {
+      a[j] = load_elems<WIDE>(x, at);
+      if constexpr (RES != 0) b[j] = load_elems<RES == 2>(res, at);
+    }
+  }
+  float s[V][8];
+  float sum = 0.f;
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int at = (tid + j * threads) * 8;
+    if (at < p.N) {
+      elems_float<WIDE>(a[j], p.in, s[j]);
+      if constexpr (RES != 0) {
+        float r[8];
+        elems_float<RES == 2>(b[j], p.res_type, r);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[j][i] += r[i];
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum = fmaf(s[j][i], s[j][i], sum);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[j][i] = 0.f;
+    }
+  }
+  sum = warp_sum(sum);
+  if constexpr (!WARP) {
+    if (tid % 32 == 0) part[tid / 32] = sum;
+    __syncthreads();
+    sum = warp_sum((tid & 31) < threads / 32 ? part[tid & 31] : 0.f);
+  }
+  // after the barrier: every element of the row has been read
+  const float by = 1.f / sqrtf(sum / static_cast<float>(p.N) + p.eps);
+  void* res_out = p.res_out ? static_cast<uint8_t*>(p.res_out) + m * p.res_out_stride * (p.res_type == QGEMV_OUT_F32 ? 4 : 2) : nullptr;
+  void* y = p.y ? static_cast<uint8_t*>(p.y) + m * p.y_stride * (p.out == QGEMV_OUT_F32 ? 4 : 2) : nullptr;
+  uint8_t* codes = p.codes ? static_cast<uint8_t*>(p.codes) + m * p.codes_stride : nullptr;
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int at = (tid + j * threads) * 8;
+    const bool in = at < p.N;
+    if (in && res_out) store_elems(res_out, at, p.res_type, s[j]);
+    if (p.weight) {
+      float w[8] = {};
+      if (in) {
+        if (p.weight_type == QGEMV_OUT_F32)
+          elems_float<true>(load_elems<true>(p.weight, at), p.weight_type, w);
+        else
+          elems_float<false>(load_elems<false>(p.weight, at), p.weight_type, w);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[j][i] = in ? s[j][i] * by * (p.offset + w[i]) : 0.f;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[j][i] = in ? s[j][i] * by : 0.f;
+    }
+    if (in && y) store_elems(y, at, p.out, s[j]);
+    if (codes) store_codes(s[j], in, at, codes, p.scale + m * p.scale_stride);
+  }
+}
+
+// Codes of rows.  A thread has eight elements of kQuantV groups of its row, whose reads are in flight together.
+constexpr int kQuantThreads = 128;
+constexpr int kQuantV = 2;
+
+template <bool WIDE, bool GATED>
+__global__ void __launch_bounds__(kQuantThreads) quant_kernel(const __grid_constant__ qgemv_quant_t p, unsigned chunks) {
+  const int64_t m = blockIdx.x / chunks;
+  const int64_t first = static_cast<int64_t>(blockIdx.x % chunks) * (kQuantThreads * kQuantV);
+  pdl_launch_dependents();
+  pdl_wait();
+  const uint8_t* x = static_cast<const uint8_t*>(p.x) + m * p.x_stride * (WIDE ? 4 : 2);
+  const uint8_t* up = static_cast<const uint8_t*>(p.up) + m * p.up_stride * (WIDE ? 4 : 2);
+  Elems8<WIDE> a[kQuantV], b[GATED ? kQuantV : 1];
+#pragma unroll
+  for (int j = 0; j < kQuantV; ++j) {
+    const int64_t at = (first + threadIdx.x + j * kQuantThreads) * 8;
+    if (at < p.N) {
+      a[j] = load_elems<WIDE>(x, at);
+      if constexpr (GATED) b[j] = load_elems<WIDE>(up, at);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kQuantV; ++j) {
+    const int64_t at = (first + threadIdx.x + j * kQuantThreads) * 8;
+    const bool in = at < p.N;
+    float f[8] = {};
+    if (in) {
+      elems_float<WIDE>(a[j], p.in, f);
+      if constexpr (GATED) {
+        float u[8];
+        elems_float<WIDE>(b[j], p.in, u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = f[i] / (1.f + expf(-f[i])) * u[i];
+      }
+    }
+    // columns of a group within it: a row can be longer than 32 bits' worth of elements, a group is not
+    const int64_t g = at / (8 * kGroupLanes);
+    store_codes(f, in, static_cast<int>(at % (8 * kGroupLanes)), static_cast<uint8_t*>(p.codes) + m * p.codes_stride + g * (8 * kGroupLanes),
+                p.scale + m * p.scale_stride + g);
+  }
+}
+
+}  // namespace qg

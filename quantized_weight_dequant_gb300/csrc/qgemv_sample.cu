@@ -1,0 +1,35 @@
+// Entry point of the sampler.  See include/qgemv.h.
+#include "qgemv_sample.cuh"
+
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "qgemv_handle.cuh"
+#include "qgemv_serve.cuh"
+
+using namespace qg;
+
+extern "C" qgemv_status_t qgemv_sample(qgemv_handle_t hh, const qgemv_sample_t* sample, cudaStream_t stream) {
+  const Handle* h = handle_of(hh);
+  if (!h || !sample) return QGEMV_ERR_INVALID_ARG;
+  const qgemv_sample_t& p = *sample;
+  if (p.type != QGEMV_OUT_F32 && p.type != QGEMV_OUT_F16 && p.type != QGEMV_OUT_BF16) return QGEMV_ERR_INVALID_ARG;
+  if (p.rows < 0 || p.rows > 0x7fffffff / kSampleMaxCluster || p.V < 1 || p.V > (1 << 20) || p.stride < p.V || p.stride > (int64_t{1} << 40))
+    return QGEMV_ERR_BAD_SHAPE;
+  if (p.rows > 0 && (!p.logits || !p.u || !p.tokens)) return QGEMV_ERR_INVALID_ARG;
+  if (!aligned16(p.logits) || ((reinterpret_cast<uintptr_t>(p.u) | reinterpret_cast<uintptr_t>(p.temperature) | reinterpret_cast<uintptr_t>(p.top_k) |
+                                reinterpret_cast<uintptr_t>(p.top_p) | reinterpret_cast<uintptr_t>(p.min_p) |
+                                reinterpret_cast<uintptr_t>(p.tokens) | reinterpret_cast<uintptr_t>(p.logprobs)) & 3))
+    return QGEMV_ERR_MISALIGNED;
+  if (p.rows == 0) return QGEMV_OK;
+  // as many CTAs a row as keep two on every SM, each with 2048 logits at least
+  int ctas = 1;
+  while (ctas < kSampleMaxCluster && p.rows * ctas * 2 <= 2 * int64_t{h->sms} && p.V >= ctas * 2 * 2048) ctas *= 2;
+  const void* fn = p.type == QGEMV_OUT_F32   ? reinterpret_cast<const void*>(sample_kernel<QGEMV_OUT_F32>)
+                   : p.type == QGEMV_OUT_F16 ? reinterpret_cast<const void*>(sample_kernel<QGEMV_OUT_F16>)
+                                             : reinterpret_cast<const void*>(sample_kernel<QGEMV_OUT_BF16>);
+  void* args[] = {const_cast<qgemv_sample_t*>(&p)};
+  return launch_dependent(fn, dim3(static_cast<unsigned>(p.rows * ctas)), kSampleThreads, sizeof(SampleSmem), ctas, args, stream) ? QGEMV_OK
+                                                                                                                                 : QGEMV_ERR_CUDA;
+}

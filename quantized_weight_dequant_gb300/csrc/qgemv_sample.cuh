@@ -1,0 +1,464 @@
+// Sampling the next token of each row: temperature, top-k, top-p and min-p from one random number.
+//
+// With w_i = 2^((l_i - max l) log2(e) / T) the tokens that stay are a beginning of the order (logit descending,
+// index ascending), cut by a count (top-k) and by a sum of weights (top-p), and a floor under the weights
+// (min-p); the draw is the first index whose running sum of kept weights exceeds u times their sum.  Nothing is
+// sorted: a cut is found by histograms over ever finer ranges of the logits, and the draw by sums of the warps'
+// pieces of the row.
+//
+//  * Weights are whole numbers of 2^-43, computed to 2^-32 of themselves, and their sums are exact: the result
+//    does not depend on which thread adds what.  32-bit weights are not enough: an error of 2^-24 in a
+//    few heavy tokens moves the borders of all the others, and of 10^4 draws some would go to a neighbour.
+//  * A row belongs to a cluster of CTAs, each with a piece of it in index order, each warp with a piece of that.
+//  * Histogram 0 goes by z = (max - l) log2(e) / T, 40 buckets for each halving of the weight (where weights
+//    matter; coarser behind 2^-32): monotone in the logit, so its buckets are ranges of the order.  The
+//    bucket with the border is then divided by the logits' bits, 2048 ways at a time, until the border falls between two
+//    ranges or within one value, whose equals are counted by index.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+#include "../../include/qgemv.h"
+#include "qgemv_ptx.cuh"
+
+namespace qg {
+
+constexpr int kSampleThreads = 512;
+constexpr int kSampleWarps = kSampleThreads / 32;
+constexpr int kSampleBuckets = 2048;
+constexpr int kSampleGroups = 32;  // of 64 buckets
+constexpr int kSampleMaxCluster = 8;
+constexpr int kSampleUnit = 43;    // weights in units of 2^-43: 2^20 of them stay below 2^64
+constexpr float kInf = __builtin_huge_valf();
+
+struct SampleHist {
+  uint32_t count[kSampleBuckets], lo[kSampleBuckets], hi[kSampleBuckets];  // hi:lo a 64-bit sum
+};
+struct SampleSmem {
+  SampleHist hist[2];
+  uint64_t group_mass[2][kSampleGroups];
+  uint32_t group_count[2][kSampleGroups];
+  uint64_t warp_sum[kSampleWarps];
+  uint64_t cta_sum[2];    // for the cluster
+  uint32_t found[2];      // for the cluster
+  uint64_t best_warp[kSampleWarps];
+  uint64_t best;          // for the cluster
+  uint64_t pick_before, pick_mass;
+  uint32_t pick_bucket, pick_count;
+  uint64_t pick_total;
+  float th[8], tl[8];     // 2^(j/8) 2^31 as two floats
+  uint64_t ti[8];         // and times 2^9 as a whole number
+};
+
+// ---------------------------------------------------------------------------- cluster
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_ctas() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_meet() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t remote_u32(const void* p, uint32_t rank) {
+  uint32_t a, v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint64_t remote_u64(const void* p, uint32_t rank) {
+  uint32_t a;
+  uint64_t v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint64_t warp_sum64(uint64_t v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ uint64_t warp_scan64(uint64_t v, int lane) {  // inclusive
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint64_t u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  return v;
+}
+
+// ---------------------------------------------------------------------------- logits
+template <int T>
+__device__ __forceinline__ float logit_at(const void* row, int64_t i) {
+  float l;
+  if constexpr (T == QGEMV_OUT_F32) {
+    l = static_cast<const float*>(row)[i];
+  } else {
+    const uint32_t b = static_cast<const uint16_t*>(row)[i];
+    if constexpr (T == QGEMV_OUT_F16)
+      l = __half2float(__ushort_as_half(static_cast<unsigned short>(b)));
+    else
+      l = __uint_as_float(b << 16);
+  }
+  // NaN as -inf; -0 as 0, so that equal logits have equal bits
+  return l == l ? l + 0.f : -kInf;
+}
+// The logit's place in the order: smaller for larger logits.
+__device__ __forceinline__ uint32_t rank_key(float l) {
+  const uint32_t b = __float_as_uint(l);
+  return b & 0x80000000u ? b : ~(b | 0x80000000u);
+}
+
+// 2^(j/8) 2^31 as two floats, and 2^(j/8) 2^40 as a whole number.
+__constant__ const float kPowHi[8] = {2147483648.f, 2341847552.f, 2553802752.f, 2784941824.f, 3037000448.f, 3311872512.f, 3611622656.f, 3938502400.f};
+__constant__ const float kPowLo[8] = {0.f, -28.0838032f, 81.5535965f, -86.3073578f, 51.9760513f, 17.3321362f, -53.1616592f, -24.1361656f};
+__constant__ const uint64_t kPowInt[8] = {1099511627776ull, 1199025932245ull, 1307547050779ull, 1425890169699ull, 1554944255988ull, 1695678735018ull, 1849150772653ull, 2016513216442ull};
+
+// What the weights of a row go by: its largest logit, and 8 log2(e) / T in two floats.
+struct RowScale {
+  float m, hi, lo, z;  // z: log2(e) / T
+};
+
+// 2^43 w, rounded down.  y = (l - m) 8 log2(e) / T as a sum of two floats; y = k + f with k whole and |f| <= 1/2; 2^(f/8) - 1 by
+// its series in g = f ln(2)/8, |g| < 0.044, whose first term is kept as two floats; 2^(k/8) = 2^(k >> 3) times one
+// of eight constants.  Relative error 2^-32 at most, 2^-40 in the mean (against 80 bits, over 2 10^7 arguments).
+__device__ __forceinline__ uint64_t weight_of(float l, const RowScale& r, const SampleSmem& s) {
+  if (l == r.m) return 1ull << kSampleUnit;
+  const float d = l - r.m;
+  const float back = d - l;
+  const float off = (l - (d - back)) + (-r.m - back);  // l - m = d + off
+  const float p = d * r.hi;
+  if (!(p > -8.f * (kSampleUnit + 2))) return 0;  // and -inf
+  const float e = fmaf(d, r.hi, -p) + fmaf(d, r.lo, off * r.hi);
+  const float kf = p + 12582912.f;  // 1.5 2^23: rounds to a whole number
+  const int k = __float_as_int(kf) - 0x4b400000;
+  const float f = p - (kf - 12582912.f);
+  constexpr float kL = 0.086643397569656372f, kLlo = -2.3808178e-10f;  // ln(2) / 8
+  const float g = f * kL;
+  const float rest = fmaf(e, kL, fmaf(f, kLlo, fmaf(f, kL, -g)));
+  const float q = g * g * fmaf(g, fmaf(g, fmaf(g, 1.f / 120.f, 1.f / 24.f), 1.f / 6.f), 0.5f);
+  const int j = k & 7;
+  const float t = s.th[j];
+  // t (1 + g) in units of 2^-31 as whole numbers, what they leave in units of 2^-40
+  const float a = t * g;
+  const int whole = __float2int_rn(a);
+  const float b = fmaf(s.tl[j], g, fmaf(t, q + fmaf(rest, g + q, rest), fmaf(t, g, -a))) + (a - static_cast<float>(whole));
+  const uint64_t mant = s.ti[j] + static_cast<uint64_t>(static_cast<int64_t>(whole) * 512 + __float2int_rn(b * 512.f));
+  return (mant << (kSampleUnit - 40)) >> (-(k >> 3));
+}
+
+__device__ __forceinline__ int bucket_of(float l, const RowScale& r) {
+  const float z = (r.m - l) * r.z;
+  if (l == -kInf || !(z < 131072.f)) return l == r.m ? 0 : kSampleBuckets - 1;
+  if (z < 32.f) return static_cast<int>(z * 40.f);
+  return min(kSampleBuckets - 1, 1280 + ((__float_as_int(z) - __float_as_int(32.f)) >> 17));
+}
+// Logits of bucket b as a range of rank keys, somewhat wider.  (Whether it holds them all is counted.)
+__device__ __forceinline__ void bucket_keys(int b, const RowScale& r, uint32_t& lo, uint32_t& hi) {
+  auto z_at = [](int c) { return c <= 1280 ? static_cast<float>(c) / 40.f : __int_as_float(__float_as_int(32.f) + ((c - 1280) << 17)); };
+  const float z0 = z_at(b), z1 = z_at(b + 1);
+  const float wide = 1e-5f * fabsf(r.m);
+  lo = rank_key(r.m - z0 * 0.99999f / r.z + wide);
+  hi = b == kSampleBuckets - 1 ? 0xffffffffu : rank_key(r.m - z1 * 1.00001f / r.z - wide);
+  if (!(lo <= hi)) lo = 0, hi = 0xffffffffu;
+}
+
+// The tokens that stay: a beginning of the order.
+struct Cut {
+  int bucket;
+  uint32_t key, index;  // within the bucket: smaller keys, and of this key indexes up to `index`
+};
+__device__ __forceinline__ bool stays(const Cut& c, int b, float l, uint32_t i) {
+  if (b != c.bucket) return b < c.bucket;
+  const uint32_t k = rank_key(l);
+  return k < c.key || (k == c.key && i <= c.index);
+}
+
+// What both leave.
+__device__ __forceinline__ Cut both_cuts(const Cut& a, const Cut& b) {
+  if (a.bucket != b.bucket) return a.bucket < b.bucket ? a : b;
+  if (a.key != b.key) return a.key < b.key ? a : b;
+  return a.index < b.index ? a : b;
+}
+
+// A cluster's view of one row.
+template <int T>
+struct SampleRow {
+  SampleSmem& s;
+  const void* row;
+  uint32_t rank, ctas;
+  int64_t lo, hi;  // this warp's piece
+  int lane, warp;
+  RowScale r;
+  int turn = 0, hist_turn = 0;  // buffers that the cluster reads are used in turn: a CTA that passed the next meeting has read the last
+
+  template <class F>
+  __device__ __forceinline__ void each(F f) const {
+#pragma unroll 4
+    for (int64_t i = lo + lane; i < hi; i += 32) f(logit_at<T>(row, i), static_cast<uint32_t>(i));
+  }
+
+  __device__ __forceinline__ void add(SampleHist& h, int b, uint64_t w) const {
+    atomicAdd(&h.count[b], 1u);
+    if (w) {
+      const uint32_t wl = static_cast<uint32_t>(w), old = atomicAdd(&h.lo[b], wl);
+      const uint32_t wh = static_cast<uint32_t>(w >> 32) + (old + wl < old);
+      if (wh) atomicAdd(&h.hi[b], wh);
+    }
+  }
+
+  // The histogram that was filled, over the whole cluster: the first bucket at which the running count (mass) reaches
+  // `target` - `before`, which is left in s.pick_*; mass targets can be a share of the sum.
+  template <bool MASS>
+  __device__ void pick(uint64_t target, uint64_t before, float share, bool first) {
+    const int which = hist_turn;
+    hist_turn ^= 1;
+    __syncthreads();
+    SampleHist& h = s.hist[which];
+    // sums of the 32 groups: 16 threads each
+    {
+      const int g = threadIdx.x / 16, at = threadIdx.x % 16;
+      uint64_t m = 0;
+      uint32_t c = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int b = g * 64 + j * 16 + at;
+        c += h.count[b];
+        m += static_cast<uint64_t>(h.hi[b]) << 32 | h.lo[b];
+      }
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) {
+        m += __shfl_xor_sync(0xffffffffu, m, o);
+        c += __shfl_xor_sync(0xffffffffu, c, o);
+      }
+      if (at == 0) s.group_mass[which][g] = m, s.group_count[which][g] = c;
+    }
+    cluster_meet();
+    if (warp == 0) {
+      uint64_t m = 0;
+      uint32_t c = 0;
+      for (uint32_t q = 0; q < ctas; ++q) {
+        m += remote_u64(&s.group_mass[which][lane], q);
+        c += remote_u32(&s.group_count[which][lane], q);
+      }
+      uint64_t v = MASS ? m : c;
+      uint64_t run = warp_scan64(v, lane);
+      const uint64_t total = __shfl_sync(0xffffffffu, run, 31);
+      if (MASS && first) {
+        target = static_cast<uint64_t>(ceil(static_cast<double>(share) * static_cast<double>(total)));
+        if (target == 0) target = 1;
+      }
+      uint32_t hit = __ballot_sync(0xffffffffu, before + run >= target);
+      const int g = hit ? __ffs(hit) - 1 : 31;
+      before += __shfl_sync(0xffffffffu, run - v, g);
+      // the group's 64 buckets, two a lane
+      uint64_t bm[2] = {};
+      uint32_t bc[2] = {};
+      for (uint32_t q = 0; q < ctas; ++q)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int b = g * 64 + 2 * lane + j;
+          bc[j] += remote_u32(&h.count[b], q);
+          bm[j] += static_cast<uint64_t>(remote_u32(&h.hi[b], q)) << 32 | remote_u32(&h.lo[b], q);
+        }
+      const uint64_t v0 = MASS ? bm[0] : bc[0], v1 = MASS ? bm[1] : bc[1];
+      run = warp_scan64(v0 + v1, lane);
+      hit = __ballot_sync(0xffffffffu, before + run >= target);
+      const int at = hit ? __ffs(hit) - 1 : 31;
+      const bool second = before + run - v1 < target;
+      if (lane == at) {
+        s.pick_before = before + run - v1 - (second ? 0 : v0);
+        s.pick_bucket = g * 64 + 2 * lane + (second ? 1 : 0);
+        s.pick_mass = second ? bm[1] : bm[0];
+        s.pick_count = second ? bc[1] : bc[0];
+      }
+      if (lane == 0) s.pick_total = MASS && first ? target : total;
+    } else {  // the other histogram, which the cluster read before this meeting
+      uint32_t* other = s.hist[which ^ 1].count;
+      for (int i = threadIdx.x - 32; i < static_cast<int>(sizeof(SampleHist) / 4); i += kSampleThreads - 32) other[i] = 0;
+    }
+    __syncthreads();
+  }
+
+  // The first index at which the running sum of `weigh` exceeds `aim(sum)`; `take` is called by one thread of the cluster with
+  // the index, its weight and the sum.
+  template <class W, class A, class K>
+  __device__ void locate(W weigh, A aim, K take) {
+    uint64_t mine = 0;
+    each([&](float l, uint32_t i) { mine += weigh(l, i); });
+    mine = warp_sum64(mine);
+    if (lane == 0) s.warp_sum[warp] = mine;
+    __syncthreads();
+    uint64_t before = 0, cta = 0;
+    for (int q = 0; q < kSampleWarps; ++q) {
+      const uint64_t v = s.warp_sum[q];
+      if (q < warp) before += v;
+      cta += v;
+    }
+    if (threadIdx.x == 0) s.cta_sum[turn] = cta;
+    cluster_meet();
+    uint64_t total = 0;
+    for (uint32_t q = 0; q < ctas; ++q) {
+      const uint64_t v = remote_u64(&s.cta_sum[turn], q);
+      if (q < rank) before += v;
+      total += v;
+    }
+    turn ^= 1;
+    const uint64_t target = aim(total);
+    if (target >= before && target < before + mine) {  // the same for all lanes
+      for (int64_t at = lo; at < hi; at += 32) {
+        const int64_t i = at + lane;
+        const uint64_t w = i < hi ? weigh(logit_at<T>(row, i), static_cast<uint32_t>(i)) : 0;
+        const uint64_t run = before + warp_scan64(w, lane);
+        const uint32_t hit = __ballot_sync(0xffffffffu, run > target);
+        if (hit) {
+          if (lane == __ffs(hit) - 1) take(static_cast<uint32_t>(i), w, total);
+          break;
+        }
+        before = __shfl_sync(0xffffffffu, run, 31);
+      }
+    }
+  }
+
+  // The cut after `target` tokens (MASS: after the shortest beginning with `share` of the mass) of those that `in` keeps.
+  template <bool MASS>
+  __device__ Cut cut_at(uint64_t target, float share, const Cut& in) {
+    SampleHist* h = &s.hist[hist_turn];
+    each([&](float l, uint32_t i) {
+      const int b = bucket_of(l, r);
+      if (stays(in, b, l, i)) add(*h, b, MASS ? weight_of(l, r, s) : 0);
+    });
+    pick<MASS>(target, 0, share, true);
+    if (MASS) target = s.pick_total;
+    const int bucket = static_cast<int>(s.pick_bucket);
+    const uint32_t held = s.pick_count;
+    uint64_t before = s.pick_before;
+    uint64_t part = MASS ? s.pick_mass : held;
+    Cut c{bucket, 0xffffffffu, 0xffffffffu};
+    if (held == 1 || before + part == target) return c;
+    uint32_t klo, khi;
+    bucket_keys(bucket, r, klo, khi);
+    bool checked = false;
+    for (;;) {
+      const int bits = 32 - __clz(khi - klo);
+      const int shift = max(0, bits - 11);
+      h = &s.hist[hist_turn];
+      each([&](float l, uint32_t i) {
+        const int b = bucket_of(l, r);
+        if (b != bucket) return;
+        const uint32_t k = rank_key(l);
+        if (k >= klo && k <= khi && stays(in, b, l, i)) add(*h, (k - klo) >> shift, MASS ? weight_of(l, r, s) : 0);
+      });
+      pick<MASS>(target, before, 0.f, false);
+      if (!checked && s.pick_total != part) {  // the range was too narrow
+        klo = 0, khi = 0xffffffffu, checked = true;
+        continue;
+      }
+      checked = true;
+      before = s.pick_before;
+      part = MASS ? s.pick_mass : s.pick_count;
+      klo += s.pick_bucket << shift;
+      khi = klo + ((1u << shift) - 1);
+      c.key = khi;
+      if (s.pick_count == 1 || before + part == target) return c;
+      if (shift == 0) break;
+    }
+    // equal logits: the first of them by index
+    uint64_t n = target - before;
+    if (MASS) {
+      const uint64_t one = part / s.pick_count;
+      n = (n + one - 1) / one;
+    }
+    const int f = turn;
+    locate([&](float l, uint32_t i) { return static_cast<uint64_t>(rank_key(l) == klo && bucket_of(l, r) == bucket && stays(in, bucket, l, i)); },
+           [&](uint64_t) { return n - 1; }, [&](uint32_t i, uint64_t, uint64_t) { s.found[f] = i; });
+    cluster_meet();
+    uint32_t at = 0xffffffffu;
+    for (uint32_t q = 0; q < ctas; ++q) at = min(at, remote_u32(&s.found[f], q));
+    c.index = at;
+    return c;
+  }
+};
+
+template <int T>
+__global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const __grid_constant__ qgemv_sample_t p) {
+  extern __shared__ __align__(16) uint8_t sample_smem[];
+  SampleSmem& s = *reinterpret_cast<SampleSmem*>(sample_smem);
+  const uint32_t ctas = cluster_ctas(), rank = cluster_rank();
+  const int64_t m = blockIdx.x / ctas;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  pdl_launch_dependents();
+  SampleRow<T> row{s, static_cast<const uint8_t*>(p.logits) + m * p.stride * (T == QGEMV_OUT_F32 ? 4 : 2), rank, ctas};
+  const int64_t warps = static_cast<int64_t>(ctas) * kSampleWarps;
+  const int64_t piece = (p.V + warps * 32 - 1) / (warps * 32) * 32;
+  row.lo = min(static_cast<int64_t>(p.V), (rank * kSampleWarps + warp) * piece);
+  row.hi = min(static_cast<int64_t>(p.V), row.lo + piece);
+  row.lane = lane;
+  row.warp = warp;
+  if (threadIdx.x < 2) s.found[threadIdx.x] = 0xffffffffu;
+  if (threadIdx.x < 8) s.th[threadIdx.x] = kPowHi[threadIdx.x], s.tl[threadIdx.x] = kPowLo[threadIdx.x], s.ti[threadIdx.x] = kPowInt[threadIdx.x];
+  for (int i = threadIdx.x; i < static_cast<int>(sizeof(SampleHist) / 4); i += kSampleThreads) s.hist[0].count[i] = 0;
+  pdl_wait();
+  // the largest logit and its first index
+  float top = -kInf;
+  uint32_t at = 0xffffffffu;
+  row.each([&](float l, uint32_t i) {
+    if (l > top) top = l, at = i;
+  });
+  uint64_t best = at == 0xffffffffu ? 0 : static_cast<uint64_t>(~rank_key(top)) << 32 | (0xffffffffu - at);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
+  if (lane == 0) s.best_warp[warp] = best;
+  __syncthreads();
+  for (int q = 0; q < kSampleWarps; ++q) best = max(best, s.best_warp[q]);
+  if (threadIdx.x == 0) s.best = best;
+  cluster_meet();
+  for (uint32_t q = 0; q < ctas; ++q) best = max(best, remote_u64(&s.best, q));
+  const float temperature = p.temperature ? p.temperature[m] : 1.f;
+  const bool one = best == 0 || !(temperature > 0.f);
+  if (one) {
+    if (rank == 0 && threadIdx.x == 0) {
+      p.tokens[m] = best ? static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(best)) : -1;
+      if (p.logprobs) p.logprobs[m] = best ? 0.f : -kInf;
+    }
+  } else {
+    const uint32_t key = ~static_cast<uint32_t>(best >> 32);  // of the largest logit
+    row.r.m = __uint_as_float(key & 0x80000000u ? key : ~key & 0x7fffffffu);
+    const double c = 1.4426950408889634 / fmax(static_cast<double>(temperature), 5.421010862427522e-20);
+    row.r.z = static_cast<float>(c);
+    row.r.hi = static_cast<float>(8.0 * c);
+    row.r.lo = static_cast<float>(8.0 * c - row.r.hi);
+    Cut cut{kSampleBuckets, 0, 0};
+    const int32_t k = p.top_k ? p.top_k[m] : 0;
+    if (k > 0 && k < p.V) cut = row.template cut_at<false>(static_cast<uint64_t>(k), 0.f, cut);
+    const float top_p = p.top_p ? p.top_p[m] : 1.f;
+    if (top_p < 1.f) cut = both_cuts(cut, row.template cut_at<true>(0, fmaxf(top_p, 0.f), cut));
+    const float min_p = p.min_p ? p.min_p[m] : 0.f;
+    const uint64_t floor_w = min_p > 0.f ? static_cast<uint64_t>(ceil(static_cast<double>(fminf(min_p, 1.f)) * 8796093022208.0)) : 0;
+    const float u = p.u[m];
+    __syncthreads();  // s.warp_sum
+    row.locate(
+        [&](float l, uint32_t i) -> uint64_t {
+          if (!stays(cut, bucket_of(l, row.r), l, i)) return 0;
+          const uint64_t w = weight_of(l, row.r, s);
+          return w >= floor_w ? w : 0;
+        },
+        [&](uint64_t total) {
+          const double x = u > 0.f ? static_cast<double>(fminf(u, 1.f)) * static_cast<double>(total) : 0.0;
+          return min(total - 1, static_cast<uint64_t>(x));
+        },
+        [&](uint32_t i, uint64_t w, uint64_t total) {
+          p.tokens[m] = static_cast<int32_t>(i);
+          if (p.logprobs) p.logprobs[m] = logf(static_cast<float>(static_cast<double>(w) / static_cast<double>(total)));
+        });
+  }
+  cluster_meet();  // no CTA leaves while another reads its shared memory
+}
+
+}  // namespace qg

@@ -79,10 +79,44 @@ class Lora(ctypes.Structure):
                 ("rank", ctypes.c_int32), ("type", ctypes.c_int), ("out", ctypes.c_int)]
 
 
+class Norm(ctypes.Structure):
+    """qgemv_norm_t: root-mean-square norm with the residual's addition."""
+    _fields_ = [("x", ctypes.c_void_p), ("res", ctypes.c_void_p), ("res_out", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+                ("y", ctypes.c_void_p), ("codes", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("x_stride", ctypes.c_int64),
+                ("res_stride", ctypes.c_int64), ("res_out_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64),
+                ("codes_stride", ctypes.c_int64), ("scale_stride", ctypes.c_int64), ("rows", ctypes.c_int64),
+                ("N", ctypes.c_int32), ("eps", ctypes.c_float), ("offset", ctypes.c_float), ("in_type", ctypes.c_int),
+                ("res_type", ctypes.c_int), ("weight_type", ctypes.c_int), ("out", ctypes.c_int)]
+
+
+class Quant(ctypes.Structure):
+    """qgemv_quant_t: e4m3 codes and scales of rows."""
+    _fields_ = [("x", ctypes.c_void_p), ("up", ctypes.c_void_p), ("codes", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+                ("x_stride", ctypes.c_int64), ("up_stride", ctypes.c_int64), ("codes_stride", ctypes.c_int64),
+                ("scale_stride", ctypes.c_int64), ("rows", ctypes.c_int64), ("N", ctypes.c_int64), ("in_type", ctypes.c_int)]
+
+
+class Scaled(ctypes.Structure):
+    """qgemv_scaled_t: a projection of e4m3 rows by e4m3 weights."""
+    _fields_ = [("x", ctypes.c_void_p), ("x_scale", ctypes.c_void_p), ("W", ctypes.c_void_p), ("w_scale", ctypes.c_void_p),
+                ("y", ctypes.c_void_p), ("x_stride", ctypes.c_int64), ("x_scale_stride", ctypes.c_int64),
+                ("y_stride", ctypes.c_int64), ("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
+                ("out", ctypes.c_int)]
+
+
+class Sample(ctypes.Structure):
+    """qgemv_sample_t: the next token of each row of logits."""
+    _fields_ = [("logits", ctypes.c_void_p), ("stride", ctypes.c_int64), ("u", ctypes.c_void_p),
+                ("temperature", ctypes.c_void_p), ("top_k", ctypes.c_void_p), ("top_p", ctypes.c_void_p),
+                ("min_p", ctypes.c_void_p), ("tokens", ctypes.c_void_p), ("logprobs", ctypes.c_void_p),
+                ("rows", ctypes.c_int64), ("V", ctypes.c_int32), ("type", ctypes.c_int)]
+
+
 EXPORTS = ["qgemv_create", "qgemv_destroy", "qgemv_run", "qgemv_unpack", "qgemv_check_error",
            "qgemv_status_string", "qgemv_packed_bytes", "qgemv_group_size", "qgemv_set_option",
            "qgemv_describe", "qgemv_build_marker", "qgemv_run_noalloc", "qgemv_run_group", "qgemv_run_ex", "qgemv_run_batch",
-           "qgemv_run_gemm", "qgemv_page_plan", "qgemv_kv_store", "qgemv_attn_decode", "qgemv_run_lora"]
+           "qgemv_run_gemm", "qgemv_page_plan", "qgemv_kv_store", "qgemv_attn_decode", "qgemv_run_lora",
+           "qgemv_run_norm", "qgemv_quant_rows", "qgemv_run_scaled", "qgemv_sample"]
 
 _lib = None
 
@@ -124,10 +158,15 @@ def lib() -> ctypes.CDLL:
         L.qgemv_kv_store.argtypes = [vp, ctypes.POINTER(KvStore), vp]
         L.qgemv_attn_decode.argtypes = [vp, ctypes.POINTER(AttnDecode), vp]
         L.qgemv_run_lora.argtypes = [vp, ctypes.POINTER(Lora), vp]
+        L.qgemv_run_norm.argtypes = [vp, ctypes.POINTER(Norm), vp]
+        L.qgemv_quant_rows.argtypes = [vp, ctypes.POINTER(Quant), vp]
+        L.qgemv_run_scaled.argtypes = [vp, ctypes.POINTER(Scaled), vp]
+        L.qgemv_sample.argtypes = [vp, ctypes.POINTER(Sample), vp]
         for name in ("qgemv_create", "qgemv_destroy", "qgemv_run", "qgemv_unpack", "qgemv_check_error",
                      "qgemv_set_option", "qgemv_describe", "qgemv_run_noalloc", "qgemv_run_group",
                      "qgemv_run_ex", "qgemv_run_batch", "qgemv_run_gemm", "qgemv_page_plan", "qgemv_kv_store",
-                     "qgemv_attn_decode", "qgemv_run_lora"):
+                     "qgemv_attn_decode", "qgemv_run_lora", "qgemv_run_norm", "qgemv_quant_rows", "qgemv_run_scaled",
+                     "qgemv_sample"):
             getattr(L, name).restype = st
         _lib = L
     return _lib
@@ -503,4 +542,149 @@ def run_lora(h: Handle, desc: Lora, stream=None, check: bool = True) -> int:
     st = lib().qgemv_run_lora(h.ptr, desc, _stream(stream))
     if check:
         _check(st, "qgemv_run_lora")
+    return st
+
+
+# ------------------------------------------------------------------ projections in 8 bits
+_ANY = (OUT_F32, OUT_F16, OUT_BF16)
+
+
+def _grid(t, what, dtypes=None):
+    """The row stride of a device tensor [rows, columns] with contiguous rows."""
+    if t.dim() != 2 or (dtypes is not None and t.dtype not in dtypes):
+        raise TypeError(f"{what}: a tensor [rows, columns]{'' if dtypes is None else f' of type {dtypes[-1]}'} is wanted")
+    return _rows(t, what)
+
+
+def _same_shape(t, like, what):
+    if t.shape != like.shape:
+        raise ValueError(f"{what}: the shape {tuple(like.shape)} is wanted, got {tuple(t.shape)}")
+
+
+def _codes(codes, scale, rows, N, what):
+    """The strides of e4m3 codes (uint8 or float8_e4m3fn) [rows, N] and of their fp32 scales [rows, ceil(N / 128)]."""
+    import torch
+    strides = _grid(codes, f"{what}: codes", (torch.uint8, torch.float8_e4m3fn)), _grid(scale, f"{what}: scale", (torch.float32,))
+    if codes.shape != (rows, N) or scale.shape != (rows, -(-N // 128)):
+        raise ValueError(f"{what}: codes [rows, N] and scale [rows, ceil(N / 128)] are wanted")
+    return strides
+
+
+def norm_desc(x, weight, eps: float, y=None, codes=None, scale=None, res=None, res_out=None, offset: float = 0.0) -> Norm:
+    """s = x + res into res_out, and s / sqrt(mean(s^2) + eps) * (offset + weight) into y, or into e4m3 codes with
+    a scale per 128 columns, or both; all [rows, N] (scale [rows, ceil(N / 128)]), weight [N] or None."""
+    rows, N = x.shape
+    x_stride = _grid(x, "run_norm: x")
+    in_type = _elem(x, _ANY, "run_norm: x")
+    res_type = weight_type = out = OUT_F32
+    res_stride = res_out_stride = y_stride = codes_stride = scale_stride = 0
+    if res is not None or res_out is not None:
+        if res is not None and res_out is not None and res.dtype != res_out.dtype:
+            raise TypeError("run_norm: res and res_out of one type are wanted")
+        res_type = _elem(res if res is not None else res_out, _ANY, "run_norm: res")
+    if res is not None:
+        res_stride = _grid(res, "run_norm: res")
+        _same_shape(res, x, "run_norm: res")
+    if res_out is not None:
+        res_out_stride = _grid(res_out, "run_norm: res_out")
+        _same_shape(res_out, x, "run_norm: res_out")
+    if weight is not None:
+        weight_type = _elem(weight, _ANY, "run_norm: weight")
+        _want(weight, weight.dtype, "run_norm: weight", 1)
+        _size(weight, N, "run_norm: weight")
+    if y is not None:
+        y_stride, out = _grid(y, "run_norm: y"), _elem(y, _ANY, "run_norm: y")
+        _same_shape(y, x, "run_norm: y")
+    if (codes is None) != (scale is None):
+        raise ValueError("run_norm: codes together with scale are wanted")
+    if codes is not None:
+        codes_stride, scale_stride = _codes(codes, scale, rows, N, "run_norm")
+    d = Norm(_ptr(x), _ptr(res), _ptr(res_out), _ptr(weight), _ptr(y), _ptr(codes), _ptr(scale), x_stride, res_stride,
+             res_out_stride, y_stride, codes_stride, scale_stride, rows, N, eps, offset, in_type, res_type, weight_type, out)
+    d.keep = (x, res, res_out, weight, y, codes, scale)
+    return d
+
+
+def run_norm(h: Handle, desc: Norm, stream=None, check: bool = True) -> int:
+    """The norm that `desc` (norm_desc) describes."""
+    st = lib().qgemv_run_norm(h.ptr, desc, _stream(stream))
+    if check:
+        _check(st, "qgemv_run_norm")
+    return st
+
+
+def quant_desc(x, codes, scale, up=None) -> Quant:
+    """e4m3 codes [rows, N] and scales [rows, ceil(N / 128)] of x [rows, N], or with up of silu(x) * up."""
+    rows, N = x.shape
+    x_stride, up_stride = _grid(x, "quant_rows: x"), 0
+    if up is not None:
+        up_stride = _grid(up, "quant_rows: up", (x.dtype,))
+        _same_shape(up, x, "quant_rows: up")
+    codes_stride, scale_stride = _codes(codes, scale, rows, N, "quant_rows")
+    d = Quant(_ptr(x), _ptr(up), _ptr(codes), _ptr(scale), x_stride, up_stride, codes_stride, scale_stride, rows, N,
+              _elem(x, _ANY, "quant_rows: x"))
+    d.keep = (x, up, codes, scale)
+    return d
+
+
+def quant_rows(h: Handle, desc: Quant, stream=None, check: bool = True) -> int:
+    """The quantisation that `desc` (quant_desc) describes."""
+    st = lib().qgemv_quant_rows(h.ptr, desc, _stream(stream))
+    if check:
+        _check(st, "qgemv_quant_rows")
+    return st
+
+
+def scaled_desc(x, x_scale, W, w_scale, y) -> Scaled:
+    """y [M, N] = (x * x_scale) (W * w_scale)^T: x [M, K] and W [N, K] e4m3, x_scale [M, ceil(K / 128)] and
+    w_scale [ceil(N / 128), ceil(K / 128)] fp32 for blocks of 128."""
+    import torch
+    f8 = (torch.uint8, torch.float8_e4m3fn)
+    (M, K), N = x.shape, W.shape[0]
+    x_stride, xs_stride = _codes(x, x_scale, M, K, "run_scaled: x")
+    if W.dtype not in f8 or w_scale.dtype != torch.float32:
+        raise TypeError("run_scaled: W e4m3 (uint8 or float8_e4m3fn) and w_scale float32 are wanted")
+    _want(W, W.dtype, "run_scaled: W", 2)
+    _want(w_scale, torch.float32, "run_scaled: w_scale", 2)
+    if W.shape[1] != K or w_scale.shape != (-(-N // 128), -(-K // 128)):
+        raise ValueError("run_scaled: W [N, K] and w_scale [ceil(N / 128), ceil(K / 128)] are wanted")
+    y_stride = _grid(y, "run_scaled: y")
+    if y.shape != (M, N):
+        raise ValueError("run_scaled: y [M, N] is wanted")
+    d = Scaled(_ptr(x), _ptr(x_scale), _ptr(W), _ptr(w_scale), _ptr(y), x_stride, xs_stride, y_stride, M, N, K,
+            _elem(y, _ANY, "run_scaled: y"))
+    d.keep = (x, x_scale, W, w_scale, y)
+    return d
+
+
+def run_scaled(h: Handle, desc: Scaled, stream=None, check: bool = True) -> int:
+    """The projection that `desc` (scaled_desc) describes."""
+    st = lib().qgemv_run_scaled(h.ptr, desc, _stream(stream))
+    if check:
+        _check(st, "qgemv_run_scaled")
+    return st
+
+
+def sample_desc(logits, u, tokens, temperature=None, top_k=None, top_p=None, min_p=None, logprobs=None) -> Sample:
+    """tokens[r] drawn from logits [rows, V] by u[r] in [0, 1), with each row's temperature, top_k, top_p and
+    min_p (fp32, top_k int32; None: 1 and no limits); logprobs[r] its log probability among those left."""
+    import torch
+    rows, V = logits.shape
+    stride = _grid(logits, "sample: logits")
+    for t, dtype, what in ((u, torch.float32, "u"), (tokens, torch.int32, "tokens"), (temperature, torch.float32, "temperature"),
+                           (top_k, torch.int32, "top_k"), (top_p, torch.float32, "top_p"), (min_p, torch.float32, "min_p"),
+                           (logprobs, torch.float32, "logprobs")):
+        _want(t, dtype, f"sample: {what}", 1)
+        _size(t, rows, f"sample: {what}")
+    d = Sample(_ptr(logits), stride, _ptr(u), _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p), _ptr(tokens),
+               _ptr(logprobs), rows, V, _elem(logits, _ANY, "sample: logits"))
+    d.keep = (logits, u, tokens, temperature, top_k, top_p, min_p, logprobs)
+    return d
+
+
+def sample(h: Handle, desc: Sample, stream=None, check: bool = True) -> int:
+    """The draw that `desc` (sample_desc) describes."""
+    st = lib().qgemv_sample(h.ptr, desc, _stream(stream))
+    if check:
+        _check(st, "qgemv_sample")
     return st
