@@ -1,12 +1,49 @@
 // Entry point of the 8-bit projection.  See include/qgemv.h.
 #include "qgemm_scaled.cuh"
 
+#include <cuda.h>
 #include <cuda_runtime.h>
+
+#include <algorithm>
 
 #include "qgemv_handle.cuh"
 #include "qgemv_serve.cuh"
 
 using namespace qg;
+
+namespace {
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// Rows of K bytes at `stride`, read in boxes of 128 bytes x `box_rows` with the 128-byte swizzle.
+bool encode(const Handle& h, const void* at, int64_t rows, int64_t K, int64_t stride, int box_rows, CUtensorMap* map) {
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride)};
+  const cuuint32_t box[2] = {kScaledBlock, static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t estr[2] = {1, 1};
+  return reinterpret_cast<EncodeFn>(h.encode_tiled)(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(at), dims, strides, box, estr,
+                                                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int BT>
+qgemv_status_t launch_few(const Handle& h, const qgemv_scaled_t& p, ScaledArgs a, cudaStream_t stream) {
+  CUtensorMap wmap, xmap;
+  if (!encode(h, p.W, p.N, p.K, p.K, kScaledRows, &wmap) || !encode(h, p.x, p.M, p.K, p.x_stride, BT, &xmap)) return QGEMV_ERR_CUDA;
+  a.x_tiles = static_cast<int>((p.M + BT - 1) / BT);
+  a.units = (p.N + kScaledRows - 1) / kScaledRows * a.x_tiles * a.blocks;
+  int64_t grid = std::min<int64_t>(a.units, h.sms);
+  grid = std::min<int64_t>(grid, static_cast<int64_t>(kWsFloats) / (2 * BT * kScaledRows));  // two parts of each in the workspace
+  void* args[] = {&wmap, &xmap, &a};
+  return launch_dependent(reinterpret_cast<const void*>(scaled_few_kernel<BT>), dim3(static_cast<unsigned>(grid)), kFewThreads, few_smem_bytes(BT), 1,
+                          args, stream)
+             ? QGEMV_OK
+             : QGEMV_ERR_CUDA;
+}
+
+}  // namespace
 
 extern "C" qgemv_status_t qgemv_run_scaled(qgemv_handle_t hh, const qgemv_scaled_t* scaled, cudaStream_t stream) {
   const Handle* h = handle_of(hh);
@@ -22,10 +59,25 @@ extern "C" qgemv_status_t qgemv_run_scaled(qgemv_handle_t hh, const qgemv_scaled
       ((reinterpret_cast<uintptr_t>(p.x_scale) | reinterpret_cast<uintptr_t>(p.w_scale)) & 3))
     return QGEMV_ERR_MISALIGNED;
   if (p.M == 0) return QGEMV_OK;
-  unsigned row_sets = static_cast<unsigned>((p.M + kFp8SimpleRows - 1) / kFp8SimpleRows);
-  const int64_t grid = (p.N + 7) / 8 * row_sets;
-  if (grid > most) return QGEMV_ERR_BAD_SHAPE;
-  void* args[] = {const_cast<qgemv_scaled_t*>(&p), &row_sets};
-  return launch_dependent(reinterpret_cast<const void*>(fp8_simple_kernel), dim3(static_cast<unsigned>(grid)), 256, 0, 1, args, stream) ? QGEMV_OK
-                                                                                                                                : QGEMV_ERR_CUDA;
+  if (!h->encode_tiled) return QGEMV_ERR_CUDA;  // no TMA descriptors from this driver
+  ScaledArgs a{};
+  a.xs = p.x_scale;
+  a.ws = p.w_scale;
+  a.y = p.y;
+  a.xs_stride = p.x_scale_stride;
+  a.y_stride = p.y_stride;
+  a.M = static_cast<int>(p.M);
+  a.N = static_cast<int>(p.N);
+  a.blocks = static_cast<int>((p.K + kScaledBlock - 1) / kScaledBlock);
+  a.out = p.out;
+  a.parts = h->ws;
+  a.cnt = h->cnt;
+  a.err = h->err;
+  a.spin_ns = h->spin_ns;
+  a.early = h->pdl;
+  a.stall = h->test_stall;
+  if (p.M <= 16) return launch_few<16>(*h, p, a, stream);
+  if (p.M <= 32) return launch_few<32>(*h, p, a, stream);
+  if (p.M <= 64) return launch_few<64>(*h, p, a, stream);
+  return launch_few<128>(*h, p, a, stream);
 }
