@@ -9,6 +9,42 @@
 #include "qgemv_handle.cuh"
 #include "qgemv_serve.cuh"
 
+namespace qg {
+
+const void* few_kernel_for(int BT) {
+  return BT > 64   ? reinterpret_cast<const void*>(scaled_few_kernel<128>)
+         : BT > 32 ? reinterpret_cast<const void*>(scaled_few_kernel<64>)
+         : BT > 16 ? reinterpret_cast<const void*>(scaled_few_kernel<32>)
+                   : reinterpret_cast<const void*>(scaled_few_kernel<16>);
+}
+
+// How many clusters of each size run at once, once for a handle.
+bool scaled_prepare(Handle& h) {
+  for (int BT : {16, 32, 64, 128}) {
+    if (cudaFuncSetAttribute(few_kernel_for(BT), cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(few_smem_bytes(BT))) != cudaSuccess)
+      return false;
+    for (int ks = 2; ks <= 8; ++ks) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(static_cast<unsigned>(ks), 1, 1);
+      cfg.blockDim = dim3(static_cast<unsigned>(few_threads(BT)), 1, 1);
+      cfg.dynamicSmemBytes = few_smem_bytes(BT);
+      cudaLaunchAttribute at[1];
+      at[0].id = cudaLaunchAttributeClusterDimension;
+      at[0].val.clusterDim.x = static_cast<unsigned>(ks);
+      at[0].val.clusterDim.y = 1;
+      at[0].val.clusterDim.z = 1;
+      cfg.attrs = at;
+      cfg.numAttrs = 1;
+      int n = 0;
+      if (cudaOccupancyMaxActiveClusters(&n, few_kernel_for(BT), &cfg) != cudaSuccess) cudaGetLastError(), n = 0;
+      h.scaled_clusters[BT > 64 ? 3 : BT > 32 ? 2 : BT > 16 ? 1 : 0][ks] = n;
+    }
+  }
+  return true;
+}
+
+}  // namespace qg
+
 using namespace qg;
 
 namespace {
@@ -28,17 +64,19 @@ bool encode(const Handle& h, const void* at, int64_t rows, int64_t K, int64_t st
                                                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BT>
-qgemv_status_t launch_few(const Handle& h, const qgemv_scaled_t& p, ScaledArgs a, cudaStream_t stream) {
+qgemv_status_t launch_few(const Handle& h, const qgemv_scaled_t& p, ScaledArgs a, int BT, cudaStream_t stream) {
   CUtensorMap wmap, xmap;
   if (!encode(h, p.W, p.N, p.K, p.K, kScaledRows, &wmap) || !encode(h, p.x, p.M, p.K, p.x_stride, BT, &xmap)) return QGEMV_ERR_CUDA;
   a.x_tiles = static_cast<int>((p.M + BT - 1) / BT);
-  a.units = (p.N + kScaledRows - 1) / kScaledRows * a.x_tiles * a.blocks;
-  int64_t grid = std::min<int64_t>(a.units, h.sms);
-  grid = std::min<int64_t>(grid, static_cast<int64_t>(kWsFloats) / (2 * BT * kScaledRows));  // two parts of each in the workspace
+  const int64_t tiles = (p.N + kScaledRows - 1) / kScaledRows * a.x_tiles;
+  // the largest cluster with which all tiles run at once, of two blocks a CTA at least
+  const int* most = h.scaled_clusters[BT > 64 ? 3 : BT > 32 ? 2 : BT > 16 ? 1 : 0];
+  a.ks = 1;
+  for (int ks = 2; ks <= 8; ++ks)
+    if (tiles <= most[ks] && a.blocks >= 2 * ks) a.ks = ks;
+  if (tiles * a.ks > 0x7fffffff) return QGEMV_ERR_BAD_SHAPE;
   void* args[] = {&wmap, &xmap, &a};
-  return launch_dependent(reinterpret_cast<const void*>(scaled_few_kernel<BT>), dim3(static_cast<unsigned>(grid)), kFewThreads, few_smem_bytes(BT), 1,
-                          args, stream)
+  return launch_dependent(few_kernel_for(BT), dim3(static_cast<unsigned>(tiles * a.ks)), few_threads(BT), few_smem_bytes(BT), a.ks, args, stream)
              ? QGEMV_OK
              : QGEMV_ERR_CUDA;
 }
@@ -70,14 +108,9 @@ extern "C" qgemv_status_t qgemv_run_scaled(qgemv_handle_t hh, const qgemv_scaled
   a.N = static_cast<int>(p.N);
   a.blocks = static_cast<int>((p.K + kScaledBlock - 1) / kScaledBlock);
   a.out = p.out;
-  a.parts = h->ws;
-  a.cnt = h->cnt;
   a.err = h->err;
   a.spin_ns = h->spin_ns;
   a.early = h->pdl;
   a.stall = h->test_stall;
-  if (p.M <= 16) return launch_few<16>(*h, p, a, stream);
-  if (p.M <= 32) return launch_few<32>(*h, p, a, stream);
-  if (p.M <= 64) return launch_few<64>(*h, p, a, stream);
-  return launch_few<128>(*h, p, a, stream);
+  return launch_few(*h, p, a, p.M <= 16 ? 16 : p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128, stream);
 }

@@ -6,15 +6,16 @@
 // fp32 accumulators in its registers: the scales change with every block, so the sum over blocks cannot stay in
 // tensor memory.
 //
-// Few rows of x (this kernel): what bounds it is the bytes of W, N K of them, so every SM gets the same share:
-// the work is the sequence of (tile of 128 weight rows x BT rows of x, block) units, tile by tile, cut into equal
-// ranges, one to a CTA.  A tile that is cut is joined by the last of its CTAs to finish (counted in the
-// handle's counters), which adds the parts from the handle's workspace in their order: the result does not
-// depend on who is last.
+// What bounds few rows of x is the bytes of W, N K of them.  A CTA has a tile of 128 weight rows x BT rows of x, or with
+// few tiles a cluster of CTAs has it and each takes a share of its blocks; then every CTA leaves its sums in shared
+// memory and adds a part of the tile over the cluster, in rank order.  Two CTAs are on an SM: where their number is no
+// multiple of the SMs', memory serves all of them alike and they still end together, and one's start and end are the other's
+// loads.  (Equal shares of all tiles' blocks, one persistent CTA an SM, joined through the workspace: 64 x 28672 x
+// 4096 32.5 us, 64 x 4096 x 4096 19.8, most of it joins.)
 //  * The weight rows are the MMA's M (TMEM lanes), the rows of x its N: a lane's accumulators then belong to
 //    one weight row and BT rows of x, and 32 lanes write 32 neighbours of a row of y.
 //  * Warp 0: one lane brings each unit's W and X tiles by TMA into a ring of stages (rows and columns past the
-//    ends read as zeros).  Warp 1: one lane issues the unit's four MMAs into one of NB accumulators of
+//    ends read as zeros).  Warp 1: one lane issues the unit's four MMAs into its part of a set of accumulators in
 //    tensor memory.  Warps 2..5: scales and sums.
 //  * Every wait is bounded; one that gives up sets the error word, and the CTA waits for its own copies and MMAs and
 //    frees its TMEM before it returns.
@@ -32,7 +33,6 @@ namespace qg {
 
 constexpr int kScaledRows = 128;   // weight rows of a tile: one row of w_scale
 constexpr int kScaledBlock = 128;  // bytes of K in a block: one 128-byte swizzle row
-constexpr int kFewThreads = 32 * 6;
 constexpr uint64_t kDrainNs = 1000000000ull;  // for a CTA's own copies and MMAs, whatever the handle's limit
 
 struct ScaledArgs {
@@ -40,30 +40,36 @@ struct ScaledArgs {
   const float* ws;
   void* y;
   int64_t xs_stride, y_stride;
-  int64_t units;  // tiles * blocks
   int M, N, blocks;
   int x_tiles;
+  int ks;         // CTAs of a cluster, which share a tile's blocks
   int out;
-  float* parts;   // of cut tiles: two slots a CTA
-  int* cnt;
   int* err;
   uint64_t spin_ns;
   int early;      // W may be read before the kernel before this one ends
-  int stall;      // test hook: the first CTA withholds its first unit's sums
+  int stall;      // test hook: the first CTA withholds its first set of sums
 };
 
+__host__ __device__ constexpr int few_halves(int BT) { return BT > 32 ? 2 : 1; }  // column halves, four warps each
+__host__ __device__ constexpr int few_threads(int BT) { return 32 * (2 + 4 * few_halves(BT)); }
 __host__ __device__ constexpr int few_stage_bytes(int BT) { return kScaledBlock * (kScaledRows + BT); }
-__host__ __device__ constexpr int few_stages(int BT) { return 196 * 1024 / few_stage_bytes(BT); }
-__host__ __device__ constexpr int few_buffers(int BT) { return BT > 64 ? 2 : 4; }
-__host__ __device__ constexpr int few_tmem_cols(int BT) { return few_buffers(BT) * BT; }  // 64 .. 256
+__host__ __device__ constexpr int few_stages(int BT) { return 108 * 1024 / few_stage_bytes(BT); }
+// Blocks whose sums are handed over together (their barriers and scales are met once): two such sets fill half of tensor
+// memory, or a quarter at BT = 16.
+__host__ __device__ constexpr int few_set(int BT) { return BT > 64 ? 1 : BT > 32 ? 2 : 4; }
+__host__ __device__ constexpr int few_tmem_cols(int BT) { return 2 * few_set(BT) * BT; }
+__host__ __device__ constexpr int few_scale_bytes(int BT) { return 2 * 3 * few_set(BT) * BT * 4; }  // two sets: products, x's and W's
 __host__ __device__ constexpr size_t few_smem_bytes(int BT) {
-  return 1024 + static_cast<size_t>(few_stages(BT)) * few_stage_bytes(BT) + 256 + 4 * 2 * BT * 4;
+  return 1024 + static_cast<size_t>(few_stages(BT)) * few_stage_bytes(BT) + 256 + few_scale_bytes(BT);
 }
 
-__device__ __forceinline__ int count_acq_rel(int* p) {
-  int old;
-  asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(old) : "l"(p) : "memory");
-  return old;
+__device__ __forceinline__ void copy4(uint32_t dst, const float* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy4_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy4_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 __device__ __forceinline__ void bar_part(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
 
@@ -76,43 +82,41 @@ __device__ __forceinline__ void scaled_store(void* y, int64_t at, int type, floa
     static_cast<__nv_bfloat16*>(y)[at] = __float2bfloat16_rn(v);
 }
 
-// A unit of a CTA's range: tile of weights, tile of x and block; the tiles of x that share a tile of weights follow one another.
-struct ScaledUnit {
-  int wt, xt, kb;
-  __device__ __forceinline__ ScaledUnit(int64_t u, const ScaledArgs& a) {
-    const int64_t tile = u / a.blocks;
-    kb = static_cast<int>(u - tile * a.blocks);
-    wt = static_cast<int>(tile / a.x_tiles);
-    xt = static_cast<int>(tile - static_cast<int64_t>(wt) * a.x_tiles);
-  }
-  __device__ __forceinline__ void next(const ScaledArgs& a) {
-    if (++kb == a.blocks) {
-      kb = 0;
-      if (++xt == a.x_tiles) xt = 0, ++wt;
-    }
-  }
-};
+__device__ __forceinline__ void scaled_cluster_meet() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float remote_f32(uint32_t at, uint32_t rank) {
+  uint32_t a;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(at), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
 
 template <int BT>
-__global__ void __launch_bounds__(kFewThreads, 1) scaled_few_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
-                                                                    const __grid_constant__ ScaledArgs a) {
-  constexpr int S = few_stages(BT), NB = few_buffers(BT), STAGE = few_stage_bytes(BT), WBYTES = kScaledRows * kScaledBlock;
+__global__ void __launch_bounds__(few_threads(BT), 2) scaled_few_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
+                                                                        const __grid_constant__ ScaledArgs a) {
+  constexpr int S = few_stages(BT), Q = few_set(BT), STAGE = few_stage_bytes(BT), WBYTES = kScaledRows * kScaledBlock;
+  constexpr int H = few_halves(BT), HB = BT / H, EPI = 128 * H;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t bars = base + S * STAGE;
-  auto full = [&](int s) { return bars + 8u * s; };               // the stage's copies have landed
-  auto empty = [&](int s) { return bars + 8u * (S + s); };        // the MMAs that read it are complete
-  auto tfull = [&](int b) { return bars + 8u * (2 * S + b); };    // a unit's sums are in TMEM
-  auto tempty = [&](int b) { return bars + 8u * (2 * S + NB + b); };  // and have been read
-  const uint32_t done = bars + 8u * (2 * S + 2 * NB), tslot = done + 8, flag = tslot + 4;
-  static_assert(8 * (2 * S + 2 * NB) + 8 + 8 <= 256, "barriers");
+  auto full = [&](int s) { return bars + 8u * s; };             // the stage's copies have landed
+  auto empty = [&](int s) { return bars + 8u * (S + s); };      // the MMAs that read it are complete
+  auto tfull = [&](int b) { return bars + 8u * (2 * S + b); };  // a set's sums are in TMEM
+  auto tempty = [&](int b) { return bars + 8u * (2 * S + 2 + b); };  // and have been read
+  const uint32_t done = bars + 8u * (2 * S + 4), tslot = done + 8;
+  static_assert(8 * (2 * S + 4) + 8 + 8 <= 256, "barriers");
+  static_assert(BT * kScaledRows * 4 <= S * STAGE, "a tile's sums take the place of the stages");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t G = gridDim.x, i0 = blockIdx.x;
-  const int64_t u0 = a.units * i0 / G, u1 = a.units * (i0 + 1) / G;
+  const unsigned ks = static_cast<unsigned>(a.ks), rank = blockIdx.x % ks, tile = blockIdx.x / ks;
+  const int wt = static_cast<int>(tile / static_cast<unsigned>(a.x_tiles)), xt = static_cast<int>(tile % static_cast<unsigned>(a.x_tiles));
+  const int kb0 = static_cast<int>(static_cast<int64_t>(a.blocks) * rank / ks), n = static_cast<int>(static_cast<int64_t>(a.blocks) * (rank + 1) / ks) - kb0;
+  const int m0 = xt * BT, rows = min(BT, a.M - m0);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) mbar_init(full(s), 1), mbar_init(empty(s), 1);
-    for (int b = 0; b < NB; ++b) mbar_init(tfull(b), 1), mbar_init(tempty(b), 4);
+    for (int b = 0; b < 2; ++b) mbar_init(tfull(b), 1), mbar_init(tempty(b), 4 * H);
     mbar_init(done, 1);
     fence_mbar_init();
   }
@@ -129,32 +133,29 @@ __global__ void __launch_bounds__(kFewThreads, 1) scaled_few_kernel(const __grid
 
   if (warp == 0) {
     if (lane == 0) {  // ---- copies
-      ScaledUnit w(u0, a), x(u0, a);
-      const int ahead = a.early ? static_cast<int>(min(static_cast<int64_t>(S), u1 - u0)) : 0;
-      for (int j = 0; j < ahead; ++j, w.next(a)) {
+      const int ahead = a.early ? min(S, n) : 0;
+      for (int j = 0; j < ahead; ++j) {
         mbar_arrive_expect_tx(full(j), STAGE);
-        tma_load_2d(base + j * STAGE, &wmap, w.kb * kScaledBlock, w.wt * kScaledRows, full(j));
+        tma_load_2d(base + j * STAGE, &wmap, (kb0 + j) * kScaledBlock, wt * kScaledRows, full(j));
       }
       pdl_wait();
-      int64_t i = 0;
-      const int64_t n = u1 - u0;
-      int s = 0;
+      int i = 0, s = 0;
       uint32_t ph = 1;
-      for (; i < n; ++i, x.next(a)) {
+      for (; i < n; ++i) {
         if (i >= S && !mbar_wait_bounded(empty(s), ph, a.spin_ns)) {
           ok = false;
           break;
         }
         if (i >= ahead) {
           mbar_arrive_expect_tx(full(s), STAGE);
-          tma_load_2d(base + s * STAGE, &wmap, x.kb * kScaledBlock, x.wt * kScaledRows, full(s));
+          tma_load_2d(base + s * STAGE, &wmap, (kb0 + i) * kScaledBlock, wt * kScaledRows, full(s));
         }
-        tma_load_2d(base + s * STAGE + WBYTES, &xmap, x.kb * kScaledBlock, x.xt * BT, full(s));
+        tma_load_2d(base + s * STAGE + WBYTES, &xmap, (kb0 + i) * kScaledBlock, m0, full(s));
         if (++s == S) s = 0, ph ^= 1;
       }
       // what was issued last has landed before the CTA may leave
-      for (int64_t j = i > S ? i - S : 0; j < i; ++j)
-        if (!mbar_wait_bounded(full(static_cast<int>(j % S)), static_cast<uint32_t>(j / S) & 1, kDrainNs)) ok = false;
+      for (int j = i > S ? i - S : 0; j < i; ++j)
+        if (!mbar_wait_bounded(full(j % S), static_cast<uint32_t>(j / S) & 1, kDrainNs)) ok = false;
     }
   } else if (warp == 1) {
     if (lane == 0) {  // ---- MMAs
@@ -162,136 +163,140 @@ __global__ void __launch_bounds__(kFewThreads, 1) scaled_few_kernel(const __grid
       const uint64_t d0 = tc_desc_sw128(base);
       int s = 0, b = 0;
       uint32_t ph = 0, tph = 1;
-      const int64_t n = u1 - u0;
-      for (int64_t i = 0; i < n; ++i) {
-        if ((i >= NB && !mbar_wait_bounded(tempty(b), tph, a.spin_ns)) || !mbar_wait_bounded(full(s), ph, a.spin_ns)) {
+      for (int i = 0; i < n && ok;) {
+        const int nq = min(Q, n - i);
+        if (i >= 2 * Q && !mbar_wait_bounded(tempty(b), tph, a.spin_ns)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint64_t wd = d0 + static_cast<uint64_t>(s * (STAGE / 16)), xd = wd + WBYTES / 16;
+        for (int q = 0; q < nq; ++q) {
+          if (!mbar_wait_bounded(full(s), ph, a.spin_ns)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t wd = d0 + static_cast<uint64_t>(s * (STAGE / 16)), xd = wd + WBYTES / 16;
 #pragma unroll
-        for (int k = 0; k < kScaledBlock / 32; ++k) tc_mma_f8(tmem + b * BT, wd + 2 * k, xd + 2 * k, idesc, k > 0);
-        tc_commit(empty(s));
-        if (!(a.stall && i0 == 0 && i == 0)) tc_commit(tfull(b));
-        if (++s == S) s = 0, ph ^= 1;
-        if (++b == NB) b = 0, tph ^= 1;
+          for (int k = 0; k < kScaledBlock / 32; ++k) tc_mma_f8(tmem + (b * Q + q) * BT, wd + 2 * k, xd + 2 * k, idesc, k > 0);
+          tc_commit(empty(s));
+          if (++s == S) s = 0, ph ^= 1;
+        }
+        if (!(a.stall && blockIdx.x == 0 && i == 0)) tc_commit(tfull(b));
+        if ((b ^= 1) == 0) tph ^= 1;
+        i += nq;
       }
-      tc_commit(done);  // also after a failure: nobody leaves while MMAs run
-      if (!mbar_wait_bounded(done, 0, kDrainNs)) ok = false;
+      tc_commit(done);  // also after a failure: nobody leaves, or writes over the stages, while MMAs run
     }
   } else {
-    // ---- scales and sums: this thread's weight row is its TMEM lane
-    const int q4 = warp & 3, r = 32 * q4 + lane;
-    const uint32_t my_scales = bars + 256 + q4 * (2 * BT * 4);
-    const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * q4) << 16);
-    constexpr int V = (BT + 31) / 32;
+    // ---- scales and sums: this thread's weight row is its TMEM lane, its columns are half hh of x's rows
+    const int q4 = warp & 3, hh = (warp - 2) >> 2, r = 32 * q4 + lane, tid = threadIdx.x - 64;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * q4) << 16) + hh * HB;
+    constexpr int P = Q * BT;  // scales of a set: of block q and row c of x at q BT + c
+    const uint32_t prod = bars + 256, raw = prod + 2 * P * 4;
     pdl_wait();
-    float next[V];
-    auto fetch = [&](const ScaledUnit& u, bool in) {
-      const float w = in ? __ldg(a.ws + static_cast<int64_t>(u.wt) * a.blocks + u.kb) : 0.f;
+    // x's and W's scales of the set from block i on, copied a set ahead; each thread has its own of the P
+    auto fetch = [&](int i, int p) {
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const int64_t m = static_cast<int64_t>(u.xt) * BT + lane + 32 * j;
-        next[j] = in && lane + 32 * j < BT && m < a.M ? __ldg(a.xs + m * a.xs_stride + u.kb) * w : 0.f;
+      for (int e = tid; e < P; e += EPI) {
+        const int q = e / BT, m = e % BT;
+        if (i + q < n && m < rows) {
+          copy4(raw + (2 * p * P + e) * 4, a.xs + static_cast<int64_t>(m0 + m) * a.xs_stride + kb0 + i + q);
+          copy4(raw + ((2 * p + 1) * P + e) * 4, a.ws + static_cast<int64_t>(wt) * a.blocks + kb0 + i + q);
+        }
       }
+      copy4_commit();
     };
+    // their products (of rows past the end, too: those have zeros in x, and whatever their scales are, nobody stores their sums)
     auto keep = [&](int p) {
+      copy4_wait<0>();
 #pragma unroll
-      for (int j = 0; j < V; ++j)
-        if (lane + 32 * j < BT) asm volatile("st.shared.f32 [%0], %1;" ::"r"(my_scales + (p * BT + lane + 32 * j) * 4), "f"(next[j]) : "memory");
+      for (int e = tid; e < P; e += EPI)
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(prod + (p * P + e) * 4),
+                     "f"(__uint_as_float(lds_u32(raw + (2 * p * P + e) * 4)) * __uint_as_float(lds_u32(raw + ((2 * p + 1) * P + e) * 4))) : "memory");
     };
-    ScaledUnit now(u0, a), later(u0, a);
-    fetch(later, u0 < u1);
-    keep(0);
-    later.next(a);
-    fetch(later, u0 + 1 < u1);
-    float acc[BT];
+    fetch(0, 0);
+    float acc[HB];
 #pragma unroll
-    for (int c = 0; c < BT; ++c) acc[c] = 0.f;
-    int64_t first = u0;  // of this tile
-    int b = 0, p = 0;
+    for (int c = 0; c < HB; ++c) acc[c] = 0.f;
+    int b = 0;
     uint32_t tph = 0;
-    for (int64_t u = u0; u < u1; ++u) {
-      __syncwarp();
+    for (int i = 0; i < n;) {
+      const int nq = min(Q, n - i);
+      keep(b);
+      fetch(i + nq, b ^ 1);
+      bar_part(1, EPI);  // the products
       // a warp that gave up goes on without waiting, so that the others do not miss it at their barriers
       if (ok && !mbar_wait_bounded(tfull(b), tph, a.spin_ns)) ok = false;
       tc_fence_after();
+      constexpr int CH = 16, NC = HB / CH;
+      uint32_t d[2][CH];
+      auto load = [&](int q, int c, uint32_t (&v)[CH]) { tmem_ld16(lanes + (b * Q + q) * BT + c, v); };
+      load(0, 0, d[0]);
 #pragma unroll
-      for (int c = 0; c < BT; c += 16) {
-        uint32_t d[16];
-        tmem_ld16(lanes + b * BT + c, d);
-        tmem_ld_wait();
+      for (int q = 0; q < Q; ++q) {
+        if (q < nq) {
 #pragma unroll
-        for (int j = 0; j < 16; j += 4) {
-          const uint4 f = lds_v4(my_scales + (p * BT + c + j) * 4);
-          acc[c + j] = fmaf(__uint_as_float(d[j]), __uint_as_float(f.x), acc[c + j]);
-          acc[c + j + 1] = fmaf(__uint_as_float(d[j + 1]), __uint_as_float(f.y), acc[c + j + 1]);
-          acc[c + j + 2] = fmaf(__uint_as_float(d[j + 2]), __uint_as_float(f.z), acc[c + j + 2]);
-          acc[c + j + 3] = fmaf(__uint_as_float(d[j + 3]), __uint_as_float(f.w), acc[c + j + 3]);
+          for (int k = 0; k < NC; ++k) {
+            uint32_t(&v)[CH] = d[(q * NC + k) & 1];
+            tmem_ld_arrived(v);
+            // the next columns are on their way while these are added
+            if (k + 1 < NC)
+              load(q, (k + 1) * CH, d[(q * NC + k + 1) & 1]);
+            else if (q + 1 < Q && q + 1 < nq)
+              load(q + 1, 0, d[(q * NC + k + 1) & 1]);
+#pragma unroll
+            for (int j = 0; j < CH; j += 4) {
+              const uint4 f = lds_v4(prod + (b * P + q * BT + hh * HB + k * CH + j) * 4);
+              float* to = acc + k * CH + j;
+              to[0] = fmaf(__uint_as_float(v[j]), __uint_as_float(f.x), to[0]);
+              to[1] = fmaf(__uint_as_float(v[j + 1]), __uint_as_float(f.y), to[1]);
+              to[2] = fmaf(__uint_as_float(v[j + 2]), __uint_as_float(f.z), to[2]);
+              to[3] = fmaf(__uint_as_float(v[j + 3]), __uint_as_float(f.w), to[3]);
+            }
+          }
         }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(tempty(b));
-      if (++b == NB) b = 0, tph ^= 1;
-      p ^= 1;
-      keep(p);
-      later.next(a);
-      fetch(later, u + 2 < u1);
-      if (now.kb == a.blocks - 1 || u == u1 - 1) {
-        // ---- the tile, or this CTA's part of it
-        bool write = true;
-        const int64_t t0 = u - now.kb;  // the tile's first unit
-        if (first != t0 || now.kb != a.blocks - 1) {
-          const int64_t head = ((t0 + 1) * G - 1) / a.units, tail = ((t0 + a.blocks) * G - 1) / a.units;  // CTAs of its first and last unit
-          float* mine = a.parts + (2 * i0 + (first == t0)) * (BT * kScaledRows) + r;
-#pragma unroll
-          for (int c = 0; c < BT; ++c) __stcg(mine + c * kScaledRows, acc[c]);
-          bar_part(1, 128);
-          if (threadIdx.x == 64) {
-            const bool last = count_acq_rel(a.cnt + head) == static_cast<int>(tail - head);
-            if (last) a.cnt[head] = 0;
-            asm volatile("st.shared.u32 [%0], %1;" ::"r"(flag), "r"(static_cast<uint32_t>(last)) : "memory");
-          }
-          bar_part(1, 128);
-          write = lds_u32(flag) != 0;
-          if (write) {
-#pragma unroll
-            for (int c0 = 0; c0 < BT; c0 += 16) {
-#pragma unroll
-              for (int c = 0; c < 16; ++c) acc[c0 + c] = 0.f;
-              for (int64_t j = head; j <= tail; j += 2) {  // two parts in flight
-                const float* one = a.parts + (2 * j + (j == head)) * (BT * kScaledRows) + r;
-                const float* two = a.parts + 2 * (j + 1) * (BT * kScaledRows) + r;
-                const bool both = j < tail;
-                float v[16], w[16];
-#pragma unroll
-                for (int c = 0; c < 16; ++c) {
-                  v[c] = __ldcg(one + (c0 + c) * kScaledRows);
-                  w[c] = both ? __ldcg(two + (c0 + c) * kScaledRows) : 0.f;
-                }
-#pragma unroll
-                for (int c = 0; c < 16; ++c) acc[c0 + c] = acc[c0 + c] + v[c] + w[c];
-              }
-            }
-          }
-          bar_part(1, 128);  // the flag has been read
-        }
-        const int64_t n = static_cast<int64_t>(now.wt) * kScaledRows + r;
-        if (write && n < a.N) {
-          const int64_t m0 = static_cast<int64_t>(now.xt) * BT;
-          const int rows = static_cast<int>(min(static_cast<int64_t>(BT), a.M - m0));
-#pragma unroll
-          for (int c = 0; c < BT; ++c)
-            if (c < rows) scaled_store(a.y, (m0 + c) * a.y_stride + n, a.out, acc[c]);
-        }
-#pragma unroll
-        for (int c = 0; c < BT; ++c) acc[c] = 0.f;
-        first = u + 1;
-      }
-      now.next(a);
+      if ((b ^= 1) == 0) tph ^= 1;
+      i += nq;
     }
+    if (ks == 1) {
+      const int64_t col = static_cast<int64_t>(wt) * kScaledRows + r;
+      if (col < a.N) {
+#pragma unroll
+        for (int c = 0; c < HB; ++c)
+          if (hh * HB + c < rows) scaled_store(a.y, static_cast<int64_t>(m0 + hh * HB + c) * a.y_stride + col, a.out, acc[c]);
+      }
+    } else {
+      // the MMAs have read the stages: this CTA's sums take their place, [row of x][weight row]
+      if (!mbar_wait_bounded(done, 0, kDrainNs)) ok = false;
+#pragma unroll
+      for (int c = 0; c < HB; ++c)
+        if (hh * HB + c < rows)
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + ((hh * HB + c) * kScaledRows + r) * 4), "f"(acc[c]) : "memory");
+    }
+  }
+  __syncwarp();
+  if (warp < 2 && !mbar_wait_bounded(done, 0, kDrainNs)) ok = false;
+  if (ks > 1) {
+    scaled_cluster_meet();
+    // this CTA's share of the tile's rows x 128 sums, over the ranks in their order
+    const int all = rows * kScaledRows;
+    const int e1 = static_cast<int>(static_cast<unsigned>(all) * (rank + 1) / ks);
+    for (int e = static_cast<int>(static_cast<unsigned>(all) * rank / ks) + static_cast<int>(threadIdx.x); e < e1; e += few_threads(BT)) {
+      float v[8];
+#pragma unroll
+      for (unsigned q = 0; q < 8; ++q) v[q] = q < ks ? remote_f32(base + e * 4, q) : 0.f;
+      float sum = v[0];
+#pragma unroll
+      for (int q = 1; q < 8; ++q) sum += v[q];
+      const int64_t col = static_cast<int64_t>(wt) * kScaledRows + e % kScaledRows;
+      if (col < a.N) scaled_store(a.y, static_cast<int64_t>(m0 + e / kScaledRows) * a.y_stride + col, a.out, sum);
+    }
+    scaled_cluster_meet();  // nobody leaves while its sums are read
   }
   if (!ok) atomicOr(a.err, kDevErrTimeout);
   tc_fence_before();
@@ -301,5 +306,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) scaled_few_kernel(const __grid
     tmem_dealloc(tmem, few_tmem_cols(BT));
   }
 }
+
+const void* few_kernel_for(int BT);
 
 }  // namespace qg

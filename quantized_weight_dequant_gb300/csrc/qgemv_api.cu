@@ -594,6 +594,10 @@ qgemv_status_t qgemv_create(qgemv_handle_t* out, int device) {
       cudaGetLastError();
     }
   }
+  if (!scaled_prepare(*h)) {
+    release();
+    return QGEMV_ERR_CUDA;
+  }
   *out = reinterpret_cast<qgemv_handle_t>(h);
   return QGEMV_OK;
 }
