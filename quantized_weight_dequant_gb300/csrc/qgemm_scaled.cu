@@ -18,7 +18,8 @@ const void* few_kernel_for(int BT) {
                    : reinterpret_cast<const void*>(scaled_few_kernel<16>);
 }
 
-// How many clusters of each size run at once, once for a handle.
+// How many clusters of each size run at once, asked once for a handle.  The answer counts a single CTA to an SM, as of every kernel
+// that allocates tensor memory; these take half of it at most, and two are there at a time.
 bool scaled_prepare(Handle& h) {
   for (int BT : {16, 32, 64, 128}) {
     if (cudaFuncSetAttribute(few_kernel_for(BT), cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(few_smem_bytes(BT))) != cudaSuccess)
@@ -37,7 +38,7 @@ bool scaled_prepare(Handle& h) {
       cfg.numAttrs = 1;
       int n = 0;
       if (cudaOccupancyMaxActiveClusters(&n, few_kernel_for(BT), &cfg) != cudaSuccess) cudaGetLastError(), n = 0;
-      h.scaled_clusters[BT > 64 ? 3 : BT > 32 ? 2 : BT > 16 ? 1 : 0][ks] = n;
+      h.scaled_clusters[BT > 64 ? 3 : BT > 32 ? 2 : BT > 16 ? 1 : 0][ks] = 2 * n;
     }
   }
   return true;
