@@ -82,6 +82,22 @@ qgemv_status_t launch_few(const Handle& h, const qgemv_scaled_t& p, ScaledArgs a
              : QGEMV_ERR_CUDA;
 }
 
+qgemv_status_t launch_many(const Handle& h, const qgemv_scaled_t& p, ScaledArgs a, cudaStream_t stream) {
+  a.x_tiles = static_cast<int>((p.M + kManyRows - 1) / kManyRows);
+  const int64_t pairs = h.sms / 2;
+  // rounds of tiles, by the time that a tile takes
+  auto cost = [&](int BN) { return (a.x_tiles * ((p.N + BN - 1) / BN) + pairs - 1) / pairs * BN; };
+  const int BN = cost(128) < cost(256) ? 128 : 256;
+  CUtensorMap wmap, xmap;
+  if (!encode(h, p.W, p.N, p.K, p.K, BN / 2, &wmap) || !encode(h, p.x, p.M, p.K, p.x_stride, kManyRows / 2, &xmap)) return QGEMV_ERR_CUDA;
+  const int64_t tiles = a.x_tiles * ((p.N + BN - 1) / BN);
+  void* args[] = {&wmap, &xmap, &a};
+  const void* fn = BN == 128 ? reinterpret_cast<const void*>(scaled_many_kernel<128>) : reinterpret_cast<const void*>(scaled_many_kernel<256>);
+  return launch_dependent(fn, dim3(static_cast<unsigned>(2 * std::min<int64_t>(tiles, pairs))), kManyThreads, many_smem_bytes(BN), 2, args, stream)
+             ? QGEMV_OK
+             : QGEMV_ERR_CUDA;
+}
+
 }  // namespace
 
 extern "C" qgemv_status_t qgemv_run_scaled(qgemv_handle_t hh, const qgemv_scaled_t* scaled, cudaStream_t stream) {
@@ -113,5 +129,6 @@ extern "C" qgemv_status_t qgemv_run_scaled(qgemv_handle_t hh, const qgemv_scaled
   a.spin_ns = h->spin_ns;
   a.early = h->pdl;
   a.stall = h->test_stall;
-  return launch_few(*h, p, a, p.M <= 16 ? 16 : p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128, stream);
+  if (p.M > 64) return launch_many(*h, p, a, stream);
+  return launch_few(*h, p, a, p.M <= 16 ? 16 : p.M <= 32 ? 32 : 64, stream);
 }

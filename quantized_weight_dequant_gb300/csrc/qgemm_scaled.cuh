@@ -307,6 +307,230 @@ __global__ void __launch_bounds__(few_threads(BT), 2) scaled_few_kernel(const __
   }
 }
 
+// ---------------------------------------------------------------------------- many rows
+// From 65 rows of x on, what bounds the projection is the matrix instructions, or until some hundred rows still W's bytes.  A
+// pair of CTAs (cta_group::2) has a tile of 256 rows of x x BN weight rows: here x is the MMA's M, so that a
+// lane's accumulators belong to one row of x and a single factor xs * ws scales all of a thread's columns of a
+// block.  Each CTA loads its 128 rows of x and half of the weight rows, which halves what its shared memory takes in for
+// W (a CTA alone would need 96 bytes a cycle for the operands and 96 for the copies, of 128).  One persistent pair on
+// every two SMs, tiles of x first, so that the weights that are being read are shared by all of x.  Eight warps
+// scale and add, a half of the columns each, and write through shared memory, whole rows' pieces at a time.
+constexpr int kManyThreads = 32 * 10;
+constexpr int kManyRows = 256;  // rows of x of a tile
+constexpr int kManyRing = 8;    // scales on their way, per thread
+
+__host__ __device__ constexpr int many_stage_bytes(int BN) { return kScaledBlock * (kManyRows / 2 + BN / 2); }
+__host__ __device__ constexpr int many_stages(int BN) { return 164 * 1024 / many_stage_bytes(BN); }
+constexpr int kManyPad = 33;
+constexpr int kManyOutBytes = 8 * 32 * kManyPad * 4;                 // a warp's 32 rows x 32 words
+constexpr int kManyScaleBytes = 2 * kManyRing * 256 * 4;
+__host__ __device__ constexpr size_t many_smem_bytes(int BN) {
+  return 1024 + static_cast<size_t>(many_stages(BN)) * many_stage_bytes(BN) + 256 + kManyOutBytes + kManyScaleBytes;
+}
+
+template <int BN>
+__global__ void __launch_bounds__(kManyThreads, 1) scaled_many_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
+                                                                      const __grid_constant__ ScaledArgs a) {
+  constexpr int S = many_stages(BN), STAGE = many_stage_bytes(BN), XBYTES = kScaledBlock * kManyRows / 2, HB = BN / 2;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t bars = base + S * STAGE;
+  auto full = [&](int s) { return bars + 8u * s; };             // of the pair's first CTA: both CTAs' copies have landed
+  auto empty = [&](int s) { return bars + 8u * (S + s); };      // the MMAs that read the stage are complete
+  auto tfull = [&](int b) { return bars + 8u * (2 * S + b); };  // a block's sums are in TMEM
+  auto tempty = [&](int b) { return bars + 8u * (2 * S + 2 + b); };  // of the first CTA: both CTAs have read them
+  const uint32_t done = bars + 8u * (2 * S + 4), tslot = done + 8;
+  static_assert(8 * (2 * S + 4) + 8 + 8 <= 256, "barriers");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const unsigned rank = blockIdx.x & 1, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int64_t tiles = static_cast<int64_t>(a.x_tiles) * ((static_cast<int64_t>(a.N) + BN - 1) / BN);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) mbar_init(full(s), 1), mbar_init(empty(s), 1);
+    for (int b = 0; b < 2; ++b) mbar_init(tfull(b), 1), mbar_init(tempty(b), 16);
+    mbar_init(done, 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tslot, 2 * BN);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  scaled_cluster_meet();  // both CTAs' barriers are ready
+  tc_fence_after();
+  const uint32_t tmem = lds_u32(tslot);
+  bool ok = true;
+  pdl_launch_dependents();
+  pdl_wait();
+
+  if (warp == 0) {
+    if (lane == 0) {  // ---- copies
+      int s = 0;
+      uint32_t ph = 1;
+      bool filled = false;  // every stage has been used
+      for (int64_t t = pair; t < tiles && ok; t += pairs) {
+        const int m = static_cast<int>(t % a.x_tiles) * kManyRows + static_cast<int>(rank) * (kManyRows / 2);
+        const int64_t n = t / a.x_tiles * BN + rank * HB;
+        for (int kb = 0; kb < a.blocks; ++kb) {
+          if (filled && !mbar_wait_bounded(empty(s), ph, a.spin_ns)) {
+            ok = false;
+            break;
+          }
+          if (rank == 0) mbar_arrive_expect_tx(full(s), 2 * STAGE);
+          const uint32_t bar = cluster_address(full(s), 0);
+          tma_load_2d_pair(base + s * STAGE, &xmap, kb * kScaledBlock, m, bar);
+          tma_load_2d_pair(base + s * STAGE + XBYTES, &wmap, kb * kScaledBlock, static_cast<int>(n), bar);
+          if (++s == S) s = 0, ph ^= 1, filled = true;
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {  // ---- MMAs
+      constexpr uint32_t idesc = tc_idesc_e4m3(kManyRows, BN);
+      const uint64_t d0 = tc_desc_sw128(base);
+      int s = 0, b = 0;
+      uint32_t ph = 0, tph = 1;
+      int64_t seen = 0;
+      for (int64_t t = pair; t < tiles && ok; t += pairs) {
+        for (int kb = 0; kb < a.blocks; ++kb, ++seen) {
+          if ((seen >= 2 && !mbar_wait_bounded(tempty(b), tph, a.spin_ns)) || !mbar_wait_bounded(full(s), ph, a.spin_ns)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t xd = d0 + static_cast<uint64_t>(s * (STAGE / 16)), wd = xd + XBYTES / 16;
+#pragma unroll
+          for (int k = 0; k < kScaledBlock / 32; ++k) tc_mma_f8_pair(tmem + b * BN, xd + 2 * k, wd + 2 * k, idesc, k > 0);
+          tc_commit_pair(empty(s));
+          if (!(a.stall && pair == 0 && seen == 0)) tc_commit_pair(tfull(b));
+          if (++s == S) s = 0, ph ^= 1;
+          if ((b ^= 1) == 0) tph ^= 1;
+        }
+      }
+      tc_commit_pair(done);  // also after a failure: nobody leaves while MMAs run
+    }
+  } else {
+    // ---- scales and sums: this thread's row of x is its TMEM lane, its columns are half hh of the weight rows
+    const int q4 = warp & 3, hh = (warp - 2) >> 2, r = 32 * q4 + lane;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * q4) << 16) + hh * HB;
+    const uint32_t out = bars + 256 + (warp - 2) * (32 * kManyPad * 4), ring = bars + 256 + kManyOutBytes + (threadIdx.x - 64) * 4;
+    const uint32_t tempty_at[2] = {cluster_address(tempty(0), 0), cluster_address(tempty(1), 0)};
+    auto row_of = [&](int64_t t) { return static_cast<int64_t>(t % a.x_tiles) * kManyRows + rank * (kManyRows / 2) + r; };
+    auto col_of = [&](int64_t t) { return t / a.x_tiles * BN + hh * HB; };
+    // scales of the blocks to come, in this thread's own ring (rows and columns past the end have none: nobody stores their sums)
+    int64_t ft = pair;
+    int fkb = 0, fslot = 0;
+    const float *fx = nullptr, *fw = nullptr;
+    auto aim = [&] {
+      const int64_t m = row_of(ft), n = col_of(ft);
+      fx = ft < tiles && m < a.M ? a.xs + m * a.xs_stride : nullptr;
+      fw = ft < tiles && n < a.N ? a.ws + n / kScaledRows * a.blocks : nullptr;
+    };
+    auto fetch = [&] {
+      if (fx) copy4(ring + fslot * 1024, fx + fkb);
+      if (fw) copy4(ring + (kManyRing + fslot) * 1024, fw + fkb);
+      copy4_commit();
+      if (++fslot == kManyRing) fslot = 0;
+      if (++fkb == a.blocks) {
+        fkb = 0;
+        ft += pairs;
+        aim();
+      }
+    };
+    aim();
+#pragma unroll 1
+    for (int j = 0; j < kManyRing - 1; ++j) fetch();
+    float acc[HB];
+    int b = 0, slot = 0;
+    uint32_t tph = 0;
+    for (int64_t t = pair; t < tiles; t += pairs) {
+#pragma unroll
+      for (int c = 0; c < HB; ++c) acc[c] = 0.f;
+      for (int kb = 0; kb < a.blocks; ++kb) {
+        copy4_wait<kManyRing - 2>();
+        const float f = __uint_as_float(lds_u32(ring + slot * 1024)) * __uint_as_float(lds_u32(ring + (kManyRing + slot) * 1024));
+        if (++slot == kManyRing) slot = 0;
+        fetch();
+        // a warp that gave up goes on without waiting: the other CTA counts on it
+        if (ok && !mbar_wait_bounded(tfull(b), tph, a.spin_ns)) ok = false;
+        tc_fence_after();
+        constexpr int CH = 16, NC = HB / CH;
+        uint32_t d[2][CH];
+        tmem_ld16(lanes + b * BN, d[0]);
+#pragma unroll
+        for (int k = 0; k < NC; ++k) {
+          tmem_ld_arrived(d[k & 1]);
+          if (k + 1 < NC) tmem_ld16(lanes + b * BN + (k + 1) * CH, d[(k + 1) & 1]);
+#pragma unroll
+          for (int j = 0; j < CH; ++j) acc[k * CH + j] = fmaf(__uint_as_float(d[k & 1][j]), f, acc[k * CH + j]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(tempty_at[b]);
+        if ((b ^= 1) == 0) tph ^= 1;
+      }
+      // ---- the tile: 32 rows x 32 words at a time through shared memory, then a row's words by neighbouring lanes
+      const int64_t row0 = row_of(t) - lane, col0 = col_of(t);
+      const bool half = a.out != QGEMV_OUT_F32;
+      const int cols = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(HB), a.N - col0)));
+      const int rows = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(32), a.M - row0)));
+      const bool whole = !half || a.y_stride % 2 == 0;  // words of two elements are aligned
+      const uint32_t mine = out + lane * (kManyPad * 4);
+      auto flush = [&](int c, int n) {  // columns c .. of this half, n of them in a word
+        __syncwarp();
+        const int at = c + n * lane;
+#pragma unroll 4
+        for (int i = 0; i < rows; ++i) {
+          const uint32_t w = lds_u32(out + (i * kManyPad + lane) * 4);
+          const int64_t to = (row0 + i) * a.y_stride + col0 + at;
+          if (n == 1) {
+            if (at < cols) static_cast<uint32_t*>(a.y)[to] = w;
+          } else if (whole && at + 1 < cols) {
+            *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.y) + to) = w;
+          } else {
+            if (at < cols) static_cast<uint16_t*>(a.y)[to] = static_cast<uint16_t>(w);
+            if (at + 1 < cols) static_cast<uint16_t*>(a.y)[to + 1] = static_cast<uint16_t>(w >> 16);
+          }
+        }
+        __syncwarp();
+      };
+      if (half) {
+#pragma unroll
+        for (int c = 0; c < HB; c += 64) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(mine + j * 4), "r"(pack2(a.out, acc[c + 2 * j], acc[c + 2 * j + 1])) : "memory");
+          flush(c, 2);
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < HB; c += 32) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) asm volatile("st.shared.f32 [%0], %1;" ::"r"(mine + j * 4), "f"(acc[c + j]) : "memory");
+          flush(c, 1);
+        }
+      }
+    }
+  }
+  __syncwarp();
+  if (!mbar_wait_bounded(done, 0, kDrainNs)) ok = false;
+  if (!ok) {
+    atomicOr(a.err, kDevErrTimeout);
+    // copies that were asked for but that no MMA waited for: they have a millisecond to land
+    const long long t0 = clock64();
+    while (clock64() - t0 < 2000000) {
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  scaled_cluster_meet();  // nobody leaves while the other CTA's arrivals are on their way
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 2 * BN);
+  }
+}
+
 const void* few_kernel_for(int BT);
 
 }  // namespace qg
