@@ -84,6 +84,7 @@ qgemv_status_t launch_few(const Handle& h, const qgemv_scaled_t& p, ScaledArgs a
 
 qgemv_status_t launch_many(const Handle& h, const qgemv_scaled_t& p, ScaledArgs a, cudaStream_t stream) {
   a.x_tiles = static_cast<int>((p.M + kManyRows - 1) / kManyRows);
+  a.wide = a.blocks % 4 == 0 && p.x_scale_stride % 4 == 0 && aligned16(p.x_scale) && aligned16(p.w_scale);
   const int64_t pairs = h.sms / 2;
   // rounds of tiles, by the time that a tile takes
   auto cost = [&](int BN) { return (a.x_tiles * ((p.N + BN - 1) / BN) + pairs - 1) / pairs * BN; };
@@ -91,6 +92,7 @@ qgemv_status_t launch_many(const Handle& h, const qgemv_scaled_t& p, ScaledArgs 
   CUtensorMap wmap, xmap;
   if (!encode(h, p.W, p.N, p.K, p.K, BN / 2, &wmap) || !encode(h, p.x, p.M, p.K, p.x_stride, kManyRows / 2, &xmap)) return QGEMV_ERR_CUDA;
   const int64_t tiles = a.x_tiles * ((p.N + BN - 1) / BN);
+  if (tiles > 0x7fffffff) return QGEMV_ERR_BAD_SHAPE;
   void* args[] = {&wmap, &xmap, &a};
   const void* fn = BN == 128 ? reinterpret_cast<const void*>(scaled_many_kernel<128>) : reinterpret_cast<const void*>(scaled_many_kernel<256>);
   return launch_dependent(fn, dim3(static_cast<unsigned>(2 * std::min<int64_t>(tiles, pairs))), kManyThreads, many_smem_bytes(BN), 2, args, stream)

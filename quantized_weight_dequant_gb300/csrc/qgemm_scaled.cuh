@@ -46,6 +46,7 @@ struct ScaledArgs {
   int out;
   int* err;
   uint64_t spin_ns;
+  int wide;       // the scales of four blocks are 16 aligned bytes
   int early;      // W may be read before the kernel before this one ends
   int stall;      // test hook: the first CTA withholds its first set of sums
 };
@@ -315,17 +316,16 @@ __global__ void __launch_bounds__(few_threads(BT), 2) scaled_few_kernel(const __
 // W (a CTA alone would need 96 bytes a cycle for the operands and 96 for the copies, of 128).  One persistent pair on
 // every two SMs, tiles of x first, so that the weights that are being read are shared by all of x.  Eight warps
 // scale and add, a half of the columns each, and write through shared memory, whole rows' pieces at a time.
-constexpr int kManyThreads = 32 * 10;
+constexpr int kManyThreads = 128 * 3;  // copies and MMAs, and two warpgroups of sums
+constexpr int kManyRegs[2] = {104, 200};  // together what the block is launched with, 3 x 168
 constexpr int kManyRows = 256;  // rows of x of a tile
-constexpr int kManyRing = 8;    // scales on their way, per thread
 
 __host__ __device__ constexpr int many_stage_bytes(int BN) { return kScaledBlock * (kManyRows / 2 + BN / 2); }
-__host__ __device__ constexpr int many_stages(int BN) { return 164 * 1024 / many_stage_bytes(BN); }
-constexpr int kManyPad = 33;
+__host__ __device__ constexpr int many_stages(int BN) { return 188 * 1024 / many_stage_bytes(BN); }
+constexpr int kManyPad = 36;  // words of a row's 32, so that 16-byte accesses meet no bank twice
 constexpr int kManyOutBytes = 8 * 32 * kManyPad * 4;                 // a warp's 32 rows x 32 words
-constexpr int kManyScaleBytes = 2 * kManyRing * 256 * 4;
 __host__ __device__ constexpr size_t many_smem_bytes(int BN) {
-  return 1024 + static_cast<size_t>(many_stages(BN)) * many_stage_bytes(BN) + 256 + kManyOutBytes + kManyScaleBytes;
+  return 1024 + static_cast<size_t>(many_stages(BN)) * many_stage_bytes(BN) + 256 + kManyOutBytes;
 }
 
 template <int BN>
@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) scaled_many_kernel(const __gr
   static_assert(8 * (2 * S + 4) + 8 + 8 <= 256, "barriers");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const unsigned rank = blockIdx.x & 1, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-  const int64_t tiles = static_cast<int64_t>(a.x_tiles) * ((static_cast<int64_t>(a.N) + BN - 1) / BN);
+  const unsigned x_tiles = static_cast<unsigned>(a.x_tiles), tiles = x_tiles * ((static_cast<unsigned>(a.N) + BN - 1) / BN);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) mbar_init(full(s), 1), mbar_init(empty(s), 1);
@@ -364,14 +364,14 @@ __global__ void __launch_bounds__(kManyThreads, 1) scaled_many_kernel(const __gr
   pdl_launch_dependents();
   pdl_wait();
 
+  if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kManyRegs[0]));
   if (warp == 0) {
     if (lane == 0) {  // ---- copies
       int s = 0;
       uint32_t ph = 1;
       bool filled = false;  // every stage has been used
-      for (int64_t t = pair; t < tiles && ok; t += pairs) {
-        const int m = static_cast<int>(t % a.x_tiles) * kManyRows + static_cast<int>(rank) * (kManyRows / 2);
-        const int64_t n = t / a.x_tiles * BN + rank * HB;
+      for (unsigned t = pair; t < tiles && ok; t += pairs) {
+        const int m = static_cast<int>(t % x_tiles * kManyRows + rank * (kManyRows / 2)), n = static_cast<int>(t / x_tiles * BN + rank * HB);
         for (int kb = 0; kb < a.blocks; ++kb) {
           if (filled && !mbar_wait_bounded(empty(s), ph, a.spin_ns)) {
             ok = false;
@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) scaled_many_kernel(const __gr
           if (rank == 0) mbar_arrive_expect_tx(full(s), 2 * STAGE);
           const uint32_t bar = cluster_address(full(s), 0);
           tma_load_2d_pair(base + s * STAGE, &xmap, kb * kScaledBlock, m, bar);
-          tma_load_2d_pair(base + s * STAGE + XBYTES, &wmap, kb * kScaledBlock, static_cast<int>(n), bar);
+          tma_load_2d_pair(base + s * STAGE + XBYTES, &wmap, kb * kScaledBlock, n, bar);
           if (++s == S) s = 0, ph ^= 1, filled = true;
         }
       }
@@ -392,122 +392,159 @@ __global__ void __launch_bounds__(kManyThreads, 1) scaled_many_kernel(const __gr
       int s = 0, b = 0;
       uint32_t ph = 0, tph = 1;
       int64_t seen = 0;
-      for (int64_t t = pair; t < tiles && ok; t += pairs) {
+      bool is_full = mbar_test(full(0), 0);  // asked while the block before is being issued
+      for (unsigned t = pair; t < tiles && ok; t += pairs) {
         for (int kb = 0; kb < a.blocks; ++kb, ++seen) {
-          if ((seen >= 2 && !mbar_wait_bounded(tempty(b), tph, a.spin_ns)) || !mbar_wait_bounded(full(s), ph, a.spin_ns)) {
+          if ((seen >= 2 && !mbar_wait_bounded(tempty(b), tph, a.spin_ns)) || (!is_full && !mbar_wait_bounded(full(s), ph, a.spin_ns))) {
             ok = false;
             break;
           }
           tc_fence_after();
           const uint64_t xd = d0 + static_cast<uint64_t>(s * (STAGE / 16)), wd = xd + XBYTES / 16;
-#pragma unroll
-          for (int k = 0; k < kScaledBlock / 32; ++k) tc_mma_f8_pair(tmem + b * BN, xd + 2 * k, wd + 2 * k, idesc, k > 0);
-          tc_commit_pair(empty(s));
-          if (!(a.stall && pair == 0 && seen == 0)) tc_commit_pair(tfull(b));
+          const int now = b;
           if (++s == S) s = 0, ph ^= 1;
           if ((b ^= 1) == 0) tph ^= 1;
+          is_full = mbar_test(full(s), ph);
+#pragma unroll
+          for (int k = 0; k < kScaledBlock / 32; ++k) tc_mma_f8_pair(tmem + now * BN, xd + 2 * k, wd + 2 * k, idesc, k > 0);
+          if (!(a.stall && pair == 0 && seen == 0)) tc_commit_pair(tfull(now));
         }
       }
       tc_commit_pair(done);  // also after a failure: nobody leaves while MMAs run
     }
-  } else {
+  } else if (warp >= 4) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs[1]));
     // ---- scales and sums: this thread's row of x is its TMEM lane, its columns are half hh of the weight rows
-    const int q4 = warp & 3, hh = (warp - 2) >> 2, r = 32 * q4 + lane;
+    const int q4 = warp & 3, hh = (warp - 4) >> 2, r = 32 * q4 + lane;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * q4) << 16) + hh * HB;
-    const uint32_t out = bars + 256 + (warp - 2) * (32 * kManyPad * 4), ring = bars + 256 + kManyOutBytes + (threadIdx.x - 64) * 4;
-    const uint32_t tempty_at[2] = {cluster_address(tempty(0), 0), cluster_address(tempty(1), 0)};
-    auto row_of = [&](int64_t t) { return static_cast<int64_t>(t % a.x_tiles) * kManyRows + rank * (kManyRows / 2) + r; };
-    auto col_of = [&](int64_t t) { return t / a.x_tiles * BN + hh * HB; };
-    // scales of the blocks to come, in this thread's own ring (rows and columns past the end have none: nobody stores their sums)
-    int64_t ft = pair;
-    int fkb = 0, fslot = 0;
-    const float *fx = nullptr, *fw = nullptr;
-    auto aim = [&] {
-      const int64_t m = row_of(ft), n = col_of(ft);
-      fx = ft < tiles && m < a.M ? a.xs + m * a.xs_stride : nullptr;
-      fw = ft < tiles && n < a.N ? a.ws + n / kScaledRows * a.blocks : nullptr;
+    const uint32_t out = bars + 256 + (warp - 4) * (32 * kManyPad * 4);
+    const uint32_t tempty_at = cluster_address(tempty(0), 0);  // of the second buffer 8 bytes behind
+    // the scales of four blocks are read while the four before them are added (rows and columns past the end have none: nobody
+    // stores their sums)
+    struct Four {
+      float x[4], w[4];
     };
-    auto fetch = [&] {
-      if (fx) copy4(ring + fslot * 1024, fx + fkb);
-      if (fw) copy4(ring + (kManyRing + fslot) * 1024, fw + fkb);
-      copy4_commit();
-      if (++fslot == kManyRing) fslot = 0;
-      if (++fkb == a.blocks) {
-        fkb = 0;
-        ft += pairs;
-        aim();
+    int64_t row = 0, col = 0;  // of the tile whose scales are being read
+    const float *xs = nullptr, *ws = nullptr;
+    auto aim = [&](unsigned t) {
+      row = static_cast<int64_t>(t % x_tiles) * kManyRows + rank * (kManyRows / 2) + r;
+      col = static_cast<int64_t>(t / x_tiles) * BN + hh * HB;
+      const bool in = t < tiles && row < a.M && col < a.N;
+      xs = in ? a.xs + row * a.xs_stride : nullptr;
+      ws = in ? a.ws + col / kScaledRows * a.blocks : nullptr;
+    };
+    auto fetch = [&](int kb) {
+      Four v;
+      if (a.wide) {
+        const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+        const float4 xv = xs ? __ldg(reinterpret_cast<const float4*>(xs + kb)) : zero, wv = xs ? __ldg(reinterpret_cast<const float4*>(ws + kb)) : zero;
+        v.x[0] = xv.x, v.x[1] = xv.y, v.x[2] = xv.z, v.x[3] = xv.w;
+        v.w[0] = wv.x, v.w[1] = wv.y, v.w[2] = wv.z, v.w[3] = wv.w;
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const bool here = xs && kb + q < a.blocks;
+          v.x[q] = here ? __ldg(xs + kb + q) : 0.f;
+          v.w[q] = here ? __ldg(ws + kb + q) : 0.f;
+        }
       }
+      return v;
     };
-    aim();
-#pragma unroll 1
-    for (int j = 0; j < kManyRing - 1; ++j) fetch();
     float acc[HB];
-    int b = 0, slot = 0;
+    int b = 0, s = 0;
     uint32_t tph = 0;
-    for (int64_t t = pair; t < tiles; t += pairs) {
+    aim(pair);
+    Four next = fetch(0);
+    for (unsigned t = pair; t < tiles; t += pairs) {
+      const int64_t row0 = row - lane, col0 = col;
 #pragma unroll
       for (int c = 0; c < HB; ++c) acc[c] = 0.f;
-      for (int kb = 0; kb < a.blocks; ++kb) {
-        copy4_wait<kManyRing - 2>();
-        const float f = __uint_as_float(lds_u32(ring + slot * 1024)) * __uint_as_float(lds_u32(ring + (kManyRing + slot) * 1024));
-        if (++slot == kManyRing) slot = 0;
-        fetch();
-        // a warp that gave up goes on without waiting: the other CTA counts on it
-        if (ok && !mbar_wait_bounded(tfull(b), tph, a.spin_ns)) ok = false;
-        tc_fence_after();
-        constexpr int CH = 16, NC = HB / CH;
-        uint32_t d[2][CH];
-        tmem_ld16(lanes + b * BN, d[0]);
+      for (int kb = 0; kb < a.blocks; kb += 4) {
+        float f[4];
 #pragma unroll
-        for (int k = 0; k < NC; ++k) {
-          tmem_ld_arrived(d[k & 1]);
-          if (k + 1 < NC) tmem_ld16(lanes + b * BN + (k + 1) * CH, d[(k + 1) & 1]);
+        for (int q = 0; q < 4; ++q) f[q] = next.x[q] * next.w[q];
+        const bool last = kb + 4 >= a.blocks;
+        if (last) aim(t + pairs);
+        next = fetch(last ? 0 : kb + 4);
 #pragma unroll
-          for (int j = 0; j < CH; ++j) acc[k * CH + j] = fmaf(__uint_as_float(d[k & 1][j]), f, acc[k * CH + j]);
+        for (int q = 0; q < 4; ++q) {
+          if (kb + q >= a.blocks) break;
+          // a warp that gave up goes on without waiting: the other CTA counts on it
+          if (ok && !mbar_wait_bounded(tfull(b), tph, a.spin_ns)) ok = false;
+          tc_fence_after();
+          constexpr int CH = 32, NC = HB / CH;
+          uint32_t d[CH];
+          const uint32_t from = lanes + b * BN, to = tempty_at + 8u * b;
+          // the block's MMAs are complete, and so are their reads of its stage
+          if (warp == 4 && lane == 0) mbar_arrive(empty(s));
+          if (++s == S) s = 0;
+          if ((b ^= 1) == 0) tph ^= 1;
+#pragma unroll
+          for (int k = 0; k < NC; ++k) {
+            tmem_ld32(from + k * CH, d);
+            if (k + 1 == NC) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive_remote(to);
+            }
+#pragma unroll
+            for (int j = 0; j < CH; ++j) acc[k * CH + j] = fmaf(__uint_as_float(d[j]), f[q], acc[k * CH + j]);
+          }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_remote(tempty_at[b]);
-        if ((b ^= 1) == 0) tph ^= 1;
       }
-      // ---- the tile: 32 rows x 32 words at a time through shared memory, then a row's words by neighbouring lanes
-      const int64_t row0 = row_of(t) - lane, col0 = col_of(t);
-      const bool half = a.out != QGEMV_OUT_F32;
+      // ---- the tile: 32 rows x 32 words at a time through shared memory, then a row's words by neighbouring lanes, four each
+      // where rows of y are whole 16 bytes apart
       const int cols = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(HB), a.N - col0)));
       const int rows = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(32), a.M - row0)));
-      const bool whole = !half || a.y_stride % 2 == 0;  // words of two elements are aligned
-      const uint32_t mine = out + lane * (kManyPad * 4);
       auto flush = [&](int c, int n) {  // columns c .. of this half, n of them in a word
         __syncwarp();
-        const int at = c + n * lane;
-#pragma unroll 4
-        for (int i = 0; i < rows; ++i) {
-          const uint32_t w = lds_u32(out + (i * kManyPad + lane) * 4);
-          const int64_t to = (row0 + i) * a.y_stride + col0 + at;
-          if (n == 1) {
-            if (at < cols) static_cast<uint32_t*>(a.y)[to] = w;
-          } else if (whole && at + 1 < cols) {
-            *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.y) + to) = w;
-          } else {
-            if (at < cols) static_cast<uint16_t*>(a.y)[to] = static_cast<uint16_t>(w);
-            if (at + 1 < cols) static_cast<uint16_t*>(a.y)[to + 1] = static_cast<uint16_t>(w >> 16);
+        const bool wide = a.y_stride % (4 * n) == 0 && c + 32 * n <= cols;
+        if (wide) {
+          const int at = c + 4 * n * (lane & 7);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int row = 4 * i + (lane >> 3);
+            const uint4 w = lds_v4(out + (row * kManyPad + 4 * (lane & 7)) * 4);
+            const int64_t to = (row0 + row) * a.y_stride + col0 + at;
+            if (row < rows) *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.y) + to * (4 / n)) = w;
+          }
+        } else {
+          const int at = c + n * lane;
+          for (int i = 0; i < rows; ++i) {
+            const uint32_t w = lds_u32(out + (i * kManyPad + lane) * 4);
+            const int64_t to = (row0 + i) * a.y_stride + col0 + at;
+            if (n == 1) {
+              if (at < cols) static_cast<uint32_t*>(a.y)[to] = w;
+            } else {
+              if (at < cols) static_cast<uint16_t*>(a.y)[to] = static_cast<uint16_t>(w);
+              if (at + 1 < cols) static_cast<uint16_t*>(a.y)[to + 1] = static_cast<uint16_t>(w >> 16);
+            }
           }
         }
         __syncwarp();
       };
-      if (half) {
+      const uint32_t mine = out + lane * (kManyPad * 4);
+      auto put = [&](int j, uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3) {
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(mine + j * 4), "r"(w0), "r"(w1), "r"(w2), "r"(w3) : "memory");
+      };
+      if (a.out != QGEMV_OUT_F32) {
 #pragma unroll
         for (int c = 0; c < HB; c += 64) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            asm volatile("st.shared.u32 [%0], %1;" ::"r"(mine + j * 4), "r"(pack2(a.out, acc[c + 2 * j], acc[c + 2 * j + 1])) : "memory");
+          for (int j = 0; j < 32; j += 4) {
+            const float* v = acc + c + 2 * j;
+            put(j, pack2(a.out, v[0], v[1]), pack2(a.out, v[2], v[3]), pack2(a.out, v[4], v[5]), pack2(a.out, v[6], v[7]));
+          }
           flush(c, 2);
         }
       } else {
 #pragma unroll
         for (int c = 0; c < HB; c += 32) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) asm volatile("st.shared.f32 [%0], %1;" ::"r"(mine + j * 4), "f"(acc[c + j]) : "memory");
+          for (int j = 0; j < 32; j += 4) {
+            const float* v = acc + c + j;
+            put(j, __float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+          }
           flush(c, 1);
         }
       }
