@@ -132,63 +132,56 @@ __global__ void __launch_bounds__(few_threads(BT), 2) scaled_few_kernel(const __
   bool ok = true;
   pdl_launch_dependents();
 
-  if (warp == 0) {
-    if (lane == 0) {  // ---- copies
-      const int ahead = a.early ? min(S, n) : 0;
-      for (int j = 0; j < ahead; ++j) {
+  // The copying and the issuing warp go through their loops as a whole and let one lane do the work: what is the same for all
+  // lanes then stays in uniform registers.  One that gave up goes on without waiting (and copying).
+  if (warp == 0) {  // ---- copies
+    const int ahead = a.early ? min(S, n) : 0;
+    for (int j = 0; j < ahead; ++j) {
+      if (elect_one()) {
         mbar_arrive_expect_tx(full(j), STAGE);
         tma_load_2d(base + j * STAGE, &wmap, (kb0 + j) * kScaledBlock, wt * kScaledRows, full(j));
       }
-      pdl_wait();
-      int i = 0, s = 0;
-      uint32_t ph = 1;
-      for (; i < n; ++i) {
-        if (i >= S && !mbar_wait_bounded(empty(s), ph, a.spin_ns)) {
-          ok = false;
-          break;
-        }
+    }
+    pdl_wait();
+    int s = 0, issued = 0;
+    uint32_t ph = 1;
+    for (int i = 0; i < n; ++i) {
+      if (ok && i >= S) ok = mbar_wait_bounded(empty(s), ph, a.spin_ns);
+      if (ok) issued = i + 1;
+      if (ok && elect_one()) {
         if (i >= ahead) {
           mbar_arrive_expect_tx(full(s), STAGE);
           tma_load_2d(base + s * STAGE, &wmap, (kb0 + i) * kScaledBlock, wt * kScaledRows, full(s));
         }
         tma_load_2d(base + s * STAGE + WBYTES, &xmap, (kb0 + i) * kScaledBlock, m0, full(s));
-        if (++s == S) s = 0, ph ^= 1;
       }
-      // what was issued last has landed before the CTA may leave
-      for (int j = i > S ? i - S : 0; j < i; ++j)
-        if (!mbar_wait_bounded(full(j % S), static_cast<uint32_t>(j / S) & 1, kDrainNs)) ok = false;
+      if (++s == S) s = 0, ph ^= 1;
     }
-  } else if (warp == 1) {
-    if (lane == 0) {  // ---- MMAs
-      constexpr uint32_t idesc = tc_idesc_e4m3(kScaledRows, BT);
-      const uint64_t d0 = tc_desc_sw128(base);
-      int s = 0, b = 0;
-      uint32_t ph = 0, tph = 1;
-      for (int i = 0; i < n && ok;) {
-        const int nq = min(Q, n - i);
-        if (i >= 2 * Q && !mbar_wait_bounded(tempty(b), tph, a.spin_ns)) {
-          ok = false;
-          break;
-        }
+    // what was issued last has landed before the CTA may leave
+    for (int j = max(issued - S, 0); j < issued; ++j)
+      if (!mbar_wait_bounded(full(j % S), static_cast<uint32_t>(j / S) & 1, kDrainNs)) ok = false;
+  } else if (warp == 1) {  // ---- MMAs
+    constexpr uint32_t idesc = tc_idesc_e4m3(kScaledRows, BT);
+    const uint64_t d0 = tc_desc_sw128(base);
+    int s = 0, b = 0;
+    uint32_t ph = 0, tph = 1;
+    for (int i = 0; i < n; i += Q) {
+      if (ok && i >= 2 * Q) ok = mbar_wait_bounded(tempty(b), tph, a.spin_ns);
+      for (int q = 0; q < Q && i + q < n; ++q) {
+        if (ok) ok = mbar_wait_bounded(full(s), ph, a.spin_ns);
         tc_fence_after();
-        for (int q = 0; q < nq; ++q) {
-          if (!mbar_wait_bounded(full(s), ph, a.spin_ns)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint64_t wd = d0 + static_cast<uint64_t>(s * (STAGE / 16)), xd = wd + WBYTES / 16;
+        const uint64_t wd = d0 + static_cast<uint64_t>(s * (STAGE / 16)), xd = wd + WBYTES / 16;
+        if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < kScaledBlock / 32; ++k) tc_mma_f8(tmem + (b * Q + q) * BT, wd + 2 * k, xd + 2 * k, idesc, k > 0);
           tc_commit(empty(s));
-          if (++s == S) s = 0, ph ^= 1;
         }
-        if (!(a.stall && blockIdx.x == 0 && i == 0)) tc_commit(tfull(b));
-        if ((b ^= 1) == 0) tph ^= 1;
-        i += nq;
+        if (++s == S) s = 0, ph ^= 1;
       }
-      tc_commit(done);  // also after a failure: nobody leaves, or writes over the stages, while MMAs run
+      if (!(a.stall && blockIdx.x == 0 && i == 0) && elect_one()) tc_commit(tfull(b));
+      if ((b ^= 1) == 0) tph ^= 1;
     }
+    if (elect_one()) tc_commit(done);  // nobody leaves, or writes over the stages, while MMAs run
   } else {
     // ---- scales and sums: this thread's weight row is its TMEM lane, its columns are half hh of x's rows
     const int q4 = warp & 3, hh = (warp - 2) >> 2, r = 32 * q4 + lane, tid = threadIdx.x - 64;
@@ -365,52 +358,48 @@ __global__ void __launch_bounds__(kManyThreads, 1) scaled_many_kernel(const __gr
   pdl_wait();
 
   if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kManyRegs[0]));
-  if (warp == 0) {
-    if (lane == 0) {  // ---- copies
-      int s = 0;
-      uint32_t ph = 1;
-      bool filled = false;  // every stage has been used
-      for (unsigned t = pair; t < tiles && ok; t += pairs) {
-        const int m = static_cast<int>(t % x_tiles * kManyRows + rank * (kManyRows / 2)), n = static_cast<int>(t / x_tiles * BN + rank * HB);
-        for (int kb = 0; kb < a.blocks; ++kb) {
-          if (filled && !mbar_wait_bounded(empty(s), ph, a.spin_ns)) {
-            ok = false;
-            break;
-          }
+  if (warp == 0) {  // ---- copies (whole warps go through the loops, as above)
+    int s = 0;
+    uint32_t ph = 1;
+    bool filled = false;  // every stage has been used
+    for (unsigned t = pair; t < tiles; t += pairs) {
+      const int m = static_cast<int>(t % x_tiles * kManyRows + rank * (kManyRows / 2)), n = static_cast<int>(t / x_tiles * BN + rank * HB);
+      for (int kb = 0; kb < a.blocks; ++kb) {
+        if (ok && filled) ok = mbar_wait_bounded(empty(s), ph, a.spin_ns);
+        const uint32_t bar = cluster_address(full(s), 0);
+        if (ok && elect_one()) {
           if (rank == 0) mbar_arrive_expect_tx(full(s), 2 * STAGE);
-          const uint32_t bar = cluster_address(full(s), 0);
           tma_load_2d_pair(base + s * STAGE, &xmap, kb * kScaledBlock, m, bar);
           tma_load_2d_pair(base + s * STAGE + XBYTES, &wmap, kb * kScaledBlock, n, bar);
-          if (++s == S) s = 0, ph ^= 1, filled = true;
         }
+        if (++s == S) s = 0, ph ^= 1, filled = true;
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {  // ---- MMAs
+    if (rank == 0) {  // ---- MMAs
       constexpr uint32_t idesc = tc_idesc_e4m3(kManyRows, BN);
       const uint64_t d0 = tc_desc_sw128(base);
       int s = 0, b = 0;
       uint32_t ph = 0, tph = 1;
-      int64_t seen = 0;
-      bool is_full = mbar_test(full(0), 0);  // asked while the block before is being issued
-      for (unsigned t = pair; t < tiles && ok; t += pairs) {
-        for (int kb = 0; kb < a.blocks; ++kb, ++seen) {
-          if ((seen >= 2 && !mbar_wait_bounded(tempty(b), tph, a.spin_ns)) || (!is_full && !mbar_wait_bounded(full(s), ph, a.spin_ns))) {
-            ok = false;
-            break;
-          }
+      bool used = false;    // both buffers have been
+      bool is_full = false;  // asked while the block before is being issued
+      for (unsigned t = pair; t < tiles; t += pairs) {
+        for (int kb = 0; kb < a.blocks; ++kb) {
+          if (ok && used) ok = mbar_wait_bounded(tempty(b), tph, a.spin_ns);
+          if (ok && !is_full) ok = mbar_wait_bounded(full(s), ph, a.spin_ns);
           tc_fence_after();
           const uint64_t xd = d0 + static_cast<uint64_t>(s * (STAGE / 16)), wd = xd + XBYTES / 16;
-          const int now = b;
-          if (++s == S) s = 0, ph ^= 1;
-          if ((b ^= 1) == 0) tph ^= 1;
-          is_full = mbar_test(full(s), ph);
+          if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < kScaledBlock / 32; ++k) tc_mma_f8_pair(tmem + now * BN, xd + 2 * k, wd + 2 * k, idesc, k > 0);
-          if (!(a.stall && pair == 0 && seen == 0)) tc_commit_pair(tfull(now));
+            for (int k = 0; k < kScaledBlock / 32; ++k) tc_mma_f8_pair(tmem + b * BN, xd + 2 * k, wd + 2 * k, idesc, k > 0);
+            if (!(a.stall && pair == 0 && t == pair && kb == 0)) tc_commit_pair(tfull(b));
+          }
+          if (++s == S) s = 0, ph ^= 1;
+          if ((b ^= 1) == 0) tph ^= 1, used = true;
+          is_full = mbar_test(full(s), ph);
         }
       }
-      tc_commit_pair(done);  // also after a failure: nobody leaves while MMAs run
+      if (elect_one()) tc_commit_pair(done);  // nobody leaves while MMAs run
     }
   } else if (warp >= 4) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs[1]));
