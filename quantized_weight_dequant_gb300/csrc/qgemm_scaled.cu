@@ -86,8 +86,8 @@ qgemv_status_t launch_many(const Handle& h, const qgemv_scaled_t& p, ScaledArgs 
   a.x_tiles = static_cast<int>((p.M + kManyRows - 1) / kManyRows);
   a.wide = a.blocks % 4 == 0 && p.x_scale_stride % 4 == 0 && aligned16(p.x_scale) && aligned16(p.w_scale);
   const int64_t pairs = h.sms / 2;
-  // rounds of tiles, by the time that a tile takes
-  auto cost = [&](int BN) { return (a.x_tiles * ((p.N + BN - 1) / BN) + pairs - 1) / pairs * BN; };
+  // rounds of tiles, by the time that a block of a tile takes
+  auto cost = [&](int BN) { return (a.x_tiles * ((p.N + BN - 1) / BN) + pairs - 1) / pairs * (BN == 128 ? 3 : 4); };
   const int BN = cost(128) < cost(256) ? 128 : 256;
   CUtensorMap wmap, xmap;
   if (!encode(h, p.W, p.N, p.K, p.K, BN / 2, &wmap) || !encode(h, p.x, p.M, p.K, p.x_stride, kManyRows / 2, &xmap)) return QGEMV_ERR_CUDA;

@@ -23,9 +23,11 @@
 #include <cuda.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "../../include/qgemv.h"
 #include "qgemv_elems.cuh"
+#include "qgemv_mma.cuh"
 #include "qgemv_ptx.cuh"
 #include "qgemv_tcgen05.cuh"
 
@@ -309,38 +311,43 @@ __global__ void __launch_bounds__(few_threads(BT), 2) scaled_few_kernel(const __
 // W (a CTA alone would need 96 bytes a cycle for the operands and 96 for the copies, of 128).  One persistent pair on
 // every two SMs, tiles of x first, so that the weights that are being read are shared by all of x.  Eight warps
 // scale and add, a half of the columns each, and write through shared memory, whole rows' pieces at a time.
-constexpr int kManyThreads = 128 * 3;  // copies and MMAs, and two warpgroups of sums
-constexpr int kManyRegs[2] = {104, 200};  // together what the block is launched with, 3 x 168
+constexpr int kManyParts = 2;  // warpgroups of sums, each with a part of the columns
+constexpr int kManyThreads = 128 * (1 + kManyParts);
+constexpr int kManyRegs[2] = {88, 208};  // of the first warpgroup and the others: together what the block is launched with, 3 x 168
+constexpr int kManyChunk = 16;  // columns that are read at a time
 constexpr int kManyRows = 256;  // rows of x of a tile
 
 __host__ __device__ constexpr int many_stage_bytes(int BN) { return kScaledBlock * (kManyRows / 2 + BN / 2); }
-__host__ __device__ constexpr int many_stages(int BN) { return 188 * 1024 / many_stage_bytes(BN); }
-constexpr int kManyPad = 36;  // words of a row's 32, so that 16-byte accesses meet no bank twice
-constexpr int kManyOutBytes = 8 * 32 * kManyPad * 4;                 // a warp's 32 rows x 32 words
+__host__ __device__ constexpr int many_stages(int BN) { return 176 * 1024 / many_stage_bytes(BN); }
+constexpr int kManyPad = 64 / kManyParts + 4;  // so that 16-byte accesses meet no bank twice
+constexpr int kManyWords = 64 / kManyParts;  // of a row that a warp stages at a time
+constexpr int kManyOutBytes = 4 * kManyParts * 32 * kManyPad * 4;
+constexpr int kManyScaleBytes = 4 * 2 * 128 * 4;  // four blocks' products of the scales of 128 rows of x and up to two of W
 __host__ __device__ constexpr size_t many_smem_bytes(int BN) {
-  return 1024 + static_cast<size_t>(many_stages(BN)) * many_stage_bytes(BN) + 256 + kManyOutBytes;
+  return 1024 + static_cast<size_t>(many_stages(BN)) * many_stage_bytes(BN) + 256 + kManyOutBytes + kManyScaleBytes;
 }
 
 template <int BN>
 __global__ void __launch_bounds__(kManyThreads, 1) scaled_many_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
                                                                       const __grid_constant__ ScaledArgs a) {
-  constexpr int S = many_stages(BN), STAGE = many_stage_bytes(BN), XBYTES = kScaledBlock * kManyRows / 2, HB = BN / 2;
+  constexpr int S = many_stages(BN), STAGE = many_stage_bytes(BN), XBYTES = kScaledBlock * kManyRows / 2, HB = BN / kManyParts;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t bars = base + S * STAGE;
   auto full = [&](int s) { return bars + 8u * s; };             // of the pair's first CTA: both CTAs' copies have landed
   auto empty = [&](int s) { return bars + 8u * (S + s); };      // the MMAs that read the stage are complete
-  auto tfull = [&](int b) { return bars + 8u * (2 * S + b); };  // a block's sums are in TMEM
+  auto tfull = [&](int b) { return bars + 8u * (2 * S + b); };  // a block's sums are in TMEM and its scales' products in shared memory
   auto tempty = [&](int b) { return bars + 8u * (2 * S + 2 + b); };  // of the first CTA: both CTAs have read them
   const uint32_t done = bars + 8u * (2 * S + 4), tslot = done + 8;
   static_assert(8 * (2 * S + 4) + 8 + 8 <= 256, "barriers");
+  const uint32_t prod = bars + 256 + kManyOutBytes;  // [block % 4][128 rows of W][row of x]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const unsigned rank = blockIdx.x & 1, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const unsigned x_tiles = static_cast<unsigned>(a.x_tiles), tiles = x_tiles * ((static_cast<unsigned>(a.N) + BN - 1) / BN);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) mbar_init(full(s), 1), mbar_init(empty(s), 1);
-    for (int b = 0; b < 2; ++b) mbar_init(tfull(b), 1), mbar_init(tempty(b), 16);
+    for (int b = 0; b < 2; ++b) mbar_init(tfull(b), 3), mbar_init(tempty(b), 2 * 4 * kManyParts);
     mbar_init(done, 1);
     fence_mbar_init();
   }
@@ -363,7 +370,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) scaled_many_kernel(const __gr
     uint32_t ph = 1;
     bool filled = false;  // every stage has been used
     for (unsigned t = pair; t < tiles; t += pairs) {
-      const int m = static_cast<int>(t % x_tiles * kManyRows + rank * (kManyRows / 2)), n = static_cast<int>(t / x_tiles * BN + rank * HB);
+      const int m = static_cast<int>(t % x_tiles * kManyRows + rank * (kManyRows / 2)), n = static_cast<int>(t / x_tiles * BN + rank * (BN / 2));
       for (int kb = 0; kb < a.blocks; ++kb) {
         if (ok && filled) ok = mbar_wait_bounded(empty(s), ph, a.spin_ns);
         const uint32_t bar = cluster_address(full(s), 0);
@@ -401,106 +408,123 @@ __global__ void __launch_bounds__(kManyThreads, 1) scaled_many_kernel(const __gr
       }
       if (elect_one()) tc_commit_pair(done);  // nobody leaves while MMAs run
     }
-  } else if (warp >= 4) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs[1]));
-    // ---- scales and sums: this thread's row of x is its TMEM lane, its columns are half hh of the weight rows
-    const int q4 = warp & 3, hh = (warp - 4) >> 2, r = 32 * q4 + lane;
-    const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * q4) << 16) + hh * HB;
-    const uint32_t out = bars + 256 + (warp - 4) * (32 * kManyPad * 4);
-    const uint32_t tempty_at = cluster_address(tempty(0), 0);  // of the second buffer 8 bytes behind
-    // the scales of four blocks are read while the four before them are added (rows and columns past the end have none: nobody
-    // stores their sums)
+  } else if (warp < 4) {
+    // ---- products of scales: two rows of x a lane.  The scales of four blocks are read while the four before them are used (rows
+    // and columns past the end have none: nobody stores their sums)
+    constexpr int WB = BN / kScaledRows;
+    const unsigned r = (warp - 2) * 32 + lane;  // and 64 rows further
     struct Four {
-      float x[4], w[4];
+      float x[2][4], w[WB][4];
     };
-    int64_t row = 0, col = 0;  // of the tile whose scales are being read
-    const float *xs = nullptr, *ws = nullptr;
-    auto aim = [&](unsigned t) {
-      row = static_cast<int64_t>(t % x_tiles) * kManyRows + rank * (kManyRows / 2) + r;
-      col = static_cast<int64_t>(t / x_tiles) * BN + hh * HB;
-      const bool in = t < tiles && row < a.M && col < a.N;
-      xs = in ? a.xs + row * a.xs_stride : nullptr;
-      ws = in ? a.ws + col / kScaledRows * a.blocks : nullptr;
-    };
-    auto fetch = [&](int kb) {
+    auto fetch = [&](unsigned t, int kb) {
       Four v;
-      if (a.wide) {
-        const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-        const float4 xv = xs ? __ldg(reinterpret_cast<const float4*>(xs + kb)) : zero, wv = xs ? __ldg(reinterpret_cast<const float4*>(ws + kb)) : zero;
-        v.x[0] = xv.x, v.x[1] = xv.y, v.x[2] = xv.z, v.x[3] = xv.w;
-        v.w[0] = wv.x, v.w[1] = wv.y, v.w[2] = wv.z, v.w[3] = wv.w;
-      } else {
+      const int64_t row = static_cast<int64_t>(t % x_tiles) * kManyRows + rank * (kManyRows / 2) + r, wrow = static_cast<int64_t>(t / x_tiles) * WB;
+      auto four = [&](const float* at, bool in, float (&f)[4]) {
+        if (a.wide) {
+          const float4 q = in ? __ldg(reinterpret_cast<const float4*>(at)) : make_float4(0.f, 0.f, 0.f, 0.f);
+          f[0] = q.x, f[1] = q.y, f[2] = q.z, f[3] = q.w;
+        } else {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const bool here = xs && kb + q < a.blocks;
-          v.x[q] = here ? __ldg(xs + kb + q) : 0.f;
-          v.w[q] = here ? __ldg(ws + kb + q) : 0.f;
+          for (int q = 0; q < 4; ++q) f[q] = in && kb + q < a.blocks ? __ldg(at + q) : 0.f;
         }
-      }
+      };
+#pragma unroll
+      for (int j = 0; j < 2; ++j) four(a.xs + (row + 64 * j) * a.xs_stride + kb, t < tiles && row + 64 * j < a.M, v.x[j]);
+#pragma unroll
+      for (int j = 0; j < WB; ++j) four(a.ws + (wrow + j) * a.blocks + kb, t < tiles && (wrow + j) * kScaledRows < a.N, v.w[j]);
       return v;
     };
-    float acc[HB];
-    int b = 0, s = 0;
-    uint32_t tph = 0;
-    aim(pair);
-    Four next = fetch(0);
+    // The products of a block go out when the sums of the one two before it are known to be there: its MMAs began when the sums
+    // of the block before that in the same place, and with them the products, had been read.
+    int b = 0, slot = 0;
+    uint32_t ph = 1;
+    bool used = false;
+    Four next = fetch(pair, 0);
     for (unsigned t = pair; t < tiles; t += pairs) {
-      const int64_t row0 = row - lane, col0 = col;
-#pragma unroll
-      for (int c = 0; c < HB; ++c) acc[c] = 0.f;
       for (int kb = 0; kb < a.blocks; kb += 4) {
-        float f[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) f[q] = next.x[q] * next.w[q];
+        const Four now = next;
         const bool last = kb + 4 >= a.blocks;
-        if (last) aim(t + pairs);
-        next = fetch(last ? 0 : kb + 4);
+        next = fetch(last ? t + pairs : t, last ? 0 : kb + 4);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           if (kb + q >= a.blocks) break;
-          // a warp that gave up goes on without waiting: the other CTA counts on it
-          if (ok && !mbar_wait_bounded(tfull(b), tph, a.spin_ns)) ok = false;
-          tc_fence_after();
-          constexpr int CH = 32, NC = HB / CH;
-          uint32_t d[CH];
-          const uint32_t from = lanes + b * BN, to = tempty_at + 8u * b;
-          // the block's MMAs are complete, and so are their reads of its stage
-          if (warp == 4 && lane == 0) mbar_arrive(empty(s));
-          if (++s == S) s = 0;
-          if ((b ^= 1) == 0) tph ^= 1;
+          if (ok && used) ok = mbar_wait_bounded(tfull(b), ph, a.spin_ns);
+          const uint32_t to = prod + slot * (2 * 128 * 4) + r * 4;
+          slot = (slot + 1) & 3;
 #pragma unroll
-          for (int k = 0; k < NC; ++k) {
-            tmem_ld32(from + k * CH, d);
-            if (k + 1 == NC) {
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive_remote(to);
-            }
+          for (int w = 0; w < WB; ++w)
 #pragma unroll
-            for (int j = 0; j < CH; ++j) acc[k * CH + j] = fmaf(__uint_as_float(d[j]), f[q], acc[k * CH + j]);
-          }
+            for (int j = 0; j < 2; ++j)
+              asm volatile("st.shared.f32 [%0], %1;" ::"r"(to + (w * 128 + j * 64) * 4), "f"(now.x[j][q] * now.w[w][q]) : "memory");
+          __syncwarp();
+          if (elect_one()) mbar_arrive(tfull(b));
+          if ((b ^= 1) == 0) ph ^= 1, used = true;
         }
       }
-      // ---- the tile: 32 rows x 32 words at a time through shared memory, then a row's words by neighbouring lanes, four each
-      // where rows of y are whole 16 bytes apart
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs[1]));
+    // ---- scales and sums: this thread's row of x is its TMEM lane, its columns are part hh of the weight rows
+    const int q4 = warp & 3, hh = (warp - 4) >> 2, r = 32 * q4 + lane;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * q4) << 16) + hh * HB;
+    const uint32_t out = bars + 256 + (warp - 4) * (32 * kManyPad * 4);
+    const uint32_t mine_f = prod + ((hh * HB) / kScaledRows * 128 + r) * 4;
+    const uint32_t tempty_at = cluster_address(tempty(0), 0);  // of the second buffer 8 bytes behind
+    float acc[HB];
+    int b = 0, s = 0, slot = 0;
+    uint32_t tph = 0;
+    for (unsigned t = pair; t < tiles; t += pairs) {
+#pragma unroll
+      for (int c = 0; c < HB; ++c) acc[c] = 0.f;
+#pragma unroll 1
+      for (int kb = 0; kb < a.blocks; ++kb) {
+        // a warp that gave up goes on without waiting: the other CTA counts on it
+        if (ok) ok = mbar_wait_bounded(tfull(b), tph, a.spin_ns);
+        tc_fence_after();
+        const uint32_t from = lanes + b * BN;
+        const float f = __uint_as_float(lds_u32(mine_f + slot * (2 * 128 * 4)));
+        slot = (slot + 1) & 3;
+        constexpr int CH = kManyChunk, NC = HB / CH;
+        uint32_t d[CH];
+#pragma unroll
+        for (int k = 0; k < NC; ++k) {
+          tmem_ld_now(from + k * CH, d);
+          if (k + 1 == NC) {
+            tc_fence_before();
+            __syncwarp();
+            if (elect_one()) {
+              mbar_arrive_remote(tempty_at + 8u * b);
+              if (warp == 4) mbar_arrive(empty(s));  // the block's MMAs are complete, and so are their reads of its stage
+            }
+            if (++s == S) s = 0;
+          }
+#pragma unroll
+          for (int j = 0; j < CH; ++j) acc[k * CH + j] = fmaf(__uint_as_float(d[j]), f, acc[k * CH + j]);
+        }
+        if ((b ^= 1) == 0) tph ^= 1;
+      }
+      // ---- the tile: 32 rows x kManyWords words at a time through shared memory, then a row's words by neighbouring lanes, four
+      // each where rows of y are whole 16 bytes apart
+      const int64_t row0 = static_cast<int64_t>(t % x_tiles) * kManyRows + rank * (kManyRows / 2) + 32 * q4, col0 = static_cast<int64_t>(t / x_tiles) * BN + hh * HB;
       const int cols = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(HB), a.N - col0)));
       const int rows = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(32), a.M - row0)));
-      auto flush = [&](int c, int n) {  // columns c .. of this half, n of them in a word
+      auto flush = [&](int c, int n) {  // columns c .. of this part, n of them in a word
+        constexpr int L = kManyWords / 4;  // lanes of a row
         __syncwarp();
-        const bool wide = a.y_stride % (4 * n) == 0 && c + 32 * n <= cols;
-        if (wide) {
-          const int at = c + 4 * n * (lane & 7);
+        if (a.y_stride % (4 * n) == 0 && c + kManyWords * n <= cols) {
+          const int64_t to = (row0 + lane / L) * a.y_stride + col0 + c + 4 * n * (lane % L);
+          uint8_t* y = static_cast<uint8_t*>(a.y) + to * (4 / n);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int row = 4 * i + (lane >> 3);
-            const uint4 w = lds_v4(out + (row * kManyPad + 4 * (lane & 7)) * 4);
-            const int64_t to = (row0 + row) * a.y_stride + col0 + at;
-            if (row < rows) *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.y) + to * (4 / n)) = w;
+          for (int i = 0; i < L; ++i) {
+            const int row = 32 / L * i + lane / L;
+            const uint4 w = lds_v4(out + (row * kManyPad + 4 * (lane % L)) * 4);
+            if (row < rows) *reinterpret_cast<uint4*>(y) = w;
+            y += 32 / L * a.y_stride * (4 / n);
           }
         } else {
-          const int at = c + n * lane;
-          for (int i = 0; i < rows; ++i) {
-            const uint32_t w = lds_u32(out + (i * kManyPad + lane) * 4);
+          const int at = c + n * (lane % kManyWords);
+          for (int i = lane / kManyWords; i < rows; i += 32 / kManyWords) {
+            const uint32_t w = lds_u32(out + (i * kManyPad + lane % kManyWords) * 4);
             const int64_t to = (row0 + i) * a.y_stride + col0 + at;
             if (n == 1) {
               if (at < cols) static_cast<uint32_t*>(a.y)[to] = w;
@@ -516,21 +540,26 @@ __global__ void __launch_bounds__(kManyThreads, 1) scaled_many_kernel(const __gr
       auto put = [&](int j, uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3) {
         asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(mine + j * 4), "r"(w0), "r"(w1), "r"(w2), "r"(w3) : "memory");
       };
-      if (a.out != QGEMV_OUT_F32) {
+      auto put_pairs = [&](auto bf) {
 #pragma unroll
-        for (int c = 0; c < HB; c += 64) {
+        for (int c = 0; c < HB; c += 2 * kManyWords) {
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) {
+          for (int j = 0; j < kManyWords; j += 4) {
             const float* v = acc + c + 2 * j;
-            put(j, pack2(a.out, v[0], v[1]), pack2(a.out, v[2], v[3]), pack2(a.out, v[4], v[5]), pack2(a.out, v[6], v[7]));
+            put(j, pair16<bf.value>(v[0], v[1]), pair16<bf.value>(v[2], v[3]), pair16<bf.value>(v[4], v[5]), pair16<bf.value>(v[6], v[7]));
           }
           flush(c, 2);
         }
+      };
+      if (a.out == QGEMV_OUT_BF16) {
+        put_pairs(std::true_type{});
+      } else if (a.out == QGEMV_OUT_F16) {
+        put_pairs(std::false_type{});
       } else {
 #pragma unroll
-        for (int c = 0; c < HB; c += 32) {
+        for (int c = 0; c < HB; c += kManyWords) {
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) {
+          for (int j = 0; j < kManyWords; j += 4) {
             const float* v = acc + c + j;
             put(j, __float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
           }
