@@ -33,21 +33,17 @@ constexpr int kSampleMaxCluster = 8;
 constexpr int kSampleUnit = 43;    // weights in units of 2^-43: 2^20 of them stay below 2^64
 constexpr float kInf = __builtin_huge_valf();
 
-struct SampleHist {
+struct alignas(16) SampleSmem {
   uint32_t count[kSampleBuckets], lo[kSampleBuckets], hi[kSampleBuckets];  // hi:lo a 64-bit sum
-};
-struct SampleSmem {
-  SampleHist hist[2];
-  uint64_t group_mass[2][kSampleGroups];
-  uint32_t group_count[2][kSampleGroups];
+  uint64_t group_mass[kSampleGroups];
+  uint32_t group_count[kSampleGroups];
   uint64_t warp_sum[kSampleWarps];
   uint64_t cta_sum[2];    // for the cluster
   uint32_t found[2];      // for the cluster
   uint64_t best_warp[kSampleWarps];
   uint64_t best;          // for the cluster
-  uint64_t pick_before, pick_mass;
+  uint64_t pick_before, pick_mass, pick_target;
   uint32_t pick_bucket, pick_count;
-  uint64_t pick_total;
   float th[8], tl[8];     // 2^(j/8) 2^31 as two floats
   uint64_t ti[8];         // and times 2^9 as a whole number
 };
@@ -95,25 +91,49 @@ __device__ __forceinline__ uint64_t warp_scan64(uint64_t v, int lane) {  // incl
 
 // ---------------------------------------------------------------------------- logits
 template <int T>
-__device__ __forceinline__ float logit_at(const void* row, int64_t i) {
-  float l;
-  if constexpr (T == QGEMV_OUT_F32) {
-    l = static_cast<const float*>(row)[i];
-  } else {
-    const uint32_t b = static_cast<const uint16_t*>(row)[i];
-    if constexpr (T == QGEMV_OUT_F16)
-      l = __half2float(__ushort_as_half(static_cast<unsigned short>(b)));
-    else
-      l = __uint_as_float(b << 16);
+constexpr int kVec = T == QGEMV_OUT_F32 ? 4 : 8;  // logits in 16 bytes
+
+// What takes part: NaN as -inf, -0 as 0 (so that equal logits have equal bits).
+__device__ __forceinline__ float usual(float l) { return l == l ? l + 0.f : -kInf; }
+
+template <int T>
+__device__ __forceinline__ void unpack(const uint4& v, float (&l)[kVec<T>]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (T == QGEMV_OUT_F32) {
+      l[j] = __uint_as_float(w[j]);
+    } else if constexpr (T == QGEMV_OUT_F16) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+      l[2 * j] = f.x, l[2 * j + 1] = f.y;
+    } else {
+      l[2 * j] = __uint_as_float(w[j] << 16), l[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+    }
   }
-  // NaN as -inf; -0 as 0, so that equal logits have equal bits
-  return l == l ? l + 0.f : -kInf;
+}
+// Back, for values that `unpack` gave (or -inf or 0).
+template <int T>
+__device__ __forceinline__ uint4 repack(const float (&l)[kVec<T>]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (T == QGEMV_OUT_F32) {
+      w[j] = __float_as_uint(l[j]);
+    } else if constexpr (T == QGEMV_OUT_F16) {
+      const __half2 h = __floats2half2_rn(l[2 * j], l[2 * j + 1]);
+      w[j] = *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+      w[j] = __float_as_uint(l[2 * j]) >> 16 | (__float_as_uint(l[2 * j + 1]) & 0xffff0000u);
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 // The logit's place in the order: smaller for larger logits.
 __device__ __forceinline__ uint32_t rank_key(float l) {
   const uint32_t b = __float_as_uint(l);
   return b & 0x80000000u ? b : ~(b | 0x80000000u);
 }
+__device__ __forceinline__ float key_logit(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k : ~k & 0x7fffffffu); }
 
 // 2^(j/8) 2^31 as two floats, and 2^(j/8) 2^40 as a whole number.
 __constant__ const float kPowHi[8] = {2147483648.f, 2341847552.f, 2553802752.f, 2784941824.f, 3037000448.f, 3311872512.f, 3611622656.f, 3938502400.f};
@@ -153,33 +173,46 @@ __device__ __forceinline__ uint64_t weight_of(float l, const RowScale& r, const 
   return (mant << (kSampleUnit - 40)) >> (-(k >> 3));
 }
 
+// Histogram 0: 40 buckets for each halving of the weight, behind 2^-32 64 for each doubling of the distance.
 __device__ __forceinline__ int bucket_of(float l, const RowScale& r) {
   const float z = (r.m - l) * r.z;
-  if (l == -kInf || !(z < 131072.f)) return l == r.m ? 0 : kSampleBuckets - 1;
-  if (z < 32.f) return static_cast<int>(z * 40.f);
-  return min(kSampleBuckets - 1, 1280 + ((__float_as_int(z) - __float_as_int(32.f)) >> 17));
-}
-// Logits of bucket b as a range of rank keys, somewhat wider.  (Whether it holds them all is counted.)
-__device__ __forceinline__ void bucket_keys(int b, const RowScale& r, uint32_t& lo, uint32_t& hi) {
-  auto z_at = [](int c) { return c <= 1280 ? static_cast<float>(c) / 40.f : __int_as_float(__float_as_int(32.f) + ((c - 1280) << 17)); };
-  const float z0 = z_at(b), z1 = z_at(b + 1);
-  const float wide = 1e-5f * fabsf(r.m);
-  lo = rank_key(r.m - z0 * 0.99999f / r.z + wide);
-  hi = b == kSampleBuckets - 1 ? 0xffffffffu : rank_key(r.m - z1 * 1.00001f / r.z - wide);
-  if (!(lo <= hi)) lo = 0, hi = 0xffffffffu;
+  if (!(z < 32.f)) {
+    if (l == r.m) return 0;  // infinite
+    if (!(z < 131072.f)) return kSampleBuckets - 1;
+    return min(kSampleBuckets - 1, 1280 + ((__float_as_int(z) - __float_as_int(32.f)) >> 17));
+  }
+  return static_cast<int>(z * 40.f);
 }
 
-// The tokens that stay: a beginning of the order.
+// The tokens that stay, a beginning of the order: those of smaller buckets, and of `bucket` those of smaller keys and of `key`
+// the indexes up to `index`.  Logits from `sure` on are of smaller buckets, those up to `never` of larger ones: few need more than
+// two comparisons.
 struct Cut {
   int bucket;
-  uint32_t key, index;  // within the bucket: smaller keys, and of this key indexes up to `index`
+  uint32_t key, index;
+  float sure, never;
 };
-__device__ __forceinline__ bool stays(const Cut& c, int b, float l, uint32_t i) {
+__device__ __forceinline__ Cut cut_in(int bucket, const RowScale& r) {
+  Cut c{bucket, 0xffffffffu, 0xffffffffu, kInf, -kInf};
+  auto z_at = [](int b) { return b <= 1280 ? static_cast<float>(b) / 40.f : __int_as_float(__float_as_int(32.f) + ((b - 1280) << 17)); };
+  const float wide = 1e-5f * fabsf(r.m);
+  // buckets are monotone in the logit: a logit of a smaller bucket proves it of all larger ones
+  const float sure = r.m - z_at(bucket) * 0.99999f / r.z + wide, never = r.m - z_at(bucket + 1) * 1.00001f / r.z - wide;
+  if (sure == sure && bucket_of(sure, r) < bucket) c.sure = sure;
+  if (never == never && bucket < kSampleBuckets - 1 && bucket_of(never, r) > bucket) c.never = never;
+  return c;
+}
+__device__ __forceinline__ bool in_bucket(const Cut& c, float l, const RowScale& r) {
+  return l < c.sure && l > c.never && bucket_of(l, r) == c.bucket;
+}
+__device__ __forceinline__ bool stays(const Cut& c, float l, uint32_t i, const RowScale& r) {
+  if (l >= c.sure) return true;
+  if (l <= c.never) return false;
+  const int b = bucket_of(l, r);
   if (b != c.bucket) return b < c.bucket;
   const uint32_t k = rank_key(l);
   return k < c.key || (k == c.key && i <= c.index);
 }
-
 // What both leave.
 __device__ __forceinline__ Cut both_cuts(const Cut& a, const Cut& b) {
   if (a.bucket != b.bucket) return a.bucket < b.bucket ? a : b;
@@ -187,70 +220,127 @@ __device__ __forceinline__ Cut both_cuts(const Cut& a, const Cut& b) {
   return a.index < b.index ? a : b;
 }
 
-// A cluster's view of one row.
-template <int T>
+// A cluster's view of one row.  HELD: each CTA has its piece in shared memory, with what does not take part as -inf.
+template <int T, bool HELD>
 struct SampleRow {
   SampleSmem& s;
-  const void* row;
+  const void* row;       // global
+  const uint4* vecs;     // 16 bytes each; the first holds logits before the row's, too, where the row begins inside it
   uint32_t rank, ctas;
-  int64_t lo, hi;  // this warp's piece
+  int before_row;        // how many
+  int V;
+  int lo, hi;            // this warp's vectors
   int lane, warp;
   RowScale r;
-  int turn = 0, hist_turn = 0;  // buffers that the cluster reads are used in turn: a CTA that passed the next meeting has read the last
+  int turn = 0;
+  bool reading = false;  // others may still be reading this CTA's histogram
 
-  template <class F>
-  __device__ __forceinline__ void each(F f) const {
-#pragma unroll 4
-    for (int64_t i = lo + lane; i < hi; i += 32) f(logit_at<T>(row, i), static_cast<uint32_t>(i));
+  __device__ __forceinline__ int index_of(int v) const { return v * kVec<T> - before_row; }
+
+  // Vector v as the row has it.
+  __device__ __forceinline__ void load_global(int v, float (&l)[kVec<T>]) const {
+    const int i0 = index_of(v);
+    if (i0 >= 0 && i0 + kVec<T> <= V) {
+      unpack<T>(__ldg(vecs + v), l);
+#pragma unroll
+      for (int j = 0; j < kVec<T>; ++j) l[j] = usual(l[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kVec<T>; ++j) {
+        l[j] = -kInf;
+        if (i0 + j >= 0 && i0 + j < V) {
+          if constexpr (T == QGEMV_OUT_F32) {
+            l[j] = static_cast<const float*>(row)[i0 + j];
+          } else {
+            const uint32_t b = static_cast<const uint16_t*>(row)[i0 + j];
+            if constexpr (T == QGEMV_OUT_F16)
+              l[j] = __half2float(__ushort_as_half(static_cast<unsigned short>(b)));
+            else
+              l[j] = __uint_as_float(b << 16);
+          }
+          l[j] = usual(l[j]);
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void load(int v, float (&l)[kVec<T>]) const {
+    if constexpr (HELD)
+      unpack<T>(vecs[v], l);
+    else
+      load_global(v, l);
   }
 
-  __device__ __forceinline__ void add(SampleHist& h, int b, uint64_t w) const {
-    atomicAdd(&h.count[b], 1u);
-    if (w) {
-      const uint32_t wl = static_cast<uint32_t>(w), old = atomicAdd(&h.lo[b], wl);
-      const uint32_t wh = static_cast<uint32_t>(w >> 32) + (old + wl < old);
-      if (wh) atomicAdd(&h.hi[b], wh);
+  // f(logit, index) of this warp's piece, vectors by lanes in turn
+  template <class F>
+  __device__ __forceinline__ void each(F f) const {
+#pragma unroll 2
+    for (int v = lo + lane; v < hi; v += 32) {
+      float l[kVec<T>];
+      load(v, l);
+      const uint32_t i = static_cast<uint32_t>(index_of(v));
+#pragma unroll
+      for (int j = 0; j < kVec<T>; ++j) f(l[j], i + j);
     }
   }
 
-  // The histogram that was filled, over the whole cluster: the first bucket at which the running count (mass) reaches
-  // `target` - `before`, which is left in s.pick_*; mass targets can be a share of the sum.
-  template <bool MASS>
-  __device__ void pick(uint64_t target, uint64_t before, float share, bool first) {
-    const int which = hist_turn;
-    hist_turn ^= 1;
+  __device__ __forceinline__ void meet() {
+    if (ctas > 1)
+      cluster_meet();
+    else
+      __syncthreads();
+  }
+
+  // An empty histogram.
+  __device__ __forceinline__ void begin() {
+    if (reading) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    reading = false;
+    uint4* h = reinterpret_cast<uint4*>(s.count);
+    for (int i = threadIdx.x; i < 3 * kSampleBuckets / 4; i += kSampleThreads) h[i] = make_uint4(0, 0, 0, 0);
     __syncthreads();
-    SampleHist& h = s.hist[which];
-    // sums of the 32 groups: 16 threads each
-    {
+  }
+  __device__ __forceinline__ void settle() {
+    if (reading) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    reading = false;
+  }
+
+  __device__ __forceinline__ void add_mass(int b, uint64_t w) const {
+    if (!w) return;
+    const uint32_t wl = static_cast<uint32_t>(w), old = atomicAdd(&s.lo[b], wl);
+    const uint32_t wh = static_cast<uint32_t>(w >> 32) + (old + wl < old);
+    if (wh) atomicAdd(&s.hi[b], wh);
+  }
+
+  // The first bucket of the histogram, over the whole cluster, at which the running count (mass) reaches `target` - `before`;
+  // s.pick_* say which and what it holds.  SHARE: the target is a share of the mass.
+  template <bool MASS, bool SHARE>
+  __device__ void pick(uint64_t target, uint64_t before, float share) {
+    __syncthreads();
+    {  // sums of the 32 groups: 16 threads each
       const int g = threadIdx.x / 16, at = threadIdx.x % 16;
       uint64_t m = 0;
       uint32_t c = 0;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int b = g * 64 + j * 16 + at;
-        c += h.count[b];
-        m += static_cast<uint64_t>(h.hi[b]) << 32 | h.lo[b];
+        c += s.count[b];
+        if (MASS) m += static_cast<uint64_t>(s.hi[b]) << 32 | s.lo[b];
       }
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) {
-        m += __shfl_xor_sync(0xffffffffu, m, o);
+        if (MASS) m += __shfl_xor_sync(0xffffffffu, m, o);
         c += __shfl_xor_sync(0xffffffffu, c, o);
       }
-      if (at == 0) s.group_mass[which][g] = m, s.group_count[which][g] = c;
+      if (at == 0) s.group_mass[g] = m, s.group_count[g] = c;
     }
-    cluster_meet();
+    meet();
     if (warp == 0) {
-      uint64_t m = 0;
-      uint32_t c = 0;
-      for (uint32_t q = 0; q < ctas; ++q) {
-        m += remote_u64(&s.group_mass[which][lane], q);
-        c += remote_u32(&s.group_count[which][lane], q);
-      }
-      uint64_t v = MASS ? m : c;
+      uint64_t v = 0;
+#pragma unroll
+      for (uint32_t q = 0; q < kSampleMaxCluster; ++q)
+        if (q < ctas) v += MASS ? remote_u64(&s.group_mass[lane], q) : remote_u32(&s.group_count[lane], q);
       uint64_t run = warp_scan64(v, lane);
-      const uint64_t total = __shfl_sync(0xffffffffu, run, 31);
-      if (MASS && first) {
+      if (SHARE) {
+        const uint64_t total = __shfl_sync(0xffffffffu, run, 31);
         target = static_cast<uint64_t>(ceil(static_cast<double>(share) * static_cast<double>(total)));
         if (target == 0) target = 1;
       }
@@ -260,12 +350,15 @@ struct SampleRow {
       // the group's 64 buckets, two a lane
       uint64_t bm[2] = {};
       uint32_t bc[2] = {};
-      for (uint32_t q = 0; q < ctas; ++q)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int b = g * 64 + 2 * lane + j;
-          bc[j] += remote_u32(&h.count[b], q);
-          bm[j] += static_cast<uint64_t>(remote_u32(&h.hi[b], q)) << 32 | remote_u32(&h.lo[b], q);
+      for (uint32_t q = 0; q < kSampleMaxCluster; ++q)
+        if (q < ctas) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int b = g * 64 + 2 * lane + j;
+            bc[j] += remote_u32(&s.count[b], q);
+            if (MASS) bm[j] += static_cast<uint64_t>(remote_u32(&s.hi[b], q)) << 32 | remote_u32(&s.lo[b], q);
+          }
         }
       const uint64_t v0 = MASS ? bm[0] : bc[0], v1 = MASS ? bm[1] : bc[1];
       run = warp_scan64(v0 + v1, lane);
@@ -277,13 +370,14 @@ struct SampleRow {
         s.pick_bucket = g * 64 + 2 * lane + (second ? 1 : 0);
         s.pick_mass = second ? bm[1] : bm[0];
         s.pick_count = second ? bc[1] : bc[0];
+        s.pick_target = target;
       }
-      if (lane == 0) s.pick_total = MASS && first ? target : total;
-    } else {  // the other histogram, which the cluster read before this meeting
-      uint32_t* other = s.hist[which ^ 1].count;
-      for (int i = threadIdx.x - 32; i < static_cast<int>(sizeof(SampleHist) / 4); i += kSampleThreads - 32) other[i] = 0;
     }
     __syncthreads();
+    if (ctas > 1) {
+      asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+      reading = true;
+    }
   }
 
   // The first index at which the running sum of `weigh` exceeds `aim(sum)`; `take` is called by one thread of the cluster with
@@ -293,32 +387,57 @@ struct SampleRow {
     uint64_t mine = 0;
     each([&](float l, uint32_t i) { mine += weigh(l, i); });
     mine = warp_sum64(mine);
+    settle();
+    __syncthreads();
     if (lane == 0) s.warp_sum[warp] = mine;
     __syncthreads();
     uint64_t before = 0, cta = 0;
+#pragma unroll
     for (int q = 0; q < kSampleWarps; ++q) {
       const uint64_t v = s.warp_sum[q];
       if (q < warp) before += v;
       cta += v;
     }
-    if (threadIdx.x == 0) s.cta_sum[turn] = cta;
-    cluster_meet();
-    uint64_t total = 0;
-    for (uint32_t q = 0; q < ctas; ++q) {
-      const uint64_t v = remote_u64(&s.cta_sum[turn], q);
-      if (q < rank) before += v;
-      total += v;
+    uint64_t total = cta;
+    if (ctas > 1) {
+      if (threadIdx.x == 0) s.cta_sum[turn] = cta;
+      cluster_meet();
+      total = 0;
+#pragma unroll
+      for (uint32_t q = 0; q < kSampleMaxCluster; ++q) {
+        const uint64_t v = q < ctas ? remote_u64(&s.cta_sum[turn], q) : 0;
+        if (q < rank) before += v;
+        total += v;
+      }
     }
     turn ^= 1;
     const uint64_t target = aim(total);
     if (target >= before && target < before + mine) {  // the same for all lanes
-      for (int64_t at = lo; at < hi; at += 32) {
-        const int64_t i = at + lane;
-        const uint64_t w = i < hi ? weigh(logit_at<T>(row, i), static_cast<uint32_t>(i)) : 0;
-        const uint64_t run = before + warp_scan64(w, lane);
+      for (int at = lo; at < hi; at += 32) {
+        const int v = at + lane;
+        float l[kVec<T>];
+        uint64_t w[kVec<T>], sum = 0;
+        if (v < hi) load(v, l);
+#pragma unroll
+        for (int j = 0; j < kVec<T>; ++j) {
+          w[j] = v < hi ? weigh(l[j], static_cast<uint32_t>(index_of(v) + j)) : 0;
+          sum += w[j];
+        }
+        const uint64_t run = before + warp_scan64(sum, lane);
         const uint32_t hit = __ballot_sync(0xffffffffu, run > target);
         if (hit) {
-          if (lane == __ffs(hit) - 1) take(static_cast<uint32_t>(i), w, total);
+          if (lane == __ffs(hit) - 1) {
+            uint64_t part = run - sum;
+            bool open = true;
+#pragma unroll
+            for (int j = 0; j < kVec<T>; ++j) {
+              part += w[j];
+              if (open && part > target) {
+                take(static_cast<uint32_t>(index_of(v) + j), w[j], total);
+                open = false;
+              }
+            }
+          }
           break;
         }
         before = __shfl_sync(0xffffffffu, run, 31);
@@ -329,38 +448,35 @@ struct SampleRow {
   // The cut after `target` tokens (MASS: after the shortest beginning with `share` of the mass) of those that `in` keeps.
   template <bool MASS>
   __device__ Cut cut_at(uint64_t target, float share, const Cut& in) {
-    SampleHist* h = &s.hist[hist_turn];
+    begin();
     each([&](float l, uint32_t i) {
-      const int b = bucket_of(l, r);
-      if (stays(in, b, l, i)) add(*h, b, MASS ? weight_of(l, r, s) : 0);
+      if (!stays(in, l, i, r)) return;
+      if (MASS)
+        add_mass(bucket_of(l, r), weight_of(l, r, s));
+      else
+        atomicAdd(&s.count[bucket_of(l, r)], 1u);
     });
-    pick<MASS>(target, 0, share, true);
-    if (MASS) target = s.pick_total;
-    const int bucket = static_cast<int>(s.pick_bucket);
-    const uint32_t held = s.pick_count;
+    pick<MASS, MASS>(target, 0, share);
+    target = s.pick_target;
     uint64_t before = s.pick_before;
-    uint64_t part = MASS ? s.pick_mass : held;
-    Cut c{bucket, 0xffffffffu, 0xffffffffu};
-    if (held == 1 || before + part == target) return c;
-    uint32_t klo, khi;
-    bucket_keys(bucket, r, klo, khi);
-    bool checked = false;
+    uint64_t part = MASS ? s.pick_mass : s.pick_count;
+    Cut c = cut_in(static_cast<int>(s.pick_bucket), r);
+    if (before + part == target) return c;
+    // the bucket's logits lie between these
+    uint32_t klo = c.sure < kInf ? rank_key(c.sure) : 0, khi = c.never > -kInf ? rank_key(c.never) : 0xffffffffu;
     for (;;) {
       const int bits = 32 - __clz(khi - klo);
       const int shift = max(0, bits - 11);
-      h = &s.hist[hist_turn];
+      begin();
       each([&](float l, uint32_t i) {
-        const int b = bucket_of(l, r);
-        if (b != bucket) return;
+        if (!in_bucket(c, l, r)) return;
         const uint32_t k = rank_key(l);
-        if (k >= klo && k <= khi && stays(in, b, l, i)) add(*h, (k - klo) >> shift, MASS ? weight_of(l, r, s) : 0);
+        if (k < klo || k > khi || !stays(in, l, i, r)) return;
+        const int b = static_cast<int>((k - klo) >> shift);
+        atomicAdd(&s.count[b], 1u);
+        if (MASS) add_mass(b, weight_of(l, r, s));
       });
-      pick<MASS>(target, before, 0.f, false);
-      if (!checked && s.pick_total != part) {  // the range was too narrow
-        klo = 0, khi = 0xffffffffu, checked = true;
-        continue;
-      }
-      checked = true;
+      pick<MASS, false>(target, before, 0.f);
       before = s.pick_before;
       part = MASS ? s.pick_mass : s.pick_count;
       klo += s.pick_bucket << shift;
@@ -376,9 +492,10 @@ struct SampleRow {
       n = (n + one - 1) / one;
     }
     const int f = turn;
-    locate([&](float l, uint32_t i) { return static_cast<uint64_t>(rank_key(l) == klo && bucket_of(l, r) == bucket && stays(in, bucket, l, i)); },
-           [&](uint64_t) { return n - 1; }, [&](uint32_t i, uint64_t, uint64_t) { s.found[f] = i; });
-    cluster_meet();
+    const float equal = key_logit(klo);
+    locate([&](float l, uint32_t i) { return static_cast<uint64_t>(l == equal && stays(in, l, i, r)); }, [&](uint64_t) { return n - 1; },
+           [&](uint32_t i, uint64_t, uint64_t) { s.found[f] = i; });
+    meet();
     uint32_t at = 0xffffffffu;
     for (uint32_t q = 0; q < ctas; ++q) at = min(at, remote_u32(&s.found[f], q));
     c.index = at;
@@ -386,40 +503,57 @@ struct SampleRow {
   }
 };
 
-template <int T>
+template <int T, bool HELD>
 __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const __grid_constant__ qgemv_sample_t p) {
   extern __shared__ __align__(16) uint8_t sample_smem[];
   SampleSmem& s = *reinterpret_cast<SampleSmem*>(sample_smem);
+  constexpr int E = kVec<T>;
   const uint32_t ctas = cluster_ctas(), rank = cluster_rank();
   const int64_t m = blockIdx.x / ctas;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_launch_dependents();
-  SampleRow<T> row{s, static_cast<const uint8_t*>(p.logits) + m * p.stride * (T == QGEMV_OUT_F32 ? 4 : 2), rank, ctas};
-  const int64_t warps = static_cast<int64_t>(ctas) * kSampleWarps;
-  const int64_t piece = (p.V + warps * 32 - 1) / (warps * 32) * 32;
-  row.lo = min(static_cast<int64_t>(p.V), (rank * kSampleWarps + warp) * piece);
-  row.hi = min(static_cast<int64_t>(p.V), row.lo + piece);
+  const uint8_t* at_row = static_cast<const uint8_t*>(p.logits) + m * p.stride * (16 / E);
+  const int skip = static_cast<int>((reinterpret_cast<uintptr_t>(at_row) & 15) / (16 / E));
+  const uint4* global = reinterpret_cast<const uint4*>(at_row - skip * (16 / E));
+  uint4* held = reinterpret_cast<uint4*>(sample_smem + sizeof(SampleSmem));
+  const int vectors = (skip + p.V + E - 1) / E;
+  const int c0 = static_cast<int>(static_cast<int64_t>(vectors) * rank / ctas), c1 = static_cast<int>(static_cast<int64_t>(vectors) * (rank + 1) / ctas);
+  const int per = (c1 - c0 + kSampleWarps - 1) / kSampleWarps;
+  SampleRow<T, HELD> row{s, at_row, global, rank, ctas, skip, p.V};
+  row.lo = min(c1, c0 + warp * per);
+  row.hi = min(c1, row.lo + per);
   row.lane = lane;
   row.warp = warp;
   if (threadIdx.x < 2) s.found[threadIdx.x] = 0xffffffffu;
   if (threadIdx.x < 8) s.th[threadIdx.x] = kPowHi[threadIdx.x], s.tl[threadIdx.x] = kPowLo[threadIdx.x], s.ti[threadIdx.x] = kPowInt[threadIdx.x];
-  for (int i = threadIdx.x; i < static_cast<int>(sizeof(SampleHist) / 4); i += kSampleThreads) s.hist[0].count[i] = 0;
   pdl_wait();
-  // the largest logit and its first index
+  // the largest logit and its first index; the piece into shared memory
   float top = -kInf;
-  uint32_t at = 0xffffffffu;
-  row.each([&](float l, uint32_t i) {
-    if (l > top) top = l, at = i;
-  });
-  uint64_t best = at == 0xffffffffu ? 0 : static_cast<uint64_t>(~rank_key(top)) << 32 | (0xffffffffu - at);
+  int at = -1;
+#pragma unroll 4
+  for (int v = row.lo + lane; v < row.hi; v += 32) {
+    float l[E];
+    row.load_global(v, l);
+    if (HELD) held[v - c0] = repack<T>(l);
+#pragma unroll
+    for (int j = 0; j < E; ++j)
+      if (l[j] > top) top = l[j], at = row.index_of(v) + j;
+  }
+  if (HELD) row.vecs = held - c0;
+  uint64_t best = at < 0 ? 0 : static_cast<uint64_t>(~rank_key(top)) << 32 | (0xffffffffu - static_cast<uint32_t>(at));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
   if (lane == 0) s.best_warp[warp] = best;
   __syncthreads();
+#pragma unroll
   for (int q = 0; q < kSampleWarps; ++q) best = max(best, s.best_warp[q]);
-  if (threadIdx.x == 0) s.best = best;
-  cluster_meet();
-  for (uint32_t q = 0; q < ctas; ++q) best = max(best, remote_u64(&s.best, q));
+  if (ctas > 1) {
+    if (threadIdx.x == 0) s.best = best;
+    cluster_meet();
+#pragma unroll
+    for (uint32_t q = 0; q < kSampleMaxCluster; ++q)
+      if (q < ctas) best = max(best, remote_u64(&s.best, q));
+  }
   const float temperature = p.temperature ? p.temperature[m] : 1.f;
   const bool one = best == 0 || !(temperature > 0.f);
   if (one) {
@@ -428,13 +562,12 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const __grid_
       if (p.logprobs) p.logprobs[m] = best ? 0.f : -kInf;
     }
   } else {
-    const uint32_t key = ~static_cast<uint32_t>(best >> 32);  // of the largest logit
-    row.r.m = __uint_as_float(key & 0x80000000u ? key : ~key & 0x7fffffffu);
+    row.r.m = key_logit(~static_cast<uint32_t>(best >> 32));
     const double c = 1.4426950408889634 / fmax(static_cast<double>(temperature), 5.421010862427522e-20);
     row.r.z = static_cast<float>(c);
     row.r.hi = static_cast<float>(8.0 * c);
     row.r.lo = static_cast<float>(8.0 * c - row.r.hi);
-    Cut cut{kSampleBuckets, 0, 0};
+    Cut cut{kSampleBuckets, 0, 0, -kInf, -kInf};
     const int32_t k = p.top_k ? p.top_k[m] : 0;
     if (k > 0 && k < p.V) cut = row.template cut_at<false>(static_cast<uint64_t>(k), 0.f, cut);
     const float top_p = p.top_p ? p.top_p[m] : 1.f;
@@ -442,10 +575,9 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const __grid_
     const float min_p = p.min_p ? p.min_p[m] : 0.f;
     const uint64_t floor_w = min_p > 0.f ? static_cast<uint64_t>(ceil(static_cast<double>(fminf(min_p, 1.f)) * 8796093022208.0)) : 0;
     const float u = p.u[m];
-    __syncthreads();  // s.warp_sum
     row.locate(
         [&](float l, uint32_t i) -> uint64_t {
-          if (!stays(cut, bucket_of(l, row.r), l, i)) return 0;
+          if (!stays(cut, l, i, row.r)) return 0;
           const uint64_t w = weight_of(l, row.r, s);
           return w >= floor_w ? w : 0;
         },
@@ -458,7 +590,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const __grid_
           if (p.logprobs) p.logprobs[m] = logf(static_cast<float>(static_cast<double>(w) / static_cast<double>(total)));
         });
   }
-  cluster_meet();  // no CTA leaves while another reads its shared memory
+  if (ctas > 1) cluster_meet();  // no CTA leaves while another reads its shared memory
 }
 
 }  // namespace qg
