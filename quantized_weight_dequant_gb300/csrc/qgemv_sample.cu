@@ -12,7 +12,7 @@ using namespace qg;
 
 namespace {
 
-constexpr int64_t kSampleHeld = 80 * 1024;  // of a row in a CTA
+constexpr int64_t kSampleHeld = 82 * 1024;  // of a row in a CTA, beside its table: two CTAs are on an SM
 
 template <int T>
 const void* kernel_for(bool held) {
@@ -36,11 +36,12 @@ extern "C" qgemv_status_t qgemv_sample(qgemv_handle_t hh, const qgemv_sample_t* 
   if (p.rows == 0) return QGEMV_OK;
   // as many CTAs a row as hold it in shared memory beside a second CTA on the SM, or with few rows as keep two on every SM with 2048
   // logits at least
+  const int64_t most = kSampleHeld - static_cast<int64_t>(sample_table_bytes(p.type));
   const int64_t row_bytes = (int64_t{p.V} + 16) * (p.type == QGEMV_OUT_F32 ? 4 : 2);
   int ctas = 1;
-  while (ctas < kSampleMaxCluster && (row_bytes > kSampleHeld * ctas || (p.rows * ctas * 2 <= 2 * int64_t{h->sms} && p.V >= ctas * 2 * 2048))) ctas *= 2;
-  const bool held = row_bytes <= kSampleHeld * ctas;
-  const size_t smem = sizeof(SampleSmem) + (held ? static_cast<size_t>((row_bytes / 16 / ctas + 2) * 16) : 0);
+  while (ctas < kSampleMaxCluster && (row_bytes > most * ctas || (p.rows * ctas * 2 <= 2 * int64_t{h->sms} && p.V >= ctas * 2 * 2048))) ctas *= 2;
+  const bool held = row_bytes <= most * ctas;
+  const size_t smem = sizeof(SampleSmem) + sample_table_bytes(p.type) + (held ? static_cast<size_t>((row_bytes / 16 / ctas + 2) * 16) : 0);
   const void* fn = p.type == QGEMV_OUT_F32 ? kernel_for<QGEMV_OUT_F32>(held) : p.type == QGEMV_OUT_F16 ? kernel_for<QGEMV_OUT_F16>(held) : kernel_for<QGEMV_OUT_BF16>(held);
   void* args[] = {const_cast<qgemv_sample_t*>(&p)};
   return launch_dependent(fn, dim3(static_cast<unsigned>(p.rows * ctas)), kSampleThreads, smem, ctas, args, stream) ? QGEMV_OK : QGEMV_ERR_CUDA;

@@ -31,6 +31,7 @@ constexpr int kSampleBuckets = 2048;
 constexpr int kSampleGroups = 32;  // of 64 buckets
 constexpr int kSampleMaxCluster = 8;
 constexpr int kSampleUnit = 43;    // weights in units of 2^-43: 2^20 of them stay below 2^64
+constexpr uint32_t kTableFirst = 119 << 7, kTableValues = 15 << 7;  // bf16: magnitudes of 2^-8 up to 2^7
 constexpr float kInf = __builtin_huge_valf();
 
 struct alignas(16) SampleSmem {
@@ -44,9 +45,11 @@ struct alignas(16) SampleSmem {
   uint64_t best;          // for the cluster
   uint64_t pick_before, pick_mass, pick_target;
   uint32_t pick_bucket, pick_count;
-  float th[8], tl[8];     // 2^(j/8) 2^31 as two floats
-  uint64_t ti[8];         // and times 2^9 as a whole number
+  uint64_t pow40[8];
+  int32_t pow30[8];
 };
+
+__host__ __device__ constexpr size_t sample_table_bytes(int type) { return type == QGEMV_OUT_BF16 ? 2 * kTableValues * 8 : 0; }
 
 // ---------------------------------------------------------------------------- cluster
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -135,42 +138,43 @@ __device__ __forceinline__ uint32_t rank_key(float l) {
 }
 __device__ __forceinline__ float key_logit(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k : ~k & 0x7fffffffu); }
 
-// 2^(j/8) 2^31 as two floats, and 2^(j/8) 2^40 as a whole number.
-__constant__ const float kPowHi[8] = {2147483648.f, 2341847552.f, 2553802752.f, 2784941824.f, 3037000448.f, 3311872512.f, 3611622656.f, 3938502400.f};
-__constant__ const float kPowLo[8] = {0.f, -28.0838032f, 81.5535965f, -86.3073578f, 51.9760513f, 17.3321362f, -53.1616592f, -24.1361656f};
-__constant__ const uint64_t kPowInt[8] = {1099511627776ull, 1199025932245ull, 1307547050779ull, 1425890169699ull, 1554944255988ull, 1695678735018ull, 1849150772653ull, 2016513216442ull};
+// 2^(j/8) in units of 2^-40 and of 2^-30.
+__constant__ const uint64_t kPow40[8] = {1099511627776ull, 1199025932245ull, 1307547050779ull, 1425890169699ull, 1554944255988ull, 1695678735018ull, 1849150772653ull, 2016513216442ull};
+__constant__ const int32_t kPow30[8] = {1073741824, 1170923762, 1276901417, 1392470869, 1518500250, 1655936265, 1805811301, 1969251188};
 
 // What the weights of a row go by: its largest logit, and 8 log2(e) / T in two floats.
 struct RowScale {
   float m, hi, lo, z;  // z: log2(e) / T
 };
 
-// 2^43 w, rounded down.  y = (l - m) 8 log2(e) / T as a sum of two floats; y = k + f with k whole and |f| <= 1/2; 2^(f/8) - 1 by
-// its series in g = f ln(2)/8, |g| < 0.044, whose first term is kept as two floats; 2^(k/8) = 2^(k >> 3) times one
-// of eight constants.  Relative error 2^-32 at most, 2^-40 in the mean (against 80 bits, over 2 10^7 arguments).
-__device__ __forceinline__ uint64_t weight_of(float l, const RowScale& r, const SampleSmem& s) {
-  if (l == r.m) return 1ull << kSampleUnit;
+// 2^43 w, rounded down, for a finite largest logit.  y = (l - m) 8 log2(e) / T as a sum of two floats; y = k + f with k whole and
+// |f| <= 1/2; 2^(f/8) - 1 by its series in g = f ln(2)/8, |g| < 0.044, whose first term is kept as two floats, and in whole
+// numbers of 2^-22 and of 2^-44; times 2^(k/8) = 2^(k >> 3) times one of eight constants.  Relative error 2^-32.6 at
+// most, 2^-35.5 as a root of the mean square, 2^-38 in the mean (against 80 bits, over 3 10^7 arguments).  Conversions between floats
+// and whole numbers are additions of 1.5 2^23 units, since the converting instructions go at a sixteenth of the rate.
+__device__ __forceinline__ uint64_t weight_of(float l, const RowScale& r, const uint64_t* pow40, const int32_t* pow30) {
   const float d = l - r.m;
   const float back = d - l;
   const float off = (l - (d - back)) + (-r.m - back);  // l - m = d + off
-  const float p = d * r.hi;
-  if (!(p > -8.f * (kSampleUnit + 2))) return 0;  // and -inf
+  const float p = fmaxf(d * r.hi, -8.f * (kSampleUnit + 2));  // smaller weights are 0, and that of -inf (NaN: the larger of two is a number)
   const float e = fmaf(d, r.hi, -p) + fmaf(d, r.lo, off * r.hi);
-  const float kf = p + 12582912.f;  // 1.5 2^23: rounds to a whole number
+  const float kf = p + 12582912.f;
   const int k = __float_as_int(kf) - 0x4b400000;
   const float f = p - (kf - 12582912.f);
   constexpr float kL = 0.086643397569656372f, kLlo = -2.3808178e-10f;  // ln(2) / 8
   const float g = f * kL;
   const float rest = fmaf(e, kL, fmaf(f, kLlo, fmaf(f, kL, -g)));
-  const float q = g * g * fmaf(g, fmaf(g, fmaf(g, 1.f / 120.f, 1.f / 24.f), 1.f / 6.f), 0.5f);
+  const float u = g * g * fmaf(g, fmaf(g, fmaf(g, 1.f / 120.f, 1.f / 24.f), 1.f / 6.f), 0.5f);
+  const float q = u + fmaf(rest, g + u, rest);
+  const float x = g + q, left = (g - x) + q;  // 2^(f/8) - 1 = x + left
+  const float a = x + 3.f;                    // units of 2^-22
+  const float b = ((x - (a - 3.f)) + left) + 7.152557373046875e-07f;  // 1.5 2^-21: units of 2^-44
+  const int n1 = __float_as_int(a) - 0x40400000, n2 = __float_as_int(b) - 0x35400000;
   const int j = k & 7;
-  const float t = s.th[j];
-  // t (1 + g) in units of 2^-31 as whole numbers, what they leave in units of 2^-40
-  const float a = t * g;
-  const int whole = __float2int_rn(a);
-  const float b = fmaf(s.tl[j], g, fmaf(t, q + fmaf(rest, g + q, rest), fmaf(t, g, -a))) + (a - static_cast<float>(whole));
-  const uint64_t mant = s.ti[j] + static_cast<uint64_t>(static_cast<int64_t>(whole) * 512 + __float2int_rn(b * 512.f));
-  return (mant << (kSampleUnit - 40)) >> (-(k >> 3));
+  const int64_t c = pow30[j];
+  const uint64_t mant = pow40[j] + static_cast<uint64_t>((c * n1 >> 12) + (c * n2 >> 34));
+  // a clamped p leaves e and what follows without meaning
+  return p > -8.f * (kSampleUnit + 2) ? (mant << (kSampleUnit - 40)) >> (-(k >> 3)) : 0;
 }
 
 // Histogram 0: 40 buckets for each halving of the weight, behind 2^-32 64 for each doubling of the distance.
@@ -232,8 +236,28 @@ struct SampleRow {
   int lo, hi;            // this warp's vectors
   int lane, warp;
   RowScale r;
+  const uint64_t* table;  // bf16: weights of the values of 15 octaves, positive ones first
+  bool infinite;         // the largest logit is
   int turn = 0;
   bool reading = false;  // others may still be reading this CTA's histogram
+
+  __device__ __forceinline__ uint64_t weight(float l) const {
+    if constexpr (T == QGEMV_OUT_BF16) {
+      const uint32_t b = __float_as_uint(l) >> 16, i = (b & 0x7fff) - kTableFirst;
+      if (i < kTableValues) return table[i + (b >> 15) * kTableValues];
+    }
+    if (infinite) return l == r.m ? 1ull << kSampleUnit : 0;
+    return weight_of(l, r, s.pow40, s.pow30);
+  }
+  // bf16 has few values: their weights are computed once (a weight is 50 instructions, a row has thousands of equal logits).
+  __device__ __forceinline__ void fill(uint64_t* to) {
+    for (int i = threadIdx.x; i < 2 * static_cast<int>(kTableValues); i += kSampleThreads) {
+      const uint32_t v = i < static_cast<int>(kTableValues) ? kTableFirst + i : 0x8000u + kTableFirst + i - kTableValues;
+      const float l = __uint_as_float(v << 16);
+      to[i] = infinite || l > r.m ? 0 : weight_of(l, r, s.pow40, s.pow30);
+    }
+    __syncthreads();
+  }
 
   __device__ __forceinline__ int index_of(int v) const { return v * kVec<T> - before_row; }
 
@@ -452,7 +476,7 @@ struct SampleRow {
     each([&](float l, uint32_t i) {
       if (!stays(in, l, i, r)) return;
       if (MASS)
-        add_mass(bucket_of(l, r), weight_of(l, r, s));
+        add_mass(bucket_of(l, r), weight(l));
       else
         atomicAdd(&s.count[bucket_of(l, r)], 1u);
     });
@@ -474,7 +498,7 @@ struct SampleRow {
         if (k < klo || k > khi || !stays(in, l, i, r)) return;
         const int b = static_cast<int>((k - klo) >> shift);
         atomicAdd(&s.count[b], 1u);
-        if (MASS) add_mass(b, weight_of(l, r, s));
+        if (MASS) add_mass(b, weight(l));
       });
       pick<MASS, false>(target, before, 0.f);
       before = s.pick_before;
@@ -515,17 +539,18 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const __grid_
   const uint8_t* at_row = static_cast<const uint8_t*>(p.logits) + m * p.stride * (16 / E);
   const int skip = static_cast<int>((reinterpret_cast<uintptr_t>(at_row) & 15) / (16 / E));
   const uint4* global = reinterpret_cast<const uint4*>(at_row - skip * (16 / E));
-  uint4* held = reinterpret_cast<uint4*>(sample_smem + sizeof(SampleSmem));
+  uint4* held = reinterpret_cast<uint4*>(sample_smem + sizeof(SampleSmem) + sample_table_bytes(T));
   const int vectors = (skip + p.V + E - 1) / E;
   const int c0 = static_cast<int>(static_cast<int64_t>(vectors) * rank / ctas), c1 = static_cast<int>(static_cast<int64_t>(vectors) * (rank + 1) / ctas);
   const int per = (c1 - c0 + kSampleWarps - 1) / kSampleWarps;
   SampleRow<T, HELD> row{s, at_row, global, rank, ctas, skip, p.V};
+  uint64_t* table = reinterpret_cast<uint64_t*>(sample_smem + sizeof(SampleSmem));
   row.lo = min(c1, c0 + warp * per);
   row.hi = min(c1, row.lo + per);
   row.lane = lane;
   row.warp = warp;
   if (threadIdx.x < 2) s.found[threadIdx.x] = 0xffffffffu;
-  if (threadIdx.x < 8) s.th[threadIdx.x] = kPowHi[threadIdx.x], s.tl[threadIdx.x] = kPowLo[threadIdx.x], s.ti[threadIdx.x] = kPowInt[threadIdx.x];
+  if (threadIdx.x < 8) s.pow40[threadIdx.x] = kPow40[threadIdx.x], s.pow30[threadIdx.x] = kPow30[threadIdx.x];
   pdl_wait();
   // the largest logit and its first index; the piece into shared memory
   float top = -kInf;
@@ -567,6 +592,9 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const __grid_
     row.r.z = static_cast<float>(c);
     row.r.hi = static_cast<float>(8.0 * c);
     row.r.lo = static_cast<float>(8.0 * c - row.r.hi);
+    row.infinite = row.r.m == kInf;
+    row.table = table;
+    if (T == QGEMV_OUT_BF16) row.fill(table);
     Cut cut{kSampleBuckets, 0, 0, -kInf, -kInf};
     const int32_t k = p.top_k ? p.top_k[m] : 0;
     if (k > 0 && k < p.V) cut = row.template cut_at<false>(static_cast<uint64_t>(k), 0.f, cut);
@@ -578,7 +606,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const __grid_
     row.locate(
         [&](float l, uint32_t i) -> uint64_t {
           if (!stays(cut, l, i, row.r)) return 0;
-          const uint64_t w = weight_of(l, row.r, s);
+          const uint64_t w = row.weight(l);
           return w >= floor_w ? w : 0;
         },
         [&](uint64_t total) {
