@@ -12,7 +12,7 @@ using namespace qg;
 
 namespace {
 
-constexpr int64_t kSampleHeld = 82 * 1024;  // of a row in a CTA, beside its table: two CTAs are on an SM
+constexpr int64_t kSampleHeld = 52 * 1024;  // of a row in a CTA, beside its table: two CTAs are on an SM
 
 template <int T>
 const void* kernel_for(bool held) {
@@ -34,12 +34,12 @@ extern "C" qgemv_status_t qgemv_sample(qgemv_handle_t hh, const qgemv_sample_t* 
                                 reinterpret_cast<uintptr_t>(p.tokens) | reinterpret_cast<uintptr_t>(p.logprobs)) & 3))
     return QGEMV_ERR_MISALIGNED;
   if (p.rows == 0) return QGEMV_OK;
-  // as many CTAs a row as hold it in shared memory beside a second CTA on the SM, or with few rows as keep two on every SM with 2048
-  // logits at least
+  // as many CTAs a row as keep two on every SM, of 2048 logits at least; they hold it in shared memory where that is enough for it
+  // beside a second CTA on the SM
   const int64_t most = kSampleHeld - static_cast<int64_t>(sample_table_bytes(p.type));
   const int64_t row_bytes = (int64_t{p.V} + 16) * (p.type == QGEMV_OUT_F32 ? 4 : 2);
   int ctas = 1;
-  while (ctas < kSampleMaxCluster && (row_bytes > most * ctas || (p.rows * ctas * 2 <= 2 * int64_t{h->sms} && p.V >= ctas * 2 * 2048))) ctas *= 2;
+  while (ctas < kSampleMaxCluster && p.rows * ctas * 2 <= 2 * int64_t{h->sms} && p.V >= ctas * 2 * 2048) ctas *= 2;
   const bool held = row_bytes <= most * ctas;
   const size_t smem = sizeof(SampleSmem) + sample_table_bytes(p.type) + (held ? static_cast<size_t>((row_bytes / 16 / ctas + 2) * 16) : 0);
   const void* fn = p.type == QGEMV_OUT_F32 ? kernel_for<QGEMV_OUT_F32>(held) : p.type == QGEMV_OUT_F16 ? kernel_for<QGEMV_OUT_F16>(held) : kernel_for<QGEMV_OUT_BF16>(held);

@@ -30,6 +30,7 @@ constexpr int kSampleWarps = kSampleThreads / 32;
 constexpr int kSampleBuckets = 2048;
 constexpr int kSampleGroups = 32;  // of 64 buckets
 constexpr int kSampleMaxCluster = 8;
+constexpr int kSampleList = 4096;  // candidates that one CTA finishes alone
 constexpr int kSampleUnit = 43;    // weights in units of 2^-43: 2^20 of them stay below 2^64
 constexpr uint32_t kTableFirst = 119 << 7, kTableValues = 15 << 7;  // bf16: magnitudes of 2^-8 up to 2^7
 constexpr float kInf = __builtin_huge_valf();
@@ -41,12 +42,18 @@ struct alignas(16) SampleSmem {
   uint64_t warp_sum[kSampleWarps];
   uint64_t cta_sum[2];    // for the cluster
   uint32_t found[2];      // for the cluster
+  uint32_t listed;        // candidates, of the whole cluster in its first CTA
+  uint32_t mine, base;    // this CTA's, and where they go
   uint64_t best_warp[kSampleWarps];
   uint64_t best;          // for the cluster
-  uint64_t pick_before, pick_mass, pick_target;
+  uint4 edge[2];          // the row's first and last 16 bytes, with -inf in the places of what is not the row's
+  float scale[2];         // of the row: hi, lo
+  uint64_t pick_before, pick_mass, pick_target, pick_total;
   uint32_t pick_bucket, pick_count;
   uint64_t pow40[8];
   int32_t pow30[8];
+  float list_logit[kSampleList];
+  uint32_t list_index[kSampleList];
 };
 
 __host__ __device__ constexpr size_t sample_table_bytes(int type) { return type == QGEMV_OUT_BF16 ? 2 * kTableValues * 8 : 0; }
@@ -78,6 +85,17 @@ __device__ __forceinline__ uint64_t remote_u64(const void* p, uint32_t rank) {
   asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
   return v;
 }
+__device__ __forceinline__ void store_remote(const void* p, uint32_t rank, uint32_t v) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t add_remote(const void* p, uint32_t rank, uint32_t v) {
+  uint32_t a, old;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(old) : "r"(a), "r"(v) : "memory");
+  return old;
+}
 __device__ __forceinline__ uint64_t warp_sum64(uint64_t v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -92,12 +110,31 @@ __device__ __forceinline__ uint64_t warp_scan64(uint64_t v, int lane) {  // incl
   return v;
 }
 
+// floor(u total), and whether that is all of it, for u in (0, 1): 24 bits times 64, shifted.  (Every thread needs it: in 64-bit
+// floats, of which an SM does two a cycle, it takes the CTA 3400 cycles.)
+__device__ __forceinline__ uint64_t share_of(float u, uint64_t total, bool& whole) {
+  const uint32_t b = __float_as_uint(u), e = b >> 23;
+  const uint64_t mant = (b & 0x7fffff) | (e ? 0x800000 : 0);
+  const int shift = 150 - static_cast<int>(max(e, 1u));  // u = mant 2^-shift, shift >= 24
+  const uint64_t hi = __umul64hi(total, mant), lo = total * mant;
+  if (shift >= 64) {
+    if (shift >= 128) {
+      whole = false;
+      return 0;
+    }
+    whole = lo == 0 && (shift == 64 || hi << (128 - shift) == 0);
+    return shift == 64 ? hi : hi >> (shift - 64);
+  }
+  whole = lo << (64 - shift) == 0;
+  return hi << (64 - shift) | lo >> shift;
+}
+
 // ---------------------------------------------------------------------------- logits
 template <int T>
 constexpr int kVec = T == QGEMV_OUT_F32 ? 4 : 8;  // logits in 16 bytes
 
-// What takes part: NaN as -inf, -0 as 0 (so that equal logits have equal bits).
-__device__ __forceinline__ float usual(float l) { return l == l ? l + 0.f : -kInf; }
+// -0 as 0, so that equal logits have equal bits.  (NaN stays: it is above nothing, in the last bucket and of weight 0, like -inf.)
+__device__ __forceinline__ float usual(float l) { return l + 0.f; }
 
 template <int T>
 __device__ __forceinline__ void unpack(const uint4& v, float (&l)[kVec<T>]) {
@@ -144,7 +181,7 @@ __constant__ const int32_t kPow30[8] = {1073741824, 1170923762, 1276901417, 1392
 
 // What the weights of a row go by: its largest logit, and 8 log2(e) / T in two floats.
 struct RowScale {
-  float m, hi, lo, z;  // z: log2(e) / T
+  float m, hi, lo;
 };
 
 // 2^43 w, rounded down, for a finite largest logit.  y = (l - m) 8 log2(e) / T as a sum of two floats; y = k + f with k whole and
@@ -156,8 +193,9 @@ __device__ __forceinline__ uint64_t weight_of(float l, const RowScale& r, const 
   const float d = l - r.m;
   const float back = d - l;
   const float off = (l - (d - back)) + (-r.m - back);  // l - m = d + off
-  const float p = fmaxf(d * r.hi, -8.f * (kSampleUnit + 2));  // smaller weights are 0, and that of -inf (NaN: the larger of two is a number)
-  const float e = fmaf(d, r.hi, -p) + fmaf(d, r.lo, off * r.hi);
+  constexpr float kNone = -8.f * (kSampleUnit + 2);  // from here on the weight is 0 (also for -inf and NaN: the larger of two is a number)
+  const float p = fmaxf(d * r.hi, kNone);
+  const float e = p > kNone ? fmaf(d, r.hi, -p) + fmaf(d, r.lo, off * r.hi) : 0.f;
   const float kf = p + 12582912.f;
   const int k = __float_as_int(kf) - 0x4b400000;
   const float f = p - (kf - 12582912.f);
@@ -173,19 +211,19 @@ __device__ __forceinline__ uint64_t weight_of(float l, const RowScale& r, const 
   const int j = k & 7;
   const int64_t c = pow30[j];
   const uint64_t mant = pow40[j] + static_cast<uint64_t>((c * n1 >> 12) + (c * n2 >> 34));
-  // a clamped p leaves e and what follows without meaning
-  return p > -8.f * (kSampleUnit + 2) ? (mant << (kSampleUnit - 40)) >> (-(k >> 3)) : 0;
+  return (mant << (kSampleUnit - 40)) >> (-(k >> 3));
 }
 
 // Histogram 0: 40 buckets for each halving of the weight, behind 2^-32 64 for each doubling of the distance.
 __device__ __forceinline__ int bucket_of(float l, const RowScale& r) {
-  const float z = (r.m - l) * r.z;
-  if (!(z < 32.f)) {
+  const float y = (l - r.m) * r.hi;  // eighths of halvings
+  if (!(y > -256.f)) {
     if (l == r.m) return 0;  // infinite
+    const float z = y * -0.125f;
     if (!(z < 131072.f)) return kSampleBuckets - 1;
     return min(kSampleBuckets - 1, 1280 + ((__float_as_int(z) - __float_as_int(32.f)) >> 17));
   }
-  return static_cast<int>(z * 40.f);
+  return __float_as_int(fmaf(y, -5.f, 12582912.f)) - 0x4b400000;  // to the nearest
 }
 
 // The tokens that stay, a beginning of the order: those of smaller buckets, and of `bucket` those of smaller keys and of `key`
@@ -198,10 +236,10 @@ struct Cut {
 };
 __device__ __forceinline__ Cut cut_in(int bucket, const RowScale& r) {
   Cut c{bucket, 0xffffffffu, 0xffffffffu, kInf, -kInf};
-  auto z_at = [](int b) { return b <= 1280 ? static_cast<float>(b) / 40.f : __int_as_float(__float_as_int(32.f) + ((b - 1280) << 17)); };
+  auto z_at = [](int b) { return b <= 1280 ? (static_cast<float>(b) - 0.5f) / 40.f : __int_as_float(__float_as_int(32.f) + ((b - 1280) << 17)); };
   const float wide = 1e-5f * fabsf(r.m);
   // buckets are monotone in the logit: a logit of a smaller bucket proves it of all larger ones
-  const float sure = r.m - z_at(bucket) * 0.99999f / r.z + wide, never = r.m - z_at(bucket + 1) * 1.00001f / r.z - wide;
+  const float sure = r.m - z_at(bucket) * (8.f * 0.99999f) / r.hi + wide, never = r.m - z_at(bucket + 1) * (8.f * 1.00001f) / r.hi - wide;
   if (sure == sure && bucket_of(sure, r) < bucket) c.sure = sure;
   if (never == never && bucket < kSampleBuckets - 1 && bucket_of(never, r) > bucket) c.never = never;
   return c;
@@ -233,18 +271,20 @@ struct SampleRow {
   uint32_t rank, ctas;
   int before_row;        // how many
   int V;
+  int last;              // vector of the row
   int lo, hi;            // this warp's vectors
   int lane, warp;
   RowScale r;
   const uint64_t* table;  // bf16: weights of the values of 15 octaves, positive ones first
   bool infinite;         // the largest logit is
+  bool alone = false;    // the candidates are listed in this CTA, and the others have nothing to do
   int turn = 0;
   bool reading = false;  // others may still be reading this CTA's histogram
 
   __device__ __forceinline__ uint64_t weight(float l) const {
     if constexpr (T == QGEMV_OUT_BF16) {
       const uint32_t b = __float_as_uint(l) >> 16, i = (b & 0x7fff) - kTableFirst;
-      if (i < kTableValues) return table[i + (b >> 15) * kTableValues];
+      if (table && i < kTableValues) return table[i + (b >> 15) * kTableValues];
     }
     if (infinite) return l == r.m ? 1ull << kSampleUnit : 0;
     return weight_of(l, r, s.pow40, s.pow30);
@@ -287,23 +327,39 @@ struct SampleRow {
       }
     }
   }
-  __device__ __forceinline__ void load(int v, float (&l)[kVec<T>]) const {
-    if constexpr (HELD)
-      unpack<T>(vecs[v], l);
-    else
-      load_global(v, l);
+  __device__ __forceinline__ uint4 load(int v) const {
+    if constexpr (HELD) return vecs[v];
+    const uint4* at = vecs + v;
+    if (v == last) at = &s.edge[1];
+    if (v == 0) at = &s.edge[0];
+    return *at;
   }
 
-  // f(logit, index) of this warp's piece, vectors by lanes in turn
+  // f(logit, index) of this warp's piece, vectors by lanes in turn; of the candidates once they are listed
   template <class F>
   __device__ __forceinline__ void each(F f) const {
-#pragma unroll 2
-    for (int v = lo + lane; v < hi; v += 32) {
-      float l[kVec<T>];
-      load(v, l);
-      const uint32_t i = static_cast<uint32_t>(index_of(v));
+    if (alone) {
+      for (uint32_t i = threadIdx.x; i < s.listed; i += kSampleThreads) f(s.list_logit[i], s.list_index[i]);
+      return;
+    }
+    constexpr int U = HELD ? 2 : 4;  // reads that are in flight together
+    for (int v0 = lo + lane; v0 < hi; v0 += 32 * U) {
+      uint4 raw[U];
 #pragma unroll
-      for (int j = 0; j < kVec<T>; ++j) f(l[j], i + j);
+      for (int u = 0; u < U; ++u)
+        if (v0 + 32 * u < hi) raw[u] = load(v0 + 32 * u);
+#pragma unroll 1
+      for (int u = 0; u < U; ++u) {
+        const int v = v0 + 32 * u;
+        if (v >= hi) break;
+        float l[kVec<T>];
+        unpack<T>(raw[0], l);
+#pragma unroll
+        for (int w = 0; w + 1 < U; ++w) raw[w] = raw[w + 1];
+        const uint32_t i = static_cast<uint32_t>(index_of(v));
+#pragma unroll
+        for (int j = 0; j < kVec<T>; ++j) f(HELD ? l[j] : usual(l[j]), i + j);
+      }
     }
   }
 
@@ -334,10 +390,10 @@ struct SampleRow {
     if (wh) atomicAdd(&s.hi[b], wh);
   }
 
-  // The first bucket of the histogram, over the whole cluster, at which the running count (mass) reaches `target` - `before`;
-  // s.pick_* say which and what it holds.  SHARE: the target is a share of the mass.
-  template <bool MASS, bool SHARE>
-  __device__ void pick(uint64_t target, uint64_t before, float share) {
+  // The first bucket of the histogram, over the whole cluster, at which the running count (mass) reaches aim(sum) - `before`;
+  // s.pick_* say which and what it holds.
+  template <bool MASS, class A>
+  __device__ void pick(A aim, uint64_t before) {
     __syncthreads();
     {  // sums of the 32 groups: 16 threads each
       const int g = threadIdx.x / 16, at = threadIdx.x % 16;
@@ -346,55 +402,75 @@ struct SampleRow {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int b = g * 64 + j * 16 + at;
-        c += s.count[b];
-        if (MASS) m += static_cast<uint64_t>(s.hi[b]) << 32 | s.lo[b];
+        if (MASS)
+          m += static_cast<uint64_t>(s.hi[b]) << 32 | s.lo[b];
+        else
+          c += s.count[b];
       }
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) {
-        if (MASS) m += __shfl_xor_sync(0xffffffffu, m, o);
-        c += __shfl_xor_sync(0xffffffffu, c, o);
+        if (MASS)
+          m += __shfl_xor_sync(0xffffffffu, m, o);
+        else
+          c += __shfl_xor_sync(0xffffffffu, c, o);
       }
-      if (at == 0) s.group_mass[g] = m, s.group_count[g] = c;
+      if (at == 0) s.group_mass[g] = MASS ? m : c;
     }
     meet();
     if (warp == 0) {
-      uint64_t v = 0;
+      const uint32_t last = ctas - 1;
+      uint64_t v = s.group_mass[lane];
+      if (ctas > 1) {
+        uint64_t part[kSampleMaxCluster];
 #pragma unroll
-      for (uint32_t q = 0; q < kSampleMaxCluster; ++q)
-        if (q < ctas) v += MASS ? remote_u64(&s.group_mass[lane], q) : remote_u32(&s.group_count[lane], q);
-      uint64_t run = warp_scan64(v, lane);
-      if (SHARE) {
-        const uint64_t total = __shfl_sync(0xffffffffu, run, 31);
-        target = static_cast<uint64_t>(ceil(static_cast<double>(share) * static_cast<double>(total)));
-        if (target == 0) target = 1;
+        for (uint32_t q = 0; q < kSampleMaxCluster; ++q) part[q] = remote_u64(&s.group_mass[lane], min(q, last));
+        v = 0;
+#pragma unroll
+        for (uint32_t q = 0; q < kSampleMaxCluster; ++q) v += q < ctas ? part[q] : 0;
       }
+      uint64_t run = warp_scan64(v, lane);
+      const uint64_t total = __shfl_sync(0xffffffffu, run, 31), target = aim(total);
       uint32_t hit = __ballot_sync(0xffffffffu, before + run >= target);
       const int g = hit ? __ffs(hit) - 1 : 31;
       before += __shfl_sync(0xffffffffu, run - v, g);
       // the group's 64 buckets, two a lane
-      uint64_t bm[2] = {};
-      uint32_t bc[2] = {};
+      const int b0 = g * 64 + 2 * lane;
+      uint64_t bm[2] = {}, bc = 0;  // bc: counts in halves
+      if (ctas > 1) {
+        uint64_t c[kSampleMaxCluster], lo[kSampleMaxCluster], hi[kSampleMaxCluster];
 #pragma unroll
-      for (uint32_t q = 0; q < kSampleMaxCluster; ++q)
-        if (q < ctas) {
+        for (uint32_t q = 0; q < kSampleMaxCluster; ++q) {
+          c[q] = remote_u64(&s.count[b0], min(q, last));
+          if (MASS) lo[q] = remote_u64(&s.lo[b0], min(q, last)), hi[q] = remote_u64(&s.hi[b0], min(q, last));
+        }
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int b = g * 64 + 2 * lane + j;
-            bc[j] += remote_u32(&s.count[b], q);
-            if (MASS) bm[j] += static_cast<uint64_t>(remote_u32(&s.hi[b], q)) << 32 | remote_u32(&s.lo[b], q);
+        for (uint32_t q = 0; q < kSampleMaxCluster; ++q) {
+          if (q >= ctas) continue;
+          bc += c[q];
+          if (MASS) {
+            bm[0] += hi[q] << 32 | (lo[q] & 0xffffffffu);
+            bm[1] += (hi[q] & 0xffffffff00000000ull) | lo[q] >> 32;
           }
         }
-      const uint64_t v0 = MASS ? bm[0] : bc[0], v1 = MASS ? bm[1] : bc[1];
+      } else {
+        bc = static_cast<uint64_t>(s.count[b0 + 1]) << 32 | s.count[b0];
+        if (MASS) {
+          bm[0] = static_cast<uint64_t>(s.hi[b0]) << 32 | s.lo[b0];
+          bm[1] = static_cast<uint64_t>(s.hi[b0 + 1]) << 32 | s.lo[b0 + 1];
+        }
+      }
+      const uint64_t v0 = MASS ? bm[0] : bc & 0xffffffffu, v1 = MASS ? bm[1] : bc >> 32;
       run = warp_scan64(v0 + v1, lane);
       hit = __ballot_sync(0xffffffffu, before + run >= target);
       const int at = hit ? __ffs(hit) - 1 : 31;
       const bool second = before + run - v1 < target;
       if (lane == at) {
         s.pick_before = before + run - v1 - (second ? 0 : v0);
-        s.pick_bucket = g * 64 + 2 * lane + (second ? 1 : 0);
-        s.pick_mass = second ? bm[1] : bm[0];
-        s.pick_count = second ? bc[1] : bc[0];
+        s.pick_bucket = b0 + (second ? 1 : 0);
+        s.pick_mass = second ? v1 : v0;
+        s.pick_count = static_cast<uint32_t>(second ? bc >> 32 : bc);
         s.pick_target = target;
+        s.pick_total = total;
       }
     }
     __syncthreads();
@@ -404,10 +480,59 @@ struct SampleRow {
     }
   }
 
+  // The candidates, those of `c`'s bucket and smaller ones that `in` keeps, go into the list of the cluster's first CTA, in no
+  // order (what follows goes by logits and indexes); where they fit, it goes on alone.
+  __device__ void list(const Cut& c, const Cut& in) {
+    settle();
+    uint32_t* count = rank == 0 ? &s.listed : &s.mine;
+    each([&](float l, uint32_t i) {
+      if (l <= c.never || i >= static_cast<uint32_t>(V) || (l < c.sure && bucket_of(l, r) > c.bucket) || !stays(in, l, i, r)) return;
+      const uint32_t at = atomicAdd(count, 1u);
+      if (at < kSampleList) s.list_logit[at] = l, s.list_index[at] = i;
+    });
+    __syncthreads();
+    uint32_t all = s.listed;
+    if (ctas > 1) {
+      const uint32_t n = s.mine;
+      if (rank != 0 && n) {
+        if (threadIdx.x == 0) s.base = add_remote(&s.listed, 0, n);
+        __syncthreads();
+        const uint32_t base = s.base;
+        for (uint32_t i = threadIdx.x; i < n && base + i < kSampleList; i += kSampleThreads) {
+          store_remote(&s.list_logit[base + i], 0, __float_as_uint(s.list_logit[i]));
+          store_remote(&s.list_index[base + i], 0, s.list_index[i]);
+        }
+      }
+      cluster_meet();
+      all = remote_u32(&s.listed, 0);
+    }
+    if (all > kSampleList) return;
+    alone = true;
+    ctas = 1;
+  }
+
   // The first index at which the running sum of `weigh` exceeds `aim(sum)`; `take` is called by one thread of the cluster with
   // the index, its weight and the sum.
   template <class W, class A, class K>
   __device__ void locate(W weigh, A aim, K take) {
+    if (alone) {  // the running sum over ranges of indexes
+      uint32_t first = 0;
+      uint64_t target = 0, before = 0, total = 0;
+      for (int shift = max(0, 32 - __clz(V - 1) - 11), width = 32;; width = shift, shift = max(0, shift - 11)) {
+        begin();
+        each([&](float l, uint32_t i) {
+          if (i >= first && (width == 32 || (i - first) >> width == 0)) add_mass(static_cast<int>((i - first) >> shift), weigh(l, i));
+        });
+        pick<true>([&](uint64_t sum) { return width == 32 ? aim(sum) + 1 : target; }, before);
+        if (width == 32) total = s.pick_total;
+        target = s.pick_target;
+        before = s.pick_before;
+        first += s.pick_bucket << shift;
+        if (shift == 0) break;
+      }
+      if (threadIdx.x == 0) take(first, s.pick_mass, total);
+      return;
+    }
     uint64_t mine = 0;
     each([&](float l, uint32_t i) { mine += weigh(l, i); });
     mine = warp_sum64(mine);
@@ -434,17 +559,16 @@ struct SampleRow {
         total += v;
       }
     }
-    turn ^= 1;
     const uint64_t target = aim(total);
     if (target >= before && target < before + mine) {  // the same for all lanes
       for (int at = lo; at < hi; at += 32) {
         const int v = at + lane;
         float l[kVec<T>];
         uint64_t w[kVec<T>], sum = 0;
-        if (v < hi) load(v, l);
+        if (v < hi) unpack<T>(load(v), l);
 #pragma unroll
         for (int j = 0; j < kVec<T>; ++j) {
-          w[j] = v < hi ? weigh(l[j], static_cast<uint32_t>(index_of(v) + j)) : 0;
+          w[j] = v < hi ? weigh(usual(l[j]), static_cast<uint32_t>(index_of(v) + j)) : 0;
           sum += w[j];
         }
         const uint64_t run = before + warp_scan64(sum, lane);
@@ -469,9 +593,10 @@ struct SampleRow {
     }
   }
 
-  // The cut after `target` tokens (MASS: after the shortest beginning with `share` of the mass) of those that `in` keeps.
-  template <bool MASS>
-  __device__ Cut cut_at(uint64_t target, float share, const Cut& in) {
+  // The cut after `aim(sum)` tokens (MASS: after the shortest beginning that has that mass) of those that `in` keeps.  In CTAs that
+  // have nothing more to do then (alone, and not the first) it means nothing.
+  template <bool MASS, class A>
+  __device__ Cut cut_at(A aim, const Cut& in) {
     begin();
     each([&](float l, uint32_t i) {
       if (!stays(in, l, i, r)) return;
@@ -480,12 +605,13 @@ struct SampleRow {
       else
         atomicAdd(&s.count[bucket_of(l, r)], 1u);
     });
-    pick<MASS, MASS>(target, 0, share);
-    target = s.pick_target;
+    pick<MASS>(aim, 0);
+    const uint64_t target = s.pick_target;
     uint64_t before = s.pick_before;
     uint64_t part = MASS ? s.pick_mass : s.pick_count;
     Cut c = cut_in(static_cast<int>(s.pick_bucket), r);
-    if (before + part == target) return c;
+    if (!alone && (MASS || before + part <= kSampleList)) list(c, in);
+    if ((alone && rank != 0) || before + part == target) return c;
     // the bucket's logits lie between these
     uint32_t klo = c.sure < kInf ? rank_key(c.sure) : 0, khi = c.never > -kInf ? rank_key(c.never) : 0xffffffffu;
     for (;;) {
@@ -500,7 +626,7 @@ struct SampleRow {
         atomicAdd(&s.count[b], 1u);
         if (MASS) add_mass(b, weight(l));
       });
-      pick<MASS, false>(target, before, 0.f);
+      pick<MASS>([&](uint64_t) { return target; }, before);
       before = s.pick_before;
       part = MASS ? s.pick_mass : s.pick_count;
       klo += s.pick_bucket << shift;
@@ -519,9 +645,10 @@ struct SampleRow {
     const float equal = key_logit(klo);
     locate([&](float l, uint32_t i) { return static_cast<uint64_t>(l == equal && stays(in, l, i, r)); }, [&](uint64_t) { return n - 1; },
            [&](uint32_t i, uint64_t, uint64_t) { s.found[f] = i; });
+    turn ^= 1;
     meet();
     uint32_t at = 0xffffffffu;
-    for (uint32_t q = 0; q < ctas; ++q) at = min(at, remote_u32(&s.found[f], q));
+    for (uint32_t q = 0; q < ctas; ++q) at = min(at, ctas > 1 ? remote_u32(&s.found[f], q) : s.found[f]);
     c.index = at;
     return c;
   }
@@ -543,15 +670,19 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const __grid_
   const int vectors = (skip + p.V + E - 1) / E;
   const int c0 = static_cast<int>(static_cast<int64_t>(vectors) * rank / ctas), c1 = static_cast<int>(static_cast<int64_t>(vectors) * (rank + 1) / ctas);
   const int per = (c1 - c0 + kSampleWarps - 1) / kSampleWarps;
-  SampleRow<T, HELD> row{s, at_row, global, rank, ctas, skip, p.V};
+  SampleRow<T, HELD> row{s, at_row, global, rank, ctas, skip, p.V, vectors - 1};
   uint64_t* table = reinterpret_cast<uint64_t*>(sample_smem + sizeof(SampleSmem));
   row.lo = min(c1, c0 + warp * per);
   row.hi = min(c1, row.lo + per);
   row.lane = lane;
   row.warp = warp;
   if (threadIdx.x < 2) s.found[threadIdx.x] = 0xffffffffu;
+  if (threadIdx.x == 2) s.listed = 0, s.mine = 0;
   if (threadIdx.x < 8) s.pow40[threadIdx.x] = kPow40[threadIdx.x], s.pow30[threadIdx.x] = kPow30[threadIdx.x];
   pdl_wait();
+  const float temperature = p.temperature ? __ldg(p.temperature + m) : 1.f, top_p = p.top_p ? __ldg(p.top_p + m) : 1.f;
+  const float min_p = p.min_p ? __ldg(p.min_p + m) : 0.f, u = __ldg(p.u + m);
+  const int32_t k = p.top_k ? __ldg(p.top_k + m) : 0;
   // the largest logit and its first index; the piece into shared memory
   float top = -kInf;
   int at = -1;
@@ -559,7 +690,10 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const __grid_
   for (int v = row.lo + lane; v < row.hi; v += 32) {
     float l[E];
     row.load_global(v, l);
-    if (HELD) held[v - c0] = repack<T>(l);
+    if (HELD)
+      held[v - c0] = repack<T>(l);
+    else if (v == 0 || v == vectors - 1)
+      s.edge[v != 0] = repack<T>(l);
 #pragma unroll
     for (int j = 0; j < E; ++j)
       if (l[j] > top) top = l[j], at = row.index_of(v) + j;
@@ -569,6 +703,10 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const __grid_
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
   if (lane == 0) s.best_warp[warp] = best;
+  if (threadIdx.x == kSampleThreads - 1) {
+    const double c = 8.0 * 1.4426950408889634 / fmin(fmax(static_cast<double>(temperature), 5.421010862427522e-20), 1.2676506002282294e30);
+    s.scale[0] = static_cast<float>(c), s.scale[1] = static_cast<float>(c - s.scale[0]);
+  }
   __syncthreads();
 #pragma unroll
   for (int q = 0; q < kSampleWarps; ++q) best = max(best, s.best_warp[q]);
@@ -579,7 +717,6 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const __grid_
     for (uint32_t q = 0; q < kSampleMaxCluster; ++q)
       if (q < ctas) best = max(best, remote_u64(&s.best, q));
   }
-  const float temperature = p.temperature ? p.temperature[m] : 1.f;
   const bool one = best == 0 || !(temperature > 0.f);
   if (one) {
     if (rank == 0 && threadIdx.x == 0) {
@@ -587,36 +724,38 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const __grid_
       if (p.logprobs) p.logprobs[m] = best ? 0.f : -kInf;
     }
   } else {
-    row.r.m = key_logit(~static_cast<uint32_t>(best >> 32));
-    const double c = 1.4426950408889634 / fmax(static_cast<double>(temperature), 5.421010862427522e-20);
-    row.r.z = static_cast<float>(c);
-    row.r.hi = static_cast<float>(8.0 * c);
-    row.r.lo = static_cast<float>(8.0 * c - row.r.hi);
+    row.r = RowScale{key_logit(~static_cast<uint32_t>(best >> 32)), s.scale[0], s.scale[1]};
     row.infinite = row.r.m == kInf;
-    row.table = table;
-    if (T == QGEMV_OUT_BF16) row.fill(table);
+    const bool limited = k > 0 && k < p.V;
+    row.table = T == QGEMV_OUT_BF16 && !(limited && k <= kSampleList) ? table : nullptr;  // a list's weights are fewer than the table's
+    if (row.table) row.fill(table);
     Cut cut{kSampleBuckets, 0, 0, -kInf, -kInf};
-    const int32_t k = p.top_k ? p.top_k[m] : 0;
-    if (k > 0 && k < p.V) cut = row.template cut_at<false>(static_cast<uint64_t>(k), 0.f, cut);
-    const float top_p = p.top_p ? p.top_p[m] : 1.f;
-    if (top_p < 1.f) cut = both_cuts(cut, row.template cut_at<true>(0, fmaxf(top_p, 0.f), cut));
-    const float min_p = p.min_p ? p.min_p[m] : 0.f;
-    const uint64_t floor_w = min_p > 0.f ? static_cast<uint64_t>(ceil(static_cast<double>(fminf(min_p, 1.f)) * 8796093022208.0)) : 0;
-    const float u = p.u[m];
-    row.locate(
-        [&](float l, uint32_t i) -> uint64_t {
-          if (!stays(cut, l, i, row.r)) return 0;
-          const uint64_t w = row.weight(l);
-          return w >= floor_w ? w : 0;
-        },
-        [&](uint64_t total) {
-          const double x = u > 0.f ? static_cast<double>(fminf(u, 1.f)) * static_cast<double>(total) : 0.0;
-          return min(total - 1, static_cast<uint64_t>(x));
-        },
-        [&](uint32_t i, uint64_t w, uint64_t total) {
-          p.tokens[m] = static_cast<int32_t>(i);
-          if (p.logprobs) p.logprobs[m] = logf(static_cast<float>(static_cast<double>(w) / static_cast<double>(total)));
-        });
+    if (limited) cut = row.template cut_at<false>([&](uint64_t) { return static_cast<uint64_t>(k); }, cut);
+    if (top_p < 1.f && !(row.alone && rank != 0))
+      cut = both_cuts(cut, row.template cut_at<true>(
+                               [&](uint64_t total) {
+                                 bool whole = true;
+                                 const uint64_t t = top_p > 0.f ? share_of(top_p, total, whole) : 0;
+                                 return max(t + !whole, static_cast<uint64_t>(1));
+                               },
+                               cut));
+    if (!(row.alone && rank != 0)) {
+      const uint64_t floor_w = min_p > 0.f ? static_cast<uint64_t>(ceilf(fminf(min_p, 1.f) * 8796093022208.f)) : 0;  // 2^43 times it is exact
+      row.locate(
+          [&](float l, uint32_t i) -> uint64_t {
+            if (!stays(cut, l, i, row.r)) return 0;
+            const uint64_t w = row.weight(l);
+            return w >= floor_w ? w : 0;
+          },
+          [&](uint64_t total) {
+            bool whole;
+            return u >= 1.f ? total - 1 : u > 0.f ? share_of(u, total, whole) : 0;
+          },
+          [&](uint32_t i, uint64_t w, uint64_t total) {
+            p.tokens[m] = static_cast<int32_t>(i);
+            if (p.logprobs) p.logprobs[m] = logf(static_cast<float>(static_cast<double>(w) / static_cast<double>(total)));
+          });
+    }
   }
   if (ctas > 1) cluster_meet();  // no CTA leaves while another reads its shared memory
 }
