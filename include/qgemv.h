@@ -614,7 +614,7 @@ qgemv_status_t qgemv_run_scaled(qgemv_handle_t h, const qgemv_scaled_t* scaled, 
  *   tokens        [rows] int32; -1 for a row without a token above -inf.
  *   logprobs      [rows] fp32 or NULL: log of the probability with which the token was drawn, among those
  *                 left (0 for the largest logit, -inf for token -1).
- * Weights are held to 2^-32 of themselves, as whole numbers of 2^-43 (rounded down: smaller ones count as 0), their sums
+ * Weights are held to 2^-32 of the largest, as whole numbers of 2^-43 (rounded down: smaller ones count as 0), their sums
  * exactly, so a result does not depend on the order of a sum; borders are compared in 64 bits.
  * V 1 .. 2^20; logits 16-byte aligned (rows need not be). */
 typedef struct {

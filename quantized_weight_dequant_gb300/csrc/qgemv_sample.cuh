@@ -6,7 +6,7 @@
 // sorted: a cut is found by histograms over ever finer ranges of the logits, and the draw by sums of the warps'
 // pieces of the row.
 //
-//  * Weights are whole numbers of 2^-43, computed to 2^-32 of themselves, and their sums are exact: the result
+//  * Weights are whole numbers of 2^-43, computed to 2^-32 of the largest, and their sums are exact: the result
 //    does not depend on which thread adds what.  32-bit weights are not enough: an error of 2^-24 in a
 //    few heavy tokens moves the borders of all the others, and of 10^4 draws some would go to a neighbour.
 //  * A row belongs to a cluster of CTAs, each with a piece of it in index order, each warp with a piece of that.
@@ -50,8 +50,7 @@ struct alignas(16) SampleSmem {
   float scale[2];         // of the row: hi, lo
   uint64_t pick_before, pick_mass, pick_target, pick_total;
   uint32_t pick_bucket, pick_count;
-  uint64_t pow40[8];
-  int32_t pow30[8];
+  uint64_t pow[64];
   float list_logit[kSampleList];
   uint32_t list_index[kSampleList];
 };
@@ -175,55 +174,62 @@ __device__ __forceinline__ uint32_t rank_key(float l) {
 }
 __device__ __forceinline__ float key_logit(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k : ~k & 0x7fffffffu); }
 
-// 2^(j/8) in units of 2^-40 and of 2^-30.
-__constant__ const uint64_t kPow40[8] = {1099511627776ull, 1199025932245ull, 1307547050779ull, 1425890169699ull, 1554944255988ull, 1695678735018ull, 1849150772653ull, 2016513216442ull};
-__constant__ const int32_t kPow30[8] = {1073741824, 1170923762, 1276901417, 1392470869, 1518500250, 1655936265, 1805811301, 1969251188};
+// 2^(j/64) in units of 2^-43.
+__constant__ const uint64_t kPow[64] = {
+    8796093022208ull, 8891876195264ull, 8988702378691ull, 9086582930126ull, 9185529330885ull, 9285553187305ull,
+    9386666232110ull, 9488880325783ull, 9592207457961ull, 9696659748838ull, 9802249450589ull, 9908988948806ull,
+    10016890763953ull, 10125967552830ull, 10236232110063ull, 10347697369602ull, 10460376406236ull, 10574282437131ull,
+    10689428823381ull, 10805829071568ull, 10923496835354ull, 11042445917079ull, 11162690269381ull, 11284243996830ull,
+    11407121357589ull, 11531336765078ull, 11656904789672ull, 11783840160404ull, 11912157766698ull, 12041872660113ull,
+    12173000056107ull, 12305555335825ull, 12439554047902ull, 12575011910285ull, 12711944812080ull, 12850368815412ull,
+    12990300157313ull, 13131755251623ull, 13274750690919ull, 13419303248457ull, 13565429880144ull, 13713147726524ull,
+    13862474114787ull, 14013426560807ull, 14166022771192ull, 14320280645363ull, 14476218277651ull, 14633853959423ull,
+    14793206181226ull, 14954293634955ull, 15117135216047ull, 15281750025697ull, 15448157373097ull, 15616376777705ull,
+    15786427971528ull, 15958330901445ull, 16132105731538ull, 16307772845465ull, 16485352848846ull, 16664866571680ull,
+    16846335070792ull, 17029779632301ull, 17215221774115ull, 17402683248456ull};
 
-// What the weights of a row go by: its largest logit, and 8 log2(e) / T in two floats.
+// What the weights of a row go by: its largest logit, and 64 log2(e) / T in two floats.
 struct RowScale {
   float m, hi, lo;
 };
 
-// 2^43 w, rounded down, for a finite largest logit.  y = (l - m) 8 log2(e) / T as a sum of two floats; y = k + f with k whole and
-// |f| <= 1/2; 2^(f/8) - 1 by its series in g = f ln(2)/8, |g| < 0.044, whose first term is kept as two floats, and in whole
-// numbers of 2^-22 and of 2^-44; times 2^(k/8) = 2^(k >> 3) times one of eight constants.  Relative error 2^-32.6 at
-// most, 2^-35.5 as a root of the mean square, 2^-38 in the mean (against 80 bits, over 3 10^7 arguments).  Conversions between floats
-// and whole numbers are additions of 1.5 2^23 units, since the converting instructions go at a sixteenth of the rate.
-__device__ __forceinline__ uint64_t weight_of(float l, const RowScale& r, const uint64_t* pow40, const int32_t* pow30) {
+// 2^43 w, rounded down, for a finite largest logit.  y = (l - m) 64 log2(e) / T as a sum of two floats; y = k + f with k whole and
+// |f| <= 1/2; 2^(f/64) - 1 by its series in g = f ln(2)/64, |g| < 0.0055, as a sum of two floats again, and that in whole numbers
+// of 2^-22 and of 2^-44; times 2^(k/64) = 2^(k >> 6) times one of 64 constants.  Weights near 1 are right to 2^-33.4 of
+// themselves, all to 2^-32.7 of the largest; the mean is right to 2^-37 (against 80 bits, over 6 10^7 arguments).  Conversions
+// between floats and whole numbers are additions of 1.5 2^23 units, since the converting instructions go at a quarter of the rate.
+__device__ __forceinline__ uint64_t weight_of(float l, const RowScale& r, const uint64_t* pow) {
   const float d = l - r.m;
   const float back = d - l;
   const float off = (l - (d - back)) + (-r.m - back);  // l - m = d + off
-  constexpr float kNone = -8.f * (kSampleUnit + 2);  // from here on the weight is 0 (also for -inf and NaN: the larger of two is a number)
+  constexpr float kNone = -64.f * (kSampleUnit + 2);  // from here on the weight is 0 (also for -inf and NaN: the larger of two is a number)
   const float p = fmaxf(d * r.hi, kNone);
-  const float e = p > kNone ? fmaf(d, r.hi, -p) + fmaf(d, r.lo, off * r.hi) : 0.f;
+  const float e = p > kNone ? fmaf(off, r.hi, fmaf(d, r.lo, fmaf(d, r.hi, -p))) : 0.f;
   const float kf = p + 12582912.f;
   const int k = __float_as_int(kf) - 0x4b400000;
   const float f = p - (kf - 12582912.f);
-  constexpr float kL = 0.086643397569656372f, kLlo = -2.3808178e-10f;  // ln(2) / 8
+  constexpr float kL = 0.0108304247f;  // ln(2) / 64
   const float g = f * kL;
-  const float rest = fmaf(e, kL, fmaf(f, kLlo, fmaf(f, kL, -g)));
-  const float u = g * g * fmaf(g, fmaf(g, fmaf(g, 1.f / 120.f, 1.f / 24.f), 1.f / 6.f), 0.5f);
-  const float q = u + fmaf(rest, g + u, rest);
-  const float x = g + q, left = (g - x) + q;  // 2^(f/8) - 1 = x + left
+  const float q = fmaf(g * g, fmaf(g, 1.f / 6.f, 0.5f), fmaf(e, kL, fmaf(f, kL, -g)));
+  const float x = g + q, left = (g - x) + q;  // 2^(f/64) - 1 = x + left
   const float a = x + 3.f;                    // units of 2^-22
   const float b = ((x - (a - 3.f)) + left) + 7.152557373046875e-07f;  // 1.5 2^-21: units of 2^-44
   const int n1 = __float_as_int(a) - 0x40400000, n2 = __float_as_int(b) - 0x35400000;
-  const int j = k & 7;
-  const int64_t c = pow30[j];
-  const uint64_t mant = pow40[j] + static_cast<uint64_t>((c * n1 >> 12) + (c * n2 >> 34));
-  return (mant << (kSampleUnit - 40)) >> (-(k >> 3));
+  const uint64_t t = pow[k & 63];
+  const int64_t c = static_cast<int32_t>(t >> 13);
+  return (t + static_cast<uint64_t>((c * n1 >> 9) + (c * n2 >> 31))) >> (-(k >> 6));
 }
 
 // Histogram 0: 40 buckets for each halving of the weight, behind 2^-32 64 for each doubling of the distance.
 __device__ __forceinline__ int bucket_of(float l, const RowScale& r) {
-  const float y = (l - r.m) * r.hi;  // eighths of halvings
-  if (!(y > -256.f)) {
+  const float y = (l - r.m) * r.hi;  // 64 for each halving
+  if (!(y > -2048.f)) {
     if (l == r.m) return 0;  // infinite
-    const float z = y * -0.125f;
+    const float z = y * -0.015625f;
     if (!(z < 131072.f)) return kSampleBuckets - 1;
     return min(kSampleBuckets - 1, 1280 + ((__float_as_int(z) - __float_as_int(32.f)) >> 17));
   }
-  return __float_as_int(fmaf(y, -5.f, 12582912.f)) - 0x4b400000;  // to the nearest
+  return __float_as_int(fmaf(y, -0.625f, 12582912.f)) - 0x4b400000;  // to the nearest
 }
 
 // The tokens that stay, a beginning of the order: those of smaller buckets, and of `bucket` those of smaller keys and of `key`
@@ -239,13 +245,10 @@ __device__ __forceinline__ Cut cut_in(int bucket, const RowScale& r) {
   auto z_at = [](int b) { return b <= 1280 ? (static_cast<float>(b) - 0.5f) / 40.f : __int_as_float(__float_as_int(32.f) + ((b - 1280) << 17)); };
   const float wide = 1e-5f * fabsf(r.m);
   // buckets are monotone in the logit: a logit of a smaller bucket proves it of all larger ones
-  const float sure = r.m - z_at(bucket) * (8.f * 0.99999f) / r.hi + wide, never = r.m - z_at(bucket + 1) * (8.f * 1.00001f) / r.hi - wide;
+  const float sure = r.m - z_at(bucket) * (64.f * 0.99999f) / r.hi + wide, never = r.m - z_at(bucket + 1) * (64.f * 1.00001f) / r.hi - wide;
   if (sure == sure && bucket_of(sure, r) < bucket) c.sure = sure;
   if (never == never && bucket < kSampleBuckets - 1 && bucket_of(never, r) > bucket) c.never = never;
   return c;
-}
-__device__ __forceinline__ bool in_bucket(const Cut& c, float l, const RowScale& r) {
-  return l < c.sure && l > c.never && bucket_of(l, r) == c.bucket;
 }
 __device__ __forceinline__ bool stays(const Cut& c, float l, uint32_t i, const RowScale& r) {
   if (l >= c.sure) return true;
@@ -287,14 +290,14 @@ struct SampleRow {
       if (table && i < kTableValues) return table[i + (b >> 15) * kTableValues];
     }
     if (infinite) return l == r.m ? 1ull << kSampleUnit : 0;
-    return weight_of(l, r, s.pow40, s.pow30);
+    return weight_of(l, r, s.pow);
   }
-  // bf16 has few values: their weights are computed once (a weight is 50 instructions, a row has thousands of equal logits).
+  // bf16 has few values: their weights are computed once (a weight is 45 instructions, a row has thousands of equal logits).
   __device__ __forceinline__ void fill(uint64_t* to) {
     for (int i = threadIdx.x; i < 2 * static_cast<int>(kTableValues); i += kSampleThreads) {
       const uint32_t v = i < static_cast<int>(kTableValues) ? kTableFirst + i : 0x8000u + kTableFirst + i - kTableValues;
       const float l = __uint_as_float(v << 16);
-      to[i] = infinite || l > r.m ? 0 : weight_of(l, r, s.pow40, s.pow30);
+      to[i] = infinite || l > r.m ? 0 : weight_of(l, r, s.pow);
     }
     __syncthreads();
   }
@@ -335,32 +338,76 @@ struct SampleRow {
     return *at;
   }
 
-  // f(logit, index) of this warp's piece, vectors by lanes in turn; of the candidates once they are listed
-  template <class F>
-  __device__ __forceinline__ void each(F f) const {
+  // f(logits, index of the first, how many) of this warp's piece, U vectors' reads in flight together; of the candidates, one by one,
+  // once they are listed
+  template <int U, class F, class G>
+  __device__ __forceinline__ void each(F f, G g) const {
     if (alone) {
-      for (uint32_t i = threadIdx.x; i < s.listed; i += kSampleThreads) f(s.list_logit[i], s.list_index[i]);
+      for (uint32_t i = threadIdx.x; i < s.listed; i += kSampleThreads) g(s.list_logit[i], s.list_index[i]);
       return;
     }
-    constexpr int U = HELD ? 2 : 4;  // reads that are in flight together
     for (int v0 = lo + lane; v0 < hi; v0 += 32 * U) {
       uint4 raw[U];
 #pragma unroll
       for (int u = 0; u < U; ++u)
         if (v0 + 32 * u < hi) raw[u] = load(v0 + 32 * u);
-#pragma unroll 1
+#pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int v = v0 + 32 * u;
-        if (v >= hi) break;
+        if (v0 + 32 * u >= hi) break;
         float l[kVec<T>];
-        unpack<T>(raw[0], l);
+        unpack<T>(raw[u], l);
+        if (!HELD) {
 #pragma unroll
-        for (int w = 0; w + 1 < U; ++w) raw[w] = raw[w + 1];
-        const uint32_t i = static_cast<uint32_t>(index_of(v));
-#pragma unroll
-        for (int j = 0; j < kVec<T>; ++j) f(HELD ? l[j] : usual(l[j]), i + j);
+          for (int j = 0; j < kVec<T>; ++j) l[j] = usual(l[j]);
+        }
+        f(l, static_cast<uint32_t>(index_of(v0 + 32 * u)));
       }
     }
+  }
+  // f(logit, index) where pick(logit) says so, which few do
+  template <class P, class F>
+  __device__ __forceinline__ void each_of(P pick, F f) const {
+    each<HELD ? 2 : 4>(
+        [&](const float (&l)[kVec<T>], uint32_t i) {
+          uint32_t some = 0;
+#pragma unroll
+          for (int j = 0; j < kVec<T>; ++j) some |= static_cast<uint32_t>(pick(l[j])) << j;
+          while (some) {
+            const int j = __ffs(some) - 1;
+            some &= some - 1;
+            float one = l[0];
+#pragma unroll
+            for (int q = 1; q < kVec<T>; ++q)
+              if (j == q) one = l[q];
+            f(one, i + j);
+          }
+        },
+        [&](float l, uint32_t i) {
+          if (pick(l)) f(l, i);
+        });
+  }
+  // f(weight, logit, index) where stays(in), whose weights are computed four at a time
+  template <class F>
+  __device__ __forceinline__ void each_weight(const Cut& in, F f) const {
+    each<2>(
+        [&](const float (&l)[kVec<T>], uint32_t i) {
+#pragma unroll
+          for (int h = 0; h < kVec<T>; h += 4) {
+            bool here[4], any = false;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) any |= here[j] = stays(in, l[h + j], i + h + j, r);
+            if (!any) continue;
+            uint64_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = weight(l[h + j]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (here[j]) f(w[j], l[h + j], i + h + j);
+          }
+        },
+        [&](float l, uint32_t i) {
+          if (stays(in, l, i, r)) f(weight(l), l, i);
+        });
   }
 
   __device__ __forceinline__ void meet() {
@@ -485,11 +532,12 @@ struct SampleRow {
   __device__ void list(const Cut& c, const Cut& in) {
     settle();
     uint32_t* count = rank == 0 ? &s.listed : &s.mine;
-    each([&](float l, uint32_t i) {
-      if (l <= c.never || i >= static_cast<uint32_t>(V) || (l < c.sure && bucket_of(l, r) > c.bucket) || !stays(in, l, i, r)) return;
-      const uint32_t at = atomicAdd(count, 1u);
-      if (at < kSampleList) s.list_logit[at] = l, s.list_index[at] = i;
-    });
+    each_of([&](float l) { return l > c.never; },
+            [&](float l, uint32_t i) {
+              if (i >= static_cast<uint32_t>(V) || (l < c.sure && bucket_of(l, r) > c.bucket) || !stays(in, l, i, r)) return;
+              const uint32_t at = atomicAdd(count, 1u);
+              if (at < kSampleList) s.list_logit[at] = l, s.list_index[at] = i;
+            });
     __syncthreads();
     uint32_t all = s.listed;
     if (ctas > 1) {
@@ -511,18 +559,19 @@ struct SampleRow {
     ctas = 1;
   }
 
-  // The first index at which the running sum of `weigh` exceeds `aim(sum)`; `take` is called by one thread of the cluster with
+  // The first index at which the running sum of `weigh` exceeds `aim(all)`; sum(): this thread's part of it; `take` is called by one thread of the cluster with
   // the index, its weight and the sum.
-  template <class W, class A, class K>
-  __device__ void locate(W weigh, A aim, K take) {
+  template <class S, class W, class A, class K>
+  __device__ void locate(S sum, W weigh, A aim, K take) {
     if (alone) {  // the running sum over ranges of indexes
       uint32_t first = 0;
       uint64_t target = 0, before = 0, total = 0;
       for (int shift = max(0, 32 - __clz(V - 1) - 11), width = 32;; width = shift, shift = max(0, shift - 11)) {
         begin();
-        each([&](float l, uint32_t i) {
-          if (i >= first && (width == 32 || (i - first) >> width == 0)) add_mass(static_cast<int>((i - first) >> shift), weigh(l, i));
-        });
+        for (uint32_t e = threadIdx.x; e < s.listed; e += kSampleThreads) {
+          const uint32_t i = s.list_index[e];
+          if (i >= first && (width == 32 || (i - first) >> width == 0)) add_mass(static_cast<int>((i - first) >> shift), weigh(s.list_logit[e], i));
+        }
         pick<true>([&](uint64_t sum) { return width == 32 ? aim(sum) + 1 : target; }, before);
         if (width == 32) total = s.pick_total;
         target = s.pick_target;
@@ -533,9 +582,7 @@ struct SampleRow {
       if (threadIdx.x == 0) take(first, s.pick_mass, total);
       return;
     }
-    uint64_t mine = 0;
-    each([&](float l, uint32_t i) { mine += weigh(l, i); });
-    mine = warp_sum64(mine);
+    const uint64_t mine = warp_sum64(sum());
     settle();
     __syncthreads();
     if (lane == 0) s.warp_sum[warp] = mine;
@@ -593,18 +640,24 @@ struct SampleRow {
     }
   }
 
+  // Lists the tokens that can be among the first k: those whose bucket is no larger than that of the k-th largest of the threads' largest
+  // logits, `top`.
+  __device__ void list_first(uint32_t k, float top) {
+    begin();
+    if (top > -kInf) atomicAdd(&s.count[bucket_of(top, r)], 1u);
+    pick<false>([&](uint64_t) { return static_cast<uint64_t>(k); }, 0);
+    if (s.pick_total >= k) list(cut_in(static_cast<int>(s.pick_bucket), r), Cut{kSampleBuckets, 0, 0, -kInf, -kInf});
+  }
+
   // The cut after `aim(sum)` tokens (MASS: after the shortest beginning that has that mass) of those that `in` keeps.  In CTAs that
   // have nothing more to do then (alone, and not the first) it means nothing.
   template <bool MASS, class A>
   __device__ Cut cut_at(A aim, const Cut& in) {
     begin();
-    each([&](float l, uint32_t i) {
-      if (!stays(in, l, i, r)) return;
-      if (MASS)
-        add_mass(bucket_of(l, r), weight(l));
-      else
-        atomicAdd(&s.count[bucket_of(l, r)], 1u);
-    });
+    if constexpr (MASS)
+      each_weight(in, [&](uint64_t w, float l, uint32_t) { add_mass(bucket_of(l, r), w); });
+    else
+      each_of([&](float) { return true; }, [&](float l, uint32_t i) { if (stays(in, l, i, r)) atomicAdd(&s.count[bucket_of(l, r)], 1u); });
     pick<MASS>(aim, 0);
     const uint64_t target = s.pick_target;
     uint64_t before = s.pick_before;
@@ -618,14 +671,14 @@ struct SampleRow {
       const int bits = 32 - __clz(khi - klo);
       const int shift = max(0, bits - 11);
       begin();
-      each([&](float l, uint32_t i) {
-        if (!in_bucket(c, l, r)) return;
-        const uint32_t k = rank_key(l);
-        if (k < klo || k > khi || !stays(in, l, i, r)) return;
-        const int b = static_cast<int>((k - klo) >> shift);
-        atomicAdd(&s.count[b], 1u);
-        if (MASS) add_mass(b, weight(l));
-      });
+      each_of([&](float l) { return l < c.sure && l > c.never; },
+              [&](float l, uint32_t i) {
+                const uint32_t k = rank_key(l);
+                if (k < klo || k > khi || bucket_of(l, r) != c.bucket || !stays(in, l, i, r)) return;
+                const int b = static_cast<int>((k - klo) >> shift);
+                atomicAdd(&s.count[b], 1u);
+                if (MASS) add_mass(b, weight(l));
+              });
       pick<MASS>([&](uint64_t) { return target; }, before);
       before = s.pick_before;
       part = MASS ? s.pick_mass : s.pick_count;
@@ -643,8 +696,14 @@ struct SampleRow {
     }
     const int f = turn;
     const float equal = key_logit(klo);
-    locate([&](float l, uint32_t i) { return static_cast<uint64_t>(l == equal && stays(in, l, i, r)); }, [&](uint64_t) { return n - 1; },
-           [&](uint32_t i, uint64_t, uint64_t) { s.found[f] = i; });
+    const auto is = [&](float l, uint32_t i) { return static_cast<uint64_t>(l == equal && stays(in, l, i, r)); };
+    locate(
+        [&] {
+          uint64_t mine = 0;
+          each_of([&](float l) { return l == equal; }, [&](float l, uint32_t i) { mine += is(l, i); });
+          return mine;
+        },
+        is, [&](uint64_t) { return n - 1; }, [&](uint32_t i, uint64_t, uint64_t) { s.found[f] = i; });
     turn ^= 1;
     meet();
     uint32_t at = 0xffffffffu;
@@ -678,7 +737,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const __grid_
   row.warp = warp;
   if (threadIdx.x < 2) s.found[threadIdx.x] = 0xffffffffu;
   if (threadIdx.x == 2) s.listed = 0, s.mine = 0;
-  if (threadIdx.x < 8) s.pow40[threadIdx.x] = kPow40[threadIdx.x], s.pow30[threadIdx.x] = kPow30[threadIdx.x];
+  if (threadIdx.x < 64) s.pow[threadIdx.x] = kPow[threadIdx.x];
   pdl_wait();
   const float temperature = p.temperature ? __ldg(p.temperature + m) : 1.f, top_p = p.top_p ? __ldg(p.top_p + m) : 1.f;
   const float min_p = p.min_p ? __ldg(p.min_p + m) : 0.f, u = __ldg(p.u + m);
@@ -704,7 +763,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const __grid_
   for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
   if (lane == 0) s.best_warp[warp] = best;
   if (threadIdx.x == kSampleThreads - 1) {
-    const double c = 8.0 * 1.4426950408889634 / fmin(fmax(static_cast<double>(temperature), 5.421010862427522e-20), 1.2676506002282294e30);
+    const double c = 64.0 * 1.4426950408889634 / fmin(fmax(static_cast<double>(temperature), 5.421010862427522e-20), 1.2676506002282294e30);
     s.scale[0] = static_cast<float>(c), s.scale[1] = static_cast<float>(c - s.scale[0]);
   }
   __syncthreads();
@@ -730,7 +789,8 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const __grid_
     row.table = T == QGEMV_OUT_BF16 && !(limited && k <= kSampleList) ? table : nullptr;  // a list's weights are fewer than the table's
     if (row.table) row.fill(table);
     Cut cut{kSampleBuckets, 0, 0, -kInf, -kInf};
-    if (limited) cut = row.template cut_at<false>([&](uint64_t) { return static_cast<uint64_t>(k); }, cut);
+    if (limited && k <= static_cast<int>(ctas) * kSampleThreads / 2) row.list_first(static_cast<uint32_t>(k), top);
+    if (limited && !(row.alone && rank != 0)) cut = row.template cut_at<false>([&](uint64_t) { return static_cast<uint64_t>(k); }, cut);
     if (top_p < 1.f && !(row.alone && rank != 0))
       cut = both_cuts(cut, row.template cut_at<true>(
                                [&](uint64_t total) {
@@ -742,6 +802,11 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const __grid_
     if (!(row.alone && rank != 0)) {
       const uint64_t floor_w = min_p > 0.f ? static_cast<uint64_t>(ceilf(fminf(min_p, 1.f) * 8796093022208.f)) : 0;  // 2^43 times it is exact
       row.locate(
+          [&] {
+            uint64_t mine = 0;
+            row.each_weight(cut, [&](uint64_t w, float, uint32_t) { mine += w >= floor_w ? w : 0; });
+            return mine;
+          },
           [&](float l, uint32_t i) -> uint64_t {
             if (!stays(cut, l, i, row.r)) return 0;
             const uint64_t w = row.weight(l);
