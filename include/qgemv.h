@@ -607,7 +607,7 @@ qgemv_status_t qgemv_run_scaled(qgemv_handle_t h, const qgemv_scaled_t* scaled, 
  *                 drawn; where the largest is +inf, only such tokens are.
  *   u             [rows] fp32 in [0, 1) (others are clamped, NaN to 0).
  *   temperature   [rows] fp32, NULL: 1 for all.  Not above 0, or NaN: the token with the largest logit
- *                 (the first of them); below 2^-64 or above 2^100 counts as that.
+ *                 (the first of them); below 2^-64 or above 2^60 counts as that.
  *   top_k         [rows] int32, NULL: none.  Below 1, or at least V: no limit.
  *   top_p, min_p  [rows] fp32, NULL: none.  top_p not below 1 or NaN: no limit; below 0 counts as 0, which
  *                 leaves the first token.  min_p not above 0 or NaN: no limit; above 1 counts as 1.

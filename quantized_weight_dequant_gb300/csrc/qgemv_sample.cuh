@@ -174,39 +174,53 @@ __device__ __forceinline__ uint32_t rank_key(float l) {
 }
 __device__ __forceinline__ float key_logit(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k : ~k & 0x7fffffffu); }
 
-// 2^(j/64) in units of 2^-43.
+// 2^(j/64) in units of 2^-52.
 __constant__ const uint64_t kPow[64] = {
-    8796093022208ull, 8891876195264ull, 8988702378691ull, 9086582930126ull, 9185529330885ull, 9285553187305ull,
-    9386666232110ull, 9488880325783ull, 9592207457961ull, 9696659748838ull, 9802249450589ull, 9908988948806ull,
-    10016890763953ull, 10125967552830ull, 10236232110063ull, 10347697369602ull, 10460376406236ull, 10574282437131ull,
-    10689428823381ull, 10805829071568ull, 10923496835354ull, 11042445917079ull, 11162690269381ull, 11284243996830ull,
-    11407121357589ull, 11531336765078ull, 11656904789672ull, 11783840160404ull, 11912157766698ull, 12041872660113ull,
-    12173000056107ull, 12305555335825ull, 12439554047902ull, 12575011910285ull, 12711944812080ull, 12850368815412ull,
-    12990300157313ull, 13131755251623ull, 13274750690919ull, 13419303248457ull, 13565429880144ull, 13713147726524ull,
-    13862474114787ull, 14013426560807ull, 14166022771192ull, 14320280645363ull, 14476218277651ull, 14633853959423ull,
-    14793206181226ull, 14954293634955ull, 15117135216047ull, 15281750025697ull, 15448157373097ull, 15616376777705ull,
-    15786427971528ull, 15958330901445ull, 16132105731538ull, 16307772845465ull, 16485352848846ull, 16664866571680ull,
-    16846335070792ull, 17029779632301ull, 17215221774115ull, 17402683248456ull};
+    4503599627370496ull, 4552640611975265ull, 4602215617889652ull, 4652330460224456ull, 4702991017412879ull,
+    4754203231900066ull, 4805973110840145ull, 4858306726800864ull, 4911210218475899ull, 4964689791404917ull,
+    5018751718701482ull, 5073402341788886ull, 5128648071143992ull, 5184495387049181ull, 5240950840352481ull,
+    5298021053235979ull, 5355712719992597ull, 5414032607811327ull, 5472987557571019ull, 5532584484642807ull,
+    5592830379701282ull, 5653732309544490ull, 5715297417922861ull, 5777532926377168ull, 5840446135085607ull,
+    5904044423720103ull, 5968335252311938ull, 6033326162126810ull, 6099024776549417ull, 6165438801977672ull,
+    6232576028726661ull, 6300444331942437ull, 6369051672525773ull, 6438406098065967ull, 6508515743784820ull,
+    6579388833490889ull, 6651033680544135ull, 6723458688831074ull, 6796672353750547ull, 6870683263210221ull,
+    6945500098633947ull, 7021131635980086ull, 7097586746770917ull, 7174874399133264ull, 7253003658850448ull,
+    7331983690425701ull, 7411823758157149ull, 7492533227224511ull, 7574121564787629ull, 7656598341096955ull,
+    7739973230616135ull, 7824256013156818ull, 7909456575025820ull, 7995584910184779ull, 8082651121422441ull,
+    8170665421539708ull, 8259638134547591ull, 8349579696878213ull, 8440500658608991ull, 8532411684700150ull,
+    8625323556245722ull, 8719247171738151ull, 8814193548346688ull, 8910173823209688ull};
 
 // What the weights of a row go by: its largest logit, and 64 log2(e) / T in two floats.
 struct RowScale {
   float m, hi, lo;
+  float least;  // a finite logit of weight 0, as which lower ones (and NaN) count
+  bool sharp;   // every logit but the largest has weight 0: that is infinite, or neighbouring numbers are that far apart
 };
 
-// 2^43 w, rounded down, for a finite largest logit.  y = (l - m) 64 log2(e) / T as a sum of two floats; y = k + f with k whole and
+__device__ __forceinline__ RowScale row_scale(float m, float hi, float lo) {
+  RowScale r{m, hi, lo, 0.f, false};
+  const float far = 64.f * (kSampleUnit + 2) / hi;
+  r.sharp = !(fabsf(m) * 5.9604645e-08f < far);  // (the next lower logit is |m| 2^-24 away at least)
+  r.least = m - far * 1.0001f - fabsf(m) * 2.4e-7f;
+  return r;
+}
+
+// 2^43 w, rounded down, for a row that is not sharp.  y = (l - m) 64 log2(e) / T as a sum of two floats; y = k + f with k whole and
 // |f| <= 1/2; 2^(f/64) - 1 by its series in g = f ln(2)/64, |g| < 0.0055, as a sum of two floats again, and that in whole numbers
-// of 2^-22 and of 2^-44; times 2^(k/64) = 2^(k >> 6) times one of 64 constants.  Weights near 1 are right to 2^-33.4 of
-// themselves, all to 2^-32.7 of the largest; the mean is right to 2^-37 (against 80 bits, over 6 10^7 arguments).  Conversions
-// between floats and whole numbers are additions of 1.5 2^23 units, since the converting instructions go at a quarter of the rate.
-__device__ __forceinline__ uint64_t weight_of(float l, const RowScale& r, const uint64_t* pow) {
+// of 2^-22 and of 2^-44; times 2^(k/64) = 2^(k >> 6) times one of 64 constants.  Right to 2^-32 of the largest weight, weights
+// near 1 to 2^-31.8 of themselves as a root of the mean square; the mean is right to 2^-37 (against 80 bits, over 6 10^7 arguments).
+// Conversions between floats and whole numbers are additions of 1.5 2^23 units, since the converting instructions go at a quarter
+// of the rate.  45 instructions: with 117 (64-bit shifts and products as they come) 64 rows of 128000 took 56 us.
+__device__ __forceinline__ uint64_t weight_of(float l, const RowScale& r, const uint64_t* pow, float& y) {
+  l = fmaxf(l, r.least);
   const float d = l - r.m;
   const float back = d - l;
   const float off = (l - (d - back)) + (-r.m - back);  // l - m = d + off
-  constexpr float kNone = -64.f * (kSampleUnit + 2);  // from here on the weight is 0 (also for -inf and NaN: the larger of two is a number)
-  const float p = fmaxf(d * r.hi, kNone);
-  const float e = p > kNone ? fmaf(off, r.hi, fmaf(d, r.lo, fmaf(d, r.hi, -p))) : 0.f;
+  const float p = d * r.hi;
+  y = p;
+  const float e = fmaf(off, r.hi, fmaf(d, r.lo, fmaf(d, r.hi, -p)));
   const float kf = p + 12582912.f;
-  const int k = __float_as_int(kf) - 0x4b400000;
+  const int kb = __float_as_int(kf);  // 0x4b400000 + k
   const float f = p - (kf - 12582912.f);
   constexpr float kL = 0.0108304247f;  // ln(2) / 64
   const float g = f * kL;
@@ -215,21 +229,26 @@ __device__ __forceinline__ uint64_t weight_of(float l, const RowScale& r, const 
   const float a = x + 3.f;                    // units of 2^-22
   const float b = ((x - (a - 3.f)) + left) + 7.152557373046875e-07f;  // 1.5 2^-21: units of 2^-44
   const int n1 = __float_as_int(a) - 0x40400000, n2 = __float_as_int(b) - 0x35400000;
-  const uint64_t t = pow[k & 63];
-  const int64_t c = static_cast<int32_t>(t >> 13);
-  return (t + static_cast<uint64_t>((c * n1 >> 9) + (c * n2 >> 31))) >> (-(k >> 6));
+  uint64_t t = pow[kb & 63];
+  const int c = static_cast<int>(t >> 22);  // units of 2^-30
+  asm("mad.wide.s32 %0, %1, %2, %0;" : "+l"(t) : "r"(c), "r"(n1));
+  asm("mad.wide.s32 %0, %1, 1024, %0;" : "+l"(t) : "r"(__mulhi(c, n2)));
+  uint64_t w;
+  asm("shr.u64 %0, %1, %2;" : "=l"(w) : "l"(t), "r"((0x4b400000 + 639 - kb) >> 6));  // 9 - (k >> 6); from 64 on 0
+  return w;
 }
 
-// Histogram 0: 40 buckets for each halving of the weight, behind 2^-32 64 for each doubling of the distance.
+// Histogram 0: 40 buckets for each halving of the weight, behind 2^-45 16 for each doubling of the distance.
+__device__ __forceinline__ int linear_bucket(float y) { return __float_as_int(fmaf(y, -0.625f, 12582912.f)) - 0x4b400000; }  // to the nearest
 __device__ __forceinline__ int bucket_of(float l, const RowScale& r) {
   const float y = (l - r.m) * r.hi;  // 64 for each halving
-  if (!(y > -2048.f)) {
+  if (!(y > -2880.f)) {
     if (l == r.m) return 0;  // infinite
     const float z = y * -0.015625f;
-    if (!(z < 131072.f)) return kSampleBuckets - 1;
-    return min(kSampleBuckets - 1, 1280 + ((__float_as_int(z) - __float_as_int(32.f)) >> 17));
+    if (!(z < 65536.f)) return kSampleBuckets - 1;
+    return 1801 + ((__float_as_int(z) - __float_as_int(45.f)) >> 19);
   }
-  return __float_as_int(fmaf(y, -0.625f, 12582912.f)) - 0x4b400000;  // to the nearest
+  return linear_bucket(y);
 }
 
 // The tokens that stay, a beginning of the order: those of smaller buckets, and of `bucket` those of smaller keys and of `key`
@@ -242,7 +261,7 @@ struct Cut {
 };
 __device__ __forceinline__ Cut cut_in(int bucket, const RowScale& r) {
   Cut c{bucket, 0xffffffffu, 0xffffffffu, kInf, -kInf};
-  auto z_at = [](int b) { return b <= 1280 ? (static_cast<float>(b) - 0.5f) / 40.f : __int_as_float(__float_as_int(32.f) + ((b - 1280) << 17)); };
+  auto z_at = [](int b) { return b <= 1800 ? (static_cast<float>(b) - 0.5f) / 40.f : __int_as_float(__float_as_int(45.f) + ((b - 1801) << 19)); };
   const float wide = 1e-5f * fabsf(r.m);
   // buckets are monotone in the logit: a logit of a smaller bucket proves it of all larger ones
   const float sure = r.m - z_at(bucket) * (64.f * 0.99999f) / r.hi + wide, never = r.m - z_at(bucket + 1) * (64.f * 1.00001f) / r.hi - wide;
@@ -279,25 +298,33 @@ struct SampleRow {
   int lane, warp;
   RowScale r;
   const uint64_t* table;  // bf16: weights of the values of 15 octaves, positive ones first
-  bool infinite;         // the largest logit is
   bool alone = false;    // the candidates are listed in this CTA, and the others have nothing to do
   int turn = 0;
   bool reading = false;  // others may still be reading this CTA's histogram
 
-  __device__ __forceinline__ uint64_t weight(float l) const {
+  // The weight of a logit of a row that is not sharp, and y = (l - m) 64 log2(e) / T.
+  __device__ __forceinline__ uint64_t weight_y(float l, float& y) const {
     if constexpr (T == QGEMV_OUT_BF16) {
       const uint32_t b = __float_as_uint(l) >> 16, i = (b & 0x7fff) - kTableFirst;
-      if (table && i < kTableValues) return table[i + (b >> 15) * kTableValues];
+      if (table && i < kTableValues) {
+        y = (l - r.m) * r.hi;
+        return table[i + (b >> 15) * kTableValues];
+      }
     }
-    if (infinite) return l == r.m ? 1ull << kSampleUnit : 0;
-    return weight_of(l, r, s.pow);
+    return weight_of(l, r, s.pow, y);
+  }
+  __device__ __forceinline__ uint64_t sharp_weight(float l) const { return l == r.m ? 1ull << kSampleUnit : 0; }
+  __device__ __forceinline__ uint64_t weight(float l) const {
+    float y;
+    return r.sharp ? sharp_weight(l) : weight_y(l, y);
   }
   // bf16 has few values: their weights are computed once (a weight is 45 instructions, a row has thousands of equal logits).
   __device__ __forceinline__ void fill(uint64_t* to) {
     for (int i = threadIdx.x; i < 2 * static_cast<int>(kTableValues); i += kSampleThreads) {
       const uint32_t v = i < static_cast<int>(kTableValues) ? kTableFirst + i : 0x8000u + kTableFirst + i - kTableValues;
       const float l = __uint_as_float(v << 16);
-      to[i] = infinite || l > r.m ? 0 : weight_of(l, r, s.pow);
+      float y;
+      to[i] = l > r.m ? 0 : weight_of(l, r, s.pow, y);
     }
     __syncthreads();
   }
@@ -386,27 +413,39 @@ struct SampleRow {
           if (pick(l)) f(l, i);
         });
   }
-  // f(weight, logit, index) where stays(in), whose weights are computed four at a time
-  template <class F>
+  // f(weight, y, logit, index) of the tokens that `in` keeps (ALL: of all), whose weights are computed four at a time; y: as weight_of
+  // gives it
+  template <bool ALL, class F>
   __device__ __forceinline__ void each_weight(const Cut& in, F f) const {
     each<2>(
         [&](const float (&l)[kVec<T>], uint32_t i) {
 #pragma unroll
           for (int h = 0; h < kVec<T>; h += 4) {
-            bool here[4], any = false;
+            bool here[4] = {true, true, true, true}, any = ALL;
+            if (!ALL) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) any |= here[j] = stays(in, l[h + j], i + h + j, r);
+              for (int j = 0; j < 4; ++j) any |= here[j] = stays(in, l[h + j], i + h + j, r);
+            }
             if (!any) continue;
             uint64_t w[4];
+            float y[4];
+            if (r.sharp) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) w[j] = weight(l[h + j]);
+              for (int j = 0; j < 4; ++j) w[j] = sharp_weight(l[h + j]), y[j] = 0.f;
+            } else {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) w[j] = weight_y(l[h + j], y[j]);
+            }
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              if (here[j]) f(w[j], l[h + j], i + h + j);
+              if (here[j]) f(w[j], y[j], l[h + j], i + h + j);
           }
         },
         [&](float l, uint32_t i) {
-          if (stays(in, l, i, r)) f(weight(l), l, i);
+          if (!ALL && !stays(in, l, i, r)) return;
+          float y = 0.f;
+          const uint64_t w = r.sharp ? sharp_weight(l) : weight_y(l, y);
+          f(w, y, l, i);
         });
   }
 
@@ -655,7 +694,10 @@ struct SampleRow {
   __device__ Cut cut_at(A aim, const Cut& in) {
     begin();
     if constexpr (MASS)
-      each_weight(in, [&](uint64_t w, float l, uint32_t) { add_mass(bucket_of(l, r), w); });
+      if (in.bucket == kSampleBuckets)
+        each_weight<true>(in, [&](uint64_t w, float y, float, uint32_t) { add_mass(linear_bucket(y), w); });  // (what has no weight is not added)
+      else
+        each_weight<false>(in, [&](uint64_t w, float y, float, uint32_t) { add_mass(linear_bucket(y), w); });
     else
       each_of([&](float) { return true; }, [&](float l, uint32_t i) { if (stays(in, l, i, r)) atomicAdd(&s.count[bucket_of(l, r)], 1u); });
     pick<MASS>(aim, 0);
@@ -763,7 +805,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const __grid_
   for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
   if (lane == 0) s.best_warp[warp] = best;
   if (threadIdx.x == kSampleThreads - 1) {
-    const double c = 64.0 * 1.4426950408889634 / fmin(fmax(static_cast<double>(temperature), 5.421010862427522e-20), 1.2676506002282294e30);
+    const double c = 64.0 * 1.4426950408889634 / fmin(fmax(static_cast<double>(temperature), 5.421010862427522e-20), 1.152921504606847e18);
     s.scale[0] = static_cast<float>(c), s.scale[1] = static_cast<float>(c - s.scale[0]);
   }
   __syncthreads();
@@ -776,17 +818,15 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const __grid_
     for (uint32_t q = 0; q < kSampleMaxCluster; ++q)
       if (q < ctas) best = max(best, remote_u64(&s.best, q));
   }
-  const bool one = best == 0 || !(temperature > 0.f);
-  if (one) {
+  if (best != 0) row.r = row_scale(key_logit(~static_cast<uint32_t>(best >> 32)), s.scale[0], s.scale[1]);
+  if (best == 0 || !(temperature > 0.f)) {
     if (rank == 0 && threadIdx.x == 0) {
       p.tokens[m] = best ? static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(best)) : -1;
       if (p.logprobs) p.logprobs[m] = best ? 0.f : -kInf;
     }
   } else {
-    row.r = RowScale{key_logit(~static_cast<uint32_t>(best >> 32)), s.scale[0], s.scale[1]};
-    row.infinite = row.r.m == kInf;
     const bool limited = k > 0 && k < p.V;
-    row.table = T == QGEMV_OUT_BF16 && !(limited && k <= kSampleList) ? table : nullptr;  // a list's weights are fewer than the table's
+    row.table = T == QGEMV_OUT_BF16 && !row.r.sharp && !(limited && k <= kSampleList) ? table : nullptr;  // a list's weights are fewer than the table's
     if (row.table) row.fill(table);
     Cut cut{kSampleBuckets, 0, 0, -kInf, -kInf};
     if (limited && k <= static_cast<int>(ctas) * kSampleThreads / 2) row.list_first(static_cast<uint32_t>(k), top);
@@ -804,7 +844,10 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const __grid_
       row.locate(
           [&] {
             uint64_t mine = 0;
-            row.each_weight(cut, [&](uint64_t w, float, uint32_t) { mine += w >= floor_w ? w : 0; });
+            if (cut.bucket == kSampleBuckets && floor_w == 0)
+              row.template each_weight<true>(cut, [&](uint64_t w, float, float, uint32_t) { mine += w; });
+            else
+              row.template each_weight<false>(cut, [&](uint64_t w, float, float, uint32_t) { mine += w >= floor_w ? w : 0; });
             return mine;
           },
           [&](float l, uint32_t i) -> uint64_t {
