@@ -42,8 +42,7 @@ struct alignas(16) SampleSmem {
   uint64_t warp_sum[kSampleWarps];
   uint64_t cta_sum[2];    // for the cluster
   uint32_t found[2];      // for the cluster
-  uint32_t listed;        // candidates, of the whole cluster in its first CTA
-  uint32_t mine, base;    // this CTA's, and where they go
+  uint32_t mine, listed;  // candidates of this CTA's piece, and in its list
   uint64_t best_warp[kSampleWarps];
   uint64_t best;          // for the cluster
   uint4 edge[2];          // the row's first and last 16 bytes, with -inf in the places of what is not the row's
@@ -294,11 +293,13 @@ struct SampleRow {
   int before_row;        // how many
   int V;
   int last;              // vector of the row
-  int lo, hi;            // this warp's vectors
+  int begin_at, end, whole;  // this CTA's vectors, and how many a warp has
+  int lo, hi;            // this warp's
   int lane, warp;
   RowScale r;
   const uint64_t* table;  // bf16: weights of the values of 15 octaves, positive ones first
-  bool alone = false;    // the candidates are listed in this CTA, and the others have nothing to do
+  bool listed = false;   // the candidates are, in s.list_*
+  bool alone = false;    // those of the whole cluster in its first CTA, and the others have nothing to do
   int turn = 0;
   bool reading = false;  // others may still be reading this CTA's histogram
 
@@ -369,7 +370,7 @@ struct SampleRow {
   // once they are listed
   template <int U, class F, class G>
   __device__ __forceinline__ void each(F f, G g) const {
-    if (alone) {
+    if (listed) {
       for (uint32_t i = threadIdx.x; i < s.listed; i += kSampleThreads) g(s.list_logit[i], s.list_index[i]);
       return;
     }
@@ -566,43 +567,58 @@ struct SampleRow {
     }
   }
 
-  // The candidates, those of `c`'s bucket and smaller ones that `in` keeps, go into the list of the cluster's first CTA, in no
-  // order (what follows goes by logits and indexes); where they fit, it goes on alone.
+  // The candidates, those of `c`'s bucket and smaller ones that `in` keeps, go into lists, in no order (what follows goes by logits
+  // and indexes): into that of the cluster's first CTA where it holds them, which then goes on alone, else into each CTA's own.  Where
+  // one of those is too short, everything goes on over the rows.
   __device__ void list(const Cut& c, const Cut& in) {
     settle();
-    uint32_t* count = rank == 0 ? &s.listed : &s.mine;
     each_of([&](float l) { return l > c.never; },
             [&](float l, uint32_t i) {
               if (i >= static_cast<uint32_t>(V) || (l < c.sure && bucket_of(l, r) > c.bucket) || !stays(in, l, i, r)) return;
-              const uint32_t at = atomicAdd(count, 1u);
+              const uint32_t at = atomicAdd(&s.mine, 1u);
               if (at < kSampleList) s.list_logit[at] = l, s.list_index[at] = i;
             });
     __syncthreads();
-    uint32_t all = s.listed;
+    const uint32_t n = s.mine;
+    uint32_t all = n, most = n, base = 0;
     if (ctas > 1) {
-      const uint32_t n = s.mine;
-      if (rank != 0 && n) {
-        if (threadIdx.x == 0) s.base = add_remote(&s.listed, 0, n);
-        __syncthreads();
-        const uint32_t base = s.base;
-        for (uint32_t i = threadIdx.x; i < n && base + i < kSampleList; i += kSampleThreads) {
+      cluster_meet();
+      uint32_t part[kSampleMaxCluster];
+#pragma unroll
+      for (uint32_t q = 0; q < kSampleMaxCluster; ++q) part[q] = remote_u32(&s.mine, min(q, ctas - 1));
+      all = most = 0;
+#pragma unroll
+      for (uint32_t q = 0; q < kSampleMaxCluster; ++q) {
+        if (q >= ctas) continue;
+        if (q < rank) base += part[q];
+        all += part[q];
+        most = max(most, part[q]);
+      }
+    }
+    if (most > kSampleList) return;
+    listed = true;
+    alone = ctas == 1;
+    if (threadIdx.x == 0) s.listed = n;
+    if (all <= kSampleList && ctas > 1) {
+      if (rank != 0)
+        for (uint32_t i = threadIdx.x; i < n; i += kSampleThreads) {
           store_remote(&s.list_logit[base + i], 0, __float_as_uint(s.list_logit[i]));
           store_remote(&s.list_index[base + i], 0, s.list_index[i]);
         }
-      }
+      else if (threadIdx.x == 0)
+        s.listed = all;
       cluster_meet();
-      all = remote_u32(&s.listed, 0);
+      alone = true;
+      ctas = 1;
     }
-    if (all > kSampleList) return;
-    alone = true;
-    ctas = 1;
+    __syncthreads();
   }
 
   // The first index at which the running sum of `weigh` exceeds `aim(all)`; sum(): this thread's part of it; `take` is called by one thread of the cluster with
   // the index, its weight and the sum.
   template <class S, class W, class A, class K>
   __device__ void locate(S sum, W weigh, A aim, K take) {
-    if (alone) {  // the running sum over ranges of indexes
+    if (listed) {  // the running sum over ranges of indexes
       uint32_t first = 0;
       uint64_t target = 0, before = 0, total = 0;
       for (int shift = max(0, 32 - __clz(V - 1) - 11), width = 32;; width = shift, shift = max(0, shift - 11)) {
@@ -618,7 +634,8 @@ struct SampleRow {
         first += s.pick_bucket << shift;
         if (shift == 0) break;
       }
-      if (threadIdx.x == 0) take(first, s.pick_mass, total);
+      settle();
+      if (threadIdx.x == 0 && (alone || rank == 0)) take(first, s.pick_mass, total);
       return;
     }
     const uint64_t mine = warp_sum64(sum());
@@ -646,36 +663,55 @@ struct SampleRow {
       }
     }
     const uint64_t target = aim(total);
-    if (target >= before && target < before + mine) {  // the same for all lanes
-      for (int at = lo; at < hi; at += 32) {
-        const int v = at + lane;
-        float l[kVec<T>];
-        uint64_t w[kVec<T>], sum = 0;
-        if (v < hi) unpack<T>(load(v), l);
+    uint64_t start = before;  // of this CTA
 #pragma unroll
-        for (int j = 0; j < kVec<T>; ++j) {
-          w[j] = v < hi ? weigh(usual(l[j]), static_cast<uint32_t>(index_of(v) + j)) : 0;
-          sum += w[j];
-        }
-        const uint64_t run = before + warp_scan64(sum, lane);
-        const uint32_t hit = __ballot_sync(0xffffffffu, run > target);
-        if (hit) {
-          if (lane == __ffs(hit) - 1) {
-            uint64_t part = run - sum;
-            bool open = true;
+    for (int q = 0; q < kSampleWarps; ++q) start -= q < warp ? s.warp_sum[q] : 0;
+    if (target < start || target >= start + cta) return;
+    // the piece of a warp with the target in it is divided among all warps, and the part with the target gone through in order
+    int piece = 0;
+    for (; piece + 1 < kSampleWarps && target >= start + s.warp_sum[piece]; ++piece) start += s.warp_sum[piece];
+    __syncthreads();
+    const int from = min(end, begin_at + piece * whole), to = min(end, from + whole);
+    const int step = (to - from + kSampleWarps - 1) / kSampleWarps;
+    const int f0 = min(to, from + warp * step), f1 = min(to, f0 + step);
+    auto weights = [&](int v, uint64_t(&w)[kVec<T>]) {
+      float l[kVec<T>];
+      if (v < f1) unpack<T>(load(v), l);
+      uint64_t all = 0;
 #pragma unroll
-            for (int j = 0; j < kVec<T>; ++j) {
-              part += w[j];
-              if (open && part > target) {
-                take(static_cast<uint32_t>(index_of(v) + j), w[j], total);
-                open = false;
-              }
+      for (int j = 0; j < kVec<T>; ++j) {
+        w[j] = v < f1 ? weigh(usual(l[j]), static_cast<uint32_t>(index_of(v) + j)) : 0;
+        all += w[j];
+      }
+      return all;
+    };
+    uint64_t part = 0, w[kVec<T>];
+    for (int v = f0; v < f1; v += 32) part += weights(v + lane, w);
+    part = warp_sum64(part);
+    if (lane == 0) s.warp_sum[warp] = part;
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < kSampleWarps; ++q) start += q < warp ? s.warp_sum[q] : 0;
+    if (target < start || target >= start + part) return;
+    for (int v = f0; v < f1; v += 32) {
+      const uint64_t all = weights(v + lane, w), run = start + warp_scan64(all, lane);
+      const uint32_t hit = __ballot_sync(0xffffffffu, run > target);
+      if (hit) {
+        if (lane == __ffs(hit) - 1) {
+          uint64_t at = run - all;
+          bool open = true;
+#pragma unroll
+          for (int j = 0; j < kVec<T>; ++j) {
+            at += w[j];
+            if (open && at > target) {
+              take(static_cast<uint32_t>(index_of(v + lane) + j), w[j], total);
+              open = false;
             }
           }
-          break;
         }
-        before = __shfl_sync(0xffffffffu, run, 31);
+        return;
       }
+      start = __shfl_sync(0xffffffffu, run, 31);
     }
   }
 
@@ -705,7 +741,7 @@ struct SampleRow {
     uint64_t before = s.pick_before;
     uint64_t part = MASS ? s.pick_mass : s.pick_count;
     Cut c = cut_in(static_cast<int>(s.pick_bucket), r);
-    if (!alone && (MASS || before + part <= kSampleList)) list(c, in);
+    if (!listed && (MASS || before + part <= kSampleList)) list(c, in);
     if ((alone && rank != 0) || before + part == target) return c;
     // the bucket's logits lie between these
     uint32_t klo = c.sure < kInf ? rank_key(c.sure) : 0, khi = c.never > -kInf ? rank_key(c.never) : 0xffffffffu;
@@ -773,12 +809,13 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const __grid_
   const int per = (c1 - c0 + kSampleWarps - 1) / kSampleWarps;
   SampleRow<T, HELD> row{s, at_row, global, rank, ctas, skip, p.V, vectors - 1};
   uint64_t* table = reinterpret_cast<uint64_t*>(sample_smem + sizeof(SampleSmem));
+  row.begin_at = c0, row.end = c1, row.whole = per;
   row.lo = min(c1, c0 + warp * per);
   row.hi = min(c1, row.lo + per);
   row.lane = lane;
   row.warp = warp;
   if (threadIdx.x < 2) s.found[threadIdx.x] = 0xffffffffu;
-  if (threadIdx.x == 2) s.listed = 0, s.mine = 0;
+  if (threadIdx.x == 2) s.mine = 0;
   if (threadIdx.x < 64) s.pow[threadIdx.x] = kPow[threadIdx.x];
   pdl_wait();
   const float temperature = p.temperature ? __ldg(p.temperature + m) : 1.f, top_p = p.top_p ? __ldg(p.top_p + m) : 1.f;
