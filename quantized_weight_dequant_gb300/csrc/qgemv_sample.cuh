@@ -38,7 +38,7 @@ constexpr float kInf = __builtin_huge_valf();
 struct alignas(16) SampleSmem {
   uint32_t count[kSampleBuckets], lo[kSampleBuckets], hi[kSampleBuckets];  // hi:lo a 64-bit sum
   uint64_t group_mass[kSampleGroups];
-  uint32_t group_count[kSampleGroups];
+  uint32_t group_count[kSampleGroups];  // beside masses
   uint64_t warp_sum[kSampleWarps];
   uint64_t cta_sum[2];    // for the cluster
   uint32_t found[2];      // for the cluster
@@ -48,7 +48,7 @@ struct alignas(16) SampleSmem {
   uint4 edge[2];          // the row's first and last 16 bytes, with -inf in the places of what is not the row's
   float scale[2];         // of the row: hi, lo
   uint64_t pick_before, pick_mass, pick_target, pick_total;
-  uint32_t pick_bucket, pick_count;
+  uint32_t pick_bucket, pick_count, pick_first;  // pick_first: tokens up to the end of the bucket's group (MASS)
   uint64_t pow[64];
   float list_logit[kSampleList];
   uint32_t list_index[kSampleList];
@@ -299,6 +299,8 @@ struct SampleRow {
   RowScale r;
   const uint64_t* table;  // bf16: weights of the values of 15 octaves, positive ones first
   bool listed = false;   // the candidates are, in s.list_*
+  bool parted = false;   // only those of the border's bucket are, and
+  uint64_t above = 0;    // this thread's sum of the smaller buckets' weights
   bool alone = false;    // those of the whole cluster in its first CTA, and the others have nothing to do
   int turn = 0;
   bool reading = false;  // others may still be reading this CTA's histogram
@@ -489,37 +491,40 @@ struct SampleRow {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int b = g * 64 + j * 16 + at;
-        if (MASS)
-          m += static_cast<uint64_t>(s.hi[b]) << 32 | s.lo[b];
-        else
-          c += s.count[b];
+        if (MASS) m += static_cast<uint64_t>(s.hi[b]) << 32 | s.lo[b];
+        c += s.count[b];
       }
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) {
-        if (MASS)
-          m += __shfl_xor_sync(0xffffffffu, m, o);
-        else
-          c += __shfl_xor_sync(0xffffffffu, c, o);
+        if (MASS) m += __shfl_xor_sync(0xffffffffu, m, o);
+        c += __shfl_xor_sync(0xffffffffu, c, o);
       }
-      if (at == 0) s.group_mass[g] = MASS ? m : c;
+      if (at == 0) s.group_mass[g] = MASS ? m : c, s.group_count[g] = c;
     }
     meet();
     if (warp == 0) {
       const uint32_t last = ctas - 1;
       uint64_t v = s.group_mass[lane];
+      uint32_t some = s.group_count[lane];
       if (ctas > 1) {
         uint64_t part[kSampleMaxCluster];
+        uint32_t n[kSampleMaxCluster];
 #pragma unroll
-        for (uint32_t q = 0; q < kSampleMaxCluster; ++q) part[q] = remote_u64(&s.group_mass[lane], min(q, last));
-        v = 0;
+        for (uint32_t q = 0; q < kSampleMaxCluster; ++q) {
+          part[q] = remote_u64(&s.group_mass[lane], min(q, last));
+          if (MASS) n[q] = remote_u32(&s.group_count[lane], min(q, last));
+        }
+        v = some = 0;
 #pragma unroll
-        for (uint32_t q = 0; q < kSampleMaxCluster; ++q) v += q < ctas ? part[q] : 0;
+        for (uint32_t q = 0; q < kSampleMaxCluster; ++q)
+          if (q < ctas) v += part[q], some += MASS ? n[q] : 0;
       }
       uint64_t run = warp_scan64(v, lane);
       const uint64_t total = __shfl_sync(0xffffffffu, run, 31), target = aim(total);
       uint32_t hit = __ballot_sync(0xffffffffu, before + run >= target);
       const int g = hit ? __ffs(hit) - 1 : 31;
       before += __shfl_sync(0xffffffffu, run - v, g);
+      some = __reduce_add_sync(0xffffffffu, lane <= g ? some : 0);
       // the group's 64 buckets, two a lane
       const int b0 = g * 64 + 2 * lane;
       uint64_t bm[2] = {}, bc = 0;  // bc: counts in halves
@@ -558,6 +563,7 @@ struct SampleRow {
         s.pick_count = static_cast<uint32_t>(second ? bc >> 32 : bc);
         s.pick_target = target;
         s.pick_total = total;
+        s.pick_first = some;
       }
     }
     __syncthreads();
@@ -614,11 +620,62 @@ struct SampleRow {
     __syncthreads();
   }
 
+  // Where the candidates are too many for lists: those of `c`'s bucket alone are listed, and the weights (from floor_w on) of the smaller
+  // buckets' summed.
+  __device__ void split(const Cut& c, const Cut& in, uint64_t floor_w) {
+    settle();
+    uint64_t sum = 0;
+    each<2>(
+        [&](const float (&l)[kVec<T>], uint32_t i) {
+#pragma unroll
+          for (int h = 0; h < kVec<T>; h += 4) {
+            bool here[4], any = false;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              here[j] = l[h + j] > c.never && stays(in, l[h + j], i + h + j, r);
+              if (here[j] && l[h + j] < c.sure) {
+                const int b = bucket_of(l[h + j], r);
+                here[j] = b < c.bucket;
+                if (b == c.bucket && i + h + j < static_cast<uint32_t>(V)) {
+                  const uint32_t at = atomicAdd(&s.mine, 1u);
+                  if (at < kSampleList) s.list_logit[at] = l[h + j], s.list_index[at] = i + h + j;
+                }
+              }
+              any |= here[j];
+            }
+            if (!any) continue;
+            uint64_t w[4];
+            float y;
+            if (r.sharp) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) w[j] = sharp_weight(l[h + j]);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) w[j] = weight_y(l[h + j], y);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sum += here[j] && w[j] >= floor_w ? w[j] : 0;
+          }
+        },
+        [](float, uint32_t) {});
+    __syncthreads();
+    uint32_t most = s.mine;
+    if (ctas > 1) {
+      cluster_meet();
+      for (uint32_t q = 0; q < ctas; ++q) most = max(most, remote_u32(&s.mine, q));
+    }
+    if (most > kSampleList) return;
+    above = sum;
+    listed = parted = true;
+    if (threadIdx.x == 0) s.listed = s.mine;
+    __syncthreads();
+  }
+
   // The first index at which the running sum of `weigh` exceeds `aim(all)`; sum(): this thread's part of it; `take` is called by one thread of the cluster with
   // the index, its weight and the sum.
-  template <class S, class W, class A, class K>
+  template <bool FINAL, class S, class W, class A, class K>
   __device__ void locate(S sum, W weigh, A aim, K take) {
-    if (listed) {  // the running sum over ranges of indexes
+    if (listed && !(FINAL && parted)) {  // the running sum over ranges of indexes
       uint32_t first = 0;
       uint64_t target = 0, before = 0, total = 0;
       for (int shift = max(0, 32 - __clz(V - 1) - 11), width = 32;; width = shift, shift = max(0, shift - 11)) {
@@ -638,11 +695,20 @@ struct SampleRow {
       if (threadIdx.x == 0 && (alone || rank == 0)) take(first, s.pick_mass, total);
       return;
     }
-    const uint64_t mine = warp_sum64(sum());
+    const uint64_t mine = warp_sum64(listed ? above : sum());
     settle();
     __syncthreads();
     if (lane == 0) s.warp_sum[warp] = mine;
     __syncthreads();
+    if (listed) {
+      for (uint32_t e = threadIdx.x; e < s.listed; e += kSampleThreads) {
+        const uint32_t i = s.list_index[e];
+        const uint64_t w = weigh(s.list_logit[e], i);
+        const int piece = (static_cast<int>(i + before_row) / kVec<T> - begin_at) / whole;
+        if (w) atomicAdd(reinterpret_cast<unsigned long long*>(&s.warp_sum[piece]), static_cast<unsigned long long>(w));
+      }
+      __syncthreads();
+    }
     uint64_t before = 0, cta = 0;
 #pragma unroll
     for (int q = 0; q < kSampleWarps; ++q) {
@@ -727,21 +793,34 @@ struct SampleRow {
   // The cut after `aim(sum)` tokens (MASS: after the shortest beginning that has that mass) of those that `in` keeps.  In CTAs that
   // have nothing more to do then (alone, and not the first) it means nothing.
   template <bool MASS, class A>
-  __device__ Cut cut_at(A aim, const Cut& in) {
+  __device__ Cut cut_at(A aim, const Cut& in, uint64_t floor_w = 0) {
     begin();
-    if constexpr (MASS)
+    if constexpr (MASS) {
+      const auto add = [&](uint64_t w, float y, float, uint32_t) {
+        if (!w) return;
+        const int b = linear_bucket(y);
+        atomicAdd(&s.count[b], 1u);
+        add_mass(b, w);
+      };
       if (in.bucket == kSampleBuckets)
-        each_weight<true>(in, [&](uint64_t w, float y, float, uint32_t) { add_mass(linear_bucket(y), w); });  // (what has no weight is not added)
+        each_weight<true>(in, add);
       else
-        each_weight<false>(in, [&](uint64_t w, float y, float, uint32_t) { add_mass(linear_bucket(y), w); });
-    else
+        each_weight<false>(in, add);
+    } else {
       each_of([&](float) { return true; }, [&](float l, uint32_t i) { if (stays(in, l, i, r)) atomicAdd(&s.count[bucket_of(l, r)], 1u); });
+    }
     pick<MASS>(aim, 0);
     const uint64_t target = s.pick_target;
     uint64_t before = s.pick_before;
     uint64_t part = MASS ? s.pick_mass : s.pick_count;
     Cut c = cut_in(static_cast<int>(s.pick_bucket), r);
-    if (!listed && (MASS || before + part <= kSampleList)) list(c, in);
+    if (!listed) {
+      const bool fit = MASS ? s.pick_first <= kSampleList * ctas * 3 / 4 : before + part <= kSampleList;
+      if (fit) list(c, in);
+      if constexpr (MASS) {
+        if (!fit) split(c, in, floor_w);
+      }
+    }
     if ((alone && rank != 0) || before + part == target) return c;
     // the bucket's logits lie between these
     uint32_t klo = c.sure < kInf ? rank_key(c.sure) : 0, khi = c.never > -kInf ? rank_key(c.never) : 0xffffffffu;
@@ -775,7 +854,7 @@ struct SampleRow {
     const int f = turn;
     const float equal = key_logit(klo);
     const auto is = [&](float l, uint32_t i) { return static_cast<uint64_t>(l == equal && stays(in, l, i, r)); };
-    locate(
+    locate<false>(
         [&] {
           uint64_t mine = 0;
           each_of([&](float l) { return l == equal; }, [&](float l, uint32_t i) { mine += is(l, i); });
@@ -868,6 +947,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const __grid_
     Cut cut{kSampleBuckets, 0, 0, -kInf, -kInf};
     if (limited && k <= static_cast<int>(ctas) * kSampleThreads / 2) row.list_first(static_cast<uint32_t>(k), top);
     if (limited && !(row.alone && rank != 0)) cut = row.template cut_at<false>([&](uint64_t) { return static_cast<uint64_t>(k); }, cut);
+    const uint64_t floor_w = min_p > 0.f ? static_cast<uint64_t>(ceilf(fminf(min_p, 1.f) * 8796093022208.f)) : 0;  // 2^43 times it is exact
     if (top_p < 1.f && !(row.alone && rank != 0))
       cut = both_cuts(cut, row.template cut_at<true>(
                                [&](uint64_t total) {
@@ -875,10 +955,9 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const __grid_
                                  const uint64_t t = top_p > 0.f ? share_of(top_p, total, whole) : 0;
                                  return max(t + !whole, static_cast<uint64_t>(1));
                                },
-                               cut));
+                               cut, floor_w));
     if (!(row.alone && rank != 0)) {
-      const uint64_t floor_w = min_p > 0.f ? static_cast<uint64_t>(ceilf(fminf(min_p, 1.f) * 8796093022208.f)) : 0;  // 2^43 times it is exact
-      row.locate(
+      row.template locate<true>(
           [&] {
             uint64_t mine = 0;
             if (cut.bucket == kSampleBuckets && floor_w == 0)
