@@ -64,6 +64,12 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
   return m;
 }
+// The larger magnitude of two, with either sign; NaN where one is.
+__device__ __forceinline__ float max_abs_nan(float a, float b) {
+  float m;
+  asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+  return m;
+}
 
 // The scale of values whose largest magnitude is `top`: top / 448, the largest code; 1 where that is 0 or not finite.
 __device__ __forceinline__ float e4m3_scale(float top) {
@@ -78,11 +84,15 @@ __device__ __forceinline__ float e4m3_scale(float top) {
 // each costs the cache store 3 us of 36.7 (8191 tokens).
 __device__ __forceinline__ uint2 e4m3_codes(float (&x)[8], float top, float scale) {
   const float by = __frcp_rn(scale);
-  const bool finite = top < __int_as_float(0x7f800000);
+  if (top < __int_as_float(0x7f800000)) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float y = x[j] * by;
-    x[j] = finite ? fmaf(fmaf(-y, scale, x[j]), by, y) : y;
+    for (int j = 0; j < 8; ++j) {
+      const float y = x[j] * by;
+      x[j] = fmaf(fmaf(-y, scale, x[j]), by, y);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] *= by;
   }
   uint32_t w[2];
 #pragma unroll

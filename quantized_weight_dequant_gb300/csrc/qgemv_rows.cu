@@ -12,6 +12,7 @@ using namespace qg;
 
 namespace {
 
+constexpr int kNormWarpThreads = 2048, kNormThreads = 1024;  // on an SM, a warp or a CTA to a row
 constexpr int64_t kMaxStride = int64_t{1} << 40;  // elements: offsets of a row stay clear of 64 bits
 
 bool out_type(qgemv_out_t t) { return t == QGEMV_OUT_F32 || t == QGEMV_OUT_F16 || t == QGEMV_OUT_BF16; }
@@ -19,12 +20,12 @@ int64_t out_bytes(qgemv_out_t t) { return t == QGEMV_OUT_F32 ? 4 : 2; }
 
 template <bool WIDE, int RES, bool WARP>
 const void* norm_kernel_v(int v) {
-  switch (v) {
-    case 1: return reinterpret_cast<const void*>(norm_kernel<WIDE, RES, 1, WARP>);
-    case 2: return reinterpret_cast<const void*>(norm_kernel<WIDE, RES, 2, WARP>);
-    case 4: return reinterpret_cast<const void*>(norm_kernel<WIDE, RES, 4, WARP>);
-    default: return reinterpret_cast<const void*>(norm_kernel<WIDE, RES, 8, WARP>);
+  if (v == 1) return reinterpret_cast<const void*>(norm_kernel<WIDE, RES, 1, WARP>);
+  if constexpr (!WARP) {
+    if (v == 4) return reinterpret_cast<const void*>(norm_kernel<WIDE, RES, 4, WARP>);
+    if (v == 8) return reinterpret_cast<const void*>(norm_kernel<WIDE, RES, 8, WARP>);
   }
+  return reinterpret_cast<const void*>(norm_kernel<WIDE, RES, 2, WARP>);
 }
 template <bool WIDE, bool WARP>
 const void* norm_kernel_res(int res, int v) {
@@ -53,18 +54,22 @@ qgemv_status_t qgemv_run_norm(qgemv_handle_t hh, const qgemv_norm_t* norm, cudaS
       !aligned16(p.weight) || (p.codes && reinterpret_cast<uintptr_t>(p.scale) % 4))
     return QGEMV_ERR_MISALIGNED;
   if (p.rows == 0) return QGEMV_OK;
-  // up to 2048 elements: a warp per row; more: a CTA per row
-  const int vecs = p.N / 8;
-  const bool warp = vecs <= 32 * 8;
+  // Up to 512 elements a warp has a row, and 64 warps an SM; more: a CTA (2048 elements, 8191 rows: 24.6 us, with a warp
+  // for each 35).  Many rows: a thread has two pieces of its row and a CTA goes on to the row 1024 threads an SM on, whose
+  // elements it reads before it finishes the first (4096 elements: 44.8 us, 57.5 with one piece, 68.4 with four; 14336:
+  // 158, with a CTA for each row 217).  Few rows: as many threads as there are pieces.
+  const int vecs = static_cast<int>(p.N / 8);
+  const bool warp = vecs <= 64;
   int v = 1;
   if (warp) {
-    while (32 * v < vecs) v *= 2;
+    v = vecs <= 32 ? 1 : 2;
   } else {
     while (1024 * v < vecs) v *= 2;
     if (v == 1 && p.rows > 2 * h->sms) v = 2;
   }
   const int threads = warp ? 32 * kNormWarps : ((vecs + v - 1) / v + 31) / 32 * 32;
-  const int64_t grid = warp ? (p.rows + kNormWarps - 1) / kNormWarps : p.rows;
+  const int64_t resident = static_cast<int64_t>(h->sms) * std::max(1, (warp ? kNormWarpThreads : kNormThreads) / threads);
+  const int64_t grid = std::min<int64_t>(warp ? (p.rows + kNormWarps - 1) / kNormWarps : p.rows, resident);
   const int res = !p.res ? 0 : p.res_type == QGEMV_OUT_F32 ? 2 : 1;
   const bool wide = p.in == QGEMV_OUT_F32;
   const void* fn = wide ? (warp ? norm_kernel_res<true, true>(res, v) : norm_kernel_res<true, false>(res, v))
@@ -87,15 +92,13 @@ qgemv_status_t qgemv_quant_rows(qgemv_handle_t hh, const qgemv_quant_t* quant, c
   if (!aligned16(p.x) || !aligned16(p.up) || !aligned16(p.codes) || p.x_stride * el % 16 || (p.up && p.up_stride * el % 16) ||
       p.codes_stride % 16 || reinterpret_cast<uintptr_t>(p.scale) % 4)
     return QGEMV_ERR_MISALIGNED;
-  const int64_t per = int64_t{8} * kQuantThreads * kQuantV;
-  unsigned chunks = static_cast<unsigned>((p.N + per - 1) / per);
-  if (p.rows * chunks > 0x7fffffff) return QGEMV_ERR_BAD_SHAPE;
   if (p.rows == 0) return QGEMV_OK;
   const bool wide = p.in == QGEMV_OUT_F32;
   const void* fn = p.up ? (wide ? reinterpret_cast<const void*>(quant_kernel<true, true>) : reinterpret_cast<const void*>(quant_kernel<false, true>))
                         : (wide ? reinterpret_cast<const void*>(quant_kernel<true, false>) : reinterpret_cast<const void*>(quant_kernel<false, false>));
+  int chunks = (p.N + 16 * kQuantThreads - 1) / (16 * kQuantThreads);
   void* args[] = {const_cast<qgemv_quant_t*>(&p), &chunks};
-  return launch_dependent(fn, dim3(static_cast<unsigned>(p.rows * chunks)), kQuantThreads, 0, 1, args, stream) ? QGEMV_OK : QGEMV_ERR_CUDA;
+  return launch_dependent(fn, dim3(static_cast<unsigned>(p.rows), std::min(chunks, 65535)), kQuantThreads, 0, 1, args, stream) ? QGEMV_OK : QGEMV_ERR_CUDA;
 }
 
 }  // extern "C"
