@@ -42,6 +42,7 @@ struct alignas(16) SampleSmem {
   uint64_t warp_sum[kSampleWarps];
   uint64_t cta_sum[2];    // for the cluster
   uint32_t found[2];      // for the cluster
+  uint32_t others;        // add_values
   uint32_t mine, listed;  // candidates of this CTA's piece, and in its list
   uint64_t best_warp[kSampleWarps];
   uint64_t best;          // for the cluster
@@ -360,14 +361,20 @@ struct SampleRow {
       }
     }
   }
-  __device__ __forceinline__ uint4 load(int v) const {
-    if constexpr (HELD) return vecs[v];
+  __device__ __forceinline__ const uint4* where(int v) const {
     const uint4* at = vecs + v;
-    if (v == last) at = &s.edge[1];
-    if (v == 0) at = &s.edge[0];
-    return *at;
+    if (!HELD && v == last) at = &s.edge[1];
+    if (!HELD && v == 0) at = &s.edge[0];
+    return at;
   }
+  __device__ __forceinline__ uint4 load(int v) const { return *where(v); }
 
+  template <int U>
+  __device__ __forceinline__ void read(int v0, uint4 (&raw)[U]) const {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (v0 + 32 * u < hi) raw[u] = load(v0 + 32 * u);
+  }
   // f(logits, index of the first, how many) of this warp's piece, U vectors' reads in flight together; of the candidates, one by one,
   // once they are listed
   template <int U, class F, class G>
@@ -376,11 +383,17 @@ struct SampleRow {
       for (uint32_t i = threadIdx.x; i < s.listed; i += kSampleThreads) g(s.list_logit[i], s.list_index[i]);
       return;
     }
+    uint4 next[U];
+    if (!HELD) read<U>(lo + lane, next);
     for (int v0 = lo + lane; v0 < hi; v0 += 32 * U) {
       uint4 raw[U];
+      if (HELD) {
+        read<U>(v0, raw);
+      } else {
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (v0 + 32 * u < hi) raw[u] = load(v0 + 32 * u);
+        for (int u = 0; u < U; ++u) raw[u] = next[u];
+        read<U>(v0 + 32 * U, next);
+      }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         if (v0 + 32 * u >= hi) break;
@@ -397,7 +410,7 @@ struct SampleRow {
   // f(logit, index) where pick(logit) says so, which few do
   template <class P, class F>
   __device__ __forceinline__ void each_of(P pick, F f) const {
-    each<HELD ? 2 : 4>(
+    each<2>(
         [&](const float (&l)[kVec<T>], uint32_t i) {
           uint32_t some = 0;
 #pragma unroll
@@ -790,19 +803,79 @@ struct SampleRow {
     if (s.pick_total >= k) list(cut_in(static_cast<int>(s.pick_bucket), r), Cut{kSampleBuckets, 0, 0, -kInf, -kInf});
   }
 
+  // add(weight, y, ...) of all tokens' sums for the histogram: those of the table's values are counted, in the place of the list, and a
+  // count times a weight added, one add instead of three for each token.
+  template <class A>
+  __device__ void add_values(A add) {
+    uint32_t* seen = s.list_index;
+    static_assert(2 * kTableValues <= kSampleList);
+    for (int i = threadIdx.x; i < static_cast<int>(2 * kTableValues); i += kSampleThreads) seen[i] = 0;
+    if (threadIdx.x == 0) s.others = 0;
+    __syncthreads();
+    const auto add_one = [&](float l) {
+      float y;
+      const uint64_t w = weight_of(l, r, s.pow, y);
+      add(w, y, 1u);
+    };
+    constexpr int U = 2;
+    uint4 next[U];
+    read<U>(lo + lane, next);
+    for (int v0 = lo + lane; v0 < hi; v0 += 32 * U) {
+      uint4 raw[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) raw[u] = next[u];
+      read<U>(v0 + 32 * U, next);
+      uint32_t others = 0;  // a bit each
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (v0 + 32 * u >= hi) break;
+        const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t b = j % 2 ? w[j / 2] >> 16 : w[j / 2] & 0xffff, at = (b & 0x7fff) - kTableFirst;
+          if (at < kTableValues)
+            atomicAdd(&seen[at + (b >> 15) * kTableValues], 1u);
+          else
+            others |= static_cast<uint32_t>(__uint_as_float(b << 16) > r.least) << (8 * u + j);
+        }
+      }
+      while (others) {
+        const int k = __ffs(others) - 1;
+        others &= others - 1;
+        const float l = usual(__uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(where(v0 + 32 * (k / 8)))[k % 8]) << 16));
+        const uint32_t at = atomicAdd(&s.others, 1u);
+        if (at < kSampleList)
+          s.list_logit[at] = l;  // all threads will share these
+        else
+          add_one(l);
+      }
+    }
+    __syncthreads();
+    for (uint32_t i = threadIdx.x; i < min(s.others, static_cast<uint32_t>(kSampleList)); i += kSampleThreads) add_one(s.list_logit[i]);
+    for (int i = threadIdx.x; i < static_cast<int>(2 * kTableValues); i += kSampleThreads) {
+      const uint32_t n = seen[i], b = i < static_cast<int>(kTableValues) ? kTableFirst + i : 0x8000u + kTableFirst + i - kTableValues;
+      if (n) add(table[i], (__uint_as_float(b << 16) - r.m) * r.hi, n);
+    }
+  }
+
   // The cut after `aim(sum)` tokens (MASS: after the shortest beginning that has that mass) of those that `in` keeps.  In CTAs that
   // have nothing more to do then (alone, and not the first) it means nothing.
   template <bool MASS, class A>
   __device__ Cut cut_at(A aim, const Cut& in, uint64_t floor_w = 0) {
     begin();
     if constexpr (MASS) {
-      const auto add = [&](uint64_t w, float y, float, uint32_t) {
+      const auto add_n = [&](uint64_t w, float y, uint32_t n) {
         if (!w) return;
         const int b = linear_bucket(y);
-        atomicAdd(&s.count[b], 1u);
-        add_mass(b, w);
+        atomicAdd(&s.count[b], n);
+        add_mass(b, w * n);
       };
-      if (in.bucket == kSampleBuckets)
+      const auto add = [&](uint64_t w, float y, float, uint32_t) { add_n(w, y, 1); };
+      bool by_value = false;
+      if constexpr (T == QGEMV_OUT_BF16) by_value = table && !listed && in.bucket == kSampleBuckets;
+      if (by_value)
+        add_values(add_n);
+      else if (in.bucket == kSampleBuckets)
         each_weight<true>(in, add);
       else
         each_weight<false>(in, add);
