@@ -11,17 +11,21 @@
 
 namespace qg {
 
+namespace {
+
 const void* few_kernel_for(int BT) {
-  return BT > 64   ? reinterpret_cast<const void*>(scaled_few_kernel<128>)
-         : BT > 32 ? reinterpret_cast<const void*>(scaled_few_kernel<64>)
+  return BT > 32   ? reinterpret_cast<const void*>(scaled_few_kernel<64>)
          : BT > 16 ? reinterpret_cast<const void*>(scaled_few_kernel<32>)
                    : reinterpret_cast<const void*>(scaled_few_kernel<16>);
 }
+int few_index(int BT) { return BT > 32 ? 2 : BT > 16 ? 1 : 0; }
+
+}  // namespace
 
 // How many clusters of each size run at once, asked once for a handle.  The answer counts a single CTA to an SM, as of every kernel
 // that allocates tensor memory; these take half of it at most, and two are there at a time.
 bool scaled_prepare(Handle& h) {
-  for (int BT : {16, 32, 64, 128}) {
+  for (int BT : {16, 32, 64}) {
     if (cudaFuncSetAttribute(few_kernel_for(BT), cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(few_smem_bytes(BT))) != cudaSuccess)
       return false;
     for (int ks = 2; ks <= 8; ++ks) {
@@ -38,7 +42,7 @@ bool scaled_prepare(Handle& h) {
       cfg.numAttrs = 1;
       int n = 0;
       if (cudaOccupancyMaxActiveClusters(&n, few_kernel_for(BT), &cfg) != cudaSuccess) cudaGetLastError(), n = 0;
-      h.scaled_clusters[BT > 64 ? 3 : BT > 32 ? 2 : BT > 16 ? 1 : 0][ks] = 2 * n;
+      h.scaled_clusters[few_index(BT)][ks] = 2 * n;
     }
   }
   return true;
@@ -68,14 +72,12 @@ bool encode(const Handle& h, const void* at, int64_t rows, int64_t K, int64_t st
 qgemv_status_t launch_few(const Handle& h, const qgemv_scaled_t& p, ScaledArgs a, int BT, cudaStream_t stream) {
   CUtensorMap wmap, xmap;
   if (!encode(h, p.W, p.N, p.K, p.K, kScaledRows, &wmap) || !encode(h, p.x, p.M, p.K, p.x_stride, BT, &xmap)) return QGEMV_ERR_CUDA;
-  a.x_tiles = static_cast<int>((p.M + BT - 1) / BT);
-  const int64_t tiles = (p.N + kScaledRows - 1) / kScaledRows * a.x_tiles;
+  const int64_t tiles = (p.N + kScaledRows - 1) / kScaledRows;
   // the largest cluster with which all tiles run at once, of two blocks a CTA at least
-  const int* most = h.scaled_clusters[BT > 64 ? 3 : BT > 32 ? 2 : BT > 16 ? 1 : 0];
+  const int* most = h.scaled_clusters[few_index(BT)];
   a.ks = 1;
   for (int ks = 2; ks <= 8; ++ks)
     if (tiles <= most[ks] && a.blocks >= 2 * ks) a.ks = ks;
-  if (tiles * a.ks > 0x7fffffff) return QGEMV_ERR_BAD_SHAPE;
   void* args[] = {&wmap, &xmap, &a};
   return launch_dependent(few_kernel_for(BT), dim3(static_cast<unsigned>(tiles * a.ks)), few_threads(BT), few_smem_bytes(BT), a.ks, args, stream)
              ? QGEMV_OK
@@ -86,7 +88,8 @@ qgemv_status_t launch_many(const Handle& h, const qgemv_scaled_t& p, ScaledArgs 
   a.x_tiles = static_cast<int>((p.M + kManyRows - 1) / kManyRows);
   a.wide = a.blocks % 4 == 0 && p.x_scale_stride % 4 == 0 && aligned16(p.x_scale) && aligned16(p.w_scale);
   const int64_t pairs = h.sms / 2;
-  // rounds of tiles, by the time that a block of a tile takes
+  // rounds of tiles, by the time that a block of a tile takes: one of 128 weight rows three quarters of one of 256, so that those are
+  // faster unless they leave many pairs idle in the last round
   auto cost = [&](int BN) { return (a.x_tiles * ((p.N + BN - 1) / BN) + pairs - 1) / pairs * (BN == 128 ? 3 : 4); };
   const int BN = cost(128) < cost(256) ? 128 : 256;
   CUtensorMap wmap, xmap;

@@ -6,11 +6,12 @@
 // fp32 accumulators in its registers: the scales change with every block, so the sum over blocks cannot stay in
 // tensor memory.
 //
-// What bounds few rows of x is the bytes of W, N K of them.  A CTA has a tile of 128 weight rows x BT rows of x, or with
-// few tiles a cluster of CTAs has it and each takes a share of its blocks; then every CTA leaves its sums in shared
+// What bounds few rows of x, up to 64, is the bytes of W, N K of them.  A CTA has a tile of 128 weight rows and all BT rows of
+// x, or with few tiles a cluster of CTAs has it and each takes a share of its blocks; then every CTA leaves its sums in shared
 // memory and adds a part of the tile over the cluster, in rank order.  Two CTAs are on an SM: where their number is no
 // multiple of the SMs', memory serves all of them alike and they still end together, and one's start and end are the other's
-// loads.  (Equal shares of all tiles' blocks, one persistent CTA an SM, joined through the workspace: 64 x 28672 x
+// loads.  1 x 4096 x 4096 takes 6.4 us (its bytes 2.5, the launch, the first loads' way and the join the rest), 37 x 4096 x 14336
+// 15.9 (8.8) and 64 x 28672 x 4096 23.5 (17.9).  (Equal shares of all tiles' blocks, one persistent CTA an SM, joined through the workspace: 64 x 28672 x
 // 4096 32.5 us, 64 x 4096 x 4096 19.8, most of it joins.)
 //  * The weight rows are the MMA's M (TMEM lanes), the rows of x its N: a lane's accumulators then belong to
 //    one weight row and BT rows of x, and 32 lanes write 32 neighbours of a row of y.
@@ -43,8 +44,8 @@ struct ScaledArgs {
   void* y;
   int64_t xs_stride, y_stride;
   int M, N, blocks;
-  int x_tiles;
-  int ks;         // CTAs of a cluster, which share a tile's blocks
+  int x_tiles;    // many rows
+  int ks;         // few rows: CTAs of a cluster, which share a tile's blocks
   int out;
   int* err;
   uint64_t spin_ns;
@@ -59,7 +60,7 @@ __host__ __device__ constexpr int few_stage_bytes(int BT) { return kScaledBlock 
 __host__ __device__ constexpr int few_stages(int BT) { return 108 * 1024 / few_stage_bytes(BT); }
 // Blocks whose sums are handed over together (their barriers and scales are met once): two such sets fill half of tensor
 // memory, or a quarter at BT = 16.
-__host__ __device__ constexpr int few_set(int BT) { return BT > 64 ? 1 : BT > 32 ? 2 : 4; }
+__host__ __device__ constexpr int few_set(int BT) { return BT > 32 ? 2 : 4; }
 __host__ __device__ constexpr int few_tmem_cols(int BT) { return 2 * few_set(BT) * BT; }
 __host__ __device__ constexpr int few_scale_bytes(int BT) { return 2 * 3 * few_set(BT) * BT * 4; }  // two sets: products, x's and W's
 __host__ __device__ constexpr size_t few_smem_bytes(int BT) {
@@ -113,9 +114,8 @@ __global__ void __launch_bounds__(few_threads(BT), 2) scaled_few_kernel(const __
   static_assert(BT * kScaledRows * 4 <= S * STAGE, "a tile's sums take the place of the stages");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const unsigned ks = static_cast<unsigned>(a.ks), rank = blockIdx.x % ks, tile = blockIdx.x / ks;
-  const int wt = static_cast<int>(tile / static_cast<unsigned>(a.x_tiles)), xt = static_cast<int>(tile % static_cast<unsigned>(a.x_tiles));
+  const int wt = static_cast<int>(tile), rows = a.M;
   const int kb0 = static_cast<int>(static_cast<int64_t>(a.blocks) * rank / ks), n = static_cast<int>(static_cast<int64_t>(a.blocks) * (rank + 1) / ks) - kb0;
-  const int m0 = xt * BT, rows = min(BT, a.M - m0);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) mbar_init(full(s), 1), mbar_init(empty(s), 1);
@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(few_threads(BT), 2) scaled_few_kernel(const __
           mbar_arrive_expect_tx(full(s), STAGE);
           tma_load_2d(base + s * STAGE, &wmap, (kb0 + i) * kScaledBlock, wt * kScaledRows, full(s));
         }
-        tma_load_2d(base + s * STAGE + WBYTES, &xmap, (kb0 + i) * kScaledBlock, m0, full(s));
+        tma_load_2d(base + s * STAGE + WBYTES, &xmap, (kb0 + i) * kScaledBlock, 0, full(s));
       }
       if (++s == S) s = 0, ph ^= 1;
     }
@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(few_threads(BT), 2) scaled_few_kernel(const __
       for (int e = tid; e < P; e += EPI) {
         const int q = e / BT, m = e % BT;
         if (i + q < n && m < rows) {
-          copy4(raw + (2 * p * P + e) * 4, a.xs + static_cast<int64_t>(m0 + m) * a.xs_stride + kb0 + i + q);
+          copy4(raw + (2 * p * P + e) * 4, a.xs + m * a.xs_stride + kb0 + i + q);
           copy4(raw + ((2 * p + 1) * P + e) * 4, a.ws + static_cast<int64_t>(wt) * a.blocks + kb0 + i + q);
         }
       }
@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(few_threads(BT), 2) scaled_few_kernel(const __
       if (col < a.N) {
 #pragma unroll
         for (int c = 0; c < HB; ++c)
-          if (hh * HB + c < rows) scaled_store(a.y, static_cast<int64_t>(m0 + hh * HB + c) * a.y_stride + col, a.out, acc[c]);
+          if (hh * HB + c < rows) scaled_store(a.y, static_cast<int64_t>(hh * HB + c) * a.y_stride + col, a.out, acc[c]);
       }
     } else {
       // the MMAs have read the stages: this CTA's sums take their place, [row of x][weight row]
@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(few_threads(BT), 2) scaled_few_kernel(const __
 #pragma unroll
       for (int q = 1; q < 8; ++q) sum += v[q];
       const int64_t col = static_cast<int64_t>(wt) * kScaledRows + e % kScaledRows;
-      if (col < a.N) scaled_store(a.y, static_cast<int64_t>(m0 + e / kScaledRows) * a.y_stride + col, a.out, sum);
+      if (col < a.N) scaled_store(a.y, static_cast<int64_t>(e / kScaledRows) * a.y_stride + col, a.out, sum);
     }
     scaled_cluster_meet();  // nobody leaves while its sums are read
   }
@@ -311,6 +311,9 @@ __global__ void __launch_bounds__(few_threads(BT), 2) scaled_few_kernel(const __
 // W (a CTA alone would need 96 bytes a cycle for the operands and 96 for the copies, of 128).  One persistent pair on
 // every two SMs, tiles of x first, so that the weights that are being read are shared by all of x.  Eight warps
 // scale and add, a half of the columns each, and write through shared memory, whole rows' pieces at a time.
+// 4096 x 28672 x 4096 takes 347 us (249 at the rate for 8 bits), 4096 x 4096 x 14336 188.  A block of a 256 x 256 tile takes 737
+// cycles, its instructions 512: the sums come out of tensor memory in 16 turns of 16 columns, each met by its additions; the other
+// pairs' loads add 15 %, and the end of a tile 3500 cycles that no instruction of the next covers, for want of registers.
 constexpr int kManyParts = 2;  // warpgroups of sums, each with a part of the columns
 constexpr int kManyThreads = 128 * (1 + kManyParts);
 constexpr int kManyRegs[2] = {88, 208};  // of the first warpgroup and the others: together what the block is launched with, 3 x 168
@@ -585,7 +588,5 @@ __global__ void __launch_bounds__(kManyThreads, 1) scaled_many_kernel(const __gr
     tmem_dealloc_pair(tmem, 2 * BN);
   }
 }
-
-const void* few_kernel_for(int BT);
 
 }  // namespace qg
