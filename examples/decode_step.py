@@ -1,10 +1,13 @@
-"""Attention block of a decode step for many requests, with quantised projections.
+"""Decode step of one layer for many requests, with quantised projections.
 
 One layer's attention as a serving loop runs it: pages of the key-value cache are planned on
 the GPU, the QKV projection (quantised weights) is joined by each request's low-rank adapter,
 its rows are rotated and stored in the cache, every new token attends to its request's pages,
-and the output projection closes the block.  Prompts and single tokens go through the same
-calls; a step of single tokens is captured in a CUDA graph and replayed.
+and the output projection closes the block.  The MLP follows with projections in 8 bits: the norm
+takes up the residual and hands over codes, the gated product is quantised as it is formed; and from
+the normed last hidden state come the logits, of which each request's next token is drawn by its own
+temperature, top-k and top-p.  Prompts and single tokens go through the same calls of the attention;
+a step of single tokens is captured in a CUDA graph and replayed.
 
     python examples/decode_step.py [--requests 64] [--steps 20]
 """
@@ -100,6 +103,57 @@ class Step:
     pass
 
 
+def e4m3_blocks(w):
+    """Codes of a weight matrix and its scales, one for 128 x 128."""
+    n, k = w.shape
+    padded = torch.nn.functional.pad(w, (0, -k % 128, 0, -n % 128)).view(-(-n // 128), 128, -(-k // 128), 128)
+    scale = (padded.abs().amax((1, 3)) / 448).clamp(min=2.0 ** -126)
+    codes = (padded / scale[:, None, :, None]).view(-(-n // 128) * 128, -1)[:n, :k].contiguous()
+    return codes.to(torch.float8_e4m3fn), scale.contiguous()
+
+
+class TokenBlock:
+    """Residual, norm and gated MLP with projections in 8 bits, then the last norm, the logits and the next tokens.  `attended`
+    [rows][hidden] is what the attention adds to the residual `hidden`, which ends as the layer's output."""
+
+    def __init__(self, handle, attended, inner=14336, vocab=32000, residual=torch.bfloat16, seed=0):
+        self.h, (rows, hidden) = handle, attended.shape
+        g = torch.Generator(device="cuda").manual_seed(seed)
+
+        def weights(n, k):
+            return e4m3_blocks(torch.randn(n, k, generator=g, device="cuda") * k ** -0.5)
+
+        def norm_weight():
+            return (1 + 0.1 * torch.randn(hidden, generator=g, device="cuda")).bfloat16()
+
+        def codes_of(n):
+            return torch.empty(rows, n, dtype=torch.float8_e4m3fn, device="cuda"), torch.empty(rows, -(-n // 128), device="cuda")
+
+        self.w_up, self.w_down, self.w_head = weights(2 * inner, hidden), weights(hidden, inner), weights(vocab, hidden)
+        self.n_mlp, self.n_last = norm_weight(), norm_weight()
+        self.hidden = torch.zeros(rows, hidden, dtype=residual, device="cuda")
+        self.x, self.act, self.last = codes_of(hidden), codes_of(inner), codes_of(hidden)
+        self.gate_up = torch.empty(rows, 2 * inner, dtype=torch.bfloat16, device="cuda")
+        self.down = torch.empty(rows, hidden, dtype=torch.bfloat16, device="cuda")
+        self.logits = torch.empty(rows, vocab, dtype=torch.bfloat16, device="cuda")
+        self.u, self.temperature, self.top_p = torch.zeros(rows, device="cuda"), torch.ones(rows, device="cuda"), torch.ones(rows, device="cuda")
+        self.top_k = torch.zeros(rows, dtype=torch.int32, device="cuda")
+        self.tokens, self.logprobs = torch.empty(rows, dtype=torch.int32, device="cuda"), torch.empty(rows, device="cuda")
+        self.calls = [
+            (qgemv.run_norm, qgemv.norm_desc(attended, self.n_mlp, 1e-5, codes=self.x[0], scale=self.x[1], res=self.hidden, res_out=self.hidden)),
+            (qgemv.run_scaled, qgemv.scaled_desc(*self.x, *self.w_up, self.gate_up)),
+            (qgemv.quant_rows, qgemv.quant_desc(self.gate_up[:, :inner], *self.act, up=self.gate_up[:, inner:])),
+            (qgemv.run_scaled, qgemv.scaled_desc(*self.act, *self.w_down, self.down)),
+            (qgemv.run_norm, qgemv.norm_desc(self.down, self.n_last, 1e-5, codes=self.last[0], scale=self.last[1], res=self.hidden, res_out=self.hidden)),
+            (qgemv.run_scaled, qgemv.scaled_desc(*self.last, *self.w_head, self.logits)),
+            (qgemv.sample, qgemv.sample_desc(self.logits, self.u, self.tokens, temperature=self.temperature, top_k=self.top_k, top_p=self.top_p,
+                                             logprobs=self.logprobs))]
+
+    def run(self):
+        for call, desc in self.calls:
+            call(self.h, desc)
+
+
 def main():
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--requests", type=int, default=64)
@@ -116,10 +170,15 @@ def main():
     step = block.plan(torch.ones(args.requests, dtype=torch.int32, device="cuda"), args.requests)
     step.ids.copy_(torch.randint(-1, 8, (args.requests,), generator=g, device="cuda"))
     step.x.copy_(torch.randn(step.x.shape, generator=g, device="cuda").half())
+    token = TokenBlock(handle, step.y)
+    token.u.copy_(torch.rand(args.requests, generator=g, device="cuda"))
+    token.top_p.fill_(0.9)
     block.run(step)
+    token.run()
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         block.run(step)
+        token.run()
     begin, end = torch.cuda.Event(True), torch.cuda.Event(True)
     torch.cuda.synchronize()
     begin.record()
@@ -129,7 +188,7 @@ def main():
     torch.cuda.synchronize()
     assert qgemv.check_error(handle) == qgemv.OK
     print(f"{args.requests} requests, lengths {int(block.lens.min())} to {int(block.lens.max())}, "
-          f"{int(block.free_count)} pages free: {begin.elapsed_time(end) * 1e3 / args.steps:.1f} us per step of one attention block")
+          f"{int(block.free_count)} pages free: {begin.elapsed_time(end) * 1e3 / args.steps:.1f} us per step of one layer and the next tokens")
     handle.close()
 
 

@@ -376,6 +376,8 @@ __global__ void __launch_bounds__(kManyThreads, 1) scaled_many_kernel(const __gr
       const int m = static_cast<int>(t % x_tiles * kManyRows + rank * (kManyRows / 2)), n = static_cast<int>(t / x_tiles * BN + rank * (BN / 2));
       for (int kb = 0; kb < a.blocks; ++kb) {
         if (ok && filled) ok = mbar_wait_bounded(empty(s), ph, a.spin_ns);
+        // sums that gave up free stages early: a barrier is armed again only when what it was armed for has landed
+        if (ok && filled && rank == 0) ok = mbar_wait_bounded(full(s), ph, a.spin_ns);
         const uint32_t bar = cluster_address(full(s), 0);
         if (ok && elect_one()) {
           if (rank == 0) mbar_arrive_expect_tx(full(s), 2 * STAGE);

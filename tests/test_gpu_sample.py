@@ -232,3 +232,36 @@ def test_clusters_of_every_size_agree(h):
     for rows in (1, 10, 40, 100, 160):
         part = draw(h, x[:rows], **{a: b[:rows] for a, b in s.items()})
         assert part[0] == whole[0][:rows] and part[1] == whole[1][:rows]
+
+
+@pytest.mark.parametrize("typ", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("rows,V", [(1, 150000), (40, 60000), (310, 9000)])
+def test_large_nuclei(h, typ, rows, V):
+    """Nearly all of a row stays: more candidates than lists hold."""
+    x, g = rows_of(rows, rows, V, typ, spread=1.0, pad=1)
+    u = torch.rand(rows, generator=g).tolist()
+    n = list(range(rows))
+    check(h, x[:24], u[:24], p=[0.9 + 0.1 * (i % 7) / 7 for i in n][:24])
+    check(h, x[:24], u[:24], k=[V - 1 - 97 * i for i in n][:24], p=[0.99] * min(rows, 24), low=[1e-3 * (i % 3) for i in n][:24])
+    tokens, lp = draw(h, x, u, p=[0.97] * rows)
+    again, lp2 = draw(h, x[:24], u[:24], p=[0.97] * min(rows, 24))
+    assert tokens[:24] == again and lp[:24] == lp2
+
+
+@pytest.mark.parametrize("spread", [1e-4, 0.004, 60.0, 300.0])
+@pytest.mark.parametrize("rows,V", [(3, 20000), (310, 7000)])
+def test_bf16_values_beyond_the_table(h, spread, rows, V):
+    """Logits below 2^-8 or above 2^7 in magnitude, all of them or many, some masked."""
+    x, g = rows_of(5, rows, V, "bf16", spread=spread)
+    x[:, ::3] = -INF
+    u = torch.rand(rows, generator=g).tolist()
+    check(h, x[:12], u[:12], T=[0.5 + spread] * min(rows, 12), p=[0.5 + 0.04 * i for i in range(min(rows, 12))])
+    check(h, x[:12], u[:12], T=[0.5 + spread] * min(rows, 12))
+
+
+@pytest.mark.parametrize("typ", ["f32", "bf16"])
+def test_top_k_beyond_the_lists(h, typ):
+    x, g = rows_of(11, 6, 100000, typ)
+    u = torch.rand(6, generator=g).tolist()
+    check(h, x, u, k=[4095, 4096, 4097, 20000, 40000, 99999])
+    check(h, x, u, k=[257, 512, 2049, 5000, 33000, 70000], p=[0.5, 0.9, 0.99, 0.999, 0.8, 0.95])
