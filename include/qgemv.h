@@ -156,7 +156,9 @@ int qgemv_group_size(qgemv_format_t fmt);
  *                             qgemv_check_error) can be exercised without hanging a GPU; in
  *                             qgemv_run_gemm's tensor-core kernel, the first CTA's
  *                             dequantising threads withhold their arrival for its first stage,
- *                             so its MMA, copy and dequantising waits all run out.
+ *                             so its MMA, copy and dequantising waits all run out; in
+ *                             qgemv_run_scaled, the first CTA's (or pair's) first sums are never
+ *                             handed over.
  *   QGEMV_OPT_CTAS_PER_SM     streaming kernel CTAs per SM, 1 or 2 (default 2, used when
  *                             a row needs at most 8 warps); with 1, each CTA takes about half
  *                             an SM, so the next kernel of a programmatic-dependent-launch
@@ -551,7 +553,8 @@ qgemv_status_t qgemv_run_norm(qgemv_handle_t h, const qgemv_norm_t* norm, cudaSt
 /* e4m3 codes and scales (as above) of `rows` rows of N values h: h = x, or with up the gated product
  * h = silu(x) * up, silu(g) = g / (1 + e^-g), computed in fp32.
  *   x, up         [rows][N] of type `in`, row m at m * x_stride and m * up_stride (gate and up can be
- *                 halves of one projection's rows); up = NULL: no gate.
+ *                 halves of one projection's rows); up = NULL: no gate.  silu is right to 2^-20, and 0
+ *                 from g = -87.4 down.
  * N a multiple of 16; x, up and codes 16-byte aligned with row strides of a multiple of 16 bytes. */
 typedef struct {
   const void* x;
@@ -579,8 +582,10 @@ qgemv_status_t qgemv_quant_rows(qgemv_handle_t h, const qgemv_quant_t* quant, cu
  * Products are exact, sums in fp32, each block's sum scaled in fp32; y is rounded once.  NaN codes and
  * NaN or infinite scales reach the outputs of their rows and no others.  Deterministic.  M 0 ..
  * 2^31 - 1, N 1 .. 2^31 - 1, K a multiple of 16 up to 2^31 - 16; x, W and y 16-byte aligned, x_stride a
- * multiple of 16, the scales 4-byte aligned.  Uses the handle's workspace like qgemv_run; with QGEMV_OPT_PDL the first
- * weights are requested before the kernel before it on the stream ends, which must then not write W. */
+ * multiple of 16, the scales 4-byte aligned.  Of the handle it uses the error word alone: calls of one
+ * handle may run at once, and a wait that runs past QGEMV_OPT_SPIN_LIMIT_NS sets it.  With QGEMV_OPT_PDL
+ * the first weights are requested before the kernel before it on the stream ends (M <= 64), which must
+ * then not write W. */
 typedef struct {
   const void* x;
   const float* x_scale;

@@ -18,32 +18,44 @@ const void* few_kernel_for(int BT) {
          : BT > 16 ? reinterpret_cast<const void*>(scaled_few_kernel<32>)
                    : reinterpret_cast<const void*>(scaled_few_kernel<16>);
 }
+const void* many_kernel_for(int BN, bool join) {
+  if (join) return BN == 128 ? reinterpret_cast<const void*>(scaled_many_kernel<128, true>) : reinterpret_cast<const void*>(scaled_many_kernel<256, true>);
+  return BN == 128 ? reinterpret_cast<const void*>(scaled_many_kernel<128, false>) : reinterpret_cast<const void*>(scaled_many_kernel<256, false>);
+}
 int few_index(int BT) { return BT > 32 ? 2 : BT > 16 ? 1 : 0; }
 
 }  // namespace
 
-// How many clusters of each size run at once, asked once for a handle.  The answer counts a single CTA to an SM, as of every kernel
-// that allocates tensor memory; these take half of it at most, and two are there at a time.
+// How many clusters of each size run at once, asked once for a handle.
 bool scaled_prepare(Handle& h) {
+  auto clusters = [](const void* fn, int threads, size_t smem, int ctas) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = static_cast<unsigned>(ctas);
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess) cudaGetLastError(), n = 0;
+    return n;
+  };
+  auto prepare = [](const void* fn, size_t smem) {
+    return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) == cudaSuccess;
+  };
   for (int BT : {16, 32, 64}) {
-    if (cudaFuncSetAttribute(few_kernel_for(BT), cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(few_smem_bytes(BT))) != cudaSuccess)
-      return false;
-    for (int ks = 2; ks <= 8; ++ks) {
-      cudaLaunchConfig_t cfg = {};
-      cfg.gridDim = dim3(static_cast<unsigned>(ks), 1, 1);
-      cfg.blockDim = dim3(static_cast<unsigned>(few_threads(BT)), 1, 1);
-      cfg.dynamicSmemBytes = few_smem_bytes(BT);
-      cudaLaunchAttribute at[1];
-      at[0].id = cudaLaunchAttributeClusterDimension;
-      at[0].val.clusterDim.x = static_cast<unsigned>(ks);
-      at[0].val.clusterDim.y = 1;
-      at[0].val.clusterDim.z = 1;
-      cfg.attrs = at;
-      cfg.numAttrs = 1;
-      int n = 0;
-      if (cudaOccupancyMaxActiveClusters(&n, few_kernel_for(BT), &cfg) != cudaSuccess) cudaGetLastError(), n = 0;
-      h.scaled_clusters[few_index(BT)][ks] = 2 * n;
-    }
+    if (!prepare(few_kernel_for(BT), few_smem_bytes(BT))) return false;
+    // the answer counts a single CTA to an SM, as of every kernel that allocates tensor memory; these take half of it at most, and
+    // two are there at a time
+    for (int ks = 2; ks <= 8; ++ks) h.scaled_clusters[few_index(BT)][ks] = 2 * clusters(few_kernel_for(BT), few_threads(BT), few_smem_bytes(BT), ks);
+  }
+  for (int BN : {128, 256}) {
+    if (!prepare(many_kernel_for(BN, false), many_smem_bytes(BN)) || !prepare(many_kernel_for(BN, true), many_smem_bytes(BN))) return false;
+    for (int ks = 2; ks <= kManyMaxPairs; ++ks) h.scaled_pairs[BN / 256][ks] = clusters(many_kernel_for(BN, true), kManyThreads, many_smem_bytes(BN), 2 * ks);
   }
   return true;
 }
@@ -87,18 +99,30 @@ qgemv_status_t launch_few(const Handle& h, const qgemv_scaled_t& p, ScaledArgs a
 qgemv_status_t launch_many(const Handle& h, const qgemv_scaled_t& p, ScaledArgs a, cudaStream_t stream) {
   a.x_tiles = static_cast<int>((p.M + kManyRows - 1) / kManyRows);
   a.wide = a.blocks % 4 == 0 && p.x_scale_stride % 4 == 0 && aligned16(p.x_scale) && aligned16(p.w_scale);
-  const int64_t pairs = h.sms / 2;
-  // rounds of tiles, by the time that a block of a tile takes: one of 128 weight rows three quarters of one of 256, so that those are
-  // faster unless they leave many pairs idle in the last round
-  auto cost = [&](int BN) { return (a.x_tiles * ((p.N + BN - 1) / BN) + pairs - 1) / pairs * (BN == 128 ? 3 : 4); };
-  const int BN = cost(128) < cost(256) ? 128 : 256;
+  // What takes the least time, in units of 0.065 us: rounds of tiles, a pair to each, or fewer tiles than pairs with their blocks
+  // shared in clusters and joined.  A block of 128 weight rows takes 4 units and one of 256 6, the end of a tile 14 or 28, a join
+  // 33 or 58.  128 x 4096 x 14336: 20.8 us with 128 rows and two pairs to a tile, 33.5 with one, 24.8 with 256 rows and three
+  // pairs; 512 x 4096 x 4096: 12.9 with 128 rows alone, 16.0 with 256 and two pairs.
+  const int64_t pairs = h.sms / 2, fours = (a.blocks + 3) / 4;
+  int BN = 256;
+  double least = 0.;
+  for (int bn : {256, 128}) {
+    const int64_t tiles = a.x_tiles * ((p.N + bn - 1) / bn), block = bn == 256 ? 6 : 4, end = bn == 256 ? 28 : 14, join = bn == 256 ? 58 : 33;
+    for (int ks = 1; ks <= kManyMaxPairs; ++ks) {
+      if (ks > 1 && (tiles > h.scaled_pairs[bn / 256][ks] || fours < ks)) continue;
+      const int64_t rounds = ks > 1 ? 1 : (tiles + pairs - 1) / pairs, blocks = ks > 1 ? (fours + ks - 1) / ks * 4 : a.blocks;
+      const double cost = static_cast<double>(rounds) * static_cast<double>(blocks * block + end) + (ks > 1 ? join : 0);
+      if (least == 0. || cost < least) least = cost, BN = bn, a.ks = ks;
+    }
+  }
   CUtensorMap wmap, xmap;
   if (!encode(h, p.W, p.N, p.K, p.K, BN / 2, &wmap) || !encode(h, p.x, p.M, p.K, p.x_stride, kManyRows / 2, &xmap)) return QGEMV_ERR_CUDA;
   const int64_t tiles = a.x_tiles * ((p.N + BN - 1) / BN);
   if (tiles > 0x7fffffff) return QGEMV_ERR_BAD_SHAPE;
   void* args[] = {&wmap, &xmap, &a};
-  const void* fn = BN == 128 ? reinterpret_cast<const void*>(scaled_many_kernel<128>) : reinterpret_cast<const void*>(scaled_many_kernel<256>);
-  return launch_dependent(fn, dim3(static_cast<unsigned>(2 * std::min<int64_t>(tiles, pairs))), kManyThreads, many_smem_bytes(BN), 2, args, stream)
+  const void* fn = many_kernel_for(BN, a.ks > 1);
+  const int64_t clusters = a.ks > 1 ? tiles : std::min<int64_t>(tiles, pairs);
+  return launch_dependent(fn, dim3(static_cast<unsigned>(2 * a.ks * clusters)), kManyThreads, many_smem_bytes(BN), 2 * a.ks, args, stream)
              ? QGEMV_OK
              : QGEMV_ERR_CUDA;
 }

@@ -45,7 +45,7 @@ struct ScaledArgs {
   int64_t xs_stride, y_stride;
   int M, N, blocks;
   int x_tiles;    // many rows
-  int ks;         // few rows: CTAs of a cluster, which share a tile's blocks
+  int ks;         // CTAs (many rows: pairs) of a cluster, which share a tile's blocks
   int out;
   int* err;
   uint64_t spin_ns;
@@ -313,49 +313,77 @@ __global__ void __launch_bounds__(few_threads(BT), 2) scaled_few_kernel(const __
 // scale and add, a half of the columns each, and write through shared memory, whole rows' pieces at a time.
 // 4096 x 28672 x 4096 takes 347 us (249 at the rate for 8 bits), 4096 x 4096 x 14336 188.  A block of a 256 x 256 tile takes 737
 // cycles, its instructions 512: the sums come out of tensor memory in 16 turns of 16 columns, each met by its additions; the other
-// pairs' loads add 15 %, and the end of a tile 3500 cycles that no instruction of the next covers, for want of registers.
+// pairs' loads add 15 %, and the end of a tile 3500 cycles that no instruction of the next covers, for want of registers.  What all
+// SMs take in, 48 bytes a cycle each, is near what the L2 gives.
+// Where tiles are few, up to four pairs, a cluster, share a tile's blocks and join their sums (128 x 4096 x 14336: 20.7 us, 33.5
+// with a pair to a tile).  Sums of 128 columns are read ahead and added two to an instruction (32.8 us of 36.6 in that case with a
+// pair to a tile); of 256 that is slower (350 us to 357 of the large one), as registers are then short.
 constexpr int kManyParts = 2;  // warpgroups of sums, each with a part of the columns
 constexpr int kManyThreads = 128 * (1 + kManyParts);
 constexpr int kManyRegs[2] = {88, 208};  // of the first warpgroup and the others: together what the block is launched with, 3 x 168
 constexpr int kManyChunk = 16;  // columns that are read at a time
 constexpr int kManyRows = 256;  // rows of x of a tile
 
+constexpr int kManyMaxPairs = 4;  // of a cluster
+
 __host__ __device__ constexpr int many_stage_bytes(int BN) { return kScaledBlock * (kManyRows / 2 + BN / 2); }
 __host__ __device__ constexpr int many_stages(int BN) { return 176 * 1024 / many_stage_bytes(BN); }
 constexpr int kManyPad = 64 / kManyParts + 4;  // so that 16-byte accesses meet no bank twice
 constexpr int kManyWords = 64 / kManyParts;  // of a row that a warp stages at a time
 constexpr int kManyOutBytes = 4 * kManyParts * 32 * kManyPad * 4;
-constexpr int kManyScaleBytes = 4 * 2 * 128 * 4;  // four blocks' products of the scales of 128 rows of x and up to two of W
+constexpr int kManyScaleBytes = 8 * 128 * 4;  // products of the scales of 128 rows of x and one of W, or two, of eight blocks or four
 __host__ __device__ constexpr size_t many_smem_bytes(int BN) {
   return 1024 + static_cast<size_t>(many_stages(BN)) * many_stage_bytes(BN) + 256 + kManyOutBytes + kManyScaleBytes;
 }
 
-template <int BN>
+// a0 += d0 f, a1 += d1 f in one instruction.
+__device__ __forceinline__ void fma_pair(float& a0, float& a1, uint32_t d0, uint32_t d1, float f) {
+  asm("{\n\t.reg .b64 a, d, q;\n\t"
+      "mov.b64 a, {%0, %1};\n\tmov.b64 d, {%2, %3};\n\tmov.b64 q, {%4, %4};\n\t"
+      "fma.rn.f32x2 a, d, q, a;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(a0), "+f"(a1)
+      : "r"(d0), "r"(d1), "f"(f));
+}
+__device__ __forceinline__ float4 remote_v4(uint32_t at, uint32_t rank) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(cluster_address(at, rank)) : "memory");
+  return v;
+}
+
+template <int BN, bool JOIN>  // JOIN: ks > 1
 __global__ void __launch_bounds__(kManyThreads, 1) scaled_many_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
                                                                       const __grid_constant__ ScaledArgs a) {
-  constexpr int S = many_stages(BN), STAGE = many_stage_bytes(BN), XBYTES = kScaledBlock * kManyRows / 2, HB = BN / kManyParts;
+  constexpr bool kAhead = BN == 128;
+  constexpr int NB = 512 / BN, SLOTS = 2 * NB, SLOT = BN / kScaledRows * 128 * 4;  // sets of sums that fill tensor memory; slots of products
+  constexpr int S = many_stages(BN), kJoinPad = BN + 4, STAGE = many_stage_bytes(BN), XBYTES = kScaledBlock * kManyRows / 2, HB = BN / kManyParts;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t bars = base + S * STAGE;
   auto full = [&](int s) { return bars + 8u * s; };             // of the pair's first CTA: both CTAs' copies have landed
   auto empty = [&](int s) { return bars + 8u * (S + s); };      // the MMAs that read the stage are complete
   auto tfull = [&](int b) { return bars + 8u * (2 * S + b); };  // a block's sums are in TMEM and its scales' products in shared memory
-  auto tempty = [&](int b) { return bars + 8u * (2 * S + 2 + b); };  // of the first CTA: both CTAs have read them
-  const uint32_t done = bars + 8u * (2 * S + 4), tslot = done + 8;
-  static_assert(8 * (2 * S + 4) + 8 + 8 <= 256, "barriers");
-  const uint32_t prod = bars + 256 + kManyOutBytes;  // [block % 4][128 rows of W][row of x]
+  auto tempty = [&](int b) { return bars + 8u * (2 * S + NB + b); };  // of the first CTA: both CTAs have read them
+  const uint32_t done = bars + 8u * (2 * S + 2 * NB), tslot = done + 8;
+  static_assert(SLOTS * SLOT <= kManyScaleBytes && 8 * (2 * S + 2 * NB) + 8 + 8 <= 256, "barriers");
+  static_assert(kManyRows / 2 * kJoinPad * 4 <= S * STAGE, "a tile's sums take the place of the stages");
+  const uint32_t prod = bars + 256 + kManyOutBytes;  // [block % SLOTS][128 rows of W][row of x]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const unsigned rank = blockIdx.x & 1, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  // JOIN: a cluster has one tile, and pair kp of it the blocks kb0 .. kb1 (whole fours, as their scales are read)
+  const unsigned ks = JOIN ? static_cast<unsigned>(a.ks) : 1u, rank = blockIdx.x & 1, kp = JOIN ? (blockIdx.x >> 1) % ks : 0, lead = 2 * kp;
+  const unsigned pair = (blockIdx.x >> 1) / ks, pairs = (gridDim.x >> 1) / ks;
+  const int fours = (a.blocks + 3) / 4;
+  const int kb0 = JOIN ? static_cast<int>(static_cast<unsigned>(fours) * kp / ks) * 4 : 0;
+  const int kb1 = JOIN ? min(a.blocks, static_cast<int>(static_cast<unsigned>(fours) * (kp + 1) / ks) * 4) : a.blocks;
   const unsigned x_tiles = static_cast<unsigned>(a.x_tiles), tiles = x_tiles * ((static_cast<unsigned>(a.N) + BN - 1) / BN);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) mbar_init(full(s), 1), mbar_init(empty(s), 1);
-    for (int b = 0; b < 2; ++b) mbar_init(tfull(b), 3), mbar_init(tempty(b), 2 * 4 * kManyParts);
+    for (int b = 0; b < NB; ++b) mbar_init(tfull(b), 3), mbar_init(tempty(b), 2 * 4 * kManyParts);
     mbar_init(done, 1);
     fence_mbar_init();
   }
   if (warp == 1) {
-    tmem_alloc_pair(tslot, 2 * BN);
+    tmem_alloc_pair(tslot, NB * BN);
     tmem_relinquish_pair();
   }
   tc_fence_before();
@@ -374,11 +402,11 @@ __global__ void __launch_bounds__(kManyThreads, 1) scaled_many_kernel(const __gr
     bool filled = false;  // every stage has been used
     for (unsigned t = pair; t < tiles; t += pairs) {
       const int m = static_cast<int>(t % x_tiles * kManyRows + rank * (kManyRows / 2)), n = static_cast<int>(t / x_tiles * BN + rank * (BN / 2));
-      for (int kb = 0; kb < a.blocks; ++kb) {
+      for (int kb = kb0; kb < kb1; ++kb) {
         if (ok && filled) ok = mbar_wait_bounded(empty(s), ph, a.spin_ns);
         // sums that gave up free stages early: a barrier is armed again only when what it was armed for has landed
         if (ok && filled && rank == 0) ok = mbar_wait_bounded(full(s), ph, a.spin_ns);
-        const uint32_t bar = cluster_address(full(s), 0);
+        const uint32_t bar = cluster_address(full(s), lead);
         if (ok && elect_one()) {
           if (rank == 0) mbar_arrive_expect_tx(full(s), 2 * STAGE);
           tma_load_2d_pair(base + s * STAGE, &xmap, kb * kScaledBlock, m, bar);
@@ -393,10 +421,10 @@ __global__ void __launch_bounds__(kManyThreads, 1) scaled_many_kernel(const __gr
       const uint64_t d0 = tc_desc_sw128(base);
       int s = 0, b = 0;
       uint32_t ph = 0, tph = 1;
-      bool used = false;    // both buffers have been
+      bool used = false;     // all sets have been
       bool is_full = false;  // asked while the block before is being issued
       for (unsigned t = pair; t < tiles; t += pairs) {
-        for (int kb = 0; kb < a.blocks; ++kb) {
+        for (int kb = kb0; kb < kb1; ++kb) {
           if (ok && used) ok = mbar_wait_bounded(tempty(b), tph, a.spin_ns);
           if (ok && !is_full) ok = mbar_wait_bounded(full(s), ph, a.spin_ns);
           tc_fence_after();
@@ -404,14 +432,14 @@ __global__ void __launch_bounds__(kManyThreads, 1) scaled_many_kernel(const __gr
           if (elect_one()) {
 #pragma unroll
             for (int k = 0; k < kScaledBlock / 32; ++k) tc_mma_f8_pair(tmem + b * BN, xd + 2 * k, wd + 2 * k, idesc, k > 0);
-            if (!(a.stall && pair == 0 && t == pair && kb == 0)) tc_commit_pair(tfull(b));
+            if (!(a.stall && blockIdx.x == 0 && t == pair && kb == kb0)) tc_commit_pair(tfull(b), lead);
           }
           if (++s == S) s = 0, ph ^= 1;
-          if ((b ^= 1) == 0) tph ^= 1, used = true;
+          if (++b == NB) b = 0, tph ^= 1, used = true;
           is_full = mbar_test(full(s), ph);
         }
       }
-      if (elect_one()) tc_commit_pair(done);  // nobody leaves while MMAs run
+      if (elect_one()) tc_commit_pair(done, lead);  // nobody leaves while MMAs run
     }
   } else if (warp < 4) {
     // ---- products of scales: two rows of x a lane.  The scales of four blocks are read while the four before them are used (rows
@@ -430,7 +458,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) scaled_many_kernel(const __gr
           f[0] = q.x, f[1] = q.y, f[2] = q.z, f[3] = q.w;
         } else {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) f[q] = in && kb + q < a.blocks ? __ldg(at + q) : 0.f;
+          for (int q = 0; q < 4; ++q) f[q] = in && kb + q < kb1 ? __ldg(at + q) : 0.f;
         }
       };
 #pragma unroll
@@ -439,23 +467,23 @@ __global__ void __launch_bounds__(kManyThreads, 1) scaled_many_kernel(const __gr
       for (int j = 0; j < WB; ++j) four(a.ws + (wrow + j) * a.blocks + kb, t < tiles && (wrow + j) * kScaledRows < a.N, v.w[j]);
       return v;
     };
-    // The products of a block go out when the sums of the one two before it are known to be there: its MMAs began when the sums
-    // of the block before that in the same place, and with them the products, had been read.
+    // The products of a block go out when the sums of the one before it in the same place are known to be there: its MMAs began
+    // when the sums of the block before that, and with them the products, had been read.
     int b = 0, slot = 0;
     uint32_t ph = 1;
     bool used = false;
-    Four next = fetch(pair, 0);
+    Four next = fetch(pair, kb0);
     for (unsigned t = pair; t < tiles; t += pairs) {
-      for (int kb = 0; kb < a.blocks; kb += 4) {
+      for (int kb = kb0; kb < kb1; kb += 4) {
         const Four now = next;
-        const bool last = kb + 4 >= a.blocks;
-        next = fetch(last ? t + pairs : t, last ? 0 : kb + 4);
+        const bool last = kb + 4 >= kb1;
+        next = fetch(last ? t + pairs : t, last ? kb0 : kb + 4);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          if (kb + q >= a.blocks) break;
+          if (kb + q >= kb1) break;
           if (ok && used) ok = mbar_wait_bounded(tfull(b), ph, a.spin_ns);
-          const uint32_t to = prod + slot * (2 * 128 * 4) + r * 4;
-          slot = (slot + 1) & 3;
+          const uint32_t to = prod + slot * SLOT + r * 4;
+          slot = (slot + 1) % SLOTS;
 #pragma unroll
           for (int w = 0; w < WB; ++w)
 #pragma unroll
@@ -463,7 +491,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) scaled_many_kernel(const __gr
               asm volatile("st.shared.f32 [%0], %1;" ::"r"(to + (w * 128 + j * 64) * 4), "f"(now.x[j][q] * now.w[w][q]) : "memory");
           __syncwarp();
           if (elect_one()) mbar_arrive(tfull(b));
-          if ((b ^= 1) == 0) ph ^= 1, used = true;
+          if (++b == NB) b = 0, ph ^= 1, used = true;
         }
       }
     }
@@ -474,7 +502,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) scaled_many_kernel(const __gr
     const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * q4) << 16) + hh * HB;
     const uint32_t out = bars + 256 + (warp - 4) * (32 * kManyPad * 4);
     const uint32_t mine_f = prod + ((hh * HB) / kScaledRows * 128 + r) * 4;
-    const uint32_t tempty_at = cluster_address(tempty(0), 0);  // of the second buffer 8 bytes behind
+    const uint32_t tempty_at = cluster_address(tempty(0), lead);  // of the next set 8 bytes behind
     float acc[HB];
     int b = 0, s = 0, slot = 0;
     uint32_t tph = 0;
@@ -482,18 +510,25 @@ __global__ void __launch_bounds__(kManyThreads, 1) scaled_many_kernel(const __gr
 #pragma unroll
       for (int c = 0; c < HB; ++c) acc[c] = 0.f;
 #pragma unroll 1
-      for (int kb = 0; kb < a.blocks; ++kb) {
+      for (int kb = kb0; kb < kb1; ++kb) {
         // a warp that gave up goes on without waiting: the other CTA counts on it
         if (ok) ok = mbar_wait_bounded(tfull(b), tph, a.spin_ns);
         tc_fence_after();
         const uint32_t from = lanes + b * BN;
-        const float f = __uint_as_float(lds_u32(mine_f + slot * (2 * 128 * 4)));
-        slot = (slot + 1) & 3;
+        const float f = __uint_as_float(lds_u32(mine_f + slot * SLOT));
+        slot = (slot + 1) % SLOTS;
         constexpr int CH = kManyChunk, NC = HB / CH;
-        uint32_t d[CH];
+        uint32_t d[kAhead ? 2 : 1][CH];
+        if (kAhead) tmem_ld16(from, d[0]);
 #pragma unroll
         for (int k = 0; k < NC; ++k) {
-          tmem_ld_now(from + k * CH, d);
+          uint32_t(&v)[CH] = d[kAhead ? k & 1 : 0];
+          if constexpr (kAhead) {
+            tmem_ld_arrived(v);
+            if (k + 1 < NC) tmem_ld16(from + (k + 1) * CH, d[(k + 1) & 1]);
+          } else {
+            tmem_ld_now(from + k * CH, v);
+          }
           if (k + 1 == NC) {
             tc_fence_before();
             __syncwarp();
@@ -504,15 +539,70 @@ __global__ void __launch_bounds__(kManyThreads, 1) scaled_many_kernel(const __gr
             if (++s == S) s = 0;
           }
 #pragma unroll
-          for (int j = 0; j < CH; ++j) acc[k * CH + j] = fmaf(__uint_as_float(d[j]), f, acc[k * CH + j]);
+          for (int j = 0; j < CH; j += 2) {
+            if constexpr (kAhead) {
+              fma_pair(acc[k * CH + j], acc[k * CH + j + 1], v[j], v[j + 1], f);
+            } else {
+              acc[k * CH + j] = fmaf(__uint_as_float(v[j]), f, acc[k * CH + j]);
+              acc[k * CH + j + 1] = fmaf(__uint_as_float(v[j + 1]), f, acc[k * CH + j + 1]);
+            }
+          }
         }
-        if ((b ^= 1) == 0) tph ^= 1;
+        if (++b == NB) b = 0, tph ^= 1;
       }
       // ---- the tile: 32 rows x kManyWords words at a time through shared memory, then a row's words by neighbouring lanes, four
       // each where rows of y are whole 16 bytes apart
       const int64_t row0 = static_cast<int64_t>(t % x_tiles) * kManyRows + rank * (kManyRows / 2) + 32 * q4, col0 = static_cast<int64_t>(t / x_tiles) * BN + hh * HB;
       const int cols = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(HB), a.N - col0)));
       const int rows = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(32), a.M - row0)));
+      if constexpr (JOIN) {
+        // the blocks' stages have been read: these sums take their place, and each pair adds its share of the tile's rows, over the
+        // pairs in their order, four columns a thread
+#pragma unroll
+        for (int c = 0; c < HB; c += 4)
+          if (lane < rows)
+            asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(base + (r * kJoinPad + hh * HB + c) * 4), "f"(acc[c]), "f"(acc[c + 1]), "f"(acc[c + 2]),
+                         "f"(acc[c + 3])
+                         : "memory");
+        scaled_cluster_meet();
+        const int64_t m0 = static_cast<int64_t>(t % x_tiles) * kManyRows + rank * (kManyRows / 2), n0 = static_cast<int64_t>(t / x_tiles) * BN;
+        const int all = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(kManyRows / 2), a.M - m0))) * (BN / 4);
+        const int e1 = static_cast<int>(static_cast<unsigned>(all) * (kp + 1) / ks);
+        constexpr int kStep = 128 * kManyParts, U = 2;  // U pieces' reads are in flight together
+        for (int e0 = static_cast<int>(static_cast<unsigned>(all) * kp / ks) + static_cast<int>(threadIdx.x) - 128; e0 < e1; e0 += U * kStep) {
+          float4 v[U][kManyMaxPairs];
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const int e = min(e0 + u * kStep, e1 - 1);
+#pragma unroll
+            for (unsigned q = 0; q < kManyMaxPairs; ++q)
+              v[u][q] = q < ks ? remote_v4(base + (e / (BN / 4) * kJoinPad + e % (BN / 4) * 4) * 4, 2 * q + rank) : make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const int e = e0 + u * kStep, row = e / (BN / 4), c = e % (BN / 4) * 4;
+            if (e >= e1) break;
+            float4 sum = v[u][0];
+#pragma unroll
+            for (int q = 1; q < kManyMaxPairs; ++q) sum.x += v[u][q].x, sum.y += v[u][q].y, sum.z += v[u][q].z, sum.w += v[u][q].w;
+            const int64_t to = (m0 + row) * a.y_stride + n0 + c;
+            const float f4[4] = {sum.x, sum.y, sum.z, sum.w};
+            if (a.y_stride % 4 == 0 && n0 + c + 4 <= a.N) {
+              if (a.out == QGEMV_OUT_F32) {
+                *reinterpret_cast<float4*>(static_cast<float*>(a.y) + to) = sum;
+              } else {
+                const bool bf = a.out == QGEMV_OUT_BF16;
+                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + to) =
+                    make_uint2(bf ? pair16<true>(f4[0], f4[1]) : pair16<false>(f4[0], f4[1]), bf ? pair16<true>(f4[2], f4[3]) : pair16<false>(f4[2], f4[3]));
+              }
+            } else {
+              for (int j = 0; j < 4; ++j)
+                if (n0 + c + j < a.N) scaled_store(a.y, to + j, a.out, f4[j]);
+            }
+          }
+        }
+        break;
+      }
       auto flush = [&](int c, int n) {  // columns c .. of this part, n of them in a word
         constexpr int L = kManyWords / 4;  // lanes of a row
         __syncwarp();
@@ -574,6 +664,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) scaled_many_kernel(const __gr
     }
   }
   __syncwarp();
+  if (JOIN && warp < 4) scaled_cluster_meet();  // with the sums' threads
   if (!mbar_wait_bounded(done, 0, kDrainNs)) ok = false;
   if (!ok) {
     atomicOr(a.err, kDevErrTimeout);
@@ -587,7 +678,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) scaled_many_kernel(const __gr
   scaled_cluster_meet();  // nobody leaves while the other CTA's arrivals are on their way
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc_pair(tmem, 2 * BN);
+    tmem_dealloc_pair(tmem, NB * BN);
   }
 }
 

@@ -28,6 +28,7 @@ struct Handle {
   void* encode_tiled = nullptr;              // the driver's cuTensorMapEncodeTiled (null: no TMA path)
   int tc_cluster_max[3] = {1, 1, 1};         // largest cluster (K splits) the GEMM kernels can run [BT 64/128/256]
   int scaled_clusters[3][9] = {};            // clusters of the 8-bit projection that run at once [BT 16/32/64][CTAs of one]
+  int scaled_pairs[2][5] = {};               // of it for many rows [BN 128/256][pairs of one]
   int force_path = 0;
   int ring_depth = 0;
   int rows_per_stage = 0;

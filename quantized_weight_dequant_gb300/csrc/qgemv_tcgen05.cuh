@@ -93,10 +93,11 @@ __device__ __forceinline__ void tc_mma_f8_pair(uint32_t d_tmem, uint64_t adesc, 
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc)
       : "memory");
 }
-// One arrival at the barrier at `bar` of both CTAs once every MMA this thread issued before has completed.
-__device__ __forceinline__ void tc_commit_pair(uint32_t bar) {
+// One arrival at the barrier at `bar` of both CTAs, of cluster ranks `first` and first + 1, once every MMA this thread issued before
+// has completed.
+__device__ __forceinline__ void tc_commit_pair(uint32_t bar, uint32_t first) {
   asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-               "h"(static_cast<uint16_t>(3))
+               "h"(static_cast<uint16_t>(3u << first))
                : "memory");
 }
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t slot_sa, uint32_t ncols) {
