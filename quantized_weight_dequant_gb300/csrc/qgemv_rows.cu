@@ -55,9 +55,9 @@ qgemv_status_t qgemv_run_norm(qgemv_handle_t hh, const qgemv_norm_t* norm, cudaS
     return QGEMV_ERR_MISALIGNED;
   if (p.rows == 0) return QGEMV_OK;
   // Up to 512 elements a warp has a row, and 64 warps an SM; more: a CTA (2048 elements, 8191 rows: 24.6 us, with a warp
-  // for each 35).  Many rows: a thread has two pieces of its row and a CTA goes on to the row 1024 threads an SM on, whose
-  // elements it reads before it finishes the first (4096 elements: 44.8 us, 57.5 with one piece, 68.4 with four; 14336:
-  // 158, with a CTA for each row 217).  Few rows: as many threads as there are pieces.
+  // for each 35).  Many rows: a thread has two pieces of its row or more and a CTA goes on to the row 1024 threads an SM on, whose
+  // elements it reads before it finishes the first (4096 elements: 44.8 us, 57.5 with one piece, 68.4 with four; 14336: 158,
+  // with a CTA for each row 217; all before the pieces were put side by side).  Few rows: as many threads as there are pieces.
   const int vecs = static_cast<int>(p.N / 8);
   const bool warp = vecs <= 64;
   int v = 1;

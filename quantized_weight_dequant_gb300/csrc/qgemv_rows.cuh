@@ -45,26 +45,33 @@ __device__ __forceinline__ void store_elems(void* row, int64_t at, int type, con
   }
 }
 
-// Codes of this lane's eight elements, and their group's scale from its first lane.  All 32 lanes come here together;
-// lanes past the row's end bring zeros.
-__device__ __forceinline__ void store_codes(float (&f)[8], bool in, int first, uint8_t* codes, float* scale) {
-  float top = 0.f;  // NaN where one of them is
+// Codes of this lane's P times eight elements, which are neighbours, and their group's scale from its first lane.  All 32 lanes come
+// here together; `in`: the row has them.
+template <int P>
+__device__ __forceinline__ void store_codes(float (*f)[8], bool in, int first, uint8_t* codes, float* scale) {
+  constexpr int L = kGroupLanes / P;  // lanes of a group
+  float top = 0.f;                    // NaN where one of them is
 #pragma unroll
-  for (int j = 0; j < 8; ++j) top = max_abs_nan(top, f[j]);
-  top = fabsf(top);
+  for (int j = 0; j < 8 * P; ++j) top = max_abs_nan(top, f[j / 8][j % 8]);
+  top = in ? fabsf(top) : 0.f;
 #pragma unroll
-  for (int k = kGroupLanes / 2; k > 0; k >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, k));
+  for (int k = L / 2; k > 0; k >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, k));
   const float s = e4m3_scale(top);
-  const uint2 c = e4m3_codes(f, top, s);
   if (!in) return;
-  *reinterpret_cast<uint2*>(codes + first) = c;
+  const uint2 c = e4m3_codes(f[0], top, s);
+  if constexpr (P == 1) {
+    *reinterpret_cast<uint2*>(codes + first) = c;
+  } else {
+    const uint2 d = e4m3_codes(f[1], top, s);
+    *reinterpret_cast<uint4*>(codes + first) = make_uint4(c.x, c.y, d.x, d.y);
+  }
   if (first % (8 * kGroupLanes) == 0) scale[first / (8 * kGroupLanes)] = s;
 }
 
 // y = s / sqrt(mean(s^2) + eps) * (offset + weight), s = x + res.  A row is held in registers, V times eight elements a
 // thread, by one warp (kNormWarps rows in a CTA) or by a whole CTA, so that every byte is read once and the norm of a row
-// may overwrite it.  Memory bounds it: 8191 rows of 4096 in bf16 with the sum written back and codes, 235 MB, take 44.8 us
-// (5.2 TB/s); 8191 of 2048 24.6; 64 of 4096 2.9 and one row 2.7, which is the launch and one trip to memory.
+// may overwrite it.  Memory bounds it: 8191 rows of 4096 in bf16 with the sum written back and codes, 235 MB, take 42.1 us
+// (5.6 TB/s); 8191 of 2048 21.9; 64 of 4096 2.9 and one row 2.7, which is the launch and one trip to memory.
 constexpr int kNormWarps = 4;  // rows of a CTA where a warp has a row
 
 template <bool WIDE, int RES, int V, bool WARP>  // RES: 0 none, 1 of 16 bits, 2 fp32
@@ -74,6 +81,10 @@ __global__ void __launch_bounds__(WARP ? 32 * kNormWarps : 1024) norm_kernel(con
   const int64_t step = WARP ? static_cast<int64_t>(gridDim.x) * kNormWarps : gridDim.x;
   int64_t m = WARP ? static_cast<int64_t>(blockIdx.x) * kNormWarps + threadIdx.x / 32 : blockIdx.x;
   constexpr int kEl = WIDE ? 4 : 2, kResEl = RES == 2 ? 4 : 2;
+  // pieces of eight side by side, whose group's scale is worked out once (8191 x 4096 42.1 us for 44.8; of fp32 rows, 64 bytes apart
+  // then, 91 for 83)
+  constexpr int P = V == 1 || WIDE || RES == 2 ? 1 : 2;
+  auto place = [&](int j) { return ((j / P * threads + tid) * P + j % P) * 8; };
   Elems8<WIDE> a[V];
   Elems8<RES == 2> b[RES ? V : 1];
   auto read = [&] {
@@ -81,7 +92,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kNormWarps : 1024) norm_kernel(con
     const uint8_t* res = static_cast<const uint8_t*>(p.res) + m * p.res_stride * kResEl;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const int at = (tid + j * threads) * 8;
+      const int at = place(j);
       if (at < p.N) {
         a[j] = load_elems<WIDE>(x, at);
         if constexpr (RES != 0) b[j] = load_elems<RES == 2>(res, at);
@@ -98,7 +109,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kNormWarps : 1024) norm_kernel(con
     float sum = 0.f;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const int at = (tid + j * threads) * 8;
+      const int at = place(j);
       if (at < p.N) {
         elems_float<WIDE>(a[j], p.in, s[j]);
         if constexpr (RES != 0) {
@@ -130,7 +141,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kNormWarps : 1024) norm_kernel(con
     uint8_t* codes = p.codes ? static_cast<uint8_t*>(p.codes) + row * p.codes_stride : nullptr;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const int at = (tid + j * threads) * 8;
+      const int at = place(j);
       const bool in = at < p.N;
       if (in && res_out) store_elems(res_out, at, p.res_type, s[j]);
       if (p.weight) {
@@ -142,13 +153,14 @@ __global__ void __launch_bounds__(WARP ? 32 * kNormWarps : 1024) norm_kernel(con
             elems_float<false>(load_elems<false>(p.weight, at), p.weight_type, w);
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s[j][i] = in ? s[j][i] * by * (p.offset + w[i]) : 0.f;
+        for (int i = 0; i < 8; ++i) s[j][i] = s[j][i] * by * (p.offset + w[i]);
       } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s[j][i] = in ? s[j][i] * by : 0.f;
+        for (int i = 0; i < 8; ++i) s[j][i] = s[j][i] * by;
       }
       if (in && y) store_elems(y, at, p.out, s[j]);
-      if (codes) store_codes(s[j], in, at, codes, p.scale + row * p.scale_stride);
+      // (codes come in whole sixteens: both pieces are in the row or neither)
+      if (codes && j % P == P - 1) store_codes<P>(&s[j + 1 - P], in, place(j + 1 - P), codes, p.scale + row * p.scale_stride);
     }
   } while (m < p.rows);
 }
@@ -165,11 +177,10 @@ __device__ __forceinline__ float silu(float g) {
 }
 
 // Codes of rows: a scale top / 448 and quotients per 128.  A thread has 16 elements, an eighth of a group, so that the group's scale is worked out for 16 at a
-// time, and a CTA 2048 of its row.  Instructions bound it next to memory: 8191 rows of 4096 in bf16 take 18.8 us (15.0 at
+// time, and a CTA 2048 of its row.  Instructions bound it next to memory: 8191 rows of 4096 in bf16 take 18.9 us (15.0 at
 // the copy's rate; with eight elements a thread, and the finite and the infinite case chosen per element, 22.3), the gated
-// product of 14336 113 (86; with expf and a division 144), 64 rows of it 2.9, one of 4096 1.6.
+// product of 14336 114 (86; with expf and a division 144), 64 rows of it 2.9, one of 4096 1.6.
 constexpr int kQuantThreads = 128;
-constexpr int kQuantLanes = 8;  // of a group
 
 template <bool WIDE, bool GATED>
 __global__ void __launch_bounds__(kQuantThreads) quant_kernel(const __grid_constant__ qgemv_quant_t p, int chunks) {
@@ -199,17 +210,7 @@ __global__ void __launch_bounds__(kQuantThreads) quant_kernel(const __grid_const
         }
       }
     }
-    float top = 0.f;
-#pragma unroll
-    for (int j = 0; j < 16; ++j) top = max_abs_nan(top, f[j / 8][j % 8]);
-    top = fabsf(top);
-#pragma unroll
-    for (int k = kQuantLanes / 2; k > 0; k >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, k));
-    const float s = e4m3_scale(top);
-    if (!in) continue;
-    const uint2 lo = e4m3_codes(f[0], top, s), hi = e4m3_codes(f[1], top, s);
-    *reinterpret_cast<uint4*>(codes + at) = make_uint4(lo.x, lo.y, hi.x, hi.y);
-    if (threadIdx.x % kQuantLanes == 0) scale[at / (8 * kGroupLanes)] = s;
+    store_codes<2>(f, in, at, codes, scale);
   }
 }
 
