@@ -92,11 +92,12 @@ qgemv_status_t qgemv_quant_rows(qgemv_handle_t hh, const qgemv_quant_t* quant, c
   if (!aligned16(p.x) || !aligned16(p.up) || !aligned16(p.codes) || p.x_stride * el % 16 || (p.up && p.up_stride * el % 16) ||
       p.codes_stride % 16 || reinterpret_cast<uintptr_t>(p.scale) % 4)
     return QGEMV_ERR_MISALIGNED;
+  int chunks = static_cast<int>((p.N + 16 * kQuantThreads - 1) / (16 * kQuantThreads));
+  if (p.rows * chunks > 0x7fffffff) return QGEMV_ERR_BAD_SHAPE;
   if (p.rows == 0) return QGEMV_OK;
   const bool wide = p.in == QGEMV_OUT_F32;
   const void* fn = p.up ? (wide ? reinterpret_cast<const void*>(quant_kernel<true, true>) : reinterpret_cast<const void*>(quant_kernel<false, true>))
                         : (wide ? reinterpret_cast<const void*>(quant_kernel<true, false>) : reinterpret_cast<const void*>(quant_kernel<false, false>));
-  int chunks = (p.N + 16 * kQuantThreads - 1) / (16 * kQuantThreads);
   void* args[] = {const_cast<qgemv_quant_t*>(&p), &chunks};
   return launch_dependent(fn, dim3(static_cast<unsigned>(p.rows), std::min(chunks, 65535)), kQuantThreads, 0, 1, args, stream) ? QGEMV_OK : QGEMV_ERR_CUDA;
 }

@@ -14,6 +14,11 @@
 //    matter; coarser behind 2^-32): monotone in the logit, so its buckets are ranges of the order.  The
 //    bucket with the border is then divided by the logits' bits, 2048 ways at a time, until the border falls between two
 //    ranges or within one value, whose equals are counted by index.
+//  * What takes part after a cut is listed, so that it is found once: in the cluster's first CTA where it holds all, in every CTA's own
+//    list, or, of more, the border's bucket alone.  (Going over the rows every time: 64 rows of 128000 fp32 with mixed settings
+//    136 us, with lists 67; 509 of 50001 in bf16 with top-p 376 and 157.)
+//  * Instructions and shared memory's adds bound the passes with weights, the meetings of a cluster the rest: one row of 32000
+//    takes 14.6 us, of which the logits' bytes are nothing; 64 rows of 128000 without limits 36 (4.8 at the copy's rate).
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
