@@ -349,3 +349,40 @@ def test_rows_far_apart(h, op):
         torch.cuda.synchronize()
         got.append((codes.view(torch.uint8), scale))
     assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
+@pytest.mark.parametrize("rows,N", [(3000, 4096), (1301, 2048), (25000, 256), (1300, 20480)])
+def test_norm_of_many_rows_in_place(h, rows, N):
+    """CTAs that go on to further rows read those before they have written the first."""
+    g = gen(rows)
+    x, res, w = randn(g, rows, N).bfloat16(), randn(g, rows, N).bfloat16(), randn(g, N)
+    out = [torch.empty_like(x), torch.empty_like(res), torch.empty(rows, N, dtype=F8, device="cuda"), torch.empty(rows, N // 128, device="cuda")]
+    qgemv.run_norm(h, qgemv.norm_desc(x, w, 1e-6, y=out[0], codes=out[2], scale=out[3], res=res, res_out=out[1]))
+    codes, scale = torch.empty_like(out[2]), torch.empty_like(out[3])
+    qgemv.run_norm(h, qgemv.norm_desc(x, w, 1e-6, y=x, codes=codes, scale=scale, res=res, res_out=res))
+    torch.cuda.synchronize()
+    assert torch.equal(x, out[0]) and torch.equal(res, out[1]) and torch.equal(scale, out[3])
+    assert torch.equal(codes.view(torch.uint8), out[2].view(torch.uint8))
+
+
+def test_gated_ends(h):
+    """Gates from where the exponential ends to the infinities; NaN, infinite and large partners."""
+    gate = torch.tensor([-87.0, -86.5, -80.0, -30.0, -1e-30, 0.0, 1e-30, 30.0, 88.0, 89.0, 200.0, 1e30, -50.0, -60.0, -70.0, -75.0], device="cuda")
+    up = torch.tensor([1e30, 1e33, -1e30, 1e9, 1e30, 5.0, 1e30, -1.0, 1.0, 1.0, -1.0, 1.0, 1e20, 1e22, 1e25, -1e28], device="cuda")
+    rows = torch.zeros(16, 128, device="cuda")  # a value to a row, and its scale with it
+    rows[:, 0] = gate
+    ups = torch.zeros(16, 128, device="cuda")
+    ups[:, 0] = up
+    codes, scale = quantise(h, rows, ups)
+    ref = torch.zeros(16, 128, dtype=torch.float64, device="cuda")
+    ref[:, 0] = gate.double() / (1 + torch.exp(-gate.double())) * up.double()
+    check_codes(codes, scale, ref, 2.0 ** -20, "gated ends")
+    rows[:, 0] = torch.tensor([INF, -INF, NAN, -88.0, -100.0, -3e38, INF, 1.0, 1.0] + [0.0] * 7, device="cuda")
+    ups[:, 0] = torch.tensor([2.0, 1.0, 1.0, 1.0, 1.0, 1.0, 0.0, INF, NAN] + [0.0] * 7, device="cuda")
+    codes, _ = quantise(h, rows, ups)
+    c = codes.view(F8).float()[:, 0]
+    assert c[0] == 448 and c[7] == 448 and c[[1, 2, 6, 8]].isnan().all() and (c[3:6] == 0).all()
+    # every gate from where the exponential passes the largest number: 0 times a finite partner
+    far = -torch.linspace(88, 1000, 128 * 512, device="cuda").reshape(512, 128)
+    codes, scale = quantise(h, far, torch.ones_like(far))
+    assert (codes.view(F8).float() == 0).all() and (scale == 1).all()
