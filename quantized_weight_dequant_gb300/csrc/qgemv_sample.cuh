@@ -257,15 +257,15 @@ __device__ __forceinline__ int bucket_of(float l, const RowScale& r) {
 }
 
 // The tokens that stay, a beginning of the order: those of smaller buckets, and of `bucket` those of smaller keys and of `key`
-// the indexes up to `index`.  Logits from `sure` on are of smaller buckets, those up to `never` of larger ones: few need more than
-// two comparisons.
+// the indexes up to `index`.  Logits from `sure` on are of smaller buckets (NaN: none is known to be), those up to `never` of larger
+// ones: few need more than two comparisons.
 struct Cut {
   int bucket;
   uint32_t key, index;
   float sure, never;
 };
 __device__ __forceinline__ Cut cut_in(int bucket, const RowScale& r) {
-  Cut c{bucket, 0xffffffffu, 0xffffffffu, kInf, -kInf};
+  Cut c{bucket, 0xffffffffu, 0xffffffffu, __int_as_float(0x7fffffff), -kInf};
   auto z_at = [](int b) { return b <= 1800 ? (static_cast<float>(b) - 0.5f) / 40.f : __int_as_float(__float_as_int(45.f) + ((b - 1801) << 19)); };
   const float wide = 1e-5f * fabsf(r.m);
   // buckets are monotone in the logit: a logit of a smaller bucket proves it of all larger ones
@@ -598,7 +598,7 @@ struct SampleRow {
     settle();
     each_of([&](float l) { return l > c.never; },
             [&](float l, uint32_t i) {
-              if (i >= static_cast<uint32_t>(V) || (l < c.sure && bucket_of(l, r) > c.bucket) || !stays(in, l, i, r)) return;
+              if (i >= static_cast<uint32_t>(V) || (!(l >= c.sure) && bucket_of(l, r) > c.bucket) || !stays(in, l, i, r)) return;
               const uint32_t at = atomicAdd(&s.mine, 1u);
               if (at < kSampleList) s.list_logit[at] = l, s.list_index[at] = i;
             });
@@ -651,7 +651,7 @@ struct SampleRow {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               here[j] = l[h + j] > c.never && stays(in, l[h + j], i + h + j, r);
-              if (here[j] && l[h + j] < c.sure) {
+              if (here[j] && !(l[h + j] >= c.sure)) {
                 const int b = bucket_of(l[h + j], r);
                 here[j] = b < c.bucket;
                 if (b == c.bucket && i + h + j < static_cast<uint32_t>(V)) {
@@ -906,7 +906,7 @@ struct SampleRow {
       const int bits = 32 - __clz(khi - klo);
       const int shift = max(0, bits - 11);
       begin();
-      each_of([&](float l) { return l < c.sure && l > c.never; },
+      each_of([&](float l) { return !(l >= c.sure) && l > c.never; },
               [&](float l, uint32_t i) {
                 const uint32_t k = rank_key(l);
                 if (k < klo || k > khi || bucket_of(l, r) != c.bucket || !stays(in, l, i, r)) return;

@@ -265,3 +265,18 @@ def test_top_k_beyond_the_lists(h, typ):
     u = torch.rand(6, generator=g).tolist()
     check(h, x, u, k=[4095, 4096, 4097, 20000, 40000, 99999])
     check(h, x, u, k=[257, 512, 2049, 5000, 33000, 70000], p=[0.5, 0.9, 0.99, 0.999, 0.8, 0.95])
+
+
+@pytest.mark.parametrize("typ", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("rows,V", [(7, 90), (5, 30000), (320, 6000), (2, 120000)])
+def test_several_infinite_logits(h, typ, rows, V):
+    """Equal and infinite logits are cut by count, mass and index like finite ones."""
+    x, g = rows_of(rows, rows, V, typ)
+    at = [V // 7 * i for i in range(1, 6)]
+    x[:, at] = INF
+    u = [(i % 10 + 0.5) / 10 for i in range(rows)]
+    n = min(rows, 12)
+    for kw in (dict(), dict(k=[1] * n), dict(k=[2, 3, 600] * n), dict(p=[0.0, 0.3, 0.6, 0.99] * n), dict(k=[4, V - 1] * n, p=[0.5, 0.9, 0.2] * n, low=[1.0] * n)):
+        check(h, x[:n], u[:n], **{a: v[:n] for a, v in kw.items()})
+    tokens, _ = draw(h, x, u, k=[3] * rows)
+    assert tokens == [at[int(3 * v)] for v in u]
