@@ -18,7 +18,7 @@
 //    list, or, of more, the border's bucket alone.  (Going over the rows every time: 64 rows of 128000 fp32 with mixed settings
 //    136 us, with lists 67; 509 of 50001 in bf16 with top-p 376 and 157.)
 //  * Instructions and shared memory's adds bound the passes with weights, the meetings of a cluster the rest: one row of 32000
-//    takes 14.6 us, of which the logits' bytes are nothing; 64 rows of 128000 without limits 36 (4.8 at the copy's rate).
+//    takes 10.1 us, of which the logits' bytes are nothing; 64 rows of 128000 without limits 36 (4.8 at the copy's rate).
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -35,6 +35,7 @@ constexpr int kSampleWarps = kSampleThreads / 32;
 constexpr int kSampleBuckets = 2048;
 constexpr int kSampleGroups = 32;  // of 64 buckets
 constexpr int kSampleMaxCluster = 8;
+constexpr int kSampleFew = 256;    // candidates that are compared each with each
 constexpr int kSampleList = 4096;  // candidates that one CTA finishes alone
 constexpr int kSampleUnit = 43;    // weights in units of 2^-43: 2^20 of them stay below 2^64
 constexpr uint32_t kTableFirst = 119 << 7, kTableValues = 15 << 7;  // bf16: magnitudes of 2^-8 up to 2^7
@@ -308,6 +309,7 @@ struct SampleRow {
   bool parted = false;   // only those of the border's bucket are, and
   uint64_t above = 0;    // this thread's sum of the smaller buckets' weights
   bool alone = false;    // those of the whole cluster in its first CTA, and the others have nothing to do
+  uint64_t goal = 0;     // of few listed candidates, the mass at which top-p ends, once it is known
   int turn = 0;
   bool reading = false;  // others may still be reading this CTA's histogram
 
@@ -799,6 +801,58 @@ struct SampleRow {
     }
   }
 
+  __device__ __forceinline__ bool few() const { return listed && alone && s.listed <= kSampleFew; }
+
+  // All that is left for few candidates, a thread to each: its place in the order and the mass before it by comparison with all others,
+  // what is kept (k: at most so many; p_goal(mass of those): the mass at which top-p ends, and no limit where that is all ones), and
+  // the running sum by index in the same way.  (Every cut by histograms and every draw of such a list is two meetings and two
+  // passes over 2048 buckets: 1 x 32000 with k 50 and p 0.9 15.5 us for 10.1.  512 candidates would take as long either way.)
+  template <class P, class A, class K>
+  __device__ void finish(uint32_t k, P p_goal, uint64_t floor_w, A aim, K take) {
+    uint64_t* key = reinterpret_cast<uint64_t*>(s.count);
+    uint64_t* mass = reinterpret_cast<uint64_t*>(s.lo);
+    const int n = static_cast<int>(s.listed), e = threadIdx.x;
+    const bool in = e < n;
+    uint64_t mine = ~0ull, w = 0;
+    if (in) {
+      mine = static_cast<uint64_t>(rank_key(s.list_logit[e])) << 32 | s.list_index[e];
+      w = weight(s.list_logit[e]);
+      key[e] = mine;
+      mass[e] = w;
+    }
+    __syncthreads();
+    uint32_t place = 0;
+    uint64_t before = 0;
+    if (warp * 32 < n) {
+#pragma unroll 4
+      for (int j = 0; j < n; ++j) {
+        const bool less = key[j] < mine;
+        place += less;
+        before += less ? mass[j] : 0;
+      }
+    }
+    auto sum = [&](uint64_t v) {  // over the CTA
+      v = warp_sum64(v);
+      if (lane == 0) s.warp_sum[warp] = v;
+      __syncthreads();
+      v = 0;
+#pragma unroll
+      for (int q = 0; q < kSampleWarps; ++q) v += s.warp_sum[q];
+      __syncthreads();
+      return v;
+    };
+    const uint64_t end = p_goal(sum(in && place < k ? w : 0));
+    const uint64_t kept = in && place < k && before < end && w >= floor_w ? w : 0;
+    if (in) mass[e] = kept;
+    const uint64_t total = sum(kept), target = aim(total);
+    if (warp * 32 >= n) return;
+    uint64_t run = 0;
+    const uint32_t index = static_cast<uint32_t>(mine);
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) run += static_cast<uint32_t>(key[j]) <= index ? mass[j] : 0;
+    if (kept && run > target && run - kept <= target) take(index, kept, total);
+  }
+
   // Lists the tokens that can be among the first k: those whose bucket is no larger than that of the k-th largest of the threads' largest
   // logits, `top`.
   __device__ void list_first(uint32_t k, float top) {
@@ -897,6 +951,10 @@ struct SampleRow {
       if (fit) list(c, in);
       if constexpr (MASS) {
         if (!fit) split(c, in, floor_w);
+        if (few()) {
+          goal = target;
+          return c;
+        }
       }
     }
     if ((alone && rank != 0) || before + part == target) return c;
@@ -1024,17 +1082,30 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const __grid_
     if (row.table) row.fill(table);
     Cut cut{kSampleBuckets, 0, 0, -kInf, -kInf};
     if (limited && k <= static_cast<int>(ctas) * kSampleThreads / 2) row.list_first(static_cast<uint32_t>(k), top);
-    if (limited && !(row.alone && rank != 0)) cut = row.template cut_at<false>([&](uint64_t) { return static_cast<uint64_t>(k); }, cut);
     const uint64_t floor_w = min_p > 0.f ? static_cast<uint64_t>(ceilf(fminf(min_p, 1.f) * 8796093022208.f)) : 0;  // 2^43 times it is exact
-    if (top_p < 1.f && !(row.alone && rank != 0))
-      cut = both_cuts(cut, row.template cut_at<true>(
-                               [&](uint64_t total) {
-                                 bool whole = true;
-                                 const uint64_t t = top_p > 0.f ? share_of(top_p, total, whole) : 0;
-                                 return max(t + !whole, static_cast<uint64_t>(1));
-                               },
-                               cut, floor_w));
-    if (!(row.alone && rank != 0)) {
+    const auto p_goal = [&](uint64_t total) {
+      bool whole = true;
+      const uint64_t t = top_p > 0.f ? share_of(top_p, total, whole) : 0;
+      return max(t + !whole, static_cast<uint64_t>(1));
+    };
+    const auto aim = [&](uint64_t total) {
+      bool whole;
+      return u >= 1.f ? total - 1 : u > 0.f ? share_of(u, total, whole) : 0;
+    };
+    const auto take = [&](uint32_t i, uint64_t w, uint64_t total) {
+      p.tokens[m] = static_cast<int32_t>(i);
+      if (p.logprobs) p.logprobs[m] = logf(static_cast<float>(static_cast<double>(w) / static_cast<double>(total)));
+    };
+    if (!row.few()) {
+      if (limited && !(row.alone && rank != 0)) cut = row.template cut_at<false>([&](uint64_t) { return static_cast<uint64_t>(k); }, cut);
+      if (top_p < 1.f && !(row.alone && rank != 0)) cut = both_cuts(cut, row.template cut_at<true>(p_goal, cut, floor_w));
+    }
+    if (row.alone && rank != 0) {
+      // the first CTA has all that is left
+    } else if (row.goal || (row.few() && cut.bucket == kSampleBuckets)) {
+      row.finish(
+          limited ? static_cast<uint32_t>(k) : 0xffffffffu, [&](uint64_t total) { return row.goal ? row.goal : top_p < 1.f ? p_goal(total) : ~0ull; }, floor_w, aim, take);
+    } else {
       row.template locate<true>(
           [&] {
             uint64_t mine = 0;
@@ -1049,14 +1120,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const __grid_
             const uint64_t w = row.weight(l);
             return w >= floor_w ? w : 0;
           },
-          [&](uint64_t total) {
-            bool whole;
-            return u >= 1.f ? total - 1 : u > 0.f ? share_of(u, total, whole) : 0;
-          },
-          [&](uint32_t i, uint64_t w, uint64_t total) {
-            p.tokens[m] = static_cast<int32_t>(i);
-            if (p.logprobs) p.logprobs[m] = logf(static_cast<float>(static_cast<double>(w) / static_cast<double>(total)));
-          });
+          aim, take);
     }
   }
   if (ctas > 1) cluster_meet();  // no CTA leaves while another reads its shared memory
