@@ -84,15 +84,11 @@ __device__ __forceinline__ float e4m3_scale(float top) {
 // each costs the cache store 3 us of 36.7 (8191 tokens).
 __device__ __forceinline__ uint2 e4m3_codes(float (&x)[8], float top, float scale) {
   const float by = __frcp_rn(scale);
-  if (top < __int_as_float(0x7f800000)) {
+  const bool finite = top < __int_as_float(0x7f800000);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float y = x[j] * by;
-      x[j] = fmaf(fmaf(-y, scale, x[j]), by, y);
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] *= by;
+  for (int j = 0; j < 8; ++j) {
+    const float y = x[j] * by;
+    x[j] = finite ? fmaf(fmaf(-y, scale, x[j]), by, y) : y;
   }
   uint32_t w[2];
 #pragma unroll
