@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(few_threads(BT), 2) scaled_few_kernel(const __
     int s = 0, issued = 0;
     uint32_t ph = 1;
     for (int i = 0; i < n; ++i) {
-      if (ok && i >= S) ok = mbar_wait_bounded(empty(s), ph, a.spin_ns);
+      if (ok && i >= S) ok = mbar_wait_warp(empty(s), ph, a.spin_ns);
       if (ok) issued = i + 1;
       if (ok && elect_one()) {
         if (i >= ahead) {
@@ -161,16 +161,16 @@ __global__ void __launch_bounds__(few_threads(BT), 2) scaled_few_kernel(const __
     }
     // what was issued last has landed before the CTA may leave
     for (int j = max(issued - S, 0); j < issued; ++j)
-      if (!mbar_wait_bounded(full(j % S), static_cast<uint32_t>(j / S) & 1, kDrainNs)) ok = false;
+      if (!mbar_wait_warp(full(j % S), static_cast<uint32_t>(j / S) & 1, kDrainNs)) ok = false;
   } else if (warp == 1) {  // ---- MMAs
     constexpr uint32_t idesc = tc_idesc_e4m3(kScaledRows, BT);
     const uint64_t d0 = tc_desc_sw128(base);
     int s = 0, b = 0;
     uint32_t ph = 0, tph = 1;
     for (int i = 0; i < n; i += Q) {
-      if (ok && i >= 2 * Q) ok = mbar_wait_bounded(tempty(b), tph, a.spin_ns);
+      if (ok && i >= 2 * Q) ok = mbar_wait_warp(tempty(b), tph, a.spin_ns);
       for (int q = 0; q < Q && i + q < n; ++q) {
-        if (ok) ok = mbar_wait_bounded(full(s), ph, a.spin_ns);
+        if (ok) ok = mbar_wait_warp(full(s), ph, a.spin_ns);
         tc_fence_after();
         const uint64_t wd = d0 + static_cast<uint64_t>(s * (STAGE / 16)), xd = wd + WBYTES / 16;
         if (elect_one()) {
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(few_threads(BT), 2) scaled_few_kernel(const __
       fetch(i + nq, b ^ 1);
       bar_part(1, EPI);  // the products
       // a warp that gave up goes on without waiting, so that the others do not miss it at their barriers
-      if (ok && !mbar_wait_bounded(tfull(b), tph, a.spin_ns)) ok = false;
+      if (ok && !mbar_wait_warp(tfull(b), tph, a.spin_ns)) ok = false;
       tc_fence_after();
       constexpr int CH = 16, NC = HB / CH;
       uint32_t d[2][CH];
@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(few_threads(BT), 2) scaled_few_kernel(const __
       }
     } else {
       // the MMAs have read the stages: this CTA's sums take their place, [row of x][weight row]
-      if (!mbar_wait_bounded(done, 0, kDrainNs)) ok = false;
+      if (!mbar_wait_warp(done, 0, kDrainNs)) ok = false;
 #pragma unroll
       for (int c = 0; c < HB; ++c)
         if (hh * HB + c < rows)
@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(few_threads(BT), 2) scaled_few_kernel(const __
     }
   }
   __syncwarp();
-  if (warp < 2 && !mbar_wait_bounded(done, 0, kDrainNs)) ok = false;
+  if (warp < 2 && !mbar_wait_warp(done, 0, kDrainNs)) ok = false;
   if (ks > 1) {
     scaled_cluster_meet();
     // this CTA's share of the tile's rows x 128 sums, over the ranks in their order
@@ -403,9 +403,9 @@ __global__ void __launch_bounds__(kManyThreads, 1) scaled_many_kernel(const __gr
     for (unsigned t = pair; t < tiles; t += pairs) {
       const int m = static_cast<int>(t % x_tiles * kManyRows + rank * (kManyRows / 2)), n = static_cast<int>(t / x_tiles * BN + rank * (BN / 2));
       for (int kb = kb0; kb < kb1; ++kb) {
-        if (ok && filled) ok = mbar_wait_bounded(empty(s), ph, a.spin_ns);
+        if (ok && filled) ok = mbar_wait_warp(empty(s), ph, a.spin_ns);
         // sums that gave up free stages early: a barrier is armed again only when what it was armed for has landed
-        if (ok && filled && rank == 0) ok = mbar_wait_bounded(full(s), ph, a.spin_ns);
+        if (ok && filled && rank == 0) ok = mbar_wait_warp(full(s), ph, a.spin_ns);
         const uint32_t bar = cluster_address(full(s), lead);
         if (ok && elect_one()) {
           if (rank == 0) mbar_arrive_expect_tx(full(s), 2 * STAGE);
@@ -425,8 +425,8 @@ __global__ void __launch_bounds__(kManyThreads, 1) scaled_many_kernel(const __gr
       bool is_full = false;  // asked while the block before is being issued
       for (unsigned t = pair; t < tiles; t += pairs) {
         for (int kb = kb0; kb < kb1; ++kb) {
-          if (ok && used) ok = mbar_wait_bounded(tempty(b), tph, a.spin_ns);
-          if (ok && !is_full) ok = mbar_wait_bounded(full(s), ph, a.spin_ns);
+          if (ok && used) ok = mbar_wait_warp(tempty(b), tph, a.spin_ns);
+          if (ok && !is_full) ok = mbar_wait_warp(full(s), ph, a.spin_ns);
           tc_fence_after();
           const uint64_t xd = d0 + static_cast<uint64_t>(s * (STAGE / 16)), wd = xd + XBYTES / 16;
           if (elect_one()) {
@@ -436,7 +436,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) scaled_many_kernel(const __gr
           }
           if (++s == S) s = 0, ph ^= 1;
           if (++b == NB) b = 0, tph ^= 1, used = true;
-          is_full = mbar_test(full(s), ph);
+          is_full = __all_sync(0xffffffffu, mbar_test(full(s), ph));
         }
       }
       if (elect_one()) tc_commit_pair(done, lead);  // nobody leaves while MMAs run
@@ -481,7 +481,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) scaled_many_kernel(const __gr
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           if (kb + q >= kb1) break;
-          if (ok && used) ok = mbar_wait_bounded(tfull(b), ph, a.spin_ns);
+          if (ok && used) ok = mbar_wait_warp(tfull(b), ph, a.spin_ns);
           const uint32_t to = prod + slot * SLOT + r * 4;
           slot = (slot + 1) % SLOTS;
 #pragma unroll
@@ -512,7 +512,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) scaled_many_kernel(const __gr
 #pragma unroll 1
       for (int kb = kb0; kb < kb1; ++kb) {
         // a warp that gave up goes on without waiting: the other CTA counts on it
-        if (ok) ok = mbar_wait_bounded(tfull(b), tph, a.spin_ns);
+        if (ok) ok = mbar_wait_warp(tfull(b), tph, a.spin_ns);
         tc_fence_after();
         const uint32_t from = lanes + b * BN;
         const float f = __uint_as_float(lds_u32(mine_f + slot * SLOT));
@@ -665,7 +665,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) scaled_many_kernel(const __gr
   }
   __syncwarp();
   if (JOIN && warp < 4) scaled_cluster_meet();  // with the sums' threads
-  if (!mbar_wait_bounded(done, 0, kDrainNs)) ok = false;
+  if (!mbar_wait_warp(done, 0, kDrainNs)) ok = false;
   if (!ok) {
     atomicOr(a.err, kDevErrTimeout);
     // copies that were asked for but that no MMA waited for: they have a millisecond to land
