@@ -135,7 +135,8 @@ __global__ void __launch_bounds__(few_threads(BT), 2) scaled_few_kernel(const __
   pdl_launch_dependents();
 
   // The copying and the issuing warp go through their loops as a whole and let one lane do the work: what is the same for all
-  // lanes then stays in uniform registers.  One that gave up goes on without waiting (and copying).
+  // lanes then stays in uniform registers.  A warp that gave up signals nobody from then on: a stage is freed, and its barrier armed
+  // again, only when its copies have landed and the MMAs that read them are complete.  Those that wait for it give up in turn.
   if (warp == 0) {  // ---- copies
     const int ahead = a.early ? min(S, n) : 0;
     for (int j = 0; j < ahead; ++j) {
@@ -173,14 +174,14 @@ __global__ void __launch_bounds__(few_threads(BT), 2) scaled_few_kernel(const __
         if (ok) ok = mbar_wait_warp(full(s), ph, a.spin_ns);
         tc_fence_after();
         const uint64_t wd = d0 + static_cast<uint64_t>(s * (STAGE / 16)), xd = wd + WBYTES / 16;
-        if (elect_one()) {
+        if (ok && elect_one()) {
 #pragma unroll
           for (int k = 0; k < kScaledBlock / 32; ++k) tc_mma_f8(tmem + (b * Q + q) * BT, wd + 2 * k, xd + 2 * k, idesc, k > 0);
           tc_commit(empty(s));
         }
         if (++s == S) s = 0, ph ^= 1;
       }
-      if (!(a.stall && blockIdx.x == 0 && i == 0) && elect_one()) tc_commit(tfull(b));
+      if (ok && !(a.stall && blockIdx.x == 0 && i == 0) && elect_one()) tc_commit(tfull(b));
       if ((b ^= 1) == 0) tph ^= 1;
     }
     if (elect_one()) tc_commit(done);  // nobody leaves, or writes over the stages, while MMAs run
@@ -222,7 +223,7 @@ __global__ void __launch_bounds__(few_threads(BT), 2) scaled_few_kernel(const __
       keep(b);
       fetch(i + nq, b ^ 1);
       bar_part(1, EPI);  // the products
-      // a warp that gave up goes on without waiting, so that the others do not miss it at their barriers
+      // a warp that gave up goes on, so that the others do not miss it at their barriers
       if (ok && !mbar_wait_warp(tfull(b), tph, a.spin_ns)) ok = false;
       tc_fence_after();
       constexpr int CH = 16, NC = HB / CH;
@@ -255,7 +256,7 @@ __global__ void __launch_bounds__(few_threads(BT), 2) scaled_few_kernel(const __
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(tempty(b));
+      if (ok && lane == 0) mbar_arrive(tempty(b));
       if ((b ^= 1) == 0) tph ^= 1;
       i += nq;
     }
@@ -396,7 +397,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) scaled_many_kernel(const __gr
   pdl_wait();
 
   if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kManyRegs[0]));
-  if (warp == 0) {  // ---- copies (whole warps go through the loops, as above)
+  if (warp == 0) {  // ---- copies (whole warps go through the loops and signal nobody once they gave up, as above)
     int s = 0;
     uint32_t ph = 1;
     bool filled = false;  // every stage has been used
@@ -404,8 +405,6 @@ __global__ void __launch_bounds__(kManyThreads, 1) scaled_many_kernel(const __gr
       const int m = static_cast<int>(t % x_tiles * kManyRows + rank * (kManyRows / 2)), n = static_cast<int>(t / x_tiles * BN + rank * (BN / 2));
       for (int kb = kb0; kb < kb1; ++kb) {
         if (ok && filled) ok = mbar_wait_warp(empty(s), ph, a.spin_ns);
-        // sums that gave up free stages early: a barrier is armed again only when what it was armed for has landed
-        if (ok && filled && rank == 0) ok = mbar_wait_warp(full(s), ph, a.spin_ns);
         const uint32_t bar = cluster_address(full(s), lead);
         if (ok && elect_one()) {
           if (rank == 0) mbar_arrive_expect_tx(full(s), 2 * STAGE);
@@ -429,7 +428,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) scaled_many_kernel(const __gr
           if (ok && !is_full) ok = mbar_wait_warp(full(s), ph, a.spin_ns);
           tc_fence_after();
           const uint64_t xd = d0 + static_cast<uint64_t>(s * (STAGE / 16)), wd = xd + XBYTES / 16;
-          if (elect_one()) {
+          if (ok && elect_one()) {
 #pragma unroll
             for (int k = 0; k < kScaledBlock / 32; ++k) tc_mma_f8_pair(tmem + b * BN, xd + 2 * k, wd + 2 * k, idesc, k > 0);
             if (!(a.stall && blockIdx.x == 0 && t == pair && kb == kb0)) tc_commit_pair(tfull(b), lead);
@@ -490,7 +489,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) scaled_many_kernel(const __gr
             for (int j = 0; j < 2; ++j)
               asm volatile("st.shared.f32 [%0], %1;" ::"r"(to + (w * 128 + j * 64) * 4), "f"(now.x[j][q] * now.w[w][q]) : "memory");
           __syncwarp();
-          if (elect_one()) mbar_arrive(tfull(b));
+          if (ok && elect_one()) mbar_arrive(tfull(b));
           if (++b == NB) b = 0, ph ^= 1, used = true;
         }
       }
@@ -511,7 +510,6 @@ __global__ void __launch_bounds__(kManyThreads, 1) scaled_many_kernel(const __gr
       for (int c = 0; c < HB; ++c) acc[c] = 0.f;
 #pragma unroll 1
       for (int kb = kb0; kb < kb1; ++kb) {
-        // a warp that gave up goes on without waiting: the other CTA counts on it
         if (ok) ok = mbar_wait_warp(tfull(b), tph, a.spin_ns);
         tc_fence_after();
         const uint32_t from = lanes + b * BN;
@@ -532,7 +530,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) scaled_many_kernel(const __gr
           if (k + 1 == NC) {
             tc_fence_before();
             __syncwarp();
-            if (elect_one()) {
+            if (ok && elect_one()) {
               mbar_arrive_remote(tempty_at + 8u * b);
               if (warp == 4) mbar_arrive(empty(s));  // the block's MMAs are complete, and so are their reads of its stage
             }

@@ -1,0 +1,46 @@
+"""Projections in 8 bits whose waits run out: wherever that happens, the call ends, reports it, and what runs next finds nothing of it.
+With a limit of 0 a wait gives up unless it is over at once; with some thousand nanoseconds it does so in the middle of a call."""
+import os
+import sys
+
+import pytest
+import torch
+
+from quantized_weight_dequant_gb300 import qgemv
+
+sys.path.insert(0, os.path.dirname(os.path.abspath(__file__)))
+import test_gpu_scaled as scaled  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+h = scaled.h
+FEW = [(3, 300, 1024), (3, 40000, 1024), (20, 4096, 4096), (64, 256, 4096), (64, 28672, 640), (1, 4096, 4096)]
+LIMITS = [0, 500, 2_000, 6_000, 20_000]
+
+
+@pytest.mark.parametrize("M,N,K", FEW)
+@pytest.mark.parametrize("stall", [0, 1])
+def test_waits_of_any_length_end(h, M, N, K, stall):
+    x, xs, W, ws = scaled.operands(scaled.gen(M + N + K), M, N, K)
+    want, y = torch.empty(M, N, device="cuda"), torch.empty(M, N, device="cuda")
+    good, tried = qgemv.scaled_desc(x, xs, W, ws, want), qgemv.scaled_desc(x, xs, W, ws, y)
+    qgemv.run_scaled(h, good)
+    torch.cuda.synchronize()
+    assert qgemv.check_error(h) == qgemv.OK
+    again = torch.empty_like(want)
+    for limit in LIMITS:
+        qgemv.set_option(h, qgemv.OPT_SPIN_LIMIT_NS, limit)
+        qgemv.set_option(h, qgemv.OPT_TEST_STALL, stall)
+        try:
+            y.fill_(7)
+            qgemv.run_scaled(h, tried)
+            status = qgemv.check_error(h)
+        finally:
+            qgemv.set_option(h, qgemv.OPT_TEST_STALL, 0)
+            qgemv.set_option(h, qgemv.OPT_SPIN_LIMIT_NS, 1_000_000_000)
+        if stall:
+            assert status == qgemv.ERR_TIMEOUT
+        else:  # either it was in time or it says that it was not
+            assert status == qgemv.ERR_TIMEOUT or (status == qgemv.OK and torch.equal(y, want))
+        again.fill_(7)
+        qgemv.run_scaled(h, qgemv.scaled_desc(x, xs, W, ws, again))
+        assert qgemv.check_error(h) == qgemv.OK and torch.equal(again, want)
