@@ -86,6 +86,17 @@ __device__ __forceinline__ void scaled_store(void* y, int64_t at, int type, floa
     static_cast<__nv_bfloat16*>(y)[at] = __float2bfloat16_rn(v);
 }
 
+__device__ __forceinline__ void store_remote_u32(uint32_t cluster_at, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_at), "r"(v) : "memory");
+}
+__device__ __forceinline__ void store_remote_u64(uint32_t cluster_at, uint64_t v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(cluster_at), "l"(v) : "memory");
+}
+__device__ __forceinline__ int64_t lds_u64(uint32_t at) {
+  int64_t v;
+  asm volatile("ld.shared.u64 %0, [%1];" : "=l"(v) : "r"(at) : "memory");
+  return v;
+}
 __device__ __forceinline__ void scaled_cluster_meet() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -364,8 +375,9 @@ __global__ void __launch_bounds__(kManyThreads, 1) scaled_many_kernel(const __gr
   auto empty = [&](int s) { return bars + 8u * (S + s); };      // the MMAs that read the stage are complete
   auto tfull = [&](int b) { return bars + 8u * (2 * S + b); };  // a block's sums are in TMEM and its scales' products in shared memory
   auto tempty = [&](int b) { return bars + 8u * (2 * S + NB + b); };  // of the first CTA: both CTAs have read them
-  const uint32_t done = bars + 8u * (2 * S + 2 * NB), tslot = done + 8;
-  static_assert(SLOTS * SLOT <= kManyScaleBytes && 8 * (2 * S + 2 * NB) + 8 + 8 <= 256, "barriers");
+  const uint32_t done = bars + 8u * (2 * S + 2 * NB), tslot = done + 8, failed = tslot + 4;  // failed: a CTA of the cluster gave up
+  auto copied = [&](unsigned r) { return done + 16 + 8u * r; };  // of the pair's first CTA: the stages that CTA r has asked for
+  static_assert(SLOTS * SLOT <= kManyScaleBytes && 8 * (2 * S + 2 * NB) + 32 <= 256, "barriers");
   static_assert(kManyRows / 2 * kJoinPad * 4 <= S * STAGE, "a tile's sums take the place of the stages");
   const uint32_t prod = bars + 256 + kManyOutBytes;  // [block % SLOTS][128 rows of W][row of x]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -382,6 +394,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) scaled_many_kernel(const __gr
     for (int b = 0; b < NB; ++b) mbar_init(tfull(b), 3), mbar_init(tempty(b), 2 * 4 * kManyParts);
     mbar_init(done, 1);
     fence_mbar_init();
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(failed), "r"(0) : "memory");
   }
   if (warp == 1) {
     tmem_alloc_pair(tslot, NB * BN);
@@ -401,6 +414,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) scaled_many_kernel(const __gr
     int s = 0;
     uint32_t ph = 1;
     bool filled = false;  // every stage has been used
+    int64_t asked = 0;
     for (unsigned t = pair; t < tiles; t += pairs) {
       const int m = static_cast<int>(t % x_tiles * kManyRows + rank * (kManyRows / 2)), n = static_cast<int>(t / x_tiles * BN + rank * (BN / 2));
       for (int kb = kb0; kb < kb1; ++kb) {
@@ -411,9 +425,11 @@ __global__ void __launch_bounds__(kManyThreads, 1) scaled_many_kernel(const __gr
           tma_load_2d_pair(base + s * STAGE, &xmap, kb * kScaledBlock, m, bar);
           tma_load_2d_pair(base + s * STAGE + XBYTES, &wmap, kb * kScaledBlock, n, bar);
         }
+        asked += ok;
         if (++s == S) s = 0, ph ^= 1, filled = true;
       }
     }
+    if (lane == 0) store_remote_u64(cluster_address(copied(rank), lead), static_cast<uint64_t>(asked));
   } else if (warp == 1) {
     if (rank == 0) {  // ---- MMAs
       constexpr uint32_t idesc = tc_idesc_e4m3(kManyRows, BN);
@@ -666,14 +682,28 @@ __global__ void __launch_bounds__(kManyThreads, 1) scaled_many_kernel(const __gr
   if (!mbar_wait_warp(done, 0, kDrainNs)) ok = false;
   if (!ok) {
     atomicOr(a.err, kDevErrTimeout);
-    // copies that were asked for but that no MMA waited for: they have a millisecond to land
-    const long long t0 = clock64();
-    while (clock64() - t0 < 2000000) {
-    }
+    for (unsigned q = 0; q < 2 * ks; ++q) store_remote_u32(cluster_address(failed, q), 1);
   }
   tc_fence_before();
   __syncthreads();
   scaled_cluster_meet();  // nobody leaves while the other CTA's arrivals are on their way
+  if (lds_u32(failed)) {
+    // What was copied for no MMA has landed before a CTA may leave.  Both CTAs' copies are counted at the first one's barriers, where
+    // a stage is asked for again only after it was read: of each CTA the last S may be on their way, and the CTAs are no more than S
+    // apart.
+    if (warp == 0 && rank == 0) {
+      const int64_t c0 = lds_u64(copied(0)), c1 = lds_u64(copied(1)), most = max(c0, c1);
+      for (int64_t j = max(most - S, int64_t{0}); j < most; ++j) {
+        const uint32_t bar = full(static_cast<int>(j % S));
+        if (lane == 0 && j >= c0) mbar_arrive_expect_tx(bar, STAGE);  // the other's copy alone, of a stage that was not armed
+        if (lane == 0 && j >= c1) mbar_complete_tx(bar, STAGE);       // this CTA's alone, of a stage that was armed for both
+        __syncwarp();
+        if (!mbar_wait_warp(bar, static_cast<uint32_t>(j / S) & 1, kDrainNs)) break;
+      }
+    }
+    __syncwarp();
+    scaled_cluster_meet();
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, NB * BN);

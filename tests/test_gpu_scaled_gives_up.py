@@ -14,10 +14,11 @@ import test_gpu_scaled as scaled  # noqa: E402
 pytestmark = pytest.mark.gpu
 h = scaled.h
 FEW = [(3, 300, 1024), (3, 40000, 1024), (20, 4096, 4096), (64, 256, 4096), (64, 28672, 640), (1, 4096, 4096)]
-LIMITS = [0, 500, 2_000, 6_000, 20_000]
+MANY = [(65, 300, 1024), (128, 4096, 14336), (300, 4096, 14336), (512, 4096, 4096), (1500, 20000, 640), (4096, 5000, 1040)]
+LIMITS = [0, 500, 2_000, 6_000, 20_000, 60_000]
 
 
-@pytest.mark.parametrize("M,N,K", FEW)
+@pytest.mark.parametrize("M,N,K", FEW + MANY)
 @pytest.mark.parametrize("stall", [0, 1])
 def test_waits_of_any_length_end(h, M, N, K, stall):
     x, xs, W, ws = scaled.operands(scaled.gen(M + N + K), M, N, K)
