@@ -127,12 +127,6 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
   }
 }
 
-// The same for a whole warp.  Each lane gives up by its own clock; the vote makes them agree, as what the warp does together
-// afterwards (elect.sync, tcgen05, barriers) needs all of them.
-__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
-  return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, limit_ns));
-}
-
 // True in one lane of the (whole) warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t yes;
