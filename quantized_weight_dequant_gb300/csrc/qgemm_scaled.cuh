@@ -472,11 +472,11 @@ __global__ void __launch_bounds__(kManyThreads, 1) scaled_many_kernel(const __gr
       const int64_t row = static_cast<int64_t>(t % x_tiles) * kManyRows + rank * (kManyRows / 2) + r, wrow = static_cast<int64_t>(t / x_tiles) * WB;
       auto four = [&](const float* at, bool in, float (&f)[4]) {
         if (a.wide) {
-          const float4 q = in ? __ldg(reinterpret_cast<const float4*>(at)) : make_float4(0.f, 0.f, 0.f, 0.f);
+          const float4 q = in ? *reinterpret_cast<const float4*>(at) : make_float4(0.f, 0.f, 0.f, 0.f);
           f[0] = q.x, f[1] = q.y, f[2] = q.z, f[3] = q.w;
         } else {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) f[q] = in && kb + q < kb1 ? __ldg(at + q) : 0.f;
+          for (int q = 0; q < 4; ++q) f[q] = in && kb + q < kb1 ? at[q] : 0.f;
         }
       };
 #pragma unroll

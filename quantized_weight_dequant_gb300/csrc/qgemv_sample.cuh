@@ -346,7 +346,7 @@ struct SampleRow {
   __device__ __forceinline__ void load_global(int v, float (&l)[kVec<T>]) const {
     const int i0 = index_of(v);
     if (i0 >= 0 && i0 + kVec<T> <= V) {
-      unpack<T>(__ldg(vecs + v), l);
+      unpack<T>(vecs[v], l);
 #pragma unroll
       for (int j = 0; j < kVec<T>; ++j) l[j] = usual(l[j]);
     } else {
@@ -1033,9 +1033,9 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const __grid_
   if (threadIdx.x == 2) s.mine = 0;
   if (threadIdx.x < 64) s.pow[threadIdx.x] = kPow[threadIdx.x];
   pdl_wait();
-  const float temperature = p.temperature ? __ldg(p.temperature + m) : 1.f, top_p = p.top_p ? __ldg(p.top_p + m) : 1.f;
-  const float min_p = p.min_p ? __ldg(p.min_p + m) : 0.f, u = __ldg(p.u + m);
-  const int32_t k = p.top_k ? __ldg(p.top_k + m) : 0;
+  const float temperature = p.temperature ? p.temperature[m] : 1.f, top_p = p.top_p ? p.top_p[m] : 1.f;
+  const float min_p = p.min_p ? p.min_p[m] : 0.f, u = p.u[m];
+  const int32_t k = p.top_k ? p.top_k[m] : 0;
   // the largest logit and its first index; the piece into shared memory
   float top = -kInf;
   int at = -1;

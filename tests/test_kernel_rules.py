@@ -16,3 +16,13 @@ def test_every_lane_comes_to_elect_in_the_projection():
     text = source("qgemm_scaled.cuh")
     assert text.count("elect_one()") > 10
     assert not re.search(r"&&[^;{}]*elect_one\(\)", text), "an election that some lanes skip"
+
+
+def test_dependent_launches_read_nothing_through_the_non_coherent_path():
+    """Such a kernel is there while the one before it still writes what it will read; the non-coherent path (ld.global.nc, which the
+    compiler also takes for const __restrict__ pointers) is for memory that does not change during a kernel's life."""
+    names = [n for n in os.listdir(CSRC) if n.endswith((".cu", ".cuh")) and "pdl_wait" in source(n)]
+    assert {"qgemm_scaled.cuh", "qgemv_sample.cuh", "qgemv_rows.cuh", "qgemv_attn.cuh", "qgemv_pages.cuh", "qgemv_lora.cuh"} <= set(names)
+    for name in names + ["qgemv_elems.cuh", "qgemv_serve.cuh"]:
+        for word in ("__ldg", "ld.global.nc", "__restrict__"):
+            assert word not in source(name), (name, word)
