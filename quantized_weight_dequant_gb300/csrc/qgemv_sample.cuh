@@ -593,9 +593,16 @@ struct SampleRow {
     }
   }
 
+  // An empty list again, once all CTAs have seen how long it was.
+  __device__ __forceinline__ void forget() {
+    meet();
+    if (threadIdx.x == 0) s.mine = 0;
+    __syncthreads();
+  }
+
   // The candidates, those of `c`'s bucket and smaller ones that `in` keeps, go into lists, in no order (what follows goes by logits
   // and indexes): into that of the cluster's first CTA where it holds them, which then goes on alone, else into each CTA's own.  Where
-  // one of those is too short, everything goes on over the rows.
+  // one of those is too short nothing is listed, and a later list begins empty.
   __device__ void list(const Cut& c, const Cut& in) {
     settle();
     each_of([&](float l) { return l > c.never; },
@@ -621,7 +628,10 @@ struct SampleRow {
         most = max(most, part[q]);
       }
     }
-    if (most > kSampleList) return;
+    if (most > kSampleList) {
+      forget();
+      return;
+    }
     listed = true;
     alone = ctas == 1;
     if (threadIdx.x == 0) s.listed = n;
@@ -684,7 +694,10 @@ struct SampleRow {
       cluster_meet();
       for (uint32_t q = 0; q < ctas; ++q) most = max(most, remote_u32(&s.mine, q));
     }
-    if (most > kSampleList) return;
+    if (most > kSampleList) {
+      forget();
+      return;
+    }
     above = sum;
     listed = parted = true;
     if (threadIdx.x == 0) s.listed = s.mine;
@@ -950,7 +963,7 @@ struct SampleRow {
       const bool fit = MASS ? s.pick_first <= kSampleList * ctas * 3 / 4 : before + part <= kSampleList;
       if (fit) list(c, in);
       if constexpr (MASS) {
-        if (!fit) split(c, in, floor_w);
+        if (!listed) split(c, in, floor_w);  // (one CTA can have most of the candidates: what a mask leaves is often one range)
         if (few()) {
           goal = target;
           return c;
