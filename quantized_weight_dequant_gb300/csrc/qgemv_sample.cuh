@@ -34,6 +34,7 @@ constexpr int kSampleThreads = 512;
 constexpr int kSampleWarps = kSampleThreads / 32;
 constexpr int kSampleBuckets = 2048;
 constexpr int kSampleGroups = 32;  // of 64 buckets
+constexpr int kSampleNothing = 1801;  // the first bucket whose tokens weigh nothing: 45 halvings, 40 buckets each, to the nearest
 constexpr int kSampleMaxCluster = 8;
 constexpr int kSampleFew = 256;    // candidates that are compared each with each
 constexpr int kSampleList = 4096;  // candidates that one CTA finishes alone
@@ -252,7 +253,7 @@ __device__ __forceinline__ int bucket_of(float l, const RowScale& r) {
     if (l == r.m) return 0;  // infinite
     const float z = y * -0.015625f;
     if (!(z < 65536.f)) return kSampleBuckets - 1;
-    return 1801 + ((__float_as_int(z) - __float_as_int(45.f)) >> 19);
+    return kSampleNothing + ((__float_as_int(z) - __float_as_int(45.f)) >> 19);
   }
   return linear_bucket(y);
 }
@@ -267,7 +268,7 @@ struct Cut {
 };
 __device__ __forceinline__ Cut cut_in(int bucket, const RowScale& r) {
   Cut c{bucket, 0xffffffffu, 0xffffffffu, __int_as_float(0x7fffffff), -kInf};
-  auto z_at = [](int b) { return b <= 1800 ? (static_cast<float>(b) - 0.5f) / 40.f : __int_as_float(__float_as_int(45.f) + ((b - 1801) << 19)); };
+  auto z_at = [](int b) { return b < kSampleNothing ? (static_cast<float>(b) - 0.5f) / 40.f : __int_as_float(__float_as_int(45.f) + ((b - kSampleNothing) << 19)); };
   const float wide = 1e-5f * fabsf(r.m);
   // buckets are monotone in the logit: a logit of a smaller bucket proves it of all larger ones
   const float sure = r.m - z_at(bucket) * (64.f * 0.99999f) / r.hi + wide, never = r.m - z_at(bucket + 1) * (64.f * 1.00001f) / r.hi - wide;
@@ -959,6 +960,8 @@ struct SampleRow {
     uint64_t before = s.pick_before;
     uint64_t part = MASS ? s.pick_mass : s.pick_count;
     Cut c = cut_in(static_cast<int>(s.pick_bucket), r);
+    // A count that ends among tokens of weight 0 (those a mask took out among them) cuts nothing that can be drawn.
+    if (!MASS && c.bucket >= kSampleNothing) return c;
     if (!listed) {
       const bool fit = MASS ? s.pick_first <= kSampleList * ctas * 3 / 4 : before + part <= kSampleList;
       if (fit) list(c, in);
