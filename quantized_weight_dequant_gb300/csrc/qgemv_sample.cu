@@ -41,8 +41,9 @@ extern "C" qgemv_status_t qgemv_sample(qgemv_handle_t hh, const qgemv_sample_t* 
   int ctas = 1;
   while (ctas < kSampleMaxCluster && p.rows * ctas * 2 <= 2 * int64_t{h->sms} && p.V >= ctas * 2 * 2048) ctas *= 2;
   const bool held = row_bytes <= most * ctas;
-  const size_t smem = sizeof(SampleSmem) + sample_table_bytes(p.type) + (held ? static_cast<size_t>((row_bytes / 16 / ctas + 2) * 16) : 0);
+  const size_t fixed = sizeof(SampleSmem) + sample_table_bytes(p.type), smem = fixed + (held ? static_cast<size_t>((row_bytes / 16 / ctas + 2) * 16) : 0);
+  const size_t largest = fixed + (held ? static_cast<size_t>((most / 16 + 2) * 16) : 0);  // row_bytes <= most * ctas
   const void* fn = p.type == QGEMV_OUT_F32 ? kernel_for<QGEMV_OUT_F32>(held) : p.type == QGEMV_OUT_F16 ? kernel_for<QGEMV_OUT_F16>(held) : kernel_for<QGEMV_OUT_BF16>(held);
   void* args[] = {const_cast<qgemv_sample_t*>(&p)};
-  return launch_dependent(fn, dim3(static_cast<unsigned>(p.rows * ctas)), kSampleThreads, smem, ctas, args, stream) ? QGEMV_OK : QGEMV_ERR_CUDA;
+  return launch_dependent(fn, dim3(static_cast<unsigned>(p.rows * ctas)), kSampleThreads, smem, ctas, args, stream, largest) ? QGEMV_OK : QGEMV_ERR_CUDA;
 }

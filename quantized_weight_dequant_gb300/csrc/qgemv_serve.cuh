@@ -20,9 +20,12 @@ inline int64_t kv_elem_bytes(const qgemv_kv_cache_t& c) { return c.type == QGEMV
 // small launches this takes the launch latency out of the stream (1.5 us each).  What the kernel before writes
 // changes while this one is there already, so nothing is read through the non-coherent path (__ldg, const
 // __restrict__), which is for memory that nobody writes during a kernel's whole life.
-inline bool launch_dependent(const void* fn, dim3 grid, int threads, size_t smem, int cluster, void** args, cudaStream_t stream) {
+// The dynamic shared memory that a kernel may have belongs to the function on its device, so that what one host thread asks for
+// holds for another one's launch: every call asks for the same.  `most`: of a kernel whose `smem` varies, the largest.
+inline bool launch_dependent(const void* fn, dim3 grid, int threads, size_t smem, int cluster, void** args, cudaStream_t stream, size_t most = 0) {
+  if (most == 0) most = smem;
   // up to 48 KB, with what the kernel has statically (none more than 24 KB beside dynamic memory), need no request
-  if (smem > 24 * 1024 && cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess) {
+  if (most > 24 * 1024 && cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most)) != cudaSuccess) {
     cudaGetLastError();
     return false;
   }
