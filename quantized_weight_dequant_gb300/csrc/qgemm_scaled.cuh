@@ -179,6 +179,7 @@ __global__ void __launch_bounds__(few_threads(BT), 2) scaled_few_kernel(const __
   } else if (warp == 1) {  // ---- MMAs
     constexpr uint32_t idesc = tc_idesc_e4m3(kScaledRows, BT);
     const uint64_t d0 = tc_desc_sw128(base);
+    pdl_wait();  // the copies do, and the time until then is not theirs
     int s = 0, b = 0;
     uint32_t ph = 0, tph = 1;
     for (int i = 0; i < n; i += Q) {

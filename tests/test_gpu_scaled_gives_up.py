@@ -45,3 +45,30 @@ def test_waits_of_any_length_end(h, M, N, K, stall):
         again.fill_(7)
         qgemv.run_scaled(h, qgemv.scaled_desc(x, xs, W, ws, again))
         assert qgemv.check_error(h) == qgemv.OK and torch.equal(again, want)
+
+
+@pytest.mark.parametrize("M", [1, 30, 64])
+@pytest.mark.parametrize("pdl", [0, 1])
+def test_the_kernel_before_does_not_count_as_waiting(h, M, pdl):
+    """A projection that is there early, beside a long draw that leaves it room, waits for that one's end without a limit."""
+    N, K = 512, 512
+    x, xs, W, ws = scaled.operands(scaled.gen(M), M, N, K)
+    want, y = torch.empty(M, N, device="cuda"), torch.empty(M, N, device="cuda")
+    qgemv.run_scaled(h, qgemv.scaled_desc(x, xs, W, ws, want))
+    logits = torch.randn(2, 1 << 20, device="cuda")  # two clusters, some 100 us
+    u, tokens = torch.rand(2, device="cuda"), torch.empty(2, dtype=torch.int32, device="cuda")
+    draw = qgemv.sample_desc(logits, u, tokens, top_p=torch.full((2,), 0.9, device="cuda"))
+    desc = qgemv.scaled_desc(x, xs, W, ws, y)
+    qgemv.sample(h, draw)
+    assert qgemv.check_error(h) == qgemv.OK
+    qgemv.set_option(h, qgemv.OPT_PDL, pdl)
+    qgemv.set_option(h, qgemv.OPT_SPIN_LIMIT_NS, 25_000)  # the projection's own waits are below 10 us
+    try:
+        for _ in range(3):
+            qgemv.sample(h, draw)
+            qgemv.run_scaled(h, desc)
+            assert qgemv.check_error(h) == qgemv.OK
+            assert torch.equal(y, want)
+    finally:
+        qgemv.set_option(h, qgemv.OPT_PDL, 0)
+        qgemv.set_option(h, qgemv.OPT_SPIN_LIMIT_NS, 1_000_000_000)
