@@ -135,6 +135,13 @@ __device__ __forceinline__ uint64_t share_of(float u, uint64_t total, bool& whol
   return hi << (64 - shift) | lo >> shift;
 }
 
+// log(part / total) to fp32's precision: near 1 by what is missing, which a quotient of 24 bits has lost.
+__device__ __forceinline__ float log_share(uint64_t part, uint64_t total) {
+  const uint64_t rest = total - part;
+  const float q = static_cast<float>(static_cast<double>(min(part, rest)) / static_cast<double>(total));
+  return part > rest ? log1pf(-q) : logf(q);
+}
+
 // ---------------------------------------------------------------------------- logits
 template <int T>
 constexpr int kVec = T == QGEMV_OUT_F32 ? 4 : 8;  // logits in 16 bytes
@@ -1110,7 +1117,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const __grid_
     };
     const auto take = [&](uint32_t i, uint64_t w, uint64_t total) {
       p.tokens[m] = static_cast<int32_t>(i);
-      if (p.logprobs) p.logprobs[m] = logf(static_cast<float>(static_cast<double>(w) / static_cast<double>(total)));
+      if (p.logprobs) p.logprobs[m] = log_share(w, total);
     };
     if (!row.few()) {
       if (limited && !(row.alone && rank != 0)) cut = row.template cut_at<false>([&](uint64_t) { return static_cast<uint64_t>(k); }, cut);
