@@ -98,6 +98,7 @@ __device__ __forceinline__ int64_t lds_u64(uint32_t at) {
   return v;
 }
 __device__ __forceinline__ void scaled_cluster_meet() {
+  __syncwarp();  // .aligned: whole warps, whatever their lanes did before
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 __device__ __forceinline__ float remote_f32(uint32_t at, uint32_t rank) {
@@ -682,7 +683,6 @@ __global__ void __launch_bounds__(kManyThreads, 1) scaled_many_kernel(const __gr
       }
     }
   }
-  __syncwarp();
   if (JOIN && warp < 4) scaled_cluster_meet();  // with the sums' threads
   if (!mbar_wait_bounded(done, 0, kDrainNs)) ok = false;
   if (!ok) {
@@ -705,7 +705,6 @@ __global__ void __launch_bounds__(kManyThreads, 1) scaled_many_kernel(const __gr
         if (!mbar_wait_bounded(bar, static_cast<uint32_t>(j / S) & 1, kDrainNs)) break;
       }
     }
-    __syncwarp();
     scaled_cluster_meet();
   }
   if (warp == 1) {

@@ -103,6 +103,7 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
 // Every thread of every CTA of the cluster arrives; this CTA's earlier shared-memory writes are
 // visible to the cluster after the wait.
 __device__ __forceinline__ void cluster_sync() {
+  __syncwarp();  // .aligned: whole warps, whatever their lanes did before
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // fp32 at shared address `a` of cluster CTA `rank`
@@ -335,7 +336,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_nvfp4_kernel(const __grid_co
     // ---- split K: the cluster's partial tiles are complete after the first barrier; CTA ksi
     // adds columns [ksi BT / ks, (ksi + 1) BT / ks) of all of them, in rank order, then the
     // second barrier keeps every CTA's shared memory alive until the others are done with it.
-    __syncwarp();
     cluster_sync();
     const int c_lo = (ksi * BT) / a.ks, c_hi = ((ksi + 1) * BT) / a.ks;
     const int per = (c_hi - c_lo) * kTcRows;

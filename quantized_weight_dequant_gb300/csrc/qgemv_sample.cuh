@@ -75,8 +75,18 @@ __device__ __forceinline__ uint32_t cluster_ctas() {
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
   return r;
 }
+// (.aligned: whole warps come here, whatever their lanes did before)
+__device__ __forceinline__ void cluster_arrive_all() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait_all() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void cluster_meet() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  cluster_arrive_all();
+  cluster_wait_all();
 }
 __device__ __forceinline__ uint32_t remote_u32(const void* p, uint32_t rank) {
   uint32_t a, v;
@@ -489,14 +499,14 @@ struct SampleRow {
 
   // An empty histogram.
   __device__ __forceinline__ void begin() {
-    if (reading) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (reading) cluster_wait_all();
     reading = false;
     uint4* h = reinterpret_cast<uint4*>(s.count);
     for (int i = threadIdx.x; i < 3 * kSampleBuckets / 4; i += kSampleThreads) h[i] = make_uint4(0, 0, 0, 0);
     __syncthreads();
   }
   __device__ __forceinline__ void settle() {
-    if (reading) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (reading) cluster_wait_all();
     reading = false;
   }
 
@@ -596,7 +606,7 @@ struct SampleRow {
     }
     __syncthreads();
     if (ctas > 1) {
-      asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+      cluster_arrive_all();
       reading = true;
     }
   }

@@ -26,3 +26,14 @@ def test_dependent_launches_read_nothing_through_the_non_coherent_path():
     for name in names + ["qgemv_elems.cuh", "qgemv_serve.cuh"]:
         for word in ("__ldg", "ld.global.nc", "__restrict__"):
             assert word not in source(name), (name, word)
+
+
+def test_aligned_cluster_barriers_of_divergent_code_follow_a_warp_barrier():
+    """barrier.cluster.*.aligned takes whole warps; these kernels come to theirs from code whose lanes go different ways."""
+    names = [n for n in os.listdir(CSRC) if "barrier.cluster" in source(n)]
+    assert {"qgemm_scaled.cuh", "qgemv_sample.cuh", "qgemv_lora.cuh", "qgemm_tc.cuh"} <= set(names)
+    for name in names:
+        text = source(name)
+        functions = re.findall(r"\{\s*(?:__syncwarp\(\);\s*)?asm volatile\(\"barrier\.cluster", text)
+        assert functions and all("__syncwarp" in f for f in functions), name
+        assert text.count('asm volatile("barrier.cluster') == len(functions), name
