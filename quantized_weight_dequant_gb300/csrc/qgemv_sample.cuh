@@ -11,7 +11,7 @@
 //    few heavy tokens moves the borders of all the others, and of 10^4 draws some would go to a neighbour.
 //  * A row belongs to a cluster of CTAs, each with a piece of it in index order, each warp with a piece of that.
 //  * Histogram 0 goes by z = (max - l) log2(e) / T, 40 buckets for each halving of the weight (where weights
-//    matter; coarser behind 2^-32): monotone in the logit, so its buckets are ranges of the order.  The
+//    matter; coarser behind 2^-45): monotone in the logit, so its buckets are ranges of the order.  The
 //    bucket with the border is then divided by the logits' bits, 2048 ways at a time, until the border falls between two
 //    ranges or within one value, whose equals are counted by index.
 //  * What takes part after a cut is listed, so that it is found once: in the cluster's first CTA where it holds all, in every CTA's own
@@ -105,12 +105,6 @@ __device__ __forceinline__ void store_remote(const void* p, uint32_t rank, uint3
   uint32_t a;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
-}
-__device__ __forceinline__ uint32_t add_remote(const void* p, uint32_t rank, uint32_t v) {
-  uint32_t a, old;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-  asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(old) : "r"(a), "r"(v) : "memory");
-  return old;
 }
 __device__ __forceinline__ uint64_t warp_sum64(uint64_t v) {
 #pragma unroll
