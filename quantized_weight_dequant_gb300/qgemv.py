@@ -33,7 +33,18 @@ class Problem(ctypes.Structure):
                 ("beta", ctypes.c_float), ("out", ctypes.c_int), ("swiglu", ctypes.c_int)]
 
 
-class KvCache(ctypes.Structure):
+class _Desc(ctypes.Structure):
+    """A description.  Numbers past the 32 bits of their field are refused; ctypes alone would keep their low bits."""
+
+    def __init__(self, *args, **kw):
+        super().__init__(*args, **kw)
+        given = dict(zip((f[0] for f in self._fields_), args), **kw)
+        for name, kind in self._fields_:
+            if kind is ctypes.c_int32 and given.get(name, getattr(self, name)) != getattr(self, name):
+                raise ValueError(f"{type(self).__name__}: {name} = {given[name]} does not fit 32 bits")
+
+
+class KvCache(_Desc):
     """qgemv_kv_cache_t: a paged key-value cache."""
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
                 ("v_scale", ctypes.c_void_p), ("page_stride", ctypes.c_int64), ("scale_stride", ctypes.c_int64),
@@ -41,7 +52,7 @@ class KvCache(ctypes.Structure):
                 ("head_dim", ctypes.c_int32), ("type", ctypes.c_int)]
 
 
-class PagePlan(ctypes.Structure):
+class PagePlan(_Desc):
     """qgemv_page_plan_t: block tables and slot maps of one step."""
     _fields_ = [("cached", ctypes.c_void_p), ("fresh", ctypes.c_void_p), ("table", ctypes.c_void_p),
                 ("table_stride", ctypes.c_int64), ("free_pages", ctypes.c_void_p), ("free_count", ctypes.c_void_p),
@@ -51,7 +62,7 @@ class PagePlan(ctypes.Structure):
                 ("page_size", ctypes.c_int32)]
 
 
-class KvStore(ctypes.Structure):
+class KvStore(_Desc):
     """qgemv_kv_store_t: q and k rotated, k and v stored in the cache."""
     _fields_ = [("cache", KvCache), ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
                 ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
@@ -61,7 +72,7 @@ class KvStore(ctypes.Structure):
                 ("q_heads", ctypes.c_int32), ("in_type", ctypes.c_int), ("q_type", ctypes.c_int)]
 
 
-class AttnDecode(ctypes.Structure):
+class AttnDecode(_Desc):
     """qgemv_attn_decode_t: one new token per request over the paged cache."""
     _fields_ = [("cache", KvCache), ("q", ctypes.c_void_p), ("q_stride", ctypes.c_int64), ("out", ctypes.c_void_p),
                 ("out_stride", ctypes.c_int64), ("lse", ctypes.c_void_p), ("table", ctypes.c_void_p),
@@ -70,7 +81,7 @@ class AttnDecode(ctypes.Structure):
                 ("q_heads", ctypes.c_int32), ("type", ctypes.c_int)]
 
 
-class Lora(ctypes.Structure):
+class Lora(_Desc):
     """qgemv_lora_t: low-rank adapters added to a projection's output."""
     _fields_ = [("x", ctypes.c_void_p), ("x_stride", ctypes.c_int64), ("A", ctypes.c_void_p), ("B", ctypes.c_void_p),
                 ("ids", ctypes.c_void_p), ("ranks", ctypes.c_void_p), ("scales", ctypes.c_void_p),
@@ -79,7 +90,7 @@ class Lora(ctypes.Structure):
                 ("rank", ctypes.c_int32), ("type", ctypes.c_int), ("out", ctypes.c_int)]
 
 
-class Norm(ctypes.Structure):
+class Norm(_Desc):
     """qgemv_norm_t: root-mean-square norm with the residual's addition."""
     _fields_ = [("x", ctypes.c_void_p), ("res", ctypes.c_void_p), ("res_out", ctypes.c_void_p), ("weight", ctypes.c_void_p),
                 ("y", ctypes.c_void_p), ("codes", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("x_stride", ctypes.c_int64),
@@ -89,14 +100,14 @@ class Norm(ctypes.Structure):
                 ("res_type", ctypes.c_int), ("weight_type", ctypes.c_int), ("out", ctypes.c_int)]
 
 
-class Quant(ctypes.Structure):
+class Quant(_Desc):
     """qgemv_quant_t: e4m3 codes and scales of rows."""
     _fields_ = [("x", ctypes.c_void_p), ("up", ctypes.c_void_p), ("codes", ctypes.c_void_p), ("scale", ctypes.c_void_p),
                 ("x_stride", ctypes.c_int64), ("up_stride", ctypes.c_int64), ("codes_stride", ctypes.c_int64),
                 ("scale_stride", ctypes.c_int64), ("rows", ctypes.c_int64), ("N", ctypes.c_int64), ("in_type", ctypes.c_int)]
 
 
-class Scaled(ctypes.Structure):
+class Scaled(_Desc):
     """qgemv_scaled_t: a projection of e4m3 rows by e4m3 weights."""
     _fields_ = [("x", ctypes.c_void_p), ("x_scale", ctypes.c_void_p), ("W", ctypes.c_void_p), ("w_scale", ctypes.c_void_p),
                 ("y", ctypes.c_void_p), ("x_stride", ctypes.c_int64), ("x_scale_stride", ctypes.c_int64),
@@ -104,7 +115,7 @@ class Scaled(ctypes.Structure):
                 ("out", ctypes.c_int)]
 
 
-class Sample(ctypes.Structure):
+class Sample(_Desc):
     """qgemv_sample_t: the next token of each row of logits."""
     _fields_ = [("logits", ctypes.c_void_p), ("stride", ctypes.c_int64), ("u", ctypes.c_void_p),
                 ("temperature", ctypes.c_void_p), ("top_k", ctypes.c_void_p), ("top_p", ctypes.c_void_p),
