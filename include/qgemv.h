@@ -147,8 +147,13 @@ int qgemv_group_size(qgemv_format_t fmt);
  *                             launch: they may start while the previous kernel on the stream
  *                             is still running, and they request their first weight stages
  *                             before waiting for it; activations are read only after it
- *                             completes.  packed_W must therefore not be written by the kernel
- *                             launched just before.  0 (default) launches them normally.
+ *                             completes.  packed_W must therefore not be written by a kernel
+ *                             that may still be running then: not by the one launched just
+ *                             before, nor, where that one is a dependent launch itself (under
+ *                             this option, or of the serving operators and those in 8 bits),
+ *                             by the one before it, and so on up to and with the first that
+ *                             is none: each of them lets the next one start before it has
+ *                             waited for its own predecessor.  0 (default) launches normally.
  *   QGEMV_OPT_TEST_STALL      test hook, default 0.  1 makes warp 0 of the first CTA of every
  *                             streaming launch also wait on a barrier that nothing completes,
  *                             bounded by the spin limit, so the timeout path (error word,
@@ -584,8 +589,8 @@ qgemv_status_t qgemv_quant_rows(qgemv_handle_t h, const qgemv_quant_t* quant, cu
  * 2^31 - 1, N 1 .. 2^31 - 1, K a multiple of 16 up to 2^31 - 16; x, W and y 16-byte aligned, x_stride a
  * multiple of 16, the scales 4-byte aligned.  Of the handle it uses the error word alone: calls of one
  * handle may run at once, and a wait that runs past QGEMV_OPT_SPIN_LIMIT_NS sets it.  With QGEMV_OPT_PDL
- * the first weights are requested before the kernel before it on the stream ends (M <= 64), which must
- * then not write W. */
+ * the first weights are requested before the kernel before it on the stream ends (M <= 64): W must then not
+ * be written by that kernel or another one that may still be running, as said at the option. */
 typedef struct {
   const void* x;
   const float* x_scale;
