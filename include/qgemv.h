@@ -608,6 +608,11 @@ typedef struct {
 
 qgemv_status_t qgemv_run_scaled(qgemv_handle_t h, const qgemv_scaled_t* scaled, cudaStream_t stream);
 
+/* Describe the launch qgemv_run_scaled would make for x [M][K] and W [N][K] into `buf` (as qgemv_describe): its
+ * path (few rows of x or many), the tiles' rows of x and of W, how many CTAs (of many rows: pairs) share one,
+ * tiles and CTAs. */
+qgemv_status_t qgemv_describe_scaled(qgemv_handle_t h, int64_t M, int64_t N, int64_t K, char* buf, size_t len);
+
 /* The next token of each of `rows` requests from its logits and one random number:
  *   w_i = exp((l_i - max l) / temperature); the tokens in the order of their logits, equal ones by
  *   index; of these the first top_k; of these the shortest beginning whose weights reach top_p of

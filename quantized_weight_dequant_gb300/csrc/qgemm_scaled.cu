@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cstdio>
 
 #include "qgemv_handle.cuh"
 #include "qgemv_serve.cuh"
@@ -81,50 +82,69 @@ bool encode(const Handle& h, const void* at, int64_t rows, int64_t K, int64_t st
                                                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-qgemv_status_t launch_few(const Handle& h, const qgemv_scaled_t& p, ScaledArgs a, int BT, cudaStream_t stream) {
-  CUtensorMap wmap, xmap;
-  if (!encode(h, p.W, p.N, p.K, p.K, kScaledRows, &wmap) || !encode(h, p.x, p.M, p.K, p.x_stride, BT, &xmap)) return QGEMV_ERR_CUDA;
-  const int64_t tiles = (p.N + kScaledRows - 1) / kScaledRows;
+// The launch for a shape: tiles of `columns` weight rows by `rows` rows of x, each shared by ks CTAs (of many rows: pairs of CTAs).
+struct ScaledPlan {
+  bool many;
+  int rows, columns, ks;
+  int64_t tiles, ctas;
+};
+
+ScaledPlan plan_few(const Handle& h, int64_t M, int64_t N, int64_t blocks) {
+  ScaledPlan pl{false, M <= 16 ? 16 : M <= 32 ? 32 : 64, kScaledRows, 1, (N + kScaledRows - 1) / kScaledRows, 0};
   // the largest cluster with which all tiles run at once, of two blocks a CTA at least
-  const int* most = h.scaled_clusters[few_index(BT)];
-  a.ks = 1;
+  const int* most = h.scaled_clusters[few_index(pl.rows)];
   for (int ks = 2; ks <= 8; ++ks)
-    if (tiles <= most[ks] && a.blocks >= 2 * ks) a.ks = ks;
-  void* args[] = {&wmap, &xmap, &a};
-  return launch_dependent(few_kernel_for(BT), dim3(static_cast<unsigned>(tiles * a.ks)), few_threads(BT), few_smem_bytes(BT), a.ks, args, stream)
-             ? QGEMV_OK
-             : QGEMV_ERR_CUDA;
+    if (pl.tiles <= most[ks] && blocks >= 2 * ks) pl.ks = ks;
+  pl.ctas = pl.tiles * pl.ks;
+  return pl;
 }
 
-qgemv_status_t launch_many(const Handle& h, const qgemv_scaled_t& p, ScaledArgs a, cudaStream_t stream) {
-  a.x_tiles = static_cast<int>((p.M + kManyRows - 1) / kManyRows);
-  a.wide = a.blocks % 4 == 0 && p.x_scale_stride % 4 == 0 && aligned16(p.x_scale) && aligned16(p.w_scale);
+ScaledPlan plan_many(const Handle& h, int64_t M, int64_t N, int64_t blocks) {
+  ScaledPlan pl{true, kManyRows, 256, 1, 0, 0};
+  const int64_t x_tiles = (M + kManyRows - 1) / kManyRows;
   // What takes the least time, in units of 0.065 us: rounds of tiles, a pair to each, or fewer tiles than pairs with their blocks
   // shared in clusters and joined.  A block of 128 weight rows takes 4 units and one of 256 6, the end of a tile 14 or 28, a join
   // 33 or 58.  128 x 4096 x 14336: 20.8 us with 128 rows and two pairs to a tile, 33.5 with one, 24.8 with 256 rows and three
   // pairs; 512 x 4096 x 4096: 12.9 with 128 rows alone, 16.0 with 256 and two pairs.
-  const int64_t pairs = h.sms / 2, fours = (a.blocks + 3) / 4;
-  int BN = 256;
+  const int64_t pairs = std::max(1, h.sms / 2), fours = (blocks + 3) / 4;
   double least = 0.;
   for (int bn : {256, 128}) {
-    const int64_t tiles = a.x_tiles * ((p.N + bn - 1) / bn), block = bn == 256 ? 6 : 4, end = bn == 256 ? 28 : 14, join = bn == 256 ? 58 : 33;
+    const int64_t tiles = x_tiles * ((N + bn - 1) / bn), block = bn == 256 ? 6 : 4, end = bn == 256 ? 28 : 14, join = bn == 256 ? 58 : 33;
     for (int ks = 1; ks <= kManyMaxPairs; ++ks) {
       if (ks > 1 && (tiles > h.scaled_pairs[bn / 256][ks] || fours < ks)) continue;
-      const int64_t rounds = ks > 1 ? 1 : (tiles + pairs - 1) / pairs, blocks = ks > 1 ? (fours + ks - 1) / ks * 4 : a.blocks;
-      const double cost = static_cast<double>(rounds) * static_cast<double>(blocks * block + end) + (ks > 1 ? join : 0);
-      if (least == 0. || cost < least) least = cost, BN = bn, a.ks = ks;
+      const int64_t rounds = ks > 1 ? 1 : (tiles + pairs - 1) / pairs, each = ks > 1 ? (fours + ks - 1) / ks * 4 : blocks;
+      const double cost = static_cast<double>(rounds) * static_cast<double>(each * block + end) + (ks > 1 ? join : 0);
+      if (least == 0. || cost < least) least = cost, pl.columns = bn, pl.ks = ks;
     }
   }
+  pl.tiles = x_tiles * ((N + pl.columns - 1) / pl.columns);
+  pl.ctas = 2 * pl.ks * (pl.ks > 1 ? pl.tiles : std::min<int64_t>(pl.tiles, pairs));
+  return pl;
+}
+
+// The plan of a valid shape with rows.
+qgemv_status_t plan_scaled(const Handle& h, int64_t M, int64_t N, int64_t K, ScaledPlan& pl) {
+  const int64_t blocks = (K + kScaledBlock - 1) / kScaledBlock;
+  pl = M > 64 ? plan_many(h, M, N, blocks) : plan_few(h, M, N, blocks);
+  return pl.tiles > 0x7fffffff ? QGEMV_ERR_BAD_SHAPE : QGEMV_OK;
+}
+
+bool shape_ok(int64_t M, int64_t N, int64_t K) {
+  constexpr int64_t most = 0x7fffffff;
+  return M >= 0 && M <= most && N >= 1 && N <= most && K >= 16 && K <= most && K % 16 == 0;
+}
+
+qgemv_status_t launch(const Handle& h, const qgemv_scaled_t& p, const ScaledPlan& pl, ScaledArgs a, cudaStream_t stream) {
   CUtensorMap wmap, xmap;
-  if (!encode(h, p.W, p.N, p.K, p.K, BN / 2, &wmap) || !encode(h, p.x, p.M, p.K, p.x_stride, kManyRows / 2, &xmap)) return QGEMV_ERR_CUDA;
-  const int64_t tiles = a.x_tiles * ((p.N + BN - 1) / BN);
-  if (tiles > 0x7fffffff) return QGEMV_ERR_BAD_SHAPE;
+  if (!encode(h, p.W, p.N, p.K, p.K, pl.many ? pl.columns / 2 : kScaledRows, &wmap) ||
+      !encode(h, p.x, p.M, p.K, p.x_stride, pl.many ? kManyRows / 2 : pl.rows, &xmap))
+    return QGEMV_ERR_CUDA;
+  a.ks = pl.ks;
   void* args[] = {&wmap, &xmap, &a};
-  const void* fn = many_kernel_for(BN, a.ks > 1);
-  const int64_t clusters = a.ks > 1 ? tiles : std::min<int64_t>(tiles, pairs);
-  return launch_dependent(fn, dim3(static_cast<unsigned>(2 * a.ks * clusters)), kManyThreads, many_smem_bytes(BN), 2 * a.ks, args, stream)
-             ? QGEMV_OK
-             : QGEMV_ERR_CUDA;
+  const dim3 grid(static_cast<unsigned>(pl.ctas));
+  const bool ok = pl.many ? launch_dependent(many_kernel_for(pl.columns, pl.ks > 1), grid, kManyThreads, many_smem_bytes(pl.columns), 2 * pl.ks, args, stream)
+                          : launch_dependent(few_kernel_for(pl.rows), grid, few_threads(pl.rows), few_smem_bytes(pl.rows), pl.ks, args, stream);
+  return ok ? QGEMV_OK : QGEMV_ERR_CUDA;
 }
 
 }  // namespace
@@ -134,9 +154,9 @@ extern "C" qgemv_status_t qgemv_run_scaled(qgemv_handle_t hh, const qgemv_scaled
   if (!h || !scaled) return QGEMV_ERR_INVALID_ARG;
   const qgemv_scaled_t& p = *scaled;
   if (p.out != QGEMV_OUT_F32 && p.out != QGEMV_OUT_F16 && p.out != QGEMV_OUT_BF16) return QGEMV_ERR_INVALID_ARG;
-  constexpr int64_t most = 0x7fffffff, far = int64_t{1} << 38;
-  if (p.M < 0 || p.M > most || p.N < 1 || p.N > most || p.K < 16 || p.K > most || p.K % 16 || p.x_stride < p.K || p.x_stride > far ||
-      p.x_scale_stride < (p.K + 127) / 128 || p.x_scale_stride > far || p.y_stride < p.N || p.y_stride > far)
+  constexpr int64_t far = int64_t{1} << 38;
+  if (!shape_ok(p.M, p.N, p.K) || p.x_stride < p.K || p.x_stride > far || p.x_scale_stride < (p.K + 127) / 128 || p.x_scale_stride > far ||
+      p.y_stride < p.N || p.y_stride > far)
     return QGEMV_ERR_BAD_SHAPE;
   if (!p.W || !p.w_scale || (p.M > 0 && (!p.x || !p.x_scale || !p.y))) return QGEMV_ERR_INVALID_ARG;
   if (!aligned16(p.x) || !aligned16(p.W) || !aligned16(p.y) || p.x_stride % 16 ||
@@ -144,6 +164,9 @@ extern "C" qgemv_status_t qgemv_run_scaled(qgemv_handle_t hh, const qgemv_scaled
     return QGEMV_ERR_MISALIGNED;
   if (p.M == 0) return QGEMV_OK;
   if (!h->encode_tiled) return QGEMV_ERR_CUDA;  // no TMA descriptors from this driver
+  ScaledPlan pl;
+  const qgemv_status_t st = plan_scaled(*h, p.M, p.N, p.K, pl);
+  if (st != QGEMV_OK) return st;
   ScaledArgs a{};
   a.xs = p.x_scale;
   a.ws = p.w_scale;
@@ -158,6 +181,22 @@ extern "C" qgemv_status_t qgemv_run_scaled(qgemv_handle_t hh, const qgemv_scaled
   a.spin_ns = h->spin_ns;
   a.early = h->pdl;
   a.stall = h->test_stall;
-  if (p.M > 64) return launch_many(*h, p, a, stream);
-  return launch_few(*h, p, a, p.M <= 16 ? 16 : p.M <= 32 ? 32 : 64, stream);
+  a.x_tiles = static_cast<int>((p.M + kManyRows - 1) / kManyRows);
+  a.wide = a.blocks % 4 == 0 && p.x_scale_stride % 4 == 0 && aligned16(p.x_scale) && aligned16(p.w_scale);
+  return launch(*h, p, pl, a, stream);
+}
+
+extern "C" qgemv_status_t qgemv_describe_scaled(qgemv_handle_t hh, int64_t M, int64_t N, int64_t K, char* buf, size_t len) {
+  const Handle* h = handle_of(hh);
+  if (!h) return QGEMV_ERR_INVALID_ARG;
+  if (!shape_ok(M, N, K)) return QGEMV_ERR_BAD_SHAPE;
+  ScaledPlan pl{};
+  const qgemv_status_t st = M > 0 ? plan_scaled(*h, M, N, K, pl) : QGEMV_OK;
+  if (st != QGEMV_OK || !buf || !len) return st;
+  if (M == 0)
+    snprintf(buf, len, "path=none");
+  else
+    snprintf(buf, len, "path=%s rows=%d columns=%d share=%d tiles=%lld ctas=%lld", pl.many ? "many" : "few", pl.rows, pl.columns, pl.ks,
+             static_cast<long long>(pl.tiles), static_cast<long long>(pl.ctas));
+  return QGEMV_OK;
 }

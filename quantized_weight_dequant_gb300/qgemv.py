@@ -127,7 +127,7 @@ EXPORTS = ["qgemv_create", "qgemv_destroy", "qgemv_run", "qgemv_unpack", "qgemv_
            "qgemv_status_string", "qgemv_packed_bytes", "qgemv_group_size", "qgemv_set_option",
            "qgemv_describe", "qgemv_build_marker", "qgemv_run_noalloc", "qgemv_run_group", "qgemv_run_ex", "qgemv_run_batch",
            "qgemv_run_gemm", "qgemv_page_plan", "qgemv_kv_store", "qgemv_attn_decode", "qgemv_run_lora",
-           "qgemv_run_norm", "qgemv_quant_rows", "qgemv_run_scaled", "qgemv_sample"]
+           "qgemv_run_norm", "qgemv_quant_rows", "qgemv_run_scaled", "qgemv_describe_scaled", "qgemv_sample"]
 
 _lib = None
 
@@ -172,12 +172,13 @@ def lib() -> ctypes.CDLL:
         L.qgemv_run_norm.argtypes = [vp, ctypes.POINTER(Norm), vp]
         L.qgemv_quant_rows.argtypes = [vp, ctypes.POINTER(Quant), vp]
         L.qgemv_run_scaled.argtypes = [vp, ctypes.POINTER(Scaled), vp]
+        L.qgemv_describe_scaled.argtypes = [vp, i64, i64, i64, ctypes.c_char_p, ctypes.c_size_t]
         L.qgemv_sample.argtypes = [vp, ctypes.POINTER(Sample), vp]
         for name in ("qgemv_create", "qgemv_destroy", "qgemv_run", "qgemv_unpack", "qgemv_check_error",
                      "qgemv_set_option", "qgemv_describe", "qgemv_run_noalloc", "qgemv_run_group",
                      "qgemv_run_ex", "qgemv_run_batch", "qgemv_run_gemm", "qgemv_page_plan", "qgemv_kv_store",
                      "qgemv_attn_decode", "qgemv_run_lora", "qgemv_run_norm", "qgemv_quant_rows", "qgemv_run_scaled",
-                     "qgemv_sample"):
+                     "qgemv_describe_scaled", "qgemv_sample"):
             getattr(L, name).restype = st
         _lib = L
     return _lib
@@ -674,6 +675,13 @@ def run_scaled(h: Handle, desc: Scaled, stream=None, check: bool = True) -> int:
     if check:
         _check(st, "qgemv_run_scaled")
     return st
+
+
+def describe_scaled(h: Handle, M: int, N: int, K: int) -> str:
+    """The launch that run_scaled would make for x [M, K] and W [N, K]."""
+    buf = ctypes.create_string_buffer(512)
+    _check(lib().qgemv_describe_scaled(h.ptr, M, N, K, buf, 512), "qgemv_describe_scaled")
+    return buf.value.decode()
 
 
 def sample_desc(logits, u, tokens, temperature=None, top_k=None, top_p=None, min_p=None, logprobs=None) -> Sample:
