@@ -45,6 +45,11 @@ bool scaled_prepare(Handle& h) {
     if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess) cudaGetLastError(), n = 0;
     return n;
   };
+  // the many rows' kernels share out the registers they are launched with: of fewer, the share that grows would be waited for for ever
+  auto registers = [](const void* fn) {
+    cudaFuncAttributes fa;
+    return cudaFuncGetAttributes(&fa, fn) == cudaSuccess && fa.numRegs * (1 + kManyParts) >= kManyRegs[0] + kManyParts * kManyRegs[1];
+  };
   auto prepare = [](const void* fn, size_t smem) {
     return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) == cudaSuccess;
   };
@@ -55,6 +60,7 @@ bool scaled_prepare(Handle& h) {
     for (int ks = 2; ks <= 8; ++ks) h.scaled_clusters[few_index(BT)][ks] = 2 * clusters(few_kernel_for(BT), few_threads(BT), few_smem_bytes(BT), ks);
   }
   for (int BN : {128, 256}) {
+    if (!registers(many_kernel_for(BN, false)) || !registers(many_kernel_for(BN, true))) return false;
     if (!prepare(many_kernel_for(BN, false), many_smem_bytes(BN)) || !prepare(many_kernel_for(BN, true), many_smem_bytes(BN))) return false;
     for (int ks = 2; ks <= kManyMaxPairs; ++ks) h.scaled_pairs[BN / 256][ks] = clusters(many_kernel_for(BN, true), kManyThreads, many_smem_bytes(BN), 2 * ks);
   }
