@@ -110,8 +110,9 @@ ScaledPlan plan_many(const Handle& h, int64_t M, int64_t N, int64_t blocks) {
   const int64_t x_tiles = (M + kManyRows - 1) / kManyRows;
   // What takes the least time, in units of 0.065 us: rounds of tiles, a pair to each, or fewer tiles than pairs with their blocks
   // shared in clusters and joined.  A block of 128 weight rows takes 4 units and one of 256 6, the end of a tile 14 or 28, a join
-  // 33 or 58.  128 x 4096 x 14336: 20.8 us with 128 rows and two pairs to a tile, 33.5 with one, 24.8 with 256 rows and three
-  // pairs; 512 x 4096 x 4096: 12.9 with 128 rows alone, 16.0 with 256 and two pairs.
+  // 33 or 58.  128 x 4096 x 14336: 21.0 us with 128 rows and two pairs to a tile, 33.2 with one, 25.5 with 256 rows and three
+  // pairs; 512 x 4096 x 4096: 13.1 with 128 rows alone, 16.4 with 256 and two pairs; 300 x 4096 x 14336: 31.8 with 256 and two pairs,
+  // 33.1 with 128; 4096 x 28672 x 4096: 359 with 256, 430 with 128.
   const int64_t pairs = std::max(1, h.sms / 2), fours = (blocks + 3) / 4;
   double least = 0.;
   for (int bn : {256, 128}) {

@@ -10,8 +10,8 @@
 // x, or with few tiles a cluster of CTAs has it and each takes a share of its blocks; then every CTA leaves its sums in shared
 // memory and adds a part of the tile over the cluster, in rank order.  Two CTAs are on an SM: where their number is no
 // multiple of the SMs', memory serves all of them alike and they still end together, and one's start and end are the other's
-// loads.  1 x 4096 x 4096 takes 6.4 us (its bytes 2.5, the launch, the first loads' way and the join the rest), 37 x 4096 x 14336
-// 15.9 (8.8) and 64 x 28672 x 4096 23.5 (17.9).  (Equal shares of all tiles' blocks, one persistent CTA an SM, joined through the workspace: 64 x 28672 x
+// loads.  1 x 4096 x 4096 takes 6.8 us from memory (its bytes 2.5, the launch, the first loads' way and the join the rest) and 5.8
+// where L2 has W, 37 x 4096 x 14336 16.2 (8.8) and 64 x 28672 x 4096 23.9 (17.9).  (Equal shares of all tiles' blocks, one persistent CTA an SM, joined through the workspace: 64 x 28672 x
 // 4096 32.5 us, 64 x 4096 x 4096 19.8, most of it joins.)
 //  * The weight rows are the MMA's M (TMEM lanes), the rows of x its N: a lane's accumulators then belong to
 //    one weight row and BT rows of x, and 32 lanes write 32 neighbours of a row of y.
@@ -328,11 +328,12 @@ __global__ void __launch_bounds__(few_threads(BT), 2) scaled_few_kernel(const __
 // W (a CTA alone would need 96 bytes a cycle for the operands and 96 for the copies, of 128).  One persistent pair on
 // every two SMs, tiles of x first, so that the weights that are being read are shared by all of x.  Eight warps
 // scale and add, a half of the columns each, and write through shared memory, whole rows' pieces at a time.
-// 4096 x 28672 x 4096 takes 347 us (249 at the rate for 8 bits), 4096 x 4096 x 14336 188.  A block of a 256 x 256 tile takes 737
+// 4096 x 28672 x 4096 takes 382 us in calls one after another (360 while the card is cool; 249 at the rate for 8 bits), 4096 x 4096 x
+// 14336 200.  A block of a 256 x 256 tile takes 737
 // cycles, its instructions 512: the sums come out of tensor memory in 16 turns of 16 columns, each met by its additions; the other
 // pairs' loads add 15 %, and the end of a tile 3500 cycles that no instruction of the next covers, for want of registers.  What all
 // SMs take in, 48 bytes a cycle each, is near what the L2 gives.
-// Where tiles are few, up to four pairs, a cluster, share a tile's blocks and join their sums (128 x 4096 x 14336: 20.7 us, 33.5
+// Where tiles are few, up to four pairs, a cluster, share a tile's blocks and join their sums (128 x 4096 x 14336: 21.0 us, 33.2
 // with a pair to a tile).  Sums of 128 columns are read ahead and added two to an instruction (32.8 us of 36.6 in that case with a
 // pair to a tile); of 256 that is slower (350 us to 357 of the large one), as registers are then short.
 constexpr int kManyParts = 2;  // warpgroups of sums, each with a part of the columns

@@ -54,10 +54,12 @@ qgemv_status_t qgemv_run_norm(qgemv_handle_t hh, const qgemv_norm_t* norm, cudaS
       !aligned16(p.weight) || (p.codes && reinterpret_cast<uintptr_t>(p.scale) % 4))
     return QGEMV_ERR_MISALIGNED;
   if (p.rows == 0) return QGEMV_OK;
-  // Up to 512 elements a warp has a row, and 64 warps an SM; more: a CTA (2048 elements, 8191 rows: 24.6 us, with a warp
-  // for each 35).  Many rows: a thread has two pieces of its row or more and a CTA goes on to the row 1024 threads an SM on, whose
-  // elements it reads before it finishes the first (4096 elements: 44.8 us, 57.5 with one piece, 68.4 with four; 14336: 158,
-  // with a CTA for each row 217; all before the pieces were put side by side).  Few rows: as many threads as there are pieces.
+  // Up to 512 elements a warp has a row, and 64 warps an SM; more: a CTA (65528 rows of 256: 25.5 us, with a CTA for each 40.4; of
+  // 512 the two are close, 44.1 and 39.6).  Many rows: a thread has two pieces of its row or more and a CTA goes on to the row 1024
+  // threads an SM on, whose elements it reads before it finishes the first (8191 rows of 4096 in bf16: 40.0 us, 52.7 with one piece,
+  // 55.8 with four, 46.7 with a CTA for each row; of 14336 144, with a CTA for each 211; fp32 rows of 4096 with a bf16 residual 48.1,
+  // 53.7 with one piece, 82.5 with four; with an fp32 residual one piece would do: 83.6 and 66.4).  Few rows: as many threads as
+  // there are pieces.
   const int vecs = static_cast<int>(p.N / 8);
   const bool warp = vecs <= 64;
   int v = 1;

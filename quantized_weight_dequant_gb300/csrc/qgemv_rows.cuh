@@ -70,8 +70,8 @@ __device__ __forceinline__ void store_codes(float (*f)[8], bool in, int first, u
 
 // y = s / sqrt(mean(s^2) + eps) * (offset + weight), s = x + res.  A row is held in registers, V times eight elements a
 // thread, by one warp (kNormWarps rows in a CTA) or by a whole CTA, so that every byte is read once and the norm of a row
-// may overwrite it.  Memory bounds it: 8191 rows of 4096 in bf16 with the sum written back and codes, 235 MB, take 40.1 us
-// (5.9 TB/s); 8191 of 2048 22.2; 64 of 4096 2.9 and one row 2.7, which is the launch and one trip to memory.  (Rows of more than 16384
+// may overwrite it.  Memory bounds it: 8191 rows of 4096 in bf16 with the sum written back and codes, 235 MB, take 40.0 us
+// (5.9 TB/s); 8191 of 2048 22.3; 64 of 4096 2.9 and one row 2.7, which is the launch and one trip to memory.  (Rows of more than 16384
 // columns are partly kept in local memory: 1024 threads have 64 registers each.)
 constexpr int kNormWarps = 4;  // rows of a CTA where a warp has a row
 
@@ -82,8 +82,8 @@ __global__ void __launch_bounds__(WARP ? 32 * kNormWarps : 1024) norm_kernel(con
   const int64_t step = WARP ? static_cast<int64_t>(gridDim.x) * kNormWarps : gridDim.x;
   int64_t m = WARP ? static_cast<int64_t>(blockIdx.x) * kNormWarps + threadIdx.x / 32 : blockIdx.x;
   constexpr int kEl = WIDE ? 4 : 2, kResEl = RES == 2 ? 4 : 2;
-  // pieces of eight side by side, whose group's scale is worked out once (8191 x 4096 42.1 us for 44.8; of fp32 rows, 64 bytes apart
-  // then, 91 for 83)
+  // pieces of eight side by side, whose group's scale is worked out once (8191 x 4096 42.1 us for 44.8; of fp32 rows with an fp32
+  // residual, 64 bytes apart then, 91 for 83)
   constexpr int P = V == 1 || WIDE || RES == 2 ? 1 : 2;
   auto place = [&](int j) { return ((j / P * threads + tid) * P + j % P) * 8; };
   Elems8<WIDE> a[V];
@@ -179,8 +179,8 @@ __device__ __forceinline__ float silu(float g) {
 
 // Codes of rows: a scale top / 448 and quotients per 128.  A thread has 16 elements, an eighth of a group, so that the group's scale is worked out for 16 at a
 // time, and a CTA 2048 of its row.  Instructions bound it next to memory: 8191 rows of 4096 in bf16 take 18.9 us (15.0 at
-// the copy's rate; with eight elements a thread 22.3), the gated
-// product of 14336 117 (86; with expf and a division 144), 64 rows of it 2.9, one of 4096 1.6.
+// the copy's rate; with eight elements a thread 22.3; with CTAs of 64 threads 33.6, of 256 17.9), the gated
+// product of 14336 117 (86; with expf and a division 144; with 64 threads 119, with 256 121), 64 rows of it 2.9, one of 4096 1.6.
 constexpr int kQuantThreads = 128;
 
 template <bool WIDE, bool GATED>

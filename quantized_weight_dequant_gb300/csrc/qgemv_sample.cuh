@@ -16,9 +16,10 @@
 //    ranges or within one value, whose equals are counted by index.
 //  * What takes part after a cut is listed, so that it is found once: in the cluster's first CTA where it holds all, in every CTA's own
 //    list, or, of more, the border's bucket alone.  (Going over the rows every time: 64 rows of 128000 fp32 with mixed settings
-//    136 us, with lists 67; 509 of 50001 in bf16 with top-p 376 and 157.)
+//    136 us, with lists 68; 509 of 50001 in bf16 with top-p 376 and 161.)
 //  * Instructions and shared memory's adds bound the passes with weights, the meetings of a cluster the rest: one row of 32000
-//    takes 10.1 us, of which the logits' bytes are nothing; 64 rows of 128000 without limits 36 (4.8 at the copy's rate).
+//    takes 10.1 us, of which the logits' bytes are nothing; 64 rows of 128000 without limits 34 (4.8 at the copy's rate), with
+//    top-k 50 22, with the largest logit alone 9.2.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -36,8 +37,10 @@ constexpr int kSampleBuckets = 2048;
 constexpr int kSampleGroups = 32;  // of 64 buckets
 constexpr int kSampleNothing = 1801;  // the first bucket whose tokens weigh nothing: 45 halvings, 40 buckets each, to the nearest
 constexpr int kSampleMaxCluster = 8;
-constexpr int kSampleFew = 256;    // candidates that are compared each with each
-constexpr int kSampleList = 4096;  // candidates that one CTA finishes alone
+// Candidates that are compared each with each (8 x 50001, top-k 400 and top-p 0.9: 23.3 us, with 512 44.9; top-k 200: 21.8, with 128
+// 22.6), and that one CTA's list holds: so many that a second CTA finds room on the SM.
+constexpr int kSampleFew = 256;
+constexpr int kSampleList = 4096;
 constexpr int kSampleUnit = 43;    // weights in units of 2^-43: 2^20 of them stay below 2^64
 constexpr uint32_t kTableFirst = 119 << 7, kTableValues = 15 << 7;  // bf16: magnitudes of 2^-8 up to 2^7
 constexpr float kInf = __builtin_huge_valf();
@@ -831,7 +834,7 @@ struct SampleRow {
   // All that is left for few candidates, a thread to each: its place in the order and the mass before it by comparison with all others,
   // what is kept (k: at most so many; p_goal(mass of those): the mass at which top-p ends, and no limit where that is all ones), and
   // the running sum by index in the same way.  (Every cut by histograms and every draw of such a list is two meetings and two
-  // passes over 2048 buckets: 1 x 32000 with k 50 and p 0.9 15.5 us for 10.1.  512 candidates would take as long either way.)
+  // passes over 2048 buckets: 1 x 32000 with k 50 and p 0.9 15.5 us for 10.1.  512 candidates take twice as long this way.)
   template <class P, class A, class K>
   __device__ void finish(uint32_t k, P p_goal, uint64_t floor_w, A aim, K take) {
     uint64_t* key = reinterpret_cast<uint64_t*>(s.count);
@@ -974,6 +977,7 @@ struct SampleRow {
     // A count that ends among tokens of weight 0 (those a mask took out among them) cuts nothing that can be drawn.
     if (!MASS && c.bucket >= kSampleNothing) return c;
     if (!listed) {
+      // (up to 3/4 of all lists, as the CTAs' parts are not equal: with a half and with the whole every case is within 1.5 %)
       const bool fit = MASS ? s.pick_first <= kSampleList * ctas * 3 / 4 : before + part <= kSampleList;
       if (fit) list(c, in);
       if constexpr (MASS) {
